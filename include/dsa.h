@@ -431,6 +431,160 @@ int dsa_msa_attention(const void *kv_pool, int64_t num_pages, float k_scale, flo
 size_t dsa_msa_attention_workspace_size(int32_t num_rows, int32_t heads_per_group);
 
 /*
+ * ---- The dense K/V path: rotary positions, insert into a paged K/V pool, and attention of new
+ * tokens over all of it.  The two sparse layers above sit next to full-attention layers, and both
+ * take queries, keys and latents whose rotary dims are already rotated: these calls are that
+ * chain, rope -> insert -> attention, over a K/V pool with the MSA page layout generalised:
+ *
+ *   page = [kv_heads] x ([K: page_size x head_dim] [V: page_size x head_dim])
+ *
+ * in bf16 (DSA_KV_BF16) or e4m3 codes with one fp32 scale for K and one for V (DSA_KV_FP8: value =
+ * code * scale; with 4 KV heads, head_dim 128 and 128-token pages, exactly the pool
+ * dsa_msa_attention reads).  page_size is 16, 32, 64 or 128, head_dim 64 or 128.  dsa_rows.
+ * block_table then holds ids of these pages (bt_stride >= ceil(max_ctx / page_size)); token t of a
+ * request is row t % page_size of page block_table[req][t / page_size], its slot page * page_size
+ * + t % page_size.
+ */
+#define DSA_KV_BF16 5
+#define DSA_KV_FP8 6
+#define DSA_KV_MAX_HPG 128 /* query heads per KV head */
+
+typedef struct dsa_kv_cache {
+    void *base;         /* device, 16-byte aligned */
+    int32_t format;     /* DSA_KV_BF16 or DSA_KV_FP8 */
+    int32_t page_size;  /* 16, 32, 64 or 128 tokens */
+    int64_t num_pages;  /* num_pages * kv_heads * 2 * page_size < 2^31 */
+    int32_t kv_heads;
+    int32_t head_dim;   /* 64 or 128 */
+    float k_scale;      /* DSA_KV_FP8: value of a K code = code * k_scale; ignored for DSA_KV_BF16 */
+    float v_scale;
+} dsa_kv_cache;
+
+/* Element types of dsa_rope's tensors. */
+#define DSA_DTYPE_BF16 1
+#define DSA_DTYPE_FP32 2
+
+/* Which elements of the rotary part form a pair: 2i and 2i + 1, or i and i + rot_dim / 2. */
+#define DSA_ROPE_INTERLEAVED 0
+#define DSA_ROPE_HALF 1
+
+/* Frequencies stretched for contexts longer than the trained one (dsa_rope_frequencies). */
+#define DSA_ROPE_SCALE_NONE 0
+#define DSA_ROPE_SCALE_LINEAR 1
+#define DSA_ROPE_SCALE_NTK 2
+#define DSA_ROPE_SCALE_YARN 3
+
+#define DSA_ROPE_MAX_DIM 256
+#define DSA_ROPE_MAX_TENSORS 4
+
+/*
+ * Host-only helper: the angle per position of each of the rot_dim / 2 pairs, and the factor on the
+ * rotated values, from the base theta > 1 and a context stretch `factor` >= 1 (not used by
+ * DSA_ROPE_SCALE_NONE).  With f_i = theta^(-2i / rot_dim):
+ *   NONE    inv_freq_i = f_i, scale 1
+ *   LINEAR  f_i / factor, scale 1
+ *   NTK     f_i of the base theta * factor^(rot_dim / max(rot_dim - 2, 1)), scale 1
+ *   YARN    f_i (1 - r_i) + f_i / factor * r_i, scale 0.1 ln(factor) + 1; r_i rises from 0 to 1 over
+ *           the pairs from the one that turns 32 times within trained_ctx positions to the one that
+ *           turns once (Peng et al. 2023, "YaRN"): r_i = clamp((i - lo) / max(hi - lo, 0.001)), lo =
+ *           max(floor(e(32)), 0), hi = min(ceil(e(1)), rot_dim - 1), e(n) = rot_dim ln(trained_ctx /
+ *           (2 pi n)) / (2 ln theta)
+ * inv_freq: host, rot_dim / 2 doubles; scale: host.
+ */
+int dsa_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling, double factor, int32_t trained_ctx,
+                         double *inv_freq, float *scale);
+
+/*
+ * Host-only helper: num_pairs angles per position (radians, finite) as the kernels take them: the
+ * fraction of a turn, inv_freq / 2 pi mod 1, in units of 2^-64 turn.  A position's phase is then
+ * one 64-bit product that wraps exactly, so far positions lose no precision.  inv_freq, turns: host.
+ */
+int dsa_rope_turns(const double *inv_freq, int32_t num_pairs, uint64_t *turns);
+
+/* A call's angles. */
+typedef struct dsa_rope_spec {
+    const uint64_t *turns;    /* device [rot_dim / 2], from dsa_rope_turns */
+    const int32_t *positions; /* device [num_tokens]; a negative position leaves its token out */
+    int32_t rot_dim;          /* even, 2 .. DSA_ROPE_MAX_DIM */
+    float scale;              /* factor on the rotated values (finite) */
+} dsa_rope_spec;
+
+/* One tensor [num_tokens, num_heads, rot_dim]: the rotary part of every head alone, in place inside
+ * larger heads through its strides (in elements).  x may equal out (with equal strides); any other
+ * overlap is not allowed. */
+typedef struct dsa_rope_tensor {
+    const void *x;
+    void *out;
+    int32_t num_heads;
+    int32_t layout; /* DSA_ROPE_INTERLEAVED or DSA_ROPE_HALF */
+    int64_t x_token_stride, x_head_stride;
+    int64_t out_token_stride, out_head_stride;
+} dsa_rope_tensor;
+
+/*
+ * Rotary positions of 1 .. DSA_ROPE_MAX_TENSORS tensors of the same tokens, in one launch (a
+ * decode step's query heads, latent and index key).  For each pair (a, b) of token n with angle
+ * t = positions[n] * inv_freq_i:
+ *   out_a = scale (a cos t - b sin t),  out_b = scale (a sin t + b cos t)
+ * in fp32, rounded once to dtype (of every tensor).  Elements outside the rotary part are neither
+ * read nor written, nor is a token at a negative position (padding).  tensors: host array.
+ */
+int dsa_rope(const dsa_rope_spec *rope, const dsa_rope_tensor *tensors, int32_t num_tensors, int32_t dtype,
+             int32_t num_tokens, void *stream);
+
+/* New tokens' keys and values: [num_tokens, kv_heads, head_dim] bf16 with heads packed, tokens
+ * k_stride / v_stride elements apart (parts of a packed projection output). */
+typedef struct dsa_kv_rows {
+    const uint16_t *k;
+    const uint16_t *v;
+    int64_t k_stride, v_stride;
+    int32_t rot_offset; /* with a dsa_rope_spec: first rotary dim of a K head */
+    int32_t layout;     /* with a dsa_rope_spec: DSA_ROPE_INTERLEAVED or DSA_ROPE_HALF */
+} dsa_kv_rows;
+
+/*
+ * Write new tokens into the K/V pool: for each i with slots[i] >= 0, K and V at that slot, as
+ *   DSA_KV_BF16: the values (rotated K rounded once from fp32)
+ *   DSA_KV_FP8:  e4m3(x / scale), IEEE fp32 division, round to nearest even, saturating to +-448
+ * rope != NULL rotates K's dims [rot_offset, rot_offset + rot_dim) on the way, in fp32, and with
+ * q != NULL also rotates q (bf16, [num_tokens, q->num_heads, rot_dim]) as dsa_rope does, in the same
+ * launch; q needs rope.  slots: device [num_tokens], distinct (of a slot listed twice, which token's
+ * bytes it holds is unspecified).  A slot outside the pool, or a slot >= 0 of a token at a negative
+ * position, is DSA_ERR_BOUNDS and not written; every other byte of the pool keeps its value.
+ */
+int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_tokens, const dsa_kv_rows *kv,
+                  const dsa_rope_spec *rope, const dsa_rope_tensor *q, int32_t *dev_status, void *stream);
+
+/*
+ * Dense attention of new tokens over the paged cache: head h of row r reads KV head
+ * g = h / (num_heads / kv_heads) and attends to the tokens t < row_ctx[r]:
+ *   out[r, h, :] = sum_t softmax_t(sm_scale * <q[r,h,:], K_g,t>) V_g,t
+ *   lse[r, h]    = ln sum_t exp(sm_scale * <q[r,h,:], K_g,t>)
+ * q: bf16 [num_rows, num_heads, head_dim], rows q_stride elements apart (a multiple of 8), 16-byte
+ * aligned; num_heads a multiple of kv_heads, at most DSA_KV_MAX_HPG times it; out: bf16 [num_rows,
+ * num_heads, head_dim], 16-byte aligned; lse: fp32 [num_rows, num_heads] or NULL.  A head with no
+ * visible token, or whose visible scores are all -inf, gets out = 0 and lse = -inf.  What slots at
+ * or past row_ctx[r] hold never reaches row r (NaN included).  rows->rows_per_group (1, 2, 4 or 8)
+ * consecutive rows of one request (speculative verify) share each read of the cache.
+ *
+ * Each row's tokens are split into parts by its own context (the group's largest; batch
+ * invariance), one CTA per part and KV head, merged by log-sum-exp: the workspace (device, 256-byte
+ * aligned, dsa_kv_attention_workspace_size bytes, no initial contents; NULL when that is 0) holds
+ * the parts in fp32.  Scores and sums are fp32; the softmax weights multiply V as the sum of two
+ * bf16 terms (bf16 pool) or as fp16 (FP8 pool, whose codes are exact in fp16; there q is scaled to
+ * fp16 by a power of two per head).  A row_ctx outside [0, max_ctx], a row_req outside the block
+ * table, rows of a group with different requests, or a page id outside the pool is DSA_ERR_BOUNDS.
+ */
+int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint16_t *q, int64_t q_stride,
+                     int32_t num_heads, float sm_scale, uint16_t *out, float *lse, void *workspace,
+                     size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Workspace bytes dsa_kv_attention needs for num_rows rows of num_heads heads and contexts up to
+ * max_ctx; 0 when every row is one part. */
+size_t dsa_kv_attention_workspace_size(const dsa_kv_cache *cache, int32_t num_rows, int32_t num_heads,
+                                       int32_t max_ctx);
+
+/*
  * Failure-path self-test (no counterpart on the pages): one CTA whose
  * threads wait on a barrier that nothing ever arrives on.  The wait is the
  * bounded wait every kernel of the library uses; it gives up after the

@@ -47,6 +47,28 @@ class _Rows(ctypes.Structure):
                 ("max_ctx", ctypes.c_int32), ("rows_per_group", ctypes.c_int32)]
 
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("format", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class _RopeSpec(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class _RopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("num_heads", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
+
+
+class _KvRows(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("rot_offset", ctypes.c_int32), ("layout", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -111,6 +133,21 @@ def load_library(path: str | None = None):
                                       ctypes.c_size_t, P, P]
     lib.dsa_msa_attention_workspace_size.restype = ctypes.c_size_t
     lib.dsa_msa_attention_workspace_size.argtypes = [I32, I32]
+    D = ctypes.c_double
+    lib.dsa_rope_frequencies.restype = ctypes.c_int
+    lib.dsa_rope_frequencies.argtypes = [I32, D, I32, D, I32, P, P]
+    lib.dsa_rope_turns.restype = ctypes.c_int
+    lib.dsa_rope_turns.argtypes = [P, I32, P]
+    lib.dsa_rope.restype = ctypes.c_int
+    lib.dsa_rope.argtypes = [ctypes.POINTER(_RopeSpec), ctypes.POINTER(_RopeTensor), I32, I32, I32, P]
+    lib.dsa_kv_insert.restype = ctypes.c_int
+    lib.dsa_kv_insert.argtypes = [ctypes.POINTER(_KvCache), P, I32, ctypes.POINTER(_KvRows),
+                                  ctypes.POINTER(_RopeSpec), ctypes.POINTER(_RopeTensor), P, P]
+    lib.dsa_kv_attention.restype = ctypes.c_int
+    lib.dsa_kv_attention.argtypes = [ctypes.POINTER(_KvCache), ctypes.POINTER(_Rows), P, I64, I32, F, P, P, P,
+                                     ctypes.c_size_t, P, P]
+    lib.dsa_kv_attention_workspace_size.restype = ctypes.c_size_t
+    lib.dsa_kv_attention_workspace_size.argtypes = [ctypes.POINTER(_KvCache), I32, I32, I32]
     if path is None:
         _lib = lib
     return lib
@@ -122,7 +159,8 @@ EXPORTED = ("dsa_version", "dsa_status_string", "dsa_indexer_logits", "dsa_topk"
             "dsa_indexer_topk", "dsa_indexer_topk_workspace_size", "dsa_topk_slots", "dsa_topk_workspace_size",
             "dsa_sparse_mla_decode_prepare", "dsa_sparse_mla_decode_prepared", "dsa_msa_block_scores",
             "dsa_msa_select", "dsa_msa_attention", "dsa_msa_attention_workspace_size", "dsa_topk_slots_warm",
-            "dsa_selftest_wait_timeout")
+            "dsa_selftest_wait_timeout", "dsa_rope_frequencies", "dsa_rope_turns", "dsa_rope", "dsa_kv_insert",
+            "dsa_kv_attention", "dsa_kv_attention_workspace_size")
 HIST_BINS = 65536
 NOALLOC_MAX_ROWS = 8
 
@@ -430,6 +468,248 @@ def msa_attention(kv_pool, k_scale, v_scale, block_table, row_req, row_ctx, max_
                                           _stream(stream))
     _check(rc, "dsa_msa_attention")
     return out, lse
+
+
+# ------------------------------------------------------------------ dense K/V path
+KV_BF16, KV_FP8 = 5, 6
+DTYPE_BF16, DTYPE_FP32 = 1, 2
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROPE_MAX_TENSORS = 4
+
+
+def _host_ptr(t):
+    """Address of a contiguous host tensor."""
+    if t.is_cuda or not t.is_contiguous():
+        raise DsaError("a contiguous host tensor is needed here")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _expect(t, what, device, dtypes, shape=None):
+    """Raise unless t is a tensor on `device` of one of `dtypes` and, where given, of `shape`."""
+    if not t.is_cuda:
+        raise DsaError("libdsa takes device tensors only")
+    if t.device != device:
+        raise DsaError(f"{what} is on {t.device}, the call's other tensors on {device}")
+    if t.dtype not in dtypes:
+        raise DsaError(f"{what} has dtype {t.dtype}: expected {' or '.join(str(d) for d in dtypes)}")
+    if shape is not None and t.shape != shape:
+        raise DsaError(f"{what} has shape {tuple(t.shape)}: expected {tuple(shape)}")
+
+
+def _flat(t, what, device, dtypes, shape=None):
+    """_expect of a contiguous tensor; its address."""
+    _expect(t, what, device, dtypes, shape)
+    if not t.is_contiguous():
+        raise DsaError(f"{what} is not contiguous")
+    return t.data_ptr()
+
+
+def _launch(what, device, stream, fn, *args):
+    """fn(*args, stream) on the tensors' device, whichever device is current."""
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, (stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, (stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
+    _check(rc, what)
+
+
+_I32, _F32, _BF16 = (torch.int32,), (torch.float32,), (torch.bfloat16,)
+
+
+def rope_frequencies(rot_dim, theta, scaling="none", factor=1.0, trained_ctx=0):
+    """dsa_rope_frequencies: (radians per position of each pair, float64 host [rot_dim / 2]; scale)."""
+    if scaling not in ROPE_SCALINGS:
+        raise DsaError(f"unknown rotary scaling {scaling!r}: one of {', '.join(ROPE_SCALINGS)}")
+    freq, scale = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float64), ctypes.c_float()
+    rc = load_library().dsa_rope_frequencies(int(rot_dim), float(theta), ROPE_SCALINGS[scaling], float(factor),
+                                             int(trained_ctx), _host_ptr(freq), ctypes.byref(scale))
+    _check(rc, "dsa_rope_frequencies")
+    return freq, scale.value
+
+
+def rope_turns(inv_freq):
+    """dsa_rope_turns: float64 host [n] radians per position -> int64 host [n] (2^-64 turns, uint64 bits)."""
+    if inv_freq.dtype != torch.float64:
+        raise DsaError("rope_turns takes float64 frequencies")
+    turns = torch.empty(inv_freq.shape, dtype=torch.int64)
+    _check(load_library().dsa_rope_turns(_host_ptr(inv_freq), inv_freq.numel(), _host_ptr(turns)), "dsa_rope_turns")
+    return turns
+
+
+class RopeTable:
+    """The angles of `rope` and `kv_insert` on the device: `turns` int64 [rot_dim / 2], and `scale`."""
+
+    def __init__(self, turns, scale=1.0):
+        if turns.dtype != torch.int64 or not turns.is_cuda or not turns.is_contiguous() or turns.dim() != 1:
+            raise DsaError("RopeTable takes a contiguous int64 device vector (rope_turns)")
+        self.turns, self.scale, self.rot_dim = turns, float(scale), 2 * turns.shape[0]
+
+
+def rope_table(rot_dim, theta=10000.0, scaling="none", factor=1.0, trained_ctx=0, device="cuda"):
+    """The table of dsa_rope_frequencies' angles (for other angles: RopeTable(rope_turns(f).to(device), scale))."""
+    freq, scale = rope_frequencies(rot_dim, theta, scaling, factor, trained_ctx)
+    return RopeTable(rope_turns(freq).to(device), scale)
+
+
+def _rope_spec(table, positions, device, num_tokens):
+    if table.turns.device != device:
+        raise DsaError(f"the rotary table is on {table.turns.device}, the call's other tensors on {device}")
+    return _RopeSpec(table.turns.data_ptr(), _flat(positions, "positions", device, _I32, (num_tokens,)), table.rot_dim,
+                     table.scale)
+
+
+def _rope_tensor(x, out, layout, rot_dim, device, dtypes):
+    if x.dim() != 3 or x.shape[2] != rot_dim:
+        raise DsaError(f"rotated tensors are [tokens, heads, {rot_dim}] (a slice of larger heads): got {tuple(x.shape)}")
+    _expect(x, "x", device, dtypes)
+    st, ot = x.stride(), x.stride() if out is x else out.stride()
+    if out is not x:
+        _expect(out, "out", device, dtypes, x.shape)
+    if (st[2] != 1 or ot[2] != 1) and rot_dim > 1:
+        raise DsaError("the rotary dims of a head are contiguous")
+    return _RopeTensor(x.data_ptr(), out.data_ptr(), x.shape[1], layout, st[0], st[1], ot[0], ot[1])
+
+
+def rope(x, table, positions, layout=ROPE_INTERLEAVED, out=None, stream=None):
+    """dsa_rope: rotate x [tokens, heads, rot_dim] (bf16 or fp32; usually a slice x[..., a:a + rot_dim]) by
+    its tokens' positions, into `out` (default: in place).  x, layout and out may be lists of up to 4
+    tensors of the same tokens, rotated by one launch.  Tokens at negative positions are left alone."""
+    many = isinstance(x, (list, tuple))
+    xs = x if many else [x]
+    outs = xs if out is None else out if many else [out]
+    layouts = layout if isinstance(layout, (list, tuple)) else [layout] * len(xs)
+    if not 1 <= len(xs) <= ROPE_MAX_TENSORS or len(outs) != len(xs) or len(layouts) != len(xs):
+        raise DsaError(f"rope takes 1 to {ROPE_MAX_TENSORS} tensors, and as many layouts and outputs")
+    first = xs[0]
+    n, device, dtypes = first.shape[0], first.device, (first.dtype,)
+    if first.dtype not in (torch.bfloat16, torch.float32):
+        raise DsaError(f"rope takes bf16 or fp32 tensors: got {first.dtype}")
+    if any(t.shape[0] != n for t in xs):
+        raise DsaError("the tensors of one call have the same tokens")
+    ts = (_RopeTensor * len(xs))(*[_rope_tensor(a, b, p, table.rot_dim, device, dtypes)
+                                   for a, b, p in zip(xs, outs, layouts)])
+    spec = _rope_spec(table, positions, device, n)
+    _launch("dsa_rope", device, stream, load_library().dsa_rope, spec, ts, len(xs),
+            DTYPE_BF16 if first.dtype == torch.bfloat16 else DTYPE_FP32, n)
+    return outs if many else outs[0]
+
+
+class KvCache:
+    """A paged K/V pool [pages, kv_heads, 2 (K, V), page_size, head_dim]: bf16, or e4m3 codes (uint8 or
+    float8_e4m3fn) with their scales.  An MSA pool is one: KvCache(kv_pool.view(-1, 4, 2, 128, 128), ks, vs)."""
+
+    def __init__(self, pool, k_scale=1.0, v_scale=1.0):
+        if pool.dim() != 5 or pool.shape[2] != 2:
+            raise DsaError(f"a K/V pool is [pages, kv_heads, 2, page_size, head_dim]: got {tuple(pool.shape)}")
+        if pool.dtype not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn):
+            raise DsaError(f"a K/V pool is bf16 or e4m3 codes: got {pool.dtype}")
+        self.pool, self.k_scale, self.v_scale = pool, float(k_scale), float(v_scale)
+        self.format = KV_BF16 if pool.dtype == torch.bfloat16 else KV_FP8
+        self.num_pages, self.kv_heads, _, self.page_size, self.head_dim = pool.shape
+        self._c = _KvCache(_ptr(pool), self.format, self.page_size, self.num_pages, self.kv_heads, self.head_dim,
+                           self.k_scale, self.v_scale)
+
+
+def kv_insert(kv, slots, k, v, rope=None, positions=None, layout=ROPE_HALF, rot_offset=0, q=None, q_out=None,
+              status=None, stream=None):
+    """dsa_kv_insert: write k, v [tokens, kv_heads, head_dim] bf16 (parts of packed rows) at their slots of
+    the KvCache.  With `rope` (a RopeTable) and `positions`, K's dims [rot_offset, rot_offset + rot_dim) are
+    rotated first, and q [tokens, heads, rot_dim] too, into q_out (default: in place).  Returns q_out."""
+    n, device = slots.shape[0], kv.pool.device
+    shape = (n, kv.kv_heads, kv.head_dim)
+    for t, what in ((k, "k"), (v, "v")):
+        _expect(t, what, device, _BF16, shape)
+        st = t.stride()
+        if st[2] != 1 or (st[1] != kv.head_dim and kv.kv_heads > 1):
+            raise DsaError(f"the heads of a token of {what} are packed")
+    width = kv.kv_heads * kv.head_dim
+    rows = _KvRows(k.data_ptr(), v.data_ptr(), max(k.stride(0), width) if n <= 1 else k.stride(0),
+                   max(v.stride(0), width) if n <= 1 else v.stride(0), rot_offset, layout)
+    spec = qt = None
+    if rope is not None:
+        if positions is None:
+            raise DsaError("rope needs positions")
+        spec = _rope_spec(rope, positions, device, n)
+        if q is not None:
+            q_out = q if q_out is None else q_out
+            if q.shape[0] != n:
+                raise DsaError("q has the tokens of k and v")
+            qt = _rope_tensor(q, q_out, layout, rope.rot_dim, device, _BF16)
+    elif q is not None:
+        raise DsaError("q is rotated only: it needs rope")
+    _launch("dsa_kv_insert", device, stream, load_library().dsa_kv_insert, kv._c,
+            _flat(slots, "slots", device, _I32), n, rows, spec, qt,
+            None if status is None else _flat(status, "status", device, _I32))
+    return q_out
+
+
+def kv_attention_workspace_size(kv, num_rows, num_heads, max_ctx) -> int:
+    return int(load_library().dsa_kv_attention_workspace_size(kv._c, int(num_rows), int(num_heads), int(max_ctx)))
+
+
+def kv_attention(kv, block_table, row_req, row_ctx, max_ctx, q, sm_scale=None, rows_per_group=1, out=None, lse=None,
+                 workspace=None, status=None, stream=None):
+    """dsa_kv_attention: (out bf16 [R, H, head_dim], lse fp32 [R, H]) of q bf16 [R, H, head_dim] (heads packed)
+    over the KvCache's tokens below row_ctx; sm_scale defaults to 1 / sqrt(head_dim)."""
+    R, H, D = q.shape
+    device = kv.pool.device
+    _expect(q, "q", device, _BF16, (R, H, kv.head_dim))
+    st = q.stride()
+    if st[2] != 1 or (st[1] != D and H > 1):
+        raise DsaError("the heads of a row of q are packed")
+    if block_table.dim() != 2:
+        raise DsaError("the block table is [requests, pages]")
+    if out is None:
+        out = torch.empty((R, H, D), dtype=torch.bfloat16, device=device)
+    if lse is None:
+        lse = torch.empty((R, H), dtype=torch.float32, device=device)
+    if workspace is None:
+        need = kv_attention_workspace_size(kv, R, H, max_ctx)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    rows = _Rows(_flat(block_table, "block_table", device, _I32), block_table.shape[1], block_table.shape[0],
+                 _flat(row_req, "row_req", device, _I32, (R,)), _flat(row_ctx, "row_ctx", device, _I32, (R,)), R,
+                 int(max_ctx), int(rows_per_group))
+    wp, wb = (None, 0) if workspace is None else (_flat(workspace, "workspace", device, (workspace.dtype,)),
+                                                  workspace.numel() * workspace.element_size())
+    _launch("dsa_kv_attention", device, stream, load_library().dsa_kv_attention, kv._c, rows, q.data_ptr(),
+            st[0] if R > 1 else H * D, H, D ** -0.5 if sm_scale is None else float(sm_scale),
+            _flat(out, "out", device, _BF16, (R, H, D)), _flat(lse, "lse", device, _F32, (R, H)), wp, wb,
+            None if status is None else _flat(status, "status", device, _I32))
+    return out, lse
+
+
+class KvLayer:
+    """One full-attention layer's step over a resident K/V pool: rotate q and k, insert k and v, attend.
+
+    Buffers are allocated once per shape and reused, so repeated calls (and CUDA-graph capture of `run`)
+    allocate nothing.  Rows are the step's new tokens; a padding row has position -1, slot -1, context 0.
+    """
+
+    def __init__(self, kv, block_table, max_ctx, num_rows, num_heads, rope=None, layout=ROPE_HALF, rot_offset=0,
+                 rows_per_group=1, sm_scale=None):
+        self.kv, self.block_table, self.max_ctx = kv, block_table, int(max_ctx)
+        self.rope, self.layout, self.rot_offset = rope, layout, int(rot_offset)
+        self.rows_per_group, self.sm_scale = rows_per_group, sm_scale
+        R, H, device = int(num_rows), int(num_heads), kv.pool.device
+        self.out = torch.empty((R, H, kv.head_dim), dtype=torch.bfloat16, device=device)
+        self.lse = torch.empty((R, H), dtype=torch.float32, device=device)
+        need = kv_attention_workspace_size(kv, R, H, self.max_ctx)
+        self.workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        self.status = new_status(device)
+
+    def run(self, row_req, row_ctx, slots, positions, q, k, v, stream=None):
+        """q [R, H, head_dim] is rotated in place; returns (out, lse)."""
+        if self.rope is None:
+            kv_insert(self.kv, slots, k, v, status=self.status, stream=stream)
+        else:
+            part = q[..., self.rot_offset:self.rot_offset + self.rope.rot_dim]
+            kv_insert(self.kv, slots, k, v, rope=self.rope, positions=positions, layout=self.layout,
+                      rot_offset=self.rot_offset, q=part, status=self.status, stream=stream)
+        return kv_attention(self.kv, self.block_table, row_req, row_ctx, self.max_ctx, q, self.sm_scale,
+                            self.rows_per_group, out=self.out, lse=self.lse, workspace=self.workspace,
+                            status=self.status, stream=stream)
 
 
 class Layer:

@@ -573,4 +573,220 @@ int dsa_msa_attention(const void *kv_pool, int64_t num_pages, float k_scale, flo
     return launch_status(launch_msa_attention(kv_map, q_map, a, rows->num_rows, static_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------------------------------ dense K/V path
+
+int dsa_rope_frequencies(int32_t rot_dim, double theta, int32_t scaling, double factor, int32_t trained_ctx,
+                         double *inv_freq, float *scale) {
+    if (rot_dim < 2 || rot_dim % 2 != 0 || inv_freq == nullptr || scale == nullptr) return DSA_ERR_INVALID_ARG;
+    if (rot_dim > DSA_ROPE_MAX_DIM) return DSA_ERR_UNSUPPORTED;
+    if (!std::isfinite(theta) || !(theta > 1.0)) return DSA_ERR_INVALID_ARG;
+    if (scaling < DSA_ROPE_SCALE_NONE || scaling > DSA_ROPE_SCALE_YARN) return DSA_ERR_UNSUPPORTED;
+    if (scaling != DSA_ROPE_SCALE_NONE && (!std::isfinite(factor) || !(factor >= 1.0))) return DSA_ERR_INVALID_ARG;
+    if (scaling == DSA_ROPE_SCALE_YARN && trained_ctx < 1) return DSA_ERR_INVALID_ARG;
+    const double base = scaling == DSA_ROPE_SCALE_NTK
+                            ? theta * std::pow(factor, static_cast<double>(rot_dim) / (rot_dim > 2 ? rot_dim - 2 : 1))
+                            : theta;
+    if (!std::isfinite(base)) return DSA_ERR_INVALID_ARG;
+    double lo = 0.0, hi = 0.0;
+    if (scaling == DSA_ROPE_SCALE_YARN) {
+        auto pair_of = [&](double turns) {
+            return rot_dim * std::log(trained_ctx / (turns * 2.0 * M_PI)) / (2.0 * std::log(theta));
+        };
+        lo = std::fmax(std::floor(pair_of(32.0)), 0.0);
+        hi = std::fmin(std::ceil(pair_of(1.0)), static_cast<double>(rot_dim - 1));
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rot_dim);
+        if (scaling == DSA_ROPE_SCALE_LINEAR) {
+            inv_freq[i] = f / factor;
+        } else if (scaling == DSA_ROPE_SCALE_YARN) {
+            const double r = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+            inv_freq[i] = f * (1.0 - r) + f / factor * r;
+        } else {
+            inv_freq[i] = f;
+        }
+    }
+    *scale = scaling == DSA_ROPE_SCALE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return DSA_OK;
+}
+
+int dsa_rope_turns(const double *inv_freq, int32_t num_pairs, uint64_t *turns) {
+    if (num_pairs < 0) return DSA_ERR_INVALID_ARG;
+    if (num_pairs > 0 && (inv_freq == nullptr || turns == nullptr)) return DSA_ERR_INVALID_ARG;
+    for (int i = 0; i < num_pairs; ++i)
+        if (!std::isfinite(inv_freq[i])) return DSA_ERR_INVALID_ARG;
+    for (int i = 0; i < num_pairs; ++i) {
+        double x = inv_freq[i] / (2.0 * M_PI);
+        x -= std::floor(x);  // in [0, 1]: a tiny negative angle can round to a whole turn
+        turns[i] = x < 1.0 ? static_cast<uint64_t>(std::ldexp(x, 64)) : 0;
+    }
+    return DSA_OK;
+}
+
+static int check_rope_spec(const dsa_rope_spec *rope) {
+    if (rope == nullptr || rope->turns == nullptr || rope->positions == nullptr) return DSA_ERR_INVALID_ARG;
+    if (rope->rot_dim < 2 || rope->rot_dim % 2 != 0 || !std::isfinite(rope->scale)) return DSA_ERR_INVALID_ARG;
+    return rope->rot_dim > DSA_ROPE_MAX_DIM ? DSA_ERR_UNSUPPORTED : DSA_OK;
+}
+
+// One rotated tensor, and whether 16-byte accesses reach all of its rotary parts.
+static int rope_tensor(const dsa_rope_tensor &t, int32_t rot, int elem, RopeTensor *out) {
+    if (t.x == nullptr || t.out == nullptr || t.num_heads < 1) return DSA_ERR_INVALID_ARG;
+    if (t.layout != DSA_ROPE_INTERLEAVED && t.layout != DSA_ROPE_HALF) return DSA_ERR_UNSUPPORTED;
+    if (t.num_heads > kRopeMaxHeads) return DSA_ERR_UNSUPPORTED;
+    if (!aligned(t.x, elem) || !aligned(t.out, elem)) return DSA_ERR_INVALID_ARG;
+    if (t.x == t.out && (t.x_token_stride != t.out_token_stride || t.x_head_stride != t.out_head_stride))
+        return DSA_ERR_INVALID_ARG;
+    if (t.x_token_stride < 0 || t.x_head_stride < 0 || t.out_token_stride < 0 || t.out_head_stride < 0)
+        return DSA_ERR_INVALID_ARG;
+    const bool half = t.layout == DSA_ROPE_HALF;
+    const int64_t v = 16 / elem;
+    const bool vec = aligned(t.x, 16) && aligned(t.out, 16) && (half ? rot / 2 : rot) % v == 0 &&
+                     t.x_token_stride % v == 0 && t.x_head_stride % v == 0 && t.out_token_stride % v == 0 &&
+                     t.out_head_stride % v == 0;
+    *out = RopeTensor{t.x, t.out, t.num_heads, half, vec, t.x_token_stride, t.x_head_stride, t.out_token_stride,
+                      t.out_head_stride};
+    return DSA_OK;
+}
+
+int dsa_rope(const dsa_rope_spec *rope, const dsa_rope_tensor *tensors, int32_t num_tensors, int32_t dtype,
+             int32_t num_tokens, void *stream) {
+    if (num_tokens < 0 || num_tensors < 1) return DSA_ERR_INVALID_ARG;
+    if (num_tensors > DSA_ROPE_MAX_TENSORS) return DSA_ERR_UNSUPPORTED;
+    if (dtype != DSA_DTYPE_BF16 && dtype != DSA_DTYPE_FP32) return DSA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return DSA_OK;
+    int rc = check_rope_spec(rope);
+    if (rc != DSA_OK) return rc;
+    if (tensors == nullptr) return DSA_ERR_INVALID_ARG;
+    RopeArgs a = {rope->turns, rope->positions, rope->rot_dim, rope->scale, num_tokens, num_tensors, {}};
+    for (int i = 0; i < num_tensors; ++i) {
+        rc = rope_tensor(tensors[i], rope->rot_dim, dtype == DSA_DTYPE_BF16 ? 2 : 4, &a.t[i]);
+        if (rc != DSA_OK) return rc;
+    }
+    return launch_status(launch_rope(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+// Geometry and address of a K/V pool.
+static int check_kv_cache(const dsa_kv_cache *c) {
+    if (c == nullptr) return DSA_ERR_INVALID_ARG;
+    if (c->format != DSA_KV_BF16 && c->format != DSA_KV_FP8) return DSA_ERR_UNSUPPORTED;
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+        return DSA_ERR_UNSUPPORTED;
+    if (c->head_dim != 64 && c->head_dim != 128) return DSA_ERR_UNSUPPORTED;
+    if (c->kv_heads < 1 || c->num_pages <= 0) return DSA_ERR_INVALID_ARG;
+    if (c->kv_heads > kKvMaxHeads) return DSA_ERR_UNSUPPORTED;
+    if (c->num_pages >= (1ll << 31) / (2ll * c->kv_heads * c->page_size)) return DSA_ERR_UNSUPPORTED;
+    if (c->format == DSA_KV_FP8)
+        for (float v : {c->k_scale, c->v_scale})
+            if (!std::isfinite(v) || !(v > 0.f)) return DSA_ERR_INVALID_ARG;
+    return DSA_OK;
+}
+
+int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_tokens, const dsa_kv_rows *kv,
+                  const dsa_rope_spec *rope, const dsa_rope_tensor *q, int32_t *dev_status, void *stream) {
+    int rc = check_kv_cache(cache);
+    if (rc != DSA_OK) return rc;
+    if (num_tokens < 0) return DSA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return DSA_OK;
+    if (!cache->base || !aligned(cache->base, 16) || !slots || !kv || !kv->k || !kv->v) return DSA_ERR_INVALID_ARG;
+    const int64_t width = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
+    if (kv->k_stride < width || kv->v_stride < width) return DSA_ERR_INVALID_ARG;
+    if (!aligned(kv->k, 2) || !aligned(kv->v, 2)) return DSA_ERR_INVALID_ARG;
+    if (q != nullptr && rope == nullptr) return DSA_ERR_INVALID_ARG;
+    KvInsertArgs a = {};
+    a.rope.num_tokens = num_tokens;
+    if (rope != nullptr) {
+        rc = check_rope_spec(rope);
+        if (rc != DSA_OK) return rc;
+        if (kv->rot_offset < 0 || kv->rot_offset > cache->head_dim - rope->rot_dim) return DSA_ERR_INVALID_ARG;
+        if (kv->layout != DSA_ROPE_INTERLEAVED && kv->layout != DSA_ROPE_HALF) return DSA_ERR_UNSUPPORTED;
+        a.rope.turns = rope->turns;
+        a.rope.positions = rope->positions;
+        a.rope.rot = rope->rot_dim;
+        a.rope.scale = rope->scale;
+        a.rot_offset = kv->rot_offset;
+        a.half = kv->layout == DSA_ROPE_HALF;
+        if (q != nullptr) {
+            a.rope.num_tensors = 1;
+            rc = rope_tensor(*q, rope->rot_dim, 2, &a.rope.t[0]);
+            if (rc != DSA_OK) return rc;
+        }
+    }
+    // 16-byte pieces need aligned rows, and rotary parts (or halves) of whole pieces
+    a.vec = aligned(kv->k, 16) && aligned(kv->v, 16) && kv->k_stride % 8 == 0 && kv->v_stride % 8 == 0 &&
+            a.rot_offset % 8 == 0 && a.rope.rot % (a.half ? 16 : 8) == 0;
+    a.pool = static_cast<uint8_t *>(cache->base);
+    a.fp8 = cache->format == DSA_KV_FP8;
+    a.page_size = cache->page_size;
+    a.num_slots = cache->num_pages * cache->page_size;
+    a.kv_heads = cache->kv_heads;
+    a.head_dim = cache->head_dim;
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    a.slots = slots;
+    a.k = kv->k;
+    a.v = kv->v;
+    a.k_stride = kv->k_stride;
+    a.v_stride = kv->v_stride;
+    a.status = dev_status;
+    return launch_status(launch_kv_insert(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t dsa_kv_attention_workspace_size(const dsa_kv_cache *cache, int32_t num_rows, int32_t num_heads,
+                                       int32_t max_ctx) {
+    if (check_kv_cache(cache) != DSA_OK || num_rows <= 0 || num_heads <= 0 || max_ctx <= 0) return 0;
+    return kv_attention_workspace_bytes(num_rows, num_heads, cache->kv_heads, cache->head_dim, max_ctx);
+}
+
+int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint16_t *q, int64_t q_stride,
+                     int32_t num_heads, float sm_scale, uint16_t *out, float *lse, void *workspace,
+                     size_t workspace_bytes, int32_t *dev_status, void *stream) {
+    int rc = check_kv_cache(cache);
+    if (rc != DSA_OK) return rc;
+    if (rows == nullptr || rows->num_rows < 0 || rows->max_ctx < 0 || rows->num_requests < 0)
+        return DSA_ERR_INVALID_ARG;
+    const int G = rows->rows_per_group;
+    if (G != 1 && G != 2 && G != 4 && G != 8) return DSA_ERR_UNSUPPORTED;
+    if (num_heads < 1 || num_heads % cache->kv_heads != 0 || rows->num_rows % G != 0) return DSA_ERR_INVALID_ARG;
+    if (num_heads / cache->kv_heads > DSA_KV_MAX_HPG) return DSA_ERR_UNSUPPORTED;
+    if (!std::isfinite(sm_scale) || !(sm_scale > 0.f)) return DSA_ERR_INVALID_ARG;
+    if (rows->num_rows == 0) return DSA_OK;
+    if (!rows->block_table || !rows->row_req || !rows->row_ctx || !q || !out) return DSA_ERR_INVALID_ARG;
+    if (!cache->base || !aligned(cache->base, 16) || !aligned(q, 16) || !aligned(out, 16)) return DSA_ERR_INVALID_ARG;
+    if (q_stride < static_cast<int64_t>(num_heads) * cache->head_dim || q_stride % 8 != 0) return DSA_ERR_INVALID_ARG;
+    const int64_t need_pages = (static_cast<int64_t>(rows->max_ctx) + cache->page_size - 1) / cache->page_size;
+    if (rows->bt_stride < need_pages) return DSA_ERR_INVALID_ARG;
+    const size_t need = kv_attention_workspace_bytes(rows->num_rows, num_heads, cache->kv_heads, cache->head_dim,
+                                                     rows->max_ctx);
+    if (need > 0) {
+        if (workspace == nullptr || workspace_bytes < need) return DSA_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return DSA_ERR_INVALID_ARG;
+    }
+    const bool fp8 = cache->format == DSA_KV_FP8;
+    KvAttnArgs a = {};
+    a.pool = static_cast<const uint8_t *>(cache->base);
+    a.fp8 = fp8;
+    a.page_size = cache->page_size;
+    a.num_pages = cache->num_pages;
+    a.kv_heads = cache->kv_heads;
+    a.head_dim = cache->head_dim;
+    a.block_table = rows->block_table;
+    a.bt_stride = rows->bt_stride;
+    a.num_requests = rows->num_requests;
+    a.row_req = rows->row_req;
+    a.row_ctx = rows->row_ctx;
+    a.num_rows = rows->num_rows;
+    a.max_ctx = rows->max_ctx;
+    a.group = G;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.num_heads = num_heads;
+    a.s_scale = static_cast<float>(static_cast<double>(sm_scale) * (fp8 ? cache->k_scale : 1.0) * 1.4426950408889634);
+    a.v_scale = fp8 ? cache->v_scale : 1.0f;
+    a.out = out;
+    a.lse = lse;
+    a.status = dev_status;
+    return launch_status(launch_kv_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -264,6 +264,77 @@ struct InsertArgs {
 
 cudaError_t launch_cache_insert(const InsertArgs &a, cudaStream_t s);
 
+// ---- dense K/V path (rope.cu, kv_attention.cu)
+constexpr int kRopeMaxHeads = 4096;  // heads of a rotated tensor
+constexpr int kKvMaxHeads = 256;     // KV heads of a pool
+
+struct RopeTensor {
+    const void *x;
+    void *out;
+    int32_t heads;
+    bool half;     // pairs (i, i + rot / 2) instead of (2i, 2i + 1)
+    bool vec;      // 16-byte accesses fit its base addresses, strides and pair layout
+    int64_t x_token, x_head, out_token, out_head;  // strides in elements
+};
+
+struct RopeArgs {
+    const uint64_t *turns;
+    const int32_t *positions;
+    int32_t rot;
+    float scale;
+    int32_t num_tokens;
+    int32_t num_tensors;
+    RopeTensor t[DSA_ROPE_MAX_TENSORS];
+};
+
+struct KvInsertArgs {
+    RopeArgs rope;  // num_tensors 1: q is rotated too; rot 0: nothing is rotated
+    uint8_t *pool;
+    bool fp8;
+    int32_t page_size;
+    int64_t num_slots;
+    int32_t kv_heads, head_dim;
+    float k_scale, v_scale;
+    const int32_t *slots;
+    const uint16_t *k, *v;
+    int64_t k_stride, v_stride;
+    int32_t rot_offset;
+    bool half;
+    bool vec;
+    int32_t *status;
+};
+
+cudaError_t launch_rope(const RopeArgs &a, int32_t dtype, cudaStream_t s);
+cudaError_t launch_kv_insert(const KvInsertArgs &a, cudaStream_t s);
+
+struct KvAttnArgs {
+    const uint8_t *pool;
+    bool fp8;
+    int32_t page_size;
+    int64_t num_pages;
+    int32_t kv_heads, head_dim;
+    const int32_t *block_table;
+    int64_t bt_stride;
+    int32_t num_requests;
+    const int32_t *row_req;
+    const int32_t *row_ctx;
+    int32_t num_rows;
+    int32_t max_ctx;
+    int32_t group;     // rows per group
+    const uint16_t *q;
+    int64_t q_stride;
+    int32_t num_heads;
+    float s_scale;     // sm_scale * k_scale * log2(e)
+    float v_scale;
+    uint16_t *out;
+    float *lse;
+    int32_t *status;
+};
+
+cudaError_t launch_kv_attention(const KvAttnArgs &a, cudaStream_t s);
+size_t kv_attention_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
+                                    int32_t max_ctx);
+
 int device_sm_count();
 
 }  // namespace dsa
