@@ -447,7 +447,8 @@ size_t dsa_msa_attention_workspace_size(int32_t num_rows, int32_t heads_per_grou
  */
 #define DSA_KV_BF16 5
 #define DSA_KV_FP8 6
-#define DSA_KV_MAX_HPG 128 /* query heads per KV head */
+#define DSA_KV_MAX_HPG 128          /* query heads per KV head */
+#define DSA_KV_MAX_CTX (1 << 30)    /* max_ctx of dsa_kv_attention */
 
 typedef struct dsa_kv_cache {
     void *base;         /* device, 16-byte aligned */

@@ -50,6 +50,22 @@ bool encode_rows128(CUtensorMap *map, const void *base, uint64_t rows, uint32_t 
     return r == CUDA_SUCCESS;
 }
 
+// 2D byte tensor [rows, row_bytes] of a K/V pool (64, 128 or 256 bytes a row) with a box of box_rows rows by
+// one swizzle span (64 or 128 bytes).
+bool encode_kv_rows(CUtensorMap *map, const void *base, uint64_t rows, uint32_t row_bytes, uint32_t box_rows) {
+    auto enc = get_encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[2] = {row_bytes, rows};
+    const cuuint64_t strides[1] = {row_bytes};
+    const cuuint32_t box[2] = {row_bytes < 128 ? row_bytes : 128, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     row_bytes < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // 2D tensor of 4-bit values [rows, 128] with 64-byte rows (MXFP4 index keys), a [box_rows, 128]
 // box landing in shared memory as 128-byte rows (each 16 values in the low 8 bytes of a 16-byte
 // unit, the layout 4-bit tensor-core operands take), 128-byte swizzle.  Base: 32-byte aligned.
@@ -735,6 +751,7 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
 size_t dsa_kv_attention_workspace_size(const dsa_kv_cache *cache, int32_t num_rows, int32_t num_heads,
                                        int32_t max_ctx) {
     if (check_kv_cache(cache) != DSA_OK || num_rows <= 0 || num_heads <= 0 || max_ctx <= 0) return 0;
+    if (max_ctx > DSA_KV_MAX_CTX) return 0;
     return kv_attention_workspace_bytes(num_rows, num_heads, cache->kv_heads, cache->head_dim, max_ctx);
 }
 
@@ -748,7 +765,7 @@ int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint
     const int G = rows->rows_per_group;
     if (G != 1 && G != 2 && G != 4 && G != 8) return DSA_ERR_UNSUPPORTED;
     if (num_heads < 1 || num_heads % cache->kv_heads != 0 || rows->num_rows % G != 0) return DSA_ERR_INVALID_ARG;
-    if (num_heads / cache->kv_heads > DSA_KV_MAX_HPG) return DSA_ERR_UNSUPPORTED;
+    if (num_heads / cache->kv_heads > DSA_KV_MAX_HPG || rows->max_ctx > DSA_KV_MAX_CTX) return DSA_ERR_UNSUPPORTED;
     if (!std::isfinite(sm_scale) || !(sm_scale > 0.f)) return DSA_ERR_INVALID_ARG;
     if (rows->num_rows == 0) return DSA_OK;
     if (!rows->block_table || !rows->row_req || !rows->row_ctx || !q || !out) return DSA_ERR_INVALID_ARG;
@@ -764,7 +781,6 @@ int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint
     }
     const bool fp8 = cache->format == DSA_KV_FP8;
     KvAttnArgs a = {};
-    a.pool = static_cast<const uint8_t *>(cache->base);
     a.fp8 = fp8;
     a.page_size = cache->page_size;
     a.num_pages = cache->num_pages;
@@ -786,7 +802,12 @@ int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint
     a.out = out;
     a.lse = lse;
     a.status = dev_status;
-    return launch_status(launch_kv_attention(a, static_cast<cudaStream_t>(stream)));
+    CUtensorMap kv_map;
+    const uint64_t kv_rows = static_cast<uint64_t>(cache->num_pages) * cache->kv_heads * 2 * cache->page_size;
+    if (!encode_kv_rows(&kv_map, cache->base, kv_rows, static_cast<uint32_t>(cache->head_dim * (fp8 ? 1 : 2)),
+                        static_cast<uint32_t>(kv_box_rows(cache->page_size))))
+        return DSA_ERR_CUDA;
+    return launch_status(launch_kv_attention(kv_map, a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -308,7 +308,6 @@ cudaError_t launch_rope(const RopeArgs &a, int32_t dtype, cudaStream_t s);
 cudaError_t launch_kv_insert(const KvInsertArgs &a, cudaStream_t s);
 
 struct KvAttnArgs {
-    const uint8_t *pool;
     bool fp8;
     int32_t page_size;
     int64_t num_pages;
@@ -329,9 +328,17 @@ struct KvAttnArgs {
     uint16_t *out;
     float *lse;
     int32_t *status;
+    // set by launch_kv_attention
+    int32_t max_parts;    // parts of the longest contexts
+    int32_t parts_bound;  // parts of a row at most, for contexts up to max_ctx
+    int32_t col_blocks;   // CTAs side by side over the columns (group x query heads per KV head)
+    float *part_o;        // [R, H, parts_bound, D] the parts' outputs, in their own bases
+    float2 *part_ml;      // [R, H, parts_bound] their bases (log2 units) and sums
 };
 
-cudaError_t launch_kv_attention(const KvAttnArgs &a, cudaStream_t s);
+// kv_map: the pool as rows of head_dim elements, boxes of kv_box_rows(page_size) rows by at most 128 bytes.
+cudaError_t launch_kv_attention(const CUtensorMap &kv_map, KvAttnArgs &a, void *workspace, cudaStream_t s);
+int kv_box_rows(int32_t page_size);
 size_t kv_attention_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
                                     int32_t max_ctx);
 

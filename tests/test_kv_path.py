@@ -168,6 +168,21 @@ def test_attention_refusals(lib):
         assert call(**bad) == P.ERR_INVALID_ARG, bad
     assert call(heads=4 * 129, stride=1 << 20) == P.ERR_UNSUPPORTED
     assert call(rw=rows(n=3, g=3)) == P.ERR_UNSUPPORTED
+    assert call(rw=rows(ctx=(1 << 30) + 1, stride=1 << 28)) == P.ERR_UNSUPPORTED
+    long = rows(ctx=1 << 20, stride=1 << 14)
+    need = lib.dsa_kv_attention_workspace_size(kv(), 1, 64, 1 << 20)
+    assert need > 0
+    assert call(rw=long, ws=None, wb=0) == P.ERR_WORKSPACE
+    assert call(rw=long, wb=need - 1) == P.ERR_WORKSPACE
+    assert call(rw=long, ws=FAKE + 16) == P.ERR_INVALID_ARG
+
+
+def test_workspace_size_is_host_logic(lib):
+    size = lambda n, h, ctx: lib.dsa_kv_attention_workspace_size(kv(), n, h, ctx)  # noqa: E731
+    assert size(0, 64, 4096) == 0 and size(4, 0, 4096) == 0 and size(4, 64, 0) == 0
+    assert size(4, 64, 1) == 0  # one part: nothing to merge
+    assert size(8, 64, 131072) >= 2 * 8 * 64 * 128 * 4
+    assert all(size(2, 64, n) <= size(2, 64, n + 128) for n in range(1, 300000, 4999))
 
 
 # ------------------------------------------------------------------ the binding
