@@ -50,22 +50,6 @@ bool encode_rows128(CUtensorMap *map, const void *base, uint64_t rows, uint32_t 
     return r == CUDA_SUCCESS;
 }
 
-// 2D byte tensor [rows, row_bytes] of a K/V pool (64, 128 or 256 bytes a row) with a box of box_rows rows by
-// one swizzle span (64 or 128 bytes).
-bool encode_kv_rows(CUtensorMap *map, const void *base, uint64_t rows, uint32_t row_bytes, uint32_t box_rows) {
-    auto enc = get_encoder();
-    if (enc == nullptr) return false;
-    const cuuint64_t dims[2] = {row_bytes, rows};
-    const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {row_bytes < 128 ? row_bytes : 128, box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     row_bytes < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
 // 2D tensor of 4-bit values [rows, 128] with 64-byte rows (MXFP4 index keys), a [box_rows, 128]
 // box landing in shared memory as 128-byte rows (each 16 values in the low 8 bytes of a 16-byte
 // unit, the layout 4-bit tensor-core operands take), 128-byte swizzle.  Base: 32-byte aligned.
@@ -100,6 +84,22 @@ int launch_status(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CU
 
 bool encode_rows128_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows) {
     return encode_rows128(map, base, rows, box_rows);
+}
+
+// 2D byte tensor [rows, row_bytes] of a K/V pool (64, 128 or 256 bytes a row) with a box of box_rows rows by
+// one swizzle span (64 or 128 bytes).
+bool encode_kv_rows_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t row_bytes, uint32_t box_rows) {
+    auto enc = get_encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[2] = {row_bytes, rows};
+    const cuuint64_t strides[1] = {row_bytes};
+    const cuuint32_t box[2] = {row_bytes < 128 ? row_bytes : 128, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     row_bytes < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
 }
 
 int device_sm_count() {
@@ -781,6 +781,8 @@ int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint
     }
     const bool fp8 = cache->format == DSA_KV_FP8;
     KvAttnArgs a = {};
+    a.pool = cache->base;
+    a.pool_rows = static_cast<uint64_t>(cache->num_pages) * cache->kv_heads * 2 * cache->page_size;
     a.fp8 = fp8;
     a.page_size = cache->page_size;
     a.num_pages = cache->num_pages;
@@ -802,12 +804,7 @@ int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint
     a.out = out;
     a.lse = lse;
     a.status = dev_status;
-    CUtensorMap kv_map;
-    const uint64_t kv_rows = static_cast<uint64_t>(cache->num_pages) * cache->kv_heads * 2 * cache->page_size;
-    if (!encode_kv_rows(&kv_map, cache->base, kv_rows, static_cast<uint32_t>(cache->head_dim * (fp8 ? 1 : 2)),
-                        static_cast<uint32_t>(kv_box_rows(cache->page_size))))
-        return DSA_ERR_CUDA;
-    return launch_status(launch_kv_attention(kv_map, a, workspace, static_cast<cudaStream_t>(stream)));
+    return launch_status(launch_kv_attention(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -308,6 +308,8 @@ cudaError_t launch_rope(const RopeArgs &a, int32_t dtype, cudaStream_t s);
 cudaError_t launch_kv_insert(const KvInsertArgs &a, cudaStream_t s);
 
 struct KvAttnArgs {
+    const void *pool;
+    uint64_t pool_rows;   // of head_dim elements
     bool fp8;
     int32_t page_size;
     int64_t num_pages;
@@ -331,14 +333,17 @@ struct KvAttnArgs {
     // set by launch_kv_attention
     int32_t max_parts;    // parts of the longest contexts
     int32_t parts_bound;  // parts of a row at most, for contexts up to max_ctx
-    int32_t col_blocks;   // CTAs side by side over the columns (group x query heads per KV head)
+    int32_t col_blocks;   // items side by side over the columns (group x query heads per KV head)
+    uint32_t items;       // (row group, KV head, column block, part)
     float *part_o;        // [R, H, parts_bound, D] the parts' outputs, in their own bases
     float2 *part_ml;      // [R, H, parts_bound] their bases (log2 units) and sums
 };
 
-// kv_map: the pool as rows of head_dim elements, boxes of kv_box_rows(page_size) rows by at most 128 bytes.
-cudaError_t launch_kv_attention(const CUtensorMap &kv_map, KvAttnArgs &a, void *workspace, cudaStream_t s);
-int kv_box_rows(int32_t page_size);
+cudaError_t launch_kv_attention(KvAttnArgs &a, void *workspace, cudaStream_t s);
+
+// 2D byte tensor [rows, row_bytes] (64, 128 or 256 bytes a row) with a box of box_rows rows by one swizzle
+// span of 64 or 128 bytes (api.cu).
+bool encode_kv_rows_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t row_bytes, uint32_t box_rows);
 size_t kv_attention_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
                                     int32_t max_ctx);
 

@@ -6,28 +6,32 @@
 // columns of one KV head, N = rows of the group x query heads per KV head, at 4 D FLOP each, so 16
 // columns need 16 to 32 FLOP per byte: about 100 to 215 TFLOP/s at the HBM's rate.
 //
-// Split: one CTA per (row group, KV head, part of the context); the part's size goes by the group's
+// Split: an item is a (row group, KV head, part of the context); the part's size goes by the group's
 // context alone (kv_part), so a row's bits do not depend on its batch.  A part's (base, sum, output)
-// goes to the workspace in fp32 and kv_combine_kernel merges a row's parts by log-sum-exp.
+// goes to the workspace in fp32 and kv_combine_kernel merges a row's parts by log-sum-exp.  Two
+// persistent CTAs per SM take the items in turn, so that one item's K and V stream in while the one
+// before it is merged and written.
 //
-// In a CTA a producer warp streams 64-token tiles of K and V by TMA into a ring of stages, and four
-// consumer warps share out the columns (16 each) and the tile's tokens.  Each consumer is on its own:
-// it waits for a stage, takes its 16-token steps through
-//     S = Q K^T      mma m16n8k16, the 16 columns on M, Q in registers for the whole part
+// In a CTA a producer warp streams tiles of K and V by TMA into a ring of stages, a query warp brings
+// each item's queries as MMA fragments, and four consumer warps share out the columns (16 each) and
+// the tile's tokens.  Each consumer is on its own: it waits for a stage, takes its 16- or 32-token
+// steps through
+//     S = Q K^T      the 16 columns on M, Q in registers for the whole item
 //     P = 2^(S - b)  b a lazy base: it moves (and the output is rescaled) only when a score exceeds it
 //                    by 15, so that most steps need no reduction across lanes
 //     O^T += V^T P^T mma m16n8k16, 16 of the D dims on M; S's accumulator layout is this product's
 //                    B operand as it stands, so P never leaves the registers
-// and releases the stage; nothing synchronises the consumers until the part's end.  The contraction
-// per byte is small enough that warp-level MMAs keep up with the HBM (2 cycles per SM for an m16n8k16
-// measured; 64 of them per 16 tokens and 16 columns of a bf16 pool against the 356 cycles its 8 KB
-// take), and they leave the running sums in registers: no TMEM round trip per tile.
+// and releases the stage.  The contraction per byte is small enough that warp-level MMAs keep up with
+// the HBM (2 cycles per SM for an m16n8k16 measured; the 48 of them per 16
+// tokens and 16 columns of a bf16 pool against the 356 cycles its 8 KB take), and they leave the
+// running sums in registers: no TMEM round trip per tile.
 //
 // Precision.  bf16 pool: products are exact in fp32; a weight rounded to bf16 (2^-9) would add as much
 // error as rounding the output does, so P enters as hi + lo bf16 terms (2^-17).  FP8 pool: e4m3 codes
 // are exact in fp16; q is scaled by a power of two per column to fit fp16's range (exact but for
 // elements 2^-25 below the column's largest), P is one fp16 term (2^-12), scaled by 2^7 so that weights
-// down to 2^-21 of the base stay normal.
+// down to 2^-21 of the base stay normal.  (mma.sync on e4m3 operands was tried for S: the warps spend their time in
+// branches and instruction fetches there, 178 us against 108 us for 16 x 16K.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -41,10 +45,9 @@ namespace dsa {
 
 namespace {
 
-constexpr int kConsumers = 4;                     // consumer warps
-constexpr int kThreads = 32 * (kConsumers + 1);   // and the producer
-constexpr int kTile = 64;                         // tokens of a stage
-constexpr int kStep = 16;                         // tokens of an MMA step
+constexpr int kConsumers = 4;                    // consumer warps
+constexpr int kProducer = 4, kQuery = 5;         // the warp that streams K and V, the one that brings queries
+constexpr int kThreads = 32 * (kConsumers + 2);
 constexpr float kHeadroom = 15.0f;                // weights reach 2^15 (fp16 holds 65504) ...
 constexpr float kBias = 7.0f;                     // ... and a moved base leaves the largest at 2^7
 
@@ -72,23 +75,45 @@ int32_t kv_parts_bound(int32_t max_ctx, int32_t max_parts) {
     return n < 1 ? 1 : (n < max_parts ? n : max_parts);
 }
 
-template <bool kFp8, int D>
+// kColWarps consumer warps side by side over the columns (16 each), kTokWarps over a tile's tokens.
+template <bool kFp8, int D, int kColWarps>
 struct KvCfg {
+    static constexpr int kTokWarps = kConsumers / kColWarps;
     static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
     static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;  // a TMA box is one swizzle span wide
     static constexpr int kBoxes = kRowBytes / kBoxBytes;                 // boxes side by side in a row
+    static constexpr int kStageBytes = kTokWarps > 1 ? 32768 : 16384;
+    static constexpr int kTile = kStageBytes / (2 * kRowBytes);          // tokens of a stage
     static constexpr int kPlane = kTile * kBoxBytes;                     // one box column of a tile
     static constexpr int kSide = kTile * kRowBytes;                      // K (or V) of a tile
-    static constexpr int kStageBytes = 2 * kSide;
-    static constexpr int kStages = 96 * 1024 / kStageBytes;  // two CTAs per SM share its 227 KB
-    static constexpr int kMergeStride = D + 4;
-    static constexpr int kMergeBytes = kConsumers * 16 * kMergeStride * 4;
-    static_assert(kMergeBytes <= kStages * kStageBytes, "the merge reuses the stages");
-    static constexpr int OFF_BARS = kStages * kStageBytes;
-    static constexpr int OFF_ML = OFF_BARS + 2 * kStages * 8;
-    static constexpr int OFF_MISC = OFF_ML + kConsumers * 16 * 2 * 4;
-    static constexpr int kSmemBytes = OFF_MISC + 16 + 1024;  // + slack for 1024-byte alignment
+    static constexpr int kStages = kTokWarps > 1 ? 3 : 5;
+    static constexpr int kWarpTokens = kTile / kTokWarps;                // a warp's share of a tile
+    static constexpr int kSub = kWarpTokens >= 32 ? 2 : 1;               // 16-token MMA steps taken together
+    static constexpr int kStepTokens = 16 * kSub;
+    static constexpr int kQBytes = 16 * D * 2;                           // a column warp's queries, 16 bits each
+    static constexpr int kMergeFloats = 16 * D;                          // a consumer's output
+    static_assert(kTokWarps == 1 || kConsumers * kMergeFloats * 4 <= kStageBytes, "the merge fits a stage");
+    static constexpr int OFF_Q = kStages * kStageBytes;
+    static constexpr int OFF_COLS = OFF_Q + kColWarps * kQBytes;         // [16 kColWarps] scale and context
+    static constexpr int OFF_ML = OFF_COLS + 16 * kColWarps * 8;         // [item parity][consumer][16] base and sum
+    static constexpr int OFF_ITEM = OFF_ML + 2 * kConsumers * 16 * 8;
+    static constexpr int OFF_BARS = OFF_ITEM + 64;
+    static constexpr int kNumBars = 2 * kStages + 3;
+    static constexpr int OFF_MISC = OFF_BARS + kNumBars * 8;
+    static constexpr int kSmemBytes = OFF_MISC + 16 + 1024;              // + slack for 1024-byte alignment
+    static_assert(kWarpTokens % kStepTokens == 0, "whole steps");
+    static_assert(kSmemBytes <= 115712, "two CTAs per SM");
 };
+
+// What the query warp tells the consumers about an item.
+struct KvItem {
+    int32_t live;       // 0: no more items
+    int32_t t_begin, t_end;
+    int32_t ctx_min;    // tokens that every row of the group sees
+    int32_t row0, g, part, parts;
+    int32_t ctx[8];     // the group's contexts
+};
+static_assert(sizeof(KvItem) == 64, "item layout");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -111,17 +136,17 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
 }
 
 template <bool kHalf>
-__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
     if constexpr (kHalf)
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                      "{%0, %1, %2, %3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                     : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
     else
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                      "{%0, %1, %2, %3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                     : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
 // Four e4m3 codes as two fp16 pairs (exact).
@@ -154,20 +179,67 @@ __device__ __forceinline__ uint32_t unit_at(int t, int u) {
         return static_cast<uint32_t>(t * 64 + ((u ^ ((t >> 1) & 3)) << 4));
 }
 
-// kWide: more than 8 columns per warp (two n-tiles of the second product).  kColWarps: consumer warps
-// side by side over the columns; the others split the tile's tokens.
+// Byte offset of 16-byte unit `u` of column `n` of a column warp's queries: rows of 2 D bytes, units
+// swizzled so that ldmatrix's eight rows lie in different banks.
+template <int D>
+__device__ __forceinline__ uint32_t q_unit_at(int n, int u) {
+    return static_cast<uint32_t>(n * 2 * D + ((u ^ (n & 7)) << 4));
+}
+
+// Float offset of dim `d` of column `n` in a consumer's part of the merge stage; the turned bits keep the
+// MMA fragments' stores and the rows' loads free of bank conflicts.
+template <int D>
+__device__ __forceinline__ int merge_at(int n, int d) {
+    return n * D + (d ^ ((n >> 1 & 3) << 3));
+}
+
+// Item `i` of the launch: part fastest, then column block, KV head, row group.  Warp-collective; false:
+// the group's context has fewer parts.
+struct KvWhere {
+    int part, parts, col0, g, row0, req, t_begin, t_end, ctx, ctx_min, my_ctx;
+    bool bad;
+};
+
+template <int kCols>
+__device__ __forceinline__ bool kv_where(const KvAttnArgs &a, uint32_t i, int lane, KvWhere &w) {
+    w.part = static_cast<int>(i % a.parts_bound);
+    i /= a.parts_bound;
+    w.col0 = static_cast<int>(i % a.col_blocks) * kCols;
+    i /= a.col_blocks;
+    w.g = static_cast<int>(i % a.kv_heads);
+    w.row0 = static_cast<int>(i / a.kv_heads) * a.group;
+    const int row = w.row0 + (lane < a.group ? lane : 0);
+    const int n = a.row_ctx[row], req = a.row_req[row];
+    w.req = __shfl_sync(0xffffffffu, req, 0);
+    w.bad = __any_sync(0xffffffffu, n < 0 || n > a.max_ctx || req != w.req) || w.req < 0 || w.req >= a.num_requests;
+    w.my_ctx = w.bad ? 0 : n;  // of row `lane` of the group
+    w.ctx = __reduce_max_sync(0xffffffffu, w.my_ctx);
+    w.ctx_min = __reduce_min_sync(0xffffffffu, w.my_ctx);
+    const int tokens = kv_part(w.ctx, a.max_parts);
+    w.parts = kv_parts(w.ctx, a.max_parts);
+    if (w.part >= w.parts) return false;
+    w.t_begin = w.part * tokens;
+    w.t_end = w.t_begin + min(w.ctx - w.t_begin, tokens);
+    return true;
+}
+
+// kWide: more than 8 columns per warp (two n-tiles of the second product).
 template <bool kFp8, int D, bool kWide, int kColWarps>
 __global__ void __launch_bounds__(kThreads, 2)
     kv_attention_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ KvAttnArgs a) {
-    using C = KvCfg<kFp8, D>;
-    constexpr int kTokWarps = kConsumers / kColWarps;
+    using C = KvCfg<kFp8, D, kColWarps>;
+    constexpr int kTokWarps = C::kTokWarps, kCols = 16 * kColWarps;
     constexpr int NT = kWide ? 2 : 1;
-    constexpr int KS = D / 16;
+    constexpr int KS = D / 16, SUB = C::kSub;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BARS);
-    uint64_t *empty = full + C::kStages;
-    float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);  // [consumer][16] base and sum
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BARS);  // [kStages] tile landed
+    uint64_t *empty = full + C::kStages;                                // [kStages] consumers are done with it
+    uint64_t *q_full = empty + C::kStages, *q_empty = q_full + 1;       // an item and its queries
+    uint64_t *merge = q_empty + 1;                                      // every consumer's output is in the merge stage
+    float2 *cols_s = reinterpret_cast<float2 *>(smem + C::OFF_COLS);    // scale, context (int bits)
+    float2 *ml_s = reinterpret_cast<float2 *>(smem + C::OFF_ML);
+    KvItem *item_s = reinterpret_cast<KvItem *>(smem + C::OFF_ITEM);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -177,6 +249,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], kConsumers);
         }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, kConsumers);
+        mbar_init(merge, kConsumers);
         fence_mbar_init();
         prefetch_tensormap(&kv_map);
     }
@@ -184,76 +259,67 @@ __global__ void __launch_bounds__(kThreads, 2)
     pdl_wait();
     pdl_launch_dependents();
 
-    // the item: part fastest, then column block, KV head, row group
-    uint32_t item = blockIdx.x;
-    const int part = static_cast<int>(item % a.parts_bound);
-    item /= a.parts_bound;
-    const int col0 = static_cast<int>(item % a.col_blocks) * (16 * kColWarps);
-    item /= a.col_blocks;
-    const int g = static_cast<int>(item % a.kv_heads), row0 = static_cast<int>(item / a.kv_heads) * a.group;
-
-    const int req = a.row_req[row0];
-    int ctx = 0;       // the group's longest context
-    int ctx_min = INT32_MAX;
-    bool bad = req < 0 || req >= a.num_requests;
-    for (int i = 0; i < a.group; ++i) {
-        const int n = a.row_ctx[row0 + i];
-        bad |= n < 0 || n > a.max_ctx || a.row_req[row0 + i] != req;
-        ctx = max(ctx, n);
-        ctx_min = min(ctx_min, n);
-    }
-    if (bad) {
-        if (threadIdx.x == 0) report(a.status, DSA_ERR_BOUNDS);
-        ctx = ctx_min = 0;
-    }
-    const int part_tokens = kv_part(ctx, a.max_parts), parts = kv_parts(ctx, a.max_parts);
-    if (part >= parts) return;
-    const int t_begin = part * part_tokens, t_end = t_begin + min(ctx - t_begin, part_tokens);
-    const int tiles = (t_end - t_begin + kTile - 1) / kTile;
-
-    float o[KS][NT][4] = {};
-    float base[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-    const int cw = warp % kColWarps, tw = warp / kColWarps;
+    const int hpg = a.num_heads / a.kv_heads, cols = a.group * hpg;
     const int gi = lane >> 2, ji = lane & 3;
 
-    if (warp == kConsumers) {
-        // ---- producer: boxes of min(page, tile) rows, lane b issues box b of a tile
-        const int box_rows = min(a.page_size, kTile);
-        const int pages_per_tile = kTile / box_rows;
+    if (warp == kProducer) {
+        // ---- K and V: boxes of at most kTile rows, lane b issues box b of a tile
+        const int box_rows = min(a.page_size, C::kTile);
+        const int boxes = C::kTile / box_rows;
+        // box of this lane: token box b_t of the tile, K or V, column of 128 bytes
+        const int b_t = lane / (2 * C::kBoxes), b_v = lane / C::kBoxes % 2, b_x = lane % C::kBoxes;
         const uint64_t policy = l2_evict_first_policy();
-        const int first_page = t_begin / a.page_size, num_pages = (t_end + a.page_size - 1) / a.page_size;
-        const int32_t *table = a.block_table + static_cast<int64_t>(req) * a.bt_stride;
-        auto load_ids = [&](int p) { return p + lane < num_pages ? table[p + lane] : 0; };
-        int batch = first_page;  // page ids batch .. batch + 31 are in `ids`, one per lane
-        int32_t ids = load_ids(batch), ids_next = load_ids(batch + 32);
-        int issued = 0;
-        for (int i = 0; i < tiles; ++i) {
-            const int s = i % C::kStages;
-            if (i >= C::kStages && !mbar_wait_warp(&empty[s], (i / C::kStages - 1) & 1, abort, a.status)) break;
-            const int t0 = t_begin + i * kTile;
-            const int boxes_here = min(pages_per_tile, (t_end - t0 + box_rows - 1) / box_rows);  // pages with tokens
-            const int p0 = t0 / a.page_size;
-            if (p0 >= batch + 32) {
-                batch += 32;
-                ids = ids_next;
-                ids_next = load_ids(batch + 32);
-            }
-            // box b: page b / (2 kBoxes) of the tile, its K or V, its column of 128 bytes
-            const int b_page = lane / (2 * C::kBoxes), b_v = lane / C::kBoxes % 2, b_x = lane % C::kBoxes;
-            int32_t id = __shfl_sync(0xffffffffu, ids, (p0 + b_page - batch) & 31);
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], boxes_here * box_rows * 2 * C::kRowBytes);
-            __syncwarp();
-            if (b_page < boxes_here) {
-                if (id < 0 || id >= a.num_pages) {
-                    report(a.status, DSA_ERR_BOUNDS);
-                    id = 0;
+        int s = 0, issued = 0;
+        uint32_t phase = 1;
+        bool go = true;
+        for (uint32_t it = blockIdx.x; it < a.items && go; it += gridDim.x) {
+            KvWhere w;
+            if (!kv_where<kCols>(a, it, lane, w)) continue;
+            const int num_pages = (w.t_end + a.page_size - 1) / a.page_size;
+            const int32_t *table = a.block_table + static_cast<int64_t>(w.req) * a.bt_stride;
+            auto load_ids = [&](int p) { return p + lane < num_pages ? table[p + lane] : 0; };
+            int batch = w.t_begin / a.page_size;  // page ids batch .. batch + 31 are in `ids`, one per lane
+            int32_t ids = load_ids(batch), ids_next = load_ids(batch + 32);
+            for (int t0 = w.t_begin; t0 < w.t_end; t0 += C::kTile) {
+                if (!mbar_wait_warp(&empty[s], phase, abort, a.status)) {
+                    go = false;
+                    break;
                 }
-                const int y = ((id * a.kv_heads + g) * 2 + b_v) * a.page_size + t0 % a.page_size;
-                tma_load_2d_hint(smem + s * C::kStageBytes + b_v * C::kSide + b_x * C::kPlane +
-                                     b_page * box_rows * C::kBoxBytes,
-                                 &kv_map, &full[s], b_x * C::kBoxBytes, y, policy);
+                const int here = min(boxes, (w.t_end - t0 + box_rows - 1) / box_rows);  // boxes with tokens
+                if (t0 / a.page_size >= batch + 32) {
+                    batch += 32;
+                    ids = ids_next;
+                    ids_next = load_ids(batch + 32);
+                }
+                const int tb = t0 + b_t * box_rows;
+                int32_t id = __shfl_sync(0xffffffffu, ids, (tb / a.page_size - batch) & 31);
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], here * box_rows * 2 * C::kRowBytes);
+                __syncwarp();
+                if (b_t < here) {
+                    if (id < 0 || id >= a.num_pages) {
+                        report(a.status, DSA_ERR_BOUNDS);
+                        id = 0;
+                    }
+                    const int y = ((id * a.kv_heads + w.g) * 2 + b_v) * a.page_size + tb % a.page_size;
+                    tma_load_2d_hint(smem + s * C::kStageBytes + b_v * C::kSide + b_x * C::kPlane +
+                                         b_t * box_rows * C::kBoxBytes,
+                                     &kv_map, &full[s], b_x * C::kBoxBytes, y, policy);
+                }
+                ++issued;
+                if (++s == C::kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
-            issued = i + 1;
+            if (kTokWarps > 1 && go) {  // the next stage is the consumers', to merge the item's output in
+                if (!mbar_wait_warp(&empty[s], phase, abort, a.status)) break;
+                if (lane == 0) mbar_arrive(&full[s]);
+                ++issued;
+                if (++s == C::kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
+            }
         }
         if (*abort && lane == 0) {  // leave no copy in flight behind
             for (int i = max(0, issued - C::kStages); i < issued; ++i) {
@@ -262,107 +328,187 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
         }
-    } else {
-        // ---- consumer: columns n = col0 + 16 cw + {gi, gi + 8} as M rows
-        const int hpg = a.num_heads / a.kv_heads, cols = a.group * hpg;
-        uint32_t q[KS][4];
-        float scale[2];  // log2 units per unit of S
-        int cx[2];       // the columns' contexts
+        return;
+    }
+
+    if (warp == kQuery) {
+        // ---- items, and their queries in 16 bits, columns as rows
+        uint32_t phase = 1;
+        for (uint32_t it = blockIdx.x; it < a.items; it += gridDim.x) {
+            KvWhere w;
+            if (!kv_where<kCols>(a, it, lane, w)) continue;
+            if (w.bad && w.part == 0 && lane == 0) report(a.status, DSA_ERR_BOUNDS);
+            // 16 dims (a unit) of a column per lane and turn: a column's units are in neighbouring lanes.  The
+            // first 16 columns are loaded while the consumers still have the item before
+            constexpr int kUnits = D / 16, kTurns = kUnits / 2;  // 32 / kUnits columns per turn, 16 in all
+            const int unit = lane % kUnits;
+            uint4 v0[kTurns], v1[kTurns];
+            auto load = [&](int c0) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int n = col0 + 16 * cw + gi + 8 * x;
-            const bool real = n < cols;
-            const int row = real ? n / hpg : 0;
-            cx[x] = real && !bad ? a.row_ctx[row0 + row] : 0;
-            scale[x] = a.s_scale;
-            const uint16_t *src = a.q + (row0 + row) * a.q_stride +
-                                  static_cast<int64_t>(g * hpg + (real ? n % hpg : 0)) * D;
-            if constexpr (!kFp8) {
+                for (int i = 0; i < kTurns; ++i) {
+                    const int n = w.col0 + c0 + i * (32 / kUnits) + lane / kUnits;
+                    v0[i] = v1[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (n < cols) {
+                        const uint4 *src = reinterpret_cast<const uint4 *>(
+                            a.q + (w.row0 + n / hpg) * a.q_stride + static_cast<int64_t>(w.g * hpg + n % hpg) * D + unit * 16);
+                        v0[i] = src[0];
+                        v1[i] = src[1];
+                    }
+                }
+            };
+            load(0);
+            if (!mbar_wait_warp(q_empty, phase, abort, a.status)) return;
+            phase ^= 1;
+#pragma unroll 1
+            for (int c = 0; c < kColWarps; ++c) {
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    q[k][x] = real ? *reinterpret_cast<const uint32_t *>(src + k * 16 + ji * 2) : 0u;
-                    q[k][2 + x] = real ? *reinterpret_cast<const uint32_t *>(src + k * 16 + 8 + ji * 2) : 0u;
-                }
-            } else {
-                // K's codes come four dims to a lane (ldmatrix moves byte pairs): k slots 2j, 2j + 1
-                // hold dims 4j, 4j + 1 and slots 2j + 8, 2j + 9 dims 4j + 2, 4j + 3; q likewise
-                uint2 raw[KS];
-                float amax = 0.f;
+                for (int i = 0; i < kTurns; ++i) {
+                    const int n = i * (32 / kUnits) + lane / kUnits, col = w.col0 + 16 * c + n;
+                    const int ctx = __shfl_sync(0xffffffffu, w.my_ctx, col < cols ? col / hpg : 0);
+                    float scale = a.s_scale;
+                    if constexpr (kFp8) {
+                        const uint32_t h[8] = {v0[i].x, v0[i].y, v0[i].z, v0[i].w, v1[i].x, v1[i].y, v1[i].z, v1[i].w};
+                        float amax = 0.f;
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    raw[k] = real ? *reinterpret_cast<const uint2 *>(src + k * 16 + ji * 4) : make_uint2(0u, 0u);
-                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(bf16_lo(raw[k].x)), fabsf(bf16_hi(raw[k].x))),
-                                             fmaxf(fabsf(bf16_lo(raw[k].y)), fabsf(bf16_hi(raw[k].y)))));
-                }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                // 2^e brings the column's largest |q| to [2^13, 2^14); infinities stay what they are
-                int e = 0;
-                if (amax > 0.f && amax <= 3.4e38f) {
-                    e = 140 - static_cast<int>(__float_as_uint(amax) >> 23);
-                    e = max(-120, min(120, e));
-                }
-                const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                scale[x] *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                        for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(h[y])), fabsf(bf16_hi(h[y]))));
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    q[k][x] = pack_f16(bf16_lo(raw[k].x) * up, bf16_hi(raw[k].x) * up);
-                    q[k][2 + x] = pack_f16(bf16_lo(raw[k].y) * up, bf16_hi(raw[k].y) * up);
+                        for (int y = 1; y < kUnits; y <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
+                        // 2^e brings the column's largest |q| to [2^13, 2^14); infinities and NaN stay what they are
+                        int e = 0;
+                        if (amax > 0.f && amax <= 3.4e38f) {
+                            e = 140 - static_cast<int>(__float_as_uint(amax) >> 23);
+                            e = max(-120, min(120, e));
+                        }
+                        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                        scale *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                        uint32_t f[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) f[y] = pack_f16(bf16_lo(h[y]) * up, bf16_hi(h[y]) * up);
+                        // K's codes come four dims to a lane (ldmatrix moves byte pairs): the k slots of its low
+                        // and high pairs hold dims 4j, 4j + 1 and 4j + 2, 4j + 3; q's in the same order
+                        v0[i] = make_uint4(f[0], f[2], f[4], f[6]);
+                        v1[i] = make_uint4(f[1], f[3], f[5], f[7]);
+                    }
+                    // a masked score is -inf times this: neither zero nor infinity
+                    if (unit == 0)
+                        cols_s[16 * c + n] = make_float2(fminf(fmaxf(scale, 1.17549435e-38f), 3.40282347e38f),
+                                                         __int_as_float(col < cols ? ctx : 0));
+                    uint8_t *dst = smem + C::OFF_Q + c * C::kQBytes;
+                    *reinterpret_cast<uint4 *>(dst + q_unit_at<D>(n, 2 * unit)) = v0[i];
+                    *reinterpret_cast<uint4 *>(dst + q_unit_at<D>(n, 2 * unit + 1)) = v1[i];
                 }
+                if (c + 1 < kColWarps) load(16 * (c + 1));
+            }
+            if (lane < 8) item_s->ctx[lane] = w.my_ctx;
+            if (lane == 0) {
+                item_s->live = 1;
+                item_s->t_begin = w.t_begin;
+                item_s->t_end = w.t_end;
+                item_s->ctx_min = w.ctx_min;
+                item_s->row0 = w.row0;
+                item_s->g = w.g | (w.col0 << 16);
+                item_s->part = w.part;
+                item_s->parts = w.parts;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        }
+        if (!mbar_wait_warp(q_empty, phase, abort, a.status)) return;
+        if (lane == 0) {
+            item_s->live = 0;
+            mbar_arrive(q_full);
+        }
+        return;
+    }
+
+    // ---- consumers
+    const int cw = warp % kColWarps, tw = warp / kColWarps;
+    int s = 0;
+    uint32_t phase = 0, q_phase = 0;
+    for (;; q_phase ^= 1) {
+        if (!mbar_wait_warp(q_full, q_phase, abort, a.status)) return;
+        if (item_s->live == 0) return;
+        const int t_begin = item_s->t_begin, t_end = item_s->t_end, ctx_min = item_s->ctx_min;
+        const int row0 = item_s->row0, g = item_s->g & 0xffff, col0 = (item_s->g >> 16) + 16 * cw;
+        const int part = item_s->part, parts = item_s->parts;
+        uint4 q[KS];
+        {
+            // matrices: columns 0-7, 8-15 of unit 2 k, then of unit 2 k + 1
+            const uint32_t qs = smem_u32(smem + C::OFF_Q + cw * C::kQBytes);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                uint32_t r[4];
+                ldsm4(r, qs + q_unit_at<D>(lane & 15, 2 * k + (lane >> 4)));
+                q[k] = make_uint4(r[0], r[1], r[2], r[3]);
             }
         }
-        // the rows of the group among this warp's columns
-        const int row_lo = (col0 + 16 * cw) / hpg, row_hi = min(col0 + 16 * cw + 15, cols - 1) / hpg;
-        const bool idle = col0 + 16 * cw >= cols;
+        float scale[2];
+        int cx[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const float2 v = cols_s[16 * cw + gi + 8 * x];
+            scale[x] = v.x;
+            cx[x] = __float_as_int(v.y);
+        }
+        // the rows of the group among this warp's columns, and lane i's the context of row i
+        const int row_lo = col0 / hpg, row_hi = min(col0 + 15, cols - 1) / hpg;
+        const int row_ctx = item_s->ctx[lane & 7];
+        const bool idle = col0 >= cols;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty);
 
-        for (int i = 0; i < tiles; ++i) {
-            const int s = i % C::kStages;
-            if (!mbar_wait_warp(&full[s], (i / C::kStages) & 1, abort, a.status)) break;
+        float o[KS][NT][4] = {};
+        float base[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+        for (int tile0 = t_begin; tile0 < t_end; tile0 += C::kTile) {
+            if (!mbar_wait_warp(&full[s], phase, abort, a.status)) return;
             const uint32_t ks = smem_u32(smem + s * C::kStageBytes), vs = ks + C::kSide;
 #pragma unroll 1
-            for (int st = tw; st < kTile / kStep && !idle; st += kTokWarps) {
-                const int ts = st * kStep, t0 = t_begin + i * kTile + ts;  // the step's tokens, in tile and context
+            for (int ts = tw * C::kWarpTokens; ts < (tw + 1) * C::kWarpTokens && !idle; ts += C::kStepTokens) {
+                const int t0 = tile0 + ts;  // the step's first token
                 if (t0 >= t_end) break;
-                // S: columns gi, gi + 8; tokens t0 + 8 n + 2 ji + {0, 1}
-                float c[2][4] = {};
-                if constexpr (!kFp8) {
-                    // matrices: tokens 0-7 (k 0-7, 8-15), tokens 8-15 (k 0-7, 8-15)
+                // S: columns gi, gi + 8; tokens t0 + 8 n + 2 ji + {0, 1}.  ldmatrix brings tokens 0-7
+                // (units u, u + 1), then tokens 8-15 of each 16
+                float c[2 * SUB][4] = {};
+                {
                     const int t = ts + (lane & 7) + ((lane >> 4) << 3), u = (lane >> 3) & 1;
 #pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        uint32_t b[4];
-                        ldsm4(b, ks + unit_at<C>(t, 2 * k + u));
-                        mma16<false>(c[0], q[k], b[0], b[1]);
-                        mma16<false>(c[1], q[k], b[2], b[3]);
-                    }
-                } else {
-                    const int t = ts + (lane & 7) + ((lane >> 4) << 3), u = (lane >> 3) & 1;
+                    for (int k = 0; k < KS; k += kFp8 ? 2 : 1) {
 #pragma unroll
-                    for (int k = 0; k < KS; k += 2) {
-                        uint32_t b[4];
-                        ldsm4(b, ks + unit_at<C>(t, k + u));
+                        for (int y = 0; y < SUB; ++y) {
+                            uint32_t b[4];
+                            ldsm4(b, ks + unit_at<C>(t + 16 * y, (kFp8 ? k : 2 * k) + u));
+                            if constexpr (!kFp8) {
+                                mma16<false>(c[2 * y], q[k], b[0], b[1]);
+                                mma16<false>(c[2 * y + 1], q[k], b[2], b[3]);
+                            } else {
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            uint32_t b0, b1;
-                            e4m3x4_to_f16(b[2 * n], b0, b1);
-                            mma16<true>(c[n], q[k], b0, b1);
-                            e4m3x4_to_f16(b[2 * n + 1], b0, b1);
-                            mma16<true>(c[n], q[k + 1], b0, b1);
+                                for (int n = 0; n < 2; ++n) {
+                                    uint32_t b0, b1;
+                                    e4m3x4_to_f16(b[2 * n], b0, b1);
+                                    mma16<true>(c[2 * y + n], q[k], b0, b1);
+                                    e4m3x4_to_f16(b[2 * n + 1], b0, b1);
+                                    mma16<true>(c[2 * y + n], q[k + 1], b0, b1);
+                                }
+                            }
                         }
                     }
                 }
-                const bool edge = t0 + kStep > ctx_min;  // some column does not see all of the step
+                const bool edge = t0 + C::kStepTokens > ctx_min;  // some column does not see all of the step
+                if (edge) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < 2 * SUB; ++n)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        c[n][x] *= scale[x >> 1];
-                        if (edge && t0 + 8 * n + 2 * ji + (x & 1) >= cx[x >> 1]) c[n][x] = -INFINITY;
-                    }
+                        for (int x = 0; x < 4; ++x)
+                            if (t0 + 8 * n + 2 * ji + (x & 1) >= cx[x >> 1]) c[n][x] = -INFINITY;
+                }
                 float top[2];
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    top[x] = fmaxf(fmaxf(c[0][2 * x], c[0][2 * x + 1]), fmaxf(c[1][2 * x], c[1][2 * x + 1]));
+                for (int x = 0; x < 2; ++x) {
+                    top[x] = fmaxf(c[0][2 * x], c[0][2 * x + 1]);
+#pragma unroll
+                    for (int n = 1; n < 2 * SUB; ++n) top[x] = fmaxf(top[x], fmaxf(c[n][2 * x], c[n][2 * x + 1]));
+                    top[x] *= scale[x];  // (a positive factor)
+                }
                 if (__any_sync(0xffffffffu, top[0] > base[0] + kHeadroom || top[1] > base[1] + kHeadroom)) {
                     float f[2];
 #pragma unroll
@@ -390,27 +536,27 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const float b = base[x] == -INFINITY ? 0.f : base[x];
+                    const float b = base[x] == -INFINITY ? 0.f : -base[x];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < 2 * SUB; ++n)
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            c[n][2 * x + y] = ex2(c[n][2 * x + y] - b);
+                            c[n][2 * x + y] = ex2(fmaf(c[n][2 * x + y], scale[x], b));
                             sum[x] += c[n][2 * x + y];
                         }
                 }
                 // P^T as the second product's B operand: n-tile x holds columns 8 x + gi
-                uint32_t hi[NT][2], lo[NT][2];
+                uint32_t hi[2 * SUB][NT], lo[2 * SUB][NT];
 #pragma unroll
-                for (int x = 0; x < NT; ++x)
+                for (int n = 0; n < 2 * SUB; ++n)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
+                    for (int x = 0; x < NT; ++x) {
                         const float p0 = c[n][2 * x], p1 = c[n][2 * x + 1];
                         if constexpr (kFp8) {
-                            hi[x][n] = pack_f16(p0, p1);
+                            hi[n][x] = pack_f16(p0, p1);
                         } else {
-                            hi[x][n] = pack_bf16(p0, p1);
-                            lo[x][n] = pack_bf16(p0 - bf16_lo(hi[x][n]), p1 - bf16_hi(hi[x][n]));
+                            hi[n][x] = pack_bf16(p0, p1);
+                            lo[n][x] = pack_bf16(p0 - bf16_lo(hi[n][x]), p1 - bf16_hi(hi[n][x]));
                         }
                     }
                 // O^T += V^T P^T.  In an edge step the rows of the group take turns, with V's tokens at and past
@@ -418,61 +564,66 @@ __global__ void __launch_bounds__(kThreads, 2)
                 // may be NaN, and 0 x NaN must not reach its sums.
                 auto product = [&](auto edge_step, int row) {
                     constexpr bool kEdge = decltype(edge_step)::value;
-                    uint32_t keep[2];      // tokens 2 ji, 2 ji + 1 of either half
-                    bool mine[NT][2];      // columns 8 x + 2 ji + {0, 1} are this row's
+                    uint32_t keep[2 * SUB];  // tokens 8 n + 2 ji + {0, 1}
+                    bool mine[NT][2];        // columns 8 x + 2 ji + {0, 1} are this row's
                     if constexpr (kEdge) {
-                        const int n = bad ? 0 : a.row_ctx[row0 + row];
+                        const int n_ctx = __shfl_sync(0xffffffffu, row_ctx, row);
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const int t = t0 + 8 * y + 2 * ji;
-                            keep[y] = (t < n ? 0xffffu : 0u) | (t + 1 < n ? 0xffff0000u : 0u);
+                        for (int n = 0; n < 2 * SUB; ++n) {
+                            const int t = t0 + 8 * n + 2 * ji;
+                            keep[n] = (t < n_ctx ? 0xffffu : 0u) | (t + 1 < n_ctx ? 0xffff0000u : 0u);
                         }
 #pragma unroll
                         for (int x = 0; x < NT; ++x)
 #pragma unroll
-                            for (int y = 0; y < 2; ++y) mine[x][y] = (col0 + 16 * cw + 8 * x + 2 * ji + y) / hpg == row;
+                            for (int y = 0; y < 2; ++y) mine[x][y] = (col0 + 8 * x + 2 * ji + y) / hpg == row;
                     }
-                    auto accumulate = [&](float(&acc)[NT][4], uint32_t(&v)[4]) {
+                    auto accumulate = [&](float(&acc)[NT][4], uint4 v, int y) {  // 16 tokens y of the step
                         if constexpr (kEdge) {
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) v[y] &= keep[y >> 1];
+                            v.x &= keep[2 * y];
+                            v.y &= keep[2 * y];
+                            v.z &= keep[2 * y + 1];
+                            v.w &= keep[2 * y + 1];
                         }
 #pragma unroll
                         for (int x = 0; x < NT; ++x) {
                             float old[4];
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) old[y] = acc[x][y];
-                            mma16<kFp8>(acc[x], v, hi[x][0], hi[x][1]);
-                            if constexpr (!kFp8) mma16<false>(acc[x], v, lo[x][0], lo[x][1]);
+                            for (int z = 0; z < 4; ++z) old[z] = acc[x][z];
+                            mma16<kFp8>(acc[x], v, hi[2 * y][x], hi[2 * y + 1][x]);
+                            if constexpr (!kFp8) mma16<false>(acc[x], v, lo[2 * y][x], lo[2 * y + 1][x]);
                             if constexpr (kEdge) {
 #pragma unroll
-                                for (int y = 0; y < 4; ++y) acc[x][y] = mine[x][y & 1] ? acc[x][y] : old[y];
+                                for (int z = 0; z < 4; ++z) acc[x][z] = mine[x][z & 1] ? acc[x][z] : old[z];
                             }
                         }
                     };
-                    if constexpr (!kFp8) {
-                        // matrices: tokens 0-7 (d 0-7, 8-15), tokens 8-15 (d 0-7, 8-15)
-                        const int t = ts + (lane & 7) + ((lane >> 4) << 3), u = (lane >> 3) & 1;
 #pragma unroll
-                        for (int m = 0; m < KS; ++m) {
-                            uint32_t v[4];
-                            ldsm4_t(v, vs + unit_at<C>(t, 2 * m + u));
-                            accumulate(o[m], v);
-                        }
-                    } else {
-                        // matrices: unit m tokens 0-7, 8-15, unit m + 1 likewise; a lane gets codes
-                        // [t d][t d+1][t+1 d][t+1 d+1] with d = 2 gi: M row gi is dim 2 gi, row gi + 8 dim 2 gi + 1
-                        const int t = ts + (lane & 15), u = lane >> 4;
+                    for (int y = 0; y < SUB; ++y) {
+                        if constexpr (!kFp8) {
+                            // matrices: tokens 0-7 (d 0-7, 8-15), tokens 8-15 (d 0-7, 8-15)
+                            const int t = ts + 16 * y + (lane & 7) + ((lane >> 4) << 3), u = (lane >> 3) & 1;
 #pragma unroll
-                        for (int m = 0; m < KS; m += 2) {
-                            uint32_t w[4];
-                            ldsm4_t(w, vs + unit_at<C>(t, m + u));
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
+                            for (int m = 0; m < KS; ++m) {
                                 uint32_t v[4];
-                                e4m3x4_to_f16(__byte_perm(w[2 * y], 0, 0x3120), v[0], v[1]);
-                                e4m3x4_to_f16(__byte_perm(w[2 * y + 1], 0, 0x3120), v[2], v[3]);
-                                accumulate(o[m + y], v);
+                                ldsm4_t(v, vs + unit_at<C>(t, 2 * m + u));
+                                accumulate(o[m], make_uint4(v[0], v[1], v[2], v[3]), y);
+                            }
+                        } else {
+                            // matrices: unit m tokens 0-7, 8-15, unit m + 1 likewise; a lane gets codes
+                            // [t d][t d+1][t+1 d][t+1 d+1], d = 2 gi: M row gi is dim 2 gi, row gi + 8 dim 2 gi + 1
+                            const int t = ts + 16 * y + (lane & 15), u = lane >> 4;
+#pragma unroll
+                            for (int m = 0; m < KS; m += 2) {
+                                uint32_t w[4];
+                                ldsm4_t(w, vs + unit_at<C>(t, m + u));
+#pragma unroll
+                                for (int z = 0; z < 2; ++z) {
+                                    uint4 v;
+                                    e4m3x4_to_f16(__byte_perm(w[2 * z], 0, 0x3120), v.x, v.y);
+                                    e4m3x4_to_f16(__byte_perm(w[2 * z + 1], 0, 0x3120), v.z, v.w);
+                                    accumulate(o[m + z], v, y);
+                                }
                             }
                         }
                     }
@@ -486,78 +637,137 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
+            if (++s == C::kStages) {
+                s = 0;
+                phase ^= 1;
+            }
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
             sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
-            if (ji == 0) ml[warp * 16 + gi + 8 * x] = make_float2(base[x], sum[x]);
         }
-    }
-    __syncthreads();  // every stage is consumed: the merge reuses them
-    if (*abort) return;
 
-    // ---- merge the token warps of each column, each in its own base
-    float *merge = reinterpret_cast<float *>(smem);  // [consumer][16][kMergeStride]
-    if (warp < kConsumers) {
-        float f[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            float top = -INFINITY;
-            for (int w = 0; w < kTokWarps; ++w) top = fmaxf(top, ml[(w * kColWarps + cw) * 16 + gi + 8 * x].x);
-            f[x] = ex2(base[x] - (top == -INFINITY ? 0.f : top));
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float f0 = __shfl_sync(0xffffffffu, f[n], 8 * ji), f1 = __shfl_sync(0xffffffffu, f[n], 8 * ji + 4);
-            float *dst = merge + (warp * 16 + 8 * n + 2 * ji) * C::kMergeStride;
-#pragma unroll
-            for (int m = 0; m < KS; ++m) {
-                const int d0 = kFp8 ? 16 * m + 2 * gi : 16 * m + gi, d1 = kFp8 ? d0 + 1 : d0 + 8;
-                dst[d0] = o[m][n][0] * f0;
-                dst[C::kMergeStride + d0] = o[m][n][1] * f1;
-                dst[d1] = o[m][n][2] * f0;
-                dst[C::kMergeStride + d1] = o[m][n][3] * f1;
+        // ---- output
+        auto finish = [&](int64_t at, int d, const float4 &x, float b, float total) {  // dims d .. d + 3 of head `at`
+            if (parts > 1) {
+                *reinterpret_cast<float4 *>(a.part_o + (at * a.parts_bound + part) * D + d) = x;
+                if (d == 0) a.part_ml[at * a.parts_bound + part] = make_float2(b, total);
+            } else {
+                const bool none = total == 0.f;
+                const float inv = none ? 0.f : a.v_scale / total;
+                *reinterpret_cast<uint2 *>(a.out + at * D + d) =
+                    none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+                if (d == 0 && a.lse != nullptr) a.lse[at] = none ? -INFINITY : (b + log2f(total)) * 0.6931471805599453f;
             }
-        }
-    }
-    __syncthreads();
-    const int hpg = a.num_heads / a.kv_heads, cols = min(16 * kColWarps, a.group * hpg - col0);
-    for (int i = threadIdx.x; i < cols * (D / 4); i += kThreads) {
-        const int n = i / (D / 4), d = i % (D / 4) * 4;
-        const int w0 = n / 16, c = n % 16;
-        float top = -INFINITY;
-        for (int w = 0; w < kTokWarps; ++w) top = fmaxf(top, ml[(w * kColWarps + w0) * 16 + c].x);
-        const float b = top == -INFINITY ? 0.f : top;
-        float total = 0.f;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < kTokWarps; ++w) {
-            const int at = (w * kColWarps + w0) * 16 + c;
-            total += ml[at].y * ex2(ml[at].x - b);
-            const float4 y = *reinterpret_cast<const float4 *>(merge + at * C::kMergeStride + d);
-            x.x += y.x;
-            x.y += y.y;
-            x.z += y.z;
-            x.w += y.w;
-        }
-        const int row = row0 + (col0 + n) / hpg, head = g * hpg + (col0 + n) % hpg;
-        const int64_t at = static_cast<int64_t>(row) * a.num_heads + head;
-        if (parts > 1) {
-            *reinterpret_cast<float4 *>(a.part_o + (at * a.parts_bound + part) * D + d) = x;
-            if (d == 0) a.part_ml[at * a.parts_bound + part] = make_float2(top, total);
+        };
+        if constexpr (kTokWarps > 1) {
+            // the token warps' outputs meet in the next stage of the ring, each in its own base; every consumer
+            // then adds up its share of the columns, token warps in order
+            if (!mbar_wait_warp(&full[s], phase, abort, a.status)) return;
+            float *mo = reinterpret_cast<float *>(smem + s * C::kStageBytes);
+            float *mine = mo + warp * C::kMergeFloats;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int m = 0; m < KS; ++m) {
+                        const int c = 8 * n + 2 * ji + y;
+                        if constexpr (kFp8) {  // dims 16 m + 2 gi, 2 gi + 1
+                            *reinterpret_cast<float2 *>(mine + merge_at<D>(c, 16 * m + 2 * gi)) =
+                                make_float2(o[m][n][y], o[m][n][2 + y]);
+                        } else {               // dims 16 m + gi, gi + 8
+                            mine[merge_at<D>(c, 16 * m + gi)] = o[m][n][y];
+                            mine[merge_at<D>(c, 16 * m + gi + 8)] = o[m][n][2 + y];
+                        }
+                    }
+            // (two sets: a warp may be an item ahead of one that still reads)
+            float2 *ml = ml_s + q_phase * (kConsumers * 16);
+            if (ji == 0) {
+                ml[warp * 16 + gi] = make_float2(base[0], sum[0]);
+                ml[warp * 16 + gi + 8] = make_float2(base[1], sum[1]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(merge);
+            if (!mbar_wait_warp(merge, q_phase, abort, a.status)) return;
+            constexpr int kLanes = D / 4;  // lanes of a column
+            const int first = warp * (32 / kLanes) + lane / kLanes, d = lane % kLanes * 4;
+            const int here = min(kCols, cols - (col0 - 16 * cw));
+#pragma unroll 2
+            for (int n = first; n < here; n += kConsumers * (32 / kLanes)) {
+                float b = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kTokWarps; ++w) b = fmaxf(b, ml[(w * kColWarps + n / 16) * 16 + n % 16].x);
+                const float b0 = b == -INFINITY ? 0.f : b;
+                float total = 0.f;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kTokWarps; ++w) {
+                    const int from = w * kColWarps + n / 16;
+                    const float2 l = ml[from * 16 + n % 16];
+                    const float4 y = *reinterpret_cast<const float4 *>(mo + from * C::kMergeFloats + merge_at<D>(n % 16, d));
+                    const float f = ex2(l.x - b0);
+                    total += l.y * f;
+                    x.x += y.x * f;
+                    x.y += y.y * f;
+                    x.z += y.z * f;
+                    x.w += y.w * f;
+                }
+                const int col = col0 - 16 * cw + n;
+                finish(static_cast<int64_t>(row0 + col / hpg) * a.num_heads + g * hpg + col % hpg, d, x, b0, total);
+            }
+            fence_async_smem();  // the stage goes back to TMA writes
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+            if (++s == C::kStages) {
+                s = 0;
+                phase ^= 1;
+            }
         } else {
-            const float inv = total == 0.f ? 0.f : a.v_scale / total;
-            const bool none = total == 0.f;
-            *reinterpret_cast<uint2 *>(a.out + at * D + d) =
-                none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
-            if (d == 0 && a.lse != nullptr) a.lse[at] = none ? -INFINITY : (b + log2f(total)) * 0.6931471805599453f;
+            // one warp has all of a column: lanes swap dims so that each writes four in a row
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float b = __shfl_sync(0xffffffffu, base[n], 8 * ji + 4 * y);
+                    const float total = __shfl_sync(0xffffffffu, sum[n], 8 * ji + 4 * y);
+                    const int col = col0 + 8 * n + 2 * ji + y;
+                    const int64_t at = static_cast<int64_t>(row0 + col / hpg) * a.num_heads + g * hpg + col % hpg;
+#pragma unroll
+                    for (int m = 0; m < KS; ++m) {
+                        // own: dims {p, q}; FP8: 2 gi, 2 gi + 1 of 16 m; else gi, gi + 8
+                        float p = o[m][n][y], q2 = o[m][n][2 + y];
+                        if constexpr (kFp8) {
+                            const float r0 = __shfl_xor_sync(0xffffffffu, p, 4), r1 = __shfl_xor_sync(0xffffffffu, q2, 4);
+                            if ((gi & 1) == 0 && col < cols)
+                                finish(at, 16 * m + 2 * gi, make_float4(p, q2, r0, r1), b == -INFINITY ? 0.f : b, total);
+                        } else {
+                            // even gi collects dims gi, gi + 1 (and, two lanes on, gi + 2, gi + 3), odd gi the upper eight
+                            const float give = gi & 1 ? p : q2;
+                            const float got = __shfl_xor_sync(0xffffffffu, give, 4);
+                            const float e0 = gi & 1 ? got : p, e1 = gi & 1 ? q2 : got;  // dims 2 (gi / 2), + 1 of its eight
+                            const float f0 = __shfl_xor_sync(0xffffffffu, e0, 8), f1 = __shfl_xor_sync(0xffffffffu, e1, 8);
+                            if ((gi & 2) == 0 && col < cols)
+                                finish(at, 16 * m + (gi & 1) * 8 + (gi & 4), make_float4(e0, e1, f0, f1),
+                                       b == -INFINITY ? 0.f : b, total);
+                        }
+                    }
+                }
         }
     }
 }
 
-// Merge of a row's parts: one CTA per (row, head), one thread per dim.
+// Merge of a row's parts: one CTA per (row, head).  128 / (D / 4) groups of lanes take every so manyth part,
+// four dims to a lane; the groups' sums are added in order.
+constexpr int kCombineThreads = 128, kCombineParts = 256;
+
 template <int D>
-__global__ void __launch_bounds__(D) kv_combine_kernel(const __grid_constant__ KvAttnArgs a) {
+__global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const __grid_constant__ KvAttnArgs a) {
+    constexpr int kLanes = D / 4, kGroups = kCombineThreads / kLanes;
+    __shared__ float2 ml_s[kCombineParts];
+    __shared__ float4 x_s[kGroups][kLanes];
+    __shared__ float t_s[kGroups];
     pdl_wait();
     pdl_launch_dependents();
     const int64_t at = blockIdx.x;
@@ -566,26 +776,62 @@ __global__ void __launch_bounds__(D) kv_combine_kernel(const __grid_constant__ K
     for (int i = 0; i < a.group; ++i) ctx = max(ctx, min(a.row_ctx[row0 + i], a.max_ctx));
     const int parts = kv_parts(ctx, a.max_parts);
     if (parts == 1) return;  // written by the attention kernel
-    const float2 *ml = a.part_ml + at * a.parts_bound;
-    const float *po = a.part_o + at * a.parts_bound * D + threadIdx.x;
-    float top = -INFINITY;
-    for (int p = 0; p < parts; ++p) top = fmaxf(top, ml[p].x);
-    const float b = top == -INFINITY ? 0.f : top;
-    float total = 0.f, x = 0.f;
-#pragma unroll 8
-    for (int p = 0; p < parts; ++p) {
-        const float f = ex2(ml[p].x - b);
-        total += ml[p].y * f;
-        x += po[static_cast<int64_t>(p) * D] * f;
+    const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes;
+    const float4 *po = reinterpret_cast<const float4 *>(a.part_o + at * a.parts_bound * D) + d;
+    // the first parts' outputs are on their way while the bases are compared
+    constexpr int kAhead = 8;
+    float4 y[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int p = grp + i * kGroups;
+        if (p < parts) y[i] = po[static_cast<int64_t>(p) * kLanes];
+    }
+    for (int p = threadIdx.x; p < parts; p += kCombineThreads) ml_s[p] = a.part_ml[at * a.parts_bound + p];
+    __syncthreads();
+    float b = -INFINITY;
+    for (int p = threadIdx.x & 31; p < parts; p += 32) b = fmaxf(b, ml_s[p].x);
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, i));
+    const float b0 = b == -INFINITY ? 0.f : b;
+    float total = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](int p, const float4 &v) {
+        const float2 l = ml_s[p];
+        const float f = ex2(l.x - b0);
+        total += l.y * f;
+        x.x += v.x * f;
+        x.y += v.y * f;
+        x.z += v.z * f;
+        x.w += v.w * f;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (grp + i * kGroups < parts) add(grp + i * kGroups, y[i]);
+#pragma unroll 4
+    for (int p = grp + kAhead * kGroups; p < parts; p += kGroups) add(p, po[static_cast<int64_t>(p) * kLanes]);
+    x_s[grp][d] = x;
+    if (d == 0) t_s[grp] = total;
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
+        const float4 v = x_s[i][d];
+        x.x += v.x;
+        x.y += v.y;
+        x.z += v.z;
+        x.w += v.w;
+        total += t_s[i];
     }
     const bool none = total == 0.f;
-    a.out[at * D + threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(none ? 0.f : x * (a.v_scale / total)));
-    if (threadIdx.x == 0 && a.lse != nullptr) a.lse[at] = none ? -INFINITY : (b + log2f(total)) * 0.6931471805599453f;
+    const float inv = none ? 0.f : a.v_scale / total;
+    *reinterpret_cast<uint2 *>(a.out + at * D + 4 * d) =
+        none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+    if (d == 0 && a.lse != nullptr) a.lse[at] = none ? -INFINITY : (b0 + log2f(total)) * 0.6931471805599453f;
 }
 
 template <bool kFp8, int D, bool kWide, int kColWarps>
-cudaError_t launch_variant(const CUtensorMap &map, const KvAttnArgs &a, unsigned grid, cudaStream_t s) {
-    using C = KvCfg<kFp8, D>;
+cudaError_t launch_variant(const KvAttnArgs &a, cudaStream_t s) {
+    using C = KvCfg<kFp8, D, kColWarps>;
     auto kern = kv_attention_kernel<kFp8, D, kWide, kColWarps>;
     static std::atomic<uint64_t> configured{0};  // devices whose shared-memory limit is raised, a bit each
     int dev = 0;
@@ -597,26 +843,29 @@ cudaError_t launch_variant(const CUtensorMap &map, const KvAttnArgs &a, unsigned
         if (e != cudaSuccess) return e;
         if (dev < 64) configured.fetch_or(bit);
     }
-    return launch_pdl(kern, dim3(grid), dim3(kThreads), C::kSmemBytes, s, map, a);
+    CUtensorMap map;
+    if (!encode_kv_rows_map(&map, a.pool, a.pool_rows, C::kRowBytes, a.page_size < C::kTile ? a.page_size : C::kTile))
+        return cudaErrorInvalidValue;
+    const uint32_t ctas = 2u * static_cast<uint32_t>(device_sm_count());
+    if (ctas == 0) return cudaErrorInvalidDevice;
+    return launch_pdl(kern, dim3(a.items < ctas ? a.items : ctas), dim3(kThreads), C::kSmemBytes, s, map, a);
 }
 
 template <bool kFp8, int D>
-cudaError_t launch_format(const CUtensorMap &map, KvAttnArgs &a, cudaStream_t s) {
+cudaError_t launch_format(KvAttnArgs &a, cudaStream_t s) {
     const int cols = a.group * (a.num_heads / a.kv_heads);
     const int col_warps = cols <= 16 ? 1 : cols <= 32 ? 2 : 4;
     a.col_blocks = (cols + 16 * col_warps - 1) / (16 * col_warps);
-    const int64_t grid = static_cast<int64_t>(a.num_rows / a.group) * a.kv_heads * a.col_blocks * a.parts_bound;
-    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const unsigned n = static_cast<unsigned>(grid);
-    if (cols <= 8) return launch_variant<kFp8, D, false, 1>(map, a, n, s);
-    if (col_warps == 1) return launch_variant<kFp8, D, true, 1>(map, a, n, s);
-    if (col_warps == 2) return launch_variant<kFp8, D, true, 2>(map, a, n, s);
-    return launch_variant<kFp8, D, true, 4>(map, a, n, s);
+    const int64_t items = static_cast<int64_t>(a.num_rows / a.group) * a.kv_heads * a.col_blocks * a.parts_bound;
+    if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    a.items = static_cast<uint32_t>(items);
+    if (cols <= 8) return launch_variant<kFp8, D, false, 1>(a, s);
+    if (col_warps == 1) return launch_variant<kFp8, D, true, 1>(a, s);
+    if (col_warps == 2) return launch_variant<kFp8, D, true, 2>(a, s);
+    return launch_variant<kFp8, D, true, 4>(a, s);
 }
 
 }  // namespace
-
-int kv_box_rows(int32_t page_size) { return page_size < kTile ? page_size : kTile; }
 
 size_t kv_attention_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
                                     int32_t max_ctx) {
@@ -626,7 +875,7 @@ size_t kv_attention_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t
     return align256(n * static_cast<size_t>(head_dim) * 4) + align256(n * 8);
 }
 
-cudaError_t launch_kv_attention(const CUtensorMap &kv_map, KvAttnArgs &a, void *workspace, cudaStream_t s) {
+cudaError_t launch_kv_attention(KvAttnArgs &a, void *workspace, cudaStream_t s) {
     if (a.num_rows == 0) return cudaSuccess;
     a.max_parts = kv_max_parts(a.kv_heads);
     a.parts_bound = kv_parts_bound(a.max_ctx, a.max_parts);
@@ -635,12 +884,12 @@ cudaError_t launch_kv_attention(const CUtensorMap &kv_map, KvAttnArgs &a, void *
     a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
                                            align256(n * static_cast<size_t>(a.head_dim) * 4));
     cudaError_t e;
-    if (a.fp8) e = a.head_dim == 64 ? launch_format<true, 64>(kv_map, a, s) : launch_format<true, 128>(kv_map, a, s);
-    else e = a.head_dim == 64 ? launch_format<false, 64>(kv_map, a, s) : launch_format<false, 128>(kv_map, a, s);
+    if (a.fp8) e = a.head_dim == 64 ? launch_format<true, 64>(a, s) : launch_format<true, 128>(a, s);
+    else e = a.head_dim == 64 ? launch_format<false, 64>(a, s) : launch_format<false, 128>(a, s);
     if (e != cudaSuccess || a.parts_bound == 1) return e;
     const int64_t grid = static_cast<int64_t>(a.num_rows) * a.num_heads;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const dim3 gr(static_cast<unsigned>(grid)), b(static_cast<unsigned>(a.head_dim));
+    const dim3 gr(static_cast<unsigned>(grid)), b(kCombineThreads);
     return a.head_dim == 64 ? launch_pdl(kv_combine_kernel<64>, gr, b, 0, s, a)
                             : launch_pdl(kv_combine_kernel<128>, gr, b, 0, s, a);
 }
