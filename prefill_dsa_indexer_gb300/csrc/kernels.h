@@ -331,15 +331,20 @@ struct KvAttnArgs {
     float *lse;
     int32_t *status;
     // set by launch_kv_attention
-    int32_t max_parts;    // parts of the longest contexts
-    int32_t parts_bound;  // parts of a row at most, for contexts up to max_ctx
-    int32_t col_blocks;   // items side by side over the columns (group x query heads per KV head)
+    int32_t page_shift;    // log2 page_size
+    uint32_t hpg_mul;      // ceil(2^20 / hpg): column n is of row n * hpg_mul >> 20 of its group (n < 1024, hpg <= 128)
+    int32_t parts_shift;   // log2 of the parts of the longest contexts
+    uint32_t parts_bound;  // parts of a row at most, for contexts up to max_ctx
+    uint32_t col_blocks;   // items side by side over the columns (group x query heads per KV head)
     uint32_t items;       // (row group, KV head, column block, part)
     float *part_o;        // [R, H, parts_bound, D] the parts' outputs, in their own bases
     float2 *part_ml;      // [R, H, parts_bound] their bases (log2 units) and sums
 };
 
 cudaError_t launch_kv_attention(KvAttnArgs &a, void *workspace, cudaStream_t s);
+
+// The parts of an FP8 pool of head_dim 128 (kv_attention_fp8.cu; called by launch_kv_attention).
+cudaError_t launch_kv_attention_fp8(KvAttnArgs &a, cudaStream_t s);
 
 // 2D byte tensor [rows, row_bytes] (64, 128 or 256 bytes a row) with a box of box_rows rows by one swizzle
 // span of 64 or 128 bytes (api.cu).

@@ -32,18 +32,17 @@
 // elements 2^-25 below the column's largest), P is one fp16 term (2^-12), scaled by 2^7 so that weights
 // down to 2^-21 of the base stay normal.  (mma.sync on e4m3 operands was tried for S: the warps spend their time in
 // branches and instruction fetches there, 178 us against 108 us for 16 x 16K.)
-#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include <atomic>
 #include <type_traits>
 
-#include "kernels.h"
-#include "ptx.cuh"
+#include "kv_attention_common.cuh"
 
 namespace dsa {
 
 namespace {
+
+using namespace kv;
 
 constexpr int kConsumers = 4;                    // consumer warps
 constexpr int kProducer = 4, kQuery = 5;         // the warp that streams K and V, the one that brings queries
@@ -51,28 +50,10 @@ constexpr int kThreads = 32 * (kConsumers + 2);
 constexpr float kHeadroom = 15.0f;                // weights reach 2^15 (fp16 holds 65504) ...
 constexpr float kBias = 7.0f;                     // ... and a moved base leaves the largest at 2^7
 
-// The tokens of a part: as few as 128, doubled until at most max_parts cover the context.
-__host__ __device__ __forceinline__ int32_t kv_part(int32_t ctx, int32_t max_parts) {
-    int64_t p = 128;
-    while (p * max_parts < ctx) p *= 2;
-    return static_cast<int32_t>(p < ctx ? p : (ctx > 0 ? p : 128));
-}
-
-// Parts of a long context: 256 over all KV heads, so that one request alone fills the 152 SMs about
-// twice, but at least 32.
-__host__ __device__ __forceinline__ int32_t kv_max_parts(int32_t kv_heads) {
-    return kv_heads >= 8 ? 32 : kv_heads >= 4 ? 64 : kv_heads >= 2 ? 128 : 256;
-}
-
-__host__ __device__ __forceinline__ int32_t kv_parts(int32_t ctx, int32_t max_parts) {
-    const int32_t p = kv_part(ctx, max_parts);
-    return ctx <= 0 ? 1 : (ctx + p - 1) / p;
-}
-
 // Bound of kv_parts over every context up to max_ctx.
-int32_t kv_parts_bound(int32_t max_ctx, int32_t max_parts) {
-    const int32_t n = static_cast<int32_t>((static_cast<int64_t>(max_ctx) + 127) / 128);
-    return n < 1 ? 1 : (n < max_parts ? n : max_parts);
+uint32_t kv_parts_bound(int32_t max_ctx, int32_t parts_shift) {
+    const int64_t n = (static_cast<int64_t>(max_ctx) + 127) / 128, most = 1ll << parts_shift;
+    return static_cast<uint32_t>(n < 1 ? 1 : (n < most ? n : most));
 }
 
 // kColWarps consumer warps side by side over the columns (16 each), kTokWarps over a tile's tokens.
@@ -104,22 +85,6 @@ struct KvCfg {
     static_assert(kWarpTokens % kStepTokens == 0, "whole steps");
     static_assert(kSmemBytes <= 115712, "two CTAs per SM");
 };
-
-// What the query warp tells the consumers about an item.
-struct KvItem {
-    int32_t live;       // 0: no more items
-    int32_t t_begin, t_end;
-    int32_t ctx_min;    // tokens that every row of the group sees
-    int32_t row0, g, part, parts;
-    int32_t ctx[8];     // the group's contexts
-};
-static_assert(sizeof(KvItem) == 64, "item layout");
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -162,14 +127,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
-
 // Byte offset of 16-byte unit `u` of token `t` in a side (K or V) of a stage, as its TMA boxes landed.
 template <typename C>
 __device__ __forceinline__ uint32_t unit_at(int t, int u) {
@@ -191,36 +148,6 @@ __device__ __forceinline__ uint32_t q_unit_at(int n, int u) {
 template <int D>
 __device__ __forceinline__ int merge_at(int n, int d) {
     return n * D + (d ^ ((n >> 1 & 3) << 3));
-}
-
-// Item `i` of the launch: part fastest, then column block, KV head, row group.  Warp-collective; false:
-// the group's context has fewer parts.
-struct KvWhere {
-    int part, parts, col0, g, row0, req, t_begin, t_end, ctx, ctx_min, my_ctx;
-    bool bad;
-};
-
-template <int kCols>
-__device__ __forceinline__ bool kv_where(const KvAttnArgs &a, uint32_t i, int lane, KvWhere &w) {
-    w.part = static_cast<int>(i % a.parts_bound);
-    i /= a.parts_bound;
-    w.col0 = static_cast<int>(i % a.col_blocks) * kCols;
-    i /= a.col_blocks;
-    w.g = static_cast<int>(i % a.kv_heads);
-    w.row0 = static_cast<int>(i / a.kv_heads) * a.group;
-    const int row = w.row0 + (lane < a.group ? lane : 0);
-    const int n = a.row_ctx[row], req = a.row_req[row];
-    w.req = __shfl_sync(0xffffffffu, req, 0);
-    w.bad = __any_sync(0xffffffffu, n < 0 || n > a.max_ctx || req != w.req) || w.req < 0 || w.req >= a.num_requests;
-    w.my_ctx = w.bad ? 0 : n;  // of row `lane` of the group
-    w.ctx = __reduce_max_sync(0xffffffffu, w.my_ctx);
-    w.ctx_min = __reduce_min_sync(0xffffffffu, w.my_ctx);
-    const int tokens = kv_part(w.ctx, a.max_parts);
-    w.parts = kv_parts(w.ctx, a.max_parts);
-    if (w.part >= w.parts) return false;
-    w.t_begin = w.part * tokens;
-    w.t_end = w.t_begin + min(w.ctx - w.t_begin, tokens);
-    return true;
 }
 
 // kWide: more than 8 columns per warp (two n-tiles of the second product).
@@ -265,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == kProducer) {
         // ---- K and V: boxes of at most kTile rows, lane b issues box b of a tile
         const int box_rows = min(a.page_size, C::kTile);
-        const int boxes = C::kTile / box_rows;
+        const int box_shift = min(a.page_shift, 31 - __clz(C::kTile)), boxes = C::kTile >> box_shift;
         // box of this lane: token box b_t of the tile, K or V, column of 128 bytes
         const int b_t = lane / (2 * C::kBoxes), b_v = lane / C::kBoxes % 2, b_x = lane % C::kBoxes;
         const uint64_t policy = l2_evict_first_policy();
@@ -275,24 +202,25 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (uint32_t it = blockIdx.x; it < a.items && go; it += gridDim.x) {
             KvWhere w;
             if (!kv_where<kCols>(a, it, lane, w)) continue;
-            const int num_pages = (w.t_end + a.page_size - 1) / a.page_size;
+            const int num_pages = (w.t_end + a.page_size - 1) >> a.page_shift;
             const int32_t *table = a.block_table + static_cast<int64_t>(w.req) * a.bt_stride;
             auto load_ids = [&](int p) { return p + lane < num_pages ? table[p + lane] : 0; };
-            int batch = w.t_begin / a.page_size;  // page ids batch .. batch + 31 are in `ids`, one per lane
+            int batch = w.t_begin >> a.page_shift;  // page ids batch .. batch + 31 are in `ids`, one per lane
             int32_t ids = load_ids(batch), ids_next = load_ids(batch + 32);
             for (int t0 = w.t_begin; t0 < w.t_end; t0 += C::kTile) {
-                if (!mbar_wait_warp(&empty[s], phase, abort, a.status)) {
+                if (!wait_mbar_warp(&empty[s], phase, abort)) {
+                    gave_up(abort, a.status);
                     go = false;
                     break;
                 }
-                const int here = min(boxes, (w.t_end - t0 + box_rows - 1) / box_rows);  // boxes with tokens
-                if (t0 / a.page_size >= batch + 32) {
+                const int here = min(boxes, (w.t_end - t0 + box_rows - 1) >> box_shift);  // boxes with tokens
+                if ((t0 >> a.page_shift) >= batch + 32) {
                     batch += 32;
                     ids = ids_next;
                     ids_next = load_ids(batch + 32);
                 }
                 const int tb = t0 + b_t * box_rows;
-                int32_t id = __shfl_sync(0xffffffffu, ids, (tb / a.page_size - batch) & 31);
+                int32_t id = __shfl_sync(0xffffffffu, ids, ((tb >> a.page_shift) - batch) & 31);
                 if (lane == 0) mbar_arrive_expect_tx(&full[s], here * box_rows * 2 * C::kRowBytes);
                 __syncwarp();
                 if (b_t < here) {
@@ -300,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         report(a.status, DSA_ERR_BOUNDS);
                         id = 0;
                     }
-                    const int y = ((id * a.kv_heads + w.g) * 2 + b_v) * a.page_size + tb % a.page_size;
+                    const int y = ((id * a.kv_heads + w.g) * 2 + b_v) * a.page_size + (tb & (a.page_size - 1));
                     tma_load_2d_hint(smem + s * C::kStageBytes + b_v * C::kSide + b_x * C::kPlane +
                                          b_t * box_rows * C::kBoxBytes,
                                      &kv_map, &full[s], b_x * C::kBoxBytes, y, policy);
@@ -312,7 +240,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
             if (kTokWarps > 1 && go) {  // the next stage is the consumers', to merge the item's output in
-                if (!mbar_wait_warp(&empty[s], phase, abort, a.status)) break;
+                if (!wait_mbar_warp(&empty[s], phase, abort)) {
+                    gave_up(abort, a.status);
+                    break;
+                }
                 if (lane == 0) mbar_arrive(&full[s]);
                 ++issued;
                 if (++s == C::kStages) {
@@ -357,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             };
             load(0);
-            if (!mbar_wait_warp(q_empty, phase, abort, a.status)) return;
+            if (!wait_mbar_warp(q_empty, phase, abort)) return gave_up(abort, a.status);
             phase ^= 1;
 #pragma unroll 1
             for (int c = 0; c < kColWarps; ++c) {
@@ -413,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
         }
-        if (!mbar_wait_warp(q_empty, phase, abort, a.status)) return;
+        if (!wait_mbar_warp(q_empty, phase, abort)) return gave_up(abort, a.status);
         if (lane == 0) {
             item_s->live = 0;
             mbar_arrive(q_full);
@@ -426,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int s = 0;
     uint32_t phase = 0, q_phase = 0;
     for (;; q_phase ^= 1) {
-        if (!mbar_wait_warp(q_full, q_phase, abort, a.status)) return;
+        if (!wait_mbar_warp(q_full, q_phase, abort)) return gave_up(abort, a.status);
         if (item_s->live == 0) return;
         const int t_begin = item_s->t_begin, t_end = item_s->t_end, ctx_min = item_s->ctx_min;
         const int row0 = item_s->row0, g = item_s->g & 0xffff, col0 = (item_s->g >> 16) + 16 * cw;
@@ -460,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         float o[KS][NT][4] = {};
         float base[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
         for (int tile0 = t_begin; tile0 < t_end; tile0 += C::kTile) {
-            if (!mbar_wait_warp(&full[s], phase, abort, a.status)) return;
+            if (!wait_mbar_warp(&full[s], phase, abort)) return gave_up(abort, a.status);
             const uint32_t ks = smem_u32(smem + s * C::kStageBytes), vs = ks + C::kSide;
 #pragma unroll 1
             for (int ts = tw * C::kWarpTokens; ts < (tw + 1) * C::kWarpTokens && !idle; ts += C::kStepTokens) {
@@ -664,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if constexpr (kTokWarps > 1) {
             // the token warps' outputs meet in the next stage of the ring, each in its own base; every consumer
             // then adds up its share of the columns, token warps in order
-            if (!mbar_wait_warp(&full[s], phase, abort, a.status)) return;
+            if (!wait_mbar_warp(&full[s], phase, abort)) return gave_up(abort, a.status);
             float *mo = reinterpret_cast<float *>(smem + s * C::kStageBytes);
             float *mine = mo + warp * C::kMergeFloats;
 #pragma unroll
@@ -690,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(merge);
-            if (!mbar_wait_warp(merge, q_phase, abort, a.status)) return;
+            if (!wait_mbar_warp(merge, q_phase, abort)) return gave_up(abort, a.status);
             constexpr int kLanes = D / 4;  // lanes of a column
             const int first = warp * (32 / kLanes) + lane / kLanes, d = lane % kLanes * 4;
             const int here = min(kCols, cols - (col0 - 16 * cw));
@@ -774,7 +705,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const __gri
     const int row0 = static_cast<int>(at / a.num_heads) / a.group * a.group;
     int ctx = 0;
     for (int i = 0; i < a.group; ++i) ctx = max(ctx, min(a.row_ctx[row0 + i], a.max_ctx));
-    const int parts = kv_parts(ctx, a.max_parts);
+    const int parts = kv_parts(ctx, kv_part_shift(ctx, a.parts_shift));
     if (parts == 1) return;  // written by the attention kernel
     const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes;
     const float4 *po = reinterpret_cast<const float4 *>(a.part_o + at * a.parts_bound * D) + d;
@@ -833,22 +764,15 @@ template <bool kFp8, int D, bool kWide, int kColWarps>
 cudaError_t launch_variant(const KvAttnArgs &a, cudaStream_t s) {
     using C = KvCfg<kFp8, D, kColWarps>;
     auto kern = kv_attention_kernel<kFp8, D, kWide, kColWarps>;
-    static std::atomic<uint64_t> configured{0};  // devices whose shared-memory limit is raised, a bit each
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    static std::atomic<uint64_t> configured{0};
+    cudaError_t e = raise_smem_limit(kern, C::kSmemBytes, configured);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (dev >= 64 || !(configured.load() & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-        if (e != cudaSuccess) return e;
-        if (dev < 64) configured.fetch_or(bit);
-    }
     CUtensorMap map;
     if (!encode_kv_rows_map(&map, a.pool, a.pool_rows, C::kRowBytes, a.page_size < C::kTile ? a.page_size : C::kTile))
         return cudaErrorInvalidValue;
-    const uint32_t ctas = 2u * static_cast<uint32_t>(device_sm_count());
+    const uint32_t ctas = persistent_ctas(a);
     if (ctas == 0) return cudaErrorInvalidDevice;
-    return launch_pdl(kern, dim3(a.items < ctas ? a.items : ctas), dim3(kThreads), C::kSmemBytes, s, map, a);
+    return launch_pdl(kern, dim3(ctas), dim3(kThreads), C::kSmemBytes, s, map, a);
 }
 
 template <bool kFp8, int D>
@@ -869,7 +793,7 @@ cudaError_t launch_format(KvAttnArgs &a, cudaStream_t s) {
 
 size_t kv_attention_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
                                     int32_t max_ctx) {
-    const size_t parts = static_cast<size_t>(kv_parts_bound(max_ctx, kv_max_parts(kv_heads)));
+    const size_t parts = static_cast<size_t>(kv_parts_bound(max_ctx, kv_parts_shift(kv_heads)));
     if (parts <= 1) return 0;
     const size_t n = static_cast<size_t>(num_rows) * static_cast<size_t>(num_heads) * parts;
     return align256(n * static_cast<size_t>(head_dim) * 4) + align256(n * 8);
@@ -877,14 +801,17 @@ size_t kv_attention_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t
 
 cudaError_t launch_kv_attention(KvAttnArgs &a, void *workspace, cudaStream_t s) {
     if (a.num_rows == 0) return cudaSuccess;
-    a.max_parts = kv_max_parts(a.kv_heads);
-    a.parts_bound = kv_parts_bound(a.max_ctx, a.max_parts);
+    for (a.page_shift = 4; 1 << a.page_shift < a.page_size;) ++a.page_shift;
+    const uint32_t hpg = static_cast<uint32_t>(a.num_heads / a.kv_heads);
+    a.hpg_mul = ((1u << 20) + hpg - 1) / hpg;
+    a.parts_shift = kv_parts_shift(a.kv_heads);
+    a.parts_bound = kv_parts_bound(a.max_ctx, a.parts_shift);
     const size_t n = static_cast<size_t>(a.num_rows) * static_cast<size_t>(a.num_heads) * a.parts_bound;
     a.part_o = static_cast<float *>(workspace);
     a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
                                            align256(n * static_cast<size_t>(a.head_dim) * 4));
     cudaError_t e;
-    if (a.fp8) e = a.head_dim == 64 ? launch_format<true, 64>(a, s) : launch_format<true, 128>(a, s);
+    if (a.fp8) e = a.head_dim == 64 ? launch_format<true, 64>(a, s) : launch_kv_attention_fp8(a, s);
     else e = a.head_dim == 64 ? launch_format<false, 64>(a, s) : launch_format<false, 128>(a, s);
     if (e != cudaSuccess || a.parts_bound == 1) return e;
     const int64_t grid = static_cast<int64_t>(a.num_rows) * a.num_heads;

@@ -1,0 +1,796 @@
+// kv_attention_fp8.cu -- dense attention over a paged FP8 K/V pool of head_dim 128 (dsa_kv_attention).
+//
+//   out[r, h, :] = sum_t softmax_t(sm_scale <q[r,h,:], K_g,t>) V_g,t   over t < row_ctx[r]
+//
+// An FP8 token of a KV head is 256 bytes, so the bytes leave half the time of a bf16 one per column, and
+// warp-level MMAs, which need the codes as fp16 fragments, do not keep up (kv_attention.cu: 32 x 16K-64K
+// tokens in 327 us against 203 us at the copy bandwidth, nothing but conversions and issue slots in the
+// way).  Here the fifth-generation tensor cores take the codes as they lie in shared memory:
+//
+//     S^T[128 tokens x NC]  = K Q^T      A: the K tile (K-major), B: q as hi, then lo e4m3 terms
+//     O^T[128 dims x NC]   += V^T P^T    A: the V tile read MN-major, B: P as hi, then lo e4m3 terms (MN-major)
+//
+// with NC (16, 32 or 64) columns, (row of the group, query head of the KV head) pairs, in N.  An MMA with so
+// small an N costs its A operand's passage: 40 cycles an SM for N <= 32, 48 for 64 measured, so a tile's
+// 16 take 640 to 770 of the 1,490 cycles that its 32 KB take at the copy bandwidth.  A token is a TMEM lane: a
+// softmax thread reads its token's scores of all columns, P = 2^(S - b) with a lazy base b per column, splits
+// each weight into hi + lo and writes its row of P.  The base moves, and O^T is rescaled in TMEM, only when a
+// score exceeds it by 2^8.7.  The softmax is what takes the issue slots: about 6 instructions a weight, with
+// packed fp32 pairs.
+//
+// Roles: four softmax warps (TMEM lane quadrants), a TMA producer (K and V tiles of 16 KB through a ring of
+// units), an MMA issuer, a query warp (items and their query images).  Two persistent CTAs per SM take the
+// items (row group, KV head, column block, part of the context) in turn; parts are merged by
+// kv_combine_kernel (kv_attention.cu).
+//
+// Precision: e4m3 x e4m3 products are exact and accumulate in fp32.  q is scaled by a power of two per
+// column and written as hi + lo (exact but for elements 2^-10 below the column's largest, which keep 2^-18 of
+// it).  A weight as hi + lo keeps 2^-8 of itself at worst, 2^-10.5 on average, against the output's own
+// rounding of 2^-9 on average (bf16); weights below 2^-12 of the largest keep 2^-16 of that largest.
+#include "kv_attention_common.cuh"
+#include "mla_fp8_common.cuh"
+
+namespace dsa {
+
+namespace {
+
+using namespace kv;
+using fp8mla::e4m3x2;
+using fp8mla::split_pair;
+using fp8mla::sw128;
+
+constexpr int kSoftmax = 4;                                // softmax warps
+constexpr int kProducer = 4, kScores = 5, kQuery = 6, kValues = 7;  // the other warps
+constexpr int kThreads = 32 * 8;                          // two warpgroups
+// Registers: 128 a thread at launch (two CTAs fill the SM); the softmax warpgroup takes 40 of the other's.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kOtherRegs = 88;
+static_assert(kSoftmaxRegs + kOtherRegs == 2 * kLaunchRegs, "the warpgroups share what the CTA was launched with");
+constexpr int kTile = 128;                                 // tokens of a tile
+constexpr int kDim = 128;
+constexpr int kUnitBytes = kTile * kDim;                   // K or V of a tile
+constexpr float kTop = 8.7f;                               // weights reach 2^8.7 = 416 (e4m3 holds 448) ...
+constexpr float kBias = 6.0f;                              // ... and a moved base leaves the largest at 2^6
+
+// What the query warp tells the others about an item.
+struct Item {
+    int32_t live;              // 0: no more items
+    int32_t t_begin, t_end;
+    int32_t ctx_min, ctx_max;  // over the rows of the group
+    int32_t cols;              // real columns
+    int32_t part, parts;
+    int32_t ctx[8];            // the group's contexts
+};
+
+// An item's columns: log2 units per unit of score, tokens seen, row * num_heads + head.
+template <int NC>
+struct Columns {
+    float scale[NC];
+    int32_t ctx[NC], at[NC];
+};
+
+template <int NC>
+struct Cfg {
+    // K and V tiles go through rings of their own, so that whoever waits for a tile has waited for every one before
+    // it in its slot (a barrier's parity alone cannot tell a phase from the one two before it)
+    static constexpr int kK = 2, kV = NC == 16 ? 3 : 2, kUnits = kK + kV;
+    static constexpr int kQBytes = 2 * NC * kDim, kQBufs = NC == 64 ? 1 : 2;
+    static constexpr uint32_t kTmemO = 2 * NC;             // two score buffers, then the output
+    static constexpr uint32_t kTmemCols = NC == 16 ? 64 : NC == 32 ? 128 : 256;  // two CTAs share the SM's 512
+    static constexpr bool kKeep = NC <= 32;                // a thread keeps its scores in registers
+    static constexpr int OFF_Q = kUnits * kUnitBytes;      // [kQBufs]: rows hi 0 .. NC - 1, lo NC .. 2 NC - 1
+    static constexpr int OFF_P = OFF_Q + kQBufs * kQBytes;      // a token's row: NC hi, NC lo bytes; then the output's way out
+    static constexpr int OFF_COLS = OFF_P + kTile * 128;   // [2] by item parity
+    static constexpr int OFF_ITEM = OFF_COLS + 2 * static_cast<int>(sizeof(Columns<NC>));
+    static constexpr int OFF_MAX = OFF_ITEM + 2 * 64;      // [4][NC] a warp's largest score
+    static constexpr int OFF_BASE = OFF_MAX + 4 * NC * 4;  // [4][NC] minus the bases, a copy per warp
+    static constexpr int OFF_FAC = OFF_BASE + 4 * NC * 4;  // [4][NC] rescale factors
+    static constexpr int OFF_SUM = OFF_FAC + 4 * NC * 4;   // [2][4][NC] a warp's weights, by item parity
+    static constexpr int OFF_BARS = OFF_SUM + 2 * 4 * NC * 4;
+    static constexpr int kNumBars = 2 * kUnits + 2 * 2 + 2 * 2 + kQBufs + 4;
+    static constexpr int OFF_MISC = OFF_BARS + kNumBars * 8;
+    static constexpr int kSmemBytes = OFF_MISC + 16 + 1024;
+    static_assert(kTmemO + NC <= kTmemCols, "TMEM plan");
+    static_assert(kSmemBytes <= 115712, "two CTAs per SM");
+};
+
+// Sums (or maxima) over the warp's lanes of v[0..N): afterwards v[0] of lane l belongs to column
+// lane_column<N>(l).  Halves of the columns change hands, so N columns take N shuffles (N = 16: 16, 32: 31).
+template <int N, bool kMax>
+__device__ __forceinline__ void reduce_lanes(float (&v)[N], int lane) {
+    int n = N;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool up = (lane & off) != 0;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                if (i >= n) break;
+                const float keep = up ? v[i + n] : v[i];
+                const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + n], off);
+                v[i] = kMax ? fmaxf(keep, got) : keep + got;
+            }
+        } else {
+            const float got = __shfl_xor_sync(0xffffffffu, v[0], off);
+            v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+        }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ int lane_column(int lane) {
+    static_assert(N == 16 || N == 32, "");
+    return N == 32 ? lane : lane >> 1;
+}
+
+// The columns' sums or maxima over the warp's tokens into dst[0..NC).
+template <int NC, bool kMax>
+__device__ __forceinline__ void reduce_columns(const float *v, float *dst, int lane) {
+    constexpr int kN = NC < 32 ? NC : 32;
+#pragma unroll
+    for (int c = 0; c < NC; c += kN) {
+        float w[kN];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) w[j] = v[c + j];
+        reduce_lanes<kN, kMax>(w, lane);
+        if (kN == 32 || (lane & 1) == 0) dst[c + lane_column<kN>(lane)] = w[0];
+    }
+}
+
+// OR of a predicate over the four softmax warps, who all meet here.
+__device__ __forceinline__ bool meet_any(bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred.aligned q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(p))
+        : "memory");
+    return r != 0;
+}
+
+// Whether any of four e4m3 codes is NaN (0x7f or 0xff).
+__device__ __forceinline__ bool any_nan4(uint32_t v) { return __vcmpeq4(v & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0; }
+
+template <int NC>
+__global__ void __launch_bounds__(kThreads, 2)
+    kv_attention_fp8_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ KvAttnArgs a) {
+    using C = Cfg<NC>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Columns<NC> *cols_s = reinterpret_cast<Columns<NC> *>(smem + C::OFF_COLS);
+    Item *item_s = reinterpret_cast<Item *>(smem + C::OFF_ITEM);
+    float *sum_s = reinterpret_cast<float *>(smem + C::OFF_SUM);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BARS);  // [kK + kV] K or V landed
+    uint64_t *empty = full + C::kUnits;                                 // [kK + kV] the MMAs that read it are done
+    uint64_t *s_full = empty + C::kUnits;                               // [2] scores in TMEM
+    uint64_t *s_empty = s_full + 2;                             // [2] softmax has read them
+    uint64_t *q_full = s_empty + 2, *q_empty = q_full + 2;      // [2] an item and its columns, by item parity
+    uint64_t *img_empty = q_empty + 2;                                  // [kQBufs] the MMAs are done with the queries
+    uint64_t *p_full = img_empty + C::kQBufs;                                     // weights written (and O^T rescaled)
+    uint64_t *pv_done = p_full + 1;                                     // O^T += V^T P^T done
+    uint64_t *o_empty = pv_done + 1;                                    // the item's output is read
+    uint64_t *drained = o_empty + 1;                                    // after a wait gave up: no MMA is left
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+    volatile int32_t *levels_s = reinterpret_cast<volatile int32_t *>(smem + C::OFF_MISC + 8);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        *abort = 0;
+        *levels_s = 0;
+        for (int s = 0; s < C::kUnits; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&s_full[s], 1);
+            mbar_init(&s_empty[s], kSoftmax);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&q_full[s], 1);
+            mbar_init(&q_empty[s], kSoftmax + 2);
+        }
+        for (int s = 0; s < C::kQBufs; ++s) mbar_init(&img_empty[s], 1);
+        mbar_init(p_full, kSoftmax);
+        mbar_init(pv_done, 1);
+        mbar_init(o_empty, kSoftmax);
+        mbar_init(drained, 2);
+        fence_mbar_init();
+        prefetch_tensormap(&kv_map);
+    }
+    if (warp == kScores) {
+        tmem_alloc(tmem_slot, C::kTmemCols);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    const int hpg = a.num_heads / a.kv_heads, cols = a.group * hpg;
+
+    if (warp >= kSoftmax) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kProducer) {
+            // ---- K and V: boxes of at most 128 rows, lane b issues box b of a unit
+            const int box_rows = min(a.page_size, kTile);
+            const int box_shift = min(a.page_shift, 7), boxes = kTile >> box_shift;
+            const uint64_t policy = l2_evict_first_policy();
+            uint32_t issued = 0;  // tiles
+            bool go = true;
+            for (uint32_t it = blockIdx.x; it < a.items && go; it += gridDim.x) {
+                KvWhere w;
+                if (!kv_where<NC>(a, it, lane, w)) continue;
+                const int num_pages = (w.t_end + a.page_size - 1) >> a.page_shift;
+                const int32_t *table = a.block_table + static_cast<int64_t>(w.req) * a.bt_stride;
+                auto load_ids = [&](int p) { return p + lane < num_pages ? table[p + lane] : 0; };
+                int batch = w.t_begin >> a.page_shift;  // page ids batch .. batch + 31 are in `ids`, one per lane
+                int32_t ids = load_ids(batch), ids_next = load_ids(batch + 32);
+                for (int t0 = w.t_begin; t0 < w.t_end && go; t0 += kTile) {
+                    const int here = min(boxes, (w.t_end - t0 + box_rows - 1) >> box_shift);  // boxes with tokens
+                    if ((t0 >> a.page_shift) >= batch + 32) {
+                        batch += 32;
+                        ids = ids_next;
+                        ids_next = load_ids(batch + 32);
+                    }
+                    const int tb = t0 + (lane < boxes ? lane : 0) * box_rows;
+                    int32_t id = __shfl_sync(0xffffffffu, ids, ((tb >> a.page_shift) - batch) & 31);
+                    if (lane < here && (id < 0 || id >= a.num_pages)) {
+                        report(a.status, DSA_ERR_BOUNDS);
+                        id = 0;
+                    }
+                    const int y = (id * a.kv_heads + w.g) * 2 * a.page_size + (tb & (a.page_size - 1));
+#pragma unroll 1
+                    for (int v = 0; v < 2 && go; ++v) {  // K, then V
+                        const uint32_t ring = v ? C::kV : C::kK, turn = issued / ring;
+                        const uint32_t u = (v ? C::kK : 0) + issued - turn * ring;
+                        if (!wait_mbar_warp(&empty[u], (turn & 1) ^ 1, abort)) {
+                            gave_up(abort, a.status);
+                            go = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&full[u], here * box_rows * kDim);
+                        __syncwarp();
+                        if (lane < here)
+                            tma_load_2d_hint(smem + u * kUnitBytes + lane * box_rows * kDim, &kv_map, &full[u], 0,
+                                             y + v * a.page_size, policy);
+                    }
+                    ++issued;
+                }
+            }
+            if (*abort && lane == 0) {  // leave no copy in flight behind: the last tiles issued in either ring
+                for (int v = 0; v < 2; ++v) {
+                    const uint32_t ring = v ? C::kV : C::kK;
+                    for (uint32_t i = issued > ring ? issued - ring : 0; i < issued; ++i) {
+                        const long long t0 = clock64();
+                        while (!mbar_try_wait(&full[(v ? C::kK : 0) + i % ring], (i / ring) & 1) &&
+                               clock64() - t0 < kWaitTimeoutCycles) {
+                        }
+                    }
+                }
+            }
+        } else if (warp == kQuery) {
+            // ---- items, their columns and query images (rows hi 0 .. NC - 1, lo NC .. 2 NC - 1 of 128 bytes)
+            uint32_t count = 0;  // items handed on
+            bool go = true;
+            for (uint32_t it = blockIdx.x; it < a.items && go; it += gridDim.x) {
+                KvWhere w;
+                if (!kv_where<NC>(a, it, lane, w)) continue;
+                if (w.bad && w.part == 0 && lane == 0) report(a.status, DSA_ERR_BOUNDS);
+                // 16 dims (a unit) of a column per lane and turn, four columns a turn.  The first 16 columns are
+                // loaded while the item before is still worked on; then they take their places in the image as
+                // they are (their hi and lo terms fill the same 32 bytes), and one short loop converts them: code
+                // that runs once an item comes from L2, at about 150 cycles for eight instructions
+                const int unit = lane & 7, sub = lane >> 3;
+                const uint32_t parity = count & 1, buf = count % C::kQBufs;
+                uint8_t *img = smem + C::OFF_Q + buf * C::kQBytes;
+                uint4 v0[4], v1[4];
+                auto load = [&](int c0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int n = w.col0 + c0 + 4 * i + sub;
+                        v0[i] = v1[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (n < cols) {
+                            const int row = static_cast<int>(n * a.hpg_mul >> 20);
+                            const uint4 *src = reinterpret_cast<const uint4 *>(
+                                a.q + (w.row0 + row) * a.q_stride + static_cast<int64_t>(w.g * hpg + n - row * hpg) * kDim +
+                                unit * 16);
+                            v0[i] = src[0];
+                            v1[i] = src[1];
+                        }
+                    }
+                };
+                load(0);
+                if (!wait_mbar_warp(&q_empty[parity], (count >> 1 & 1) ^ 1, abort) ||
+                    !wait_mbar_warp(&img_empty[buf], (count / C::kQBufs & 1) ^ 1, abort)) {
+                    gave_up(abort, a.status);
+                    go = false;
+                    break;
+                }
+                Columns<NC> *cs = cols_s + parity;
+#pragma unroll 1
+                for (int c0 = 0; c0 < NC; c0 += 16) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        *reinterpret_cast<uint4 *>(img + sw128(c0 + 4 * i + sub, unit)) = v0[i];
+                        *reinterpret_cast<uint4 *>(img + sw128(NC + c0 + 4 * i + sub, unit)) = v1[i];
+                    }
+                    if (c0 + 16 < NC) load(c0 + 16);
+#pragma unroll 1
+                    for (int n = c0 + sub; n < c0 + 16; n += 4) {
+                        uint4 *hi_at = reinterpret_cast<uint4 *>(img + sw128(n, unit));
+                        uint4 *lo_at = reinterpret_cast<uint4 *>(img + sw128(NC + n, unit));
+                        const uint4 r0 = *hi_at, r1 = *lo_at;
+                        const uint32_t h[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+                        // the column's largest |q| by its bits (an infinity or a NaN is above every number)
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) top = max(top, max(h[y] << 16 & 0x7fff0000u, h[y] & 0x7fff0000u));
+#pragma unroll
+                        for (int y = 1; y < 8; y <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
+                        const bool finite = top < 0x7f800000u;
+                        // 2^e brings it to (224, 448]
+                        int e = 0;
+                        if (top > 0 && finite) {
+                            e = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+                            e = max(-120, min(120, e));
+                        }
+                        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const uint2 p0 = split_pair(bf16_lo(h[2 * y]) * up, bf16_hi(h[2 * y]) * up);
+                            const uint2 p1 = split_pair(bf16_lo(h[2 * y + 1]) * up, bf16_hi(h[2 * y + 1]) * up);
+                            hi[y] = p0.x | (p1.x << 16);
+                            lo[y] = p0.y | (p1.y << 16);
+                        }
+                        *hi_at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *lo_at = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        const int col = w.col0 + n, row = col < cols ? static_cast<int>(col * a.hpg_mul >> 20) : 0;
+                        const int ctx = __shfl_sync(0xffffffffu, w.my_ctx, row);
+                        if (unit == 0) {
+                            // a masked score is -inf times the scale: neither zero nor infinity.  A NaN or an infinity
+                            // in q makes its column's scores, and so its output, NaN
+                            const float scale = a.s_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                            cs->scale[n] = finite ? fminf(fmaxf(scale, 1.17549435e-38f), 3.40282347e38f)
+                                                  : __uint_as_float(0x7fc00000u);
+                            cs->ctx[n] = col < cols ? ctx : 0;
+                            cs->at[n] = (w.row0 + row) * a.num_heads + w.g * hpg + (col < cols ? col - row * hpg : 0);
+                        }
+                    }
+                }
+                Item *item = item_s + parity;
+                if (lane < 8) item->ctx[lane] = w.my_ctx;
+                if (lane == 0) {
+                    item->live = 1;
+                    item->t_begin = w.t_begin;
+                    item->t_end = w.t_end;
+                    item->ctx_min = w.ctx_min;
+                    item->ctx_max = w.ctx;
+                    item->cols = min(NC, cols - w.col0);
+                    item->part = w.part;
+                    item->parts = w.parts;
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[parity]);
+                ++count;
+            }
+            if (go && wait_mbar_warp(&q_empty[count & 1], (count >> 1 & 1) ^ 1, abort) && lane == 0) {
+                item_s[count & 1].live = 0;
+                mbar_arrive(&q_full[count & 1]);
+            }
+        } else if (lane == 0) {
+            // ---- the two MMA issuers, one thread each: an MMA's issue lasts as long as its passage through the
+            // tensor core, so one thread for both products would set the pace
+            const bool values = warp == kValues;
+            const uint32_t idesc = values ? make_idesc(kDim, NC, 0, 0, true, true) : make_idesc(kTile, NC, 0, 0, false, false);
+            const uint32_t ring = values ? C::kV : C::kK, slot0 = values ? C::kK : 0;
+            const uint32_t ua = smem_u32(smem);
+            const uint64_t b0 = sdesc_sw128(smem_u32(smem + (values ? C::OFF_P : C::OFF_Q)), 16, 1024);
+            const uint32_t step = values ? 256 : 2, lo = values ? NC / 16 : NC * kDim / 16;
+            uint32_t count = 0, p_phase = 0, o_phase = 1;  // count: tiles
+            bool ok = true;
+            for (uint32_t n = 0; ok; ++n) {
+                ok = wait_mbar(&q_full[n & 1], n >> 1 & 1, abort);
+                if (!ok) break;
+                const Item *item = item_s + (n & 1);
+                const uint64_t bd = values ? b0 : b0 + n % C::kQBufs * (C::kQBytes / 16);
+                if (item->live == 0) break;
+                const int tiles = (item->t_end - item->t_begin + kTile - 1) / kTile;
+                mbar_arrive(&q_empty[n & 1]);
+                if (!values && tiles == 0) mbar_arrive(&img_empty[n % C::kQBufs]);
+                if (values && tiles > 0) {
+                    ok = wait_mbar(o_empty, o_phase, abort);
+                    o_phase ^= 1;
+                }
+                for (int i = 0; ok && i < tiles; ++i, ++count) {
+                    const uint32_t turn = count / ring, slot = slot0 + count - turn * ring, sb = count & 1;
+                    ok = wait_mbar(&full[slot], turn & 1, abort);
+                    // values: levels 0 accumulates in O^T.  Else one product for each context of the group, into the
+                    // scores' buffer, from where the softmax warps add its columns
+                    int levels = 0;
+                    bool apart = false;
+                    while (ok) {
+                        ok = values ? wait_mbar(p_full, p_phase, abort)
+                                    : wait_mbar(&s_empty[sb], ((count >> 1) & 1) ^ 1, abort);
+                        p_phase ^= 1;
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (values && !apart) {
+                            levels = *levels_s;
+                            apart = levels > 0;
+                        }
+                        const uint32_t d = values && !apart ? tmem + C::kTmemO : tmem + sb * NC;
+                        const uint32_t add = values && !apart && i > 0 ? 1u : 0u;
+                        const uint64_t ad = sdesc_sw128(ua + slot * kUnitBytes, 16, 1024);
+#pragma unroll 2
+                        for (int k = 0; k < 8; ++k)
+                            mma_f8(d, ad + (k & 3) * step, bd + (k >> 2) * lo + (k & 3) * step, idesc, k > 0 ? 1u : add);
+                        --levels;
+                        if (levels <= 0) mma_commit(&empty[slot]);
+                        mma_commit(values ? pv_done : &s_full[sb]);
+                        if (levels <= 0) break;
+                    }
+                    if (!values && ok && i == tiles - 1) mma_commit(&img_empty[n % C::kQBufs]);
+                }
+            }
+            if (!ok) gave_up(abort, a.status);
+            if (*abort) {  // leave no MMA in flight behind
+                mma_commit(drained);
+                const long long t0 = clock64();
+                while (!mbar_try_wait(drained, 0) && clock64() - t0 < kWaitTimeoutCycles) {
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        // ---- softmax: thread = token (TMEM lane) of a tile, then dim of the output.  A wait that gives up makes
+        // its warp `dead`.  Every meeting whose first round is true has a second one that asks for dead warps,
+        // after which all leave: so no warp waits for one that has gone
+        const int self = warp * 32 + lane;
+        const uint32_t quad = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        float *max_s = reinterpret_cast<float *>(smem + C::OFF_MAX);
+        float *nbase = reinterpret_cast<float *>(smem + C::OFF_BASE) + warp * NC;
+        float *fac = reinterpret_cast<float *>(smem + C::OFF_FAC) + warp * NC;
+        uint32_t s_count = 0, pv_phase = 0;  // s_count: tiles
+        bool dead = false, pv_open = false;  // pv_open: a product of P is out whose end has not been seen
+        auto pv_wait = [&]() {
+            if (!pv_open) return;
+            dead |= !wait_mbar_warp(pv_done, pv_phase, abort);
+            pv_phase ^= 1;
+            pv_open = false;
+            tc_fence_after();
+        };
+        auto someone_dead = [&]() { return meet_any(dead) && meet_any(dead); };
+        for (uint32_t item_n = 0;; ++item_n) {
+            const uint32_t parity = item_n & 1;
+            dead |= !wait_mbar_warp(&q_full[parity], item_n >> 1 & 1, abort);
+            const Item *item = item_s + parity;
+            if (dead || item->live == 0) {
+                someone_dead();
+                break;
+            }
+            const Columns<NC> *cs = cols_s + parity;
+            const int t_begin = item->t_begin, t_end = item->t_end, ctx_min = item->ctx_min, ctx_max = item->ctx_max;
+            const int ncols = item->cols, part = item->part, parts = item->parts;
+            const int tiles = (t_end - t_begin + kTile - 1) / kTile;
+
+            float l[NC];
+#pragma unroll
+            for (int n = 0; n < NC; ++n) l[n] = 0.f;
+            for (int n = lane; n < NC; n += 32) nbase[n] = 0.f;
+            __syncwarp();
+            bool leave = false;
+            for (int i = 0; i < tiles; ++i, ++s_count) {
+                const int t0 = t_begin + i * kTile, t = t0 + self;
+                const uint32_t sb = s_count & 1;
+                const uint32_t v_turn = s_count / C::kV, vslot = C::kK + s_count - v_turn * C::kV;
+                uint4 *vrow = reinterpret_cast<uint4 *>(smem + vslot * kUnitBytes + self * kDim);
+                dead |= !wait_mbar_warp(&s_full[sb], (s_count >> 1) & 1, abort);
+                tc_fence_after();
+                const bool edge = t0 + kTile > ctx_min;  // some column does not see all of the tile
+
+                // scores of this token, columns c .. c + 15, in log2 units against their bases
+                auto scores = [&](int c, float *x) {
+                    uint32_t h[16];
+                    tmem_ld16(quad + sb * NC + c, h);
+                    tmem_ld_wait();
+                    reg_fence(h);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 sc = *reinterpret_cast<const float4 *>(cs->scale + c + j);
+                        const float4 nb = *reinterpret_cast<const float4 *>(nbase + c + j);
+                        const float2 p = __ffma2_rn(make_float2(__uint_as_float(h[j]), __uint_as_float(h[j + 1])),
+                                                    make_float2(sc.x, sc.y), make_float2(nb.x, nb.y));
+                        const float2 q = __ffma2_rn(make_float2(__uint_as_float(h[j + 2]), __uint_as_float(h[j + 3])),
+                                                    make_float2(sc.z, sc.w), make_float2(nb.z, nb.w));
+                        x[j] = p.x;
+                        x[j + 1] = p.y;
+                        x[j + 2] = q.x;
+                        x[j + 3] = q.y;
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const int4 n = *reinterpret_cast<const int4 *>(cs->ctx + c + j);
+                            if (t >= n.x) x[j] = -INFINITY;
+                            if (t >= n.y) x[j + 1] = -INFINITY;
+                            if (t >= n.z) x[j + 2] = -INFINITY;
+                            if (t >= n.w) x[j + 3] = -INFINITY;
+                        }
+                    }
+                };
+                float x[C::kKeep ? NC : 16];
+                // at most twice round: the first tile sets the bases, later ones move those that no longer fit
+#pragma unroll 1
+                for (bool settled = false;;) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < NC; c += 16) {
+                        float *xc = x + (C::kKeep ? c : 0);
+                        scores(c, xc);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) top = fmaxf(top, fmaxf(xc[j], xc[j + 1]));
+                        // (without room for all scores, each 16 columns' maxima are taken as they pass)
+                        if (!C::kKeep && i == 0 && !settled) reduce_columns<16, true>(xc, max_s + warp * NC + c, lane);
+                    }
+                    if (settled || (i > 0 && !meet_any(top > kTop || dead))) break;
+                    if (C::kKeep) {
+                        reduce_columns<NC, true>(x, max_s + warp * NC, lane);
+                    } else if (i > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < NC; c += 16) {
+                            scores(c, x);
+                            reduce_columns<16, true>(x, max_s + warp * NC + c, lane);
+                        }
+                    }
+                    if (i == 0 ? someone_dead() : meet_any(dead)) {
+                        leave = true;
+                        break;
+                    }
+                    pv_wait();  // O^T at rest
+#pragma unroll 1
+                    for (int n = lane; n < NC; n += 32) {
+                        const float m = fmaxf(fmaxf(max_s[n], max_s[NC + n]), fmaxf(max_s[2 * NC + n], max_s[3 * NC + n]));
+                        const bool on = i == 0 ? m > -INFINITY : m > kTop;
+                        fac[n] = on && i > 0 ? ex2(kBias - m) : 1.f;
+                        if (on) nbase[n] += kBias - m;
+                    }
+                    __syncwarp();
+                    if (i > 0) {
+#pragma unroll
+                        for (int n = 0; n < NC; ++n) l[n] *= fac[n];
+#pragma unroll 1
+                        for (int c = 0; c < NC; c += 16) {
+                            uint32_t h[16];
+                            tmem_ld16(quad + C::kTmemO + c, h);
+                            tmem_ld_wait();
+                            reg_fence(h);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) h[j] = __float_as_uint(__uint_as_float(h[j]) * fac[c + j]);
+                            tmem_st16(quad + C::kTmemO + c, h);
+                        }
+                        tmem_st_wait();
+                    }
+                    settled = true;
+                }
+                if (leave) break;
+                pv_wait();  // P is free
+
+                // weights: unit c / 16 of the token's row of P holds hi, unit (NC + c) / 16 lo.  hi is the weight
+                // rounded to 4 significant bits, t - (t - p) with t = p (2^20 + 1); lo the rest, exact in fp32
+#pragma unroll
+                for (int c = 0; c < NC; c += 16) {
+                    float *xc = x + (C::kKeep ? c : 0);
+                    if (!C::kKeep) scores(c, xc);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        float2 h2[2], l2[2];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int k = j + 2 * y;
+                            const float2 p = make_float2(ex2(xc[k]), ex2(xc[k + 1]));
+                            const float2 s = __fadd2_rn(make_float2(l[c + k], l[c + k + 1]), p);
+                            l[c + k] = s.x;
+                            l[c + k + 1] = s.y;
+                            const float2 tt = __fmul2_rn(p, make_float2(1048577.f, 1048577.f));
+                            const float2 minus = make_float2(-1.f, -1.f);
+                            h2[y] = __ffma2_rn(__ffma2_rn(p, minus, tt), minus, tt);
+                            l2[y] = __ffma2_rn(h2[y], minus, p);
+                        }
+                        hi[j / 4] = e4m3x2(h2[0].x, h2[0].y) | (e4m3x2(h2[1].x, h2[1].y) << 16);
+                        lo[j / 4] = e4m3x2(l2[0].x, l2[0].y) | (e4m3x2(l2[1].x, l2[1].y) << 16);
+                    }
+                    *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, c / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, (NC + c) / 16)) =
+                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                auto hand_over = [&]() {
+                    fence_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                };
+                bool apart = false;
+                if (edge) {
+                    dead |= !wait_mbar_warp(&full[vslot], v_turn & 1, abort);
+                    if (a.group > 1) {  // is a V code that only some rows see NaN?
+                        bool nan = false;
+                        if (t >= ctx_min && t < ctx_max) {
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) {
+                                const uint4 v = vrow[y];
+                                nan |= any_nan4(v.x) || any_nan4(v.y) || any_nan4(v.z) || any_nan4(v.w);
+                            }
+                        }
+                        apart = meet_any(nan || dead);
+                        if (apart && meet_any(dead)) {
+                            leave = true;
+                            break;
+                        }
+                    }
+                    if (t >= ctx_max) {  // no row sees it: whatever the slot or the stage holds
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) vrow[y] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                if (!apart) {
+                    hand_over();
+                    if (lane == 0) {
+                        mbar_arrive(&s_empty[sb]);
+                        mbar_arrive(p_full);
+                    }
+                    pv_open = true;
+                    continue;
+                }
+                // 0 x NaN must not reach the rows that do not see it.  One product per context of the group,
+                // longest first, with V's tokens past it zeroed; of each product only the columns of that
+                // context are added to O^T.
+                int levels = 0;
+                for (int prev = INT32_MAX;; ++levels) {
+                    int next = -1;
+                    for (int r = 0; r < a.group; ++r)
+                        if (item->ctx[r] < prev) next = max(next, item->ctx[r]);
+                    if (next < 0) break;
+                    prev = next;
+                }
+                if (self == 0) *levels_s = levels;
+                for (int v = 0, cur = INT32_MAX; v < levels; ++v) {
+                    int next = -1;
+                    for (int r = 0; r < a.group; ++r)
+                        if (item->ctx[r] < cur) next = max(next, item->ctx[r]);
+                    cur = next;
+                    if (t >= cur) {
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) vrow[y] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    hand_over();
+                    if (lane == 0) mbar_arrive(p_full);
+                    pv_open = true;
+                    pv_wait();
+#pragma unroll 1
+                    for (int c = 0; c < NC; c += 16) {
+                        uint32_t h[16], g[16];
+                        tmem_ld16(quad + sb * NC + c, h);
+                        tmem_ld16(quad + C::kTmemO + c, g);
+                        tmem_ld_wait();
+                        reg_fence(h);
+                        reg_fence(g);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (cs->ctx[c + j] == cur)
+                                g[j] = __float_as_uint(__uint_as_float(h[j]) + (i > 0 ? __uint_as_float(g[j]) : 0.f));
+                        tmem_st16(quad + C::kTmemO + c, g);
+                        tmem_st_wait();
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (self == 0) *levels_s = 0;
+                if (lane == 0) mbar_arrive(&s_empty[sb]);
+            }
+            if (leave) break;
+            pv_wait();
+
+            // ---- the item's sums and output
+            float *sums = sum_s + parity * kSoftmax * NC;
+            reduce_columns<NC, false>(l, sums + warp * NC, lane);
+            if (someone_dead()) break;
+            // a column's factor: 1 for a part of several, else 1 / its sum (0 without any weight)
+#pragma unroll 1
+            for (int n = lane; n < NC; n += 32) {
+                const float total = sums[n] + sums[NC + n] + sums[2 * NC + n] + sums[3 * NC + n];
+                fac[n] = tiles == 0 ? 0.f : parts > 1 ? 1.f : total == 0.f ? 0.f : a.v_scale / total;
+                if (warp == 0 && n < ncols) {
+                    const float b = -nbase[n];
+                    if (parts > 1)
+                        a.part_ml[static_cast<int64_t>(cs->at[n]) * a.parts_bound + part] = make_float2(b, total);
+                    else if (a.lse != nullptr)
+                        a.lse[cs->at[n]] = total == 0.f ? -INFINITY : (b + log2f(total)) * 0.6931471805599453f;
+                }
+            }
+            __syncwarp();
+            // 16 columns at a time go through P's place (free since the last product), each a row of 128 floats,
+            // so that the lanes write four dims in a row; a half of the place holds them
+            for (int c = 0; c < ncols; c += 16) {
+                float *out_s = reinterpret_cast<float *>(smem + C::OFF_P) + (c >> 4 & 1) * 16 * kDim;
+                uint32_t h[16];
+                tmem_ld16(quad + C::kTmemO + c, h);
+                tmem_ld_wait();
+                reg_fence(h);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) out_s[j * kDim + self] = __uint_as_float(h[j]);
+                if (someone_dead()) {
+                    leave = true;
+                    break;
+                }
+#pragma unroll 1
+                for (int n = warp; n < min(16, ncols - c); n += kSoftmax) {
+                    const float f = fac[c + n];
+                    float4 o = *reinterpret_cast<const float4 *>(out_s + n * kDim + 4 * lane);
+                    const int64_t at = cs->at[c + n];
+                    if (f == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);  // (without a tile it is no output)
+                    if (parts > 1)
+                        *reinterpret_cast<float4 *>(a.part_o + (at * a.parts_bound + part) * kDim + 4 * lane) = o;
+                    else
+                        *reinterpret_cast<uint2 *>(a.out + at * kDim + 4 * lane) =
+                            make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+                }
+            }
+            if (leave) break;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (tiles > 0) mbar_arrive(o_empty);
+                mbar_arrive(&q_empty[parity]);
+            }
+        }
+        if (dead) gave_up(abort, a.status);
+    }
+    __syncthreads();
+    if (warp == kScores) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+template <int NC>
+cudaError_t launch_columns(KvAttnArgs &a, int cols, cudaStream_t s) {
+    a.col_blocks = (cols + NC - 1) / NC;
+    const int64_t items = static_cast<int64_t>(a.num_rows / a.group) * a.kv_heads * a.col_blocks * a.parts_bound;
+    if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    a.items = static_cast<uint32_t>(items);
+    static std::atomic<uint64_t> configured{0};
+    cudaError_t e = raise_smem_limit(kv_attention_fp8_kernel<NC>, Cfg<NC>::kSmemBytes, configured);
+    if (e != cudaSuccess) return e;
+    // the register split waits forever in a CTA launched with fewer
+    static std::atomic<int> regs{0};
+    if (regs.load() == 0) {
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, kv_attention_fp8_kernel<NC>);
+        if (e != cudaSuccess) return e;
+        regs.store(fa.numRegs);
+    }
+    if (regs.load() < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    CUtensorMap map;
+    if (!encode_kv_rows_map(&map, a.pool, a.pool_rows, kDim, a.page_size)) return cudaErrorInvalidValue;
+    const uint32_t ctas = persistent_ctas(a);
+    if (ctas == 0) return cudaErrorInvalidDevice;
+    return launch_pdl(kv_attention_fp8_kernel<NC>, dim3(ctas), dim3(kThreads), Cfg<NC>::kSmemBytes, s, map, a);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_attention_fp8(KvAttnArgs &a, cudaStream_t s) {
+    const int cols = a.group * (a.num_heads / a.kv_heads);
+    if (cols <= 16) return launch_columns<16>(a, cols, s);
+    if (cols <= 32) return launch_columns<32>(a, cols, s);
+    return launch_columns<64>(a, cols, s);
+}
+
+}  // namespace dsa

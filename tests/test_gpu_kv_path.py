@@ -276,10 +276,11 @@ class Case:
                 # scores: `dim` fp32 sums of products up to big, and the exponent's argument
                 big = (q.abs() @ k.abs().T * self.sm).amax(-1, keepdim=True)
                 ds = (self.dim + 8) * 2.0 ** -24 * big
-                # weights: two bf16 terms (2^-16), or fp16 (2^-11, and 2^-25 of the largest below its
-                # normal range), exp2 (2^-22), sums over n tokens in fp32
-                w = (2.0 ** -11 if self.fmt == "fp8" else 2.0 ** -16) + 2.0 ** -22 + n * 2.0 ** -24
-                sub = n * 2.0 ** -25 * v.abs().amax() if self.fmt == "fp8" else 0
+                # weights: two bf16 terms (2^-16), two e4m3 terms (each rounds to 4 significant bits, half a
+                # step being 2^-4: 2^-8; and half of e4m3's smallest step, 2^-10, where the largest weight is at
+                # least 2^6 / 2), exp2 (2^-22), sums over n tokens in fp32
+                w = (2.0 ** -8 if self.fmt == "fp8" else 2.0 ** -16) + 2.0 ** -22 + n * 2.0 ** -24
+                sub = 2.0 ** -15 * p.amax(-1, keepdim=True) * v.abs().sum(0) if self.fmt == "fp8" else 0
                 bound = 2.0 ** -8 * ref.abs() + (1 + 2.0 ** -8) * ((w + 2 * ds) * mag + sub) + 1e-30
                 off = (out[r, at].double() - ref).abs()
                 assert (off <= bound).all(), (r, h, (off / bound).max().item())
@@ -360,21 +361,26 @@ def test_attention_row_does_not_depend_on_its_batch(fmt):
         assert torch.equal(one[0], out[r]) and torch.equal(l1[0], lse[r])
 
 
-@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
-@pytest.mark.parametrize("dim", [64, 128])
-def test_attention_values_past_a_rows_context_never_reach_it(value, dim):
+@pytest.mark.parametrize("fmt, value", [("bf16", math.nan), ("bf16", math.inf), ("bf16", -math.inf), ("fp8", math.nan)])
+@pytest.mark.parametrize("dim, hpg", [(64, 5), (128, 5), (128, 7), (128, 16)])
+@pytest.mark.parametrize("what", ["k", "v", "both"])
+def test_attention_values_past_a_rows_context_never_reach_it(fmt, value, dim, hpg, what):
     """A verify group whose newer tokens are not finite: the rows that do not see them are unharmed."""
-    clean = Case(19, "bf16", [200, 64], 2, 5, dim, 16, group=4)
+    ctx = [200, 64, 130]
+    clean = Case(19, fmt, ctx, 2, hpg, dim, 16, group=4)
     want = clean.run()
-    c = Case(19, "bf16", [200, 64], 2, 5, dim, 16, group=4)
-    for req, n in ((0, 200), (1, 64)):
+    c = Case(19, fmt, ctx, 2, hpg, dim, 16, group=4)
+    side = {"k": slice(0, 1), "v": slice(1, 2), "both": slice(0, 2)}[what]
+    for req, n in enumerate(ctx):
         for t in (n - 2, n - 1):  # seen by the last two rows, and by the last alone
-            c.pool[c.table[req, t // 16].item(), :, :, t % 16] = value
+            c.pool[c.table[req, t // 16].item(), :, side, t % 16] = value
     got = c.run()
-    for r in (0, 1, 4, 5):
+    for r in (0, 1, 4, 5, 8, 9):
         assert torch.equal(got[0][r], want[0][r]) and torch.equal(got[1][r], want[1][r])
     if value != value:
-        assert got[0][2:4].isnan().all() and got[0][6:8].isnan().all()
+        for r in (2, 3, 6, 7, 10, 11):
+            assert got[0][r].isnan().all()
+            assert got[1][r].isnan().all() or (what == "v" and torch.equal(got[1][r], want[1][r]))
 
 
 def test_attention_scores_of_minus_infinity_weigh_nothing():
