@@ -350,7 +350,7 @@ cudaError_t launch_kv_attention_fp8(KvAttnArgs &a, cudaStream_t s);
 // span of 64 or 128 bytes (api.cu).
 bool encode_kv_rows_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t row_bytes, uint32_t box_rows);
 size_t kv_attention_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
-                                    int32_t max_ctx);
+                                    int32_t max_ctx, bool fp8);
 
 int device_sm_count();
 

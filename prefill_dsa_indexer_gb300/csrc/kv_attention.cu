@@ -78,7 +78,8 @@ struct KvCfg {
     static constexpr int OFF_COLS = OFF_Q + kColWarps * kQBytes;         // [16 kColWarps] scale and context
     static constexpr int OFF_ML = OFF_COLS + 16 * kColWarps * 8;         // [item parity][consumer][16] base and sum
     static constexpr int OFF_ITEM = OFF_ML + 2 * kConsumers * 16 * 8;
-    static constexpr int OFF_BARS = OFF_ITEM + 64;
+    static constexpr int OFF_SCHED = OFF_ITEM + 64;
+    static constexpr int OFF_BARS = OFF_SCHED + static_cast<int>(sizeof(KvSchedule));
     static constexpr int kNumBars = 2 * kStages + 3;
     static constexpr int OFF_MISC = OFF_BARS + kNumBars * 8;
     static constexpr int kSmemBytes = OFF_MISC + 16 + 1024;              // + slack for 1024-byte alignment
@@ -185,6 +186,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
+    KvSchedule *sched = reinterpret_cast<KvSchedule *>(smem + C::OFF_SCHED);
+    kv_fill_schedule(a, sched);
+    __syncthreads();
 
     const int hpg = a.num_heads / a.kv_heads, cols = a.group * hpg;
     const int gi = lane >> 2, ji = lane & 3;
@@ -199,9 +203,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         int s = 0, issued = 0;
         uint32_t phase = 1;
         bool go = true;
-        for (uint32_t it = blockIdx.x; it < a.items && go; it += gridDim.x) {
-            KvWhere w;
-            if (!kv_where<kCols>(a, it, lane, w)) continue;
+        KvCursor w;
+        for (bool more = w.first<kCols>(a, sched, lane); more && go; more = w.next<kCols>(a, lane)) {
             const int num_pages = (w.t_end + a.page_size - 1) >> a.page_shift;
             const int32_t *table = a.block_table + static_cast<int64_t>(w.req) * a.bt_stride;
             auto load_ids = [&](int p) { return p + lane < num_pages ? table[p + lane] : 0; };
@@ -265,9 +268,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == kQuery) {
         // ---- items, and their queries in 16 bits, columns as rows
         uint32_t phase = 1;
-        for (uint32_t it = blockIdx.x; it < a.items; it += gridDim.x) {
-            KvWhere w;
-            if (!kv_where<kCols>(a, it, lane, w)) continue;
+        KvCursor w;
+        for (bool more = w.first<kCols>(a, sched, lane); more; more = w.next<kCols>(a, lane)) {
             if (w.bad && w.part == 0 && lane == 0) report(a.status, DSA_ERR_BOUNDS);
             // 16 dims (a unit) of a column per lane and turn: a column's units are in neighbouring lanes.  The
             // first 16 columns are loaded while the consumers still have the item before
@@ -792,8 +794,8 @@ cudaError_t launch_format(KvAttnArgs &a, cudaStream_t s) {
 }  // namespace
 
 size_t kv_attention_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
-                                    int32_t max_ctx) {
-    const size_t parts = static_cast<size_t>(kv_parts_bound(max_ctx, kv_parts_shift(kv_heads)));
+                                    int32_t max_ctx, bool fp8) {
+    const size_t parts = static_cast<size_t>(kv_parts_bound(max_ctx, kv_parts_shift(kv_heads, fp8 && head_dim == 128)));
     if (parts <= 1) return 0;
     const size_t n = static_cast<size_t>(num_rows) * static_cast<size_t>(num_heads) * parts;
     return align256(n * static_cast<size_t>(head_dim) * 4) + align256(n * 8);
@@ -804,7 +806,7 @@ cudaError_t launch_kv_attention(KvAttnArgs &a, void *workspace, cudaStream_t s) 
     for (a.page_shift = 4; 1 << a.page_shift < a.page_size;) ++a.page_shift;
     const uint32_t hpg = static_cast<uint32_t>(a.num_heads / a.kv_heads);
     a.hpg_mul = ((1u << 20) + hpg - 1) / hpg;
-    a.parts_shift = kv_parts_shift(a.kv_heads);
+    a.parts_shift = kv_parts_shift(a.kv_heads, a.fp8 && a.head_dim == 128);
     a.parts_bound = kv_parts_bound(a.max_ctx, a.parts_shift);
     const size_t n = static_cast<size_t>(a.num_rows) * static_cast<size_t>(a.num_heads) * a.parts_bound;
     a.part_o = static_cast<float *>(workspace);

@@ -1,5 +1,5 @@
 // kv_attention_common.cuh -- what the two paged-attention kernels (kv_attention.cu, kv_attention_fp8.cu) share:
-// the split of a context into parts, the launch's items and their decoding.
+// the split of a context into parts, the launch's items and their distribution.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -12,10 +12,13 @@
 namespace dsa {
 namespace kv {
 
-// Parts of a context: of 128 tokens, doubled until at most 2^parts_shift cover it.  parts_shift: 128 parts
-// over all KV heads, so that one request alone gives most of the 152 SMs a CTA, but at least 16.
-__host__ __device__ __forceinline__ int32_t kv_parts_shift(int32_t kv_heads) {
-    return kv_heads >= 8 ? 4 : kv_heads >= 4 ? 5 : kv_heads >= 2 ? 6 : 7;
+// Parts of a context: of 128 tokens, doubled until at most 2^parts_shift cover it.  All KV heads of one request
+// make 256 parts in the warp-level kernel, so that it alone fills the 152 SMs, and 128 in the FP8 kernel of
+// head_dim 128, whose parts cost more beside their tiles (32 x 16K-64K: 229 us with 128, 280 us with 256; for
+// the other kernel 8 x 128K bf16 took 331 and 318 us); but at least 32 and 16 of a head.
+__host__ __device__ __forceinline__ int32_t kv_parts_shift(int32_t kv_heads, bool fp8_kernel) {
+    const int32_t most = fp8_kernel ? 7 : 8;
+    return kv_heads >= 8 ? most - 3 : kv_heads >= 4 ? most - 2 : kv_heads >= 2 ? most - 1 : most;
 }
 
 // log2 of a part's tokens: the smallest k >= 7 with 2^(k + parts_shift) >= ctx.
@@ -37,40 +40,179 @@ struct KvItem {
 };
 static_assert(sizeof(KvItem) == 64, "item layout");
 
-// Item `i` of the launch: part fastest, then column block, KV head, row group.  Warp-collective; false:
-// the group's context has fewer parts.
-struct KvWhere {
-    int part, parts, col0, g, row0, req, t_begin, t_end, ctx, ctx_min, my_ctx;
-    bool bad;
+// ---- which items a CTA takes
+//
+// An item costs its tiles of 128 tokens and kItemCost more (its queries, its base, its output).  Counting items
+// in the order (row group, KV head, column block, part), CTA b of n takes those that start within its n-th of the
+// total cost: equal shares whatever the contexts (32 rows of 16K to 64K tokens: the busiest CTA has 1.04 times
+// the mean; with items dealt in turn it had 1.28 to 1.44 times).  A share is one run of neighbours.
+constexpr uint32_t kItemCost = 2;
+constexpr int kSchedEntries = 512;  // running costs kept in shared memory, one for every so many groups
+
+struct KvSchedule {
+    uint64_t before[kSchedEntries + 1];  // cost of all groups before the entry's
 };
 
-template <int kCols>
-__device__ __forceinline__ bool kv_where(const KvAttnArgs &a, uint32_t i, int lane, KvWhere &w) {
-    uint32_t j = i / a.parts_bound;
-    w.part = static_cast<int>(i - j * a.parts_bound);
-    w.col0 = 0;
-    if (a.col_blocks > 1) {
-        const uint32_t k = j / a.col_blocks;
-        w.col0 = static_cast<int>(j - k * a.col_blocks) * kCols;
-        j = k;
-    }
-    const uint32_t k = j / a.kv_heads;
-    w.g = static_cast<int>(j - k * a.kv_heads);
-    w.row0 = static_cast<int>(k) * a.group;
-    const int row = w.row0 + (lane < a.group ? lane : 0);
-    const int n = a.row_ctx[row], req = a.row_req[row];
-    w.req = __shfl_sync(0xffffffffu, req, 0);
-    w.bad = __any_sync(0xffffffffu, n < 0 || n > a.max_ctx || req != w.req) || w.req < 0 || w.req >= a.num_requests;
-    w.my_ctx = w.bad ? 0 : n;  // of row `lane` of the group
-    w.ctx = __reduce_max_sync(0xffffffffu, w.my_ctx);
-    w.ctx_min = __reduce_min_sync(0xffffffffu, w.my_ctx);
-    const int shift = kv_part_shift(w.ctx, a.parts_shift);
-    w.parts = kv_parts(w.ctx, shift);
-    if (w.part >= w.parts) return false;
-    w.t_begin = w.part << shift;
-    w.t_end = w.t_begin + min(w.ctx - w.t_begin, 1 << shift);
-    return true;
+// Cost of a group with this longest context, for one KV head and column block.
+__device__ __forceinline__ uint32_t kv_cost(int32_t ctx, int32_t parts_shift) {
+    return kv_parts(ctx, kv_part_shift(ctx, parts_shift)) * kItemCost + ((ctx + 127) >> 7);
 }
+
+__device__ __forceinline__ bool kv_direct(const KvAttnArgs &a) { return a.items <= gridDim.x; }  // an item a CTA
+
+// Fills `sched`; every thread of the CTA calls it, then __syncthreads.
+__device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule *sched) {
+    if (kv_direct(a)) return;
+    const int groups = a.num_rows / a.group;
+    const int per = (groups + kSchedEntries - 1) / kSchedEntries, entries = (groups + per - 1) / per;
+    for (int e = threadIdx.x; e < entries; e += blockDim.x) {
+        uint64_t sum = 0;
+#pragma unroll 1
+        for (int gi = e * per; gi < min(groups, (e + 1) * per); ++gi) {
+            const int row0 = gi * a.group, req = a.row_req[row0];
+            bool bad = req < 0 || req >= a.num_requests;
+            int ctx = 0;
+#pragma unroll 1
+            for (int r = row0; r < row0 + a.group; ++r) {
+                const int n = a.row_ctx[r];
+                bad |= n < 0 || n > a.max_ctx || a.row_req[r] != req;
+                ctx = max(ctx, n);
+            }
+            sum += kv_cost(bad ? 0 : ctx, a.parts_shift);
+        }
+        sched->before[e + 1] = sum * (static_cast<uint64_t>(a.kv_heads) * a.col_blocks);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        uint64_t carry = 0;
+        if (lane == 0) sched->before[0] = 0;
+#pragma unroll 1
+        for (int e0 = 1; e0 <= entries; e0 += 32) {
+            uint64_t v = e0 + lane <= entries ? sched->before[e0 + lane] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint64_t u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            v += carry;
+            if (e0 + lane <= entries) sched->before[e0 + lane] = v;
+            carry = __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+}
+
+// An item, and the way to the next one of this CTA.  Warp-collective.
+struct KvCursor {
+    int part, parts, col0, g, row0, req, t_begin, t_end, ctx, ctx_min;
+    int my_ctx;  // of row `lane` of the group
+    bool bad;
+    int group, head, shift;  // head: KV head and column block
+    uint64_t start, end;     // cost before the item, and where this CTA's share ends
+
+    __device__ __forceinline__ void load_group(const KvAttnArgs &a, int lane) {
+        row0 = group * a.group;
+        const int row = row0 + (lane < a.group ? lane : 0);
+        const int n = a.row_ctx[row], r = a.row_req[row];
+        req = __shfl_sync(0xffffffffu, r, 0);
+        bad = __any_sync(0xffffffffu, n < 0 || n > a.max_ctx || r != req) || req < 0 || req >= a.num_requests;
+        my_ctx = bad ? 0 : n;
+        ctx = __reduce_max_sync(0xffffffffu, my_ctx);
+        ctx_min = __reduce_min_sync(0xffffffffu, my_ctx);
+        shift = kv_part_shift(ctx, a.parts_shift);
+        parts = kv_parts(ctx, shift);
+    }
+
+    template <int kCols>
+    __device__ __forceinline__ void place(const KvAttnArgs &a) {
+        g = head;
+        col0 = 0;
+        if (a.col_blocks > 1) {
+            g = static_cast<int>(static_cast<uint32_t>(head) / a.col_blocks);
+            col0 = static_cast<int>(head - g * a.col_blocks) * kCols;
+        }
+        t_begin = part << shift;
+        t_end = t_begin + min(ctx - t_begin, 1 << shift);
+    }
+
+    // The CTA's first item; false: it has none.
+    template <int kCols>
+    __device__ __forceinline__ bool first(const KvAttnArgs &a, const KvSchedule *sched, int lane) {
+        const int heads = a.kv_heads * static_cast<int>(a.col_blocks), groups = a.num_rows / a.group;
+        if (kv_direct(a)) {
+            const uint32_t j = blockIdx.x / a.parts_bound;
+            part = static_cast<int>(blockIdx.x - j * a.parts_bound);
+            group = static_cast<int>(j / heads);
+            head = static_cast<int>(j - group * heads);
+            start = end = 0;
+            load_group(a, lane);
+            place<kCols>(a);
+            return part < parts;
+        }
+        const int per = (groups + kSchedEntries - 1) / kSchedEntries, entries = (groups + per - 1) / per;
+        const uint64_t total = sched->before[entries];
+        const uint64_t from = total * blockIdx.x / gridDim.x;
+        end = total * (blockIdx.x + 1) / gridDim.x;
+        int lo = 0, hi = entries - 1;  // the last entry with nothing of the share before it
+#pragma unroll 1
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (sched->before[mid] <= from) lo = mid;
+            else hi = mid - 1;
+        }
+        start = sched->before[lo];
+        group = lo * per;
+        uint32_t unit;  // cost of a KV head and column block
+#pragma unroll 1
+        for (;; ++group) {
+            load_group(a, lane);
+            unit = kv_cost(ctx, a.parts_shift);
+            const uint64_t all = static_cast<uint64_t>(unit) * heads;
+            if (start + all > from) break;
+            start += all;
+        }
+        // the first item that starts at or past `from`
+        uint64_t left = from - start;
+        head = 0;
+        if (left >= unit) {
+            head = static_cast<int>(left / unit);
+            left -= static_cast<uint64_t>(head) * unit;
+        }
+        start = from - left;
+        const uint32_t step = kItemCost + (1u << (shift - 7));  // of every part but the last
+        part = static_cast<int>((static_cast<uint32_t>(left) + step - 1) / step);
+        start += static_cast<uint64_t>(part) * step;
+        if (part >= parts) {
+            start = from - left + unit;
+            part = parts - 1;
+            return skip<kCols>(a, lane);
+        }
+        place<kCols>(a);
+        return start < end;
+    }
+
+    // Step to the item after (group, head, part), which starts at `start`.
+    template <int kCols>
+    __device__ __forceinline__ bool skip(const KvAttnArgs &a, int lane) {
+        if (start >= end) return false;
+        if (++part >= parts) {
+            part = 0;
+            if (++head >= a.kv_heads * static_cast<int>(a.col_blocks)) {
+                head = 0;
+                ++group;
+                load_group(a, lane);
+            }
+        }
+        place<kCols>(a);
+        return true;
+    }
+
+    template <int kCols>
+    __device__ __forceinline__ bool next(const KvAttnArgs &a, int lane) {
+        start += kItemCost + static_cast<uint32_t>((t_end - t_begin + 127) >> 7);
+        return skip<kCols>(a, lane);
+    }
+};
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

@@ -74,22 +74,26 @@ struct Cfg {
     // it in its slot (a barrier's parity alone cannot tell a phase from the one two before it)
     static constexpr int kK = 2, kV = NC == 16 ? 3 : 2, kUnits = kK + kV;
     static constexpr int kQBytes = 2 * NC * kDim, kQBufs = NC == 64 ? 1 : 2;
-    static constexpr uint32_t kTmemO = 2 * NC;             // two score buffers, then the output
-    static constexpr uint32_t kTmemCols = NC == 16 ? 64 : NC == 32 ? 128 : 256;  // two CTAs share the SM's 512
+    // hi and lo terms lie side by side in an MMA's N where TMEM has room: the scores for NC <= 32, the output always
+    static constexpr int kSN = NC == 64 ? NC : 2 * NC, kON = 2 * NC;
+    static constexpr int kPBufs = NC == 64 ? 1 : 2;        // a token's 128-byte row of P holds two tiles' weights
+    static constexpr uint32_t kTmemO = 2 * kSN;            // two score buffers, then the output
+    static constexpr uint32_t kTmemCols = NC == 16 ? 128 : 256;  // two CTAs share the SM's 512
     static constexpr bool kKeep = NC <= 32;                // a thread keeps its scores in registers
     static constexpr int OFF_Q = kUnits * kUnitBytes;      // [kQBufs]: rows hi 0 .. NC - 1, lo NC .. 2 NC - 1
-    static constexpr int OFF_P = OFF_Q + kQBufs * kQBytes;      // a token's row: NC hi, NC lo bytes; then the output's way out
+    static constexpr int OFF_P = OFF_Q + kQBufs * kQBytes;      // [kPBufs] a token's row: NC hi, NC lo bytes; then the output's way out
     static constexpr int OFF_COLS = OFF_P + kTile * 128;   // [2] by item parity
     static constexpr int OFF_ITEM = OFF_COLS + 2 * static_cast<int>(sizeof(Columns<NC>));
     static constexpr int OFF_MAX = OFF_ITEM + 2 * 64;      // [4][NC] a warp's largest score
     static constexpr int OFF_BASE = OFF_MAX + 4 * NC * 4;  // [4][NC] minus the bases, a copy per warp
     static constexpr int OFF_FAC = OFF_BASE + 4 * NC * 4;  // [4][NC] rescale factors
     static constexpr int OFF_SUM = OFF_FAC + 4 * NC * 4;   // [2][4][NC] a warp's weights, by item parity
-    static constexpr int OFF_BARS = OFF_SUM + 2 * 4 * NC * 4;
-    static constexpr int kNumBars = 2 * kUnits + 2 * 2 + 2 * 2 + kQBufs + 4;
+    static constexpr int OFF_SCHED = OFF_SUM + 2 * 4 * NC * 4;
+    static constexpr int OFF_BARS = OFF_SCHED + static_cast<int>(sizeof(KvSchedule));
+    static constexpr int kNumBars = 2 * kUnits + 2 * 2 + 2 * 2 + kQBufs + 2 * kPBufs + 2;
     static constexpr int OFF_MISC = OFF_BARS + kNumBars * 8;
     static constexpr int kSmemBytes = OFF_MISC + 16 + 1024;
-    static_assert(kTmemO + NC <= kTmemCols, "TMEM plan");
+    static_assert(kTmemO + kON <= kTmemCols, "TMEM plan");
     static_assert(kSmemBytes <= 115712, "two CTAs per SM");
 };
 
@@ -137,6 +141,17 @@ __device__ __forceinline__ void reduce_columns(const float *v, float *dst, int l
     }
 }
 
+// h += g, fp32.
+__device__ __forceinline__ void add16(uint32_t (&h)[16], const uint32_t (&g)[16]) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+        const float2 s = __fadd2_rn(make_float2(__uint_as_float(h[j]), __uint_as_float(h[j + 1])),
+                                    make_float2(__uint_as_float(g[j]), __uint_as_float(g[j + 1])));
+        h[j] = __float_as_uint(s.x);
+        h[j + 1] = __float_as_uint(s.y);
+    }
+}
+
 // OR of a predicate over the four softmax warps, who all meet here.
 __device__ __forceinline__ bool meet_any(bool p) {
     uint32_t r;
@@ -167,9 +182,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint64_t *s_empty = s_full + 2;                             // [2] softmax has read them
     uint64_t *q_full = s_empty + 2, *q_empty = q_full + 2;      // [2] an item and its columns, by item parity
     uint64_t *img_empty = q_empty + 2;                                  // [kQBufs] the MMAs are done with the queries
-    uint64_t *p_full = img_empty + C::kQBufs;                                     // weights written (and O^T rescaled)
-    uint64_t *pv_done = p_full + 1;                                     // O^T += V^T P^T done
-    uint64_t *o_empty = pv_done + 1;                                    // the item's output is read
+    uint64_t *p_full = img_empty + C::kQBufs;                           // [kPBufs] weights written (and O^T rescaled)
+    uint64_t *pv_done = p_full + C::kPBufs;                             // [kPBufs] O^T += V^T P^T done
+    uint64_t *o_empty = pv_done + C::kPBufs;                            // the item's output is read
     uint64_t *drained = o_empty + 1;                                    // after a wait gave up: no MMA is left
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
@@ -192,8 +207,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             mbar_init(&q_empty[s], kSoftmax + 2);
         }
         for (int s = 0; s < C::kQBufs; ++s) mbar_init(&img_empty[s], 1);
-        mbar_init(p_full, kSoftmax);
-        mbar_init(pv_done, 1);
+        for (int s = 0; s < C::kPBufs; ++s) {
+            mbar_init(&p_full[s], kSoftmax);
+            mbar_init(&pv_done[s], 1);
+        }
         mbar_init(o_empty, kSoftmax);
         mbar_init(drained, 2);
         fence_mbar_init();
@@ -209,6 +226,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
     pdl_launch_dependents();
+    KvSchedule *sched = reinterpret_cast<KvSchedule *>(smem + C::OFF_SCHED);
+    kv_fill_schedule(a, sched);
+    __syncthreads();
 
     const int hpg = a.num_heads / a.kv_heads, cols = a.group * hpg;
 
@@ -221,9 +241,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint64_t policy = l2_evict_first_policy();
             uint32_t issued = 0;  // tiles
             bool go = true;
-            for (uint32_t it = blockIdx.x; it < a.items && go; it += gridDim.x) {
-                KvWhere w;
-                if (!kv_where<NC>(a, it, lane, w)) continue;
+            KvCursor w;
+            for (bool more = w.first<NC>(a, sched, lane); more && go; more = w.next<NC>(a, lane)) {
                 const int num_pages = (w.t_end + a.page_size - 1) >> a.page_shift;
                 const int32_t *table = a.block_table + static_cast<int64_t>(w.req) * a.bt_stride;
                 auto load_ids = [&](int p) { return p + lane < num_pages ? table[p + lane] : 0; };
@@ -276,9 +295,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             // ---- items, their columns and query images (rows hi 0 .. NC - 1, lo NC .. 2 NC - 1 of 128 bytes)
             uint32_t count = 0;  // items handed on
             bool go = true;
-            for (uint32_t it = blockIdx.x; it < a.items && go; it += gridDim.x) {
-                KvWhere w;
-                if (!kv_where<NC>(a, it, lane, w)) continue;
+            KvCursor w;
+            for (bool more = w.first<NC>(a, sched, lane); more && go; more = w.next<NC>(a, lane)) {
                 if (w.bad && w.part == 0 && lane == 0) report(a.status, DSA_ERR_BOUNDS);
                 // 16 dims (a unit) of a column per lane and turn, four columns a turn.  The first 16 columns are
                 // loaded while the item before is still worked on; then they take their places in the image as
@@ -387,12 +405,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             // ---- the two MMA issuers, one thread each: an MMA's issue lasts as long as its passage through the
             // tensor core, so one thread for both products would set the pace
             const bool values = warp == kValues;
-            const uint32_t idesc = values ? make_idesc(kDim, NC, 0, 0, true, true) : make_idesc(kTile, NC, 0, 0, false, false);
+            const uint32_t idesc = values ? make_idesc(kDim, C::kON, 0, 0, true, true)
+                                           : make_idesc(kTile, C::kSN, 0, 0, false, false);
             const uint32_t ring = values ? C::kV : C::kK, slot0 = values ? C::kK : 0;
             const uint32_t ua = smem_u32(smem);
             const uint64_t b0 = sdesc_sw128(smem_u32(smem + (values ? C::OFF_P : C::OFF_Q)), 16, 1024);
-            const uint32_t step = values ? 256 : 2, lo = values ? NC / 16 : NC * kDim / 16;
-            uint32_t count = 0, p_phase = 0, o_phase = 1;  // count: tiles
+            const uint32_t step = values ? 256 : 2;
+            uint32_t count = 0, p_phases = 0, o_phase = 1;  // count: tiles
             bool ok = true;
             for (uint32_t n = 0; ok; ++n) {
                 ok = wait_mbar(&q_full[n & 1], n >> 1 & 1, abort);
@@ -408,31 +427,36 @@ __global__ void __launch_bounds__(kThreads, 2)
                     o_phase ^= 1;
                 }
                 for (int i = 0; ok && i < tiles; ++i, ++count) {
-                    const uint32_t turn = count / ring, slot = slot0 + count - turn * ring, sb = count & 1;
+                    const uint32_t turn = count / ring, slot = slot0 + count - turn * ring, sb = count & 1, pb = count % C::kPBufs;
                     ok = wait_mbar(&full[slot], turn & 1, abort);
                     // values: levels 0 accumulates in O^T.  Else one product for each context of the group, into the
                     // scores' buffer, from where the softmax warps add its columns
                     int levels = 0;
                     bool apart = false;
                     while (ok) {
-                        ok = values ? wait_mbar(p_full, p_phase, abort)
+                        ok = values ? wait_mbar(&p_full[pb], p_phases >> pb & 1, abort)
                                     : wait_mbar(&s_empty[sb], ((count >> 1) & 1) ^ 1, abort);
-                        p_phase ^= 1;
+                        p_phases ^= 1u << pb;
                         if (!ok) break;
                         tc_fence_after();
                         if (values && !apart) {
                             levels = *levels_s;
                             apart = levels > 0;
                         }
-                        const uint32_t d = values && !apart ? tmem + C::kTmemO : tmem + sb * NC;
+                        const uint32_t d = values && !apart ? tmem + C::kTmemO : tmem + sb * C::kSN;
                         const uint32_t add = values && !apart && i > 0 ? 1u : 0u;
                         const uint64_t ad = sdesc_sw128(ua + slot * kUnitBytes, 16, 1024);
+                        // hi and lo terms side by side in N, or hi, then lo ones into the same columns
+                        const bool in_turn = apart || (!values && C::kSN == NC);
+                        const uint32_t lo = values ? NC / 16 : NC * kDim / 16;
 #pragma unroll 2
-                        for (int k = 0; k < 8; ++k)
-                            mma_f8(d, ad + (k & 3) * step, bd + (k >> 2) * lo + (k & 3) * step, idesc, k > 0 ? 1u : add);
+                        for (uint32_t k = 0; k < (in_turn ? 8u : 4u); ++k)
+                            mma_f8(d, ad + (k & 3) * step,
+                                   bd + (values ? pb * (2 * NC / 16) : 0u) + (k >> 2) * lo + (k & 3) * step,
+                                   apart ? make_idesc(kDim, NC, 0, 0, true, true) : idesc, k > 0 ? 1u : add);
                         --levels;
                         if (levels <= 0) mma_commit(&empty[slot]);
-                        mma_commit(values ? pv_done : &s_full[sb]);
+                        mma_commit(values ? &pv_done[pb] : &s_full[sb]);
                         if (levels <= 0) break;
                     }
                     if (!values && ok && i == tiles - 1) mma_commit(&img_empty[n % C::kQBufs]);
@@ -457,14 +481,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         float *max_s = reinterpret_cast<float *>(smem + C::OFF_MAX);
         float *nbase = reinterpret_cast<float *>(smem + C::OFF_BASE) + warp * NC;
         float *fac = reinterpret_cast<float *>(smem + C::OFF_FAC) + warp * NC;
-        uint32_t s_count = 0, pv_phase = 0;  // s_count: tiles
-        bool dead = false, pv_open = false;  // pv_open: a product of P is out whose end has not been seen
-        auto pv_wait = [&]() {
-            if (!pv_open) return;
-            dead |= !wait_mbar_warp(pv_done, pv_phase, abort);
-            pv_phase ^= 1;
-            pv_open = false;
+        uint32_t s_count = 0;                   // tiles
+        uint32_t pv_open = 0, pv_phases = 0;    // a bit per buffer of P: a product is out whose end has not been seen
+        bool dead = false;
+        auto pv_wait = [&](uint32_t b) {
+            if (!(pv_open >> b & 1)) return;
+            dead |= !wait_mbar_warp(&pv_done[b], pv_phases >> b & 1, abort);
+            pv_phases ^= 1u << b;
+            pv_open &= ~(1u << b);
             tc_fence_after();
+        };
+        auto pv_wait_all = [&]() {
+#pragma unroll
+            for (uint32_t b = 0; b < C::kPBufs; ++b) pv_wait(b);
         };
         auto someone_dead = [&]() { return meet_any(dead) && meet_any(dead); };
         for (uint32_t item_n = 0;; ++item_n) {
@@ -488,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             bool leave = false;
             for (int i = 0; i < tiles; ++i, ++s_count) {
                 const int t0 = t_begin + i * kTile, t = t0 + self;
-                const uint32_t sb = s_count & 1;
+                const uint32_t sb = s_count & 1, pb = s_count % C::kPBufs;
                 const uint32_t v_turn = s_count / C::kV, vslot = C::kK + s_count - v_turn * C::kV;
                 uint4 *vrow = reinterpret_cast<uint4 *>(smem + vslot * kUnitBytes + self * kDim);
                 dead |= !wait_mbar_warp(&s_full[sb], (s_count >> 1) & 1, abort);
@@ -498,9 +527,18 @@ __global__ void __launch_bounds__(kThreads, 2)
                 // scores of this token, columns c .. c + 15, in log2 units against their bases
                 auto scores = [&](int c, float *x) {
                     uint32_t h[16];
-                    tmem_ld16(quad + sb * NC + c, h);
-                    tmem_ld_wait();
-                    reg_fence(h);
+                    tmem_ld16(quad + sb * C::kSN + c, h);
+                    if constexpr (C::kSN > NC) {
+                        uint32_t g[16];
+                        tmem_ld16(quad + sb * C::kSN + NC + c, g);
+                        tmem_ld_wait();
+                        reg_fence(h);
+                        reg_fence(g);
+                        add16(h, g);
+                    } else {
+                        tmem_ld_wait();
+                        reg_fence(h);
+                    }
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
                         const float4 sc = *reinterpret_cast<const float4 *>(cs->scale + c + j);
@@ -553,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         leave = true;
                         break;
                     }
-                    pv_wait();  // O^T at rest
+                    pv_wait_all();  // O^T at rest
 #pragma unroll 1
                     for (int n = lane; n < NC; n += 32) {
                         const float m = fmaxf(fmaxf(max_s[n], max_s[NC + n]), fmaxf(max_s[2 * NC + n], max_s[3 * NC + n]));
@@ -566,13 +604,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int n = 0; n < NC; ++n) l[n] *= fac[n];
 #pragma unroll 1
-                        for (int c = 0; c < NC; c += 16) {
+                        for (int c = 0; c < C::kON; c += 16) {
                             uint32_t h[16];
                             tmem_ld16(quad + C::kTmemO + c, h);
                             tmem_ld_wait();
                             reg_fence(h);
+                            const float *f = fac + (c < NC ? c : c - NC);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) h[j] = __float_as_uint(__uint_as_float(h[j]) * fac[c + j]);
+                            for (int j = 0; j < 16; ++j) h[j] = __float_as_uint(__uint_as_float(h[j]) * f[j]);
                             tmem_st16(quad + C::kTmemO + c, h);
                         }
                         tmem_st_wait();
@@ -580,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     settled = true;
                 }
                 if (leave) break;
-                pv_wait();  // P is free
+                pv_wait(pb);  // this buffer of P is free
 
                 // weights: unit c / 16 of the token's row of P holds hi, unit (NC + c) / 16 lo.  hi is the weight
                 // rounded to 4 significant bits, t - (t - p) with t = p (2^20 + 1); lo the rest, exact in fp32
@@ -607,8 +646,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                         hi[j / 4] = e4m3x2(h2[0].x, h2[0].y) | (e4m3x2(h2[1].x, h2[1].y) << 16);
                         lo[j / 4] = e4m3x2(l2[0].x, l2[0].y) | (e4m3x2(l2[1].x, l2[1].y) << 16);
                     }
-                    *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, c / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, (NC + c) / 16)) =
+                    *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, (2 * NC * pb + c) / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, (2 * NC * pb + NC + c) / 16)) =
                         make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 auto hand_over = [&]() {
@@ -643,9 +682,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                     hand_over();
                     if (lane == 0) {
                         mbar_arrive(&s_empty[sb]);
-                        mbar_arrive(p_full);
+                        mbar_arrive(&p_full[pb]);
                     }
-                    pv_open = true;
+                    pv_open |= 1u << pb;
                     continue;
                 }
                 // 0 x NaN must not reach the rows that do not see it.  One product per context of the group,
@@ -670,13 +709,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                         for (int y = 0; y < 8; ++y) vrow[y] = make_uint4(0u, 0u, 0u, 0u);
                     }
                     hand_over();
-                    if (lane == 0) mbar_arrive(p_full);
-                    pv_open = true;
-                    pv_wait();
+                    if (lane == 0) mbar_arrive(&p_full[pb]);
+                    pv_open |= 1u << pb;
+                    pv_wait(pb);
 #pragma unroll 1
                     for (int c = 0; c < NC; c += 16) {
                         uint32_t h[16], g[16];
-                        tmem_ld16(quad + sb * NC + c, h);
+                        tmem_ld16(quad + sb * C::kSN + c, h);
+                        // the hi half of O^T takes the sum; in the item's first tile the lo half becomes zero
                         tmem_ld16(quad + C::kTmemO + c, g);
                         tmem_ld_wait();
                         reg_fence(h);
@@ -686,6 +726,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                             if (cs->ctx[c + j] == cur)
                                 g[j] = __float_as_uint(__uint_as_float(h[j]) + (i > 0 ? __uint_as_float(g[j]) : 0.f));
                         tmem_st16(quad + C::kTmemO + c, g);
+                        if (i == 0) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) g[j] = 0u;
+                            tmem_st16(quad + C::kTmemO + NC + c, g);
+                        }
                         tmem_st_wait();
                     }
                 }
@@ -695,7 +740,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (lane == 0) mbar_arrive(&s_empty[sb]);
             }
             if (leave) break;
-            pv_wait();
 
             // ---- the item's sums and output
             float *sums = sum_s + parity * kSoftmax * NC;
@@ -715,14 +759,18 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
             __syncwarp();
+            pv_wait_all();
             // 16 columns at a time go through P's place (free since the last product), each a row of 128 floats,
             // so that the lanes write four dims in a row; a half of the place holds them
             for (int c = 0; c < ncols; c += 16) {
                 float *out_s = reinterpret_cast<float *>(smem + C::OFF_P) + (c >> 4 & 1) * 16 * kDim;
-                uint32_t h[16];
+                uint32_t h[16], g[16];
                 tmem_ld16(quad + C::kTmemO + c, h);
+                tmem_ld16(quad + C::kTmemO + NC + c, g);
                 tmem_ld_wait();
                 reg_fence(h);
+                reg_fence(g);
+                add16(h, g);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) out_s[j * kDim + self] = __uint_as_float(h[j]);
                 if (someone_dead()) {
