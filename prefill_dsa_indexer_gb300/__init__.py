@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -485,12 +486,20 @@ def _host_ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _expect(t, what, device, dtypes, shape=None):
-    """Raise unless t is a tensor on `device` of one of `dtypes` and, where given, of `shape`."""
-    if not t.is_cuda:
+def _device(t):
+    """Index of a device tensor's device."""
+    d = t.get_device()
+    if d < 0:
         raise DsaError("libdsa takes device tensors only")
-    if t.device != device:
-        raise DsaError(f"{what} is on {t.device}, the call's other tensors on {device}")
+    return d
+
+
+def _expect(t, what, device, dtypes, shape=None):
+    """Raise unless t is a tensor on device `device` of one of `dtypes` and, where given, of `shape`."""
+    d = t.get_device()
+    if d != device:
+        raise DsaError("libdsa takes device tensors only" if d < 0 else
+                       f"{what} is on device {d}, the call's other tensors on device {device}")
     if t.dtype not in dtypes:
         raise DsaError(f"{what} has dtype {t.dtype}: expected {' or '.join(str(d) for d in dtypes)}")
     if shape is not None and t.shape != shape:
@@ -505,17 +514,40 @@ def _flat(t, what, device, dtypes, shape=None):
     return t.data_ptr()
 
 
-def _launch(what, device, stream, fn, *args):
-    """fn(*args, stream) on the tensors' device, whichever device is current."""
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, (stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
+def _launch(what, device, stream, *args):
+    """The library's `what`(*args, stream) on device `device`, whichever is current."""
+    fn = _packed_function(what)
+    if device == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, (stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
-    _check(rc, what)
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
+    if rc != OK:
+        _check(rc, what)
 
 
 _I32, _F32, _BF16 = (torch.int32,), (torch.float32,), (torch.bfloat16,)
+
+# The calls of a decode step are short, so their arguments are packed into bytes (in the C structs' layouts) for
+# function objects of their own that take those, which costs a fraction of ctypes structures.
+_PACK_ROPE_SPEC = struct.Struct("PPif").pack
+_PACK_ROPE_TENSORS = [None] + [struct.Struct("PPiiqqqq" * n).pack for n in range(1, 5)]
+_PACK_KV_ROWS = struct.Struct("PPqqii").pack
+_PACK_ROWS = struct.Struct("PqiPPiii0q").pack
+_packed = {}
+
+
+def _packed_function(name):
+    """The library's `name` taking packed structs."""
+    fn = _packed.get(name)
+    if fn is None:
+        P, I32, I64, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+        fn = load_library()[name]
+        fn.restype = ctypes.c_int
+        fn.argtypes = {"dsa_rope": [P, P, I32, I32, I32, P], "dsa_kv_insert": [P, P, I32, P, P, P, P, P],
+                       "dsa_kv_attention": [P, P, P, I64, I32, F, P, P, P, ctypes.c_size_t, P, P]}[name]
+        _packed[name] = fn
+    return fn
 
 
 def rope_frequencies(rot_dim, theta, scaling="none", factor=1.0, trained_ctx=0):
@@ -545,6 +577,7 @@ class RopeTable:
         if turns.dtype != torch.int64 or not turns.is_cuda or not turns.is_contiguous() or turns.dim() != 1:
             raise DsaError("RopeTable takes a contiguous int64 device vector (rope_turns)")
         self.turns, self.scale, self.rot_dim = turns, float(scale), 2 * turns.shape[0]
+        self.device, self.address = turns.get_device(), turns.data_ptr()
 
 
 def rope_table(rot_dim, theta=10000.0, scaling="none", factor=1.0, trained_ctx=0, device="cuda"):
@@ -554,22 +587,29 @@ def rope_table(rot_dim, theta=10000.0, scaling="none", factor=1.0, trained_ctx=0
 
 
 def _rope_spec(table, positions, device, num_tokens):
-    if table.turns.device != device:
-        raise DsaError(f"the rotary table is on {table.turns.device}, the call's other tensors on {device}")
-    return _RopeSpec(table.turns.data_ptr(), _flat(positions, "positions", device, _I32, (num_tokens,)), table.rot_dim,
-                     table.scale)
+    if table.device != device:
+        raise DsaError(f"the rotary table is on device {table.device}, the call's other tensors on device {device}")
+    return _PACK_ROPE_SPEC(table.address, _flat(positions, "positions", device, _I32, (num_tokens,)), table.rot_dim,
+                           table.scale)
 
 
-def _rope_tensor(x, out, layout, rot_dim, device, dtypes):
-    if x.dim() != 3 or x.shape[2] != rot_dim:
-        raise DsaError(f"rotated tensors are [tokens, heads, {rot_dim}] (a slice of larger heads): got {tuple(x.shape)}")
+def _rope_tensor(x, out, layout, rot_dim, device, dtypes, num_tokens):
+    """The fields of a dsa_rope_tensor."""
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != rot_dim or shape[0] != num_tokens:
+        raise DsaError(f"rotated tensors are [{num_tokens}, heads, {rot_dim}] (a slice of larger heads): got {tuple(shape)}")
     _expect(x, "x", device, dtypes)
-    st, ot = x.stride(), x.stride() if out is x else out.stride()
-    if out is not x:
-        _expect(out, "out", device, dtypes, x.shape)
-    if (st[2] != 1 or ot[2] != 1) and rot_dim > 1:
+    a, b, c = x.stride()
+    if out is x:
+        p = x.data_ptr()
+        if c != 1:
+            raise DsaError("the rotary dims of a head are contiguous")
+        return p, p, shape[1], layout, a, b, a, b
+    _expect(out, "out", device, dtypes, shape)
+    d, e, f = out.stride()
+    if c != 1 or f != 1:
         raise DsaError("the rotary dims of a head are contiguous")
-    return _RopeTensor(x.data_ptr(), out.data_ptr(), x.shape[1], layout, st[0], st[1], ot[0], ot[1])
+    return x.data_ptr(), out.data_ptr(), shape[1], layout, a, b, d, e
 
 
 def rope(x, table, positions, layout=ROPE_INTERLEAVED, out=None, stream=None):
@@ -583,16 +623,14 @@ def rope(x, table, positions, layout=ROPE_INTERLEAVED, out=None, stream=None):
     if not 1 <= len(xs) <= ROPE_MAX_TENSORS or len(outs) != len(xs) or len(layouts) != len(xs):
         raise DsaError(f"rope takes 1 to {ROPE_MAX_TENSORS} tensors, and as many layouts and outputs")
     first = xs[0]
-    n, device, dtypes = first.shape[0], first.device, (first.dtype,)
-    if first.dtype not in (torch.bfloat16, torch.float32):
-        raise DsaError(f"rope takes bf16 or fp32 tensors: got {first.dtype}")
-    if any(t.shape[0] != n for t in xs):
-        raise DsaError("the tensors of one call have the same tokens")
-    ts = (_RopeTensor * len(xs))(*[_rope_tensor(a, b, p, table.rot_dim, device, dtypes)
-                                   for a, b, p in zip(xs, outs, layouts)])
-    spec = _rope_spec(table, positions, device, n)
-    _launch("dsa_rope", device, stream, load_library().dsa_rope, spec, ts, len(xs),
-            DTYPE_BF16 if first.dtype == torch.bfloat16 else DTYPE_FP32, n)
+    n, device, dtype = first.shape[0], _device(first), first.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise DsaError(f"rope takes bf16 or fp32 tensors: got {dtype}")
+    fields = []
+    for a, b, p in zip(xs, outs, layouts):
+        fields += _rope_tensor(a, b, p, table.rot_dim, device, (dtype,), n)
+    _launch("dsa_rope", device, stream, _rope_spec(table, positions, device, n), _PACK_ROPE_TENSORS[len(xs)](*fields),
+            len(xs), DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_FP32, n)
     return outs if many else outs[0]
 
 
@@ -610,6 +648,7 @@ class KvCache:
         self.num_pages, self.kv_heads, _, self.page_size, self.head_dim = pool.shape
         self._c = _KvCache(_ptr(pool), self.format, self.page_size, self.num_pages, self.kv_heads, self.head_dim,
                            self.k_scale, self.v_scale)
+        self.device, self._packed = pool.get_device(), bytes(self._c)
 
 
 def kv_insert(kv, slots, k, v, rope=None, positions=None, layout=ROPE_HALF, rot_offset=0, q=None, q_out=None,
@@ -617,16 +656,15 @@ def kv_insert(kv, slots, k, v, rope=None, positions=None, layout=ROPE_HALF, rot_
     """dsa_kv_insert: write k, v [tokens, kv_heads, head_dim] bf16 (parts of packed rows) at their slots of
     the KvCache.  With `rope` (a RopeTable) and `positions`, K's dims [rot_offset, rot_offset + rot_dim) are
     rotated first, and q [tokens, heads, rot_dim] too, into q_out (default: in place).  Returns q_out."""
-    n, device = slots.shape[0], kv.pool.device
-    shape = (n, kv.kv_heads, kv.head_dim)
+    n, device, heads, dim = slots.shape[0], kv.device, kv.kv_heads, kv.head_dim
+    shape, width = (n, heads, dim), heads * dim
+    strides = []
     for t, what in ((k, "k"), (v, "v")):
         _expect(t, what, device, _BF16, shape)
-        st = t.stride()
-        if st[2] != 1 or (st[1] != kv.head_dim and kv.kv_heads > 1):
+        a, b, c = t.stride()
+        if c != 1 or (b != dim and heads > 1):
             raise DsaError(f"the heads of a token of {what} are packed")
-    width = kv.kv_heads * kv.head_dim
-    rows = _KvRows(k.data_ptr(), v.data_ptr(), max(k.stride(0), width) if n <= 1 else k.stride(0),
-                   max(v.stride(0), width) if n <= 1 else v.stride(0), rot_offset, layout)
+        strides.append(a if n > 1 else max(a, width))
     spec = qt = None
     if rope is not None:
         if positions is None:
@@ -634,13 +672,11 @@ def kv_insert(kv, slots, k, v, rope=None, positions=None, layout=ROPE_HALF, rot_
         spec = _rope_spec(rope, positions, device, n)
         if q is not None:
             q_out = q if q_out is None else q_out
-            if q.shape[0] != n:
-                raise DsaError("q has the tokens of k and v")
-            qt = _rope_tensor(q, q_out, layout, rope.rot_dim, device, _BF16)
+            qt = _PACK_ROPE_TENSORS[1](*_rope_tensor(q, q_out, layout, rope.rot_dim, device, _BF16, n))
     elif q is not None:
         raise DsaError("q is rotated only: it needs rope")
-    _launch("dsa_kv_insert", device, stream, load_library().dsa_kv_insert, kv._c,
-            _flat(slots, "slots", device, _I32), n, rows, spec, qt,
+    _launch("dsa_kv_insert", device, stream, kv._packed, _flat(slots, "slots", device, _I32), n,
+            _PACK_KV_ROWS(k.data_ptr(), v.data_ptr(), strides[0], strides[1], rot_offset, layout), spec, qt,
             None if status is None else _flat(status, "status", device, _I32))
     return q_out
 
@@ -654,28 +690,29 @@ def kv_attention(kv, block_table, row_req, row_ctx, max_ctx, q, sm_scale=None, r
     """dsa_kv_attention: (out bf16 [R, H, head_dim], lse fp32 [R, H]) of q bf16 [R, H, head_dim] (heads packed)
     over the KvCache's tokens below row_ctx; sm_scale defaults to 1 / sqrt(head_dim)."""
     R, H, D = q.shape
-    device = kv.pool.device
+    device = kv.device
     _expect(q, "q", device, _BF16, (R, H, kv.head_dim))
-    st = q.stride()
-    if st[2] != 1 or (st[1] != D and H > 1):
+    a, b, c = q.stride()
+    if c != 1 or (b != D and H > 1):
         raise DsaError("the heads of a row of q are packed")
-    if block_table.dim() != 2:
+    requests = block_table.shape
+    if len(requests) != 2:
         raise DsaError("the block table is [requests, pages]")
     if out is None:
-        out = torch.empty((R, H, D), dtype=torch.bfloat16, device=device)
+        out = torch.empty((R, H, D), dtype=torch.bfloat16, device=q.device)
     if lse is None:
-        lse = torch.empty((R, H), dtype=torch.float32, device=device)
+        lse = torch.empty((R, H), dtype=torch.float32, device=q.device)
     if workspace is None:
         need = kv_attention_workspace_size(kv, R, H, max_ctx)
-        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    rows = _Rows(_flat(block_table, "block_table", device, _I32), block_table.shape[1], block_table.shape[0],
-                 _flat(row_req, "row_req", device, _I32, (R,)), _flat(row_ctx, "row_ctx", device, _I32, (R,)), R,
-                 int(max_ctx), int(rows_per_group))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    rows = _PACK_ROWS(_flat(block_table, "block_table", device, _I32), requests[1], requests[0],
+                      _flat(row_req, "row_req", device, _I32, (R,)), _flat(row_ctx, "row_ctx", device, _I32, (R,)), R,
+                      int(max_ctx), int(rows_per_group))
     wp, wb = (None, 0) if workspace is None else (_flat(workspace, "workspace", device, (workspace.dtype,)),
-                                                  workspace.numel() * workspace.element_size())
-    _launch("dsa_kv_attention", device, stream, load_library().dsa_kv_attention, kv._c, rows, q.data_ptr(),
-            st[0] if R > 1 else H * D, H, D ** -0.5 if sm_scale is None else float(sm_scale),
-            _flat(out, "out", device, _BF16, (R, H, D)), _flat(lse, "lse", device, _F32, (R, H)), wp, wb,
+                                                  workspace.nbytes)
+    _launch("dsa_kv_attention", device, stream, kv._packed, rows, q.data_ptr(), a if R > 1 else H * D, H,
+            D ** -0.5 if sm_scale is None else float(sm_scale), _flat(out, "out", device, _BF16, (R, H, D)),
+            _flat(lse, "lse", device, _F32, (R, H)), wp, wb,
             None if status is None else _flat(status, "status", device, _I32))
     return out, lse
 

@@ -734,11 +734,16 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
     a.pool = static_cast<uint8_t *>(cache->base);
     a.fp8 = cache->format == DSA_KV_FP8;
     a.page_size = cache->page_size;
+    for (a.page_shift = 4; 1 << a.page_shift < a.page_size;) ++a.page_shift;
     a.num_slots = cache->num_pages * cache->page_size;
     a.kv_heads = cache->kv_heads;
     a.head_dim = cache->head_dim;
     a.k_scale = cache->k_scale;
     a.v_scale = cache->v_scale;
+    // (the reciprocals serve where neither they nor the remainders leave fp32's normal range)
+    auto inverse = [](float s) { return s > 1e-20f && s < 1e20f ? static_cast<float>(1.0 / static_cast<double>(s)) : 0.f; };
+    a.k_inv = inverse(cache->k_scale);
+    a.v_inv = inverse(cache->v_scale);
     a.slots = slots;
     a.k = kv->k;
     a.v = kv->v;

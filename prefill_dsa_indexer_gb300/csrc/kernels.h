@@ -291,10 +291,11 @@ struct KvInsertArgs {
     RopeArgs rope;  // num_tensors 1: q is rotated too; rot 0: nothing is rotated
     uint8_t *pool;
     bool fp8;
-    int32_t page_size;
+    int32_t page_size, page_shift;
     int64_t num_slots;
     int32_t kv_heads, head_dim;
     float k_scale, v_scale;
+    float k_inv, v_inv;  // 1 / scale, or 0: divide
     const int32_t *slots;
     const uint16_t *k, *v;
     int64_t k_stride, v_stride;

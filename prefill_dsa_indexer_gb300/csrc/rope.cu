@@ -9,9 +9,12 @@
 // a signed number, are the phase in [-1/2, 1/2) turn; rounding them to fp32 costs at most 2^-26 turn
 // (4e-7 rad at half a turn, less nearer 0) at any position.  sincospi then needs no range reduction.
 //
-// Both kernels move each byte once and do little with it.  One CTA takes a tile of tokens of one
-// tensor (or a range of one token's heads): it computes the tile's cos and sin once per (token, pair)
-// into shared memory, then every thread rotates 16-byte pieces of the tile's heads, four in flight.
+// Both kernels move each byte once and do little with it: they are bound by the memory, and by latency for the
+// few tokens of a decode step.  One CTA takes a tile of tokens of one tensor (or a range of one token's heads):
+// it computes the tile's cos and sin once per (token, pair) into shared memory; then every thread keeps one
+// 16-byte piece of a head and walks over the tile's heads and tokens with it, four pieces in flight, so that the
+// walk has no division and the angles' place changes with the token alone.  8,192 tokens x 98 heads x 64 dims:
+// ROPE_US us; 8,192 tokens into an FP8 pool of 4 KV heads of 128 with 64 query heads rotated: INSERT_US us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -23,9 +26,8 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTileTokens = 32;                               // most tokens of a tile
+constexpr int kTileTokens = 64;                               // most tokens of a tile
 constexpr int kTabPairs = 2048;                               // (token, pair) entries of a tile's table
-constexpr int kUnroll = 4;
 constexpr int kMaxSegs = DSA_ROPE_MAX_TENSORS + 1;
 
 // A run of CTAs that share one tensor: tiles of `tokens` tokens by `heads` heads.
@@ -41,11 +43,37 @@ struct Plan {
     int32_t n;
 };
 
-// n / d for n < 2^16, d < 2^16 (m = ceil(2^32 / d), exact in that range; d = 1 has no 32-bit m).
-struct Div {
-    uint32_t d, m;
-    __device__ explicit Div(uint32_t div) : d(div), m(div > 1 ? 0xffffffffu / div + 1 : 0) {}
-    __device__ uint32_t quot(uint32_t n) const { return d > 1 ? __umulhi(n, m) : n; }
+// A thread's way over a tile of nt tokens x nh heads of `units` pieces: always the same piece of a head, the
+// heads (and tokens) a CTA's width apart.
+struct Walk {
+    int unit, tok, h;           // where it stands
+    int h0, h_step, tok_step;
+
+    __device__ __forceinline__ Walk(int units, int nt, int nh) {
+        const int lanes = kThreads / units, lane = static_cast<int>(threadIdx.x) / units;
+        unit = static_cast<int>(threadIdx.x) - lane * units;
+        if (nh >= lanes) {
+            h0 = lane;
+            h_step = lanes;
+            tok = 0;
+            tok_step = 1;
+        } else {
+            tok = lane / nh;
+            h0 = lane - tok * nh;
+            h_step = nh;
+            tok_step = lanes / nh;
+            if (tok >= tok_step) tok = nt;
+        }
+        if (lane >= lanes) tok = nt;
+        h = h0;
+    }
+    __device__ __forceinline__ void step(int nh) {
+        h += h_step;
+        if (h >= nh) {
+            h = h0;
+            tok += tok_step;
+        }
+    }
 };
 
 template <typename T>
@@ -66,12 +94,12 @@ struct alignas(V * sizeof(T)) Piece {
     T e[V];
 };
 
-// cos and sin of the tile's tokens, times the scale: tab[token in tile][pair].
-__device__ __forceinline__ void fill_table(const RopeArgs &a, float2 *tab, int t0, int nt) {
+// cos and sin of the tile's tokens, times the scale: tab[token in tile][pair].  pos_s: the tile's positions.
+__device__ __forceinline__ void fill_table(const RopeArgs &a, float2 *tab, int32_t *pos_s, int t0, int nt) {
     const int pairs = a.rot >> 1;
-    const Div dv(static_cast<uint32_t>(pairs));
+    if (static_cast<int>(threadIdx.x) < nt) pos_s[threadIdx.x] = a.positions[t0 + threadIdx.x];
     for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
-        const int tok = static_cast<int>(dv.quot(i)), p = i - tok * pairs;
+        const int tok = i / pairs, p = i - tok * pairs;
         const int64_t pos = a.positions[t0 + tok];
         const uint64_t phase = static_cast<uint64_t>(pos) * a.turns[p];
         const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
@@ -84,62 +112,62 @@ __device__ __forceinline__ void fill_table(const RopeArgs &a, float2 *tab, int t
 // Rotate the tile's pieces: V elements (V / 2 pairs) of an interleaved head, or V elements of each
 // half of a half-split head.  V = 1 (half) and 2 (interleaved) are the forms for any alignment.
 template <typename T, bool kHalf, int V>
-__device__ __forceinline__ void rotate_tile(const RopeArgs &a, const RopeTensor &x, const float2 *tab, int t0, int nt,
-                                            int h0, int nh, uint32_t units) {
+__device__ __forceinline__ void rotate_tile(const RopeArgs &a, const RopeTensor &x, const float2 *tab,
+                                            const int32_t *pos_s, int t0, int nt, int h0, int nh, int units) {
     using P = Piece<T, V>;
+    constexpr int kUnroll = V * sizeof(T) < 16 ? 1 : kHalf ? 2 : 4;  // four 16-byte loads in flight
+    constexpr int kPairs = kHalf ? V : V / 2;  // pairs of a piece
     const int pairs = a.rot >> 1;
-    const Div du(units), dh(static_cast<uint32_t>(nh));
-    const uint32_t total = static_cast<uint32_t>(nt * nh) * units;
-    const T *src = static_cast<const T *>(x.x);
-    T *dst = static_cast<T *>(x.out);
-    for (uint32_t i0 = threadIdx.x; i0 < total; i0 += kThreads * kUnroll) {
+    Walk w(units, nt, nh);
+    const T *src = static_cast<const T *>(x.x) + t0 * x.x_token + h0 * x.x_head + w.unit * V;
+    T *dst = static_cast<T *>(x.out) + t0 * x.out_token + h0 * x.out_head + w.unit * V;
+    tab += w.unit * kPairs;
+    while (w.tok < nt) {
         P lo[kUnroll], hi[kUnroll];
-        int64_t to[kUnroll];
-        int ent[kUnroll];
+        int tok[kUnroll], h[kUnroll];
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) {
-            const uint32_t i = i0 + k * kThreads;
-            ent[k] = -1;
-            if (i >= total) continue;
-            const uint32_t row = du.quot(i), u = i - row * units;
-            const uint32_t tok = dh.quot(row), h = row - tok * nh;
-            if (a.positions[t0 + tok] < 0) continue;
-            ent[k] = static_cast<int>(tok) * pairs + static_cast<int>(u) * (kHalf ? V : V / 2);
-            const int64_t from = (t0 + static_cast<int64_t>(tok)) * x.x_token + (h0 + static_cast<int64_t>(h)) * x.x_head + u * V;
-            to[k] = (t0 + static_cast<int64_t>(tok)) * x.out_token + (h0 + static_cast<int64_t>(h)) * x.out_head + u * V;
-            if constexpr (V * sizeof(T) >= 16 || kHalf) {
-                lo[k] = *reinterpret_cast<const P *>(src + from);
-                if (kHalf) hi[k] = *reinterpret_cast<const P *>(src + from + pairs);
-            } else {
+            tok[k] = w.tok;
+            h[k] = w.h;
+            if (w.tok < nt && pos_s[w.tok] < 0) tok[k] = nt;  // a padding token
+            if (tok[k] < nt) {
+                const T *p = src + tok[k] * x.x_token + h[k] * x.x_head;
+                if constexpr (V * sizeof(T) >= 16 || kHalf) {
+                    lo[k] = *reinterpret_cast<const P *>(p);
+                    if (kHalf) hi[k] = *reinterpret_cast<const P *>(p + pairs);
+                } else {
 #pragma unroll
-                for (int e = 0; e < V; ++e) lo[k].e[e] = src[from + e];
+                    for (int e = 0; e < V; ++e) lo[k].e[e] = p[e];
+                }
             }
+            w.step(nh);
         }
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) {
-            if (ent[k] < 0) continue;
-            const float2 *cs = tab + ent[k];
+            if (tok[k] >= nt) continue;
+            const float2 *cs = tab + tok[k] * pairs;
+            T *p = dst + tok[k] * x.out_token + h[k] * x.out_head;
             if constexpr (kHalf) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const float p = to_f32(lo[k].e[e]), q = to_f32(hi[k].e[e]);
-                    lo[k].e[e] = from_f32<T>(p * cs[e].x - q * cs[e].y);
-                    hi[k].e[e] = from_f32<T>(p * cs[e].y + q * cs[e].x);
+                    const float u = to_f32(lo[k].e[e]), v = to_f32(hi[k].e[e]);
+                    lo[k].e[e] = from_f32<T>(u * cs[e].x - v * cs[e].y);
+                    hi[k].e[e] = from_f32<T>(u * cs[e].y + v * cs[e].x);
                 }
-                *reinterpret_cast<P *>(dst + to[k]) = lo[k];
-                *reinterpret_cast<P *>(dst + to[k] + pairs) = hi[k];
+                *reinterpret_cast<P *>(p) = lo[k];
+                *reinterpret_cast<P *>(p + pairs) = hi[k];
             } else {
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) {
-                    const float p = to_f32(lo[k].e[2 * e]), q = to_f32(lo[k].e[2 * e + 1]);
-                    lo[k].e[2 * e] = from_f32<T>(p * cs[e].x - q * cs[e].y);
-                    lo[k].e[2 * e + 1] = from_f32<T>(p * cs[e].y + q * cs[e].x);
+                    const float u = to_f32(lo[k].e[2 * e]), v = to_f32(lo[k].e[2 * e + 1]);
+                    lo[k].e[2 * e] = from_f32<T>(u * cs[e].x - v * cs[e].y);
+                    lo[k].e[2 * e + 1] = from_f32<T>(u * cs[e].y + v * cs[e].x);
                 }
                 if constexpr (V * sizeof(T) >= 16) {
-                    *reinterpret_cast<P *>(dst + to[k]) = lo[k];
+                    *reinterpret_cast<P *>(p) = lo[k];
                 } else {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) dst[to[k] + e] = lo[k].e[e];
+                    for (int e = 0; e < V; ++e) p[e] = lo[k].e[e];
                 }
             }
         }
@@ -148,19 +176,20 @@ __device__ __forceinline__ void rotate_tile(const RopeArgs &a, const RopeTensor 
 
 template <typename T>
 __device__ __forceinline__ void rope_segment(const RopeArgs &a, const RopeTensor &x, const Segment &g, uint32_t cta,
-                                             float2 *tab) {
+                                             float2 *tab, int32_t *pos_s) {
     const uint32_t tile = cta / g.head_chunks, chunk = cta - tile * g.head_chunks;
     const int t0 = static_cast<int>(tile * g.tokens), h0 = static_cast<int>(chunk * g.heads);
     const int nt = min(static_cast<int>(g.tokens), a.num_tokens - t0), nh = min(static_cast<int>(g.heads), x.heads - h0);
-    fill_table(a, tab, t0, nt);
+    const int units = static_cast<int>(g.units);
+    fill_table(a, tab, pos_s, t0, nt);
     __syncthreads();
     constexpr int V = 16 / sizeof(T);
     if (x.half) {
-        if (x.vec) rotate_tile<T, true, V>(a, x, tab, t0, nt, h0, nh, g.units);
-        else rotate_tile<T, true, 1>(a, x, tab, t0, nt, h0, nh, g.units);
+        if (x.vec) rotate_tile<T, true, V>(a, x, tab, pos_s, t0, nt, h0, nh, units);
+        else rotate_tile<T, true, 1>(a, x, tab, pos_s, t0, nt, h0, nh, units);
     } else {
-        if (x.vec) rotate_tile<T, false, V>(a, x, tab, t0, nt, h0, nh, g.units);
-        else rotate_tile<T, false, 2>(a, x, tab, t0, nt, h0, nh, g.units);
+        if (x.vec) rotate_tile<T, false, V>(a, x, tab, pos_s, t0, nt, h0, nh, units);
+        else rotate_tile<T, false, 2>(a, x, tab, pos_s, t0, nt, h0, nh, units);
     }
 }
 
@@ -171,128 +200,158 @@ __device__ __forceinline__ const Segment &segment_of(const Plan &p, uint32_t cta
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a,
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ RopeArgs a,
                                                         const __grid_constant__ Plan p) {
     __shared__ __align__(16) float2 tab[kTabPairs];
+    __shared__ int32_t pos_s[kTileTokens];
     pdl_wait();
     pdl_launch_dependents();
     int j;
     const Segment &g = segment_of(p, blockIdx.x, j);
-    rope_segment<T>(a, a.t[j], g, blockIdx.x - g.first, tab);
+    rope_segment<T>(a, a.t[j], g, blockIdx.x - g.first, tab, pos_s);
 }
 
-__device__ __forceinline__ uint32_t e4m3_rne(float x) {
-    return static_cast<uint32_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3));
+// x / s rounded to nearest for the quotients that matter here, from r = 1 / s rounded to nearest: one correction
+// of x r by its exact remainder gives the rounded quotient (Markstein, IBM J. Res. Dev. 34, 1990).  Quotients of
+// 2^20 and more (and infinities) saturate whatever their last bit.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+    const float q = x * r;
+    const float c = copysignf(fmaf(fmaf(-q, s, x), r, q), x);
+    return fabsf(q) < 1048576.f ? c : q;
+}
+
+// Two fp32 -> two e4m3 codes, round to nearest even, saturating; lo in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2_rne(float lo, float hi) {
+    return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
 }
 
 // The tile's K and V rows (2 * kv_heads per token: K heads, then V heads) into the pool, V elements
 // at a time.  A rotated element of a half-split pair reads its partner too (from L1), so that every
-// thread writes one contiguous piece.
+// thread writes one contiguous piece.  slot_s: the tile's slots, negative where nothing is written.
 template <int V>
-__device__ __forceinline__ void insert_tile(const KvInsertArgs &a, const float2 *tab, int t0, int nt) {
+__device__ __forceinline__ void insert_tile(const KvInsertArgs &a, const float2 *tab, const int32_t *slot_s, int t0,
+                                            int nt) {
     using P = Piece<__nv_bfloat16, V>;
-    const int rot = a.rope.rot, pairs = rot >> 1, D = a.head_dim;
-    const uint32_t units = static_cast<uint32_t>(D / V), rows = 2 * static_cast<uint32_t>(a.kv_heads);
-    const Div du(units), dr(rows);
-    const uint32_t total = static_cast<uint32_t>(nt) * rows * units;
-    for (uint32_t i = threadIdx.x; i < total; i += kThreads) {
-        const uint32_t row = du.quot(i), u = i - row * units;
-        const uint32_t tok = dr.quot(row), j = row - tok * rows;
-        const int32_t slot = a.slots[t0 + tok];
-        if (slot < 0) continue;
-        if (slot >= a.num_slots || (rot > 0 && a.rope.positions[t0 + tok] < 0)) {
-            if (u == 0 && j == 0) report(a.status, DSA_ERR_BOUNDS);
-            continue;
-        }
-        const bool is_v = j >= static_cast<uint32_t>(a.kv_heads);
-        const uint32_t h = is_v ? j - a.kv_heads : j;
-        const __nv_bfloat16 *head = reinterpret_cast<const __nv_bfloat16 *>(is_v ? a.v : a.k) +
-                                    (t0 + static_cast<int64_t>(tok)) * (is_v ? a.v_stride : a.k_stride) +
-                                    static_cast<int64_t>(h) * D;
-        const int e0 = static_cast<int>(u) * V;
-        float x[V];
-        {
-            const P p = *reinterpret_cast<const P *>(head + e0);
+    constexpr int kBatch = V == 8 ? 2 : 1;
+    const int rot = a.rope.rot, pairs = rot >> 1, D = a.head_dim, rows = 2 * a.kv_heads;
+    Walk w(D / V, nt, rows);
+    const int e0 = w.unit * V, r0 = e0 - a.rot_offset;
+    const bool turned = r0 >= 0 && r0 < rot;              // this piece of a K head is rotated
+    const bool low = r0 < pairs;
+    const int partner = a.half ? (low ? pairs : -pairs) : (r0 & 1 ? -1 : 1);  // (interleaved: for V = 1 alone)
+    const __nv_bfloat16 *k = reinterpret_cast<const __nv_bfloat16 *>(a.k) + t0 * a.k_stride + e0;
+    const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(a.v) + t0 * a.v_stride + e0;
+    while (w.tok < nt) {
+        P p[kBatch], q[kBatch];
+        int tok[kBatch], row[kBatch];
 #pragma unroll
-            for (int e = 0; e < V; ++e) x[e] = __bfloat162float(p.e[e]);
+        for (int i = 0; i < kBatch; ++i) {
+            tok[i] = w.tok;
+            row[i] = w.h;
+            if (w.tok < nt && slot_s[w.tok] < 0) tok[i] = nt;
+            if (tok[i] < nt) {
+                const bool is_v = row[i] >= a.kv_heads;
+                const __nv_bfloat16 *x = is_v ? v + tok[i] * a.v_stride + (row[i] - a.kv_heads) * D
+                                              : k + tok[i] * a.k_stride + row[i] * D;
+                p[i] = *reinterpret_cast<const P *>(x);
+                if (turned && !is_v && (a.half || V == 1)) q[i] = *reinterpret_cast<const P *>(x + partner);
+            }
+            w.step(rows);
         }
-        const int r0 = e0 - a.rot_offset;
-        if (!is_v && r0 >= 0 && r0 < rot) {
-            const float2 *cs = tab + tok * pairs;
-            if (a.half) {
-                const bool low = r0 < pairs;
-                const P p = *reinterpret_cast<const P *>(head + e0 + (low ? pairs : -pairs));
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float2 w = cs[(low ? r0 : r0 - pairs) + e];
-                    const float y = __bfloat162float(p.e[e]);
-                    x[e] = low ? x[e] * w.x - y * w.y : y * w.y + x[e] * w.x;
+        for (int i = 0; i < kBatch; ++i) {
+            if (tok[i] >= nt) continue;
+            const bool is_v = row[i] >= a.kv_heads;
+            const int h = is_v ? row[i] - a.kv_heads : row[i];
+            float x[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[e] = __bfloat162float(p[i].e[e]);
+            if (turned && !is_v) {
+                const float2 *cs = tab + tok[i] * pairs;
+                if (a.half) {
+                    const float2 *c = cs + (low ? r0 : r0 - pairs);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float y = __bfloat162float(q[i].e[e]);
+                        x[e] = low ? x[e] * c[e].x - y * c[e].y : y * c[e].y + x[e] * c[e].x;
+                    }
+                } else if constexpr (V > 1) {
+#pragma unroll
+                    for (int e = 0; e < V; e += 2) {
+                        const float2 c = cs[(r0 + e) >> 1];
+                        const float u = x[e], y = x[e + 1];
+                        x[e] = u * c.x - y * c.y;
+                        x[e + 1] = u * c.y + y * c.x;
+                    }
+                } else {
+                    const float2 c = cs[r0 >> 1];
+                    const float y = __bfloat162float(q[i].e[0]);
+                    x[0] = r0 & 1 ? y * c.y + x[0] * c.x : x[0] * c.x - y * c.y;
                 }
-            } else if constexpr (V > 1) {
+            }
+            const int32_t slot = slot_s[tok[i]];
+            const int64_t page = slot >> a.page_shift;
+            const int in_page = slot & (a.page_size - 1);
+            const int64_t at = (((page * a.kv_heads + h) * 2 + (is_v ? 1 : 0)) * a.page_size + in_page) * D + e0;
+            if (a.fp8) {
+                const float s = is_v ? a.v_scale : a.k_scale, r = is_v ? a.v_inv : a.k_inv;
+                float y[V];
 #pragma unroll
-                for (int e = 0; e < V; e += 2) {
-                    const float2 w = cs[(r0 + e) >> 1];
-                    const float p = x[e], q = x[e + 1];
-                    x[e] = p * w.x - q * w.y;
-                    x[e + 1] = p * w.y + q * w.x;
+                for (int e = 0; e < V; ++e) y[e] = r > 0.f ? quotient(x[e], s, r) : x[e] / s;
+                if constexpr (V == 8) {
+                    uint2 o;
+                    o.x = e4m3x2_rne(y[0], y[1]) | e4m3x2_rne(y[2], y[3]) << 16;
+                    o.y = e4m3x2_rne(y[4], y[5]) | e4m3x2_rne(y[6], y[7]) << 16;
+                    *reinterpret_cast<uint2 *>(a.pool + at) = o;
+                } else {
+                    a.pool[at] = static_cast<uint8_t>(e4m3x2_rne(y[0], 0.f));
                 }
             } else {
-                const bool even = (r0 & 1) == 0;
-                const float2 w = cs[r0 >> 1];
-                const float y = __bfloat162float(head[e0 + (even ? 1 : -1)]);
-                x[0] = even ? x[0] * w.x - y * w.y : y * w.y + x[0] * w.x;
-            }
-        }
-        const int64_t page = slot / a.page_size;
-        const int in_page = slot % a.page_size;
-        const int64_t at = (((page * a.kv_heads + h) * 2 + (is_v ? 1 : 0)) * a.page_size + in_page) * D + e0;
-        if (a.fp8) {
-            const float s = is_v ? a.v_scale : a.k_scale;  // divided by, not multiplied by its reciprocal
-            if constexpr (V == 8) {
-                uint2 w;
-                w.x = e4m3_rne(x[0] / s) | e4m3_rne(x[1] / s) << 8 | e4m3_rne(x[2] / s) << 16 | e4m3_rne(x[3] / s) << 24;
-                w.y = e4m3_rne(x[4] / s) | e4m3_rne(x[5] / s) << 8 | e4m3_rne(x[6] / s) << 16 | e4m3_rne(x[7] / s) << 24;
-                *reinterpret_cast<uint2 *>(a.pool + at) = w;
-            } else {
-                a.pool[at] = static_cast<uint8_t>(e4m3_rne(x[0] / s));
-            }
-        } else {
-            P p;
+                P o;
 #pragma unroll
-            for (int e = 0; e < V; ++e) p.e[e] = __float2bfloat16_rn(x[e]);
-            *reinterpret_cast<P *>(reinterpret_cast<__nv_bfloat16 *>(a.pool) + at) = p;
+                for (int e = 0; e < V; ++e) o.e[e] = __float2bfloat16_rn(x[e]);
+                *reinterpret_cast<P *>(reinterpret_cast<__nv_bfloat16 *>(a.pool) + at) = o;
+            }
         }
     }
 }
 
 // Segment 0: the K and V rows; segment 1, if any: q.
-__global__ void __launch_bounds__(kThreads) kv_insert_kernel(const __grid_constant__ KvInsertArgs a,
+__global__ void __launch_bounds__(kThreads, 4) kv_insert_kernel(const __grid_constant__ KvInsertArgs a,
                                                              const __grid_constant__ Plan p) {
     __shared__ __align__(16) float2 tab[kTabPairs];
+    __shared__ int32_t pos_s[kTileTokens];
     pdl_wait();
     pdl_launch_dependents();
     int j;
     const Segment &g = segment_of(p, blockIdx.x, j);
     const uint32_t cta = blockIdx.x - g.first;
     if (j == 1) {
-        rope_segment<__nv_bfloat16>(a.rope, a.rope.t[0], g, cta, tab);
+        rope_segment<__nv_bfloat16>(a.rope, a.rope.t[0], g, cta, tab, pos_s);
         return;
     }
     const int t0 = static_cast<int>(cta * g.tokens);
     const int nt = min(static_cast<int>(g.tokens), a.rope.num_tokens - t0);
-    if (a.rope.rot > 0) {
-        fill_table(a.rope, tab, t0, nt);
-        __syncthreads();
+    __shared__ int32_t slot_s[kTileTokens];
+    if (static_cast<int>(threadIdx.x) < nt) {
+        int32_t slot = a.slots[t0 + threadIdx.x];
+        if (slot >= a.num_slots || (slot >= 0 && a.rope.rot > 0 && a.rope.positions[t0 + threadIdx.x] < 0)) {
+            report(a.status, DSA_ERR_BOUNDS);
+            slot = -1;
+        }
+        slot_s[threadIdx.x] = slot;
     }
-    if (a.vec) insert_tile<8>(a, tab, t0, nt);
-    else insert_tile<1>(a, tab, t0, nt);
+    if (a.rope.rot > 0) fill_table(a.rope, tab, pos_s, t0, nt);
+    __syncthreads();
+    if (a.vec) insert_tile<8>(a, tab, slot_s, t0, nt);
+    else insert_tile<1>(a, tab, slot_s, t0, nt);
 }
 
-// Tiles of about 1,024 pieces (four per thread) once there are enough to fill the GPU, of 256 (one
+// Tiles of about 3,072 pieces (twelve per thread) once there are enough to fill the GPU, of 256 (one
 // per thread, as many CTAs as possible) for the few tokens of a decode step.
 bool add_segment(Plan &p, uint64_t &ctas, int num_tokens, int heads, uint32_t units, int pairs, bool split_heads) {
     const uint64_t pieces = static_cast<uint64_t>(num_tokens) * heads * units;
-    const uint32_t target = pieces >= (1u << 20) ? kThreads * kUnroll : kThreads;
+    const uint32_t target = pieces >= (1u << 20) ? 12 * kThreads : kThreads;
     Segment &g = p.s[p.n++];
     const uint32_t per_token = static_cast<uint32_t>(heads) * units;
     g.units = units;
