@@ -240,12 +240,14 @@ __device__ __forceinline__ bool wait_mbar(uint64_t *bar, uint32_t parity, volati
     return true;
 }
 
+// Every lane asks, which orders the phase before every lane's later reads, and all go on together.
 __device__ __forceinline__ bool wait_mbar_warp(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    int ok = 0;
-    if ((threadIdx.x & 31) == 0) ok = wait_mbar(bar, parity, abort);
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();  // orders lane 0's acquire before every lane's later reads
-    return ok != 0;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        if (__any_sync(0xffffffffu, *abort || clock64() - t0 > kWaitTimeoutCycles)) return false;
+    return true;
 }
 
 __device__ __forceinline__ void gave_up(volatile int *abort, int32_t *status) {

@@ -39,12 +39,6 @@ using fp8mla::e4m3x2;
 using fp8mla::split_pair;
 using fp8mla::sw128;
 
-constexpr int kSoftmax = 4;                                // softmax warps
-constexpr int kProducer = 4, kScores = 5, kQuery = 6, kValues = 7;  // the other warps
-constexpr int kThreads = 32 * 8;                          // two warpgroups
-// Registers: 128 a thread at launch (two CTAs fill the SM); the softmax warpgroup takes 40 of the other's.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kOtherRegs = 88;
-static_assert(kSoftmaxRegs + kOtherRegs == 2 * kLaunchRegs, "the warpgroups share what the CTA was launched with");
 constexpr int kTile = 128;                                 // tokens of a tile
 constexpr int kDim = 128;
 constexpr int kUnitBytes = kTile * kDim;                   // K or V of a tile
@@ -74,26 +68,37 @@ struct Cfg {
     // it in its slot (a barrier's parity alone cannot tell a phase from the one two before it)
     static constexpr int kK = 2, kV = NC == 16 ? 3 : 2, kUnits = kK + kV;
     static constexpr int kQBytes = 2 * NC * kDim, kQBufs = NC == 64 ? 1 : 2;
-    // hi and lo terms lie side by side in an MMA's N where TMEM has room: the scores for NC <= 32, the output always
-    static constexpr int kSN = NC == 64 ? NC : 2 * NC, kON = 2 * NC;
+    // Softmax warpgroups, each with its share of the columns, and the four other warps behind them.
+    static constexpr int kGroups = NC == 64 ? 2 : 1, kMine = NC / kGroups;
+    static constexpr int kSoftmax = 4 * kGroups;
+    static constexpr int kProducer = kSoftmax, kScores = kSoftmax + 1, kQuery = kSoftmax + 2, kValues = kSoftmax + 3;
+    static constexpr int kThreads = 32 * (kSoftmax + 4);
+    // Registers a thread: at launch (two CTAs fill the SM), then the softmax warpgroups take some of the others'.
+    static constexpr int kLaunchRegs = kGroups == 1 ? 128 : 80;
+    static constexpr int kSoftmaxRegs = kGroups == 1 ? 168 : 88, kOtherRegs = kGroups == 1 ? 88 : 64;
+    static_assert(kGroups * kSoftmaxRegs + kOtherRegs == (kGroups + 1) * kLaunchRegs,
+                  "the warpgroups share what the CTA was launched with");
+    // hi and lo terms lie side by side in an MMA's N, or follow one another into the same columns
+    static constexpr int kSN = NC == 64 ? NC : 2 * NC, kON = NC == 64 ? NC : 2 * NC;
     static constexpr int kPBufs = NC == 64 ? 1 : 2;        // a token's 128-byte row of P holds two tiles' weights
-    static constexpr uint32_t kTmemO = 2 * kSN;            // two score buffers, then the output
+    static constexpr bool kSumsInTmem = NC == 64;          // a thread's sums of weights, if not in registers
+    static constexpr uint32_t kTmemO = 2 * kSN;            // two score buffers, then the output, then the sums
+    static constexpr uint32_t kTmemL = kTmemO + kON;
     static constexpr uint32_t kTmemCols = NC == 16 ? 128 : 256;  // two CTAs share the SM's 512
-    static constexpr bool kKeep = NC <= 32;                // a thread keeps its scores in registers
     static constexpr int OFF_Q = kUnits * kUnitBytes;      // [kQBufs]: rows hi 0 .. NC - 1, lo NC .. 2 NC - 1
     static constexpr int OFF_P = OFF_Q + kQBufs * kQBytes;      // [kPBufs] a token's row: NC hi, NC lo bytes; then the output's way out
     static constexpr int OFF_COLS = OFF_P + kTile * 128;   // [2] by item parity
     static constexpr int OFF_ITEM = OFF_COLS + 2 * static_cast<int>(sizeof(Columns<NC>));
-    static constexpr int OFF_MAX = OFF_ITEM + 2 * 64;      // [4][NC] a warp's largest score
-    static constexpr int OFF_BASE = OFF_MAX + 4 * NC * 4;  // [4][NC] minus the bases, a copy per warp
-    static constexpr int OFF_FAC = OFF_BASE + 4 * NC * 4;  // [4][NC] rescale factors
-    static constexpr int OFF_SUM = OFF_FAC + 4 * NC * 4;   // [2][4][NC] a warp's weights, by item parity
+    static constexpr int OFF_MAX = OFF_ITEM + 2 * 64;      // [kSoftmax][kMine] a warp's largest scores
+    static constexpr int OFF_BASE = OFF_MAX + 4 * NC * 4;  // [kSoftmax][kMine] minus the bases, a copy per warp
+    static constexpr int OFF_FAC = OFF_BASE + 4 * NC * 4;  // [kSoftmax][kMine] rescale factors
+    static constexpr int OFF_SUM = OFF_FAC + 4 * NC * 4;   // [2][kSoftmax][kMine] sums of weights, by item parity
     static constexpr int OFF_SCHED = OFF_SUM + 2 * 4 * NC * 4;
     static constexpr int OFF_BARS = OFF_SCHED + static_cast<int>(sizeof(KvSchedule));
     static constexpr int kNumBars = 2 * kUnits + 2 * 2 + 2 * 2 + kQBufs + 2 * kPBufs + 2;
     static constexpr int OFF_MISC = OFF_BARS + kNumBars * 8;
     static constexpr int kSmemBytes = OFF_MISC + 16 + 1024;
-    static_assert(kTmemO + kON <= kTmemCols, "TMEM plan");
+    static_assert(kTmemL + (kSumsInTmem ? NC : 0) <= kTmemCols, "TMEM plan");
     static_assert(kSmemBytes <= 115712, "two CTAs per SM");
 };
 
@@ -152,14 +157,15 @@ __device__ __forceinline__ void add16(uint32_t (&h)[16], const uint32_t (&g)[16]
     }
 }
 
-// OR of a predicate over the four softmax warps, who all meet here.
-__device__ __forceinline__ bool meet_any(bool p) {
+// OR of a predicate over the softmax warps (kN threads), who all meet here.
+template <int kN>
+__device__ __forceinline__ bool meet_any_of(bool p) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred.aligned q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+        "barrier.cta.red.or.pred.aligned q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(p))
+        : "r"(static_cast<uint32_t>(p)), "n"(kN)
         : "memory");
     return r != 0;
 }
@@ -168,9 +174,11 @@ __device__ __forceinline__ bool meet_any(bool p) {
 __device__ __forceinline__ bool any_nan4(uint32_t v) { return __vcmpeq4(v & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0; }
 
 template <int NC>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
     kv_attention_fp8_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ KvAttnArgs a) {
     using C = Cfg<NC>;
+    constexpr int kSoftmax = C::kSoftmax, kProducer = C::kProducer, kScores = C::kScores, kQuery = C::kQuery,
+                  kValues = C::kValues, kMine = C::kMine;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Columns<NC> *cols_s = reinterpret_cast<Columns<NC> *>(smem + C::OFF_COLS);
@@ -233,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int hpg = a.num_heads / a.kv_heads, cols = a.group * hpg;
 
     if (warp >= kSoftmax) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         if (warp == kProducer) {
             // ---- K and V: boxes of at most 128 rows, lane b issues box b of a unit
             const int box_rows = min(a.page_size, kTile);
@@ -447,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const uint32_t add = values && !apart && i > 0 ? 1u : 0u;
                         const uint64_t ad = sdesc_sw128(ua + slot * kUnitBytes, 16, 1024);
                         // hi and lo terms side by side in N, or hi, then lo ones into the same columns
-                        const bool in_turn = apart || (!values && C::kSN == NC);
+                        const bool in_turn = apart || (values ? C::kON : C::kSN) == NC;
                         const uint32_t lo = values ? NC / 16 : NC * kDim / 16;
 #pragma unroll 2
                         for (uint32_t k = 0; k < (in_turn ? 8u : 4u); ++k)
@@ -472,15 +480,16 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         // ---- softmax: thread = token (TMEM lane) of a tile, then dim of the output.  A wait that gives up makes
         // its warp `dead`.  Every meeting whose first round is true has a second one that asks for dead warps,
         // after which all leave: so no warp waits for one that has gone
-        const int self = warp * 32 + lane;
-        const uint32_t quad = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        float *max_s = reinterpret_cast<float *>(smem + C::OFF_MAX);
-        float *nbase = reinterpret_cast<float *>(smem + C::OFF_BASE) + warp * NC;
-        float *fac = reinterpret_cast<float *>(smem + C::OFF_FAC) + warp * NC;
+        const int self = (warp & 3) * 32 + lane;
+        const int mine = (warp >> 2) * kMine;   // this warpgroup's first column
+        const uint32_t quad = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + mine;
+        float *max_s = reinterpret_cast<float *>(smem + C::OFF_MAX) + 4 * mine;  // [4][kMine], as the sums
+        float *nbase = reinterpret_cast<float *>(smem + C::OFF_BASE) + warp * kMine;
+        float *fac = reinterpret_cast<float *>(smem + C::OFF_FAC) + warp * kMine;
         uint32_t s_count = 0;                   // tiles
         uint32_t pv_open = 0, pv_phases = 0;    // a bit per buffer of P: a product is out whose end has not been seen
         bool dead = false;
@@ -495,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (uint32_t b = 0; b < C::kPBufs; ++b) pv_wait(b);
         };
+        auto meet_any = [](bool p) { return meet_any_of<32 * kSoftmax>(p); };
         auto someone_dead = [&]() { return meet_any(dead) && meet_any(dead); };
         for (uint32_t item_n = 0;; ++item_n) {
             const uint32_t parity = item_n & 1;
@@ -509,10 +519,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int ncols = item->cols, part = item->part, parts = item->parts;
             const int tiles = (t_end - t_begin + kTile - 1) / kTile;
 
-            float l[NC];
+            float l[kMine];  // (kSumsInTmem: 16 at a time)
 #pragma unroll
-            for (int n = 0; n < NC; ++n) l[n] = 0.f;
-            for (int n = lane; n < NC; n += 32) nbase[n] = 0.f;
+            for (int n = 0; n < kMine; ++n) l[n] = 0.f;
+#pragma unroll 1
+            for (int n = lane; n < kMine; n += 32) nbase[n] = 0.f;
             __syncwarp();
             bool leave = false;
             for (int i = 0; i < tiles; ++i, ++s_count) {
@@ -541,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
-                        const float4 sc = *reinterpret_cast<const float4 *>(cs->scale + c + j);
+                        const float4 sc = *reinterpret_cast<const float4 *>(cs->scale + mine + c + j);
                         const float4 nb = *reinterpret_cast<const float4 *>(nbase + c + j);
                         const float2 p = __ffma2_rn(make_float2(__uint_as_float(h[j]), __uint_as_float(h[j + 1])),
                                                     make_float2(sc.x, sc.y), make_float2(nb.x, nb.y));
@@ -555,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (edge) {
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
-                            const int4 n = *reinterpret_cast<const int4 *>(cs->ctx + c + j);
+                            const int4 n = *reinterpret_cast<const int4 *>(cs->ctx + mine + c + j);
                             if (t >= n.x) x[j] = -INFINITY;
                             if (t >= n.y) x[j + 1] = -INFINITY;
                             if (t >= n.z) x[j + 2] = -INFINITY;
@@ -563,56 +574,51 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                     }
                 };
-                float x[C::kKeep ? NC : 16];
+                float x[kMine];
                 // at most twice round: the first tile sets the bases, later ones move those that no longer fit
 #pragma unroll 1
                 for (bool settled = false;;) {
                     float top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < NC; c += 16) {
-                        float *xc = x + (C::kKeep ? c : 0);
-                        scores(c, xc);
+                    for (int c = 0; c < kMine; c += 16) {
+                        scores(c, x + c);
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2) top = fmaxf(top, fmaxf(xc[j], xc[j + 1]));
-                        // (without room for all scores, each 16 columns' maxima are taken as they pass)
-                        if (!C::kKeep && i == 0 && !settled) reduce_columns<16, true>(xc, max_s + warp * NC + c, lane);
+                        for (int j = 0; j < 16; j += 2) top = fmaxf(top, fmaxf(x[c + j], x[c + j + 1]));
                     }
                     if (settled || (i > 0 && !meet_any(top > kTop || dead))) break;
-                    if (C::kKeep) {
-                        reduce_columns<NC, true>(x, max_s + warp * NC, lane);
-                    } else if (i > 0) {
-#pragma unroll 1
-                        for (int c = 0; c < NC; c += 16) {
-                            scores(c, x);
-                            reduce_columns<16, true>(x, max_s + warp * NC + c, lane);
-                        }
-                    }
+                    reduce_columns<kMine, true>(x, max_s + (warp & 3) * kMine, lane);
                     if (i == 0 ? someone_dead() : meet_any(dead)) {
                         leave = true;
                         break;
                     }
                     pv_wait_all();  // O^T at rest
 #pragma unroll 1
-                    for (int n = lane; n < NC; n += 32) {
-                        const float m = fmaxf(fmaxf(max_s[n], max_s[NC + n]), fmaxf(max_s[2 * NC + n], max_s[3 * NC + n]));
+                    for (int n = lane; n < kMine; n += 32) {
+                        const float m = fmaxf(fmaxf(max_s[n], max_s[kMine + n]),
+                                              fmaxf(max_s[2 * kMine + n], max_s[3 * kMine + n]));
                         const bool on = i == 0 ? m > -INFINITY : m > kTop;
                         fac[n] = on && i > 0 ? ex2(kBias - m) : 1.f;
                         if (on) nbase[n] += kBias - m;
                     }
                     __syncwarp();
                     if (i > 0) {
+                        if (!C::kSumsInTmem) {
 #pragma unroll
-                        for (int n = 0; n < NC; ++n) l[n] *= fac[n];
+                            for (int n = 0; n < kMine; ++n) l[n] *= fac[n];
+                        }
+                        // O^T and the sums in TMEM lie NC columns apart
 #pragma unroll 1
-                        for (int c = 0; c < C::kON; c += 16) {
-                            uint32_t h[16];
-                            tmem_ld16(quad + C::kTmemO + c, h);
-                            tmem_ld_wait();
-                            reg_fence(h);
-                            const float *f = fac + (c < NC ? c : c - NC);
+                        for (uint32_t at = C::kTmemO; at < C::kTmemL + (C::kSumsInTmem ? NC : 0); at += NC) {
+#pragma unroll 1
+                            for (int c = 0; c < kMine; c += 16) {
+                                uint32_t h[16];
+                                tmem_ld16(quad + at + c, h);
+                                tmem_ld_wait();
+                                reg_fence(h);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) h[j] = __float_as_uint(__uint_as_float(h[j]) * f[j]);
-                            tmem_st16(quad + C::kTmemO + c, h);
+                                for (int j = 0; j < 16; ++j) h[j] = __float_as_uint(__uint_as_float(h[j]) * fac[c + j]);
+                                tmem_st16(quad + at + c, h);
+                            }
                         }
                         tmem_st_wait();
                     }
@@ -624,9 +630,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 // weights: unit c / 16 of the token's row of P holds hi, unit (NC + c) / 16 lo.  hi is the weight
                 // rounded to 4 significant bits, t - (t - p) with t = p (2^20 + 1); lo the rest, exact in fp32
 #pragma unroll
-                for (int c = 0; c < NC; c += 16) {
-                    float *xc = x + (C::kKeep ? c : 0);
-                    if (!C::kKeep) scores(c, xc);
+                for (int c = 0; c < kMine; c += 16) {
+                    float *lc = l + (C::kSumsInTmem ? 0 : c);
+                    uint32_t sums[16];
+                    if (C::kSumsInTmem && i > 0) tmem_ld16(quad + C::kTmemL + c, sums);
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
@@ -634,10 +641,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
                             const int k = j + 2 * y;
-                            const float2 p = make_float2(ex2(xc[k]), ex2(xc[k + 1]));
-                            const float2 s = __fadd2_rn(make_float2(l[c + k], l[c + k + 1]), p);
-                            l[c + k] = s.x;
-                            l[c + k + 1] = s.y;
+                            const float2 p = make_float2(ex2(x[c + k]), ex2(x[c + k + 1]));
+                            if (C::kSumsInTmem) {
+                                x[c + k] = p.x;
+                                x[c + k + 1] = p.y;
+                            } else {
+                                const float2 s = __fadd2_rn(make_float2(lc[k], lc[k + 1]), p);
+                                lc[k] = s.x;
+                                lc[k + 1] = s.y;
+                            }
                             const float2 tt = __fmul2_rn(p, make_float2(1048577.f, 1048577.f));
                             const float2 minus = make_float2(-1.f, -1.f);
                             h2[y] = __ffma2_rn(__ffma2_rn(p, minus, tt), minus, tt);
@@ -646,10 +658,25 @@ __global__ void __launch_bounds__(kThreads, 2)
                         hi[j / 4] = e4m3x2(h2[0].x, h2[0].y) | (e4m3x2(h2[1].x, h2[1].y) << 16);
                         lo[j / 4] = e4m3x2(l2[0].x, l2[0].y) | (e4m3x2(l2[1].x, l2[1].y) << 16);
                     }
-                    *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, (2 * NC * pb + c) / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, (2 * NC * pb + NC + c) / 16)) =
-                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    const int at = 2 * NC * pb + mine + c;
+                    *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, at / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, (NC + at) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    if (C::kSumsInTmem) {
+                        if (i > 0) {
+                            tmem_ld_wait();
+                            reg_fence(sums);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sums[j] = 0u;
+                        }
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(x[c + j]);
+                        add16(sums, w);
+                        tmem_st16(quad + C::kTmemL + c, sums);
+                    }
                 }
+                if (C::kSumsInTmem) tmem_st_wait();
                 auto hand_over = [&]() {
                     fence_async_smem();
                     tc_fence_before();
@@ -673,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                             break;
                         }
                     }
-                    if (t >= ctx_max) {  // no row sees it: whatever the slot or the stage holds
+                    if (mine == 0 && t >= ctx_max) {  // no row sees it: whatever the slot or the stage holds
 #pragma unroll
                         for (int y = 0; y < 8; ++y) vrow[y] = make_uint4(0u, 0u, 0u, 0u);
                     }
@@ -698,13 +725,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (next < 0) break;
                     prev = next;
                 }
-                if (self == 0) *levels_s = levels;
+                if (threadIdx.x == 0) *levels_s = levels;
                 for (int v = 0, cur = INT32_MAX; v < levels; ++v) {
                     int next = -1;
                     for (int r = 0; r < a.group; ++r)
                         if (item->ctx[r] < cur) next = max(next, item->ctx[r]);
                     cur = next;
-                    if (t >= cur) {
+                    if (mine == 0 && t >= cur) {
 #pragma unroll
                         for (int y = 0; y < 8; ++y) vrow[y] = make_uint4(0u, 0u, 0u, 0u);
                     }
@@ -713,20 +740,20 @@ __global__ void __launch_bounds__(kThreads, 2)
                     pv_open |= 1u << pb;
                     pv_wait(pb);
 #pragma unroll 1
-                    for (int c = 0; c < NC; c += 16) {
+                    for (int c = 0; c < kMine; c += 16) {
                         uint32_t h[16], g[16];
                         tmem_ld16(quad + sb * C::kSN + c, h);
-                        // the hi half of O^T takes the sum; in the item's first tile the lo half becomes zero
+                        // the hi half of O^T takes the sum; in the item's first tile a lo half becomes zero
                         tmem_ld16(quad + C::kTmemO + c, g);
                         tmem_ld_wait();
                         reg_fence(h);
                         reg_fence(g);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            if (cs->ctx[c + j] == cur)
+                            if (cs->ctx[mine + c + j] == cur)
                                 g[j] = __float_as_uint(__uint_as_float(h[j]) + (i > 0 ? __uint_as_float(g[j]) : 0.f));
                         tmem_st16(quad + C::kTmemO + c, g);
-                        if (i == 0) {
+                        if (C::kON > NC && i == 0) {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) g[j] = 0u;
                             tmem_st16(quad + C::kTmemO + NC + c, g);
@@ -736,41 +763,66 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (self == 0) *levels_s = 0;
+                if (threadIdx.x == 0) *levels_s = 0;
                 if (lane == 0) mbar_arrive(&s_empty[sb]);
             }
             if (leave) break;
 
             // ---- the item's sums and output
-            float *sums = sum_s + parity * kSoftmax * NC;
-            reduce_columns<NC, false>(l, sums + warp * NC, lane);
+            float *sums = sum_s + parity * 4 * NC + 4 * mine;
+            if (C::kSumsInTmem && tiles > 0) {
+#pragma unroll
+                for (int c = 0; c < kMine; c += 16) {
+                    uint32_t h[16];
+                    tmem_ld16(quad + C::kTmemL + c, h);
+                    tmem_ld_wait();
+                    reg_fence(h);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) l[c + j] = __uint_as_float(h[j]);
+                }
+            }
+            reduce_columns<kMine, false>(l, sums + (warp & 3) * kMine, lane);
             if (someone_dead()) break;
             // a column's factor: 1 for a part of several, else 1 / its sum (0 without any weight)
 #pragma unroll 1
-            for (int n = lane; n < NC; n += 32) {
-                const float total = sums[n] + sums[NC + n] + sums[2 * NC + n] + sums[3 * NC + n];
+            for (int n = lane; n < kMine; n += 32) {
+                const float total = sums[n] + sums[kMine + n] + sums[2 * kMine + n] + sums[3 * kMine + n];
                 fac[n] = tiles == 0 ? 0.f : parts > 1 ? 1.f : total == 0.f ? 0.f : a.v_scale / total;
-                if (warp == 0 && n < ncols) {
+                if ((warp & 3) == 0 && mine + n < ncols) {
                     const float b = -nbase[n];
+                    const int at = cs->at[mine + n];
                     if (parts > 1)
-                        a.part_ml[static_cast<int64_t>(cs->at[n]) * a.parts_bound + part] = make_float2(b, total);
+                        a.part_ml[static_cast<int64_t>(at) * a.parts_bound + part] = make_float2(b, total);
                     else if (a.lse != nullptr)
-                        a.lse[cs->at[n]] = total == 0.f ? -INFINITY : (b + log2f(total)) * 0.6931471805599453f;
+                        a.lse[at] = total == 0.f ? -INFINITY : (b + log2f(total)) * 0.6931471805599453f;
                 }
             }
             __syncwarp();
             pv_wait_all();
             // 16 columns at a time go through P's place (free since the last product), each a row of 128 floats,
-            // so that the lanes write four dims in a row; a half of the place holds them
-            for (int c = 0; c < ncols; c += 16) {
-                float *out_s = reinterpret_cast<float *>(smem + C::OFF_P) + (c >> 4 & 1) * 16 * kDim;
-                uint32_t h[16], g[16];
+            // so that the lanes write four dims in a row.  A half of the place holds them: one for each of two
+            // warpgroups, or one after the other
+#pragma unroll 1
+            for (int c = 0; c < min(ncols, kMine); c += 16) {
+                const int half = C::kGroups == 2 ? warp >> 2 : c >> 4 & 1;
+                float *out_s = reinterpret_cast<float *>(smem + C::OFF_P) + half * 16 * kDim;
+                uint32_t h[16];
                 tmem_ld16(quad + C::kTmemO + c, h);
-                tmem_ld16(quad + C::kTmemO + NC + c, g);
-                tmem_ld_wait();
-                reg_fence(h);
-                reg_fence(g);
-                add16(h, g);
+                if constexpr (C::kON > NC) {
+                    uint32_t g[16];
+                    tmem_ld16(quad + C::kTmemO + NC + c, g);
+                    tmem_ld_wait();
+                    reg_fence(h);
+                    reg_fence(g);
+                    add16(h, g);
+                } else {
+                    tmem_ld_wait();
+                    reg_fence(h);
+                }
+                if (C::kGroups == 2 && c > 0 && someone_dead()) {  // the last columns have left the place
+                    leave = true;
+                    break;
+                }
 #pragma unroll
                 for (int j = 0; j < 16; ++j) out_s[j * kDim + self] = __uint_as_float(h[j]);
                 if (someone_dead()) {
@@ -778,10 +830,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     break;
                 }
 #pragma unroll 1
-                for (int n = warp; n < min(16, ncols - c); n += kSoftmax) {
+                for (int n = warp & 3; n < min(16, ncols - mine - c); n += 4) {
                     const float f = fac[c + n];
                     float4 o = *reinterpret_cast<const float4 *>(out_s + n * kDim + 4 * lane);
-                    const int64_t at = cs->at[c + n];
+                    const int64_t at = cs->at[mine + c + n];
                     if (f == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);  // (without a tile it is no output)
                     if (parts > 1)
                         *reinterpret_cast<float4 *>(a.part_o + (at * a.parts_bound + part) * kDim + 4 * lane) = o;
@@ -824,12 +876,12 @@ cudaError_t launch_columns(KvAttnArgs &a, int cols, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         regs.store(fa.numRegs);
     }
-    if (regs.load() < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    if (regs.load() < Cfg<NC>::kLaunchRegs) return cudaErrorInvalidConfiguration;
     CUtensorMap map;
     if (!encode_kv_rows_map(&map, a.pool, a.pool_rows, kDim, a.page_size)) return cudaErrorInvalidValue;
     const uint32_t ctas = persistent_ctas(a);
     if (ctas == 0) return cudaErrorInvalidDevice;
-    return launch_pdl(kv_attention_fp8_kernel<NC>, dim3(ctas), dim3(kThreads), Cfg<NC>::kSmemBytes, s, map, a);
+    return launch_pdl(kv_attention_fp8_kernel<NC>, dim3(ctas), dim3(Cfg<NC>::kThreads), Cfg<NC>::kSmemBytes, s, map, a);
 }
 
 }  // namespace
