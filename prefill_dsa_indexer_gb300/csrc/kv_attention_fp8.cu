@@ -53,7 +53,10 @@ struct Item {
     int32_t cols;              // real columns
     int32_t part, parts;
     int32_t ctx[8];            // the group's contexts
+    int32_t image_last;        // the next item has another query image
+    int32_t pad[15];
 };
+static_assert(sizeof(Item) == 128, "item layout");
 
 // An item's columns: log2 units per unit of score, tokens seen, row * num_heads + head.
 template <int NC>
@@ -79,17 +82,17 @@ struct Cfg {
     static_assert(kGroups * kSoftmaxRegs + kOtherRegs == (kGroups + 1) * kLaunchRegs,
                   "the warpgroups share what the CTA was launched with");
     // hi and lo terms lie side by side in an MMA's N, or follow one another into the same columns
-    static constexpr int kSN = NC == 64 ? NC : 2 * NC, kON = NC == 64 ? NC : 2 * NC;
+    static constexpr int kSN = NC == 16 ? 2 * NC : NC, kON = NC == 64 ? NC : 2 * NC;
     static constexpr int kPBufs = NC == 64 ? 1 : 2;        // a token's 128-byte row of P holds two tiles' weights
     static constexpr bool kSumsInTmem = NC == 64;          // a thread's sums of weights, if not in registers
     static constexpr uint32_t kTmemO = 2 * kSN;            // two score buffers, then the output, then the sums
     static constexpr uint32_t kTmemL = kTmemO + kON;
     static constexpr uint32_t kTmemCols = NC == 16 ? 128 : 256;  // two CTAs share the SM's 512
     static constexpr int OFF_Q = kUnits * kUnitBytes;      // [kQBufs]: rows hi 0 .. NC - 1, lo NC .. 2 NC - 1
-    static constexpr int OFF_P = OFF_Q + kQBufs * kQBytes;      // [kPBufs] a token's row: NC hi, NC lo bytes; then the output's way out
-    static constexpr int OFF_COLS = OFF_P + kTile * 128;   // [2] by item parity
+    static constexpr int OFF_P = OFF_Q + kQBufs * kQBytes;      // [kPBufs] a token's row: NC hi, NC lo bytes
+    static constexpr int OFF_COLS = OFF_P + kTile * 128;   // [2] by image parity
     static constexpr int OFF_ITEM = OFF_COLS + 2 * static_cast<int>(sizeof(Columns<NC>));
-    static constexpr int OFF_MAX = OFF_ITEM + 2 * 64;      // [kSoftmax][kMine] a warp's largest scores
+    static constexpr int OFF_MAX = OFF_ITEM + 2 * static_cast<int>(sizeof(Item));      // [kSoftmax][kMine] a warp's largest scores
     static constexpr int OFF_BASE = OFF_MAX + 4 * NC * 4;  // [kSoftmax][kMine] minus the bases, a copy per warp
     static constexpr int OFF_FAC = OFF_BASE + 4 * NC * 4;  // [kSoftmax][kMine] rescale factors
     static constexpr int OFF_SUM = OFF_FAC + 4 * NC * 4;   // [2][kSoftmax][kMine] sums of weights, by item parity
@@ -173,6 +176,64 @@ __device__ __forceinline__ bool meet_any_of(bool p) {
 // Whether any of four e4m3 codes is NaN (0x7f or 0xff).
 __device__ __forceinline__ bool any_nan4(uint32_t v) { return __vcmpeq4(v & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0; }
 
+// A column's query as hi and lo terms, and its scale.  The 16 bf16 elements of lane's unit (lane & 7) of column n
+// are in v0, v1; the eight lanes of a column work together, so a warp takes four.
+template <int NC>
+__device__ __forceinline__ void convert_query(uint8_t *img, Columns<NC> *cs, const KvAttnArgs &a, const KvCursor &w,
+                                              int n, int cols, int hpg, uint4 v0, uint4 v1, int lane) {
+    const int unit = lane & 7;
+    const uint32_t h[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    // the column's largest |q| by its bits (an infinity or a NaN is above every number)
+    uint32_t top = 0;
+#pragma unroll
+    for (int y = 0; y < 8; ++y) top = max(top, max(h[y] << 16 & 0x7fff0000u, h[y] & 0x7fff0000u));
+#pragma unroll
+    for (int y = 1; y < 8; y <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
+    const bool finite = top < 0x7f800000u;
+    // 2^e brings it to (224, 448]
+    int e = 0;
+    if (top > 0 && finite) {
+        e = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+        e = max(-120, min(120, e));
+    }
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        const uint2 p0 = split_pair(bf16_lo(h[2 * y]) * up, bf16_hi(h[2 * y]) * up);
+        const uint2 p1 = split_pair(bf16_lo(h[2 * y + 1]) * up, bf16_hi(h[2 * y + 1]) * up);
+        hi[y] = p0.x | (p1.x << 16);
+        lo[y] = p0.y | (p1.y << 16);
+    }
+    *reinterpret_cast<uint4 *>(img + sw128(n, unit)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4 *>(img + sw128(NC + n, unit)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    const int col = w.col0 + n, row = col < cols ? static_cast<int>(col * a.hpg_mul >> 20) : 0;
+    const int ctx = __shfl_sync(0xffffffffu, w.my_ctx, row);
+    if (unit == 0) {
+        // a masked score is -inf times the scale: neither zero nor infinity.  A NaN or an infinity
+        // in q makes its column's scores, and so its output, NaN
+        const float scale = a.s_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        cs->scale[n] = finite ? fminf(fmaxf(scale, 1.17549435e-38f), 3.40282347e38f) : __uint_as_float(0x7fc00000u);
+        cs->ctx[n] = col < cols ? ctx : 0;
+        cs->at[n] = (w.row0 + row) * a.num_heads + w.g * hpg + (col < cols ? col - row * hpg : 0);
+    }
+}
+
+// The 16 elements that convert_query wants of column n; zeros behind the last column.
+__device__ __forceinline__ void load_query(const KvAttnArgs &a, const KvCursor &w, int n, int cols, int hpg, int lane,
+                                           uint4 &v0, uint4 &v1) {
+    v0 = v1 = make_uint4(0u, 0u, 0u, 0u);
+    const int col = w.col0 + n;
+    if (col < cols) {
+        const int row = static_cast<int>(col * a.hpg_mul >> 20);
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (w.row0 + row) * a.q_stride +
+                                                           static_cast<int64_t>(w.g * hpg + col - row * hpg) * kDim +
+                                                           (lane & 7) * 16);
+        v0 = src[0];
+        v1 = src[1];
+    }
+}
+
 template <int NC>
 __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
     kv_attention_fp8_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ KvAttnArgs a) {
@@ -239,6 +300,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
     __syncthreads();
 
     const int hpg = a.num_heads / a.kv_heads, cols = a.group * hpg;
+    KvCursor w;
+    bool more = w.first<NC>(a, sched, lane);
 
     if (warp >= kSoftmax) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
@@ -249,8 +312,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
             const uint64_t policy = l2_evict_first_policy();
             uint32_t issued = 0;  // tiles
             bool go = true;
-            KvCursor w;
-            for (bool more = w.first<NC>(a, sched, lane); more && go; more = w.next<NC>(a, lane)) {
+            for (; more && go; more = w.next<NC>(a, lane)) {
                 const int num_pages = (w.t_end + a.page_size - 1) >> a.page_shift;
                 const int32_t *table = a.block_table + static_cast<int64_t>(w.req) * a.bt_stride;
                 auto load_ids = [&](int p) { return p + lane < num_pages ? table[p + lane] : 0; };
@@ -300,94 +362,41 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                 }
             }
         } else if (warp == kQuery) {
-            // ---- items, their columns and query images (rows hi 0 .. NC - 1, lo NC .. 2 NC - 1 of 128 bytes)
-            uint32_t count = 0;  // items handed on
-            bool go = true;
-            KvCursor w;
-            for (bool more = w.first<NC>(a, sched, lane); more && go; more = w.next<NC>(a, lane)) {
+            // ---- items, their columns and query images (rows hi 0 .. NC - 1, lo NC .. 2 NC - 1 of 128 bytes).
+            // Neighbours of one row group and KV head share an image; the first is the softmax warps' work
+            uint32_t count = 0, images = 1;  // items handed on, images begun
+            bool go = true, fresh = false;
+            if (more) named_bar_sync(2, 32 * (kSoftmax + 1));
+            for (; more && go; more = w.next<NC>(a, lane)) {
                 if (w.bad && w.part == 0 && lane == 0) report(a.status, DSA_ERR_BOUNDS);
-                // 16 dims (a unit) of a column per lane and turn, four columns a turn.  The first 16 columns are
-                // loaded while the item before is still worked on; then they take their places in the image as
-                // they are (their hi and lo terms fill the same 32 bytes), and one short loop converts them: code
-                // that runs once an item comes from L2, at about 150 cycles for eight instructions
-                const int unit = lane & 7, sub = lane >> 3;
-                const uint32_t parity = count & 1, buf = count % C::kQBufs;
-                uint8_t *img = smem + C::OFF_Q + buf * C::kQBytes;
-                uint4 v0[4], v1[4];
-                auto load = [&](int c0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int n = w.col0 + c0 + 4 * i + sub;
-                        v0[i] = v1[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (n < cols) {
-                            const int row = static_cast<int>(n * a.hpg_mul >> 20);
-                            const uint4 *src = reinterpret_cast<const uint4 *>(
-                                a.q + (w.row0 + row) * a.q_stride + static_cast<int64_t>(w.g * hpg + n - row * hpg) * kDim +
-                                unit * 16);
-                            v0[i] = src[0];
-                            v1[i] = src[1];
-                        }
-                    }
-                };
-                load(0);
-                if (!wait_mbar_warp(&q_empty[parity], (count >> 1 & 1) ^ 1, abort) ||
-                    !wait_mbar_warp(&img_empty[buf], (count / C::kQBufs & 1) ^ 1, abort)) {
+                const uint32_t parity = count & 1;
+                // a turn takes four columns, and the loads of the next turn run beside it: code that is not
+                // used all the time comes from L2, at about 150 cycles for eight instructions
+                uint4 v0, v1;
+                if (fresh) load_query(a, w, lane >> 3, cols, hpg, lane, v0, v1);
+                if (!wait_mbar_warp(&q_empty[parity], (count >> 1 & 1) ^ 1, abort)) {
                     gave_up(abort, a.status);
                     go = false;
                     break;
                 }
-                Columns<NC> *cs = cols_s + parity;
-#pragma unroll 1
-                for (int c0 = 0; c0 < NC; c0 += 16) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        *reinterpret_cast<uint4 *>(img + sw128(c0 + 4 * i + sub, unit)) = v0[i];
-                        *reinterpret_cast<uint4 *>(img + sw128(NC + c0 + 4 * i + sub, unit)) = v1[i];
+                if (fresh) {
+                    const uint32_t buf = images % C::kQBufs;
+                    if (!wait_mbar_warp(&img_empty[buf], (images / C::kQBufs & 1) ^ 1, abort)) {
+                        gave_up(abort, a.status);
+                        go = false;
+                        break;
                     }
-                    if (c0 + 16 < NC) load(c0 + 16);
 #pragma unroll 1
-                    for (int n = c0 + sub; n < c0 + 16; n += 4) {
-                        uint4 *hi_at = reinterpret_cast<uint4 *>(img + sw128(n, unit));
-                        uint4 *lo_at = reinterpret_cast<uint4 *>(img + sw128(NC + n, unit));
-                        const uint4 r0 = *hi_at, r1 = *lo_at;
-                        const uint32_t h[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-                        // the column's largest |q| by its bits (an infinity or a NaN is above every number)
-                        uint32_t top = 0;
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) top = max(top, max(h[y] << 16 & 0x7fff0000u, h[y] & 0x7fff0000u));
-#pragma unroll
-                        for (int y = 1; y < 8; y <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
-                        const bool finite = top < 0x7f800000u;
-                        // 2^e brings it to (224, 448]
-                        int e = 0;
-                        if (top > 0 && finite) {
-                            e = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-                            e = max(-120, min(120, e));
-                        }
-                        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const uint2 p0 = split_pair(bf16_lo(h[2 * y]) * up, bf16_hi(h[2 * y]) * up);
-                            const uint2 p1 = split_pair(bf16_lo(h[2 * y + 1]) * up, bf16_hi(h[2 * y + 1]) * up);
-                            hi[y] = p0.x | (p1.x << 16);
-                            lo[y] = p0.y | (p1.y << 16);
-                        }
-                        *hi_at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *lo_at = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        const int col = w.col0 + n, row = col < cols ? static_cast<int>(col * a.hpg_mul >> 20) : 0;
-                        const int ctx = __shfl_sync(0xffffffffu, w.my_ctx, row);
-                        if (unit == 0) {
-                            // a masked score is -inf times the scale: neither zero nor infinity.  A NaN or an infinity
-                            // in q makes its column's scores, and so its output, NaN
-                            const float scale = a.s_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                            cs->scale[n] = finite ? fminf(fmaxf(scale, 1.17549435e-38f), 3.40282347e38f)
-                                                  : __uint_as_float(0x7fc00000u);
-                            cs->ctx[n] = col < cols ? ctx : 0;
-                            cs->at[n] = (w.row0 + row) * a.num_heads + w.g * hpg + (col < cols ? col - row * hpg : 0);
-                        }
+                    for (int n = lane >> 3; n < NC; n += 4) {
+                        const uint4 u0 = v0, u1 = v1;
+                        load_query(a, w, n + 4 < NC ? n + 4 : cols, cols, hpg, lane, v0, v1);
+                        convert_query<NC>(smem + C::OFF_Q + buf * C::kQBytes, cols_s + (images & 1), a, w, n, cols, hpg, u0,
+                                          u1, lane);
                     }
+                    ++images;
                 }
+                // the item after this one: a part more of the same row group and KV head?
+                fresh = !(w.part + 1 < w.parts && w.start + kItemCost + ((w.t_end - w.t_begin + 127) >> 7) < w.end);
                 Item *item = item_s + parity;
                 if (lane < 8) item->ctx[lane] = w.my_ctx;
                 if (lane == 0) {
@@ -397,6 +406,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     item->ctx_min = w.ctx_min;
                     item->ctx_max = w.ctx;
                     item->cols = min(NC, cols - w.col0);
+                    item->image_last = fresh;
                     item->part = w.part;
                     item->parts = w.parts;
                 }
@@ -419,17 +429,20 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
             const uint32_t ua = smem_u32(smem);
             const uint64_t b0 = sdesc_sw128(smem_u32(smem + (values ? C::OFF_P : C::OFF_Q)), 16, 1024);
             const uint32_t step = values ? 256 : 2;
-            uint32_t count = 0, p_phases = 0, o_phase = 1;  // count: tiles
+            uint32_t count = 0, p_phases = 0, o_phase = 1, image = 0;  // count: tiles
             bool ok = true;
             for (uint32_t n = 0; ok; ++n) {
                 ok = wait_mbar(&q_full[n & 1], n >> 1 & 1, abort);
                 if (!ok) break;
                 const Item *item = item_s + (n & 1);
-                const uint64_t bd = values ? b0 : b0 + n % C::kQBufs * (C::kQBytes / 16);
+                const uint32_t buf = image % C::kQBufs;
+                const uint64_t bd = values ? b0 : b0 + buf * (C::kQBytes / 16);
                 if (item->live == 0) break;
                 const int tiles = (item->t_end - item->t_begin + kTile - 1) / kTile;
+                const bool image_last = item->image_last != 0;
                 mbar_arrive(&q_empty[n & 1]);
-                if (!values && tiles == 0) mbar_arrive(&img_empty[n % C::kQBufs]);
+                if (!values && image_last && tiles == 0) mma_commit(&img_empty[buf]);
+                image += image_last;
                 if (values && tiles > 0) {
                     ok = wait_mbar(o_empty, o_phase, abort);
                     o_phase ^= 1;
@@ -467,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                         mma_commit(values ? &pv_done[pb] : &s_full[sb]);
                         if (levels <= 0) break;
                     }
-                    if (!values && ok && i == tiles - 1) mma_commit(&img_empty[n % C::kQBufs]);
+                    if (!values && ok && image_last && i == tiles - 1) mma_commit(&img_empty[buf]);
                 }
             }
             if (!ok) gave_up(abort, a.status);
@@ -492,7 +505,18 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
         float *fac = reinterpret_cast<float *>(smem + C::OFF_FAC) + warp * kMine;
         uint32_t s_count = 0;                   // tiles
         uint32_t pv_open = 0, pv_phases = 0;    // a bit per buffer of P: a product is out whose end has not been seen
+        if (more) {  // the first item's columns, four a warp and turn
+#pragma unroll 1
+            for (int n = 4 * warp + (lane >> 3); n < NC; n += 4 * kSoftmax) {
+                uint4 v0, v1;
+                load_query(a, w, n, cols, hpg, lane, v0, v1);
+                convert_query<NC>(smem + C::OFF_Q, cols_s, a, w, n, cols, hpg, v0, v1, lane);
+            }
+            fence_async_smem();
+            asm volatile("bar.arrive 2, %0;" ::"n"(32 * (kSoftmax + 1)) : "memory");
+        }
         bool dead = false;
+        uint32_t image = 0;
         auto pv_wait = [&](uint32_t b) {
             if (!(pv_open >> b & 1)) return;
             dead |= !wait_mbar_warp(&pv_done[b], pv_phases >> b & 1, abort);
@@ -514,7 +538,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                 someone_dead();
                 break;
             }
-            const Columns<NC> *cs = cols_s + parity;
+            const Columns<NC> *cs = cols_s + (image & 1);
+            image += item->image_last != 0;
             const int t_begin = item->t_begin, t_end = item->t_end, ctx_min = item->ctx_min, ctx_max = item->ctx_max;
             const int ncols = item->cols, part = item->part, parts = item->parts;
             const int tiles = (t_end - t_begin + kTile - 1) / kTile;
@@ -535,25 +560,26 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                 tc_fence_after();
                 const bool edge = t0 + kTile > ctx_min;  // some column does not see all of the tile
 
-                // scores of this token, columns c .. c + 15, in log2 units against their bases
-                auto scores = [&](int c, float *x) {
-                    uint32_t h[16];
-                    tmem_ld16(quad + sb * C::kSN + c, h);
+                // scores of this token in log2 units against their bases
+                auto scores = [&](float (&x)[kMine]) {
+                    uint32_t h[kMine];
                     if constexpr (C::kSN > NC) {
                         uint32_t g[16];
-                        tmem_ld16(quad + sb * C::kSN + NC + c, g);
+                        tmem_ld16(quad + sb * C::kSN, h);
+                        tmem_ld16(quad + sb * C::kSN + NC, g);
                         tmem_ld_wait();
                         reg_fence(h);
                         reg_fence(g);
                         add16(h, g);
                     } else {
+                        tmem_ld32(quad + sb * C::kSN, h);
                         tmem_ld_wait();
                         reg_fence(h);
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 sc = *reinterpret_cast<const float4 *>(cs->scale + mine + c + j);
-                        const float4 nb = *reinterpret_cast<const float4 *>(nbase + c + j);
+                    for (int j = 0; j < kMine; j += 4) {
+                        const float4 sc = *reinterpret_cast<const float4 *>(cs->scale + mine + j);
+                        const float4 nb = *reinterpret_cast<const float4 *>(nbase + j);
                         const float2 p = __ffma2_rn(make_float2(__uint_as_float(h[j]), __uint_as_float(h[j + 1])),
                                                     make_float2(sc.x, sc.y), make_float2(nb.x, nb.y));
                         const float2 q = __ffma2_rn(make_float2(__uint_as_float(h[j + 2]), __uint_as_float(h[j + 3])),
@@ -565,8 +591,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     }
                     if (edge) {
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const int4 n = *reinterpret_cast<const int4 *>(cs->ctx + mine + c + j);
+                        for (int j = 0; j < kMine; j += 4) {
+                            const int4 n = *reinterpret_cast<const int4 *>(cs->ctx + mine + j);
                             if (t >= n.x) x[j] = -INFINITY;
                             if (t >= n.y) x[j + 1] = -INFINITY;
                             if (t >= n.z) x[j + 2] = -INFINITY;
@@ -579,12 +605,9 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
 #pragma unroll 1
                 for (bool settled = false;;) {
                     float top = -INFINITY;
+                    scores(x);
 #pragma unroll
-                    for (int c = 0; c < kMine; c += 16) {
-                        scores(c, x + c);
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) top = fmaxf(top, fmaxf(x[c + j], x[c + j + 1]));
-                    }
+                    for (int j = 0; j < kMine; j += 2) top = fmaxf(top, fmaxf(x[j], x[j + 1]));
                     if (settled || (i > 0 && !meet_any(top > kTop || dead))) break;
                     reduce_columns<kMine, true>(x, max_s + (warp & 3) * kMine, lane);
                     if (i == 0 ? someone_dead() : meet_any(dead)) {
@@ -799,13 +822,9 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
             }
             __syncwarp();
             pv_wait_all();
-            // 16 columns at a time go through P's place (free since the last product), each a row of 128 floats,
-            // so that the lanes write four dims in a row.  A half of the place holds them: one for each of two
-            // warpgroups, or one after the other
+            // thread = dim: a warp's lanes write 32 dims of a column in a row
 #pragma unroll 1
-            for (int c = 0; c < min(ncols, kMine); c += 16) {
-                const int half = C::kGroups == 2 ? warp >> 2 : c >> 4 & 1;
-                float *out_s = reinterpret_cast<float *>(smem + C::OFF_P) + half * 16 * kDim;
+            for (int c = 0; c < min(ncols - mine, kMine); c += 16) {
                 uint32_t h[16];
                 tmem_ld16(quad + C::kTmemO + c, h);
                 if constexpr (C::kON > NC) {
@@ -819,30 +838,16 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     tmem_ld_wait();
                     reg_fence(h);
                 }
-                if (C::kGroups == 2 && c > 0 && someone_dead()) {  // the last columns have left the place
-                    leave = true;
-                    break;
-                }
 #pragma unroll
-                for (int j = 0; j < 16; ++j) out_s[j * kDim + self] = __uint_as_float(h[j]);
-                if (someone_dead()) {
-                    leave = true;
-                    break;
-                }
-#pragma unroll 1
-                for (int n = warp & 3; n < min(16, ncols - mine - c); n += 4) {
-                    const float f = fac[c + n];
-                    float4 o = *reinterpret_cast<const float4 *>(out_s + n * kDim + 4 * lane);
-                    const int64_t at = cs->at[mine + c + n];
-                    if (f == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);  // (without a tile it is no output)
-                    if (parts > 1)
-                        *reinterpret_cast<float4 *>(a.part_o + (at * a.parts_bound + part) * kDim + 4 * lane) = o;
-                    else
-                        *reinterpret_cast<uint2 *>(a.out + at * kDim + 4 * lane) =
-                            make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+                for (int j = 0; j < 16; ++j) {
+                    if (mine + c + j >= ncols) break;
+                    const float f = fac[c + j];
+                    const float o = f == 0.f ? 0.f : __uint_as_float(h[j]) * f;  // (without a tile it is no output)
+                    const int64_t at = cs->at[mine + c + j];
+                    if (parts > 1) a.part_o[(at * a.parts_bound + part) * kDim + self] = o;
+                    else a.out[at * kDim + self] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
                 }
             }
-            if (leave) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
