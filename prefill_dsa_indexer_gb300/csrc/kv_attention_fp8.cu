@@ -149,15 +149,16 @@ __device__ __forceinline__ void reduce_columns(const float *v, float *dst, int l
     }
 }
 
-// h += g, fp32.
+// (h0, h1) += (g0, g1), fp32.
+__device__ __forceinline__ void add_pair(uint32_t &h0, uint32_t &h1, float g0, float g1) {
+    const float2 s = __fadd2_rn(make_float2(__uint_as_float(h0), __uint_as_float(h1)), make_float2(g0, g1));
+    h0 = __float_as_uint(s.x);
+    h1 = __float_as_uint(s.y);
+}
+
 __device__ __forceinline__ void add16(uint32_t (&h)[16], const uint32_t (&g)[16]) {
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-        const float2 s = __fadd2_rn(make_float2(__uint_as_float(h[j]), __uint_as_float(h[j + 1])),
-                                    make_float2(__uint_as_float(g[j]), __uint_as_float(g[j + 1])));
-        h[j] = __float_as_uint(s.x);
-        h[j + 1] = __float_as_uint(s.y);
-    }
+    for (int j = 0; j < 16; j += 2) add_pair(h[j], h[j + 1], __uint_as_float(g[j]), __uint_as_float(g[j + 1]));
 }
 
 // OR of a predicate over the softmax warps (kN threads), who all meet here.
@@ -544,9 +545,17 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
             const int ncols = item->cols, part = item->part, parts = item->parts;
             const int tiles = (t_end - t_begin + kTile - 1) / kTile;
 
-            float l[kMine];  // (kSumsInTmem: 16 at a time)
+            float l[kMine];  // a thread's sums of weights, unless they are in TMEM
 #pragma unroll
             for (int n = 0; n < kMine; ++n) l[n] = 0.f;
+            if constexpr (C::kSumsInTmem) {
+                uint32_t zeros[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) zeros[j] = 0u;
+#pragma unroll
+                for (int c = 0; c < kMine; c += 16) tmem_st16(quad + C::kTmemL + c, zeros);
+                tmem_st_wait();
+            }
 #pragma unroll 1
             for (int n = lane; n < kMine; n += 32) nbase[n] = 0.f;
             __syncwarp();
@@ -654,25 +663,37 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                 // rounded to 4 significant bits, t - (t - p) with t = p (2^20 + 1); lo the rest, exact in fp32
 #pragma unroll
                 for (int c = 0; c < kMine; c += 16) {
-                    float *lc = l + (C::kSumsInTmem ? 0 : c);
-                    uint32_t sums[16];
-                    if (C::kSumsInTmem && i > 0) tmem_ld16(quad + C::kTmemL + c, sums);
+                    if constexpr (C::kSumsInTmem) {
+#pragma unroll
+                        for (int j0 = 0; j0 < 16; j0 += 8) {  // eight at a time, for want of registers
+                            uint32_t sums[8];
+                            tmem_ld8(quad + C::kTmemL + c + j0, sums);
+#pragma unroll
+                            for (int j = j0; j < j0 + 8; ++j) x[c + j] = ex2(x[c + j]);
+                            tmem_ld_wait();
+                            reg_fence(sums);
+#pragma unroll
+                            for (int j = 0; j < 8; j += 2)
+                                add_pair(sums[j], sums[j + 1], x[c + j0 + j], x[c + j0 + j + 1]);
+                            tmem_st8(quad + C::kTmemL + c + j0, sums);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) x[c + j] = ex2(x[c + j]);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 s = __fadd2_rn(make_float2(l[c + j], l[c + j + 1]), make_float2(x[c + j], x[c + j + 1]));
+                            l[c + j] = s.x;
+                            l[c + j + 1] = s.y;
+                        }
+                    }
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
                         float2 h2[2], l2[2];
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            const int k = j + 2 * y;
-                            const float2 p = make_float2(ex2(x[c + k]), ex2(x[c + k + 1]));
-                            if (C::kSumsInTmem) {
-                                x[c + k] = p.x;
-                                x[c + k + 1] = p.y;
-                            } else {
-                                const float2 s = __fadd2_rn(make_float2(lc[k], lc[k + 1]), p);
-                                lc[k] = s.x;
-                                lc[k + 1] = s.y;
-                            }
+                            const float2 p = make_float2(x[c + j + 2 * y], x[c + j + 2 * y + 1]);
                             const float2 tt = __fmul2_rn(p, make_float2(1048577.f, 1048577.f));
                             const float2 minus = make_float2(-1.f, -1.f);
                             h2[y] = __ffma2_rn(__ffma2_rn(p, minus, tt), minus, tt);
@@ -684,20 +705,6 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     const int at = 2 * NC * pb + mine + c;
                     *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, at / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, (NC + at) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    if (C::kSumsInTmem) {
-                        if (i > 0) {
-                            tmem_ld_wait();
-                            reg_fence(sums);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) sums[j] = 0u;
-                        }
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(x[c + j]);
-                        add16(sums, w);
-                        tmem_st16(quad + C::kTmemL + c, sums);
-                    }
                 }
                 if (C::kSumsInTmem) tmem_st_wait();
                 auto hand_over = [&]() {
@@ -793,7 +800,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
 
             // ---- the item's sums and output
             float *sums = sum_s + parity * 4 * NC + 4 * mine;
-            if (C::kSumsInTmem && tiles > 0) {
+            if (C::kSumsInTmem) {
 #pragma unroll
                 for (int c = 0; c < kMine; c += 16) {
                     uint32_t h[16];
