@@ -508,7 +508,8 @@ def _expect(t, what, device, dtypes, shape=None):
 
 def _flat(t, what, device, dtypes, shape=None):
     """_expect of a contiguous tensor; its address."""
-    _expect(t, what, device, dtypes, shape)
+    if t.get_device() != device or t.dtype not in dtypes or (shape is not None and t.shape != shape):
+        _expect(t, what, device, dtypes, shape)
     if not t.is_contiguous():
         raise DsaError(f"{what} is not contiguous")
     return t.data_ptr()
@@ -516,8 +517,8 @@ def _flat(t, what, device, dtypes, shape=None):
 
 def _launch(what, device, stream, *args):
     """The library's `what`(*args, stream) on device `device`, whichever is current."""
-    fn = _packed_function(what)
-    if device == torch.cuda.current_device():
+    fn = _packed.get(what) or _packed_function(what)
+    if device == torch._C._cuda_getDevice():  # (a tensor of the call is on a device: CUDA is initialised)
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(device):
@@ -593,23 +594,25 @@ def _rope_spec(table, positions, device, num_tokens):
                            table.scale)
 
 
-def _rope_tensor(x, out, layout, rot_dim, device, dtypes, num_tokens):
+def _rope_tensor(x, out, layout, rot_dim, device, dtype, num_tokens):
     """The fields of a dsa_rope_tensor."""
     shape = x.shape
     if len(shape) != 3 or shape[2] != rot_dim or shape[0] != num_tokens:
         raise DsaError(f"rotated tensors are [{num_tokens}, heads, {rot_dim}] (a slice of larger heads): got {tuple(shape)}")
-    _expect(x, "x", device, dtypes)
+    if x.dtype is not dtype or x.get_device() != device:
+        _expect(x, "x", device, (dtype,))
     a, b, c = x.stride()
+    p = x.data_ptr()
     if out is x:
-        p = x.data_ptr()
         if c != 1:
             raise DsaError("the rotary dims of a head are contiguous")
         return p, p, shape[1], layout, a, b, a, b
-    _expect(out, "out", device, dtypes, shape)
+    if out.dtype is not dtype or out.shape != shape or out.get_device() != device:
+        _expect(out, "out", device, (dtype,), shape)
     d, e, f = out.stride()
     if c != 1 or f != 1:
         raise DsaError("the rotary dims of a head are contiguous")
-    return x.data_ptr(), out.data_ptr(), shape[1], layout, a, b, d, e
+    return p, out.data_ptr(), shape[1], layout, a, b, d, e
 
 
 def rope(x, table, positions, layout=ROPE_INTERLEAVED, out=None, stream=None):
@@ -626,9 +629,9 @@ def rope(x, table, positions, layout=ROPE_INTERLEAVED, out=None, stream=None):
     n, device, dtype = first.shape[0], _device(first), first.dtype
     if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise DsaError(f"rope takes bf16 or fp32 tensors: got {dtype}")
-    fields = []
+    fields, rot = [], table.rot_dim
     for a, b, p in zip(xs, outs, layouts):
-        fields += _rope_tensor(a, b, p, table.rot_dim, device, (dtype,), n)
+        fields += _rope_tensor(a, b, p, rot, device, dtype, n)
     _launch("dsa_rope", device, stream, _rope_spec(table, positions, device, n), _PACK_ROPE_TENSORS[len(xs)](*fields),
             len(xs), DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_FP32, n)
     return outs if many else outs[0]
@@ -658,13 +661,15 @@ def kv_insert(kv, slots, k, v, rope=None, positions=None, layout=ROPE_HALF, rot_
     rotated first, and q [tokens, heads, rot_dim] too, into q_out (default: in place).  Returns q_out."""
     n, device, heads, dim = slots.shape[0], kv.device, kv.kv_heads, kv.head_dim
     shape, width = (n, heads, dim), heads * dim
-    strides = []
     for t, what in ((k, "k"), (v, "v")):
-        _expect(t, what, device, _BF16, shape)
-        a, b, c = t.stride()
-        if c != 1 or (b != dim and heads > 1):
-            raise DsaError(f"the heads of a token of {what} are packed")
-        strides.append(a if n > 1 else max(a, width))
+        if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != device:
+            _expect(t, what, device, _BF16, shape)
+    k_stride, b, c = k.stride()
+    v_stride, d, e = v.stride()
+    if c != 1 or e != 1 or (heads > 1 and (b != dim or d != dim)):
+        raise DsaError(f"the heads of a token of {'k' if c != 1 or (heads > 1 and b != dim) else 'v'} are packed")
+    if n == 1:
+        k_stride, v_stride = max(k_stride, width), max(v_stride, width)
     spec = qt = None
     if rope is not None:
         if positions is None:
@@ -672,11 +677,11 @@ def kv_insert(kv, slots, k, v, rope=None, positions=None, layout=ROPE_HALF, rot_
         spec = _rope_spec(rope, positions, device, n)
         if q is not None:
             q_out = q if q_out is None else q_out
-            qt = _PACK_ROPE_TENSORS[1](*_rope_tensor(q, q_out, layout, rope.rot_dim, device, _BF16, n))
+            qt = _PACK_ROPE_TENSORS[1](*_rope_tensor(q, q_out, layout, rope.rot_dim, device, torch.bfloat16, n))
     elif q is not None:
         raise DsaError("q is rotated only: it needs rope")
     _launch("dsa_kv_insert", device, stream, kv._packed, _flat(slots, "slots", device, _I32), n,
-            _PACK_KV_ROWS(k.data_ptr(), v.data_ptr(), strides[0], strides[1], rot_offset, layout), spec, qt,
+            _PACK_KV_ROWS(k.data_ptr(), v.data_ptr(), k_stride, v_stride, rot_offset, layout), spec, qt,
             None if status is None else _flat(status, "status", device, _I32))
     return q_out
 
@@ -691,7 +696,8 @@ def kv_attention(kv, block_table, row_req, row_ctx, max_ctx, q, sm_scale=None, r
     over the KvCache's tokens below row_ctx; sm_scale defaults to 1 / sqrt(head_dim)."""
     R, H, D = q.shape
     device = kv.device
-    _expect(q, "q", device, _BF16, (R, H, kv.head_dim))
+    if D != kv.head_dim or q.dtype is not torch.bfloat16 or q.get_device() != device:
+        _expect(q, "q", device, _BF16, (R, H, kv.head_dim))
     a, b, c = q.stride()
     if c != 1 or (b != D and H > 1):
         raise DsaError("the heads of a row of q are packed")
