@@ -757,8 +757,7 @@ size_t dsa_kv_attention_workspace_size(const dsa_kv_cache *cache, int32_t num_ro
                                        int32_t max_ctx) {
     if (check_kv_cache(cache) != DSA_OK || num_rows <= 0 || num_heads <= 0 || max_ctx <= 0) return 0;
     if (max_ctx > DSA_KV_MAX_CTX) return 0;
-    return kv_attention_workspace_bytes(num_rows, num_heads, cache->kv_heads, cache->head_dim, max_ctx,
-                                        cache->format == DSA_KV_FP8);
+    return kv_attention_workspace_bytes(num_rows, num_heads, cache->kv_heads, cache->head_dim, max_ctx);
 }
 
 int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint16_t *q, int64_t q_stride,
@@ -780,7 +779,7 @@ int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint
     const int64_t need_pages = (static_cast<int64_t>(rows->max_ctx) + cache->page_size - 1) / cache->page_size;
     if (rows->bt_stride < need_pages) return DSA_ERR_INVALID_ARG;
     const size_t need = kv_attention_workspace_bytes(rows->num_rows, num_heads, cache->kv_heads, cache->head_dim,
-                                                     rows->max_ctx, cache->format == DSA_KV_FP8);
+                                                     rows->max_ctx);
     if (need > 0) {
         if (workspace == nullptr || workspace_bytes < need) return DSA_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return DSA_ERR_INVALID_ARG;

@@ -338,6 +338,7 @@ struct KvAttnArgs {
     uint32_t parts_bound;  // parts of a row at most, for contexts up to max_ctx
     uint32_t col_blocks;   // items side by side over the columns (group x query heads per KV head)
     uint32_t items;       // (row group, KV head, column block, part)
+    uint64_t ctas_inv;          // 2^64 / CTAs of the launch, rounded up
     float *part_o;        // [R, H, parts_bound, D] the parts' outputs, in their own bases
     float2 *part_ml;      // [R, H, parts_bound] their bases (log2 units) and sums
 };
@@ -351,7 +352,7 @@ cudaError_t launch_kv_attention_fp8(KvAttnArgs &a, cudaStream_t s);
 // span of 64 or 128 bytes (api.cu).
 bool encode_kv_rows_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t row_bytes, uint32_t box_rows);
 size_t kv_attention_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
-                                    int32_t max_ctx, bool fp8);
+                                    int32_t max_ctx);
 
 int device_sm_count();
 

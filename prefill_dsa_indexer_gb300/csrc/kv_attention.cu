@@ -52,7 +52,7 @@ constexpr float kBias = 7.0f;                     // ... and a moved base leaves
 
 // Bound of kv_parts over every context up to max_ctx.
 uint32_t kv_parts_bound(int32_t max_ctx, int32_t parts_shift) {
-    const int64_t n = (static_cast<int64_t>(max_ctx) + 127) / 128, most = 1ll << parts_shift;
+    const int64_t n = (static_cast<int64_t>(max_ctx) + (1 << kPartMin) - 1) >> kPartMin, most = 1ll << parts_shift;
     return static_cast<uint32_t>(n < 1 ? 1 : (n < most ? n : most));
 }
 
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // Merge of a row's parts: one CTA per (row, head).  128 / (D / 4) groups of lanes take every so manyth part,
 // four dims to a lane; the groups' sums are added in order.
-constexpr int kCombineThreads = 128, kCombineParts = 256;
+constexpr int kCombineThreads = 128, kCombineParts = 128;
 
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const __grid_constant__ KvAttnArgs a) {
@@ -701,13 +701,15 @@ __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const __gri
     __shared__ float2 ml_s[kCombineParts];
     __shared__ float4 x_s[kGroups][kLanes];
     __shared__ float t_s[kGroups];
-    pdl_wait();
-    pdl_launch_dependents();
+    // The attention kernel lets this one start after its own wait, so what ran before it is complete: the
+    // contexts can be read before this kernel's wait, which is for the parts.
     const int64_t at = blockIdx.x;
     const int row0 = static_cast<int>(at / a.num_heads) / a.group * a.group;
     int ctx = 0;
     for (int i = 0; i < a.group; ++i) ctx = max(ctx, min(a.row_ctx[row0 + i], a.max_ctx));
     const int parts = kv_parts(ctx, kv_part_shift(ctx, a.parts_shift));
+    pdl_wait();
+    pdl_launch_dependents();
     if (parts == 1) return;  // written by the attention kernel
     const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes;
     const float4 *po = reinterpret_cast<const float4 *>(a.part_o + at * a.parts_bound * D) + d;
@@ -763,7 +765,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const __gri
 }
 
 template <bool kFp8, int D, bool kWide, int kColWarps>
-cudaError_t launch_variant(const KvAttnArgs &a, cudaStream_t s) {
+cudaError_t launch_variant(KvAttnArgs &a, cudaStream_t s) {
     using C = KvCfg<kFp8, D, kColWarps>;
     auto kern = kv_attention_kernel<kFp8, D, kWide, kColWarps>;
     static std::atomic<uint64_t> configured{0};
@@ -794,8 +796,8 @@ cudaError_t launch_format(KvAttnArgs &a, cudaStream_t s) {
 }  // namespace
 
 size_t kv_attention_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
-                                    int32_t max_ctx, bool fp8) {
-    const size_t parts = static_cast<size_t>(kv_parts_bound(max_ctx, kv_parts_shift(kv_heads, fp8 && head_dim == 128)));
+                                    int32_t max_ctx) {
+    const size_t parts = static_cast<size_t>(kv_parts_bound(max_ctx, kv_parts_shift(kv_heads)));
     if (parts <= 1) return 0;
     const size_t n = static_cast<size_t>(num_rows) * static_cast<size_t>(num_heads) * parts;
     return align256(n * static_cast<size_t>(head_dim) * 4) + align256(n * 8);
@@ -806,7 +808,7 @@ cudaError_t launch_kv_attention(KvAttnArgs &a, void *workspace, cudaStream_t s) 
     for (a.page_shift = 4; 1 << a.page_shift < a.page_size;) ++a.page_shift;
     const uint32_t hpg = static_cast<uint32_t>(a.num_heads / a.kv_heads);
     a.hpg_mul = ((1u << 20) + hpg - 1) / hpg;
-    a.parts_shift = kv_parts_shift(a.kv_heads, a.fp8 && a.head_dim == 128);
+    a.parts_shift = kv_parts_shift(a.kv_heads);
     a.parts_bound = kv_parts_bound(a.max_ctx, a.parts_shift);
     const size_t n = static_cast<size_t>(a.num_rows) * static_cast<size_t>(a.num_heads) * a.parts_bound;
     a.part_o = static_cast<float *>(workspace);

@@ -12,18 +12,27 @@
 namespace dsa {
 namespace kv {
 
-// Parts of a context: of 128 tokens, doubled until at most 2^parts_shift cover it.  All KV heads of one request
-// make 256 parts in the warp-level kernel, so that it alone fills the 152 SMs, and 128 in the FP8 kernel of
-// head_dim 128, whose parts cost more beside their tiles (32 x 16K-64K: 229 us with 128, 280 us with 256; for
-// the other kernel 8 x 128K bf16 took 331 and 318 us); but at least 32 and 16 of a head.
-__host__ __device__ __forceinline__ int32_t kv_parts_shift(int32_t kv_heads, bool fp8_kernel) {
-    const int32_t most = fp8_kernel ? 7 : 8;
-    return kv_heads >= 8 ? most - 3 : kv_heads >= 4 ? most - 2 : kv_heads >= 2 ? most - 1 : most;
+// Parts of a context: of 2^kPartMin tokens, doubled until at most 2^parts_shift cover it.  All KV heads of one
+// request make 128 parts, but at least 16 of a head: fewer leave SMs idle under one request, and every part costs
+// its queries, its first base and its output beside its tiles.  Measured (4 KV heads of 128):
+//                                        64 parts   128 parts   256 parts
+//   bf16, 1 x 128K (40 us of bytes)        64.6        43.2        43.3 us
+//   bf16, 4 x 32K                          42.7        45.6        48.6
+//   FP8, 1 x 128K (20 us)                  61.4        35.4        28.2
+//   FP8, 24 x 8K (30 us)                   46.9        55.4        77.9
+//   parts of at least                     128 tokens  256         512
+//   bf16, one row of 4K                    10.0         9.6        11.0 us
+//   FP8, 24 x 2K (7.6 us)                  27.2        21.6        21.4
+//   FP8, 1 x 2K, 64 columns                12.8        13.8        17.7
+constexpr int32_t kPartMin = 8;
+
+__host__ __device__ __forceinline__ int32_t kv_parts_shift(int32_t kv_heads) {
+    return kv_heads >= 8 ? 4 : kv_heads >= 4 ? 5 : kv_heads >= 2 ? 6 : 7;
 }
 
-// log2 of a part's tokens: the smallest k >= 7 with 2^(k + parts_shift) >= ctx.
+// log2 of a part's tokens: the smallest k >= kPartMin with 2^(k + parts_shift) >= ctx.
 __device__ __forceinline__ int32_t kv_part_shift(int32_t ctx, int32_t parts_shift) {
-    return 7 + (32 - __clz(max(ctx - 1, 0) >> (7 + parts_shift)));
+    return kPartMin + (32 - __clz(max(ctx - 1, 0) >> (kPartMin + parts_shift)));
 }
 
 __device__ __forceinline__ int32_t kv_parts(int32_t ctx, int32_t part_shift) {
@@ -47,6 +56,7 @@ static_assert(sizeof(KvItem) == 64, "item layout");
 // total cost: equal shares whatever the contexts (32 rows of 16K to 64K tokens: the busiest CTA has 1.04 times
 // the mean; with items dealt in turn it had 1.28 to 1.44 times).  A share is one run of neighbours.
 constexpr uint32_t kItemCost = 2;
+constexpr int kMaxGroup = 8;        // rows of a group
 constexpr int kSchedEntries = 512;  // running costs kept in shared memory, one for every so many groups
 
 struct KvSchedule {
@@ -69,14 +79,21 @@ __device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule
         uint64_t sum = 0;
 #pragma unroll 1
         for (int gi = e * per; gi < min(groups, (e + 1) * per); ++gi) {
-            const int row0 = gi * a.group, req = a.row_req[row0];
-            bool bad = req < 0 || req >= a.num_requests;
+            // (all loads first: one latency)
+            const int row0 = gi * a.group;
+            int n[kMaxGroup], req[kMaxGroup];
+#pragma unroll
+            for (int r = 0; r < kMaxGroup; ++r) {
+                const int row = row0 + (r < a.group ? r : 0);
+                n[r] = a.row_ctx[row];
+                req[r] = a.row_req[row];
+            }
+            bool bad = req[0] < 0 || req[0] >= a.num_requests;
             int ctx = 0;
-#pragma unroll 1
-            for (int r = row0; r < row0 + a.group; ++r) {
-                const int n = a.row_ctx[r];
-                bad |= n < 0 || n > a.max_ctx || a.row_req[r] != req;
-                ctx = max(ctx, n);
+#pragma unroll
+            for (int r = 0; r < kMaxGroup; ++r) {
+                bad |= n[r] < 0 || n[r] > a.max_ctx || req[r] != req[0];
+                ctx = max(ctx, n[r]);
             }
             sum += kv_cost(bad ? 0 : ctx, a.parts_shift);
         }
@@ -150,16 +167,16 @@ struct KvCursor {
             return part < parts;
         }
         const int per = (groups + kSchedEntries - 1) / kSchedEntries, entries = (groups + per - 1) / per;
+        // total * b / n: exact for products below 2^64 / n, and no total is near (a token costs 2^-6 or less)
         const uint64_t total = sched->before[entries];
-        const uint64_t from = total * blockIdx.x / gridDim.x;
-        end = total * (blockIdx.x + 1) / gridDim.x;
-        int lo = 0, hi = entries - 1;  // the last entry with nothing of the share before it
+        const uint64_t from = __umul64hi(total * blockIdx.x, a.ctas_inv);
+        end = __umul64hi(total * (blockIdx.x + 1), a.ctas_inv);
+        if (from >= end) return false;
+        int lo = 0;  // the last entry with nothing of the share before it
 #pragma unroll 1
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (sched->before[mid] <= from) lo = mid;
-            else hi = mid - 1;
-        }
+        for (int e = lane; e < entries; e += 32)
+            if (sched->before[e] <= from) lo = e;
+        lo = __reduce_max_sync(0xffffffffu, lo);
         start = sched->before[lo];
         group = lo * per;
         uint32_t unit;  // cost of a KV head and column block
@@ -174,8 +191,10 @@ struct KvCursor {
         // the first item that starts at or past `from`
         uint64_t left = from - start;
         head = 0;
-        if (left >= unit) {
-            head = static_cast<int>(left / unit);
+        if (left >= unit) {  // (the quotient is below heads, so fp32 misses it by one at most)
+            head = static_cast<int>(__ull2float_rz(left) / static_cast<float>(unit));
+            head -= static_cast<uint64_t>(head) * unit > left;
+            head += static_cast<uint64_t>(head + 1) * unit <= left;
             left -= static_cast<uint64_t>(head) * unit;
         }
         start = from - left;
@@ -269,9 +288,10 @@ inline cudaError_t raise_smem_limit(K kern, int bytes, std::atomic<uint64_t> &co
 }
 
 // CTAs of a persistent launch over a.items items, two per SM; 0: no device.
-inline uint32_t persistent_ctas(const KvAttnArgs &a) {
-    const uint32_t ctas = 2u * static_cast<uint32_t>(device_sm_count());
-    return a.items < ctas ? a.items : ctas;
+inline uint32_t persistent_ctas(KvAttnArgs &a) {
+    const uint32_t most = 2u * static_cast<uint32_t>(device_sm_count()), ctas = a.items < most ? a.items : most;
+    if (ctas > 0) a.ctas_inv = ~0ull / ctas + 1;
+    return ctas;
 }
 
 }  // namespace kv
