@@ -105,9 +105,9 @@ struct Cfg {
     static_assert(kSmemBytes <= 115712, "two CTAs per SM");
 };
 
-// Sums (or maxima) over the warp's lanes of v[0..N): afterwards v[0] of lane l belongs to column
+// Sums over the warp's lanes of v[0..N): afterwards v[0] of lane l belongs to column
 // lane_column<N>(l).  Halves of the columns change hands, so N columns take N shuffles (N = 16: 16, 32: 31).
-template <int N, bool kMax>
+template <int N>
 __device__ __forceinline__ void reduce_lanes(float (&v)[N], int lane) {
     int n = N;
 #pragma unroll
@@ -118,13 +118,10 @@ __device__ __forceinline__ void reduce_lanes(float (&v)[N], int lane) {
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) {
                 if (i >= n) break;
-                const float keep = up ? v[i + n] : v[i];
-                const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + n], off);
-                v[i] = kMax ? fmaxf(keep, got) : keep + got;
+                v[i] = (up ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + n], off);
             }
         } else {
-            const float got = __shfl_xor_sync(0xffffffffu, v[0], off);
-            v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
         }
     }
 }
@@ -135,17 +132,23 @@ __device__ __forceinline__ int lane_column(int lane) {
     return N == 32 ? lane : lane >> 1;
 }
 
-// The columns' sums or maxima over the warp's tokens into dst[0..NC).
-template <int NC, bool kMax>
-__device__ __forceinline__ void reduce_columns(const float *v, float *dst, int lane) {
-    constexpr int kN = NC < 32 ? NC : 32;
+// The columns' sums over the warp's tokens into dst[0..N).
+template <int N>
+__device__ __forceinline__ void reduce_columns(float (&v)[N], float *dst, int lane) {
+    reduce_lanes<N>(v, lane);
+    if (N == 32 || (lane & 1) == 0) dst[lane_column<N>(lane)] = v[0];
+}
+
+// The columns' maxima over the warp's tokens into dst[0..N); a NaN is passed over.
+template <int N>
+__device__ __forceinline__ void max_columns(const float (&v)[N], float *dst, int lane) {
 #pragma unroll
-    for (int c = 0; c < NC; c += kN) {
-        float w[kN];
+    for (int j = 0; j < N; j += 4) {
+        float m[4];
 #pragma unroll
-        for (int j = 0; j < kN; ++j) w[j] = v[c + j];
-        reduce_lanes<kN, kMax>(w, lane);
-        if (kN == 32 || (lane & 1) == 0) dst[c + lane_column<kN>(lane)] = w[0];
+        for (int k = 0; k < 4; ++k)
+            asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m[k]) : "f"(v[j + k]));
+        if (lane == 0) *reinterpret_cast<float4 *>(dst + j) = make_float4(m[0], m[1], m[2], m[3]);
     }
 }
 
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
 #pragma unroll
                     for (int j = 0; j < kMine; j += 2) top = fmaxf(top, fmaxf(x[j], x[j + 1]));
                     if (settled || (i > 0 && !meet_any(top > kTop || dead))) break;
-                    reduce_columns<kMine, true>(x, max_s + (warp & 3) * kMine, lane);
+                    max_columns<kMine>(x, max_s + (warp & 3) * kMine, lane);
                     if (i == 0 ? someone_dead() : meet_any(dead)) {
                         leave = true;
                         break;
@@ -811,7 +814,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     for (int j = 0; j < 16; ++j) l[c + j] = __uint_as_float(h[j]);
                 }
             }
-            reduce_columns<kMine, false>(l, sums + (warp & 3) * kMine, lane);
+            reduce_columns<kMine>(l, sums + (warp & 3) * kMine, lane);
             if (someone_dead()) break;
             // a column's factor: 1 for a part of several, else 1 / its sum (0 without any weight)
 #pragma unroll 1
