@@ -528,7 +528,7 @@ typedef struct dsa_rope_tensor {
  * t = positions[n] * inv_freq_i:
  *   out_a = scale (a cos t - b sin t),  out_b = scale (a sin t + b cos t)
  * in fp32, rounded once to dtype (of every tensor).  Elements outside the rotary part are neither
- * read nor written, nor is a token at a negative position (padding).  tensors: host array.
+ * read nor written; a token at a negative position (padding) is not written.  tensors: host array.
  */
 int dsa_rope(const dsa_rope_spec *rope, const dsa_rope_tensor *tensors, int32_t num_tensors, int32_t dtype,
              int32_t num_tokens, void *stream);

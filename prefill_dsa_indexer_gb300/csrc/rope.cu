@@ -12,10 +12,12 @@
 // Both kernels move each byte once and do little with it: they are bound by the memory, and by latency for the
 // few tokens of a decode step.  One CTA takes a tile of tokens of one tensor (or a range of one token's heads):
 // it computes the tile's cos and sin once per (token, pair) into shared memory; then every thread keeps one
-// 16-byte piece of a head and walks over the tile's heads and tokens with it, four pieces in flight, so that the
-// walk has no division and the angles' place changes with the token alone.  8,192 tokens x 98 heads x 64 dims:
-// 43 us (4.8 TB/s); 8,192 tokens into an FP8 pool of 4 KV heads of 128 with 64 query heads rotated: 64 us
-// (4.6 TB/s).  CTAs of 256 threads: 45 and 66 us.
+// 16-byte piece of a head and walks over the tile's heads and tokens with it, so that the walk has no division and
+// the angles' place changes with the token alone.  What it takes is bytes in flight: a thread's next pieces come by
+// asynchronous copies into 128 bytes of its own in shared memory (with four 16-byte loads in registers instead, the
+// prefills below took 43 and 64.5 us; rings of 96 and 192 bytes 34.9 and 51.0, 40.3 and 51.0 us).
+// 8,192 tokens x 98 heads x 64 dims: 36.6 us (5.6 TB/s); 8,192 tokens into an FP8 pool of 4 KV heads of 128 with
+// 64 query heads rotated: 48.5 us (6.1 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -29,6 +31,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kTileTokens = 64;                               // most tokens of a tile
 constexpr int kTabPairs = 2048;                               // (token, pair) entries of a tile's table
+constexpr int kRingBytes = 128;                               // of a thread: its pieces in flight
 constexpr int kMaxSegs = DSA_ROPE_MAX_TENSORS + 1;
 
 // A run of CTAs that share one tensor: tiles of `tokens` tokens by `heads` heads.
@@ -95,8 +98,13 @@ struct alignas(V * sizeof(T)) Piece {
     T e[V];
 };
 
-// cos and sin of the tile's tokens, times the scale: tab[token in tile][pair].  pos_s: the tile's positions.
-__device__ __forceinline__ void fill_table(const RopeArgs &a, float2 *tab, int32_t *pos_s, int t0, int nt) {
+// cos and sin of the tile's tokens, times the scale: [token in tile][pair].
+struct Table {
+    alignas(16) float cos[kTabPairs], sin[kTabPairs];
+};
+
+// pos_s: the tile's positions.
+__device__ __forceinline__ void fill_table(const RopeArgs &a, Table &tab, int32_t *pos_s, int t0, int nt) {
     const int pairs = a.rot >> 1;
     if (static_cast<int>(threadIdx.x) < nt) pos_s[threadIdx.x] = a.positions[t0 + threadIdx.x];
     for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
@@ -106,91 +114,172 @@ __device__ __forceinline__ void fill_table(const RopeArgs &a, float2 *tab, int32
         const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
         float sn, cs;
         sincospif(half_turns, &sn, &cs);
-        tab[i] = make_float2(cs * a.scale, sn * a.scale);
+        tab.cos[i] = cs * a.scale;
+        tab.sin[i] = sn * a.scale;
     }
 }
 
-// Rotate the tile's pieces: V elements (V / 2 pairs) of an interleaved head, or V elements of each
-// half of a half-split head.  V = 1 (half) and 2 (interleaved) are the forms for any alignment.
+// N angles from a multiple of N floats.
+template <int N>
+__device__ __forceinline__ void load_angles(const float *p, float (&v)[N]) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(v + i) = *reinterpret_cast<const float4 *>(p + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = p[i];
+    }
+}
+
+// (u, v) becomes (u c - v s, u s + v c): two pairs at a time in packed fp32 where there are two.
+template <int N>
+__device__ __forceinline__ void turn(float (&u)[N], float (&v)[N], const float (&c)[N], const float (&s)[N]) {
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const float2 u2 = make_float2(u[e], u[e + 1]), v2 = make_float2(v[e], v[e + 1]);
+            const float2 c2 = make_float2(c[e], c[e + 1]), s2 = make_float2(s[e], s[e + 1]);
+            const float2 a = __ffma2_rn(v2, make_float2(-s2.x, -s2.y), __fmul2_rn(u2, c2));
+            const float2 b = __ffma2_rn(v2, c2, __fmul2_rn(u2, s2));
+            u[e] = a.x;
+            u[e + 1] = a.y;
+            v[e] = b.x;
+            v[e + 1] = b.y;
+        }
+    } else {
+        const float a = fmaf(v[0], -s[0], u[0] * c[0]);
+        v[0] = fmaf(v[0], c[0], u[0] * s[0]);
+        u[0] = a;
+    }
+}
+
+// A piece of a head: V elements (V / 2 pairs) of an interleaved one, or V elements of each half of a half-split
+// one.  V = 1 (half) and 2 (interleaved) are the forms for any alignment.
 template <typename T, bool kHalf, int V>
-__device__ __forceinline__ void rotate_tile(const RopeArgs &a, const RopeTensor &x, const float2 *tab,
-                                            const int32_t *pos_s, int t0, int nt, int h0, int nh, int units) {
+struct HeadPiece {
+    static constexpr int kPairs = kHalf ? V : V / 2;
+    static constexpr bool kWide = kHalf || V * sizeof(T) >= 16;
     using P = Piece<T, V>;
-    constexpr int kUnroll = V * sizeof(T) < 16 ? 1 : kHalf ? 2 : 4;  // four 16-byte loads in flight
-    constexpr int kPairs = kHalf ? V : V / 2;  // pairs of a piece
+    P lo, hi;
+    __device__ __forceinline__ void load(const T *p, int pairs) {
+        if constexpr (kWide) {
+            lo = *reinterpret_cast<const P *>(p);
+            if (kHalf) hi = *reinterpret_cast<const P *>(p + pairs);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) lo.e[e] = p[e];
+        }
+    }
+    __device__ __forceinline__ void rotate(const float (&c)[kPairs], const float (&s)[kPairs]) {
+        float u[kPairs], v[kPairs];
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+            u[e] = to_f32(lo.e[kHalf ? e : 2 * e]);
+            v[e] = to_f32(kHalf ? hi.e[e] : lo.e[2 * e + 1]);
+        }
+        turn<kPairs>(u, v, c, s);
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+            lo.e[kHalf ? e : 2 * e] = from_f32<T>(u[e]);
+            (kHalf ? hi.e[e] : lo.e[2 * e + 1]) = from_f32<T>(v[e]);
+        }
+    }
+    __device__ __forceinline__ void store(T *p, int pairs) const {
+        if constexpr (kWide) {
+            *reinterpret_cast<P *>(p) = lo;
+            if (kHalf) *reinterpret_cast<P *>(p + pairs) = hi;
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) p[e] = lo.e[e];
+        }
+    }
+};
+
+// 16 bytes to shared memory while the thread goes on.  Its own wait makes them visible to it.
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rotate the tile's pieces.  The 16-byte forms pass through a ring of the thread's own in shared memory, so that
+// several are in flight while one is worked on, the first ones while the table is made.
+template <typename T, bool kHalf, int V>
+__device__ __forceinline__ void rotate_tile(const RopeArgs &a, const RopeTensor &x, Table &tab, int32_t *pos_s,
+                                            uint8_t *ring, int t0, int nt, int h0, int nh, int units) {
+    using H = HeadPiece<T, kHalf, V>;
     const int pairs = a.rot >> 1;
     Walk w(units, nt, nh);
     const T *src = static_cast<const T *>(x.x) + t0 * x.x_token + h0 * x.x_head + w.unit * V;
     T *dst = static_cast<T *>(x.out) + t0 * x.out_token + h0 * x.out_head + w.unit * V;
-    tab += w.unit * kPairs;
-    while (w.tok < nt) {
-        P lo[kUnroll], hi[kUnroll];
-        int tok[kUnroll], h[kUnroll];
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            tok[k] = w.tok;
-            h[k] = w.h;
-            if (w.tok < nt && pos_s[w.tok] < 0) tok[k] = nt;  // a padding token
-            if (tok[k] < nt) {
-                const T *p = src + tok[k] * x.x_token + h[k] * x.x_head;
-                if constexpr (V * sizeof(T) >= 16 || kHalf) {
-                    lo[k] = *reinterpret_cast<const P *>(p);
-                    if (kHalf) hi[k] = *reinterpret_cast<const P *>(p + pairs);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) lo[k].e[e] = p[e];
-                }
-            }
-            w.step(nh);
+    const int unit = w.unit * H::kPairs;
+    auto finish = [&](H &piece, int tok, int h) {
+        float c[H::kPairs], s[H::kPairs];
+        load_angles<H::kPairs>(tab.cos + tok * pairs + unit, c);
+        load_angles<H::kPairs>(tab.sin + tok * pairs + unit, s);
+        piece.rotate(c, s);
+        piece.store(dst + tok * x.out_token + h * x.out_head, pairs);
+    };
+    if constexpr (V * sizeof(T) < 16) {
+        fill_table(a, tab, pos_s, t0, nt);
+        __syncthreads();
+        for (; w.tok < nt; w.step(nh)) {
+            if (pos_s[w.tok] < 0) continue;  // a padding token
+            H piece;
+            piece.load(src + w.tok * x.x_token + w.h * x.x_head, pairs);
+            finish(piece, w.tok, w.h);
         }
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            if (tok[k] >= nt) continue;
-            const float2 *cs = tab + tok[k] * pairs;
-            T *p = dst + tok[k] * x.out_token + h[k] * x.out_head;
-            if constexpr (kHalf) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float u = to_f32(lo[k].e[e]), v = to_f32(hi[k].e[e]);
-                    lo[k].e[e] = from_f32<T>(u * cs[e].x - v * cs[e].y);
-                    hi[k].e[e] = from_f32<T>(u * cs[e].y + v * cs[e].x);
-                }
-                *reinterpret_cast<P *>(p) = lo[k];
-                *reinterpret_cast<P *>(p + pairs) = hi[k];
-            } else {
-#pragma unroll
-                for (int e = 0; e < V / 2; ++e) {
-                    const float u = to_f32(lo[k].e[2 * e]), v = to_f32(lo[k].e[2 * e + 1]);
-                    lo[k].e[2 * e] = from_f32<T>(u * cs[e].x - v * cs[e].y);
-                    lo[k].e[2 * e + 1] = from_f32<T>(u * cs[e].y + v * cs[e].x);
-                }
-                if constexpr (V * sizeof(T) >= 16) {
-                    *reinterpret_cast<P *>(p) = lo[k];
-                } else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) p[e] = lo[k].e[e];
-                }
+    } else {
+        constexpr int kBytes = kHalf ? 32 : 16, kDepth = kRingBytes / kBytes;
+        Walk ahead = w;
+        uint32_t in = 0, out = 0;  // places in the ring
+        auto start = [&]() {
+            if (ahead.tok < nt) {
+                const T *p = src + ahead.tok * x.x_token + ahead.h * x.x_head;
+                uint8_t *to = ring + in * (kThreads * 16) + threadIdx.x * 16;
+                copy16(to, p);
+                if (kHalf) copy16(to + kDepth * kThreads * 16, p + pairs);
+                ahead.step(nh);
             }
+            copy_commit();
+            in = in + 1 == kDepth ? 0 : in + 1;
+        };
+#pragma unroll 1
+        for (int i = 0; i < kDepth - 1; ++i) start();
+        fill_table(a, tab, pos_s, t0, nt);
+        __syncthreads();
+#pragma unroll 1
+        for (; w.tok < nt; w.step(nh)) {
+            start();
+            copy_wait<kDepth - 1>();
+            H piece;
+            const uint8_t *from = ring + out * (kThreads * 16) + threadIdx.x * 16;
+            piece.lo = *reinterpret_cast<const typename H::P *>(from);
+            if (kHalf) piece.hi = *reinterpret_cast<const typename H::P *>(from + kDepth * kThreads * 16);
+            out = out + 1 == kDepth ? 0 : out + 1;
+            if (pos_s[w.tok] >= 0) finish(piece, w.tok, w.h);  // (a negative position: a padding token)
         }
+        copy_wait<0>();
     }
 }
 
 template <typename T>
 __device__ __forceinline__ void rope_segment(const RopeArgs &a, const RopeTensor &x, const Segment &g, uint32_t cta,
-                                             float2 *tab, int32_t *pos_s) {
+                                             Table &tab, int32_t *pos_s, uint8_t *ring) {
     const uint32_t tile = cta / g.head_chunks, chunk = cta - tile * g.head_chunks;
     const int t0 = static_cast<int>(tile * g.tokens), h0 = static_cast<int>(chunk * g.heads);
     const int nt = min(static_cast<int>(g.tokens), a.num_tokens - t0), nh = min(static_cast<int>(g.heads), x.heads - h0);
     const int units = static_cast<int>(g.units);
-    fill_table(a, tab, pos_s, t0, nt);
-    __syncthreads();
     constexpr int V = 16 / sizeof(T);
     if (x.half) {
-        if (x.vec) rotate_tile<T, true, V>(a, x, tab, pos_s, t0, nt, h0, nh, units);
-        else rotate_tile<T, true, 1>(a, x, tab, pos_s, t0, nt, h0, nh, units);
+        if (x.vec) rotate_tile<T, true, V>(a, x, tab, pos_s, ring, t0, nt, h0, nh, units);
+        else rotate_tile<T, true, 1>(a, x, tab, pos_s, ring, t0, nt, h0, nh, units);
     } else {
-        if (x.vec) rotate_tile<T, false, V>(a, x, tab, pos_s, t0, nt, h0, nh, units);
-        else rotate_tile<T, false, 2>(a, x, tab, pos_s, t0, nt, h0, nh, units);
+        if (x.vec) rotate_tile<T, false, V>(a, x, tab, pos_s, ring, t0, nt, h0, nh, units);
+        else rotate_tile<T, false, 2>(a, x, tab, pos_s, ring, t0, nt, h0, nh, units);
     }
 }
 
@@ -203,13 +292,14 @@ __device__ __forceinline__ const Segment &segment_of(const Plan &p, uint32_t cta
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant__ RopeArgs a,
                                                         const __grid_constant__ Plan p) {
-    __shared__ __align__(16) float2 tab[kTabPairs];
+    __shared__ Table tab;
+    __shared__ __align__(16) uint8_t ring[kThreads * kRingBytes];
     __shared__ int32_t pos_s[kTileTokens];
     pdl_wait();
     pdl_launch_dependents();
     int j;
     const Segment &g = segment_of(p, blockIdx.x, j);
-    rope_segment<T>(a, a.t[j], g, blockIdx.x - g.first, tab, pos_s);
+    rope_segment<T>(a, a.t[j], g, blockIdx.x - g.first, tab, pos_s, ring);
 }
 
 // x / s rounded to nearest for the quotients that matter here, from r = 1 / s rounded to nearest: one correction
@@ -230,7 +320,7 @@ __device__ __forceinline__ uint32_t e4m3x2_rne(float lo, float hi) {
 // at a time.  A rotated element of a half-split pair reads its partner too (from L1), so that every
 // thread writes one contiguous piece.  slot_s: the tile's slots, negative where nothing is written.
 template <int V>
-__device__ __forceinline__ void insert_tile(const KvInsertArgs &a, const float2 *tab, const int32_t *slot_s, int t0,
+__device__ __forceinline__ void insert_tile(const KvInsertArgs &a, const Table &tab, const int32_t *slot_s, int t0,
                                             int nt) {
     using P = Piece<__nv_bfloat16, V>;
     constexpr int kBatch = V == 8 ? 2 : 1;
@@ -268,26 +358,34 @@ __device__ __forceinline__ void insert_tile(const KvInsertArgs &a, const float2 
 #pragma unroll
             for (int e = 0; e < V; ++e) x[e] = __bfloat162float(p[i].e[e]);
             if (turned && !is_v) {
-                const float2 *cs = tab + tok[i] * pairs;
+                const float *cos = tab.cos + tok[i] * pairs, *sin = tab.sin + tok[i] * pairs;
                 if (a.half) {
-                    const float2 *c = cs + (low ? r0 : r0 - pairs);
+                    const int first = low ? r0 : r0 - pairs;
+                    float c[V], n[V];
+                    load_angles<V>(cos + first, c);
+                    load_angles<V>(sin + first, n);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const float y = __bfloat162float(q[i].e[e]);
-                        x[e] = low ? x[e] * c[e].x - y * c[e].y : y * c[e].y + x[e] * c[e].x;
-                    }
+                    for (int e = 0; e < V; ++e)  // (as turn rounds it)
+                        x[e] = low ? fmaf(__bfloat162float(q[i].e[e]), -n[e], x[e] * c[e])
+                                   : fmaf(x[e], c[e], __bfloat162float(q[i].e[e]) * n[e]);
                 } else if constexpr (V > 1) {
+                    float c[V / 2], n[V / 2], u[V / 2], y[V / 2];
+                    load_angles<V / 2>(cos + (r0 >> 1), c);
+                    load_angles<V / 2>(sin + (r0 >> 1), n);
 #pragma unroll
-                    for (int e = 0; e < V; e += 2) {
-                        const float2 c = cs[(r0 + e) >> 1];
-                        const float u = x[e], y = x[e + 1];
-                        x[e] = u * c.x - y * c.y;
-                        x[e + 1] = u * c.y + y * c.x;
+                    for (int e = 0; e < V / 2; ++e) {
+                        u[e] = x[2 * e];
+                        y[e] = x[2 * e + 1];
+                    }
+                    turn<V / 2>(u, y, c, n);
+#pragma unroll
+                    for (int e = 0; e < V / 2; ++e) {
+                        x[2 * e] = u[e];
+                        x[2 * e + 1] = y[e];
                     }
                 } else {
-                    const float2 c = cs[r0 >> 1];
-                    const float y = __bfloat162float(q[i].e[0]);
-                    x[0] = r0 & 1 ? y * c.y + x[0] * c.x : x[0] * c.x - y * c.y;
+                    const float c = cos[r0 >> 1], n = sin[r0 >> 1], y = __bfloat162float(q[i].e[0]);
+                    x[0] = r0 & 1 ? fmaf(x[0], c, y * n) : fmaf(y, -n, x[0] * c);
                 }
             }
             const int32_t slot = slot_s[tok[i]];
@@ -318,9 +416,10 @@ __device__ __forceinline__ void insert_tile(const KvInsertArgs &a, const float2 
 }
 
 // Segment 0: the K and V rows; segment 1, if any: q.
-__global__ void __launch_bounds__(kThreads, 7) kv_insert_kernel(const __grid_constant__ KvInsertArgs a,
+__global__ void __launch_bounds__(kThreads, 6) kv_insert_kernel(const __grid_constant__ KvInsertArgs a,
                                                              const __grid_constant__ Plan p) {
-    __shared__ __align__(16) float2 tab[kTabPairs];
+    __shared__ Table tab;
+    __shared__ __align__(16) uint8_t ring[kThreads * kRingBytes];
     __shared__ int32_t pos_s[kTileTokens];
     pdl_wait();
     pdl_launch_dependents();
@@ -328,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 7) kv_insert_kernel(const __grid_con
     const Segment &g = segment_of(p, blockIdx.x, j);
     const uint32_t cta = blockIdx.x - g.first;
     if (j == 1) {
-        rope_segment<__nv_bfloat16>(a.rope, a.rope.t[0], g, cta, tab, pos_s);
+        rope_segment<__nv_bfloat16>(a.rope, a.rope.t[0], g, cta, tab, pos_s, ring);
         return;
     }
     const int t0 = static_cast<int>(cta * g.tokens);
@@ -348,12 +447,12 @@ __global__ void __launch_bounds__(kThreads, 7) kv_insert_kernel(const __grid_con
     else insert_tile<1>(a, tab, slot_s, t0, nt);
 }
 
-// Tiles of twelve pieces a thread once there are enough to fill the GPU, of one a thread, as many CTAs as
-// possible, for the few tokens of a decode step.  The two prefills above with 6, 8, 12 and 24 pieces: rope 50.8,
-// 50.8, 43.1 and 42.8 us, insert 68.0, 64.7, 64.5 and 69.8 us.
+// Tiles of sixteen pieces a thread once there are enough to fill the GPU, of one a thread, as many CTAs as
+// possible, for the few tokens of a decode step.  The two prefills above with 14, 16, 18 and 24 pieces: rope 36.6,
+// 36.6, 35.4 and 36.5 us, insert 49.1, 48.5, 50.6 and 53.8 us.
 bool add_segment(Plan &p, uint64_t &ctas, int num_tokens, int heads, uint32_t units, int pairs, bool split_heads) {
     const uint64_t pieces = static_cast<uint64_t>(num_tokens) * heads * units;
-    const uint32_t target = pieces >= (1u << 20) ? 12 * kThreads : kThreads;
+    const uint32_t target = pieces >= (1u << 20) ? 16 * kThreads : kThreads;
     Segment &g = p.s[p.n++];
     const uint32_t per_token = static_cast<uint32_t>(heads) * units;
     g.units = units;
