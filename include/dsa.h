@@ -511,8 +511,9 @@ typedef struct dsa_rope_spec {
 } dsa_rope_spec;
 
 /* One tensor [num_tokens, num_heads, rot_dim]: the rotary part of every head alone, in place inside
- * larger heads through its strides (in elements).  x may equal out (with equal strides); any other
- * overlap is not allowed. */
+ * larger heads through its strides (in elements).  x may equal out (with equal strides); an output
+ * overlaps nothing else that the call reads or writes (two of its tensors at one output address, or
+ * one's output at another's input, are DSA_ERR_INVALID_ARG). */
 typedef struct dsa_rope_tensor {
     const void *x;
     void *out;
@@ -549,8 +550,8 @@ typedef struct dsa_kv_rows {
  *   DSA_KV_FP8:  e4m3(x / scale), IEEE fp32 division, round to nearest even, saturating to +-448
  * rope != NULL rotates K's dims [rot_offset, rot_offset + rot_dim) on the way, in fp32, and with
  * q != NULL also rotates q (bf16, [num_tokens, q->num_heads, rot_dim]) as dsa_rope does, in the same
- * launch; q needs rope.  slots: device [num_tokens], distinct (of a slot listed twice, which token's
- * bytes it holds is unspecified).  A slot outside the pool, or a slot >= 0 of a token at a negative
+ * launch; q needs rope.  slots: device [num_tokens], distinct (a slot listed twice holds bytes of
+ * either token, in any mixture).  A slot outside the pool, or a slot >= 0 of a token at a negative
  * position, is DSA_ERR_BOUNDS and not written; every other byte of the pool keeps its value.
  */
 int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_tokens, const dsa_kv_rows *kv,
@@ -571,9 +572,12 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
  * Each row's tokens are split into parts by its own context (the group's largest; batch
  * invariance), one CTA per part and KV head, merged by log-sum-exp: the workspace (device, 256-byte
  * aligned, dsa_kv_attention_workspace_size bytes, no initial contents; NULL when that is 0) holds
- * the parts in fp32.  Scores and sums are fp32; the softmax weights multiply V as the sum of two
- * bf16 terms (bf16 pool) or as fp16 (FP8 pool, whose codes are exact in fp16; there q is scaled to
- * fp16 by a power of two per head).  A row_ctx outside [0, max_ctx], a row_req outside the block
+ * the parts in fp32 and serves one call at a time: calls that may run at once, captured graphs
+ * among them, have one each.  Outputs overlap no input.  Scores and sums are fp32.  The softmax weights multiply V as
+ * the sum of two bf16 terms (bf16 pool), as fp16 (FP8 pool of head_dim 64, whose codes are exact in
+ * fp16), or as the sum of two e4m3 terms (FP8 pool of head_dim 128).  Over an FP8 pool q is scaled by a power
+ * of two per head and rounded to fp16 (head_dim 64) or to the sum of two e4m3 terms (128); a head
+ * of head_dim 128 with an infinity or a NaN in q gets NaN.  A row_ctx outside [0, max_ctx], a row_req outside the block
  * table, rows of a group with different requests, or a page id outside the pool is DSA_ERR_BOUNDS.
  */
 int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint16_t *q, int64_t q_stride,

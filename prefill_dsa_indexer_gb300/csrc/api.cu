@@ -645,8 +645,17 @@ static int check_rope_spec(const dsa_rope_spec *rope) {
     return rope->rot_dim > DSA_ROPE_MAX_DIM ? DSA_ERR_UNSUPPORTED : DSA_OK;
 }
 
+// Whether no two (token, head) parts of rot elements share an element: one of the strides steps over all of the
+// other's.
+static bool apart(int64_t token_stride, int64_t tokens, int64_t head_stride, int64_t heads, int64_t rot) {
+    if (heads == 1) return tokens == 1 || token_stride >= rot;
+    if (tokens == 1) return head_stride >= rot;
+    return (head_stride >= rot && token_stride >= rot + (heads - 1) * head_stride) ||
+           (token_stride >= rot && (head_stride - rot) / (tokens - 1) >= token_stride);
+}
+
 // One rotated tensor, and whether 16-byte accesses reach all of its rotary parts.
-static int rope_tensor(const dsa_rope_tensor &t, int32_t rot, int elem, RopeTensor *out) {
+static int rope_tensor(const dsa_rope_tensor &t, int32_t tokens, int32_t rot, int elem, RopeTensor *out) {
     if (t.x == nullptr || t.out == nullptr || t.num_heads < 1) return DSA_ERR_INVALID_ARG;
     if (t.layout != DSA_ROPE_INTERLEAVED && t.layout != DSA_ROPE_HALF) return DSA_ERR_UNSUPPORTED;
     if (t.num_heads > kRopeMaxHeads) return DSA_ERR_UNSUPPORTED;
@@ -655,6 +664,7 @@ static int rope_tensor(const dsa_rope_tensor &t, int32_t rot, int elem, RopeTens
         return DSA_ERR_INVALID_ARG;
     if (t.x_token_stride < 0 || t.x_head_stride < 0 || t.out_token_stride < 0 || t.out_head_stride < 0)
         return DSA_ERR_INVALID_ARG;
+    if (!apart(t.out_token_stride, tokens, t.out_head_stride, t.num_heads, rot)) return DSA_ERR_INVALID_ARG;
     const bool half = t.layout == DSA_ROPE_HALF;
     const int64_t v = 16 / elem;
     const bool vec = aligned(t.x, 16) && aligned(t.out, 16) && (half ? rot / 2 : rot) % v == 0 &&
@@ -676,8 +686,10 @@ int dsa_rope(const dsa_rope_spec *rope, const dsa_rope_tensor *tensors, int32_t 
     if (tensors == nullptr) return DSA_ERR_INVALID_ARG;
     RopeArgs a = {rope->turns, rope->positions, rope->rot_dim, rope->scale, num_tokens, num_tensors, {}};
     for (int i = 0; i < num_tensors; ++i) {
-        rc = rope_tensor(tensors[i], rope->rot_dim, dtype == DSA_DTYPE_BF16 ? 2 : 4, &a.t[i]);
+        rc = rope_tensor(tensors[i], num_tokens, rope->rot_dim, dtype == DSA_DTYPE_BF16 ? 2 : 4, &a.t[i]);
         if (rc != DSA_OK) return rc;
+        for (int j = 0; j < i; ++j)
+            if (a.t[i].out == a.t[j].out || a.t[i].out == a.t[j].x || a.t[i].x == a.t[j].out) return DSA_ERR_INVALID_ARG;
     }
     return launch_status(launch_rope(a, dtype, static_cast<cudaStream_t>(stream)));
 }
@@ -724,7 +736,7 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
         a.half = kv->layout == DSA_ROPE_HALF;
         if (q != nullptr) {
             a.rope.num_tensors = 1;
-            rc = rope_tensor(*q, rope->rot_dim, 2, &a.rope.t[0]);
+            rc = rope_tensor(*q, num_tokens, rope->rot_dim, 2, &a.rope.t[0]);
             if (rc != DSA_OK) return rc;
         }
     }

@@ -72,6 +72,41 @@ def test_rope(dtype, layout, tokens, heads, rot, pad, scaling):
     assert torch.equal(full[..., :pad], before[..., :pad])
 
 
+@pytest.mark.parametrize("dtype, heads, rot, pad", [(torch.bfloat16, 20, 128, 0), (torch.bfloat16, 33, 64, 512),
+                                                    (torch.float32, 3, 256, 64), (torch.bfloat16, 1, 256, 0)])
+@pytest.mark.parametrize("layout", [P.ROPE_INTERLEAVED, P.ROPE_HALF])
+def test_rope_of_a_long_prefill(dtype, heads, rot, pad, layout):
+    """Tiles of many pieces a thread, more in flight than fit its ring, with padding tokens among them."""
+    g = gen(heads)
+    tokens = 8195 if heads > 1 else 40001
+    x = randn(g, tokens, heads, pad + rot, dtype=dtype)[..., pad:]
+    positions = torch.randint(0, 1 << 20, (tokens,), generator=g, device="cuda", dtype=torch.int32)
+    positions[torch.randint(0, tokens, (500,), generator=g, device="cuda")] = -1
+    live = positions >= 0
+    table, freq = P.rope_table(rot, 500000.0), P.rope_frequencies(rot, 500000.0)[0]
+    out = torch.full((tokens, heads, rot), 7.0, dtype=dtype, device="cuda")
+    P.rope(x, table, positions, layout=layout, out=out)
+    for a in range(0, tokens, 5000):
+        at = slice(a, a + 5000)
+        ref, mag = ref_rotate(x[at], positions[at], freq, 1.0, layout)
+        assert ((out[at].double() - ref).abs() <= rope_bound(ref, mag, 1.0, dtype))[live[at]].all()
+    assert (out[~live] == 7.0).all()
+    kept = x[~live].clone()
+    P.rope(x, table, positions, layout=layout)
+    assert torch.equal(x[live], out[live]) and torch.equal(x[~live], kept)
+
+
+def test_rope_of_heads_before_tokens():
+    """Tensors that lie in memory as [heads, tokens, dims], in and out."""
+    g = gen(4)
+    x = randn(g, 5, 40, 64).transpose(0, 1)
+    positions = torch.arange(40, dtype=torch.int32, device="cuda") * 77
+    table, freq = P.rope_table(64), P.rope_frequencies(64, 10000.0)[0]
+    out = P.rope(x, table, positions, out=torch.empty(5, 40, 64, dtype=x.dtype, device="cuda").transpose(0, 1))
+    ref, mag = ref_rotate(x, positions, freq, 1.0, P.ROPE_INTERLEAVED)
+    assert ((out.double() - ref).abs() <= rope_bound(ref, mag, 1.0, x.dtype)).all()
+
+
 def test_rope_several_tensors_in_one_call_and_padding_tokens():
     g = gen(3)
     n, table = 6, P.rope_table(64)
@@ -135,7 +170,8 @@ def bits(t):
     (1, 1, 1, 64, 16, 0, 0, P.ROPE_HALF), (1, 4, 64, 128, 128, 64, 0, P.ROPE_HALF),
     (37, 3, 5, 64, 32, 64, 0, P.ROPE_INTERLEAVED), (70, 2, 6, 128, 64, 32, 96, P.ROPE_HALF),
     (9, 2, 2, 128, 64, 18, 3, P.ROPE_HALF), (9, 2, 3, 128, 64, 22, 7, P.ROPE_INTERLEAVED),
-    (1000, 8, 8, 128, 128, 128, 0, P.ROPE_HALF)])
+    (1000, 8, 8, 128, 128, 128, 0, P.ROPE_HALF), (8195, 4, 33, 128, 128, 64, 32, P.ROPE_HALF),
+    (8195, 8, 70, 64, 16, 64, 0, P.ROPE_INTERLEAVED)])
 def test_kv_insert(fmt, tokens, kv_heads, heads, dim, page, rot, off, layout):
     g = gen(tokens + dim + rot)
     pages = tokens // page + 4
@@ -309,7 +345,8 @@ def test_attention_long_ragged_contexts(fmt, kv_heads, hpg, dim, page):
 
 @pytest.mark.parametrize("fmt", ["bf16", "fp8"])
 @pytest.mark.parametrize("group, kv_heads, hpg, dim, page", [(2, 2, 3, 64, 16), (4, 2, 16, 128, 128), (8, 1, 4, 128, 64),
-                                                            (8, 2, 16, 64, 32)])
+                                                            (8, 2, 16, 64, 32), (2, 2, 16, 128, 32), (4, 1, 7, 128, 16),
+                                                            (8, 1, 16, 128, 128)])
 def test_attention_verify_rows(fmt, group, kv_heads, hpg, dim, page):
     c = Case(13, fmt, [group, 70, 129, 8192 + group // 2, 3000], kv_heads, hpg, dim, page, group=group)
     c.check(*c.run())
@@ -345,6 +382,30 @@ def test_attention_rows_of_a_packed_projection():
     packed[:, :32] = c.q
     a, b = c.run(q=packed[:, :32]), c.run()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_of_very_many_rows(fmt, dim):
+    """More row groups than a launch keeps running costs for, most of them short or empty."""
+    g = gen(21)
+    ctx = torch.randint(0, 40, (1301,), generator=g, device="cuda").tolist()
+    for i in range(0, 1301, 97):
+        ctx[i] = 3 * i
+    c = Case(22, fmt, ctx, 2, 3, dim, 16)
+    out, lse = c.run()
+    c.check(out, lse, rows=list(range(0, 1301, 97)) + list(range(5, 1301, 41)) + [1299, 1300])
+    empty = torch.tensor([n == 0 for n in ctx], device="cuda")
+    assert (out[empty] == 0).all() and (lse[empty] == -math.inf).all() and torch.isfinite(lse[~empty]).all()
+    assert torch.equal(c.run()[0], out)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_attention_when_no_row_sees_anything(fmt):
+    c = Case(23, fmt, [0, 0, 0], 2, 16, 128, 64)
+    c.max_ctx, c.table = 70000, torch.full((3, 1094), 0x7FFFFFF, dtype=torch.int32, device="cuda")
+    out, lse = c.run()
+    assert (out == 0).all() and (lse == -math.inf).all()
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "fp8"])
@@ -537,6 +598,51 @@ def test_calls_on_another_stream_and_two_at_once():
     torch.cuda.synchronize()
     for i, (o, l) in enumerate(got):
         assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+
+
+def test_two_captured_graphs_and_an_eager_call_at_once():
+    """Each capture has a workspace of its own, so they may run beside each other and beside an eager call."""
+    a, b = Case(42, "fp8", [9000, 12, 300], 2, 8, 128, 64, group=2), Case(43, "bf16", [20000], 4, 4, 64, 32)
+    want = a.run(), b.run()
+    graphs, outs = [], []
+    for c in (a, b, a):
+        need = P.kv_attention_workspace_size(c.kv, c.q.shape[0], c.q.shape[1], c.max_ctx)
+        ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+        o, l = torch.empty_like(want[0][0] if c is a else want[1][0]), torch.empty_like(want[0][1] if c is a else want[1][1])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            P.kv_attention(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q, rows_per_group=c.group, out=o, lse=l,
+                           workspace=ws)
+        graphs.append(graph)
+        outs.append((o, l))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(4):
+        for o, l in outs:
+            o.fill_(7.0)
+            l.fill_(7.0)
+        torch.cuda.synchronize()
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+                graph.replay()
+        eager = b.run()
+        torch.cuda.synchronize()
+        for (o, l), w in zip(outs + [eager], (want[0], want[1], want[0], want[1])):
+            assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+
+
+def test_layer_without_rotary_positions():
+    g = gen(44)
+    c = Case(45, "bf16", [33, 64], 2, 4, 64, 16)
+    layer = P.KvLayer(c.kv, c.table, c.max_ctx, 2, 8)
+    slots = torch.tensor([c.table[r, p // 16].item() * 16 + p % 16 for r, p in enumerate((32, 63))], dtype=torch.int32,
+                         device="cuda")
+    k, v = randn(g, 2, 2, 64), randn(g, 2, 2, 64)
+    out, lse = layer.run(c.row_req, c.row_ctx, slots, None, c.q, k, v)
+    checked(layer.status)
+    for r, s in enumerate(slots.tolist()):
+        assert torch.equal(c.pool[s // 16, :, 0, s % 16], k[r]) and torch.equal(c.pool[s // 16, :, 1, s % 16], v[r])
+    c.check(out, lse)
 
 
 def test_binding_refusals():

@@ -116,6 +116,22 @@ def test_rope_refusals(lib):
     assert call(spec, (P._RopeTensor * 1)(t(heads=4097))) == P.ERR_UNSUPPORTED
 
 
+def test_rope_outputs_that_overlap_are_refused(lib):
+    spec = P._RopeSpec(FAKE, FAKE, 64, 1.0)
+    t = lambda x, out, heads=4, xs=(256, 64), os=(256, 64): P._RopeTensor(x, out, heads, 0, *xs, *os)  # noqa: E731
+    call = lambda *ts, tok=3: lib.dsa_rope(spec, (P._RopeTensor * len(ts))(*ts), len(ts), 1, tok, None)  # noqa: E731
+    # one tensor at two outputs' address, one's output at another's input
+    assert call(t(FAKE, 2 * FAKE), t(3 * FAKE, 2 * FAKE)) == P.ERR_INVALID_ARG
+    assert call(t(FAKE, FAKE), t(FAKE, FAKE)) == P.ERR_INVALID_ARG
+    assert call(t(FAKE, 2 * FAKE), t(2 * FAKE, 3 * FAKE)) == P.ERR_INVALID_ARG
+    assert call(t(FAKE, 2 * FAKE), t(3 * FAKE, FAKE)) == P.ERR_INVALID_ARG
+    # strides that fold an output's tokens or heads onto each other
+    for heads, os in ((4, (0, 64)), (4, (256, 0)), (4, (255, 64)), (4, (256, 63)), (4, (64, 191)), (1, (63, 1 << 20)),
+                      (4, (192, 128))):
+        assert call(t(FAKE, 2 * FAKE, heads, os=os)) == P.ERR_INVALID_ARG, os
+    assert call(t(FAKE, 2 * FAKE, 4, os=(7, 63)), tok=1) == P.ERR_INVALID_ARG
+
+
 BAD_CACHES = [(dict(fmt=P.KEY_FP8), P.ERR_UNSUPPORTED), (dict(page=8), P.ERR_UNSUPPORTED),
               (dict(page=48), P.ERR_UNSUPPORTED), (dict(page=256), P.ERR_UNSUPPORTED), (dict(dim=96), P.ERR_UNSUPPORTED),
               (dict(dim=256), P.ERR_UNSUPPORTED), (dict(heads=0), P.ERR_INVALID_ARG), (dict(pages=0), P.ERR_INVALID_ARG),
