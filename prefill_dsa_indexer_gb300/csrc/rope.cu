@@ -15,9 +15,9 @@
 // 16-byte piece of a head and walks over the tile's heads and tokens with it, so that the walk has no division and
 // the angles' place changes with the token alone.  What it takes is bytes in flight: a thread's next pieces come by
 // asynchronous copies into 128 bytes of its own in shared memory (with four 16-byte loads in registers instead, the
-// prefills below took 43 and 64.5 us; rings of 96 and 192 bytes 34.9 and 51.0, 40.3 and 51.0 us).
-// 8,192 tokens x 98 heads x 64 dims: 36.6 us (5.6 TB/s); 8,192 tokens into an FP8 pool of 4 KV heads of 128 with
-// 64 query heads rotated: 48.5 us (6.1 TB/s).
+// prefills below took 43 and 64.5 us; a ring of 96 bytes 35.2 and 56.5 us).
+// 8,192 tokens x 98 heads x 64 dims: 35.8 us (5.7 TB/s); 8,192 tokens into an FP8 pool of 4 KV heads of 128 with
+// 64 query heads rotated: 48.0 us (6.1 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -216,13 +216,6 @@ __device__ __forceinline__ void rotate_tile(const RopeArgs &a, const RopeTensor 
     const T *src = static_cast<const T *>(x.x) + t0 * x.x_token + h0 * x.x_head + w.unit * V;
     T *dst = static_cast<T *>(x.out) + t0 * x.out_token + h0 * x.out_head + w.unit * V;
     const int unit = w.unit * H::kPairs;
-    auto finish = [&](H &piece, int tok, int h) {
-        float c[H::kPairs], s[H::kPairs];
-        load_angles<H::kPairs>(tab.cos + tok * pairs + unit, c);
-        load_angles<H::kPairs>(tab.sin + tok * pairs + unit, s);
-        piece.rotate(c, s);
-        piece.store(dst + tok * x.out_token + h * x.out_head, pairs);
-    };
     if constexpr (V * sizeof(T) < 16) {
         fill_table(a, tab, pos_s, t0, nt);
         __syncthreads();
@@ -230,37 +223,75 @@ __device__ __forceinline__ void rotate_tile(const RopeArgs &a, const RopeTensor 
             if (pos_s[w.tok] < 0) continue;  // a padding token
             H piece;
             piece.load(src + w.tok * x.x_token + w.h * x.x_head, pairs);
-            finish(piece, w.tok, w.h);
+            float c[H::kPairs], s[H::kPairs];
+            load_angles<H::kPairs>(tab.cos + w.tok * pairs + unit, c);
+            load_angles<H::kPairs>(tab.sin + w.tok * pairs + unit, s);
+            piece.rotate(c, s);
+            piece.store(dst + w.tok * x.out_token + w.h * x.out_head, pairs);
         }
     } else {
         constexpr int kBytes = kHalf ? 32 : 16, kDepth = kRingBytes / kBytes;
+        // the walk's steps in memory, so that a piece's address takes additions alone
+        struct Steps {
+            int64_t head, token;  // bytes
+            uint8_t *at, *row;    // this piece, and the first one of its token
+            __device__ __forceinline__ void step(bool same_token) {
+                at += head;
+                if (!same_token) at = row += token;
+            }
+        };
+        auto steps = [&](const void *base, int64_t token, int64_t head) {
+            Steps p{w.h_step * head * static_cast<int64_t>(sizeof(T)), w.tok_step * token * static_cast<int64_t>(sizeof(T)),
+                    nullptr, nullptr};
+            p.row = static_cast<uint8_t *>(const_cast<void *>(base)) +
+                    (w.tok * token + w.h0 * head) * static_cast<int64_t>(sizeof(T));
+            p.at = p.row;
+            return p;
+        };
         Walk ahead = w;
-        uint32_t in = 0, out = 0;  // places in the ring
+        Steps from = steps(src, x.x_token, x.x_head), to = steps(dst, x.out_token, x.out_head);
+        uint8_t *mine = ring + threadIdx.x * 16;
+        constexpr int kPlace = kThreads * 16, kHigh = kDepth * kPlace;  // (the second halves lie behind the first)
+        int in = 0, out = 0;                                            // places in the ring
+        const int other = pairs * static_cast<int>(sizeof(T));
         auto start = [&]() {
             if (ahead.tok < nt) {
-                const T *p = src + ahead.tok * x.x_token + ahead.h * x.x_head;
-                uint8_t *to = ring + in * (kThreads * 16) + threadIdx.x * 16;
-                copy16(to, p);
-                if (kHalf) copy16(to + kDepth * kThreads * 16, p + pairs);
+                copy16(mine + in, from.at);
+                if (kHalf) copy16(mine + in + kHigh, from.at + other);
+                const int tok = ahead.tok;
                 ahead.step(nh);
+                from.step(ahead.tok == tok);
             }
             copy_commit();
-            in = in + 1 == kDepth ? 0 : in + 1;
+            in = in + kPlace == kHigh ? 0 : in + kPlace;
         };
 #pragma unroll 1
         for (int i = 0; i < kDepth - 1; ++i) start();
         fill_table(a, tab, pos_s, t0, nt);
         __syncthreads();
+        float c[H::kPairs], s[H::kPairs];  // of the token at hand
+        int held = -1;
+        bool live = false;
 #pragma unroll 1
-        for (; w.tok < nt; w.step(nh)) {
+        while (w.tok < nt) {
             start();
+            if (w.tok != held) {
+                held = w.tok;
+                live = pos_s[held] >= 0;  // (a negative position: a padding token)
+                load_angles<H::kPairs>(tab.cos + held * pairs + unit, c);
+                load_angles<H::kPairs>(tab.sin + held * pairs + unit, s);
+            }
             copy_wait<kDepth - 1>();
             H piece;
-            const uint8_t *from = ring + out * (kThreads * 16) + threadIdx.x * 16;
-            piece.lo = *reinterpret_cast<const typename H::P *>(from);
-            if (kHalf) piece.hi = *reinterpret_cast<const typename H::P *>(from + kDepth * kThreads * 16);
-            out = out + 1 == kDepth ? 0 : out + 1;
-            if (pos_s[w.tok] >= 0) finish(piece, w.tok, w.h);  // (a negative position: a padding token)
+            piece.lo = *reinterpret_cast<const typename H::P *>(mine + out);
+            if (kHalf) piece.hi = *reinterpret_cast<const typename H::P *>(mine + out + kHigh);
+            out = out + kPlace == kHigh ? 0 : out + kPlace;
+            if (live) {
+                piece.rotate(c, s);
+                piece.store(reinterpret_cast<T *>(to.at), pairs);
+            }
+            w.step(nh);
+            to.step(w.tok == held);
         }
         copy_wait<0>();
     }
@@ -448,8 +479,8 @@ __global__ void __launch_bounds__(kThreads, 6) kv_insert_kernel(const __grid_con
 }
 
 // Tiles of sixteen pieces a thread once there are enough to fill the GPU, of one a thread, as many CTAs as
-// possible, for the few tokens of a decode step.  The two prefills above with 14, 16, 18 and 24 pieces: rope 36.6,
-// 36.6, 35.4 and 36.5 us, insert 49.1, 48.5, 50.6 and 53.8 us.
+// possible, for the few tokens of a decode step.  The two prefills above with 16, 18 and 24 pieces: rope 35.8,
+// 35.4 and 35.5 us, insert 48.0, 48.6 and 54.8 us.
 bool add_segment(Plan &p, uint64_t &ctas, int num_tokens, int heads, uint32_t units, int pairs, bool split_heads) {
     const uint64_t pieces = static_cast<uint64_t>(num_tokens) * heads * units;
     const uint32_t target = pieces >= (1u << 20) ? 16 * kThreads : kThreads;

@@ -604,7 +604,7 @@ def test_two_captured_graphs_and_an_eager_call_at_once():
     """Each capture has a workspace of its own, so they may run beside each other and beside an eager call."""
     a, b = Case(42, "fp8", [9000, 12, 300], 2, 8, 128, 64, group=2), Case(43, "bf16", [20000], 4, 4, 64, 32)
     want = a.run(), b.run()
-    graphs, outs = [], []
+    graphs, outs, spaces = [], [], []  # (a graph does not keep its workspace alive)
     for c in (a, b, a):
         need = P.kv_attention_workspace_size(c.kv, c.q.shape[0], c.q.shape[1], c.max_ctx)
         ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
@@ -615,6 +615,7 @@ def test_two_captured_graphs_and_an_eager_call_at_once():
                            workspace=ws)
         graphs.append(graph)
         outs.append((o, l))
+        spaces.append(ws)
     streams = [torch.cuda.Stream() for _ in graphs]
     for _ in range(4):
         for o, l in outs:
