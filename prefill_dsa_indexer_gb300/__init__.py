@@ -690,10 +690,23 @@ def kv_attention_workspace_size(kv, num_rows, num_heads, max_ctx) -> int:
     return int(load_library().dsa_kv_attention_workspace_size(kv._c, int(num_rows), int(num_heads), int(max_ctx)))
 
 
+def _attention_buffers(kv, R, H, max_ctx, device, out, lse, workspace):
+    """kv_attention's outputs and workspace, allocated where they are None."""
+    if out is None:
+        out = torch.empty((R, H, kv.head_dim), dtype=torch.bfloat16, device=device)
+    if lse is None:
+        lse = torch.empty((R, H), dtype=torch.float32, device=device)
+    if workspace is None:
+        need = kv_attention_workspace_size(kv, R, H, max_ctx)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    return out, lse, workspace
+
+
 def kv_attention(kv, block_table, row_req, row_ctx, max_ctx, q, sm_scale=None, rows_per_group=1, out=None, lse=None,
                  workspace=None, status=None, stream=None):
     """dsa_kv_attention: (out bf16 [R, H, head_dim], lse fp32 [R, H]) of q bf16 [R, H, head_dim] (heads packed)
-    over the KvCache's tokens below row_ctx; sm_scale defaults to 1 / sqrt(head_dim)."""
+    over the KvCache's tokens below row_ctx; sm_scale defaults to 1 / sqrt(head_dim).  A captured graph does not
+    keep the workspace alive: pass one that outlives it, and no other call that may run beside it uses."""
     R, H, D = q.shape
     device = kv.device
     if D != kv.head_dim or q.dtype is not torch.bfloat16 or q.get_device() != device:
@@ -704,13 +717,12 @@ def kv_attention(kv, block_table, row_req, row_ctx, max_ctx, q, sm_scale=None, r
     requests = block_table.shape
     if len(requests) != 2:
         raise DsaError("the block table is [requests, pages]")
-    if out is None:
-        out = torch.empty((R, H, D), dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty((R, H), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        need = kv_attention_workspace_size(kv, R, H, max_ctx)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    if out is None or lse is None or workspace is None:
+        if stream is None:
+            out, lse, workspace = _attention_buffers(kv, R, H, max_ctx, q.device, out, lse, workspace)
+        else:
+            with torch.cuda.stream(stream):  # what is allocated here belongs to the stream that uses it
+                out, lse, workspace = _attention_buffers(kv, R, H, max_ctx, q.device, out, lse, workspace)
     rows = _PACK_ROWS(_flat(block_table, "block_table", device, _I32), requests[1], requests[0],
                       _flat(row_req, "row_req", device, _I32, (R,)), _flat(row_ctx, "row_ctx", device, _I32, (R,)), R,
                       int(max_ctx), int(rows_per_group))

@@ -600,6 +600,20 @@ def test_calls_on_another_stream_and_two_at_once():
         assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
 
 
+def test_calls_on_a_stream_that_is_not_current():
+    """What a call allocates for itself belongs to the stream that it is given."""
+    c = Case(46, "bf16", [30000, 4000], 2, 8, 128, 64)
+    want, st = c.run(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got.append(P.kv_attention(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q, stream=st))
+        torch.full((4 << 20,), 7.0, device="cuda")  # the current stream's own allocations
+    torch.cuda.synchronize()
+    for o, l in got:
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+
+
 def test_two_captured_graphs_and_an_eager_call_at_once():
     """Each capture has a workspace of its own, so they may run beside each other and beside an eager call."""
     a, b = Case(42, "fp8", [9000, 12, 300], 2, 8, 128, 64, group=2), Case(43, "bf16", [20000], 4, 4, 64, 32)
