@@ -53,9 +53,9 @@ static_assert(sizeof(KvItem) == 64, "item layout");
 //
 // An item costs its tiles of 128 tokens and kItemCost more (its queries, its base, its output).  Counting items
 // in the order (row group, KV head, column block, part), CTA b of n takes those that start within its n-th of the
-// total cost: equal shares whatever the contexts (32 rows of 16K to 64K tokens: the busiest CTA has 1.04 times
+// total cost: equal shares whatever the contexts (32 rows of 16K to 64K tokens: the busiest CTA has 1.09 times
 // the mean; with items dealt in turn it had 1.28 to 1.44 times).  A share is one run of neighbours.
-constexpr uint32_t kItemCost = 2;
+constexpr uint32_t kItemCost = 2;   // (3 and 4 measured the same)
 constexpr int kMaxGroup = 8;        // rows of a group
 constexpr int kSchedEntries = 512;  // running costs kept in shared memory, one for every so many groups
 

@@ -5,7 +5,7 @@
 // An FP8 token of a KV head is 256 bytes, so the bytes leave half the time of a bf16 one per column, and
 // warp-level MMAs, which need the codes as fp16 fragments, do not keep up (kv_attention.cu: 32 x 16K-64K
 // tokens in 327 us against 203 us at the copy bandwidth, nothing but conversions and issue slots in the
-// way).  Here the fifth-generation tensor cores take the codes as they lie in shared memory:
+// way; here 224 us).  The fifth-generation tensor cores take the codes as they lie in shared memory:
 //
 //     S^T[128 tokens x NC]  = K Q^T      A: the K tile (K-major), B: q as hi, then lo e4m3 terms
 //     O^T[128 dims x NC]   += V^T P^T    A: the V tile read MN-major, B: P as hi, then lo e4m3 terms (MN-major)
@@ -13,15 +13,24 @@
 // with NC (16, 32 or 64) columns, (row of the group, query head of the KV head) pairs, in N.  An MMA with so
 // small an N costs its A operand's passage: 40 cycles an SM for N <= 32, 48 for 64 measured, so a tile's
 // 16 take 640 to 770 of the 1,490 cycles that its 32 KB take at the copy bandwidth.  A token is a TMEM lane: a
-// softmax thread reads its token's scores of all columns, P = 2^(S - b) with a lazy base b per column, splits
+// softmax thread reads its token's scores of its columns, P = 2^(S - b) with a lazy base b per column, splits
 // each weight into hi + lo and writes its row of P.  The base moves, and O^T is rescaled in TMEM, only when a
-// score exceeds it by 2^8.7.  The softmax is what takes the issue slots: about 6 instructions a weight, with
-// packed fp32 pairs.
+// score exceeds it by 2^8.7.
 //
-// Roles: four softmax warps (TMEM lane quadrants), a TMA producer (K and V tiles of 16 KB through a ring of
-// units), an MMA issuer, a query warp (items and their query images).  Two persistent CTAs per SM take the
-// items (row group, KV head, column block, part of the context) in turn; parts are merged by
-// kv_combine_kernel (kv_attention.cu).
+// Roles: softmax warps (TMEM lane quadrants; one warpgroup, or two that share out 64 columns), a TMA producer
+// (K and V tiles of 16 KB through a ring each), an issuer of the scores' MMAs, one of the values' (an MMA's
+// issue lasts as long as its passage, so one thread for both would set the pace), a query warp (items and
+// their query images).  Two persistent CTAs per SM take equal shares of the items (row group, KV head, column
+// block, part of the context; kv_attention_common.cuh); parts are merged by kv_combine_kernel
+// (kv_attention.cu).
+//
+// What bounds it: for 16 columns the bytes once contexts are long (32 x 16K-64K: 224 us, 90% of the copy
+// bandwidth; tiles of one CTA follow each other in 1,400 cycles when the memory lets them).  An item costs 4,500
+// cycles more: its first base (a second look at the scores), the last product's passage, its output.  For 64
+// columns a tile takes 3,900 cycles, most of them the softmax warps' latencies (43% of the issue slots are used),
+// and a verify step of 4 x 64K tokens and 4 x 16 columns 99 us against 38 us of bytes: two blocks of 32 columns,
+// which read the cache twice, take 126 us, one warpgroup for all 64 columns 172 us, sums of weights in registers
+// (which then spill) 106 us.
 //
 // Precision: e4m3 x e4m3 products are exact and accumulate in fp32.  q is scaled by a power of two per
 // column and written as hi + lo (exact but for elements 2^-10 below the column's largest, which keep 2^-18 of
