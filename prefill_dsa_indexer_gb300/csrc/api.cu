@@ -650,7 +650,7 @@ static int check_rope_spec(const dsa_rope_spec *rope) {
 static bool apart(int64_t token_stride, int64_t tokens, int64_t head_stride, int64_t heads, int64_t rot) {
     if (heads == 1) return tokens == 1 || token_stride >= rot;
     if (tokens == 1) return head_stride >= rot;
-    return (head_stride >= rot && token_stride >= rot + (heads - 1) * head_stride) ||
+    return (head_stride >= rot && (token_stride - rot) / (heads - 1) >= head_stride) ||
            (token_stride >= rot && (head_stride - rot) / (tokens - 1) >= token_stride);
 }
 
