@@ -104,7 +104,8 @@ struct Cfg {
     static constexpr int OFF_MAX = OFF_ITEM + 2 * static_cast<int>(sizeof(Item));      // [kSoftmax][kMine] a warp's largest scores
     static constexpr int OFF_BASE = OFF_MAX + 4 * NC * 4;  // [kSoftmax][kMine] minus the bases, a copy per warp
     static constexpr int OFF_FAC = OFF_BASE + 4 * NC * 4;  // [kSoftmax][kMine] rescale factors
-    static constexpr int OFF_SUM = OFF_FAC + 4 * NC * 4;   // [2][kSoftmax][kMine] sums of weights, by item parity
+    static constexpr int OFF_MOVE = OFF_FAC + 4 * NC * 4;  // [kSoftmax][kMine] and their logarithms
+    static constexpr int OFF_SUM = OFF_MOVE + 4 * NC * 4;   // [2][kSoftmax][kMine] sums of weights, by item parity
     static constexpr int OFF_SCHED = OFF_SUM + 2 * 4 * NC * 4;
     static constexpr int OFF_BARS = OFF_SCHED + static_cast<int>(sizeof(KvSchedule));
     static constexpr int kNumBars = 2 * kUnits + 2 * 2 + 2 * 2 + kQBufs + 2 * kPBufs + 2;
@@ -516,6 +517,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
         float *max_s = reinterpret_cast<float *>(smem + C::OFF_MAX) + 4 * mine;  // [4][kMine], as the sums
         float *nbase = reinterpret_cast<float *>(smem + C::OFF_BASE) + warp * kMine;
         float *fac = reinterpret_cast<float *>(smem + C::OFF_FAC) + warp * kMine;
+        float *move = reinterpret_cast<float *>(smem + C::OFF_MOVE) + warp * kMine;
         uint32_t s_count = 0;                   // tiles
         uint32_t pv_open = 0, pv_phases = 0;    // a bit per buffer of P: a product is out whose end has not been seen
         if (more) {  // the first item's columns, four a warp and turn
@@ -622,14 +624,13 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     }
                 };
                 float x[kMine];
-                // at most twice round: the first tile sets the bases, later ones move those that no longer fit
-#pragma unroll 1
-                for (bool settled = false;;) {
-                    float top = -INFINITY;
-                    scores(x);
+                scores(x);
+                float top = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < kMine; j += 2) top = fmaxf(top, fmaxf(x[j], x[j + 1]));
-                    if (settled || (i > 0 && !meet_any(top > kTop || dead))) break;
+                for (int j = 0; j < kMine; j += 2) top = fmaxf(top, fmaxf(x[j], x[j + 1]));
+                // the first tile sets the bases; later, when a score no longer fits, all columns' are raised to where a
+                // move leaves them, so that the next one is further off
+                if (i == 0 || meet_any(top > kTop || dead)) {
                     max_columns<kMine>(x, max_s + (warp & 3) * kMine, lane);
                     if (i == 0 ? someone_dead() : meet_any(dead)) {
                         leave = true;
@@ -640,11 +641,20 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     for (int n = lane; n < kMine; n += 32) {
                         const float m = fmaxf(fmaxf(max_s[n], max_s[kMine + n]),
                                               fmaxf(max_s[2 * kMine + n], max_s[3 * kMine + n]));
-                        const bool on = i == 0 ? m > -INFINITY : m > kTop;
-                        fac[n] = on && i > 0 ? ex2(kBias - m) : 1.f;
-                        if (on) nbase[n] += kBias - m;
+                        const float by = m > (i == 0 ? -INFINITY : kBias) ? kBias - m : 0.f;
+                        move[n] = by;
+                        fac[n] = ex2(by);
+                        nbase[n] += by;
                     }
                     __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < kMine; j += 4) {
+                        const float4 by = *reinterpret_cast<const float4 *>(move + j);
+                        x[j] += by.x;
+                        x[j + 1] += by.y;
+                        x[j + 2] += by.z;
+                        x[j + 3] += by.w;
+                    }
                     if (i > 0) {
                         if (!C::kSumsInTmem) {
 #pragma unroll
@@ -666,9 +676,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                         }
                         tmem_st_wait();
                     }
-                    settled = true;
                 }
-                if (leave) break;
                 pv_wait(pb);  // this buffer of P is free
 
                 // weights: unit c / 16 of the token's row of P holds hi, unit (NC + c) / 16 lo.  hi is the weight
