@@ -833,11 +833,11 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
             }
             reduce_columns<kMine>(l, sums + (warp & 3) * kMine, lane);
             if (someone_dead()) break;
-            // a column's factor: 1 for a part of several, else 1 / its sum (0 without any weight)
+            // a column's factor where the part is the whole: 1 / its sum (0 without any weight)
 #pragma unroll 1
             for (int n = lane; n < kMine; n += 32) {
                 const float total = sums[n] + sums[kMine + n] + sums[2 * kMine + n] + sums[3 * kMine + n];
-                fac[n] = tiles == 0 ? 0.f : parts > 1 ? 1.f : total == 0.f ? 0.f : a.v_scale / total;
+                fac[n] = total == 0.f ? 0.f : a.v_scale / total;
                 if ((warp & 3) == 0 && mine + n < ncols) {
                     const float b = -nbase[n];
                     const int at = cs->at[mine + n];
@@ -865,14 +865,26 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     tmem_ld_wait();
                     reg_fence(h);
                 }
+                const int here = ncols - mine - c;
+                if (parts > 1) {  // (so the part has tiles)
+                    float *dst = a.part_o + part * kDim + self;
+                    const int64_t row = static_cast<int64_t>(a.parts_bound) * kDim;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    if (mine + c + j >= ncols) break;
-                    const float f = fac[c + j];
-                    const float o = f == 0.f ? 0.f : __uint_as_float(h[j]) * f;  // (without a tile it is no output)
-                    const int64_t at = cs->at[mine + c + j];
-                    if (parts > 1) a.part_o[(at * a.parts_bound + part) * kDim + self] = o;
-                    else a.out[at * kDim + self] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+                    for (int j = 0; j < 16; j += 4) {
+                        const int4 at = *reinterpret_cast<const int4 *>(cs->at + mine + c + j);
+                        if (j < here) dst[at.x * row] = __uint_as_float(h[j]);
+                        if (j + 1 < here) dst[at.y * row] = __uint_as_float(h[j + 1]);
+                        if (j + 2 < here) dst[at.z * row] = __uint_as_float(h[j + 2]);
+                        if (j + 3 < here) dst[at.w * row] = __uint_as_float(h[j + 3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (j >= here) break;
+                        const float f = fac[c + j], o = f == 0.f ? 0.f : __uint_as_float(h[j]) * f;
+                        a.out[static_cast<int64_t>(cs->at[mine + c + j]) * kDim + self] =
+                            __bfloat16_as_ushort(__float2bfloat16_rn(o));
+                    }
                 }
             }
             tc_fence_before();
