@@ -16,14 +16,15 @@ namespace kv {
 // request make 128 parts, but at least 16 of a head: fewer leave SMs idle under one request, and every part costs
 // its queries, its first base and its output beside its tiles.  Measured (4 KV heads of 128):
 //                                        64 parts   128 parts   256 parts
-//   bf16, 1 x 128K (40 us of bytes)        64.6        43.2        43.3 us
-//   bf16, 4 x 32K                          42.7        45.6        48.6
-//   FP8, 1 x 128K (20 us)                  61.4        35.4        28.2
-//   FP8, 24 x 8K (30 us)                   46.9        55.4        77.9
+//   bf16, 1 x 128K (40 us of bytes)        64.5        43.2        43.4 us
+//   bf16, 4 x 32K                          42.4        45.8        48.6
+//   FP8, 1 x 128K (20 us)                  59.9        34.2        27.6
+//   FP8, 24 x 8K (30 us)                   43.5        49.0        48.9
+//   FP8, 32 x 16K-64K (203 us)                         222         232
 //   parts of at least                     128 tokens  256         512
-//   bf16, one row of 4K                    10.0         9.6        11.0 us
-//   FP8, 24 x 2K (7.6 us)                  27.2        21.6        21.4
-//   FP8, 1 x 2K, 64 columns                12.8        13.8        17.7
+//   bf16, one row of 4K                     9.4         9.5        11.0 us
+//   FP8, 24 x 2K (7.6 us)                  24.6        19.8        20.0
+//   FP8, 1 x 2K, 64 columns                12.2        13.3        17.1
 constexpr int32_t kPartMin = 8;
 
 __host__ __device__ __forceinline__ int32_t kv_parts_shift(int32_t kv_heads) {

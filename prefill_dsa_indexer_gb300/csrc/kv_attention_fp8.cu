@@ -5,7 +5,7 @@
 // An FP8 token of a KV head is 256 bytes, so the bytes leave half the time of a bf16 one per column, and
 // warp-level MMAs, which need the codes as fp16 fragments, do not keep up (kv_attention.cu: 32 x 16K-64K
 // tokens in 327 us against 203 us at the copy bandwidth, nothing but conversions and issue slots in the
-// way; here 224 us).  The fifth-generation tensor cores take the codes as they lie in shared memory:
+// way; here 222 us).  The fifth-generation tensor cores take the codes as they lie in shared memory:
 //
 //     S^T[128 tokens x NC]  = K Q^T      A: the K tile (K-major), B: q as hi, then lo e4m3 terms
 //     O^T[128 dims x NC]   += V^T P^T    A: the V tile read MN-major, B: P as hi, then lo e4m3 terms (MN-major)
@@ -24,13 +24,15 @@
 // block, part of the context; kv_attention_common.cuh); parts are merged by kv_combine_kernel
 // (kv_attention.cu).
 //
-// What bounds it: for 16 columns the bytes once contexts are long (32 x 16K-64K: 224 us, 90% of the copy
-// bandwidth; tiles of one CTA follow each other in 1,400 cycles when the memory lets them).  An item costs 4,500
-// cycles more: its first base (a second look at the scores), the last product's passage, its output.  For 64
-// columns a tile takes 3,900 cycles, most of them the softmax warps' latencies (43% of the issue slots are used),
-// and a verify step of 4 x 64K tokens and 4 x 16 columns 99 us against 38 us of bytes: two blocks of 32 columns,
-// which read the cache twice, take 126 us, one warpgroup for all 64 columns 172 us, sums of weights in registers
-// (which then spill) 106 us.
+// What bounds it: for 16 columns the bytes once contexts are long (32 x 16K-64K: 222 us, 91% of the copy
+// bandwidth; tiles of one CTA follow each other in 1,200 cycles when the memory lets them, an item costs about 4,000
+// cycles more: its first base, the last product's passage, its output).  Short parts show that, and the 7,000
+// cycles from the launch to the first tile (24 x 8K: 49 us against 30 us of bytes).  Writing an item's output behind
+// the next one's first weights, into a second buffer of outputs, was slower (51 us): the other CTA of the SM fills the
+// wait already.  For 64 columns a tile takes some 3,600 cycles, most of them the softmax warps' latencies (fewer than
+// half of the issue slots are used), and a verify step of 4 x 64K tokens and 4 x 16 columns 93 us against 38 us of
+// bytes.  (When it took 99: two blocks of 32 columns, which read the cache twice, 126 us, one warpgroup for all 64
+// columns 172 us, sums of weights in registers, which then spill, 106 us.)
 //
 // Precision: e4m3 x e4m3 products are exact and accumulate in fp32.  q is scaled by a power of two per
 // column and written as hi + lo (exact but for elements 2^-10 below the column's largest, which keep 2^-18 of
