@@ -153,6 +153,66 @@ __device__ __forceinline__ int merge_at(int n, int d) {
     return n * D + (d ^ ((n >> 1 & 3) << 3));
 }
 
+// A turn of the queries: of 32 / kUnits neighbouring columns from `n` (of the CTA's) on, a unit of 16 dims per lane.
+template <int D>
+struct QueryTurn {
+    static constexpr int kUnits = D / 16, kTurnCols = 32 / kUnits;
+    uint4 v0, v1;
+
+    __device__ __forceinline__ void load(const KvAttnArgs &a, const KvCursor &w, int n, int cols, int hpg, int lane) {
+        const int col = w.col0 + n + lane / kUnits;
+        v0 = v1 = make_uint4(0u, 0u, 0u, 0u);
+        if (col < cols) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (w.row0 + col / hpg) * a.q_stride +
+                                                               static_cast<int64_t>(w.g * hpg + col % hpg) * D +
+                                                               lane % kUnits * 16);
+            v0 = src[0];
+            v1 = src[1];
+        }
+    }
+
+    // Into a column warp's place in 16 bits, columns as rows, with each column's scale and context.
+    template <bool kFp8>
+    __device__ __forceinline__ void put(uint8_t *queries, float2 *cols_s, const KvAttnArgs &a, const KvCursor &w, int n,
+                                        int cols, int hpg, int lane) {
+        const int unit = lane % kUnits;
+        n += lane / kUnits;
+        const int col = w.col0 + n;
+        const int ctx = __shfl_sync(0xffffffffu, w.my_ctx, col < cols ? col / hpg : 0);
+        float scale = a.s_scale;
+        if constexpr (kFp8) {
+            const uint32_t h[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            float amax = 0.f;
+#pragma unroll
+            for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(h[y])), fabsf(bf16_hi(h[y]))));
+#pragma unroll
+            for (int y = 1; y < kUnits; y <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
+            // 2^e brings the column's largest |q| to [2^13, 2^14); infinities and NaN stay what they are
+            int e = 0;
+            if (amax > 0.f && amax <= 3.4e38f) {
+                e = 140 - static_cast<int>(__float_as_uint(amax) >> 23);
+                e = max(-120, min(120, e));
+            }
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            scale *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            uint32_t f[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) f[y] = pack_f16(bf16_lo(h[y]) * up, bf16_hi(h[y]) * up);
+            // K's codes come four dims to a lane (ldmatrix moves byte pairs): the k slots of its low
+            // and high pairs hold dims 4j, 4j + 1 and 4j + 2, 4j + 3; q's in the same order
+            v0 = make_uint4(f[0], f[2], f[4], f[6]);
+            v1 = make_uint4(f[1], f[3], f[5], f[7]);
+        }
+        // a masked score is -inf times this: neither zero nor infinity
+        if (unit == 0)
+            cols_s[n] = make_float2(fminf(fmaxf(scale, 1.17549435e-38f), 3.40282347e38f),
+                                    __int_as_float(col < cols ? ctx : 0));
+        uint8_t *dst = queries + (n >> 4) * (16 * D * 2);
+        *reinterpret_cast<uint4 *>(dst + q_unit_at<D>(n & 15, 2 * unit)) = v0;
+        *reinterpret_cast<uint4 *>(dst + q_unit_at<D>(n & 15, 2 * unit + 1)) = v1;
+    }
+};
+
 // kWide: more than 8 columns per warp (two n-tiles of the second product).
 template <bool kFp8, int D, bool kWide, int kColWarps>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -194,6 +254,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     const int hpg = a.num_heads / a.kv_heads, cols = a.group * hpg;
     const int gi = lane >> 2, ji = lane & 3;
+    KvCursor w;
+    bool more = w.first<kCols>(a, sched, lane);
+    using Turn = QueryTurn<D>;
 
     if (warp == kProducer) {
         // ---- K and V: boxes of at most kTile rows, lane b issues box b of a tile
@@ -205,8 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         int s = 0, issued = 0;
         uint32_t phase = 1;
         bool go = true;
-        KvCursor w;
-        for (bool more = w.first<kCols>(a, sched, lane); more && go; more = w.next<kCols>(a, lane)) {
+        for (; more && go; more = w.next<kCols>(a, lane)) {
             const int num_pages = (w.t_end + a.page_size - 1) >> a.page_shift;
             const int32_t *table = a.block_table + static_cast<int64_t>(w.req) * a.bt_stride;
             auto load_ids = [&](int p) { return p + lane < num_pages ? table[p + lane] : 0; };
@@ -268,72 +330,32 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 
     if (warp == kQuery) {
-        // ---- items, and their queries in 16 bits, columns as rows
+        // ---- items and their queries.  Neighbours of one row group and KV head share them; the first item's are the
+        // consumers' work
         uint32_t phase = 1;
-        KvCursor w;
-        for (bool more = w.first<kCols>(a, sched, lane); more; more = w.next<kCols>(a, lane)) {
+        bool fresh = false;
+        if (more) named_bar_sync(2, 32 * (kConsumers + 1));
+        for (; more; more = w.next<kCols>(a, lane)) {
             if (w.bad && w.part == 0 && lane == 0) report(a.status, DSA_ERR_BOUNDS);
-            // 16 dims (a unit) of a column per lane and turn: a column's units are in neighbouring lanes.  The
-            // first 16 columns are loaded while the consumers still have the item before
-            constexpr int kUnits = D / 16, kTurns = kUnits / 2;  // 32 / kUnits columns per turn, 16 in all
-            const int unit = lane % kUnits;
-            uint4 v0[kTurns], v1[kTurns];
+            // the first 16 columns are loaded while the consumers still have the item before
+            constexpr int kTurns = 16 / Turn::kTurnCols;
+            Turn turns[kTurns];
             auto load = [&](int c0) {
 #pragma unroll
-                for (int i = 0; i < kTurns; ++i) {
-                    const int n = w.col0 + c0 + i * (32 / kUnits) + lane / kUnits;
-                    v0[i] = v1[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (n < cols) {
-                        const uint4 *src = reinterpret_cast<const uint4 *>(
-                            a.q + (w.row0 + n / hpg) * a.q_stride + static_cast<int64_t>(w.g * hpg + n % hpg) * D + unit * 16);
-                        v0[i] = src[0];
-                        v1[i] = src[1];
-                    }
-                }
+                for (int i = 0; i < kTurns; ++i) turns[i].load(a, w, c0 + i * Turn::kTurnCols, cols, hpg, lane);
             };
-            load(0);
+            if (fresh) load(0);
             if (!wait_mbar_warp(q_empty, phase, abort)) return gave_up(abort, a.status);
             phase ^= 1;
 #pragma unroll 1
-            for (int c = 0; c < kColWarps; ++c) {
+            for (int c = 0; c < kCols && fresh; c += 16) {
 #pragma unroll
-                for (int i = 0; i < kTurns; ++i) {
-                    const int n = i * (32 / kUnits) + lane / kUnits, col = w.col0 + 16 * c + n;
-                    const int ctx = __shfl_sync(0xffffffffu, w.my_ctx, col < cols ? col / hpg : 0);
-                    float scale = a.s_scale;
-                    if constexpr (kFp8) {
-                        const uint32_t h[8] = {v0[i].x, v0[i].y, v0[i].z, v0[i].w, v1[i].x, v1[i].y, v1[i].z, v1[i].w};
-                        float amax = 0.f;
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(h[y])), fabsf(bf16_hi(h[y]))));
-#pragma unroll
-                        for (int y = 1; y < kUnits; y <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, y));
-                        // 2^e brings the column's largest |q| to [2^13, 2^14); infinities and NaN stay what they are
-                        int e = 0;
-                        if (amax > 0.f && amax <= 3.4e38f) {
-                            e = 140 - static_cast<int>(__float_as_uint(amax) >> 23);
-                            e = max(-120, min(120, e));
-                        }
-                        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                        scale *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                        uint32_t f[8];
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) f[y] = pack_f16(bf16_lo(h[y]) * up, bf16_hi(h[y]) * up);
-                        // K's codes come four dims to a lane (ldmatrix moves byte pairs): the k slots of its low
-                        // and high pairs hold dims 4j, 4j + 1 and 4j + 2, 4j + 3; q's in the same order
-                        v0[i] = make_uint4(f[0], f[2], f[4], f[6]);
-                        v1[i] = make_uint4(f[1], f[3], f[5], f[7]);
-                    }
-                    // a masked score is -inf times this: neither zero nor infinity
-                    if (unit == 0)
-                        cols_s[16 * c + n] = make_float2(fminf(fmaxf(scale, 1.17549435e-38f), 3.40282347e38f),
-                                                         __int_as_float(col < cols ? ctx : 0));
-                    uint8_t *dst = smem + C::OFF_Q + c * C::kQBytes;
-                    *reinterpret_cast<uint4 *>(dst + q_unit_at<D>(n, 2 * unit)) = v0[i];
-                    *reinterpret_cast<uint4 *>(dst + q_unit_at<D>(n, 2 * unit + 1)) = v1[i];
-                }
-                if (c + 1 < kColWarps) load(16 * (c + 1));
+                for (int i = 0; i < kTurns; ++i)
+                    turns[i].template put<kFp8>(smem + C::OFF_Q, cols_s, a, w, c + i * Turn::kTurnCols, cols, hpg, lane);
+                if (c + 16 < kCols) load(c + 16);
             }
+            // the item after this one: a part more of the same row group and KV head?
+            fresh = !(w.part + 1 < w.parts && w.start + kItemCost + ((w.t_end - w.t_begin + 127) >> 7) < w.end);
             if (lane < 8) item_s->ctx[lane] = w.my_ctx;
             if (lane == 0) {
                 item_s->live = 1;
@@ -357,6 +379,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 
     // ---- consumers
+    if (more) {
+#pragma unroll 1
+        for (int n = warp * Turn::kTurnCols; n < kCols; n += kConsumers * Turn::kTurnCols) {
+            Turn t;
+            t.load(a, w, n, cols, hpg, lane);
+            t.template put<kFp8>(smem + C::OFF_Q, cols_s, a, w, n, cols, hpg, lane);
+        }
+        asm volatile("bar.arrive 2, %0;" ::"n"(32 * (kConsumers + 1)) : "memory");
+    }
     const int cw = warp % kColWarps, tw = warp / kColWarps;
     int s = 0;
     uint32_t phase = 0, q_phase = 0;
