@@ -486,14 +486,6 @@ def _host_ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _device(t):
-    """Index of a device tensor's device."""
-    d = t.get_device()
-    if d < 0:
-        raise DsaError("libdsa takes device tensors only")
-    return d
-
-
 def _expect(t, what, device, dtypes, shape=None):
     """Raise unless t is a tensor on device `device` of one of `dtypes` and, where given, of `shape`."""
     d = t.get_device()
@@ -527,7 +519,8 @@ def _launch(what, device, stream, *args):
         _check(rc, what)
 
 
-_I32, _F32, _BF16 = (torch.int32,), (torch.float32,), (torch.bfloat16,)
+_int32, _float32, _bfloat16 = torch.int32, torch.float32, torch.bfloat16
+_I32, _F32, _BF16 = (_int32,), (_float32,), (_bfloat16,)
 
 # The calls of a decode step are short, so their arguments are packed into bytes (in the C structs' layouts) for
 # function objects of their own that take those, which costs a fraction of ctypes structures.
@@ -590,16 +583,21 @@ def rope_table(rot_dim, theta=10000.0, scaling="none", factor=1.0, trained_ctx=0
 def _rope_spec(table, positions, device, num_tokens):
     if table.device != device:
         raise DsaError(f"the rotary table is on device {table.device}, the call's other tensors on device {device}")
-    return _PACK_ROPE_SPEC(table.address, _flat(positions, "positions", device, _I32, (num_tokens,)), table.rot_dim,
-                           table.scale)
+    if positions.dtype is not _int32 or positions.shape != (num_tokens,) or positions.get_device() != device:
+        _expect(positions, "positions", device, _I32, (num_tokens,))
+    if not positions.is_contiguous():
+        raise DsaError("positions is not contiguous")
+    return _PACK_ROPE_SPEC(table.address, positions.data_ptr(), table.rot_dim, table.scale)
 
 
 def _rope_tensor(x, out, layout, rot_dim, device, dtype, num_tokens):
     """The fields of a dsa_rope_tensor."""
     shape = x.shape
-    if len(shape) != 3 or shape[2] != rot_dim or shape[0] != num_tokens:
-        raise DsaError(f"rotated tensors are [{num_tokens}, heads, {rot_dim}] (a slice of larger heads): got {tuple(shape)}")
-    if x.dtype is not dtype or x.get_device() != device:
+    if x.dtype is not dtype or len(shape) != 3 or shape[2] != rot_dim or shape[0] != num_tokens or \
+            x.get_device() != device:
+        if len(shape) != 3 or shape[2] != rot_dim or shape[0] != num_tokens:
+            raise DsaError(
+                f"rotated tensors are [{num_tokens}, heads, {rot_dim}] (a slice of larger heads): got {tuple(shape)}")
         _expect(x, "x", device, (dtype,))
     a, b, c = x.stride()
     p = x.data_ptr()
@@ -619,22 +617,31 @@ def rope(x, table, positions, layout=ROPE_INTERLEAVED, out=None, stream=None):
     """dsa_rope: rotate x [tokens, heads, rot_dim] (bf16 or fp32; usually a slice x[..., a:a + rot_dim]) by
     its tokens' positions, into `out` (default: in place).  x, layout and out may be lists of up to 4
     tensors of the same tokens, rotated by one launch.  Tokens at negative positions are left alone."""
-    many = isinstance(x, (list, tuple))
-    xs = x if many else [x]
-    outs = xs if out is None else out if many else [out]
-    layouts = layout if isinstance(layout, (list, tuple)) else [layout] * len(xs)
-    if not 1 <= len(xs) <= ROPE_MAX_TENSORS or len(outs) != len(xs) or len(layouts) != len(xs):
-        raise DsaError(f"rope takes 1 to {ROPE_MAX_TENSORS} tensors, and as many layouts and outputs")
-    first = xs[0]
-    n, device, dtype = first.shape[0], _device(first), first.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+    if type(x) is list or type(x) is tuple:
+        many, count, first = True, len(x), x[0] if x else None
+        layouts = layout if type(layout) is list or type(layout) is tuple else [layout] * count
+        outs = x if out is None else out
+        if not 1 <= count <= ROPE_MAX_TENSORS or len(outs) != count or len(layouts) != count:
+            raise DsaError(f"rope takes 1 to {ROPE_MAX_TENSORS} tensors, and as many layouts and outputs")
+    else:
+        many, count, first = False, 1, x
+        if isinstance(layout, (list, tuple)):
+            raise DsaError("one tensor has one layout")
+    n, device, dtype, rot = first.shape[0], first.get_device(), first.dtype, table.rot_dim
+    if device < 0:
+        raise DsaError("libdsa takes device tensors only")
+    if dtype is not _bfloat16 and dtype is not _float32:
         raise DsaError(f"rope takes bf16 or fp32 tensors: got {dtype}")
-    fields, rot = [], table.rot_dim
-    for a, b, p in zip(xs, outs, layouts):
-        fields += _rope_tensor(a, b, p, rot, device, dtype, n)
-    _launch("dsa_rope", device, stream, _rope_spec(table, positions, device, n), _PACK_ROPE_TENSORS[len(xs)](*fields),
-            len(xs), DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_FP32, n)
-    return outs if many else outs[0]
+    if many:
+        fields = []
+        for i in range(count):
+            fields += _rope_tensor(x[i], outs[i], layouts[i], rot, device, dtype, n)
+    else:
+        outs = x if out is None else out
+        fields = _rope_tensor(x, outs, layout, rot, device, dtype, n)
+    _launch("dsa_rope", device, stream, _rope_spec(table, positions, device, n), _PACK_ROPE_TENSORS[count](*fields),
+            count, DTYPE_BF16 if dtype is _bfloat16 else DTYPE_FP32, n)
+    return outs
 
 
 class KvCache:
@@ -660,10 +667,17 @@ def kv_insert(kv, slots, k, v, rope=None, positions=None, layout=ROPE_HALF, rot_
     the KvCache.  With `rope` (a RopeTable) and `positions`, K's dims [rot_offset, rot_offset + rot_dim) are
     rotated first, and q [tokens, heads, rot_dim] too, into q_out (default: in place).  Returns q_out."""
     n, device, heads, dim = slots.shape[0], kv.device, kv.kv_heads, kv.head_dim
+    if slots.dim() != 1:
+        raise DsaError(f"slots is [tokens]: got {tuple(slots.shape)}")
     shape, width = (n, heads, dim), heads * dim
-    for t, what in ((k, "k"), (v, "v")):
-        if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != device:
-            _expect(t, what, device, _BF16, shape)
+    if k.dtype is not _bfloat16 or k.shape != shape or k.get_device() != device:
+        _expect(k, "k", device, _BF16, shape)
+    if v.dtype is not _bfloat16 or v.shape != shape or v.get_device() != device:
+        _expect(v, "v", device, _BF16, shape)
+    if slots.dtype is not _int32 or slots.get_device() != device:
+        _expect(slots, "slots", device, _I32)
+    if not slots.is_contiguous():
+        raise DsaError("slots is not contiguous")
     k_stride, b, c = k.stride()
     v_stride, d, e = v.stride()
     if c != 1 or e != 1 or (heads > 1 and (b != dim or d != dim)):
@@ -677,10 +691,10 @@ def kv_insert(kv, slots, k, v, rope=None, positions=None, layout=ROPE_HALF, rot_
         spec = _rope_spec(rope, positions, device, n)
         if q is not None:
             q_out = q if q_out is None else q_out
-            qt = _PACK_ROPE_TENSORS[1](*_rope_tensor(q, q_out, layout, rope.rot_dim, device, torch.bfloat16, n))
+            qt = _PACK_ROPE_TENSORS[1](*_rope_tensor(q, q_out, layout, rope.rot_dim, device, _bfloat16, n))
     elif q is not None:
         raise DsaError("q is rotated only: it needs rope")
-    _launch("dsa_kv_insert", device, stream, kv._packed, _flat(slots, "slots", device, _I32), n,
+    _launch("dsa_kv_insert", device, stream, kv._packed, slots.data_ptr(), n,
             _PACK_KV_ROWS(k.data_ptr(), v.data_ptr(), k_stride, v_stride, rot_offset, layout), spec, qt,
             None if status is None else _flat(status, "status", device, _I32))
     return q_out
@@ -709,7 +723,7 @@ def kv_attention(kv, block_table, row_req, row_ctx, max_ctx, q, sm_scale=None, r
     keep the workspace alive: pass one that outlives it, and no other call that may run beside it uses."""
     R, H, D = q.shape
     device = kv.device
-    if D != kv.head_dim or q.dtype is not torch.bfloat16 or q.get_device() != device:
+    if D != kv.head_dim or q.dtype is not _bfloat16 or q.get_device() != device:
         _expect(q, "q", device, _BF16, (R, H, kv.head_dim))
     a, b, c = q.stride()
     if c != 1 or (b != D and H > 1):

@@ -679,6 +679,19 @@ def test_binding_refusals():
                 dict(rope=table, positions=pos, q=k[:2]), dict(rope=table, positions=pos, q=k.float())):
         with pytest.raises(P.DsaError):
             ins(**bad)
+    for bad in (dict(slots=slots[:, None]), dict(slots=slots[:2]), dict(slots=torch.arange(6, dtype=torch.int32,
+                                                                                           device="cuda")[::2]),
+                dict(slots=slots.cpu()), dict(v=k.cpu()), dict(v=k[..., :32])):
+        with pytest.raises(P.DsaError):
+            ins(**bad)
+    rope = lambda x=k, pos=pos, **kw: P.rope(x, table, pos, **kw)  # noqa: E731
+    for bad in (dict(x=[]), dict(x=[k] * 5), dict(x=k[0]), dict(x=k.half()), dict(x=k.cpu()), dict(x=k[..., :32]),
+                dict(x=[k, k]), dict(x=[k, k[:2]]), dict(x=[k, k.float()], out=[k.clone(), k.float()]),
+                dict(layout=[0]), dict(x=[k], layout=[0, 1]), dict(out=k[:2].clone()), dict(out=k.float()),
+                dict(pos=pos[:2]), dict(pos=pos.long()), dict(pos=pos[:, None]), dict(layout=7),
+                dict(x=k.transpose(1, 2).contiguous().transpose(1, 2))):
+        with pytest.raises(P.DsaError):
+            rope(**bad)
     x = randn(gen(1), 3, 2, 64)
     for bad in (dict(x=x.half()), dict(x=x[..., :32]), dict(x=[x] * 5), dict(x=[x, x[:2]]), dict(x=x[0]),
                 dict(x=x, out=x.float()), dict(x=x, out=x[:2]), dict(x=x.cpu()), dict(x=[x], layout=[0, 1])):
