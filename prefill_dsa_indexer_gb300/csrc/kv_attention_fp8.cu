@@ -29,8 +29,8 @@
 // cycles more: its first base, the last product's passage, its output).  Short parts show that, and the 7,000
 // cycles from the launch to the first tile (24 x 8K: 49 us against 30 us of bytes).  Writing an item's output behind
 // the next one's first weights, into a second buffer of outputs, was slower (51 us): the other CTA of the SM fills the
-// wait already.  For 64 columns a tile takes some 3,600 cycles, most of them the softmax warps' latencies (fewer than
-// half of the issue slots are used), and a verify step of 4 x 64K tokens and 4 x 16 columns 93 us against 38 us of
+// wait already.  For 64 columns a tile takes some 4,000 cycles, most of them the softmax warps' latencies (fewer than
+// half of the issue slots are used), and a verify step of 4 x 64K tokens and 4 x 16 columns 92 us against 38 us of
 // bytes.  (When it took 99: two blocks of 32 columns, which read the cache twice, 126 us, one warpgroup for all 64
 // columns 172 us, sums of weights in registers, which then spill, 106 us.)
 //
