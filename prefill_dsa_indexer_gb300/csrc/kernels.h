@@ -333,6 +333,9 @@ struct KvAttnArgs {
     int32_t *status;
     // set by launch_kv_attention
     int32_t page_shift;    // log2 page_size
+    int32_t hpg;           // query heads per KV head
+    int32_t groups;        // row groups, and how many share one of how many entries of a CTA's table of costs
+    int32_t sched_per, sched_entries;
     uint32_t hpg_mul;      // ceil(2^20 / hpg): column n is of row n * hpg_mul >> 20 of its group (n < 1024, hpg <= 128)
     int32_t parts_shift;   // log2 of the parts of the longest contexts
     uint32_t parts_bound;  // parts of a row at most, for contexts up to max_ctx

@@ -153,6 +153,11 @@ __device__ __forceinline__ int merge_at(int n, int d) {
     return n * D + (d ^ ((n >> 1 & 3) << 3));
 }
 
+// The row of its group that a column belongs to.
+__device__ __forceinline__ int row_of(const KvAttnArgs &a, int col) {
+    return static_cast<int>(static_cast<uint32_t>(col) * a.hpg_mul >> 20);
+}
+
 // A turn of the queries: of 32 / kUnits neighbouring columns from `n` (of the CTA's) on, a unit of 16 dims per lane.
 template <int D>
 struct QueryTurn {
@@ -163,8 +168,9 @@ struct QueryTurn {
         const int col = w.col0 + n + lane / kUnits;
         v0 = v1 = make_uint4(0u, 0u, 0u, 0u);
         if (col < cols) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (w.row0 + col / hpg) * a.q_stride +
-                                                               static_cast<int64_t>(w.g * hpg + col % hpg) * D +
+            const int row = row_of(a, col);
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (w.row0 + row) * a.q_stride +
+                                                               static_cast<int64_t>(w.g * hpg + col - row * hpg) * D +
                                                                lane % kUnits * 16);
             v0 = src[0];
             v1 = src[1];
@@ -178,7 +184,7 @@ struct QueryTurn {
         const int unit = lane % kUnits;
         n += lane / kUnits;
         const int col = w.col0 + n;
-        const int ctx = __shfl_sync(0xffffffffu, w.my_ctx, col < cols ? col / hpg : 0);
+        const int ctx = __shfl_sync(0xffffffffu, w.my_ctx, col < cols ? row_of(a, col) : 0);
         float scale = a.s_scale;
         if constexpr (kFp8) {
             const uint32_t h[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     kv_fill_schedule(a, sched);
     __syncthreads();
 
-    const int hpg = a.num_heads / a.kv_heads, cols = a.group * hpg;
+    const int hpg = a.hpg, cols = a.group * hpg;
     const int gi = lane >> 2, ji = lane & 3;
     KvCursor w;
     bool more = w.first<kCols>(a, sched, lane);
@@ -417,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             cx[x] = __float_as_int(v.y);
         }
         // the rows of the group among this warp's columns, and lane i's the context of row i
-        const int row_lo = col0 / hpg, row_hi = min(col0 + 15, cols - 1) / hpg;
+        const int row_lo = row_of(a, col0), row_hi = row_of(a, min(col0 + 15, cols - 1));
         const int row_ctx = item_s->ctx[lane & 7];
         const bool idle = col0 >= cols;
         __syncwarp();
@@ -542,7 +548,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int x = 0; x < NT; ++x)
 #pragma unroll
-                            for (int y = 0; y < 2; ++y) mine[x][y] = (col0 + 8 * x + 2 * ji + y) / hpg == row;
+                            for (int y = 0; y < 2; ++y)
+                                mine[x][y] = static_cast<uint32_t>(col0 + 8 * x + 2 * ji + y - row * hpg) <
+                                             static_cast<uint32_t>(hpg);
                     }
                     auto accumulate = [&](float(&acc)[NT][4], uint4 v, int y) {  // 16 tokens y of the step
                         if constexpr (kEdge) {
@@ -615,6 +623,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
 
         // ---- output
+        auto place_of = [&](int col) {  // row * num_heads + head
+            const int row = row_of(a, col);
+            return static_cast<int64_t>(row0 + row) * a.num_heads + g * hpg + col - row * hpg;
+        };
         auto finish = [&](int64_t at, int d, const float4 &x, float b, float total) {  // dims d .. d + 3 of head `at`
             if (parts > 1) {
                 *reinterpret_cast<float4 *>(a.part_o + (at * a.parts_bound + part) * D + d) = x;
@@ -681,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     x.w += y.w * f;
                 }
                 const int col = col0 - 16 * cw + n;
-                finish(static_cast<int64_t>(row0 + col / hpg) * a.num_heads + g * hpg + col % hpg, d, x, b0, total);
+                finish(place_of(col), d, x, b0, total);
             }
             fence_async_smem();  // the stage goes back to TMA writes
             __syncwarp();
@@ -699,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const float b = __shfl_sync(0xffffffffu, base[n], 8 * ji + 4 * y);
                     const float total = __shfl_sync(0xffffffffu, sum[n], 8 * ji + 4 * y);
                     const int col = col0 + 8 * n + 2 * ji + y;
-                    const int64_t at = static_cast<int64_t>(row0 + col / hpg) * a.num_heads + g * hpg + col % hpg;
+                    const int64_t at = place_of(col);
 #pragma unroll
                     for (int m = 0; m < KS; ++m) {
                         // own: dims {p, q}; FP8: 2 gi, 2 gi + 1 of 16 m; else gi, gi + 8
@@ -840,6 +852,7 @@ cudaError_t launch_kv_attention(KvAttnArgs &a, void *workspace, cudaStream_t s) 
     if (a.num_rows == 0) return cudaSuccess;
     for (a.page_shift = 4; 1 << a.page_shift < a.page_size;) ++a.page_shift;
     const uint32_t hpg = static_cast<uint32_t>(a.num_heads / a.kv_heads);
+    a.hpg = static_cast<int32_t>(hpg);
     a.hpg_mul = ((1u << 20) + hpg - 1) / hpg;
     a.parts_shift = kv_parts_shift(a.kv_heads);
     a.parts_bound = kv_parts_bound(a.max_ctx, a.parts_shift);

@@ -74,12 +74,11 @@ __device__ __forceinline__ bool kv_direct(const KvAttnArgs &a) { return a.items 
 // Fills `sched`; every thread of the CTA calls it, then __syncthreads.
 __device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule *sched) {
     if (kv_direct(a)) return;
-    const int groups = a.num_rows / a.group;
-    const int per = (groups + kSchedEntries - 1) / kSchedEntries, entries = (groups + per - 1) / per;
+    const int per = a.sched_per, entries = a.sched_entries;
     for (int e = threadIdx.x; e < entries; e += blockDim.x) {
         uint64_t sum = 0;
 #pragma unroll 1
-        for (int gi = e * per; gi < min(groups, (e + 1) * per); ++gi) {
+        for (int gi = e * per; gi < min(a.groups, (e + 1) * per); ++gi) {
             // (all loads first: one latency)
             const int row0 = gi * a.group;
             int n[kMaxGroup], req[kMaxGroup];
@@ -108,8 +107,8 @@ __device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule
 #pragma unroll 1
         for (int e0 = 1; e0 <= entries; e0 += 32) {
             uint64_t v = e0 + lane <= entries ? sched->before[e0 + lane] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll 1
+            for (int o = 1; o < 32; o <<= 1) {  // (rolled: code that runs once waits for its way in)
                 const uint64_t u = __shfl_up_sync(0xffffffffu, v, o);
                 if (lane >= o) v += u;
             }
@@ -156,18 +155,20 @@ struct KvCursor {
     // The CTA's first item; false: it has none.
     template <int kCols>
     __device__ __forceinline__ bool first(const KvAttnArgs &a, const KvSchedule *sched, int lane) {
-        const int heads = a.kv_heads * static_cast<int>(a.col_blocks), groups = a.num_rows / a.group;
+        const int heads = a.kv_heads * static_cast<int>(a.col_blocks);
         if (kv_direct(a)) {
-            const uint32_t j = blockIdx.x / a.parts_bound;
-            part = static_cast<int>(blockIdx.x - j * a.parts_bound);
-            group = static_cast<int>(j / heads);
-            head = static_cast<int>(j - group * heads);
+            // (the numbers are small, so the halves keep the quotients clear of whole numbers)
+            const int b = static_cast<int>(blockIdx.x), parts_of = static_cast<int>(a.parts_bound);
+            const int j = static_cast<int>(__fdividef(b + 0.5f, static_cast<float>(parts_of)));
+            part = b - j * parts_of;
+            group = static_cast<int>(__fdividef(j + 0.5f, static_cast<float>(heads)));
+            head = j - group * heads;
             start = end = 0;
             load_group(a, lane);
             place<kCols>(a);
             return part < parts;
         }
-        const int per = (groups + kSchedEntries - 1) / kSchedEntries, entries = (groups + per - 1) / per;
+        const int per = a.sched_per, entries = a.sched_entries;
         // total * b / n: exact for products below 2^64 / n, and no total is near (a token costs 2^-6 or less)
         const uint64_t total = sched->before[entries];
         const uint64_t from = __umul64hi(total * blockIdx.x, a.ctas_inv);
@@ -193,14 +194,15 @@ struct KvCursor {
         uint64_t left = from - start;
         head = 0;
         if (left >= unit) {  // (the quotient is below heads, so fp32 misses it by one at most)
-            head = static_cast<int>(__ull2float_rz(left) / static_cast<float>(unit));
+            head = static_cast<int>(__fdividef(__ull2float_rz(left), static_cast<float>(unit)));
             head -= static_cast<uint64_t>(head) * unit > left;
             head += static_cast<uint64_t>(head + 1) * unit <= left;
             left -= static_cast<uint64_t>(head) * unit;
         }
         start = from - left;
         const uint32_t step = kItemCost + (1u << (shift - 7));  // of every part but the last
-        part = static_cast<int>((static_cast<uint32_t>(left) + step - 1) / step);
+        part = static_cast<int>(__fdividef(static_cast<float>(left), static_cast<float>(step)));  // (at most 128)
+        while (static_cast<uint32_t>(part) * step < left) ++part;
         start += static_cast<uint64_t>(part) * step;
         if (part >= parts) {
             start = from - left + unit;
@@ -292,6 +294,9 @@ inline cudaError_t raise_smem_limit(K kern, int bytes, std::atomic<uint64_t> &co
 inline uint32_t persistent_ctas(KvAttnArgs &a) {
     const uint32_t most = 2u * static_cast<uint32_t>(device_sm_count()), ctas = a.items < most ? a.items : most;
     if (ctas > 0) a.ctas_inv = ~0ull / ctas + 1;
+    a.groups = a.num_rows / a.group;
+    a.sched_per = (a.groups + kSchedEntries - 1) / kSchedEntries;
+    a.sched_entries = (a.groups + a.sched_per - 1) / a.sched_per;
     return ctas;
 }
 

@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
     kv_fill_schedule(a, sched);
     __syncthreads();
 
-    const int hpg = a.num_heads / a.kv_heads, cols = a.group * hpg;
+    const int hpg = a.hpg, cols = a.group * hpg;
     KvCursor w;
     bool more = w.first<NC>(a, sched, lane);
 
