@@ -11,7 +11,7 @@
 // goes to the workspace in fp32 and kv_combine_kernel merges a row's parts by log-sum-exp.  Two
 // persistent CTAs per SM take equal shares of the items, and one item's K and V stream in while the one
 // before it is merged and written.  8 x 128K tokens of a bf16 pool (4 KV heads of 128, 8 query heads each):
-// 316 us, the copy bandwidth; 23 ragged rows of up to 9,001 tokens (3 heads of 64, 16-token pages): 21 us
+// 316 us, the copy bandwidth; 23 ragged rows of up to 9,001 tokens (3 heads of 64, 16-token pages): 20 us
 // against 12 us of bytes, the rest start-up, the first tiles' latency and the merge.
 //
 // In a CTA a producer warp streams tiles of K and V by TMA into a ring of stages, a query warp brings
@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncthreads();
     pdl_wait();
-    pdl_launch_dependents();
+    const bool direct = kv_direct(a);
+    if (direct) pdl_launch_dependents();
     KvSchedule *sched = reinterpret_cast<KvSchedule *>(smem + C::OFF_SCHED);
     kv_fill_schedule(a, sched);
     __syncthreads();
@@ -325,6 +326,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
         }
+        // With many items only now: the merge's CTAs beside this one's start took it 2,000 cycles and more (23 ragged
+        // rows of head_dim 64: 20.8 us against 19.8).  With few it is better early (four rows of 256 tokens: 7.3 us
+        // against 8.4).
+        if (!direct) pdl_launch_dependents();
         if (*abort && lane == 0) {  // leave no copy in flight behind
             for (int i = max(0, issued - C::kStages); i < issued; ++i) {
                 const long long t0 = clock64();

@@ -26,11 +26,11 @@
 //
 // What bounds it: for 16 columns the bytes once contexts are long (32 x 16K-64K: 222 us, 91% of the copy
 // bandwidth; tiles of one CTA follow each other in 1,200 cycles when the memory lets them, an item costs about 4,000
-// cycles more: its first base, the last product's passage, its output).  Short parts show that, and the 7,000
-// cycles from the launch to the first tile (24 x 8K: 49 us against 30 us of bytes).  Writing an item's output behind
+// cycles more: its first base, the last product's passage, its output).  Short parts show that, and the 5,000
+// cycles from the launch to the first tile (24 x 8K: 48 us against 30 us of bytes).  Writing an item's output behind
 // the next one's first weights, into a second buffer of outputs, was slower (51 us): the other CTA of the SM fills the
 // wait already.  For 64 columns a tile takes some 4,000 cycles, most of them the softmax warps' latencies (fewer than
-// half of the issue slots are used), and a verify step of 4 x 64K tokens and 4 x 16 columns 92 us against 38 us of
+// half of the issue slots are used), and a verify step of 4 x 64K tokens and 4 x 16 columns 89 us against 38 us of
 // bytes.  (When it took 99: two blocks of 32 columns, which read the cache twice, 126 us, one warpgroup for all 64
 // columns 172 us, sums of weights in registers, which then spill, 106 us.)
 //
@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
-    pdl_launch_dependents();
+    const bool direct = kv_direct(a);
+    if (direct) pdl_launch_dependents();
     KvSchedule *sched = reinterpret_cast<KvSchedule *>(smem + C::OFF_SCHED);
     kv_fill_schedule(a, sched);
     __syncthreads();
@@ -366,6 +367,10 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     ++issued;
                 }
             }
+            // With many items only now: the merge's CTAs beside this one's start took it 2,000 cycles and more (23 ragged
+            // rows of head_dim 64: 20.8 us against 19.8).  With few it is better early (four rows of 256 tokens: 7.3 us
+            // against 8.4).
+            if (!direct) pdl_launch_dependents();
             if (*abort && lane == 0) {  // leave no copy in flight behind: the last tiles issued in either ring
                 for (int v = 0; v < 2; ++v) {
                     const uint32_t ring = v ? C::kV : C::kK;
