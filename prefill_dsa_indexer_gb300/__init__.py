@@ -666,9 +666,9 @@ def kv_insert(kv, slots, k, v, rope=None, positions=None, layout=ROPE_HALF, rot_
     """dsa_kv_insert: write k, v [tokens, kv_heads, head_dim] bf16 (parts of packed rows) at their slots of
     the KvCache.  With `rope` (a RopeTable) and `positions`, K's dims [rot_offset, rot_offset + rot_dim) are
     rotated first, and q [tokens, heads, rot_dim] too, into q_out (default: in place).  Returns q_out."""
-    n, device, heads, dim = slots.shape[0], kv.device, kv.kv_heads, kv.head_dim
     if slots.dim() != 1:
         raise DsaError(f"slots is [tokens]: got {tuple(slots.shape)}")
+    n, device, heads, dim = slots.shape[0], kv.device, kv.kv_heads, kv.head_dim
     shape, width = (n, heads, dim), heads * dim
     if k.dtype is not _bfloat16 or k.shape != shape or k.get_device() != device:
         _expect(k, "k", device, _BF16, shape)

@@ -660,6 +660,23 @@ def test_layer_without_rotary_positions():
     c.check(out, lse)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_calls_without_a_token(fmt):
+    """No token, no row: nothing is launched or touched."""
+    g = gen(47)
+    c = Case(48, fmt, [20], 2, 4, 128, 16)
+    table, none = P.rope_table(64), torch.empty(0, dtype=torch.int32, device="cuda")
+    before = bits(c.pool).clone()
+    k = randn(g, 0, 2, 128)
+    q = randn(g, 0, 8, 128)[..., :64]
+    assert P.kv_insert(c.kv, none, k, k, rope=table, positions=none, q=q).shape == (0, 8, 64)
+    assert P.kv_insert(c.kv, none, k, k) is None
+    assert P.rope(q, table, none).shape == (0, 8, 64)
+    out, lse = P.kv_attention(c.kv, c.table, none, none, c.max_ctx, randn(g, 0, 8, 128))
+    torch.cuda.synchronize()
+    assert out.shape == (0, 8, 128) and lse.shape == (0, 8) and torch.equal(bits(c.pool), before)
+
+
 def test_binding_refusals():
     c = Case(50, "bf16", [100], 2, 4, 64, 16)
     call = lambda **k: P.kv_attention(**{**dict(kv=c.kv, block_table=c.table, row_req=c.row_req, row_ctx=c.row_ctx,  # noqa: E731
