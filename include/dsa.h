@@ -569,8 +569,8 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
  * or past row_ctx[r] hold never reaches row r (NaN included).  rows->rows_per_group (1, 2, 4 or 8)
  * consecutive rows of one request (speculative verify) share each read of the cache.
  *
- * Each row's tokens are split into parts by its own context (the group's largest; batch
- * invariance), one CTA per part and KV head, merged by log-sum-exp: the workspace (device, 256-byte
+ * Each row's tokens are split into parts by its own context (the group's largest), merged by
+ * log-sum-exp, and a row's bits depend on nothing outside its group (batch invariance): the workspace (device, 256-byte
  * aligned, dsa_kv_attention_workspace_size bytes, no initial contents; NULL when that is 0) holds
  * the parts in fp32 and serves one call at a time: calls that may run at once, captured graphs
  * among them, have one each.  Outputs overlap no input.  Scores and sums are fp32.  The softmax weights multiply V as

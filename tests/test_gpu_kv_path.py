@@ -376,6 +376,24 @@ def test_attention_huge_queries_over_an_fp8_pool():
     c.check(*c.run(sm_scale=1e28))
 
 
+@pytest.mark.parametrize("fmt, dim", [("bf16", 64), ("bf16", 128), ("fp8", 64), ("fp8", 128)])
+@pytest.mark.parametrize("hpg, group", [(5, 1), (16, 2), (16, 4)])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_attention_a_head_of_no_numbers_stays_alone(fmt, dim, hpg, group, value):
+    """A NaN or an infinity in one head's query reaches neither its neighbours nor the other rows of its group."""
+    c = Case(49, fmt, [700, 90], 2, hpg, dim, 32, group=group)
+    want = c.run()
+    q, r, h = c.q.clone(), len(c.rows) - 1, hpg + 2
+    q[r, h, 3] = value
+    out, lse = c.run(q=q)
+    assert torch.isnan(out[r, h]).any() and not torch.isfinite(lse[r, h])
+    rest = torch.ones(out.shape[:2], dtype=torch.bool, device="cuda")
+    rest[r, h] = False
+    c.check(out, lse, rows=range(r))
+    assert torch.isfinite(out[rest].float()).all()
+    assert torch.equal(out[:r], want[0][:r]) or fmt == "fp8"  # (an FP8 group's bases move together)
+
+
 def test_attention_rows_of_a_packed_projection():
     c = Case(17, "bf16", [513, 77, 2000], 4, 8, 128, 64)
     packed = torch.zeros(3, 32 + 8, 128, dtype=torch.bfloat16, device="cuda")
