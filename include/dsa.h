@@ -570,15 +570,16 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
  * consecutive rows of one request (speculative verify) share each read of the cache.
  *
  * Each row's tokens are split into parts by its own context (the group's largest), merged by
- * log-sum-exp, and a row's bits depend on nothing outside its group (batch invariance): the workspace (device, 256-byte
- * aligned, dsa_kv_attention_workspace_size bytes, no initial contents; NULL when that is 0) holds
- * the parts in fp32 and serves one call at a time: calls that may run at once, captured graphs
- * among them, have one each.  Outputs overlap no input.  Scores and sums are fp32.  The softmax weights multiply V as
- * the sum of two bf16 terms (bf16 pool), as fp16 (FP8 pool of head_dim 64, whose codes are exact in
- * fp16), or as the sum of two e4m3 terms (FP8 pool of head_dim 128).  Over an FP8 pool q is scaled by a power
- * of two per head and rounded to fp16 (head_dim 64) or to the sum of two e4m3 terms (128); a head
- * of head_dim 128 with an infinity or a NaN in q gets NaN.  A row_ctx outside [0, max_ctx], a row_req outside the block
- * table, rows of a group with different requests, or a page id outside the pool is DSA_ERR_BOUNDS.
+ * log-sum-exp, and a row's bits depend on nothing outside its group (batch invariance): the workspace
+ * (device, 256-byte aligned, dsa_kv_attention_workspace_size bytes, no initial contents; NULL when
+ * that is 0) holds the parts in fp32 and serves one call at a time: calls that may run at once,
+ * captured graphs among them, have one each.  Outputs overlap no input.  Scores and sums are fp32.
+ * The softmax weights multiply V as the sum of two bf16 terms (bf16 pool), as fp16 (FP8 pool of
+ * head_dim 64, whose codes are exact in fp16), or as the sum of two e4m3 terms (FP8 pool of
+ * head_dim 128).  Over an FP8 pool q is scaled by a power of two per head and rounded to fp16
+ * (head_dim 64) or to the sum of two e4m3 terms (128); a head of head_dim 128 with an infinity or a
+ * NaN in q gets NaN.  A row_ctx outside [0, max_ctx], a row_req outside the block table, rows of a
+ * group with different requests, or a page id outside the pool is DSA_ERR_BOUNDS.
  */
 int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint16_t *q, int64_t q_stride,
                      int32_t num_heads, float sm_scale, uint16_t *out, float *lse, void *workspace,
