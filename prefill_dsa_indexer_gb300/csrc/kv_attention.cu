@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         auto finish = [&](int64_t at, int d, const float4 &x, float b, float total) {  // dims d .. d + 3 of head `at`
             if (parts > 1) {
                 *reinterpret_cast<float4 *>(a.part_o + (at * a.parts_bound + part) * D + d) = x;
-                if (d == 0) a.part_ml[at * a.parts_bound + part] = make_float2(b, total);
+                if (d == 0) a.part_ml[at * a.parts_bound + part] = make_float2(part_base(b, total), total);
             } else {
                 const bool none = total == 0.f;
                 const float inv = none ? 0.f : a.v_scale / total;

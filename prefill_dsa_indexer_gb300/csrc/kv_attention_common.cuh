@@ -242,6 +242,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// A part's base as the merge takes it.  A part without any weight (a row of a group that ends before it, or scores
+// that are all -inf) has none: 0 in its place would be the row's largest where all scores lie below, and the factors
+// 2^(base - largest) of the parts that count would underflow.
+__device__ __forceinline__ float part_base(float b, float sum) { return sum == 0.f ? -INFINITY : b; }
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);

@@ -849,7 +849,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     const float b = -nbase[n];
                     const int at = cs->at[mine + n];
                     if (parts > 1)
-                        a.part_ml[static_cast<int64_t>(at) * a.parts_bound + part] = make_float2(b, total);
+                        a.part_ml[static_cast<int64_t>(at) * a.parts_bound + part] = make_float2(part_base(b, total), total);
                     else if (a.lse != nullptr)
                         a.lse[at] = total == 0.f ? -INFINITY : (b + log2f(total)) * 0.6931471805599453f;
                 }

@@ -1,0 +1,96 @@
+"""Paged attention in the corners of its formula, against 64-bit evaluations of it."""
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_kv_path import Case, bits
+
+pytestmark = pytest.mark.gpu
+
+
+def weight_error(fmt, dim):
+    """A softmax weight as it multiplies V: (relative to itself, against its part's largest).  bf16 pools: two bf16
+    terms, 2^-9 2^-8.  FP8 pools of head_dim 64: fp16, half a step being 2^-11, with a smallest step of 2^-24 where the
+    largest weight is at least 2^7; of head_dim 128: two e4m3 terms, 2^-8, with a smallest step of 2^-9 (half of it
+    for each term) where the largest is at least 2^6."""
+    if fmt == "bf16":
+        return 2.0 ** -16, 0.0
+    return (2.0 ** -8, 2.0 ** -15) if dim == 128 else (2.0 ** -11, 2.0 ** -32)
+
+
+def check_weights(c, out, lse, rows=None):
+    """Case.check with the weights' own errors."""
+    for r in range(len(c.rows)) if rows is None else rows:
+        n = c.rows[r]
+        if n == 0:
+            assert (out[r] == 0).all() and (lse[r] == -math.inf).all()
+            continue
+        for h in range(c.q.shape[1] // c.hpg):
+            at = slice(h * c.hpg, (h + 1) * c.hpg)
+            k, v = c.tokens(r, h)
+            q = c.q[r, at].double()
+            s = q @ k.T * c.sm
+            p = torch.softmax(s, -1)
+            ref, mag = p @ v, p @ v.abs()
+            big = (q.abs() @ k.abs().T * c.sm).amax(-1, keepdim=True)
+            # scores: fp32 sums; over FP8 pools of head_dim 128 q is two e4m3 terms, which leave 2^-10 where the
+            # largest element is above 224; of head_dim 64 fp16, which leaves 2^-25 where it is at least 2^13
+            ds = (c.dim + 8) * 2.0 ** -24 * big
+            if c.fmt == "fp8":
+                step = 2.0 ** -10 / 224 if c.dim == 128 else 2.0 ** -25 / 2 ** 13
+                ds = ds + step * q.abs().amax(-1, keepdim=True) * k.abs().sum(-1).max() * c.sm
+            own, floor = weight_error(c.fmt, c.dim)
+            w = own + 2.0 ** -22 + n * 2.0 ** -24
+            # (a part's weights against the row's largest: no part has a larger one)
+            sub = floor * p.amax(-1, keepdim=True) * v.abs().sum(0)
+            bound = 2.0 ** -8 * ref.abs() + (1 + 2.0 ** -8) * ((w + 2 * ds) * mag + sub) + 1e-30
+            off = (out[r, at].double() - ref).abs()
+            assert (off <= bound).all(), (r, h, (off / bound).max().item())
+            want = torch.logsumexp(s, -1)
+            lb = ds[:, 0] + n * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -22 * want.abs()
+            assert ((lse[r, at].double() - want).abs() <= lb).all(), (r, h)
+
+
+# ------------------------------------------------------------------ parts in which a row sees nothing
+
+def shift_scores(c, nats):
+    """Every key of the case gets a first element that adds `nats` (negative) to all scores: a constant that the softmax
+    does not see."""
+    code = -448.0 if c.fmt == "fp8" else -32.0
+    c.pool.view(torch.uint8 if c.fmt == "fp8" else torch.int16)[:, :, 0, :, 0] = \
+        bits(torch.tensor([code], device="cuda").to(c.pool.dtype)).item()
+    c.q[..., 0] = nats / (code * c.ks * c.sm)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("nats", [-150.0, -1000.0])
+@pytest.mark.parametrize("group, row_ctx", [
+    (2, [256, 257]), (2, [257, 256]), (2, [64, 5000, 511, 513]), (4, [8190, 8191, 8192, 8193]),
+    (4, [100, 8193, 300, 5000]), (8, [0, 1, 255, 256, 257, 512, 513, 20000])])
+@pytest.mark.parametrize("hpg", [2, 16])
+def test_rows_whose_last_parts_are_empty(fmt, dim, nats, group, row_ctx, hpg):
+    ctx = [max(row_ctx[i:i + group]) for i in range(0, len(row_ctx), group)]
+    c = Case(61, fmt, ctx, 2, hpg, dim, 64, group=group, row_ctx=row_ctx)
+    shift_scores(c, nats)
+    check_weights(c, *c.run())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_part_whose_scores_are_all_minus_infinity(dim):
+    c = Case(62, "bf16", [1500], 1, 4, dim, 16)
+    shift_scores(c, -200.0)
+    hidden = range(256, 512)  # one part of the row
+    for t in hidden:
+        c.pool[c.table[0, t // 16].item(), :, 0, t % 16, 0] = -math.inf
+    out, lse = c.run()
+    keep = torch.ones(1500, dtype=torch.bool, device="cuda")
+    keep[256:512] = False
+    k, v = (x[keep] for x in c.tokens(0, 0))
+    s = c.q[0].double() @ k.T * c.sm
+    p = torch.softmax(s, -1)
+    # fp32 scores of size 200: 2^-24 (dim + 8) of them each; the output's rounding
+    ds = (dim + 8) * 2.0 ** -24 * 300
+    assert ((out[0].double() - p @ v).abs() <= 2.0 ** -8 * (p @ v).abs() + (2 * ds + 2.0 ** -12) * (p @ v.abs())).all()
+    assert ((lse[0].double() - torch.logsumexp(s, -1)).abs() <= ds + 2.0 ** -14).all()
