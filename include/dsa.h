@@ -578,8 +578,9 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
  * head_dim 64, whose codes are exact in fp16), or as the sum of two e4m3 terms (FP8 pool of
  * head_dim 128).  Over an FP8 pool q is scaled by a power of two per head and rounded to fp16
  * (head_dim 64) or to the sum of two e4m3 terms (128); a head of head_dim 128 with an infinity or a
- * NaN in q gets NaN.  A row_ctx outside [0, max_ctx], a row_req outside the block table, rows of a
- * group with different requests, or a page id outside the pool is DSA_ERR_BOUNDS.
+ * NaN in q gets NaN.  A row_ctx outside [0, max_ctx], a row_req outside the block table or rows of a
+ * group with different requests are DSA_ERR_BOUNDS, and their group gets out = 0 and lse = -inf; a
+ * page id outside the pool is DSA_ERR_BOUNDS, and page 0 is read in its place.
  */
 int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint16_t *q, int64_t q_stride,
                      int32_t num_heads, float sm_scale, uint16_t *out, float *lse, void *workspace,

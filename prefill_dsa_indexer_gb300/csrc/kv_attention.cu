@@ -752,11 +752,12 @@ __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const __gri
     __shared__ float4 x_s[kGroups][kLanes];
     __shared__ float t_s[kGroups];
     // The attention kernel lets this one start after its own wait, so what ran before it is complete: the
-    // contexts can be read before this kernel's wait, which is for the parts.
+    // contexts can be read before this kernel's wait, which is for the parts.  (A refused group is one part.)
     const int64_t at = blockIdx.x;
-    const int row0 = static_cast<int>(at / a.num_heads) / a.group * a.group;
-    int ctx = 0;
-    for (int i = 0; i < a.group; ++i) ctx = max(ctx, min(a.row_ctx[row0 + i], a.max_ctx));
+    int req;
+    bool bad;
+    const int my_ctx = kv_load_group(a, static_cast<int>(at / a.num_heads) / a.group * a.group, threadIdx.x & 31, req, bad);
+    const int ctx = __reduce_max_sync(0xffffffffu, my_ctx);
     const int parts = kv_parts(ctx, kv_part_shift(ctx, a.parts_shift));
     pdl_wait();
     pdl_launch_dependents();

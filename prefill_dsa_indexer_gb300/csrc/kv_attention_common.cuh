@@ -71,6 +71,22 @@ __device__ __forceinline__ uint32_t kv_cost(int32_t ctx, int32_t parts_shift) {
 
 __device__ __forceinline__ bool kv_direct(const KvAttnArgs &a) { return a.items <= gridDim.x; }  // an item a CTA
 
+// Whether a row of context n and request req has no place in the group of a row of request first: its whole group is
+// answered with nothing (out = 0, lse = -inf), as one part.
+__device__ __forceinline__ bool kv_refused(const KvAttnArgs &a, int n, int req, int first) {
+    return n < 0 || n > a.max_ctx || req != first || req < 0 || req >= a.num_requests;
+}
+
+// A lane's context of the group (of row `lane`, or of the first), its rows' request, and whether it is refused: then
+// all contexts are 0.  Warp-collective.
+__device__ __forceinline__ int kv_load_group(const KvAttnArgs &a, int row0, int lane, int &req, bool &bad) {
+    const int row = row0 + (lane < a.group ? lane : 0);
+    const int n = a.row_ctx[row], r = a.row_req[row];
+    req = __shfl_sync(0xffffffffu, r, 0);
+    bad = __any_sync(0xffffffffu, kv_refused(a, n, r, req));
+    return bad ? 0 : n;
+}
+
 // Fills `sched`; every thread of the CTA calls it, then __syncthreads.
 __device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule *sched) {
     if (kv_direct(a)) return;
@@ -88,11 +104,11 @@ __device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule
                 n[r] = a.row_ctx[row];
                 req[r] = a.row_req[row];
             }
-            bool bad = req[0] < 0 || req[0] >= a.num_requests;
+            bool bad = false;
             int ctx = 0;
 #pragma unroll
             for (int r = 0; r < kMaxGroup; ++r) {
-                bad |= n[r] < 0 || n[r] > a.max_ctx || req[r] != req[0];
+                bad |= kv_refused(a, n[r], req[r], req[0]);
                 ctx = max(ctx, n[r]);
             }
             sum += kv_cost(bad ? 0 : ctx, a.parts_shift);
@@ -129,11 +145,7 @@ struct KvCursor {
 
     __device__ __forceinline__ void load_group(const KvAttnArgs &a, int lane) {
         row0 = group * a.group;
-        const int row = row0 + (lane < a.group ? lane : 0);
-        const int n = a.row_ctx[row], r = a.row_req[row];
-        req = __shfl_sync(0xffffffffu, r, 0);
-        bad = __any_sync(0xffffffffu, n < 0 || n > a.max_ctx || r != req) || req < 0 || req >= a.num_requests;
-        my_ctx = bad ? 0 : n;
+        my_ctx = kv_load_group(a, row0, lane, req, bad);
         ctx = __reduce_max_sync(0xffffffffu, my_ctx);
         ctx_min = __reduce_min_sync(0xffffffffu, my_ctx);
         shift = kv_part_shift(ctx, a.parts_shift);

@@ -4,6 +4,7 @@ import math
 import pytest
 import torch
 
+import prefill_dsa_indexer_gb300 as P
 from tests.test_gpu_kv_path import Case, bits
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +95,40 @@ def test_a_part_whose_scores_are_all_minus_infinity(dim):
     ds = (dim + 8) * 2.0 ** -24 * 300
     assert ((out[0].double() - p @ v).abs() <= 2.0 ** -8 * (p @ v).abs() + (2 * ds + 2.0 ** -12) * (p @ v.abs())).all()
     assert ((lse[0].double() - torch.logsumexp(s, -1)).abs() <= ds + 2.0 ** -14).all()
+
+
+# ------------------------------------------------------------------ rows that are refused on the device
+
+@pytest.mark.parametrize("fmt, dim", [("bf16", 64), ("bf16", 128), ("fp8", 64), ("fp8", 128)])
+@pytest.mark.parametrize("bad", ["request below", "request above", "two requests", "context above", "context below"])
+def test_a_refused_group_is_answered_with_nothing(fmt, dim, bad):
+    """Out is 0 and lse -inf, whatever the workspace holds, and the other groups keep their bits."""
+    group = 2
+    c = Case(63, fmt, [5000, 9000, 700], 2, 4, dim, 32, group=group)
+    need = P.kv_attention_workspace_size(c.kv, 6, 8, c.max_ctx)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    want = [x.clone() for x in c.run(workspace=ws)]
+    c.check(*want)
+    req, ctx = c.row_req.clone(), c.row_ctx.clone()
+    if bad == "request below":
+        req[2:4] = -1
+    elif bad == "request above":
+        req[2:4] = 3
+    elif bad == "two requests":
+        req[3] = 0
+    elif bad == "context above":
+        ctx[3] = c.max_ctx + 1
+    else:
+        ctx[2] = -1
+    for fill in (0xFF, None):  # NaN, and what the call before left there
+        if fill is not None:
+            ws.fill_(fill)
+        status = P.new_status()
+        out, lse = P.kv_attention(c.kv, c.table, req, ctx, c.max_ctx, c.q, rows_per_group=group, workspace=ws,
+                                  status=status)
+        torch.cuda.synchronize()
+        assert status.item() == P.ERR_BOUNDS
+        assert (out[2:4] == 0).all() and (lse[2:4] == -math.inf).all()
+        for got, w in zip((out, lse), want):
+            assert torch.equal(got[:2], w[:2]) and torch.equal(got[4:], w[4:])
+        c.run(workspace=ws)
