@@ -574,11 +574,11 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
  * (device, 256-byte aligned, dsa_kv_attention_workspace_size bytes, no initial contents; NULL when
  * that is 0) holds the parts in fp32 and serves one call at a time: calls that may run at once,
  * captured graphs among them, have one each.  Outputs overlap no input.  Scores and sums are fp32.
- * The softmax weights multiply V as the sum of two bf16 terms (bf16 pool), as fp16 (FP8 pool of
- * head_dim 64, whose codes are exact in fp16), or as the sum of two e4m3 terms (FP8 pool of
- * head_dim 128).  Over an FP8 pool q is scaled by a power of two per head and rounded to fp16
- * (head_dim 64) or to the sum of two e4m3 terms (128); a head of head_dim 128 with an infinity or a
- * NaN in q gets NaN.  A row_ctx outside [0, max_ctx], a row_req outside the block table or rows of a
+ * The softmax weights multiply V as the sum of two bf16 terms (bf16 pool) or rounded to fp16 (FP8
+ * pool), where they keep steps of 2^-29 of the largest of their part (head_dim 64: 2^-31) or better.
+ * Over an FP8 pool q is scaled by a power of two per head and rounded to fp16 (head_dim 64) or to the
+ * sum of two e4m3 terms (128: exact down to 2^-9 of the head's largest element, smaller ones within
+ * 2^-17 of that largest); a head of head_dim 128 with an infinity or a NaN in q gets NaN.  A row_ctx outside [0, max_ctx], a row_req outside the block table or rows of a
  * group with different requests are DSA_ERR_BOUNDS, and their group gets out = 0 and lse = -inf; a
  * page id outside the pool is DSA_ERR_BOUNDS, and page 0 is read in its place.
  */

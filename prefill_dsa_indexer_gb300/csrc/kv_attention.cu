@@ -34,8 +34,6 @@
 // elements 2^-25 below the column's largest), P is one fp16 term (2^-12), scaled by 2^7 so that weights
 // down to 2^-21 of the base stay normal.  (mma.sync on e4m3 operands was tried for S: the warps spend their time in
 // branches and instruction fetches there, 178 us against 108 us for 16 x 16K.)
-#include <cuda_fp16.h>
-
 #include <type_traits>
 
 #include "kv_attention_common.cuh"
@@ -123,11 +121,6 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t &lo, uint32_t
         "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(v));
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // Byte offset of 16-byte unit `u` of token `t` in a side (K or V) of a stage, as its TMA boxes landed.

@@ -8,14 +8,14 @@
 // way; here 222 us).  The fifth-generation tensor cores take the codes as they lie in shared memory:
 //
 //     S^T[128 tokens x NC]  = K Q^T      A: the K tile (K-major), B: q as hi, then lo e4m3 terms
-//     O^T[128 dims x NC]   += V^T P^T    A: the V tile read MN-major, B: P as hi, then lo e4m3 terms (MN-major)
+//     O^T[128 dims x NC]   += V^T P^T    A: the V tile read MN-major, B: P as three e5m2 terms (MN-major)
 //
 // with NC (16, 32 or 64) columns, (row of the group, query head of the KV head) pairs, in N.  An MMA with so
-// small an N costs its A operand's passage: 40 cycles an SM for N <= 32, 48 for 64 measured, so a tile's
-// 16 take 640 to 770 of the 1,490 cycles that its 32 KB take at the copy bandwidth.  A token is a TMEM lane: a
-// softmax thread reads its token's scores of its columns, P = 2^(S - b) with a lazy base b per column, splits
-// each weight into hi + lo and writes its row of P.  The base moves, and O^T is rescaled in TMEM, only when a
-// score exceeds it by 2^8.7.
+// small an N costs its A operand's passage: 40 cycles an SM for N <= 32, 48 for 64, 64 for 128 measured, so a tile's
+// 8, 12 or 16 take some 340 to 830 of the 1,490 cycles that its 32 KB take at the copy bandwidth.  A token is a TMEM
+// lane: a softmax thread reads its token's scores of its columns, P = 2^(S - b) with a lazy base b per column, splits
+// each weight into three terms and writes its row of P.  The base moves, and O^T is rescaled in TMEM, only when a
+// score exceeds it by 2^15.7.
 //
 // Roles: softmax warps (TMEM lane quadrants; one warpgroup, or two that share out 64 columns), a TMA producer
 // (K and V tiles of 16 KB through a ring each), an issuer of the scores' MMAs, one of the values' (an MMA's
@@ -27,17 +27,21 @@
 // What bounds it: for 16 columns the bytes once contexts are long (32 x 16K-64K: 222 us, 91% of the copy
 // bandwidth; tiles of one CTA follow each other in 1,200 cycles when the memory lets them, an item costs about 4,000
 // cycles more: its first base, the last product's passage, its output).  Short parts show that, and the 5,000
-// cycles from the launch to the first tile (24 x 8K: 48 us against 30 us of bytes).  Writing an item's output behind
+// cycles from the launch to the first tile (24 x 8K: 50 us against 30 us of bytes).  Writing an item's output behind
 // the next one's first weights, into a second buffer of outputs, was slower (51 us): the other CTA of the SM fills the
 // wait already.  For 64 columns a tile takes some 4,000 cycles, most of them the softmax warps' latencies (fewer than
-// half of the issue slots are used), and a verify step of 4 x 64K tokens and 4 x 16 columns 89 us against 38 us of
+// half of the issue slots are used), and a verify step of 4 x 64K tokens and 4 x 16 columns 92 us against 38 us of
 // bytes.  (When it took 99: two blocks of 32 columns, which read the cache twice, 126 us, one warpgroup for all 64
-// columns 172 us, sums of weights in registers, which then spill, 106 us.)
+// columns 172 us, sums of weights in registers, which then spill, 106 us.)  P's third term costs 3 to 4 us of the 92;
+// all three one after the other into one accumulator, with a second score buffer in the place of the other, 102 us.
 //
 // Precision: e4m3 x e4m3 products are exact and accumulate in fp32.  q is scaled by a power of two per
-// column and written as hi + lo (exact but for elements 2^-10 below the column's largest, which keep 2^-18 of
-// it).  A weight as hi + lo keeps 2^-8 of itself at worst, 2^-10.5 on average, against the output's own
-// rounding of 2^-9 on average (bf16); weights below 2^-12 of the largest keep 2^-16 of that largest.
+// column and written as hi + lo (exact but for elements 2^-9 below the column's largest, which are within 2^-17 of
+// it).  A weight is rounded to fp16 (2^-11 of itself at worst, against the output's own 2^-8), whose 11 bits three
+// e5m2 terms of 3 hold exactly; e5m2's smallest step is 2^-16 and the largest weight at least 2^13, so weights keep
+// 2^-29 of their part's largest: the background behind an attention sink counts, however many tokens make it up.
+// (Two e4m3 terms over a largest of 2^6 lost what lay 2^16 below it: with a first token 11 nats ahead of 131,072
+// others, whose values it opposes, an output of +0.26 for +0.30.)
 #include "kv_attention_common.cuh"
 #include "mla_fp8_common.cuh"
 
@@ -46,15 +50,14 @@ namespace dsa {
 namespace {
 
 using namespace kv;
-using fp8mla::e4m3x2;
 using fp8mla::split_pair;
 using fp8mla::sw128;
 
 constexpr int kTile = 128;                                 // tokens of a tile
 constexpr int kDim = 128;
 constexpr int kUnitBytes = kTile * kDim;                   // K or V of a tile
-constexpr float kTop = 8.7f;                               // weights reach 2^8.7 = 416 (e4m3 holds 448) ...
-constexpr float kBias = 6.0f;                              // ... and a moved base leaves the largest at 2^6
+constexpr float kTop = 15.7f;                              // weights reach 2^15.7 = 53,232 (e5m2 holds 57,344) ...
+constexpr float kBias = 13.0f;                             // ... and a moved base leaves the largest at 2^13
 
 // What the query warp tells the others about an item.
 struct Item {
@@ -92,28 +95,46 @@ struct Cfg {
     static constexpr int kSoftmaxRegs = kGroups == 1 ? 168 : 88, kOtherRegs = kGroups == 1 ? 88 : 64;
     static_assert(kGroups * kSoftmaxRegs + kOtherRegs == (kGroups + 1) * kLaunchRegs,
                   "the warpgroups share what the CTA was launched with");
-    // hi and lo terms lie side by side in an MMA's N, or follow one another into the same columns
-    static constexpr int kSN = NC == 16 ? 2 * NC : NC, kON = NC == 64 ? NC : 2 * NC;
-    static constexpr int kPBufs = NC == 64 ? 1 : 2;        // a token's 128-byte row of P holds two tiles' weights
+    // A product's terms lie side by side in an MMA's N, each with its accumulator, or follow one another into one: q's
+    // hi and lo for 16 columns, else one after the other; P's three, but for 64 columns the third after the first
+    static constexpr int kSN = NC == 16 ? 2 * NC : NC, kON = NC == 64 ? 2 * NC : 3 * NC;
+    static constexpr int kSTurns = NC == 16 ? 1 : 2, kOTurns = NC == 64 ? 2 : 1;
+    static constexpr int kSBufs = NC == 64 ? 1 : 2, kPBufs = NC == 16 ? 2 : 1;
+    // P: a token's 128-byte row holds its three terms (64 columns: the first two) of each buffer; the third terms of
+    // 64 columns have rows of 64 bytes, tokens 64 and up beside the first 64 in 128
+    static constexpr int kPRow = (NC == 64 ? 2 : 3) * NC / 16;  // 16-byte units of a buffer in a token's row
+    static constexpr int kP3Bytes = NC == 64 ? kTile * 64 : 0;
+    static constexpr uint32_t kP3Offset = kTile * 128 / 16;     // units from P's rows to the third terms'
+    // (a softmax warp that waits for a V tile alone, on an edge, has seen the product of the tile kPBufs before: the
+    // barrier's phase before the awaited one is over)
+    static_assert(kPBufs <= kV, "a V tile's phases are told apart");
     static constexpr bool kSumsInTmem = NC == 64;          // a thread's sums of weights, if not in registers
-    static constexpr uint32_t kTmemO = 2 * kSN;            // two score buffers, then the output, then the sums
+    static constexpr uint32_t kTmemO = kSBufs * kSN;       // score buffers, then the output, then the sums
     static constexpr uint32_t kTmemL = kTmemO + kON;
-    static constexpr uint32_t kTmemCols = NC == 16 ? 128 : 256;  // two CTAs share the SM's 512
+    static constexpr uint32_t kTmemCols = 256;             // two CTAs share the SM's 512
+    // where a product for the columns of one context of a group goes: of 64 columns into the scores' buffer, one of
+    // O^T's two accumulators at a time
+    static constexpr bool kApartInScores = NC == 64;
+    static constexpr int kApartTurns = kApartInScores ? 2 : 1, kXN = kON / kApartTurns;
+    static constexpr uint32_t kTmemX = kApartInScores ? 0 : kTmemL;
     static constexpr int OFF_Q = kUnits * kUnitBytes;      // [kQBufs]: rows hi 0 .. NC - 1, lo NC .. 2 NC - 1
-    static constexpr int OFF_P = OFF_Q + kQBufs * kQBytes;      // [kPBufs] a token's row: NC hi, NC lo bytes
-    static constexpr int OFF_COLS = OFF_P + kTile * 128;   // [2] by image parity
+    static constexpr int OFF_P = OFF_Q + kQBufs * kQBytes;
+    static constexpr int OFF_P3 = OFF_P + kTile * 128;
+    static constexpr int OFF_SCHED = OFF_P;                // of use before the first weights alone
+    static constexpr int OFF_COLS = OFF_P3 + kP3Bytes;     // [2] by image parity
     static constexpr int OFF_ITEM = OFF_COLS + 2 * static_cast<int>(sizeof(Columns<NC>));
     static constexpr int OFF_MAX = OFF_ITEM + 2 * static_cast<int>(sizeof(Item));      // [kSoftmax][kMine] a warp's largest scores
     static constexpr int OFF_BASE = OFF_MAX + 4 * NC * 4;  // [kSoftmax][kMine] minus the bases, a copy per warp
     static constexpr int OFF_FAC = OFF_BASE + 4 * NC * 4;  // [kSoftmax][kMine] rescale factors
     static constexpr int OFF_MOVE = OFF_FAC + 4 * NC * 4;  // [kSoftmax][kMine] and their logarithms
     static constexpr int OFF_SUM = OFF_MOVE + 4 * NC * 4;   // [2][kSoftmax][kMine] sums of weights, by item parity
-    static constexpr int OFF_SCHED = OFF_SUM + 2 * 4 * NC * 4;
-    static constexpr int OFF_BARS = OFF_SCHED + static_cast<int>(sizeof(KvSchedule));
+    static constexpr int OFF_BARS = OFF_SUM + 2 * 4 * NC * 4;
     static constexpr int kNumBars = 2 * kUnits + 2 * 2 + 2 * 2 + kQBufs + 2 * kPBufs + 2;
     static constexpr int OFF_MISC = OFF_BARS + kNumBars * 8;
     static constexpr int kSmemBytes = OFF_MISC + 16 + 1024;
-    static_assert(kTmemL + (kSumsInTmem ? NC : 0) <= kTmemCols, "TMEM plan");
+    static_assert(sizeof(KvSchedule) <= kTile * 128, "the schedule fits P");
+    static_assert(kTmemL + (kSumsInTmem ? NC : 0) + (kApartInScores ? 0 : kXN) <= kTmemCols, "TMEM plan");
+    static_assert(kApartInScores ? kXN <= kSN : !kSumsInTmem, "TMEM plan");
     static_assert(kSmemBytes <= 115712, "two CTAs per SM");
 };
 
@@ -169,6 +190,24 @@ __device__ __forceinline__ void add_pair(uint32_t &h0, uint32_t &h1, float g0, f
     const float2 s = __fadd2_rn(make_float2(__uint_as_float(h0), __uint_as_float(h1)), make_float2(g0, g1));
     h0 = __float_as_uint(s.x);
     h1 = __float_as_uint(s.y);
+}
+
+// Four weights as fp16 in (a, b): their first, second and third e5m2 terms.  An e5m2 number is the upper byte of an
+// fp16 one: each term is what is left, rounded to that byte (half a step up), and the rest is exact.
+__device__ __forceinline__ void weight_terms(uint32_t a, uint32_t b, uint32_t &t1, uint32_t &t2, uint32_t &t3) {
+    auto rest = [](uint32_t x, uint32_t rounded) {
+        const uint32_t byte = rounded & 0xff00ff00u;
+        const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&byte));
+        return *reinterpret_cast<const uint32_t *>(&d);
+    };
+    uint32_t ra = a + 0x00800080u, rb = b + 0x00800080u;
+    t1 = __byte_perm(ra, rb, 0x7531);
+    a = rest(a, ra);
+    b = rest(b, rb);
+    ra = a + 0x00800080u;
+    rb = b + 0x00800080u;
+    t2 = __byte_perm(ra, rb, 0x7531);
+    t3 = __byte_perm(rest(a, ra), rest(b, rb), 0x7531);
 }
 
 __device__ __forceinline__ void add16(uint32_t (&h)[16], const uint32_t (&g)[16]) {
@@ -319,6 +358,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
     const int hpg = a.hpg, cols = a.group * hpg;
     KvCursor w;
     bool more = w.first<NC>(a, sched, lane);
+    if (!direct) __syncthreads();  // the schedule's place is P's
 
     if (warp >= kSoftmax) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
@@ -444,8 +484,10 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
             // ---- the two MMA issuers, one thread each: an MMA's issue lasts as long as its passage through the
             // tensor core, so one thread for both products would set the pace
             const bool values = warp == kValues;
-            const uint32_t idesc = values ? make_idesc(kDim, C::kON, 0, 0, true, true)
+            // (formats: 0 e4m3, 1 e5m2)
+            const uint32_t idesc = values ? make_idesc(kDim, C::kON, 0, 1, true, true)
                                            : make_idesc(kTile, C::kSN, 0, 0, false, false);
+            const uint32_t idesc_turn = values ? make_idesc(kDim, NC, 0, 1, true, true) : idesc;  // (of one term)
             const uint32_t ring = values ? C::kV : C::kK, slot0 = values ? C::kK : 0;
             const uint32_t ua = smem_u32(smem);
             const uint64_t b0 = sdesc_sw128(smem_u32(smem + (values ? C::OFF_P : C::OFF_Q)), 16, 1024);
@@ -469,15 +511,16 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     o_phase ^= 1;
                 }
                 for (int i = 0; ok && i < tiles; ++i, ++count) {
-                    const uint32_t turn = count / ring, slot = slot0 + count - turn * ring, sb = count & 1, pb = count % C::kPBufs;
+                    const uint32_t turn = count / ring, slot = slot0 + count - turn * ring, sb = count % C::kSBufs;
+                    const uint32_t pb = count % C::kPBufs;
                     ok = wait_mbar(&full[slot], turn & 1, abort);
-                    // values: levels 0 accumulates in O^T.  Else one product for each context of the group, into the
-                    // scores' buffer, from where the softmax warps add its columns
+                    // values: levels 0 accumulates in O^T.  Else one product for each context of the group, on a copy
+                    // of O^T from which the softmax warps take its columns
                     int levels = 0;
                     bool apart = false;
                     while (ok) {
                         ok = values ? wait_mbar(&p_full[pb], p_phases >> pb & 1, abort)
-                                    : wait_mbar(&s_empty[sb], ((count >> 1) & 1) ^ 1, abort);
+                                    : wait_mbar(&s_empty[sb], ((count / C::kSBufs) & 1) ^ 1, abort);
                         p_phases ^= 1u << pb;
                         if (!ok) break;
                         tc_fence_after();
@@ -485,17 +528,23 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                             levels = *levels_s;
                             apart = levels > 0;
                         }
-                        const uint32_t d = values && !apart ? tmem + C::kTmemO : tmem + sb * C::kSN;
-                        const uint32_t add = values && !apart && i > 0 ? 1u : 0u;
+                        const uint32_t x = C::kApartInScores ? sb * C::kSN : C::kTmemX;
+                        const uint32_t d = tmem + (!values ? sb * C::kSN : apart ? x : C::kTmemO);
+                        const uint32_t add = values && i > 0 ? 1u : 0u;
                         const uint64_t ad = sdesc_sw128(ua + slot * kUnitBytes, 16, 1024);
-                        // hi and lo terms side by side in N, or hi, then lo ones into the same columns
-                        const bool in_turn = apart || (values ? C::kON : C::kSN) == NC;
-                        const uint32_t lo = values ? NC / 16 : NC * kDim / 16;
-#pragma unroll 2
-                        for (uint32_t k = 0; k < (in_turn ? 8u : 4u); ++k)
-                            mma_f8(d, ad + (k & 3) * step,
-                                   bd + (values ? pb * (2 * NC / 16) : 0u) + (k >> 2) * lo + (k & 3) * step,
-                                   apart ? make_idesc(kDim, NC, 0, 0, true, true) : idesc, k > 0 ? 1u : add);
+                        // (of two accumulators in turn: the first and third terms, then the second ones)
+                        const bool part = C::kApartTurns > 1 && apart, second = part && (levels & 1);
+                        const uint32_t turns = !values ? C::kSTurns : second ? 1 : C::kOTurns;
+                        const uint64_t bt = bd + (values ? pb * C::kPRow + (second ? NC / 16 : 0) : 0);
+#pragma unroll 1
+                        for (uint32_t m = 0; m < turns; ++m) {
+                            const uint32_t id = part || m > 0 ? idesc_turn : idesc;
+                            const uint64_t bm = bt + (m > 0 ? (values ? C::kP3Offset : NC * kDim / 16) : 0u);
+                            const uint32_t far = values && m > 0 ? 4 : 2 * step;
+#pragma unroll
+                            for (uint32_t j = 0; j < 4; ++j)
+                                mma_f8(d, ad + j * step, bm + (j & 1) * step + (j >> 1) * far, id, m + j > 0 ? 1u : add);
+                        }
                         --levels;
                         if (levels <= 0) mma_commit(&empty[slot]);
                         mma_commit(values ? &pv_done[pb] : &s_full[sb]);
@@ -583,10 +632,10 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
             bool leave = false;
             for (int i = 0; i < tiles; ++i, ++s_count) {
                 const int t0 = t_begin + i * kTile, t = t0 + self;
-                const uint32_t sb = s_count & 1, pb = s_count % C::kPBufs;
+                const uint32_t sb = s_count % C::kSBufs, pb = s_count % C::kPBufs;
                 const uint32_t v_turn = s_count / C::kV, vslot = C::kK + s_count - v_turn * C::kV;
                 uint4 *vrow = reinterpret_cast<uint4 *>(smem + vslot * kUnitBytes + self * kDim);
-                dead |= !wait_mbar_warp(&s_full[sb], (s_count >> 1) & 1, abort);
+                dead |= !wait_mbar_warp(&s_full[sb], (s_count / C::kSBufs) & 1, abort);
                 tc_fence_after();
                 const bool edge = t0 + kTile > ctx_min;  // some column does not see all of the tile
 
@@ -632,6 +681,12 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                 };
                 float x[kMine];
                 scores(x);
+                const bool keep = C::kSBufs > 1 || edge;  // an only buffer goes back at once, unless it is of use once more
+                if (!keep) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_empty[sb]);
+                }
                 float top = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < kMine; j += 2) top = fmaxf(top, fmaxf(x[j], x[j + 1]));
@@ -686,8 +741,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                 }
                 pv_wait(pb);  // this buffer of P is free
 
-                // weights: unit c / 16 of the token's row of P holds hi, unit (NC + c) / 16 lo.  hi is the weight
-                // rounded to 4 significant bits, t - (t - p) with t = p (2^20 + 1); lo the rest, exact in fp32
+                // weights, 16 columns at a time
 #pragma unroll
                 for (int c = 0; c < kMine; c += 16) {
                     if constexpr (C::kSumsInTmem) {
@@ -714,24 +768,18 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                             l[c + j + 1] = s.y;
                         }
                     }
-                    uint32_t hi[4], lo[4];
+                    uint32_t t1[4], t2[4], t3[4];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        float2 h2[2], l2[2];
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const float2 p = make_float2(x[c + j + 2 * y], x[c + j + 2 * y + 1]);
-                            const float2 tt = __fmul2_rn(p, make_float2(1048577.f, 1048577.f));
-                            const float2 minus = make_float2(-1.f, -1.f);
-                            h2[y] = __ffma2_rn(__ffma2_rn(p, minus, tt), minus, tt);
-                            l2[y] = __ffma2_rn(h2[y], minus, p);
-                        }
-                        hi[j / 4] = e4m3x2(h2[0].x, h2[0].y) | (e4m3x2(h2[1].x, h2[1].y) << 16);
-                        lo[j / 4] = e4m3x2(l2[0].x, l2[0].y) | (e4m3x2(l2[1].x, l2[1].y) << 16);
-                    }
-                    const int at = 2 * NC * pb + mine + c;
-                    *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, at / 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(smem + C::OFF_P + sw128(self, (NC + at) / 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    for (int j = 0; j < 16; j += 4)
+                        weight_terms(pack_f16(x[c + j], x[c + j + 1]), pack_f16(x[c + j + 2], x[c + j + 3]), t1[j / 4],
+                                     t2[j / 4], t3[j / 4]);
+                    const int at = C::kPRow * pb + (mine + c) / 16;
+                    uint8_t *p_s = smem + C::OFF_P;
+                    *reinterpret_cast<uint4 *>(p_s + sw128(self, at)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                    *reinterpret_cast<uint4 *>(p_s + sw128(self, at + NC / 16)) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+                    const uint32_t third = NC < 64 ? sw128(self, at + 2 * NC / 16)
+                                                   : kTile * 128 + sw128(self & 63, (self >> 6) * 4 + (mine + c) / 16);
+                    *reinterpret_cast<uint4 *>(p_s + third) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
                 }
                 if (C::kSumsInTmem) tmem_st_wait();
                 auto hand_over = [&]() {
@@ -765,15 +813,16 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                 if (!apart) {
                     hand_over();
                     if (lane == 0) {
-                        mbar_arrive(&s_empty[sb]);
+                        if (keep) mbar_arrive(&s_empty[sb]);
                         mbar_arrive(&p_full[pb]);
                     }
                     pv_open |= 1u << pb;
                     continue;
                 }
                 // 0 x NaN must not reach the rows that do not see it.  One product per context of the group,
-                // longest first, with V's tokens past it zeroed; of each product only the columns of that
-                // context are added to O^T.
+                // longest first, with V's tokens past it zeroed, on a copy of O^T (so a column's bits are those of the
+                // one product for all); of each only the columns of that context are taken over.
+                pv_wait_all();  // O^T at rest
                 int levels = 0;
                 for (int prev = INT32_MAX;; ++levels) {
                     int next = -1;
@@ -782,15 +831,34 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     if (next < 0) break;
                     prev = next;
                 }
+                levels *= C::kApartTurns;
                 if (threadIdx.x == 0) *levels_s = levels;
+                const uint32_t xo = quad + (C::kApartInScores ? sb * C::kSN : C::kTmemX);
                 for (int v = 0, cur = INT32_MAX; v < levels; ++v) {
-                    int next = -1;
-                    for (int r = 0; r < a.group; ++r)
-                        if (item->ctx[r] < cur) next = max(next, item->ctx[r]);
-                    cur = next;
-                    if (mine == 0 && t >= cur) {
+                    const uint32_t of = quad + C::kTmemO + v % C::kApartTurns * C::kXN;
+                    if (v % C::kApartTurns == 0) {
+                        int next = -1;
+                        for (int r = 0; r < a.group; ++r)
+                            if (item->ctx[r] < cur) next = max(next, item->ctx[r]);
+                        cur = next;
+                        if (mine == 0 && t >= cur) {
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) vrow[y] = make_uint4(0u, 0u, 0u, 0u);
+                            for (int y = 0; y < 8; ++y) vrow[y] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    if (i > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < kMine; c += 16) {
+#pragma unroll 1
+                            for (int y = c; y < C::kXN; y += NC) {
+                                uint32_t g[16];
+                                tmem_ld16(of + y, g);
+                                tmem_ld_wait();
+                                reg_fence(g);
+                                tmem_st16(xo + y, g);
+                            }
+                        }
+                        tmem_st_wait();
                     }
                     hand_over();
                     if (lane == 0) mbar_arrive(&p_full[pb]);
@@ -798,30 +866,26 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     pv_wait(pb);
 #pragma unroll 1
                     for (int c = 0; c < kMine; c += 16) {
-                        uint32_t h[16], g[16];
-                        tmem_ld16(quad + sb * C::kSN + c, h);
-                        // the hi half of O^T takes the sum; in the item's first tile a lo half becomes zero
-                        tmem_ld16(quad + C::kTmemO + c, g);
-                        tmem_ld_wait();
-                        reg_fence(h);
-                        reg_fence(g);
+#pragma unroll 1
+                        for (int y = c; y < C::kXN; y += NC) {
+                            uint32_t h[16], g[16];
+                            tmem_ld16(xo + y, h);
+                            tmem_ld16(of + y, g);
+                            tmem_ld_wait();
+                            reg_fence(h);
+                            reg_fence(g);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (cs->ctx[mine + c + j] == cur)
-                                g[j] = __float_as_uint(__uint_as_float(h[j]) + (i > 0 ? __uint_as_float(g[j]) : 0.f));
-                        tmem_st16(quad + C::kTmemO + c, g);
-                        if (C::kON > NC && i == 0) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) g[j] = 0u;
-                            tmem_st16(quad + C::kTmemO + NC + c, g);
+                            for (int j = 0; j < 16; ++j)
+                                if (cs->ctx[mine + c + j] == cur) g[j] = h[j];
+                            tmem_st16(of + y, g);
                         }
-                        tmem_st_wait();
                     }
+                    tmem_st_wait();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (threadIdx.x == 0) *levels_s = 0;
-                if (lane == 0) mbar_arrive(&s_empty[sb]);
+                if (keep && lane == 0) mbar_arrive(&s_empty[sb]);
             }
             if (leave) break;
 
@@ -861,16 +925,15 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
             for (int c = 0; c < min(ncols - mine, kMine); c += 16) {
                 uint32_t h[16];
                 tmem_ld16(quad + C::kTmemO + c, h);
-                if constexpr (C::kON > NC) {
+                tmem_ld_wait();
+                reg_fence(h);
+#pragma unroll
+                for (int y = NC; y < C::kON; y += NC) {
                     uint32_t g[16];
-                    tmem_ld16(quad + C::kTmemO + NC + c, g);
+                    tmem_ld16(quad + C::kTmemO + y + c, g);
                     tmem_ld_wait();
-                    reg_fence(h);
                     reg_fence(g);
                     add16(h, g);
-                } else {
-                    tmem_ld_wait();
-                    reg_fence(h);
                 }
                 const int here = ncols - mine - c;
                 if (parts > 1) {  // (so the part has tiles)

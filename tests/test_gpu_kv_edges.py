@@ -12,12 +12,11 @@ pytestmark = pytest.mark.gpu
 
 def weight_error(fmt, dim):
     """A softmax weight as it multiplies V: (relative to itself, against its part's largest).  bf16 pools: two bf16
-    terms, 2^-9 2^-8.  FP8 pools of head_dim 64: fp16, half a step being 2^-11, with a smallest step of 2^-24 where the
-    largest weight is at least 2^7; of head_dim 128: two e4m3 terms, 2^-8, with a smallest step of 2^-9 (half of it
-    for each term) where the largest is at least 2^6."""
+    terms, 2^-9 2^-8.  FP8 pools: fp16, half a step being 2^-11, with a smallest step of 2^-16 or 2^-24 where the
+    largest weight is at least 2^13 or 2^7."""
     if fmt == "bf16":
         return 2.0 ** -16, 0.0
-    return (2.0 ** -8, 2.0 ** -15) if dim == 128 else (2.0 ** -11, 2.0 ** -32)
+    return 2.0 ** -11, 2.0 ** -29 if dim == 128 else 2.0 ** -32
 
 
 def check_weights(c, out, lse, rows=None):
@@ -132,3 +131,36 @@ def test_a_refused_group_is_answered_with_nothing(fmt, dim, bad):
         for got, w in zip((out, lse), want):
             assert torch.equal(got[:2], w[:2]) and torch.equal(got[4:], w[4:])
         c.run(workspace=ws)
+
+
+# ------------------------------------------------------------------ small weights beside large ones
+
+@pytest.mark.parametrize("fmt, dim", [("fp8", 128), ("fp8", 64), ("bf16", 128)])
+@pytest.mark.parametrize("kv_heads, hpg, group", [(4, 13, 1), (4, 13, 2), (4, 13, 4), (8, 13, 1), (8, 13, 8)])
+@pytest.mark.parametrize("ctx", [500, 32768, 131072])
+@pytest.mark.parametrize("noise", [0.0, 0.5])
+def test_the_background_behind_an_attention_sink(fmt, dim, kv_heads, hpg, group, ctx, noise):
+    """The first token 8 to 20 log2 units ahead of all others, a head each, and values of one sign: the many small
+    weights come to as much as the large one."""
+    c = Case(64, fmt, [ctx], kv_heads, hpg, dim, 128, group=group)
+    raw = bits(c.pool)
+    code = lambda x: bits(torch.tensor([x], device="cuda").to(c.pool.dtype)).item()  # noqa: E731
+    first = c.table[0, 0].item()
+    raw[:, :, 1] = code(64.0)
+    raw[first, :, 1, 0] = code(-64.0)
+    key = c.pool[:, :, 0].float() * noise
+    key[..., 0] = 0.0
+    key = key.to(c.pool.dtype)
+    key[first, :, 0, 0] = 64.0
+    c.pool[:, :, 0].copy_(key) if fmt == "bf16" else raw[:, :, 0].copy_(key.view(torch.uint8))
+    ahead = 8.0 + torch.arange(hpg, device="cuda").float().repeat(kv_heads)
+    c.q[..., 0] = (ahead * math.log(2.0) / (64.0 * c.ks * c.sm)).to(torch.bfloat16)
+    check_weights(c, *c.run(), rows=range(0, group, 3))
+
+
+@pytest.mark.parametrize("fmt, dim", [("fp8", 128), ("fp8", 64), ("bf16", 128), ("bf16", 64)])
+@pytest.mark.parametrize("kv_heads, hpg, group", [(2, 7, 1), (2, 16, 2), (1, 33, 2), (2, 4, 8), (1, 128, 1)])
+@pytest.mark.parametrize("q_scale", [0.3, 1.0, 4.0])
+def test_weights_keep_their_bits(fmt, dim, kv_heads, hpg, group, q_scale):
+    c = Case(65, fmt, [group + 1, 140, 1000, 6000], kv_heads, hpg, dim, 64, group=group, q_scale=q_scale)
+    check_weights(c, *c.run())
