@@ -565,7 +565,9 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
  * q: bf16 [num_rows, num_heads, head_dim], rows q_stride elements apart (a multiple of 8), 16-byte
  * aligned; num_heads a multiple of kv_heads, at most DSA_KV_MAX_HPG times it; out: bf16 [num_rows,
  * num_heads, head_dim], 16-byte aligned; lse: fp32 [num_rows, num_heads] or NULL.  A head with no
- * visible token, or whose visible scores are all -inf, gets out = 0 and lse = -inf.  What slots at
+ * visible token, or whose visible scores are all -inf, gets out = 0 and lse = -inf.  An infinity of
+ * V (bf16 pool) that it sees makes its dim infinite, or NaN beside one of the other sign or where its
+ * weight is 0 in fp32.  What slots at
  * or past row_ctx[r] hold never reaches row r (NaN included).  rows->rows_per_group (1, 2, 4 or 8)
  * consecutive rows of one request (speculative verify) share each read of the cache.
  *

@@ -29,7 +29,7 @@
 // running sums in registers: no TMEM round trip per tile.
 //
 // Precision.  bf16 pool: products are exact in fp32; a weight rounded to bf16 (2^-9) would add as much
-// error as rounding the output does, so P enters as hi + lo bf16 terms (2^-17).  FP8 pool: e4m3 codes
+// error as rounding the output does, so P enters as hi + lo bf16 terms (2^-16).  FP8 pool: e4m3 codes
 // are exact in fp16; q is scaled by a power of two per column to fit fp16's range (exact but for
 // elements 2^-25 below the column's largest), P is one fp16 term (2^-12), scaled by 2^7 so that weights
 // down to 2^-21 of the base stay normal.  (mma.sync on e4m3 operands was tried for S: the warps spend their time in
@@ -121,6 +121,18 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t &lo, uint32_t
         "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(v));
+}
+
+// Two weights as hi + lo bf16 terms.  hi is cut off, not rounded, so that lo is positive, and lo is never 0 beside a hi
+// that is not: an infinity of V times the one and the other is the same infinity.
+__device__ __forceinline__ void split_weights(float p0, float p1, uint32_t &hi, uint32_t &lo) {
+    hi = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+    const uint32_t least = 0x00800080u;  // 2^-126
+    const __nv_bfloat162 rest = __floats2bfloat162_rn(p0 - bf16_lo(hi), p1 - bf16_hi(hi));
+    const __nv_bfloat162 some = __hmin2(*reinterpret_cast<const __nv_bfloat162 *>(&hi),
+                                        *reinterpret_cast<const __nv_bfloat162 *>(&least));
+    const __nv_bfloat162 l = __hmax2(rest, some);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
 // Byte offset of 16-byte unit `u` of token `t` in a side (K or V) of a stage, as its TMA boxes landed.
@@ -525,8 +537,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         if constexpr (kFp8) {
                             hi[n][x] = pack_f16(p0, p1);
                         } else {
-                            hi[n][x] = pack_bf16(p0, p1);
-                            lo[n][x] = pack_bf16(p0 - bf16_lo(hi[n][x]), p1 - bf16_hi(hi[n][x]));
+                            split_weights(p0, p1, hi[n][x], lo[n][x]);
                         }
                     }
                 // O^T += V^T P^T.  In an edge step the rows of the group take turns, with V's tokens at and past

@@ -164,3 +164,28 @@ def test_the_background_behind_an_attention_sink(fmt, dim, kv_heads, hpg, group,
 def test_weights_keep_their_bits(fmt, dim, kv_heads, hpg, group, q_scale):
     c = Case(65, fmt, [group + 1, 140, 1000, 6000], kv_heads, hpg, dim, 64, group=group, q_scale=q_scale)
     check_weights(c, *c.run())
+
+
+# ------------------------------------------------------------------ values that are no numbers
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hpg, group", [(1, 1), (5, 1), (16, 2), (7, 4)])
+@pytest.mark.parametrize("ctx", [40, 3000])
+def test_infinite_values_that_a_row_sees(dim, hpg, group, ctx):
+    """bf16 pools: an infinity of V makes its dim infinite, two of opposite signs make it NaN."""
+    c = Case(66, "bf16", [ctx], 2, hpg, dim, 16, group=group)
+    at = [(t, d) for d, t in enumerate((0, 3, 17, ctx - group, ctx // 2, ctx // 3))]
+    for sign, (t, d) in zip((1, -1, 1, -1, 1, -1), at):
+        c.pool[c.table[0, t // 16].item(), :, 1, t % 16, d] = sign * math.inf
+    for t, sign in ((5, 1), (30, -1)):
+        c.pool[c.table[0, t // 16].item(), :, 1, t % 16, 20] = sign * math.inf
+    out, lse = c.run()
+    for r in range(group):
+        for h in range(2):
+            k, v = c.tokens(r, h)
+            ref = torch.softmax(c.q[r, h * hpg:(h + 1) * hpg].double() @ k.T * c.sm, -1) @ v
+            got = out[r, h * hpg:(h + 1) * hpg].double()
+            assert torch.equal(torch.isnan(got), torch.isnan(ref)) and torch.isnan(ref[:, 20]).all()
+            odd = torch.isinf(ref)
+            assert torch.equal(torch.isinf(got), odd) and odd.sum() >= 5 * hpg and torch.equal(got[odd], ref[odd])
+    assert torch.isfinite(lse).all()
