@@ -703,7 +703,7 @@ static int check_kv_cache(const dsa_kv_cache *c) {
     if (c->head_dim != 64 && c->head_dim != 128) return DSA_ERR_UNSUPPORTED;
     if (c->kv_heads < 1 || c->num_pages <= 0) return DSA_ERR_INVALID_ARG;
     if (c->kv_heads > kKvMaxHeads) return DSA_ERR_UNSUPPORTED;
-    if (c->num_pages >= (1ll << 31) / (2ll * c->kv_heads * c->page_size)) return DSA_ERR_UNSUPPORTED;
+    if (c->num_pages > ((1ll << 31) - 1) / (2ll * c->kv_heads * c->page_size)) return DSA_ERR_UNSUPPORTED;
     if (c->format == DSA_KV_FP8)
         for (float v : {c->k_scale, c->v_scale})
             if (!std::isfinite(v) || !(v > 0.f)) return DSA_ERR_INVALID_ARG;

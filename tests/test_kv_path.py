@@ -140,6 +140,15 @@ BAD_CACHES = [(dict(fmt=P.KEY_FP8), P.ERR_UNSUPPORTED), (dict(page=8), P.ERR_UNS
               (dict(ks=float("inf")), P.ERR_INVALID_ARG), (dict(vs=float("nan")), P.ERR_INVALID_ARG)]
 
 
+def test_the_largest_pool(lib):
+    """Of rows of head_dim, counted exactly: num_pages * kv_heads * 2 * page_size < 2^31."""
+    most = ((1 << 31) - 1) // (3 * 2 * 16)
+    assert most * 3 * 2 * 16 < 1 << 31 <= (most + 1) * 3 * 2 * 16
+    size = lambda n: lib.dsa_kv_attention_workspace_size(kv(heads=3, page=16, pages=n), 1, 3, 1 << 20)  # noqa: E731
+    assert size(most) > 0 and size(most + 1) == 0
+    assert lib.dsa_kv_attention_workspace_size(kv(heads=4, page=16, pages=1 << 24), 1, 4, 1 << 20) == 0
+
+
 @pytest.mark.parametrize("change, want", BAD_CACHES)
 def test_cache_refusals(lib, change, want):
     c = kv(**change)
