@@ -189,3 +189,23 @@ def test_infinite_values_that_a_row_sees(dim, hpg, group, ctx):
             odd = torch.isinf(ref)
             assert torch.equal(torch.isinf(got), odd) and odd.sum() >= 5 * hpg and torch.equal(got[odd], ref[odd])
     assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("fmt, dim", [("bf16", 64), ("bf16", 128), ("fp8", 64), ("fp8", 128)])
+@pytest.mark.parametrize("hpg, group", [(5, 1), (16, 2), (16, 4)])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_a_head_of_no_numbers_leaves_other_groups_their_bits(fmt, dim, hpg, group, value):
+    c = Case(49, fmt, [700, 90], 2, hpg, dim, 32, group=group)
+    want = c.run()
+    q = c.q.clone()
+    q[-1, hpg + 2, 3] = value
+    got = c.run(q=q)
+    for a, b in zip(got, want):
+        assert torch.equal(a[:group], b[:group])
+        assert torch.equal(a[group:, :hpg], b[group:, :hpg])  # (the other KV head)
+    # the other heads of its block: either answer is within its rounding and its weights' of the formula's (values up to
+    # 448 / 90 or 6)
+    rest = torch.ones(q.shape[:2], dtype=torch.bool, device="cuda")
+    rest[-1, hpg + 2] = False
+    a, b = (x[0][rest].float() for x in (got, want))
+    assert ((a - b).abs() <= 2 * (2.0 ** -8 * b.abs() + 2.0 ** -10 * 6)).all()
