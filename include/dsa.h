@@ -512,8 +512,9 @@ typedef struct dsa_rope_spec {
 
 /* One tensor [num_tokens, num_heads, rot_dim]: the rotary part of every head alone, in place inside
  * larger heads through its strides (in elements).  x may equal out (with equal strides); an output
- * overlaps nothing else that the call reads or writes (two of its tensors at one output address, or
- * one's output at another's input, are DSA_ERR_INVALID_ARG). */
+ * overlaps nothing else that the call reads or writes.  What can be told from the layouts is
+ * DSA_ERR_INVALID_ARG: tensors at one address, and any overlap of tensors whose tokens follow one
+ * another at the same distance (parts of one packed projection) or of a single token. */
 typedef struct dsa_rope_tensor {
     const void *x;
     void *out;
@@ -550,7 +551,7 @@ typedef struct dsa_kv_rows {
  *   DSA_KV_FP8:  e4m3(x / scale), IEEE fp32 division, round to nearest even, saturating to +-448
  * rope != NULL rotates K's dims [rot_offset, rot_offset + rot_dim) on the way, in fp32, and with
  * q != NULL also rotates q (bf16, [num_tokens, q->num_heads, rot_dim]) as dsa_rope does, in the same
- * launch; q needs rope.  slots: device [num_tokens], distinct (a slot listed twice holds bytes of
+ * launch; q needs rope, and its output overlaps neither k, v nor the pool.  slots: device [num_tokens], distinct (a slot listed twice holds bytes of
  * either token, in any mixture).  A slot outside the pool, or a slot >= 0 of a token at a negative
  * position, is DSA_ERR_BOUNDS and not written; every other byte of the pool keeps its value.
  */
@@ -575,7 +576,8 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
  * log-sum-exp, and a row's bits depend on nothing outside its group (batch invariance): the workspace
  * (device, 256-byte aligned, dsa_kv_attention_workspace_size bytes, no initial contents; NULL when
  * that is 0) holds the parts in fp32 and serves one call at a time: calls that may run at once,
- * captured graphs among them, have one each.  Outputs overlap no input.  Scores and sums are fp32.
+ * captured graphs among them, have one each.  Outputs overlap no input (out or lse over q, or over one
+ * another: DSA_ERR_INVALID_ARG).  Scores and sums are fp32.
  * The softmax weights multiply V as the sum of two bf16 terms (bf16 pool) or rounded to fp16 (FP8
  * pool), where they keep steps of 2^-29 of the largest of their part (head_dim 64: 2^-31) or better.
  * Over an FP8 pool q is scaled by a power of two per head and rounded to fp16 (head_dim 64) or to the

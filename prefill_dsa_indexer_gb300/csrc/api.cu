@@ -654,6 +654,56 @@ static bool apart(int64_t token_stride, int64_t tokens, int64_t head_stride, int
            (token_stride >= rot && (head_stride - rot) / (tokens - 1) >= token_stride);
 }
 
+// Memory that a tensor takes: `width` bytes at base + t * token + h * head.
+struct Span {
+    uintptr_t base;
+    int64_t tokens, token, heads, head, width;
+    int64_t row() const { return (heads - 1) * head + width; }  // from a token's first byte to its last
+};
+
+// Whether the heads of two tokens meet, the second's first head `off` bytes behind the first's.
+static bool rows_meet(const Span &a, const Span &b, int64_t off) {
+    for (int64_t i = 0, j = 0; i < a.heads && j < b.heads;) {
+        if (i * a.head + a.width <= off + j * b.head) ++i;
+        else if (off + j * b.head + b.width <= i * a.head) ++j;
+        else return true;
+    }
+    return false;
+}
+
+// Whether two tensors are known to share a byte: of tokens that follow one another (no token begins before the one
+// before it ends) at one distance, or of a single token, that is decided; other layouts that lie within each other's
+// range are left to the caller.
+static bool meet(const Span &a, const Span &b) {
+    const uintptr_t a_end = a.base + static_cast<uintptr_t>((a.tokens - 1) * a.token + a.row());
+    const uintptr_t b_end = b.base + static_cast<uintptr_t>((b.tokens - 1) * b.token + b.row());
+    if (a_end <= b.base || b_end <= a.base) return false;
+    const int64_t d = static_cast<int64_t>(b.base - a.base);
+    if (a.tokens == 1 && b.tokens == 1) return rows_meet(a, b, d);
+    const int64_t step = a.tokens == 1 ? b.token : a.token;
+    if ((a.tokens > 1 && b.tokens > 1 && a.token != b.token) || step < a.row() || step < b.row()) return false;
+    // tokens whose numbers differ by q lie `off` apart, those one further off - step
+    const int64_t q = d >= 0 ? d / step : -((-d + step - 1) / step), off = d - q * step;
+    return (q < a.tokens && -q < b.tokens && rows_meet(a, b, off)) ||
+           (q + 1 < a.tokens && -(q + 1) < b.tokens && rows_meet(a, b, off - step));
+}
+
+// Whether some token's row reaches into a block of memory.
+static bool within(const Span &a, const Span &block) {
+    const int64_t lo = static_cast<int64_t>(block.base - a.base) - a.row(), hi = lo + a.row() + block.width;
+    if (hi <= 0) return false;             // token t does where lo < t * a.token < hi
+    if (lo < 0 || a.tokens == 1 || a.token == 0) return lo < 0;
+    const int64_t t = lo / a.token + 1;
+    return t < a.tokens && t * a.token < hi;
+}
+
+static Span input_of(const RopeTensor &t, int32_t tokens, int32_t rot, int elem) {
+    return {reinterpret_cast<uintptr_t>(t.x), tokens, t.x_token * elem, t.heads, t.x_head * elem, rot * elem};
+}
+static Span output_of(const RopeTensor &t, int32_t tokens, int32_t rot, int elem) {
+    return {reinterpret_cast<uintptr_t>(t.out), tokens, t.out_token * elem, t.heads, t.out_head * elem, rot * elem};
+}
+
 // One rotated tensor, and whether 16-byte accesses reach all of its rotary parts.
 static int rope_tensor(const dsa_rope_tensor &t, int32_t tokens, int32_t rot, int elem, RopeTensor *out) {
     if (t.x == nullptr || t.out == nullptr || t.num_heads < 1) return DSA_ERR_INVALID_ARG;
@@ -672,6 +722,8 @@ static int rope_tensor(const dsa_rope_tensor &t, int32_t tokens, int32_t rot, in
                      t.out_head_stride % v == 0;
     *out = RopeTensor{t.x, t.out, t.num_heads, half, vec, t.x_token_stride, t.x_head_stride, t.out_token_stride,
                       t.out_head_stride};
+    if (t.x != t.out && meet(input_of(*out, tokens, rot, elem), output_of(*out, tokens, rot, elem)))
+        return DSA_ERR_INVALID_ARG;
     return DSA_OK;
 }
 
@@ -685,11 +737,18 @@ int dsa_rope(const dsa_rope_spec *rope, const dsa_rope_tensor *tensors, int32_t 
     if (rc != DSA_OK) return rc;
     if (tensors == nullptr) return DSA_ERR_INVALID_ARG;
     RopeArgs a = {rope->turns, rope->positions, rope->rot_dim, rope->scale, num_tokens, num_tensors, {}};
+    const int elem = dtype == DSA_DTYPE_BF16 ? 2 : 4;
     for (int i = 0; i < num_tensors; ++i) {
-        rc = rope_tensor(tensors[i], num_tokens, rope->rot_dim, dtype == DSA_DTYPE_BF16 ? 2 : 4, &a.t[i]);
+        rc = rope_tensor(tensors[i], num_tokens, rope->rot_dim, elem, &a.t[i]);
         if (rc != DSA_OK) return rc;
-        for (int j = 0; j < i; ++j)
-            if (a.t[i].out == a.t[j].out || a.t[i].out == a.t[j].x || a.t[i].x == a.t[j].out) return DSA_ERR_INVALID_ARG;
+        const Span out = output_of(a.t[i], num_tokens, rope->rot_dim, elem);
+        const Span x = input_of(a.t[i], num_tokens, rope->rot_dim, elem);
+        for (int j = 0; j < i; ++j) {
+            const Span other = output_of(a.t[j], num_tokens, rope->rot_dim, elem);
+            if (a.t[i].out == a.t[j].out || a.t[i].out == a.t[j].x || a.t[i].x == a.t[j].out || meet(out, other) ||
+                meet(x, other) || meet(out, input_of(a.t[j], num_tokens, rope->rot_dim, elem)))
+                return DSA_ERR_INVALID_ARG;
+        }
     }
     return launch_status(launch_rope(a, dtype, static_cast<cudaStream_t>(stream)));
 }
@@ -738,6 +797,12 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
             a.rope.num_tensors = 1;
             rc = rope_tensor(*q, num_tokens, rope->rot_dim, 2, &a.rope.t[0]);
             if (rc != DSA_OK) return rc;
+            const Span out = output_of(a.rope.t[0], num_tokens, rope->rot_dim, 2);
+            const Span k = {reinterpret_cast<uintptr_t>(kv->k), num_tokens, kv->k_stride * 2, 1, 0, width * 2};
+            const Span v = {reinterpret_cast<uintptr_t>(kv->v), num_tokens, kv->v_stride * 2, 1, 0, width * 2};
+            const Span pool = {reinterpret_cast<uintptr_t>(cache->base), 1, 0, 1, 0,
+                               cache->num_pages * cache->page_size * 2 * width * (cache->format == DSA_KV_FP8 ? 1 : 2)};
+            if (meet(out, k) || meet(out, v) || within(out, pool)) return DSA_ERR_INVALID_ARG;
         }
     }
     // 16-byte pieces need aligned rows, and rotary parts (or halves) of whole pieces
@@ -796,6 +861,12 @@ int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint
         if (workspace == nullptr || workspace_bytes < need) return DSA_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return DSA_ERR_INVALID_ARG;
     }
+    const int64_t row = static_cast<int64_t>(num_heads) * cache->head_dim * 2;
+    const Span q_span = {reinterpret_cast<uintptr_t>(q), rows->num_rows, q_stride * 2, 1, 0, row};
+    const Span out_span = {reinterpret_cast<uintptr_t>(out), 1, 0, 1, 0, rows->num_rows * row};
+    const Span lse_span = {reinterpret_cast<uintptr_t>(lse), 1, 0, 1, 0, static_cast<int64_t>(rows->num_rows) * num_heads * 4};
+    if (within(q_span, out_span) || (lse != nullptr && (within(q_span, lse_span) || within(out_span, lse_span))))
+        return DSA_ERR_INVALID_ARG;
     const bool fp8 = cache->format == DSA_KV_FP8;
     KvAttnArgs a = {};
     a.pool = cache->base;

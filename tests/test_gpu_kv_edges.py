@@ -209,3 +209,69 @@ def test_a_head_of_no_numbers_leaves_other_groups_their_bits(fmt, dim, hpg, grou
     rest[-1, hpg + 2] = False
     a, b = (x[0][rest].float() for x in (got, want))
     assert ((a - b).abs() <= 2 * (2.0 ** -8 * b.abs() + 2.0 ** -10 * 6)).all()
+
+
+# ------------------------------------------------------------------ tensors that share a buffer
+
+def test_rope_takes_parts_of_one_buffer_that_do_not_overlap():
+    """Random pairs of tensors in one buffer: refused if and only if an output meets anything but its own input."""
+    g = torch.Generator().manual_seed(5)
+    pick = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))  # noqa: E731
+    table = P.rope_table(8)
+    refused = 0
+    for case in range(400):
+        n, step = pick(1, 4), pick(40, 90)
+        buffer = torch.arange(step * 8, device="cuda").to(torch.bfloat16)
+        positions = torch.arange(n, device="cuda", dtype=torch.int32)
+
+        def view():
+            heads = pick(1, 3)
+            head = pick(8, min(16, (step - 8) // max(heads - 1, 1)))
+            return buffer.as_strided((n, heads, 8), (step, head, 1), pick(0, step * 3))
+
+        xs = [view(), view()]
+        outs = [x if pick(0, 1) else buffer.as_strided(x.shape, x.stride(), pick(0, step * 3)) for x in xs]
+        index = torch.arange(buffer.numel())
+        used = lambda t: set(index.as_strided(t.shape, t.stride(), t.storage_offset()).flatten().tolist())  # noqa: E731
+        meets = bool(used(outs[0]) & used(outs[1]))
+        for i in range(2):
+            same = outs[i].storage_offset() == xs[i].storage_offset()
+            meets |= bool(used(outs[i]) & used(xs[1 - i])) or (not same and bool(used(outs[i]) & used(xs[i])))
+        before = buffer.clone()
+        if meets:
+            refused += 1
+            with pytest.raises(P.DsaError):
+                P.rope(xs, table, positions, out=outs)
+            continue
+        want = [P.rope(x.contiguous(), table, positions) for x in xs]
+        P.rope(xs, table, positions, out=outs)
+        rest = torch.ones_like(buffer, dtype=torch.bool)
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w), case
+            rest.as_strided(o.shape, o.stride(), o.storage_offset()).fill_(False)
+        assert torch.equal(buffer[rest], before[rest]), case
+    assert 50 < refused < 350
+
+
+def test_outputs_beside_their_inputs_in_one_buffer():
+    """A step whose queries, keys, values, rotated queries and answers are parts of one buffer."""
+    c = Case(67, "bf16", [300, 90], 2, 4, 64, 16)
+    R, H, D = 2, 8, 64
+    buffer = torch.zeros(R * 3 * H * D + R * H * D, dtype=torch.bfloat16, device="cuda")
+    rows = buffer[:R * 3 * H * D].view(R, 3 * H, D)
+    q, k, v, turned = rows[:, :H], rows[:, H:H + 2], rows[:, H + 2:H + 4], rows[:, 2 * H:]
+    q.copy_(c.q)
+    k.copy_(c.q[:, :2])
+    v.copy_(c.q[:, 2:4])
+    out = buffer[R * 3 * H * D:].view(R, H, D)
+    slots = torch.tensor([c.table[r, (n - 1) // 16].item() * 16 + (n - 1) % 16 for r, n in enumerate(c.rows)],
+                         dtype=torch.int32, device="cuda")
+    positions = (c.row_ctx - 1).contiguous()
+    P.kv_insert(c.kv, slots, k, v, rope=P.rope_table(D), positions=positions, q=q, q_out=turned)
+    _, lse = P.kv_attention(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, turned, out=out)
+    c.q = turned.clone()
+    check_weights(c, out, lse)
+    with pytest.raises(P.DsaError):
+        P.kv_attention(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q, out=c.q)
+    with pytest.raises(P.DsaError):
+        P.kv_insert(c.kv, slots, k, v, rope=P.rope_table(D), positions=positions, q=q, q_out=rows[:, H - 1:2 * H - 1])

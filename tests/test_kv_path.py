@@ -132,6 +132,45 @@ def test_rope_outputs_that_overlap_are_refused(lib):
     assert call(t(FAKE, 2 * FAKE, 4, os=(7, 63)), tok=1) == P.ERR_INVALID_ARG
 
 
+def test_rope_outputs_that_overlap_in_part_are_refused(lib):
+    """Tensors whose tokens lie at one distance, and single tokens."""
+    spec = P._RopeSpec(FAKE, FAKE, 64, 1.0)
+    t = lambda x, out, heads=4, xs=(256, 64), os=(256, 64): P._RopeTensor(x, out, heads, 0, *xs, *os)  # noqa: E731
+    call = lambda *ts, tok=3, dt=1: lib.dsa_rope(spec, (P._RopeTensor * len(ts))(*ts), len(ts), dt, tok, None)  # noqa: E731
+    # an output a little ahead of or behind its own input; tokens are 512 bytes apart
+    for shift in (2, -2, 64, 126, 512, -1024, 1026, 512 * 3 - 2):
+        assert call(t(4 * FAKE, 4 * FAKE + shift)) == P.ERR_INVALID_ARG, shift
+    # a packed row of 8 heads of 128 (2,048 bytes): outputs of heads 0-3 and 3-6, and of a later token's
+    packed = lambda at, heads=4, x=FAKE: t(x, 4 * FAKE + at, heads, os=(1024, 128))  # noqa: E731
+    for at in (3 * 256, 3 * 256 + 126, 256, 2048 + 256, 2 * 2048 + 3 * 256):
+        assert call(packed(0), packed(at, x=2 * FAKE)) == P.ERR_INVALID_ARG, at
+        assert call(packed(at), packed(0, x=2 * FAKE)) == P.ERR_INVALID_ARG, at
+    # an output over another tensor's input
+    assert call(packed(0), t(4 * FAKE + 130, 8 * FAKE, 4, xs=(1024, 128))) == P.ERR_INVALID_ARG
+    assert call(t(4 * FAKE - 1922, 8 * FAKE, 4, xs=(1024, 128)), packed(0)) == P.ERR_INVALID_ARG
+    # single tokens of any strides, fp32
+    assert call(t(FAKE, 4 * FAKE, 4, os=(0, 100)), t(2 * FAKE, 4 * FAKE + 1000, 2, os=(0, 64)), tok=1, dt=2) == \
+        P.ERR_INVALID_ARG
+
+
+def test_insert_and_attention_outputs_that_overlap_are_refused(lib):
+    spec = P._RopeSpec(FAKE, FAKE, 64, 1.0)
+    base = 16 * FAKE  # the pool: 10 pages of 64 tokens, 655,360 bytes
+    call = lambda out, k=FAKE, v=2 * FAKE, ks=2048: lib.dsa_kv_insert(  # noqa: E731
+        kv(base=base), FAKE, 3, P._KvRows(k, v, ks, ks, 0, 0), spec, P._RopeTensor(out, out, 4, 0, 2048, 128, 2048, 128),
+        None, None)
+    for out in (base, base + 655360 - 128, base - 128 + 16, base - 2 * 4096 - 768):
+        assert call(out) == P.ERR_INVALID_ARG, out
+    assert call(FAKE + 1000) == P.ERR_INVALID_ARG and call(2 * FAKE + 4096 - 768) == P.ERR_INVALID_ARG
+    att = lambda q, out, lse=None, n=3, stride=8192: lib.dsa_kv_attention(  # noqa: E731
+        kv(base=base), rows(n=n), q, stride, 64, 0.1, out, lse, None, 0, None, None)
+    for q, out, lse in ((FAKE, FAKE, None), (FAKE, FAKE + 16, None), (FAKE + 3 * 16384 - 16, FAKE, None),
+                        (8 * FAKE, FAKE, 8 * FAKE + 4), (8 * FAKE, FAKE, FAKE + 3 * 16384 - 4)):
+        assert att(q, out, lse) == P.ERR_INVALID_ARG
+    # out over the second row of a q whose rows lie further apart
+    assert att(FAKE, FAKE + 32768 - 16, n=2, stride=16384) == P.ERR_INVALID_ARG
+
+
 BAD_CACHES = [(dict(fmt=P.KEY_FP8), P.ERR_UNSUPPORTED), (dict(page=8), P.ERR_UNSUPPORTED),
               (dict(page=48), P.ERR_UNSUPPORTED), (dict(page=256), P.ERR_UNSUPPORTED), (dict(dim=96), P.ERR_UNSUPPORTED),
               (dict(dim=256), P.ERR_UNSUPPORTED), (dict(heads=0), P.ERR_INVALID_ARG), (dict(pages=0), P.ERR_INVALID_ARG),
