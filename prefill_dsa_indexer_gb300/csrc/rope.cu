@@ -480,10 +480,18 @@ __global__ void __launch_bounds__(kThreads, 6) kv_insert_kernel(const __grid_con
 
 // Tiles of sixteen pieces a thread once there are enough to fill the GPU, of one a thread, as many CTAs as
 // possible, for the few tokens of a decode step.  The two prefills above with 16, 18 and 24 pieces: rope 35.8,
-// 35.4 and 35.5 us, insert 48.0, 48.6 and 54.8 us.
-bool add_segment(Plan &p, uint64_t &ctas, int num_tokens, int heads, uint32_t units, int pairs, bool split_heads) {
+// 35.4 and 35.5 us, insert 48.0, 48.6 and 54.8 us.  "Enough", in pieces, one / sixteen a thread (us in a graph):
+//   rope     98,304 (128 tokens of 98 heads of 64)       3.4 / 4.1    196,608  5.4 / 4.1    786,432  14.8 / 7.5
+//   insert's q, K and V at one: 262,144 (512 x 64 heads) 7.0 / 8.1    524,288 12.7 / 10.1
+//   K and V  262,144 (2,048 tokens of 8 heads of 128)    7.7 / 13.0   524,288 (4,096 of 4, beside q) 33.1 / 31.7
+//            1,048,576 (8,192 of 4, beside q)           65.7 / 47.7   (no ring brings their pieces, so that long
+//            tiles on few SMs take longer)
+constexpr uint64_t kManyRope = 1u << 17, kManyQ = 1u << 19, kManyKv = 1u << 20;
+
+bool add_segment(Plan &p, uint64_t &ctas, int num_tokens, int heads, uint32_t units, int pairs, bool split_heads,
+                 uint64_t many) {
     const uint64_t pieces = static_cast<uint64_t>(num_tokens) * heads * units;
-    const uint32_t target = pieces >= (1u << 20) ? 16 * kThreads : kThreads;
+    const uint32_t target = pieces >= many ? 16 * kThreads : kThreads;
     Segment &g = p.s[p.n++];
     const uint32_t per_token = static_cast<uint32_t>(heads) * units;
     g.units = units;
@@ -517,7 +525,7 @@ cudaError_t launch_rope(const RopeArgs &a, int32_t dtype, cudaStream_t s) {
     uint64_t ctas = 0;
     const int v = dtype == DSA_DTYPE_BF16 ? 8 : 4;
     for (int i = 0; i < a.num_tensors; ++i)
-        if (!add_segment(p, ctas, a.num_tokens, a.t[i].heads, rope_units(a.t[i], a.rot, v), a.rot / 2, true))
+        if (!add_segment(p, ctas, a.num_tokens, a.t[i].heads, rope_units(a.t[i], a.rot, v), a.rot / 2, true, kManyRope))
             return cudaErrorInvalidConfiguration;
     return dtype == DSA_DTYPE_BF16
                ? launch_pdl(rope_kernel<__nv_bfloat16>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, a, p)
@@ -529,11 +537,11 @@ cudaError_t launch_kv_insert(const KvInsertArgs &a, cudaStream_t s) {
     Plan p = {};
     uint64_t ctas = 0;
     if (!add_segment(p, ctas, a.rope.num_tokens, 2 * a.kv_heads, static_cast<uint32_t>(a.head_dim / (a.vec ? 8 : 1)),
-                     a.rope.rot / 2, false))
+                     a.rope.rot / 2, false, kManyKv))
         return cudaErrorInvalidConfiguration;
     if (a.rope.num_tensors > 0 &&
         !add_segment(p, ctas, a.rope.num_tokens, a.rope.t[0].heads, rope_units(a.rope.t[0], a.rope.rot, 8),
-                     a.rope.rot / 2, true))
+                     a.rope.rot / 2, true, kManyQ))
         return cudaErrorInvalidConfiguration;
     return launch_pdl(kv_insert_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, a, p);
 }

@@ -275,3 +275,25 @@ def test_outputs_beside_their_inputs_in_one_buffer():
         P.kv_attention(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q, out=c.q)
     with pytest.raises(P.DsaError):
         P.kv_insert(c.kv, slots, k, v, rope=P.rope_table(D), positions=positions, q=q, q_out=rows[:, H - 1:2 * H - 1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", [P.ROPE_INTERLEAVED, P.ROPE_HALF])
+@pytest.mark.parametrize("heads, rot, pad", [(5, 64, 0), (5, 64, 1), (24, 32, 8), (1, 34, 0)])
+def test_rope_tiles_of_either_size(dtype, layout, heads, rot, pad):
+    """Around the number of pieces (of 16 bytes; of a pair where the rows are not aligned) from which a tile is larger: the
+    same bits as the same tokens' in small calls."""
+    g = torch.Generator(device="cuda").manual_seed(heads)
+    vec = (rot if layout == P.ROPE_INTERLEAVED else rot // 2) % (16 // dtype.itemsize) == 0 and pad != 1
+    pieces = rot * dtype.itemsize // (16 if layout == P.ROPE_INTERLEAVED else 32) if vec else rot // 2
+    most = -(-(1 << 17) // (heads * pieces))
+    table = P.rope_table(rot)
+    x = torch.randn((most + 3, heads, pad + rot), generator=g, device="cuda").to(dtype)[..., pad:]
+    positions = torch.randint(0, 1 << 20, (most + 3,), generator=g, device="cuda", dtype=torch.int32)
+    want = torch.cat([P.rope(x[i:i + 97], table, positions[i:i + 97], layout=layout,
+                             out=torch.empty_like(x[i:i + 97], memory_format=torch.contiguous_format))
+                      for i in range(0, most + 3, 97)])
+    for n in (most - 1, most, most + 3):
+        out = torch.full((n, heads, rot), 7.0, dtype=dtype, device="cuda")
+        P.rope(x[:n], table, positions[:n], layout=layout, out=out)
+        assert torch.equal(out, want[:n])
