@@ -11,8 +11,10 @@
 // goes to the workspace in fp32 and kv_combine_kernel merges a row's parts by log-sum-exp.  Two
 // persistent CTAs per SM take equal shares of the items, and one item's K and V stream in while the one
 // before it is merged and written.  8 x 128K tokens of a bf16 pool (4 KV heads of 128, 8 query heads each):
-// 316 us, the copy bandwidth; 23 ragged rows of up to 9,001 tokens (3 heads of 64, 16-token pages): 20 us
-// against 12 us of bytes, the rest start-up, the first tiles' latency and the merge.
+// 317 us, the copy bandwidth; 24 x 8K 67 us against 60; 23 ragged rows of up to 9,001 tokens (3 heads of 64, 16-token
+// pages): 20 us against 12 us of bytes, the rest start-up, the first tiles' latency and the merge.  FP8 of head_dim 64 (4
+// KV heads, 16 query heads each): 32 x 16K-64K 112 us against 102, but 24 x 8K 34 us against 15 and 4 x 4 rows of 64K 78
+// us against 20, where the codes' conversions to fp16 take the issue slots.
 //
 // In a CTA a producer warp streams tiles of K and V by TMA into a ring of stages, a query warp brings
 // each item's queries as MMA fragments, and four consumer warps share out the columns (16 each) and

@@ -15,13 +15,18 @@ namespace kv {
 
 // Parts of a context: of 2^kPartMin tokens, doubled until at most 2^parts_shift cover it.  All KV heads of one
 // request make 128 parts, but at least 16 of a head: fewer leave SMs idle under one request, and every part costs
-// its queries, its first base and its output beside its tiles.  Measured (4 KV heads of 128):
+// its queries, its first base and its output beside its tiles.  128 is nowhere more than 1.2 times the best; 64 is
+// up to 1.7 times it for one request, 256 costs the long batches.  Measured (4 KV heads of 128, calls in a row on the
+// same inputs; their bytes in brackets):
 //                                        64 parts   128 parts   256 parts
-//   bf16, 1 x 128K (40 us of bytes)        64.5        43.2        43.4 us
-//   bf16, 4 x 32K                          42.4        45.8        48.6
-//   FP8, 1 x 128K (20 us)                  59.9        34.2        27.6
-//   FP8, 24 x 8K (30 us)                   43.5        49.0        48.9
-//   FP8, 32 x 16K-64K (203 us)                         222         232
+//   bf16, 1 x 128K (40 us)                 64.7        42.4        42.5 us
+//   bf16, 4 x 32K (40)                     41.8        44.1        46.7
+//   bf16, 24 x 8K (60)                     67.1        67.4        67.3
+//   FP8, 1 x 128K (20)                     54.5        32.2        26.9
+//   FP8, 24 x 8K (30)                      41.9        49.4        49.4
+//   FP8, 32 x 16K-64K (203)               212         212         221
+//   FP8, 4 x 4 rows of 60K-64K (38)        82.2        92.8       100
+//   bf16, 23 ragged rows, 3 x 64           16.3        15.8        15.8
 //   parts of at least                     128 tokens  256         512
 //   bf16, one row of 4K                     9.4         9.5        11.0 us
 //   FP8, 24 x 2K (7.6 us)                  24.6        19.8        20.0

@@ -35,7 +35,7 @@
 // columns 172 us, sums of weights in registers, which then spill, 106 us.)  P's third term costs 3 to 4 us of the 92;
 // all three one after the other into one accumulator, with a second score buffer in the place of the other, 102 us.
 //
-// Precision: e4m3 x e4m3 products are exact and accumulate in fp32.  q is scaled by a power of two per
+// Precision: products of two 8-bit numbers are exact and accumulate in fp32.  q is scaled by a power of two per
 // column and written as hi + lo (exact but for elements 2^-9 below the column's largest, which are within 2^-17 of
 // it).  A weight is rounded to fp16 (2^-11 of itself at worst, against the output's own 2^-8), whose 11 bits three
 // e5m2 terms of 3 hold exactly; e5m2's smallest step is 2^-16 and the largest weight at least 2^13, so weights keep
@@ -407,9 +407,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     ++issued;
                 }
             }
-            // With many items only now: the merge's CTAs beside this one's start took it 2,000 cycles and more (23 ragged
-            // rows of head_dim 64: 20.8 us against 19.8).  With few it is better early (four rows of 256 tokens: 7.3 us
-            // against 8.4).
+            // (with many items only now, as in kv_attention_kernel; 4 x 8K: 14.6 us early, 12.9 so)
             if (!direct) pdl_launch_dependents();
             if (*abort && lane == 0) {  // leave no copy in flight behind: the last tiles issued in either ring
                 for (int v = 0; v < 2; ++v) {

@@ -16,8 +16,10 @@
 // the angles' place changes with the token alone.  What it takes is bytes in flight: a thread's next pieces come by
 // asynchronous copies into 128 bytes of its own in shared memory (with four 16-byte loads in registers instead, the
 // prefills below took 43 and 64.5 us; a ring of 96 bytes 35.2 and 56.5 us).
-// 8,192 tokens x 98 heads x 64 dims: 35.8 us (5.7 TB/s); 8,192 tokens into an FP8 pool of 4 KV heads of 128 with
-// 64 query heads rotated: 48.0 us (6.1 TB/s).
+// 8,192 tokens x 98 heads x 64 dims: 35.8 us (5.7 TB/s; in fp32, 96 heads, 60.9 us, 6.6 TB/s); 8,192 tokens into an
+// FP8 pool of 4 KV heads of 128 with 64 query heads rotated: 48.0 us (6.1 TB/s; bf16 pool 48.6 us, 6.2 TB/s).  Rows that
+// 16-byte accesses do not fit go element by element: the same rope from an odd element on 158 us, the same insert with
+// 90 rotary dims 246 us; a decode step's few tokens take as long as aligned ones (8 tokens: 1.7 and 1.9 us).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
