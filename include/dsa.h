@@ -549,11 +549,12 @@ typedef struct dsa_kv_rows {
  * Write new tokens into the K/V pool: for each i with slots[i] >= 0, K and V at that slot, as
  *   DSA_KV_BF16: the values (rotated K rounded once from fp32)
  *   DSA_KV_FP8:  e4m3(x / scale), IEEE fp32 division, round to nearest even, saturating to +-448
- * rope != NULL rotates K's dims [rot_offset, rot_offset + rot_dim) on the way, in fp32, and with
- * q != NULL also rotates q (bf16, [num_tokens, q->num_heads, rot_dim]) as dsa_rope does, in the same
- * launch; q needs rope, and its output overlaps neither k, v nor the pool.  slots: device [num_tokens], distinct (a slot listed twice holds bytes of
- * either token, in any mixture).  A slot outside the pool, or a slot >= 0 of a token at a negative
- * position, is DSA_ERR_BOUNDS and not written; every other byte of the pool keeps its value.
+ * rope != NULL rotates K's dims [rot_offset, rot_offset + rot_dim) on the way, in fp32, and with q
+ * != NULL also rotates q (bf16, [num_tokens, q->num_heads, rot_dim]) as dsa_rope does, in the same
+ * launch; q needs rope, and its output overlaps neither k, v nor the pool.  slots: device
+ * [num_tokens], distinct (a slot listed twice holds bytes of either token, in any mixture).  A
+ * slot outside the pool, or a slot >= 0 of a token at a negative position, is DSA_ERR_BOUNDS and
+ * not written; every other byte of the pool keeps its value.
  */
 int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_tokens, const dsa_kv_rows *kv,
                   const dsa_rope_spec *rope, const dsa_rope_tensor *q, int32_t *dev_status, void *stream);
@@ -566,25 +567,26 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
  * q: bf16 [num_rows, num_heads, head_dim], rows q_stride elements apart (a multiple of 8), 16-byte
  * aligned; num_heads a multiple of kv_heads, at most DSA_KV_MAX_HPG times it; out: bf16 [num_rows,
  * num_heads, head_dim], 16-byte aligned; lse: fp32 [num_rows, num_heads] or NULL.  A head with no
- * visible token, or whose visible scores are all -inf, gets out = 0 and lse = -inf.  An infinity of
- * V (bf16 pool) that it sees makes its dim infinite, or NaN beside one of the other sign or where its
- * weight is 0 in fp32.  What slots at
- * or past row_ctx[r] hold never reaches row r (NaN included).  rows->rows_per_group (1, 2, 4 or 8)
- * consecutive rows of one request (speculative verify) share each read of the cache.
+ * visible token, or whose visible scores are all -inf, gets out = 0 and lse = -inf.  An infinity
+ * of V (bf16 pool) that it sees makes its dim infinite, or NaN beside one of the other sign or
+ * where its weight is 0 in fp32.  What slots at or past row_ctx[r] hold never reaches row r (NaN
+ * included).  rows->rows_per_group (1, 2, 4 or 8) consecutive rows of one request (speculative
+ * verify) share each read of the cache.
  *
  * Each row's tokens are split into parts by its own context (the group's largest), merged by
- * log-sum-exp, and a row's bits depend on nothing outside its group (batch invariance): the workspace
- * (device, 256-byte aligned, dsa_kv_attention_workspace_size bytes, no initial contents; NULL when
- * that is 0) holds the parts in fp32 and serves one call at a time: calls that may run at once,
- * captured graphs among them, have one each.  Outputs overlap no input (out or lse over q, or over one
- * another: DSA_ERR_INVALID_ARG).  Scores and sums are fp32.
- * The softmax weights multiply V as the sum of two bf16 terms (bf16 pool) or rounded to fp16 (FP8
- * pool), where they keep steps of 2^-29 of the largest of their part (head_dim 64: 2^-31) or better.
- * Over an FP8 pool q is scaled by a power of two per head and rounded to fp16 (head_dim 64) or to the
- * sum of two e4m3 terms (128: exact down to 2^-9 of the head's largest element, smaller ones within
- * 2^-17 of that largest); a head of head_dim 128 with an infinity or a NaN in q gets NaN.  A row_ctx outside [0, max_ctx], a row_req outside the block table or rows of a
- * group with different requests are DSA_ERR_BOUNDS, and their group gets out = 0 and lse = -inf; a
- * page id outside the pool is DSA_ERR_BOUNDS, and page 0 is read in its place.
+ * log-sum-exp, and a row's bits depend on nothing outside its group (batch invariance): the
+ * workspace (device, 256-byte aligned, dsa_kv_attention_workspace_size bytes, no initial contents;
+ * NULL when that is 0) holds the parts in fp32 and serves one call at a time: calls that may run
+ * at once, captured graphs among them, have one each.  Outputs overlap no input (out or lse over
+ * q, or over one another: DSA_ERR_INVALID_ARG).  Scores and sums are fp32.  The softmax weights
+ * multiply V as the sum of two bf16 terms (bf16 pool) or rounded to fp16 (FP8 pool), where they
+ * keep steps of 2^-29 of the largest of their part (head_dim 64: 2^-31) or better.  Over an FP8
+ * pool q is scaled by a power of two per head and rounded to fp16 (head_dim 64) or to the sum of
+ * two e4m3 terms (128: exact down to 2^-9 of the head's largest element, smaller ones within 2^-17
+ * of that largest); a head of head_dim 128 with an infinity or a NaN in q gets NaN.  A row_ctx
+ * outside [0, max_ctx], a row_req outside the block table or rows of a group with different
+ * requests are DSA_ERR_BOUNDS, and their group gets out = 0 and lse = -inf; a page id outside the
+ * pool is DSA_ERR_BOUNDS, and page 0 is read in its place.
  */
 int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint16_t *q, int64_t q_stride,
                      int32_t num_heads, float sm_scale, uint16_t *out, float *lse, void *workspace,

@@ -297,3 +297,38 @@ def test_rope_tiles_of_either_size(dtype, layout, heads, rot, pad):
         out = torch.full((n, heads, rot), 7.0, dtype=dtype, device="cuda")
         P.rope(x[:n], table, positions[:n], layout=layout, out=out)
         assert torch.equal(out, want[:n])
+
+
+# ------------------------------------------------------------------ values past a row's context, in many tiles
+
+@pytest.mark.parametrize("fmt, dim", [("fp8", 128), ("fp8", 64), ("bf16", 128)])
+@pytest.mark.parametrize("kv_heads, hpg, group, row_ctx", [
+    (2, 5, 2, [700, 3000, 128, 129]),                # 10 columns
+    (2, 7, 4, [64, 700, 1300, 700, 0, 5, 2000, 257]),  # 28
+    (1, 16, 4, [9000, 300, 8999, 4100]),             # 64
+    (1, 20, 8, [1, 255, 256, 257, 511, 900, 1400, 40]),  # two blocks of columns and a rest
+    (4, 8, 8, [20000, 19999, 19871, 19872, 19873, 5000, 19744, 64])])
+def test_nan_values_in_tiles_that_some_rows_see(fmt, dim, kv_heads, hpg, group, row_ctx):
+    """NaN in V behind each row's context, in tiles where the others' sums go on: rows keep their bits, and each sees its
+    own NaN alone."""
+    ctx = [max(row_ctx[i:i + group]) for i in range(0, len(row_ctx), group)]
+    make = lambda: Case(68, fmt, ctx, kv_heads, hpg, dim, 32, group=group, row_ctx=row_ctx)  # noqa: E731
+    want = make().run()
+    nan = {"fp8": 0x7F, "bf16": 0x7FFF}[fmt]
+    for at in sorted(set(row_ctx)):
+        c = make()
+        struck = [r for r, n in enumerate(row_ctx) if n > at]  # token `at` is the first that a row of context `at` misses
+        if not struck:
+            continue
+        for req, longest in enumerate(ctx):
+            for t in range(at, longest, 97):  # and many behind it
+                bits(c.pool)[c.table[req, t // 32].item(), :, 1, t % 32, 3] = nan
+        out, lse = c.run()
+        assert torch.equal(lse, want[1])
+        for r in range(len(row_ctx)):
+            if r in struck:
+                assert out[r, :, 3].isnan().all()
+                rest = [d for d in range(dim) if d != 3]
+                assert torch.equal(out[r][:, rest], want[0][r][:, rest])
+            else:
+                assert torch.equal(out[r], want[0][r])
