@@ -257,13 +257,14 @@ def test_outputs_beside_their_inputs_in_one_buffer():
     """A step whose queries, keys, values, rotated queries and answers are parts of one buffer."""
     c = Case(67, "bf16", [300, 90], 2, 4, 64, 16)
     R, H, D = 2, 8, 64
-    buffer = torch.zeros(R * 3 * H * D + R * H * D, dtype=torch.bfloat16, device="cuda")
-    rows = buffer[:R * 3 * H * D].view(R, 3 * H, D)
-    q, k, v, turned = rows[:, :H], rows[:, H:H + 2], rows[:, H + 2:H + 4], rows[:, 2 * H:]
+    wide = R * (3 * H + 2) * D
+    buffer = torch.zeros(wide + R * H * D, dtype=torch.bfloat16, device="cuda")
+    rows = buffer[:wide].view(R, 3 * H + 2, D)
+    q, k, v, turned = rows[:, :H], rows[:, H:H + 2], rows[:, H + 2:H + 4], rows[:, 2 * H:3 * H]
     q.copy_(c.q)
     k.copy_(c.q[:, :2])
     v.copy_(c.q[:, 2:4])
-    out = buffer[R * 3 * H * D:].view(R, H, D)
+    out = buffer[wide:].view(R, H, D)
     slots = torch.tensor([c.table[r, (n - 1) // 16].item() * 16 + (n - 1) % 16 for r, n in enumerate(c.rows)],
                          dtype=torch.int32, device="cuda")
     positions = (c.row_ctx - 1).contiguous()
