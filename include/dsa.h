@@ -535,6 +535,36 @@ typedef struct dsa_rope_tensor {
 int dsa_rope(const dsa_rope_spec *rope, const dsa_rope_tensor *tensors, int32_t num_tensors, int32_t dtype,
              int32_t num_tokens, void *stream);
 
+/*
+ * Positions of several axes (time, height and width of images and video, say): each pair of the
+ * rotary part turns with one of them, and a text token has the same position on all.
+ */
+#define DSA_ROPE_MAX_AXES 4
+#define DSA_ROPE_AXES_SPLIT 0 /* the first sections[0] pairs are axis 0's, the next sections[1] axis 1's, ... */
+#define DSA_ROPE_AXES_CYCLE 1 /* the axes in turn, pair by pair, each while it has pairs left */
+
+/*
+ * Host-only helper: the axis of each pair from the pairs that each axis has (sections: host,
+ * num_axes counts >= 0 of together num_pairs) into axis (host, num_pairs bytes).
+ */
+int dsa_rope_sections(const int32_t *sections, int32_t num_axes, int32_t order, int32_t num_pairs, uint8_t *axis);
+
+/* A call's angles, with several positions a token. */
+typedef struct dsa_rope_axes {
+    const uint64_t *turns;    /* device [rot_dim / 2], from dsa_rope_turns */
+    const int32_t *positions; /* device [num_axes, num_tokens], axes axis_stride elements apart; a token
+                                 with a negative position on any axis is left out */
+    int64_t axis_stride;      /* >= 0; 0: one position for all axes */
+    const uint8_t *axis;      /* host [rot_dim / 2]: the axis of each pair, below num_axes */
+    int32_t num_axes;         /* 1 .. DSA_ROPE_MAX_AXES */
+    int32_t rot_dim;          /* even, 2 .. DSA_ROPE_MAX_DIM */
+    float scale;              /* factor on the rotated values (finite) */
+} dsa_rope_axes;
+
+/* dsa_rope with pair i of token n turned by positions[axis[i]][n] * inv_freq_i; everything else as there. */
+int dsa_rope_with_axes(const dsa_rope_axes *rope, const dsa_rope_tensor *tensors, int32_t num_tensors, int32_t dtype,
+                       int32_t num_tokens, void *stream);
+
 /* New tokens' keys and values: [num_tokens, kv_heads, head_dim] bf16 with heads packed, tokens
  * k_stride / v_stride elements apart (parts of a packed projection output). */
 typedef struct dsa_kv_rows {
@@ -558,6 +588,11 @@ typedef struct dsa_kv_rows {
  */
 int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_tokens, const dsa_kv_rows *kv,
                   const dsa_rope_spec *rope, const dsa_rope_tensor *q, int32_t *dev_status, void *stream);
+
+/* dsa_kv_insert with positions of several axes: K and q are rotated as dsa_rope_with_axes
+ * does, and a slot >= 0 of a token with a negative position on any axis is DSA_ERR_BOUNDS. */
+int dsa_kv_insert_with_axes(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_tokens, const dsa_kv_rows *kv,
+                            const dsa_rope_axes *rope, const dsa_rope_tensor *q, int32_t *dev_status, void *stream);
 
 /*
  * Dense attention of new tokens over the paged cache: head h of row r reads KV head
@@ -596,6 +631,94 @@ int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint
  * max_ctx; 0 when every row is one part. */
 size_t dsa_kv_attention_workspace_size(const dsa_kv_cache *cache, int32_t num_rows, int32_t num_heads,
                                        int32_t max_ctx);
+
+/*
+ * dsa_kv_attention of a batch whose rows share a prefix: rows first_row[s] .. first_row[s + 1] - 1 make
+ * segment s, and the first shared_ctx[s] tokens of their requests are the same (their block tables list
+ * the same pages there, or pages that hold the same).  Outputs are those of dsa_kv_attention, but the
+ * shared tokens are read once for all rows of a segment, by its first row's block table: as many of
+ * them as every row of the segment that sees any token sees, in whole tiles of 128 (and none for a segment
+ * of one row group, which shares its reads already); each row reads the rest by its own table.
+ *
+ * Rows before first_row[0] and from first_row[num_segments] on are in no segment.  first_row ascends (an
+ * empty segment is allowed), from 0 at least to num_rows at most, at whole row groups; a segment that does not,
+ * or with a negative shared_ctx, is DSA_ERR_BOUNDS, and its rows are as if in none.
+ */
+typedef struct dsa_kv_segments {
+    const int32_t *first_row;  /* device [num_segments + 1] (dsa_kv_step.segment_rows) */
+    const int32_t *shared_ctx; /* device [num_segments] */
+    int32_t num_segments;      /* 0: plain dsa_kv_attention */
+} dsa_kv_segments;
+
+/*
+ * Everything not said above is as in dsa_kv_attention.  A row's bits depend on its segment and nothing else.
+ * workspace: dsa_kv_attention_shared_workspace_size bytes, otherwise as there.  Over the shared tokens of a
+ * bf16 pool the softmax weights are rounded to bf16, of an FP8 pool to fp16 (in steps of 2^-31 of their
+ * part's largest).
+ */
+int dsa_kv_attention_shared(const dsa_kv_cache *cache, const dsa_rows *rows, const dsa_kv_segments *segments,
+                            const uint16_t *q, int64_t q_stride, int32_t num_heads, float sm_scale, uint16_t *out,
+                            float *lse, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Workspace bytes of dsa_kv_attention_shared for num_rows rows in num_segments segments. */
+size_t dsa_kv_attention_shared_workspace_size(const dsa_kv_cache *cache, int32_t num_rows, int32_t num_heads,
+                                              int32_t max_ctx, int32_t num_segments);
+
+/*
+ * ---- A step's rows, slots and pages from the lengths of its requests (dsa_kv_plan): the row_req,
+ * row_ctx, positions, slots and block table that the calls above take, made on the device, so that
+ * a serving loop (or a captured graph of one) needs no host between its steps.
+ *
+ * Request i has context[i] tokens in the cache, listed by its row of the block table, and gets
+ * new_tokens[i] >= 0 more; -1: it has ended, and its pages from first_own[i] on (those before belong
+ * to a prefix that others use too) go back to the free ones.  Free pages are a stack, free_count[0]
+ * entries of free_pages, the last one taken first: what ended requests give back is put on it, in
+ * the order of requests and pages, then the others' new pages are taken, in that order too.  With
+ *   need_i = ceil((context_i + new_i) / page_size) - ceil(context_i / page_size)
+ *   wide_i = new_i raised to a multiple of rows_per_group
+ * request i gets its tokens if the pages needed by requests 0 .. i are at hand and their rows fit
+ * max_rows (one that needs none of the one is not held up by the other); else it gets none of them
+ * and no page.
+ * Rows: request after request, wide_i each (also where it gets nothing).  Row j < granted_i: row_req =
+ * i, positions = context_i + j, row_ctx one more, slots = the position's slot.  Every other row, up to
+ * max_rows, is padding: positions and slots -1, row_ctx 0, row_req i (behind the last request's: 0).
+ * Bit for bit reproducible.  Lengths that cannot be (context < 0 or longer than a row of the table lists,
+ * together with the new tokens too, new_tokens < -1, first_own < 0) are DSA_ERR_BOUNDS, and their
+ * request is as one without new tokens; a page id outside the pool in a row's place is, with slot -1;
+ * so are a free_count outside [0, free_capacity] (taken as the nearer one), pages given back beyond
+ * free_capacity (which are lost), and, unless `granted` is there to tell, a request that gets nothing.
+ */
+#define DSA_KV_PLAN_MAX_REQUESTS 16384
+
+typedef struct dsa_kv_step {
+    int32_t num_requests;          /* 0 .. DSA_KV_PLAN_MAX_REQUESTS */
+    int32_t page_size;             /* 16, 32, 64 or 128 */
+    int64_t num_pages;             /* of the pool; num_pages * page_size < 2^31 */
+    const int32_t *context;        /* device [num_requests] */
+    const int32_t *new_tokens;     /* device [num_requests] */
+    const int32_t *first_own;      /* device [num_requests], or NULL: 0 */
+    int32_t *block_table;          /* device [num_requests, bt_stride]; entries of new pages are written */
+    int64_t bt_stride;
+    int32_t *free_pages;           /* device [free_capacity]; entries given back are written */
+    const int32_t *free_count;     /* device [1] */
+    int32_t free_capacity;
+    int32_t num_segments;          /* 0: none */
+    const int32_t *segment_requests; /* device [num_segments + 1] requests, 0 .. num_requests */
+    int32_t max_rows;              /* a multiple of rows_per_group */
+    int32_t rows_per_group;        /* 1, 2, 4 or 8 */
+    int32_t *row_req;              /* device [max_rows] */
+    int32_t *row_ctx;              /* device [max_rows] */
+    int32_t *positions;            /* device [max_rows], or NULL */
+    int32_t *slots;                /* device [max_rows], or NULL */
+    int32_t *row_start;            /* device [num_requests + 1] first row of each request and the end, or NULL */
+    int32_t *granted;              /* device [num_requests] tokens that it gets, or NULL */
+    int32_t *context_out;          /* device [num_requests] context + granted (0 if ended); may be context, or NULL */
+    int32_t *free_count_out;       /* device [1]; may be free_count, or NULL */
+    int32_t *segment_rows;         /* device [num_segments + 1] first row of each segment_requests' request */
+} dsa_kv_step;
+
+/* Outputs overlap nothing else (DSA_ERR_INVALID_ARG), except where a comment above says so. */
+int dsa_kv_plan(const dsa_kv_step *step, int32_t *dev_status, void *stream);
 
 /*
  * Failure-path self-test (no counterpart on the pages): one CTA whose

@@ -59,10 +59,32 @@ class _RopeSpec(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class _RopeAxes(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("axis_stride", ctypes.c_int64),
+                ("axis", ctypes.c_void_p), ("num_axes", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
 class _RopeTensor(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("num_heads", ctypes.c_int32),
                 ("layout", ctypes.c_int32), ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
                 ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
+
+
+class _KvSegments(ctypes.Structure):
+    _fields_ = [("first_row", ctypes.c_void_p), ("shared_ctx", ctypes.c_void_p), ("num_segments", ctypes.c_int32)]
+
+
+class _KvStep(ctypes.Structure):
+    _fields_ = [("num_requests", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+                ("context", ctypes.c_void_p), ("new_tokens", ctypes.c_void_p), ("first_own", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("bt_stride", ctypes.c_int64), ("free_pages", ctypes.c_void_p),
+                ("free_count", ctypes.c_void_p), ("free_capacity", ctypes.c_int32), ("num_segments", ctypes.c_int32),
+                ("segment_requests", ctypes.c_void_p), ("max_rows", ctypes.c_int32),
+                ("rows_per_group", ctypes.c_int32), ("row_req", ctypes.c_void_p), ("row_ctx", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("row_start", ctypes.c_void_p),
+                ("granted", ctypes.c_void_p), ("context_out", ctypes.c_void_p), ("free_count_out", ctypes.c_void_p),
+                ("segment_rows", ctypes.c_void_p)]
 
 
 class _KvRows(ctypes.Structure):
@@ -144,9 +166,23 @@ def load_library(path: str | None = None):
     lib.dsa_kv_insert.restype = ctypes.c_int
     lib.dsa_kv_insert.argtypes = [ctypes.POINTER(_KvCache), P, I32, ctypes.POINTER(_KvRows),
                                   ctypes.POINTER(_RopeSpec), ctypes.POINTER(_RopeTensor), P, P]
+    lib.dsa_kv_plan.restype = ctypes.c_int
+    lib.dsa_kv_plan.argtypes = [ctypes.POINTER(_KvStep), P, P]
+    lib.dsa_rope_sections.restype = ctypes.c_int
+    lib.dsa_rope_sections.argtypes = [P, I32, I32, I32, P]
+    lib.dsa_rope_with_axes.restype = ctypes.c_int
+    lib.dsa_rope_with_axes.argtypes = [ctypes.POINTER(_RopeAxes), ctypes.POINTER(_RopeTensor), I32, I32, I32, P]
+    lib.dsa_kv_insert_with_axes.restype = ctypes.c_int
+    lib.dsa_kv_insert_with_axes.argtypes = [ctypes.POINTER(_KvCache), P, I32, ctypes.POINTER(_KvRows),
+                                            ctypes.POINTER(_RopeAxes), ctypes.POINTER(_RopeTensor), P, P]
     lib.dsa_kv_attention.restype = ctypes.c_int
     lib.dsa_kv_attention.argtypes = [ctypes.POINTER(_KvCache), ctypes.POINTER(_Rows), P, I64, I32, F, P, P, P,
                                      ctypes.c_size_t, P, P]
+    lib.dsa_kv_attention_shared.restype = ctypes.c_int
+    lib.dsa_kv_attention_shared.argtypes = [ctypes.POINTER(_KvCache), ctypes.POINTER(_Rows),
+                                            ctypes.POINTER(_KvSegments), P, I64, I32, F, P, P, P, ctypes.c_size_t, P, P]
+    lib.dsa_kv_attention_shared_workspace_size.restype = ctypes.c_size_t
+    lib.dsa_kv_attention_shared_workspace_size.argtypes = [ctypes.POINTER(_KvCache), I32, I32, I32, I32]
     lib.dsa_kv_attention_workspace_size.restype = ctypes.c_size_t
     lib.dsa_kv_attention_workspace_size.argtypes = [ctypes.POINTER(_KvCache), I32, I32, I32]
     if path is None:
@@ -161,7 +197,9 @@ EXPORTED = ("dsa_version", "dsa_status_string", "dsa_indexer_logits", "dsa_topk"
             "dsa_sparse_mla_decode_prepare", "dsa_sparse_mla_decode_prepared", "dsa_msa_block_scores",
             "dsa_msa_select", "dsa_msa_attention", "dsa_msa_attention_workspace_size", "dsa_topk_slots_warm",
             "dsa_selftest_wait_timeout", "dsa_rope_frequencies", "dsa_rope_turns", "dsa_rope", "dsa_kv_insert",
-            "dsa_kv_attention", "dsa_kv_attention_workspace_size")
+            "dsa_kv_attention", "dsa_kv_attention_workspace_size", "dsa_rope_sections", "dsa_rope_with_axes",
+            "dsa_kv_insert_with_axes", "dsa_kv_plan", "dsa_kv_attention_shared",
+            "dsa_kv_attention_shared_workspace_size")
 HIST_BINS = 65536
 NOALLOC_MAX_ROWS = 8
 
@@ -476,7 +514,9 @@ KV_BF16, KV_FP8 = 5, 6
 DTYPE_BF16, DTYPE_FP32 = 1, 2
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROPE_AXES_ORDERS = {"split": 0, "cycle": 1}
 ROPE_MAX_TENSORS = 4
+KV_PLAN_MAX_REQUESTS = 16384
 
 
 def _host_ptr(t):
@@ -525,8 +565,11 @@ _I32, _F32, _BF16 = (_int32,), (_float32,), (_bfloat16,)
 # The calls of a decode step are short, so their arguments are packed into bytes (in the C structs' layouts) for
 # function objects of their own that take those, which costs a fraction of ctypes structures.
 _PACK_ROPE_SPEC = struct.Struct("PPif").pack
+_PACK_ROPE_AXES = struct.Struct("PPqPiif").pack
 _PACK_ROPE_TENSORS = [None] + [struct.Struct("PPiiqqqq" * n).pack for n in range(1, 5)]
 _PACK_KV_ROWS = struct.Struct("PPqqii").pack
+_PACK_SEGMENTS = struct.Struct("PPi").pack
+_PACK_STEP = struct.Struct("iiqPPPPqPPiiPiiPPPPPPPPP").pack
 _PACK_ROWS = struct.Struct("PqiPPiii0q").pack
 _packed = {}
 
@@ -538,8 +581,11 @@ def _packed_function(name):
         P, I32, I64, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
         fn = load_library()[name]
         fn.restype = ctypes.c_int
-        fn.argtypes = {"dsa_rope": [P, P, I32, I32, I32, P], "dsa_kv_insert": [P, P, I32, P, P, P, P, P],
-                       "dsa_kv_attention": [P, P, P, I64, I32, F, P, P, P, ctypes.c_size_t, P, P]}[name]
+        rope, insert = [P, P, I32, I32, I32, P], [P, P, I32, P, P, P, P, P]
+        fn.argtypes = {"dsa_rope": rope, "dsa_rope_with_axes": rope, "dsa_kv_insert": insert,
+                       "dsa_kv_insert_with_axes": insert, "dsa_kv_plan": [P, P, P],
+                       "dsa_kv_attention": [P, P, P, I64, I32, F, P, P, P, ctypes.c_size_t, P, P],
+                       "dsa_kv_attention_shared": [P, P, P, P, I64, I32, F, P, P, P, ctypes.c_size_t, P, P]}[name]
         _packed[name] = fn
     return fn
 
@@ -564,27 +610,70 @@ def rope_turns(inv_freq):
     return turns
 
 
-class RopeTable:
-    """The angles of `rope` and `kv_insert` on the device: `turns` int64 [rot_dim / 2], and `scale`."""
+def rope_sections(sections, order="split"):
+    """dsa_rope_sections: the axis of each pair, uint8 host [pairs], from how many pairs each axis has: one axis's
+    after the other's ("split"), or the axes in turn while they have pairs left ("cycle")."""
+    if order not in ROPE_AXES_ORDERS:
+        raise DsaError(f"unknown order of axes {order!r}: one of {', '.join(ROPE_AXES_ORDERS)}")
+    counts = torch.tensor([int(n) for n in sections], dtype=torch.int32)
+    pairs = int(counts.sum())
+    axis = torch.empty(max(pairs, 1), dtype=torch.uint8)
+    rc = load_library().dsa_rope_sections(_host_ptr(counts), counts.numel(), ROPE_AXES_ORDERS[order], pairs,
+                                          _host_ptr(axis))
+    _check(rc, "dsa_rope_sections")
+    return axis
 
-    def __init__(self, turns, scale=1.0):
+
+class RopeTable:
+    """The angles of `rope` and `kv_insert` on the device: `turns` int64 [rot_dim / 2], and `scale`.  With `axis`
+    (uint8 host [rot_dim / 2], rope_sections) a token has a position on each of num_axes axes, and pair i turns by
+    the one on axis[i]."""
+
+    def __init__(self, turns, scale=1.0, axis=None, num_axes=None):
         if turns.dtype != torch.int64 or not turns.is_cuda or not turns.is_contiguous() or turns.dim() != 1:
             raise DsaError("RopeTable takes a contiguous int64 device vector (rope_turns)")
         self.turns, self.scale, self.rot_dim = turns, float(scale), 2 * turns.shape[0]
         self.device, self.address = turns.get_device(), turns.data_ptr()
+        self.num_axes, self.axis = 0, None  # 0: one position a token
+        if axis is not None:
+            if axis.dtype != torch.uint8 or axis.shape != turns.shape or axis.is_cuda or not axis.is_contiguous():
+                raise DsaError(f"the pairs' axes are a contiguous uint8 host vector of {turns.shape[0]}")
+            self.axis = axis.clone()
+            self.axis_address = self.axis.data_ptr()
+            self.num_axes = int(axis.max()) + 1 if num_axes is None else int(num_axes)
 
 
-def rope_table(rot_dim, theta=10000.0, scaling="none", factor=1.0, trained_ctx=0, device="cuda"):
-    """The table of dsa_rope_frequencies' angles (for other angles: RopeTable(rope_turns(f).to(device), scale))."""
+def rope_table(rot_dim, theta=10000.0, scaling="none", factor=1.0, trained_ctx=0, device="cuda", sections=None,
+               order="split", restart=False):
+    """The table of dsa_rope_frequencies' angles (for other angles: RopeTable(rope_turns(f).to(device), scale)).
+    `sections`, as many pairs for each axis of positions, in `order` (rope_sections); with `restart` each axis's
+    pairs have the frequencies of a rotary part of their own instead of their places' in the whole."""
     freq, scale = rope_frequencies(rot_dim, theta, scaling, factor, trained_ctx)
-    return RopeTable(rope_turns(freq).to(device), scale)
+    if sections is None:
+        return RopeTable(rope_turns(freq).to(device), scale)
+    axis = rope_sections(sections, order)
+    if 2 * axis.numel() != rot_dim:
+        raise DsaError(f"the sections make up {axis.numel()} pairs: expected {rot_dim // 2}")
+    if restart:
+        for a, n in enumerate(sections):
+            if n > 0:
+                freq[axis == a] = rope_frequencies(2 * n, theta, scaling, factor, trained_ctx)[0]
+    return RopeTable(rope_turns(freq).to(device), scale, axis, len(sections))
 
 
 def _rope_spec(table, positions, device, num_tokens):
     if table.device != device:
         raise DsaError(f"the rotary table is on device {table.device}, the call's other tensors on device {device}")
-    if positions.dtype is not _int32 or positions.shape != (num_tokens,) or positions.get_device() != device:
-        _expect(positions, "positions", device, _I32, (num_tokens,))
+    axes = table.num_axes
+    shape = (axes, num_tokens) if axes else (num_tokens,)
+    if positions.dtype is not _int32 or positions.shape != shape or positions.get_device() != device:
+        _expect(positions, "positions", device, _I32, shape)
+    if axes:
+        stride, one = positions.stride()
+        if (one != 1 and num_tokens > 1) or stride < 0:
+            raise DsaError("the positions on an axis are contiguous")
+        return _PACK_ROPE_AXES(table.address, positions.data_ptr(), stride, table.axis_address, axes, table.rot_dim,
+                               table.scale)
     if not positions.is_contiguous():
         raise DsaError("positions is not contiguous")
     return _PACK_ROPE_SPEC(table.address, positions.data_ptr(), table.rot_dim, table.scale)
@@ -615,7 +704,8 @@ def _rope_tensor(x, out, layout, rot_dim, device, dtype, num_tokens):
 
 def rope(x, table, positions, layout=ROPE_INTERLEAVED, out=None, stream=None):
     """dsa_rope: rotate x [tokens, heads, rot_dim] (bf16 or fp32; usually a slice x[..., a:a + rot_dim]) by
-    its tokens' positions, into `out` (default: in place).  x, layout and out may be lists of up to 4
+    its tokens' positions [tokens] (int32; a table with axes: [axes, tokens], dsa_rope_with_axes), into `out`
+    (default: in place).  x, layout and out may be lists of up to 4
     tensors of the same tokens, rotated by one launch.  Tokens at negative positions are left alone."""
     if type(x) is list or type(x) is tuple:
         many, count, first = True, len(x), x[0] if x else None
@@ -639,9 +729,13 @@ def rope(x, table, positions, layout=ROPE_INTERLEAVED, out=None, stream=None):
     else:
         outs = x if out is None else out
         fields = _rope_tensor(x, outs, layout, rot, device, dtype, n)
-    _launch("dsa_rope", device, stream, _rope_spec(table, positions, device, n), _PACK_ROPE_TENSORS[count](*fields),
-            count, DTYPE_BF16 if dtype is _bfloat16 else DTYPE_FP32, n)
+    _launch("dsa_rope_with_axes" if table.num_axes else "dsa_rope", device, stream,
+            _rope_spec(table, positions, device, n), _PACK_ROPE_TENSORS[count](*fields), count,
+            DTYPE_BF16 if dtype is _bfloat16 else DTYPE_FP32, n)
     return outs
+
+
+rope_with_axes = rope  # (which of the two C calls is made goes by the table)
 
 
 class KvCache:
@@ -664,8 +758,9 @@ class KvCache:
 def kv_insert(kv, slots, k, v, rope=None, positions=None, layout=ROPE_HALF, rot_offset=0, q=None, q_out=None,
               status=None, stream=None):
     """dsa_kv_insert: write k, v [tokens, kv_heads, head_dim] bf16 (parts of packed rows) at their slots of
-    the KvCache.  With `rope` (a RopeTable) and `positions`, K's dims [rot_offset, rot_offset + rot_dim) are
-    rotated first, and q [tokens, heads, rot_dim] too, into q_out (default: in place).  Returns q_out."""
+    the KvCache.  With `rope` (a RopeTable) and `positions` (as `rope` takes them), K's dims [rot_offset,
+    rot_offset + rot_dim) are rotated first, and q [tokens, heads, rot_dim] too, into q_out (default: in place).
+    Returns q_out."""
     if slots.dim() != 1:
         raise DsaError(f"slots is [tokens]: got {tuple(slots.shape)}")
     n, device, heads, dim = slots.shape[0], kv.device, kv.kv_heads, kv.head_dim
@@ -694,33 +789,105 @@ def kv_insert(kv, slots, k, v, rope=None, positions=None, layout=ROPE_HALF, rot_
             qt = _PACK_ROPE_TENSORS[1](*_rope_tensor(q, q_out, layout, rope.rot_dim, device, _bfloat16, n))
     elif q is not None:
         raise DsaError("q is rotated only: it needs rope")
-    _launch("dsa_kv_insert", device, stream, kv._packed, slots.data_ptr(), n,
+    _launch("dsa_kv_insert_with_axes" if rope is not None and rope.num_axes else "dsa_kv_insert", device, stream,
+            kv._packed, slots.data_ptr(), n,
             _PACK_KV_ROWS(k.data_ptr(), v.data_ptr(), k_stride, v_stride, rot_offset, layout), spec, qt,
             None if status is None else _flat(status, "status", device, _I32))
     return q_out
+
+
+kv_insert_with_axes = kv_insert  # (as rope_with_axes)
+
+
+def kv_plan(context, new_tokens, block_table, free_pages, free_count, page_size, num_pages, row_req, row_ctx,
+            positions=None, slots=None, first_own=None, segment_requests=None, segment_rows=None, row_start=None,
+            granted=None, context_out=None, free_count_out=None, rows_per_group=1, status=None, stream=None):
+    """dsa_kv_plan: the rows (row_req, row_ctx, positions, slots), new pages and lengths of a step in which request i
+    gets new_tokens[i] tokens (-1: it has ended).  All tensors are int32; block_table, free_pages and the tensors
+    from row_req on are written (not first_own and segment_requests)."""
+    device = context.get_device()
+    if device < 0:
+        raise DsaError("libdsa takes device tensors only")
+    if block_table.dim() != 2:
+        raise DsaError("the block table is [requests, pages]")
+    n, width = block_table.shape
+    rows, segments = row_req.shape[0], 0
+    if (segment_requests is None) != (segment_rows is None):
+        raise DsaError("segment_requests and segment_rows come together")
+    if segment_requests is not None:
+        segments = max(segment_requests.numel() - 1, 0)
+
+    def at(t, what, shape):
+        return 0 if t is None else _flat(t, what, device, _I32, shape)
+    of = (n,)
+    step = _PACK_STEP(
+        n, int(page_size), int(num_pages), _flat(context, "context", device, _I32, of),
+        _flat(new_tokens, "new_tokens", device, _I32, of), at(first_own, "first_own", of),
+        _flat(block_table, "block_table", device, _I32), width,
+        _flat(free_pages, "free_pages", device, _I32, (free_pages.numel(),)),
+        _flat(free_count, "free_count", device, _I32, (1,)), free_pages.numel(), segments,
+        at(segment_requests, "segment_requests", (segments + 1,)), rows, int(rows_per_group),
+        _flat(row_req, "row_req", device, _I32, (rows,)), _flat(row_ctx, "row_ctx", device, _I32, (rows,)),
+        at(positions, "positions", (rows,)), at(slots, "slots", (rows,)), at(row_start, "row_start", (n + 1,)),
+        at(granted, "granted", of), at(context_out, "context_out", of), at(free_count_out, "free_count_out", (1,)),
+        at(segment_rows, "segment_rows", (segments + 1,)))
+    _launch("dsa_kv_plan", device, stream, step, None if status is None else _flat(status, "status", device, _I32))
+
+
+class KvPlan:
+    """The rows of a batch's steps (kv_plan), in buffers allocated once, so that repeated calls and captured graphs
+    allocate nothing: row_req, row_ctx, positions, slots [max_rows], row_start [num_requests + 1], granted and context
+    [num_requests], free_count [1] and segment_rows [num_segments + 1] hold what the last `run` made."""
+
+    def __init__(self, num_requests, max_rows, page_size, num_pages, rows_per_group=1, num_segments=0, device="cuda"):
+        n, rows, self.num_segments = int(num_requests), int(max_rows), int(num_segments)
+        self.page_size, self.num_pages, self.rows_per_group = int(page_size), int(num_pages), int(rows_per_group)
+
+        def new(size, value):
+            return torch.full((size,), value, dtype=torch.int32, device=device)
+        self.row_req, self.row_ctx = new(rows, 0), new(rows, 0)
+        self.positions, self.slots = new(rows, -1), new(rows, -1)
+        self.row_start, self.granted, self.context, self.free_count = new(n + 1, 0), new(n, 0), new(n, 0), new(1, 0)
+        self.segment_rows = new(self.num_segments + 1 if self.num_segments else 0, 0)
+        self.status = new_status(device)
+
+    def run(self, context, new_tokens, block_table, free_pages, free_count, first_own=None, segment_requests=None,
+            stream=None):
+        """context and free_count may be the plan's own of the step before.  Returns self."""
+        if (segment_requests is None) != (self.num_segments == 0):
+            raise DsaError(f"the plan is of {self.num_segments} segments")
+        kv_plan(context, new_tokens, block_table, free_pages, free_count, self.page_size, self.num_pages, self.row_req,
+                self.row_ctx, self.positions, self.slots, first_own, segment_requests,
+                None if segment_requests is None else self.segment_rows, self.row_start, self.granted, self.context,
+                self.free_count, self.rows_per_group, self.status, stream)
+        return self
 
 
 def kv_attention_workspace_size(kv, num_rows, num_heads, max_ctx) -> int:
     return int(load_library().dsa_kv_attention_workspace_size(kv._c, int(num_rows), int(num_heads), int(max_ctx)))
 
 
-def _attention_buffers(kv, R, H, max_ctx, device, out, lse, workspace):
-    """kv_attention's outputs and workspace, allocated where they are None."""
+def kv_attention_shared_workspace_size(kv, num_rows, num_heads, max_ctx, num_segments) -> int:
+    return int(load_library().dsa_kv_attention_shared_workspace_size(kv._c, int(num_rows), int(num_heads), int(max_ctx),
+                                                                     int(num_segments)))
+
+
+def _attention_buffers(kv, R, H, max_ctx, segments, device, out, lse, workspace):
+    """The attention calls' outputs and workspace, allocated where they are None."""
     if out is None:
         out = torch.empty((R, H, kv.head_dim), dtype=torch.bfloat16, device=device)
     if lse is None:
         lse = torch.empty((R, H), dtype=torch.float32, device=device)
     if workspace is None:
-        need = kv_attention_workspace_size(kv, R, H, max_ctx)
+        need = kv_attention_shared_workspace_size(kv, R, H, max_ctx, segments) if segments else \
+            kv_attention_workspace_size(kv, R, H, max_ctx)
         workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     return out, lse, workspace
 
 
-def kv_attention(kv, block_table, row_req, row_ctx, max_ctx, q, sm_scale=None, rows_per_group=1, out=None, lse=None,
-                 workspace=None, status=None, stream=None):
-    """dsa_kv_attention: (out bf16 [R, H, head_dim], lse fp32 [R, H]) of q bf16 [R, H, head_dim] (heads packed)
-    over the KvCache's tokens below row_ctx; sm_scale defaults to 1 / sqrt(head_dim).  A captured graph does not
-    keep the workspace alive: pass one that outlives it, and no other call that may run beside it uses."""
+def _attention(name, segments, packed, kv, block_table, row_req, row_ctx, max_ctx, q, sm_scale, rows_per_group, out,
+               lse, workspace, status, stream):
+    """The library's `name`; packed: what it takes of its segments."""
     R, H, D = q.shape
     device = kv.device
     if D != kv.head_dim or q.dtype is not _bfloat16 or q.get_device() != device:
@@ -733,20 +900,40 @@ def kv_attention(kv, block_table, row_req, row_ctx, max_ctx, q, sm_scale=None, r
         raise DsaError("the block table is [requests, pages]")
     if out is None or lse is None or workspace is None:
         if stream is None:
-            out, lse, workspace = _attention_buffers(kv, R, H, max_ctx, q.device, out, lse, workspace)
+            out, lse, workspace = _attention_buffers(kv, R, H, max_ctx, segments, q.device, out, lse, workspace)
         else:
             with torch.cuda.stream(stream):  # what is allocated here belongs to the stream that uses it
-                out, lse, workspace = _attention_buffers(kv, R, H, max_ctx, q.device, out, lse, workspace)
+                out, lse, workspace = _attention_buffers(kv, R, H, max_ctx, segments, q.device, out, lse, workspace)
     rows = _PACK_ROWS(_flat(block_table, "block_table", device, _I32), requests[1], requests[0],
                       _flat(row_req, "row_req", device, _I32, (R,)), _flat(row_ctx, "row_ctx", device, _I32, (R,)), R,
                       int(max_ctx), int(rows_per_group))
     wp, wb = (None, 0) if workspace is None else (_flat(workspace, "workspace", device, (workspace.dtype,)),
                                                   workspace.nbytes)
-    _launch("dsa_kv_attention", device, stream, kv._packed, rows, q.data_ptr(), a if R > 1 else H * D, H,
+    _launch(name, device, stream, kv._packed, rows, *packed, q.data_ptr(), a if R > 1 else H * D, H,
             D ** -0.5 if sm_scale is None else float(sm_scale), _flat(out, "out", device, _BF16, (R, H, D)),
             _flat(lse, "lse", device, _F32, (R, H)), wp, wb,
             None if status is None else _flat(status, "status", device, _I32))
     return out, lse
+
+
+def kv_attention(kv, block_table, row_req, row_ctx, max_ctx, q, sm_scale=None, rows_per_group=1, out=None, lse=None,
+                 workspace=None, status=None, stream=None):
+    """dsa_kv_attention: (out bf16 [R, H, head_dim], lse fp32 [R, H]) of q bf16 [R, H, head_dim] (heads packed)
+    over the KvCache's tokens below row_ctx; sm_scale defaults to 1 / sqrt(head_dim).  A captured graph does not
+    keep the workspace alive: pass one that outlives it, and no other call that may run beside it uses."""
+    return _attention("dsa_kv_attention", 0, (), kv, block_table, row_req, row_ctx, max_ctx, q, sm_scale,
+                      rows_per_group, out, lse, workspace, status, stream)
+
+
+def kv_attention_shared(kv, block_table, row_req, row_ctx, max_ctx, q, segment_rows, segment_ctx, sm_scale=None,
+                        rows_per_group=1, out=None, lse=None, workspace=None, status=None, stream=None):
+    """dsa_kv_attention_shared: kv_attention of rows of which segment_rows[s] .. segment_rows[s + 1] - 1 (int32
+    [segments + 1]) have their first segment_ctx[s] tokens (int32 [segments]) in common, read once for all of them."""
+    device, segments = kv.device, segment_ctx.shape[0]
+    packed = _PACK_SEGMENTS(_flat(segment_rows, "segment_rows", device, _I32, (segments + 1,)),
+                            _flat(segment_ctx, "segment_ctx", device, _I32, (segments,)), segments)
+    return _attention("dsa_kv_attention_shared", segments, (packed,), kv, block_table, row_req, row_ctx, max_ctx, q,
+                      sm_scale, rows_per_group, out, lse, workspace, status, stream)
 
 
 class KvLayer:
@@ -757,25 +944,31 @@ class KvLayer:
     """
 
     def __init__(self, kv, block_table, max_ctx, num_rows, num_heads, rope=None, layout=ROPE_HALF, rot_offset=0,
-                 rows_per_group=1, sm_scale=None):
+                 rows_per_group=1, sm_scale=None, num_segments=0):
         self.kv, self.block_table, self.max_ctx = kv, block_table, int(max_ctx)
         self.rope, self.layout, self.rot_offset = rope, layout, int(rot_offset)
         self.rows_per_group, self.sm_scale = rows_per_group, sm_scale
         R, H, device = int(num_rows), int(num_heads), kv.pool.device
         self.out = torch.empty((R, H, kv.head_dim), dtype=torch.bfloat16, device=device)
         self.lse = torch.empty((R, H), dtype=torch.float32, device=device)
-        need = kv_attention_workspace_size(kv, R, H, self.max_ctx)
+        need = max(kv_attention_workspace_size(kv, R, H, self.max_ctx),
+                   kv_attention_shared_workspace_size(kv, R, H, self.max_ctx, num_segments))
         self.workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
         self.status = new_status(device)
 
-    def run(self, row_req, row_ctx, slots, positions, q, k, v, stream=None):
-        """q [R, H, head_dim] is rotated in place; returns (out, lse)."""
+    def run(self, row_req, row_ctx, slots, positions, q, k, v, stream=None, segment_rows=None, segment_ctx=None):
+        """q [R, H, head_dim] is rotated in place; returns (out, lse).  With segment_rows and segment_ctx (of at most
+        num_segments segments) the rows' common prefixes are read once (kv_attention_shared)."""
         if self.rope is None:
             kv_insert(self.kv, slots, k, v, status=self.status, stream=stream)
         else:
             part = q[..., self.rot_offset:self.rot_offset + self.rope.rot_dim]
             kv_insert(self.kv, slots, k, v, rope=self.rope, positions=positions, layout=self.layout,
                       rot_offset=self.rot_offset, q=part, status=self.status, stream=stream)
+        if segment_ctx is not None:
+            return kv_attention_shared(self.kv, self.block_table, row_req, row_ctx, self.max_ctx, q, segment_rows,
+                                       segment_ctx, self.sm_scale, self.rows_per_group, out=self.out, lse=self.lse,
+                                       workspace=self.workspace, status=self.status, stream=stream)
         return kv_attention(self.kv, self.block_table, row_req, row_ctx, self.max_ctx, q, self.sm_scale,
                             self.rows_per_group, out=self.out, lse=self.lse, workspace=self.workspace,
                             status=self.status, stream=stream)

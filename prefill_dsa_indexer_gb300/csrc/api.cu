@@ -645,6 +645,55 @@ static int check_rope_spec(const dsa_rope_spec *rope) {
     return rope->rot_dim > DSA_ROPE_MAX_DIM ? DSA_ERR_UNSUPPORTED : DSA_OK;
 }
 
+extern "C++" {
+// The angles of a call as the kernels take them.
+static int rope_angles(const dsa_rope_spec *rope, RopeArgs *a) {
+    const int rc = check_rope_spec(rope);
+    if (rc != DSA_OK) return rc;
+    a->turns = rope->turns;
+    a->positions = rope->positions;
+    a->rot = rope->rot_dim;
+    a->scale = rope->scale;
+    return DSA_OK;
+}
+
+static int rope_angles(const dsa_rope_axes *rope, RopeArgs *a) {
+    if (rope == nullptr) return DSA_ERR_INVALID_ARG;
+    const dsa_rope_spec one = {rope->turns, rope->positions, rope->rot_dim, rope->scale};
+    const int rc = rope_angles(&one, a);
+    if (rc != DSA_OK) return rc;
+    if (rope->axis == nullptr || rope->num_axes < 1 || rope->axis_stride < 0) return DSA_ERR_INVALID_ARG;
+    if (rope->num_axes > DSA_ROPE_MAX_AXES) return DSA_ERR_UNSUPPORTED;
+    a->num_axes = rope->num_axes;
+    a->axis_stride = rope->axis_stride;
+    for (int p = 0; p < rope->rot_dim / 2; ++p) {
+        if (rope->axis[p] >= rope->num_axes) return DSA_ERR_INVALID_ARG;
+        a->axis[p >> 4] |= static_cast<uint32_t>(rope->axis[p]) << 2 * (p & 15);
+    }
+    return DSA_OK;
+}
+}  // extern "C++"
+
+int dsa_rope_sections(const int32_t *sections, int32_t num_axes, int32_t order, int32_t num_pairs, uint8_t *axis) {
+    if (num_axes > DSA_ROPE_MAX_AXES || num_pairs > DSA_ROPE_MAX_DIM / 2) return DSA_ERR_UNSUPPORTED;
+    if (order != DSA_ROPE_AXES_SPLIT && order != DSA_ROPE_AXES_CYCLE) return DSA_ERR_UNSUPPORTED;
+    if (sections == nullptr || axis == nullptr || num_axes < 1 || num_pairs < 1) return DSA_ERR_INVALID_ARG;
+    int32_t left[DSA_ROPE_MAX_AXES] = {};
+    int64_t total = 0;
+    for (int x = 0; x < num_axes; ++x) {
+        if (sections[x] < 0) return DSA_ERR_INVALID_ARG;
+        total += left[x] = sections[x];
+    }
+    if (total != num_pairs) return DSA_ERR_INVALID_ARG;
+    for (int p = 0, x = 0; p < num_pairs; ++p) {
+        while (left[x] == 0) x = x + 1 < num_axes ? x + 1 : 0;
+        axis[p] = static_cast<uint8_t>(x);
+        --left[x];
+        if (order == DSA_ROPE_AXES_CYCLE) x = x + 1 < num_axes ? x + 1 : 0;
+    }
+    return DSA_OK;
+}
+
 // Whether no two (token, head) parts of rot elements share an element: one of the strides steps over all of the
 // other's.
 static bool apart(int64_t token_stride, int64_t tokens, int64_t head_stride, int64_t heads, int64_t rot) {
@@ -727,16 +776,20 @@ static int rope_tensor(const dsa_rope_tensor &t, int32_t tokens, int32_t rot, in
     return DSA_OK;
 }
 
-int dsa_rope(const dsa_rope_spec *rope, const dsa_rope_tensor *tensors, int32_t num_tensors, int32_t dtype,
-             int32_t num_tokens, void *stream) {
+extern "C++" {
+template <typename Spec>
+static int rope_call(const Spec *rope, const dsa_rope_tensor *tensors, int32_t num_tensors, int32_t dtype,
+                     int32_t num_tokens, void *stream) {
     if (num_tokens < 0 || num_tensors < 1) return DSA_ERR_INVALID_ARG;
     if (num_tensors > DSA_ROPE_MAX_TENSORS) return DSA_ERR_UNSUPPORTED;
     if (dtype != DSA_DTYPE_BF16 && dtype != DSA_DTYPE_FP32) return DSA_ERR_UNSUPPORTED;
     if (num_tokens == 0) return DSA_OK;
-    int rc = check_rope_spec(rope);
+    RopeArgs a = {};
+    int rc = rope_angles(rope, &a);
     if (rc != DSA_OK) return rc;
     if (tensors == nullptr) return DSA_ERR_INVALID_ARG;
-    RopeArgs a = {rope->turns, rope->positions, rope->rot_dim, rope->scale, num_tokens, num_tensors, {}};
+    a.num_tokens = num_tokens;
+    a.num_tensors = num_tensors;
     const int elem = dtype == DSA_DTYPE_BF16 ? 2 : 4;
     for (int i = 0; i < num_tensors; ++i) {
         rc = rope_tensor(tensors[i], num_tokens, rope->rot_dim, elem, &a.t[i]);
@@ -751,6 +804,17 @@ int dsa_rope(const dsa_rope_spec *rope, const dsa_rope_tensor *tensors, int32_t 
         }
     }
     return launch_status(launch_rope(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+}  // extern "C++"
+
+int dsa_rope(const dsa_rope_spec *rope, const dsa_rope_tensor *tensors, int32_t num_tensors, int32_t dtype,
+             int32_t num_tokens, void *stream) {
+    return rope_call(rope, tensors, num_tensors, dtype, num_tokens, stream);
+}
+
+int dsa_rope_with_axes(const dsa_rope_axes *rope, const dsa_rope_tensor *tensors, int32_t num_tensors, int32_t dtype,
+                       int32_t num_tokens, void *stream) {
+    return rope_call(rope, tensors, num_tensors, dtype, num_tokens, stream);
 }
 
 // Geometry and address of a K/V pool.
@@ -769,8 +833,10 @@ static int check_kv_cache(const dsa_kv_cache *c) {
     return DSA_OK;
 }
 
-int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_tokens, const dsa_kv_rows *kv,
-                  const dsa_rope_spec *rope, const dsa_rope_tensor *q, int32_t *dev_status, void *stream) {
+extern "C++" {
+template <typename Spec>
+static int insert_call(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_tokens, const dsa_kv_rows *kv,
+                       const Spec *rope, const dsa_rope_tensor *q, int32_t *dev_status, void *stream) {
     int rc = check_kv_cache(cache);
     if (rc != DSA_OK) return rc;
     if (num_tokens < 0) return DSA_ERR_INVALID_ARG;
@@ -783,14 +849,10 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
     KvInsertArgs a = {};
     a.rope.num_tokens = num_tokens;
     if (rope != nullptr) {
-        rc = check_rope_spec(rope);
+        rc = rope_angles(rope, &a.rope);
         if (rc != DSA_OK) return rc;
         if (kv->rot_offset < 0 || kv->rot_offset > cache->head_dim - rope->rot_dim) return DSA_ERR_INVALID_ARG;
         if (kv->layout != DSA_ROPE_INTERLEAVED && kv->layout != DSA_ROPE_HALF) return DSA_ERR_UNSUPPORTED;
-        a.rope.turns = rope->turns;
-        a.rope.positions = rope->positions;
-        a.rope.rot = rope->rot_dim;
-        a.rope.scale = rope->scale;
         a.rot_offset = kv->rot_offset;
         a.half = kv->layout == DSA_ROPE_HALF;
         if (q != nullptr) {
@@ -829,6 +891,17 @@ int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_t
     a.status = dev_status;
     return launch_status(launch_kv_insert(a, static_cast<cudaStream_t>(stream)));
 }
+}  // extern "C++"
+
+int dsa_kv_insert(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_tokens, const dsa_kv_rows *kv,
+                  const dsa_rope_spec *rope, const dsa_rope_tensor *q, int32_t *dev_status, void *stream) {
+    return insert_call(cache, slots, num_tokens, kv, rope, q, dev_status, stream);
+}
+
+int dsa_kv_insert_with_axes(const dsa_kv_cache *cache, const int32_t *slots, int32_t num_tokens, const dsa_kv_rows *kv,
+                            const dsa_rope_axes *rope, const dsa_rope_tensor *q, int32_t *dev_status, void *stream) {
+    return insert_call(cache, slots, num_tokens, kv, rope, q, dev_status, stream);
+}
 
 size_t dsa_kv_attention_workspace_size(const dsa_kv_cache *cache, int32_t num_rows, int32_t num_heads,
                                        int32_t max_ctx) {
@@ -837,9 +910,10 @@ size_t dsa_kv_attention_workspace_size(const dsa_kv_cache *cache, int32_t num_ro
     return kv_attention_workspace_bytes(num_rows, num_heads, cache->kv_heads, cache->head_dim, max_ctx);
 }
 
-int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint16_t *q, int64_t q_stride,
-                     int32_t num_heads, float sm_scale, uint16_t *out, float *lse, void *workspace,
-                     size_t workspace_bytes, int32_t *dev_status, void *stream) {
+// segments: NULL, or with one segment at least.
+static int attention_call(const dsa_kv_cache *cache, const dsa_rows *rows, const dsa_kv_segments *segments,
+                          const uint16_t *q, int64_t q_stride, int32_t num_heads, float sm_scale, uint16_t *out,
+                          float *lse, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream) {
     int rc = check_kv_cache(cache);
     if (rc != DSA_OK) return rc;
     if (rows == nullptr || rows->num_rows < 0 || rows->max_ctx < 0 || rows->num_requests < 0)
@@ -855,6 +929,7 @@ int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint
     if (q_stride < static_cast<int64_t>(num_heads) * cache->head_dim || q_stride % 8 != 0) return DSA_ERR_INVALID_ARG;
     const int64_t need_pages = (static_cast<int64_t>(rows->max_ctx) + cache->page_size - 1) / cache->page_size;
     if (rows->bt_stride < need_pages) return DSA_ERR_INVALID_ARG;
+    if (segments != nullptr && (!segments->first_row || !segments->shared_ctx)) return DSA_ERR_INVALID_ARG;
     const size_t need = kv_attention_workspace_bytes(rows->num_rows, num_heads, cache->kv_heads, cache->head_dim,
                                                      rows->max_ctx);
     if (need > 0) {
@@ -892,7 +967,106 @@ int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint
     a.out = out;
     a.lse = lse;
     a.status = dev_status;
-    return launch_status(launch_kv_attention(a, workspace, static_cast<cudaStream_t>(stream)));
+    if (segments == nullptr) return launch_status(launch_kv_attention(a, workspace, static_cast<cudaStream_t>(stream)));
+    const KvSegmentArgs seg = {segments->first_row, segments->shared_ctx, segments->num_segments, rows->num_rows, G,
+                               dev_status};
+    return launch_status(launch_kv_attention_shared(seg, a, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint16_t *q, int64_t q_stride,
+                     int32_t num_heads, float sm_scale, uint16_t *out, float *lse, void *workspace,
+                     size_t workspace_bytes, int32_t *dev_status, void *stream) {
+    return attention_call(cache, rows, nullptr, q, q_stride, num_heads, sm_scale, out, lse, workspace, workspace_bytes,
+                          dev_status, stream);
+}
+
+size_t dsa_kv_attention_shared_workspace_size(const dsa_kv_cache *cache, int32_t num_rows, int32_t num_heads,
+                                              int32_t max_ctx, int32_t num_segments) {
+    if (num_segments < 0) return 0;
+    return dsa_kv_attention_workspace_size(cache, num_rows, num_heads, max_ctx);
+}
+
+int dsa_kv_attention_shared(const dsa_kv_cache *cache, const dsa_rows *rows, const dsa_kv_segments *segments,
+                            const uint16_t *q, int64_t q_stride, int32_t num_heads, float sm_scale, uint16_t *out,
+                            float *lse, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream) {
+    if (segments == nullptr || segments->num_segments < 0) return DSA_ERR_INVALID_ARG;
+    return attention_call(cache, rows, segments->num_segments > 0 ? segments : nullptr, q, q_stride, num_heads, sm_scale,
+                          out, lse, workspace, workspace_bytes, dev_status, stream);
+}
+
+int dsa_kv_plan(const dsa_kv_step *step, int32_t *dev_status, void *stream) {
+    if (step == nullptr) return DSA_ERR_INVALID_ARG;
+    const dsa_kv_step &p = *step;
+    if (p.page_size != 16 && p.page_size != 32 && p.page_size != 64 && p.page_size != 128) return DSA_ERR_UNSUPPORTED;
+    if (p.rows_per_group != 1 && p.rows_per_group != 2 && p.rows_per_group != 4 && p.rows_per_group != 8)
+        return DSA_ERR_UNSUPPORTED;
+    if (p.num_requests < 0 || p.num_pages < 0 || p.bt_stride < 0 || p.free_capacity < 0 || p.num_segments < 0 ||
+        p.max_rows < 0 || p.max_rows % p.rows_per_group != 0)
+        return DSA_ERR_INVALID_ARG;
+    if (p.num_requests > DSA_KV_PLAN_MAX_REQUESTS || p.num_pages > ((1ll << 31) - 1) / p.page_size)
+        return DSA_ERR_UNSUPPORTED;
+    if (p.free_count == nullptr || (p.free_capacity > 0 && p.free_pages == nullptr)) return DSA_ERR_INVALID_ARG;
+    if (p.num_requests > 0 && (!p.context || !p.new_tokens || (p.bt_stride > 0 && !p.block_table)))
+        return DSA_ERR_INVALID_ARG;
+    if (p.max_rows > 0 && (!p.row_req || !p.row_ctx)) return DSA_ERR_INVALID_ARG;
+    if (p.num_segments > 0 && (!p.segment_requests || !p.segment_rows)) return DSA_ERR_INVALID_ARG;
+    if (p.bt_stride > (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+    // what a call writes lies apart from all else that it touches
+    struct Block {
+        const void *base;
+        int64_t words;
+        bool written;
+    };
+    const int64_t n = p.num_requests, rows = p.max_rows, segs = p.num_segments > 0 ? p.num_segments + 1ll : 0;
+    const bool same_context = p.context_out == p.context, same_count = p.free_count_out == p.free_count;
+    const Block blocks[] = {{p.context, n, same_context}, {p.new_tokens, n, false}, {p.first_own, n, false},
+                            {p.free_count, 1, same_count}, {p.segment_requests, segs, false},
+                            {p.block_table, n * p.bt_stride, true}, {p.free_pages, p.free_capacity, true},
+                            {p.row_req, rows, true}, {p.row_ctx, rows, true}, {p.positions, rows, true},
+                            {p.slots, rows, true}, {p.row_start, n + 1, true}, {p.granted, n, true},
+                            {same_context ? nullptr : p.context_out, n, true},
+                            {same_count ? nullptr : p.free_count_out, 1, true},
+                            {p.segment_rows, segs, true}, {dev_status, 1, true}};
+    for (const Block &x : blocks) {
+        if (x.base == nullptr || x.words == 0) continue;
+        if (!aligned(x.base, 4)) return DSA_ERR_INVALID_ARG;
+        for (const Block *y = blocks; y != &x; ++y) {
+            if (y->base == nullptr || y->words == 0 || !(x.written || y->written)) continue;
+            const uintptr_t a = reinterpret_cast<uintptr_t>(x.base), b = reinterpret_cast<uintptr_t>(y->base);
+            if (a < b + static_cast<uintptr_t>(y->words) * 4 && b < a + static_cast<uintptr_t>(x.words) * 4)
+                return DSA_ERR_INVALID_ARG;
+        }
+    }
+    KvPlanArgs a = {};
+    a.num_requests = p.num_requests;
+    a.page_size = p.page_size;
+    for (a.page_shift = 4; 1 << a.page_shift < a.page_size;) ++a.page_shift;
+    a.num_pages = p.num_pages;
+    const int64_t most = p.bt_stride * p.page_size;
+    a.capacity = most < 0x7fffffff ? static_cast<int32_t>(most) : 0x7fffffff;
+    a.context = p.context;
+    a.new_tokens = p.new_tokens;
+    a.first_own = p.first_own;
+    a.block_table = p.block_table;
+    a.bt_stride = p.bt_stride;
+    a.free_pages = p.free_pages;
+    a.free_capacity = p.free_capacity;
+    a.free_count = p.free_count;
+    a.segment_requests = p.segment_requests;
+    a.num_segments = p.num_segments;
+    a.max_rows = p.max_rows;
+    a.group = p.rows_per_group;
+    a.row_req = p.row_req;
+    a.row_ctx = p.row_ctx;
+    a.positions = p.positions;
+    a.slots = p.slots;
+    a.row_start = p.row_start;
+    a.granted = p.granted;
+    a.context_out = p.context_out;
+    a.free_count_out = p.free_count_out;
+    a.segment_rows = p.segment_rows;
+    a.status = dev_status;
+    return launch_status(launch_kv_plan(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -285,6 +285,9 @@ struct RopeArgs {
     int32_t num_tokens;
     int32_t num_tensors;
     RopeTensor t[DSA_ROPE_MAX_TENSORS];
+    int32_t num_axes;      // 0 or 1: one position a token
+    int64_t axis_stride;   // positions of the next axis
+    uint32_t axis[DSA_ROPE_MAX_DIM / 2 / 16];  // two bits a pair: its axis
 };
 
 struct KvInsertArgs {
@@ -307,6 +310,30 @@ struct KvInsertArgs {
 
 cudaError_t launch_rope(const RopeArgs &a, int32_t dtype, cudaStream_t s);
 cudaError_t launch_kv_insert(const KvInsertArgs &a, cudaStream_t s);
+
+// ---- a step's rows, slots and pages (plan.cu)
+constexpr int kPlanMaxRequests = DSA_KV_PLAN_MAX_REQUESTS;  // (their sums are in shared memory: 128 KB)
+constexpr int kPlanOneCtaRows = 1024;
+
+struct KvPlanArgs {
+    int32_t num_requests, page_size, page_shift;
+    int64_t num_pages;
+    int32_t capacity;  // tokens that a row of the table can list
+    const int32_t *context, *new_tokens, *first_own;
+    int32_t *block_table;
+    int64_t bt_stride;
+    int32_t *free_pages;
+    int32_t free_capacity;
+    const int32_t *free_count;
+    const int32_t *segment_requests;
+    int32_t num_segments;
+    int32_t max_rows, group;
+    int32_t *row_req, *row_ctx, *positions, *slots;
+    int32_t *row_start, *granted, *context_out, *free_count_out, *segment_rows;
+    int32_t *status;
+};
+
+cudaError_t launch_kv_plan(const KvPlanArgs &a, cudaStream_t s);
 
 struct KvAttnArgs {
     const void *pool;
@@ -347,6 +374,16 @@ struct KvAttnArgs {
 };
 
 cudaError_t launch_kv_attention(KvAttnArgs &a, void *workspace, cudaStream_t s);
+
+// ---- rows that share prefixes (kv_attention_shared.cu)
+struct KvSegmentArgs {
+    const int32_t *first_row, *shared_ctx;
+    int32_t num_segments;
+    int32_t num_rows, group;
+    int32_t *status;
+};
+
+cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, void *workspace, cudaStream_t s);
 
 // The parts of an FP8 pool of head_dim 128 (kv_attention_fp8.cu; called by launch_kv_attention).
 cudaError_t launch_kv_attention_fp8(KvAttnArgs &a, cudaStream_t s);

@@ -105,13 +105,26 @@ struct Table {
     alignas(16) float cos[kTabPairs], sin[kTabPairs];
 };
 
-// pos_s: the tile's positions.
+// A token's position as far as its sign goes: negative if one of its axes' is.
+template <bool kAxes>
+__device__ __forceinline__ int32_t sign_position(const RopeArgs &a, int token) {
+    int32_t pos = a.positions[token];
+    if constexpr (kAxes)
+        for (int x = 1; x < a.num_axes; ++x) pos |= a.positions[x * a.axis_stride + token];
+    return pos;
+}
+
+// pos_s: the tile's positions (their signs).  kAxes: pair p's angle goes by the position on its own axis; the axes
+// of all pairs come with the launch, two bits each.
+template <bool kAxes>
 __device__ __forceinline__ void fill_table(const RopeArgs &a, Table &tab, int32_t *pos_s, int t0, int nt) {
     const int pairs = a.rot >> 1;
-    if (static_cast<int>(threadIdx.x) < nt) pos_s[threadIdx.x] = a.positions[t0 + threadIdx.x];
+    if (static_cast<int>(threadIdx.x) < nt) pos_s[threadIdx.x] = sign_position<kAxes>(a, t0 + threadIdx.x);
     for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
         const int tok = i / pairs, p = i - tok * pairs;
-        const int64_t pos = a.positions[t0 + tok];
+        const int32_t *of = a.positions;
+        if constexpr (kAxes) of += (a.axis[p >> 4] >> 2 * (p & 15) & 3u) * a.axis_stride;
+        const int64_t pos = of[t0 + tok];
         const uint64_t phase = static_cast<uint64_t>(pos) * a.turns[p];
         const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
         float sn, cs;
@@ -209,7 +222,7 @@ __device__ __forceinline__ void copy_wait() {
 
 // Rotate the tile's pieces.  The 16-byte forms pass through a ring of the thread's own in shared memory, so that
 // several are in flight while one is worked on, the first ones while the table is made.
-template <typename T, bool kHalf, int V>
+template <bool kAxes, typename T, bool kHalf, int V>
 __device__ __forceinline__ void rotate_tile(const RopeArgs &a, const RopeTensor &x, Table &tab, int32_t *pos_s,
                                             uint8_t *ring, int t0, int nt, int h0, int nh, int units) {
     using H = HeadPiece<T, kHalf, V>;
@@ -219,7 +232,7 @@ __device__ __forceinline__ void rotate_tile(const RopeArgs &a, const RopeTensor 
     T *dst = static_cast<T *>(x.out) + t0 * x.out_token + h0 * x.out_head + w.unit * V;
     const int unit = w.unit * H::kPairs;
     if constexpr (V * sizeof(T) < 16) {
-        fill_table(a, tab, pos_s, t0, nt);
+        fill_table<kAxes>(a, tab, pos_s, t0, nt);
         __syncthreads();
         for (; w.tok < nt; w.step(nh)) {
             if (pos_s[w.tok] < 0) continue;  // a padding token
@@ -269,7 +282,7 @@ __device__ __forceinline__ void rotate_tile(const RopeArgs &a, const RopeTensor 
         };
 #pragma unroll 1
         for (int i = 0; i < kDepth - 1; ++i) start();
-        fill_table(a, tab, pos_s, t0, nt);
+        fill_table<kAxes>(a, tab, pos_s, t0, nt);
         __syncthreads();
         float c[H::kPairs], s[H::kPairs];  // of the token at hand
         int held = -1;
@@ -299,7 +312,7 @@ __device__ __forceinline__ void rotate_tile(const RopeArgs &a, const RopeTensor 
     }
 }
 
-template <typename T>
+template <bool kAxes, typename T>
 __device__ __forceinline__ void rope_segment(const RopeArgs &a, const RopeTensor &x, const Segment &g, uint32_t cta,
                                              Table &tab, int32_t *pos_s, uint8_t *ring) {
     const uint32_t tile = cta / g.head_chunks, chunk = cta - tile * g.head_chunks;
@@ -308,11 +321,11 @@ __device__ __forceinline__ void rope_segment(const RopeArgs &a, const RopeTensor
     const int units = static_cast<int>(g.units);
     constexpr int V = 16 / sizeof(T);
     if (x.half) {
-        if (x.vec) rotate_tile<T, true, V>(a, x, tab, pos_s, ring, t0, nt, h0, nh, units);
-        else rotate_tile<T, true, 1>(a, x, tab, pos_s, ring, t0, nt, h0, nh, units);
+        if (x.vec) rotate_tile<kAxes, T, true, V>(a, x, tab, pos_s, ring, t0, nt, h0, nh, units);
+        else rotate_tile<kAxes, T, true, 1>(a, x, tab, pos_s, ring, t0, nt, h0, nh, units);
     } else {
-        if (x.vec) rotate_tile<T, false, V>(a, x, tab, pos_s, ring, t0, nt, h0, nh, units);
-        else rotate_tile<T, false, 2>(a, x, tab, pos_s, ring, t0, nt, h0, nh, units);
+        if (x.vec) rotate_tile<kAxes, T, false, V>(a, x, tab, pos_s, ring, t0, nt, h0, nh, units);
+        else rotate_tile<kAxes, T, false, 2>(a, x, tab, pos_s, ring, t0, nt, h0, nh, units);
     }
 }
 
@@ -322,7 +335,7 @@ __device__ __forceinline__ const Segment &segment_of(const Plan &p, uint32_t cta
     return p.s[which];
 }
 
-template <typename T>
+template <typename T, bool kAxes>
 __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant__ RopeArgs a,
                                                         const __grid_constant__ Plan p) {
     __shared__ Table tab;
@@ -332,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant
     pdl_launch_dependents();
     int j;
     const Segment &g = segment_of(p, blockIdx.x, j);
-    rope_segment<T>(a, a.t[j], g, blockIdx.x - g.first, tab, pos_s, ring);
+    rope_segment<kAxes, T>(a, a.t[j], g, blockIdx.x - g.first, tab, pos_s, ring);
 }
 
 // x / s rounded to nearest for the quotients that matter here, from r = 1 / s rounded to nearest: one correction
@@ -449,6 +462,7 @@ __device__ __forceinline__ void insert_tile(const KvInsertArgs &a, const Table &
 }
 
 // Segment 0: the K and V rows; segment 1, if any: q.
+template <bool kAxes>
 __global__ void __launch_bounds__(kThreads, 6) kv_insert_kernel(const __grid_constant__ KvInsertArgs a,
                                                              const __grid_constant__ Plan p) {
     __shared__ Table tab;
@@ -460,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 6) kv_insert_kernel(const __grid_con
     const Segment &g = segment_of(p, blockIdx.x, j);
     const uint32_t cta = blockIdx.x - g.first;
     if (j == 1) {
-        rope_segment<__nv_bfloat16>(a.rope, a.rope.t[0], g, cta, tab, pos_s, ring);
+        rope_segment<kAxes, __nv_bfloat16>(a.rope, a.rope.t[0], g, cta, tab, pos_s, ring);
         return;
     }
     const int t0 = static_cast<int>(cta * g.tokens);
@@ -468,13 +482,13 @@ __global__ void __launch_bounds__(kThreads, 6) kv_insert_kernel(const __grid_con
     __shared__ int32_t slot_s[kTileTokens];
     if (static_cast<int>(threadIdx.x) < nt) {
         int32_t slot = a.slots[t0 + threadIdx.x];
-        if (slot >= a.num_slots || (slot >= 0 && a.rope.rot > 0 && a.rope.positions[t0 + threadIdx.x] < 0)) {
+        if (slot >= a.num_slots || (slot >= 0 && a.rope.rot > 0 && sign_position<kAxes>(a.rope, t0 + threadIdx.x) < 0)) {
             report(a.status, DSA_ERR_BOUNDS);
             slot = -1;
         }
         slot_s[threadIdx.x] = slot;
     }
-    if (a.rope.rot > 0) fill_table(a.rope, tab, pos_s, t0, nt);
+    if (a.rope.rot > 0) fill_table<kAxes>(a.rope, tab, pos_s, t0, nt);
     __syncthreads();
     if (a.vec) insert_tile<8>(a, tab, slot_s, t0, nt);
     else insert_tile<1>(a, tab, slot_s, t0, nt);
@@ -529,9 +543,10 @@ cudaError_t launch_rope(const RopeArgs &a, int32_t dtype, cudaStream_t s) {
     for (int i = 0; i < a.num_tensors; ++i)
         if (!add_segment(p, ctas, a.num_tokens, a.t[i].heads, rope_units(a.t[i], a.rot, v), a.rot / 2, true, kManyRope))
             return cudaErrorInvalidConfiguration;
-    return dtype == DSA_DTYPE_BF16
-               ? launch_pdl(rope_kernel<__nv_bfloat16>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, a, p)
-               : launch_pdl(rope_kernel<float>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, a, p);
+    const bool axes = a.num_axes > 1;
+    auto kern = dtype == DSA_DTYPE_BF16 ? (axes ? rope_kernel<__nv_bfloat16, true> : rope_kernel<__nv_bfloat16, false>)
+                                        : (axes ? rope_kernel<float, true> : rope_kernel<float, false>);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, a, p);
 }
 
 cudaError_t launch_kv_insert(const KvInsertArgs &a, cudaStream_t s) {
@@ -545,7 +560,8 @@ cudaError_t launch_kv_insert(const KvInsertArgs &a, cudaStream_t s) {
         !add_segment(p, ctas, a.rope.num_tokens, a.rope.t[0].heads, rope_units(a.rope.t[0], a.rope.rot, 8),
                      a.rope.rot / 2, true, kManyQ))
         return cudaErrorInvalidConfiguration;
-    return launch_pdl(kv_insert_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, a, p);
+    return launch_pdl(a.rope.num_axes > 1 ? kv_insert_kernel<true> : kv_insert_kernel<false>,
+                      dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, s, a, p);
 }
 
 }  // namespace dsa
