@@ -930,8 +930,11 @@ static int attention_call(const dsa_kv_cache *cache, const dsa_rows *rows, const
     const int64_t need_pages = (static_cast<int64_t>(rows->max_ctx) + cache->page_size - 1) / cache->page_size;
     if (rows->bt_stride < need_pages) return DSA_ERR_INVALID_ARG;
     if (segments != nullptr && (!segments->first_row || !segments->shared_ctx)) return DSA_ERR_INVALID_ARG;
-    const size_t need = kv_attention_workspace_bytes(rows->num_rows, num_heads, cache->kv_heads, cache->head_dim,
-                                                     rows->max_ctx);
+    const size_t need = segments == nullptr
+                            ? kv_attention_workspace_bytes(rows->num_rows, num_heads, cache->kv_heads, cache->head_dim,
+                                                           rows->max_ctx)
+                            : kv_attention_shared_workspace_bytes(rows->num_rows, num_heads, cache->kv_heads,
+                                                                  cache->head_dim, rows->max_ctx, segments->num_segments);
     if (need > 0) {
         if (workspace == nullptr || workspace_bytes < need) return DSA_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return DSA_ERR_INVALID_ARG;
@@ -968,8 +971,7 @@ static int attention_call(const dsa_kv_cache *cache, const dsa_rows *rows, const
     a.lse = lse;
     a.status = dev_status;
     if (segments == nullptr) return launch_status(launch_kv_attention(a, workspace, static_cast<cudaStream_t>(stream)));
-    const KvSegmentArgs seg = {segments->first_row, segments->shared_ctx, segments->num_segments, rows->num_rows, G,
-                               dev_status};
+    const KvSegmentArgs seg = {segments->first_row, segments->shared_ctx, segments->num_segments};
     return launch_status(launch_kv_attention_shared(seg, a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
@@ -982,16 +984,21 @@ int dsa_kv_attention(const dsa_kv_cache *cache, const dsa_rows *rows, const uint
 
 size_t dsa_kv_attention_shared_workspace_size(const dsa_kv_cache *cache, int32_t num_rows, int32_t num_heads,
                                               int32_t max_ctx, int32_t num_segments) {
-    if (num_segments < 0) return 0;
-    return dsa_kv_attention_workspace_size(cache, num_rows, num_heads, max_ctx);
+    if (num_segments <= 0)
+        return num_segments < 0 ? 0 : dsa_kv_attention_workspace_size(cache, num_rows, num_heads, max_ctx);
+    if (check_kv_cache(cache) != DSA_OK || num_rows <= 0 || num_heads <= 0 || max_ctx <= 0) return 0;
+    if (max_ctx > DSA_KV_MAX_CTX) return 0;
+    return kv_attention_shared_workspace_bytes(num_rows, num_heads, cache->kv_heads, cache->head_dim, max_ctx,
+                                               num_segments);
 }
 
 int dsa_kv_attention_shared(const dsa_kv_cache *cache, const dsa_rows *rows, const dsa_kv_segments *segments,
                             const uint16_t *q, int64_t q_stride, int32_t num_heads, float sm_scale, uint16_t *out,
                             float *lse, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream) {
     if (segments == nullptr || segments->num_segments < 0) return DSA_ERR_INVALID_ARG;
-    return attention_call(cache, rows, segments->num_segments > 0 ? segments : nullptr, q, q_stride, num_heads, sm_scale,
-                          out, lse, workspace, workspace_bytes, dev_status, stream);
+    const bool some = segments->num_segments > 0 && rows != nullptr && rows->max_ctx > 0;
+    return attention_call(cache, rows, some ? segments : nullptr, q, q_stride, num_heads, sm_scale, out, lse, workspace,
+                          workspace_bytes, dev_status, stream);
 }
 
 int dsa_kv_plan(const dsa_kv_step *step, int32_t *dev_status, void *stream) {

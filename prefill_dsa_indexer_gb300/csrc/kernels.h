@@ -350,6 +350,9 @@ struct KvAttnArgs {
     int32_t num_rows;
     int32_t max_ctx;
     int32_t group;     // rows per group
+    const int32_t *row_begin;  // or NULL: each row's tokens before this one (a multiple of 128) are read elsewhere, and
+                               // row_ctx counts from it; of rows that share a group, one
+    bool keep_parts;   // a row's only part goes to the workspace too
     const uint16_t *q;
     int64_t q_stride;
     int32_t num_heads;
@@ -375,15 +378,18 @@ struct KvAttnArgs {
 
 cudaError_t launch_kv_attention(KvAttnArgs &a, void *workspace, cudaStream_t s);
 
+// launch_kv_attention without the merge: the parts' outputs in a.part_o and a.part_ml.
+cudaError_t launch_kv_attention_parts(KvAttnArgs &a, void *workspace, cudaStream_t s);
+
 // ---- rows that share prefixes (kv_attention_shared.cu)
 struct KvSegmentArgs {
     const int32_t *first_row, *shared_ctx;
     int32_t num_segments;
-    int32_t num_rows, group;
-    int32_t *status;
 };
 
 cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, void *workspace, cudaStream_t s);
+size_t kv_attention_shared_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
+                                           int32_t max_ctx, int32_t num_segments);
 
 // The parts of an FP8 pool of head_dim 128 (kv_attention_fp8.cu; called by launch_kv_attention).
 cudaError_t launch_kv_attention_fp8(KvAttnArgs &a, cudaStream_t s);
@@ -392,7 +398,7 @@ cudaError_t launch_kv_attention_fp8(KvAttnArgs &a, cudaStream_t s);
 // span of 64 or 128 bytes (api.cu).
 bool encode_kv_rows_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t row_bytes, uint32_t box_rows);
 size_t kv_attention_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
-                                    int32_t max_ctx);
+                                    int32_t max_ctx, bool keep_parts = false);
 
 int device_sm_count();
 

@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         bool go = true;
         for (; more && go; more = w.next<kCols>(a, lane)) {
             const int num_pages = (w.t_end + a.page_size - 1) >> a.page_shift;
-            const int32_t *table = a.block_table + static_cast<int64_t>(w.req) * a.bt_stride;
+            const int32_t *table = kv_table(a, w.req, w.row0);
             auto load_ids = [&](int p) { return p + lane < num_pages ? table[p + lane] : 0; };
             int batch = w.t_begin >> a.page_shift;  // page ids batch .. batch + 31 are in `ids`, one per lane
             int32_t ids = load_ids(batch), ids_next = load_ids(batch + 32);
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             return static_cast<int64_t>(row0 + row) * a.num_heads + g * hpg + col - row * hpg;
         };
         auto finish = [&](int64_t at, int d, const float4 &x, float b, float total) {  // dims d .. d + 3 of head `at`
-            if (parts > 1) {
+            if (parts > 1 || a.keep_parts) {
                 *reinterpret_cast<float4 *>(a.part_o + (at * a.parts_bound + part) * D + d) = x;
                 if (d == 0) a.part_ml[at * a.parts_bound + part] = make_float2(part_base(b, total), total);
             } else {
@@ -853,15 +853,14 @@ cudaError_t launch_format(KvAttnArgs &a, cudaStream_t s) {
 }  // namespace
 
 size_t kv_attention_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
-                                    int32_t max_ctx) {
+                                    int32_t max_ctx, bool keep_parts) {
     const size_t parts = static_cast<size_t>(kv_parts_bound(max_ctx, kv_parts_shift(kv_heads)));
-    if (parts <= 1) return 0;
+    if (parts <= 1 && !keep_parts) return 0;
     const size_t n = static_cast<size_t>(num_rows) * static_cast<size_t>(num_heads) * parts;
     return align256(n * static_cast<size_t>(head_dim) * 4) + align256(n * 8);
 }
 
-cudaError_t launch_kv_attention(KvAttnArgs &a, void *workspace, cudaStream_t s) {
-    if (a.num_rows == 0) return cudaSuccess;
+cudaError_t launch_kv_attention_parts(KvAttnArgs &a, void *workspace, cudaStream_t s) {
     for (a.page_shift = 4; 1 << a.page_shift < a.page_size;) ++a.page_shift;
     const uint32_t hpg = static_cast<uint32_t>(a.num_heads / a.kv_heads);
     a.hpg = static_cast<int32_t>(hpg);
@@ -872,9 +871,13 @@ cudaError_t launch_kv_attention(KvAttnArgs &a, void *workspace, cudaStream_t s) 
     a.part_o = static_cast<float *>(workspace);
     a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
                                            align256(n * static_cast<size_t>(a.head_dim) * 4));
-    cudaError_t e;
-    if (a.fp8) e = a.head_dim == 64 ? launch_format<true, 64>(a, s) : launch_kv_attention_fp8(a, s);
-    else e = a.head_dim == 64 ? launch_format<false, 64>(a, s) : launch_format<false, 128>(a, s);
+    if (a.fp8) return a.head_dim == 64 ? launch_format<true, 64>(a, s) : launch_kv_attention_fp8(a, s);
+    return a.head_dim == 64 ? launch_format<false, 64>(a, s) : launch_format<false, 128>(a, s);
+}
+
+cudaError_t launch_kv_attention(KvAttnArgs &a, void *workspace, cudaStream_t s) {
+    if (a.num_rows == 0) return cudaSuccess;
+    const cudaError_t e = launch_kv_attention_parts(a, workspace, s);
     if (e != cudaSuccess || a.parts_bound == 1) return e;
     const int64_t grid = static_cast<int64_t>(a.num_rows) * a.num_heads;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;

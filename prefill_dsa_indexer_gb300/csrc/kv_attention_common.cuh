@@ -93,6 +93,12 @@ __device__ __forceinline__ int kv_load_group(const KvAttnArgs &a, int row0, int 
     return bad ? 0 : n;
 }
 
+// A row group's entries of the block table, from the first token that its rows read here.
+__device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req, int row0) {
+    const int32_t *table = a.block_table + static_cast<int64_t>(req) * a.bt_stride;
+    return a.row_begin == nullptr ? table : table + (a.row_begin[row0] >> a.page_shift);
+}
+
 // Fills `sched`; every thread of the CTA calls it, then __syncthreads.
 __device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule *sched) {
     if (kv_direct(a)) return;

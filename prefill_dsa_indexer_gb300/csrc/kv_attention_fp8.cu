@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
             bool go = true;
             for (; more && go; more = w.next<NC>(a, lane)) {
                 const int num_pages = (w.t_end + a.page_size - 1) >> a.page_shift;
-                const int32_t *table = a.block_table + static_cast<int64_t>(w.req) * a.bt_stride;
+                const int32_t *table = kv_table(a, w.req, w.row0);
                 auto load_ids = [&](int p) { return p + lane < num_pages ? table[p + lane] : 0; };
                 int batch = w.t_begin >> a.page_shift;  // page ids batch .. batch + 31 are in `ids`, one per lane
                 int32_t ids = load_ids(batch), ids_next = load_ids(batch + 32);
@@ -610,7 +610,8 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
             const Columns<NC> *cs = cols_s + (image & 1);
             image += item->image_last != 0;
             const int t_begin = item->t_begin, t_end = item->t_end, ctx_min = item->ctx_min, ctx_max = item->ctx_max;
-            const int ncols = item->cols, part = item->part, parts = item->parts;
+            const int ncols = item->cols, part = item->part;
+            const bool to_parts = item->parts > 1 || a.keep_parts;  // the output goes to the workspace
             const int tiles = (t_end - t_begin + kTile - 1) / kTile;
 
             float l[kMine];  // a thread's sums of weights, unless they are in TMEM
@@ -910,7 +911,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                 if ((warp & 3) == 0 && mine + n < ncols) {
                     const float b = -nbase[n];
                     const int at = cs->at[mine + n];
-                    if (parts > 1)
+                    if (to_parts)
                         a.part_ml[static_cast<int64_t>(at) * a.parts_bound + part] = make_float2(part_base(b, total), total);
                     else if (a.lse != nullptr)
                         a.lse[at] = total == 0.f ? -INFINITY : (b + log2f(total)) * 0.6931471805599453f;
@@ -934,7 +935,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     add16(h, g);
                 }
                 const int here = ncols - mine - c;
-                if (parts > 1) {  // (so the part has tiles)
+                if (to_parts) {  // (a part without tiles, the only one of its group, is not looked at)
                     float *dst = a.part_o + part * kDim + self;
                     const int64_t row = static_cast<int64_t>(a.parts_bound) * kDim;
 #pragma unroll

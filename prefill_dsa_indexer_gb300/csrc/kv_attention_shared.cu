@@ -1,43 +1,878 @@
 // kv_attention_shared.cu -- attention of a batch whose rows share prefixes (dsa_kv_attention_shared).
 //
-// This form lets every row read all of its tokens by itself (kv_attention.cu): right for every case, and as slow as
-// if nothing were shared.  The segments are checked only.
+//   out[r, h, :] = sum_t softmax_t(sm_scale <q[r,h,:], K_g,t>) V_g,t   over t < row_ctx[r],
+//
+// where the tokens before a segment's S are the same for all of its rows.  The sum is split at S: the shared tokens are
+// read once for all rows of the segment (kv_shared_kernel), each row reads the others by itself (kv_attention.cu, from
+// an offset into its table), and kv_join_kernel adds the parts up by log-sum-exp.  kv_segments_kernel works out S, a
+// multiple of 128, and who does what.  S is at most what every row of the segment that sees any token sees, so no
+// score of a shared token is ever masked, whatever its V holds.
+//
+// A token of a KV head is 4 D bytes in bf16 (2 D in e4m3) and serves N = rows x query heads per KV head columns at
+// 4 D FLOP each: from N = 300 in bf16 (150 in e4m3) on the products take longer than the bytes.  So the columns go on
+// M, the tensor core's 128 rows, twice:
+//
+//   S[128 columns x 128 tokens] = Q K^T     Q and K from shared memory, S in TMEM
+//   P = 2^(S - b)                           a thread a column: it reads its row of S, keeps its base and sum in registers
+//                                           and puts P over S in TMEM, in 16 bits
+//   O[128 columns x D] += P V               P from TMEM, V from shared memory, O in TMEM for the whole item
+//
+// A CTA has two such chains, each with a warpgroup for its softmax, so that one's products run beside the other's
+// exponentials.  An item of more than 128 columns has 128 for each chain, and every tile of K and V serves both; one of
+// fewer has the same columns in both, which then take every other tile.
+//
+// Precision.  bf16 pool: products are exact, P is rounded to bf16 (2^-8 of itself; kv_attention.cu's second term would
+// make the second product, half of all, twice as long).  FP8 pool: q as two e4m3 terms against K's codes as they
+// are, V's codes exactly as fp16 (a third warpgroup converts them) and P rounded to fp16 (2^-11, in steps of 2^-24 with
+// the largest at 2^7 or more).
 #include "kv_attention_common.cuh"
+#include "mla_fp8_common.cuh"
 
 namespace dsa {
 
 namespace {
 
-constexpr int kThreads = 1024;
+using namespace kv;
+using fp8mla::split_pair;
 
-__global__ void __launch_bounds__(kThreads, 1) kv_segments_kernel(const __grid_constant__ KvSegmentArgs a) {
+constexpr int kTile = 128;       // tokens of a tile, and columns of a chain
+constexpr int kSharedCtas = 152;  // an SM each; a constant, so that the split does not go by the device
+
+// A segment's work.
+struct KvSharedSeg {
+    int32_t row0, rows;
+    int32_t tiles;          // of its shared tokens
+    int32_t req;            // whose block table lists them
+    int32_t parts, blocks;  // an item is a (KV head, block of 256 columns, part of the tiles)
+    int32_t entries;        // outputs of a (row, head): one a part, or two where chains share the columns
+    int32_t cost;           // of an item, in tiles of one chain
+    int64_t entry0, cost0;  // before the segment's
+};
+static_assert(sizeof(KvSharedSeg) == 48, "segment layout");
+
+struct KvSharedArgs {
+    KvAttnArgs a;                 // row_ctx: what a row reads itself
+    const int32_t *row_ctx;       // the call's
+    const int32_t *first_row, *shared_ctx;
+    int32_t num_segments;
+    int32_t *own_ctx, *row_begin, *row_seg;  // [R]; row_seg: -1 where nothing is shared
+    KvSharedSeg *seg;             // [num_segments + 1]
+    float *so;                    // [entry][H][D]
+    float2 *sml;                  // [entry][H]
+};
+
+constexpr int32_t kItemTiles = 6;  // what an item costs beside its tiles
+constexpr int32_t kMinTiles = 4;   // of a part
+
+__host__ __device__ __forceinline__ int32_t shared_parts_cap(int32_t units) {
+    return units >= kSharedCtas / 2 ? 2 : kSharedCtas / units;
+}
+
+// ------------------------------------------------------------------ who reads what
+
+constexpr int kSegThreads = 1024;
+
+__global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __grid_constant__ KvSharedArgs s) {
+    const KvAttnArgs &a = s.a;
+    __shared__ int32_t tops[kSegThreads];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hpg = a.num_heads / a.kv_heads;
     pdl_wait();
     pdl_launch_dependents();
+    // every row by itself at first; -1: its group is refused
+    for (int g = threadIdx.x; g < a.num_rows / a.group; g += kSegThreads) {
+        const int row0 = g * a.group;
+        bool bad = false;
+        for (int r = row0; r < row0 + a.group; ++r) bad |= kv_refused(a, s.row_ctx[r], a.row_req[r], a.row_req[row0]);
+        for (int r = row0; r < row0 + a.group; ++r) {
+            s.own_ctx[r] = bad ? -1 : s.row_ctx[r];
+            s.row_begin[r] = 0;
+            s.row_seg[r] = -1;
+        }
+    }
     // a segment begins at or behind every bound before it
-    __shared__ int32_t tops[kThreads];
-    const int per = (a.num_segments + kThreads) / kThreads, lo = min(a.num_segments + 1, static_cast<int>(threadIdx.x) * per);
-    const int hi = min(a.num_segments + 1, lo + per);
+    const int per = (s.num_segments + kSegThreads) / kSegThreads, lo = min(s.num_segments + 1, static_cast<int>(threadIdx.x) * per);
+    const int hi = min(s.num_segments + 1, lo + per);
     int32_t top = INT32_MIN;
-    for (int i = lo; i < hi; ++i) top = max(top, a.first_row[i]);
+    for (int i = lo; i < hi; ++i) top = max(top, s.first_row[i]);
     tops[threadIdx.x] = top;
     __syncthreads();
     top = INT32_MIN;
     for (int t = 0; t < static_cast<int>(threadIdx.x) && lo < hi; ++t) top = max(top, tops[t]);
-    for (int s = lo; s < min(hi, a.num_segments); ++s) {
-        const int32_t first = a.first_row[s], end = a.first_row[s + 1];
-        if (first < 0 || first < top || end < first || end > a.num_rows || first % a.group != 0 || end % a.group != 0 ||
-            a.shared_ctx[s] < 0)
-            report(a.status, DSA_ERR_BOUNDS);
+    for (int i = lo; i < min(hi, s.num_segments); ++i) {
+        const int32_t first = s.first_row[i], end = s.first_row[i + 1];
+        const bool bad = first < 0 || first < top || end < first || end > a.num_rows || first % a.group != 0 ||
+                         end % a.group != 0 || s.shared_ctx[i] < 0;
+        if (bad) report(a.status, DSA_ERR_BOUNDS);
+        KvSharedSeg g = {};
+        g.row0 = bad ? 0 : first;
+        g.rows = bad ? 0 : end - first;
+        s.seg[i] = g;
         top = max(top, first);
     }
+    __syncthreads();
+    // a warp a segment: what all its rows see, and how that is cut
+    for (int i = warp; i < s.num_segments; i += kSegThreads / 32) {
+        KvSharedSeg g = s.seg[i];
+        const int groups = g.rows / a.group;
+        int32_t least = INT32_MAX, lead = INT32_MAX, live = 0;
+        for (int j = lane; j < groups; j += 32) {
+            bool sees = false;
+            for (int r = g.row0 + j * a.group; r < g.row0 + (j + 1) * a.group; ++r) {
+                const int32_t n = s.own_ctx[r];
+                if (n > 0) {
+                    least = min(least, n);
+                    sees = true;
+                }
+            }
+            live += sees;
+            if (sees) lead = min(lead, g.row0 + j * a.group);
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+        lead = __reduce_min_sync(0xffffffffu, lead);
+        live = __reduce_add_sync(0xffffffffu, live);
+        if (live >= 2) g.tiles = min(least, s.shared_ctx[i]) / kTile;
+        if (g.tiles > 0) {
+            const int cols = g.rows * hpg;
+            g.blocks = (cols + 2 * kTile - 1) / (2 * kTile);
+            g.req = a.row_req[lead];
+            const bool narrow = cols - (g.blocks - 1) * 2 * kTile <= kTile;  // the last block is of one chain's columns
+            const int each = g.blocks == 1 && narrow ? 1 : 2;                // tiles of one chain that a tile makes
+            // the parts that end first, if an item a CTA runs at a time; of those that are as good the fewest
+            const int units = a.kv_heads * g.blocks, most = min(shared_parts_cap(units), max(1, g.tiles / kMinTiles));
+            uint64_t best = ~0ull;
+            for (int p = 1 + lane; p <= most; p += 32) {
+                const uint32_t waves = (static_cast<uint32_t>(units) * p + kSharedCtas - 1) / kSharedCtas;
+                const uint64_t t = static_cast<uint64_t>(waves) * ((g.tiles + p - 1) / p * each + kItemTiles);
+                best = min(best, t << 16 | static_cast<uint32_t>(p));
+            }
+            for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+            g.parts = static_cast<int32_t>(best & 0xffff);
+            g.entries = narrow ? 2 * g.parts : g.parts;
+            g.cost = (g.tiles + g.parts - 1) / g.parts * each + kItemTiles;
+            for (int r = g.row0 + lane; r < g.row0 + g.rows; r += 32) {
+                const int32_t n = s.own_ctx[r];
+                s.row_begin[r] = g.tiles * kTile;
+                if (n > 0) {
+                    s.own_ctx[r] = n - g.tiles * kTile;
+                    s.row_seg[r] = i;
+                }
+            }
+        }
+        if (lane == 0) s.seg[i] = g;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    int64_t entry0 = 0, cost0 = 0;
+    for (int i0 = 0; i0 <= s.num_segments; i0 += 32) {
+        const int i = i0 + lane;
+        int64_t entries = 0, cost = 0;
+        if (i < s.num_segments) {
+            const KvSharedSeg &g = s.seg[i];
+            entries = static_cast<int64_t>(g.rows) * g.entries;
+            cost = static_cast<int64_t>(a.kv_heads) * g.blocks * g.parts * g.cost;
+        }
+        int64_t e = entries, c = cost;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, e, o), v = __shfl_up_sync(0xffffffffu, c, o);
+            if (lane >= o) {
+                e += u;
+                c += v;
+            }
+        }
+        if (i <= s.num_segments) {
+            s.seg[i].entry0 = entry0 + e - entries;
+            s.seg[i].cost0 = cost0 + c - cost;
+        }
+        entry0 += __shfl_sync(0xffffffffu, e, 31);
+        cost0 += __shfl_sync(0xffffffffu, c, 31);
+    }
+}
+
+// ------------------------------------------------------------------ the shared tokens
+
+// A CTA's items: those that start within its share of the cost of all.  Warp-collective.
+struct SharedCursor {
+    KvSharedSeg g;
+    int s, i, items;        // segment, item of it
+    int64_t at, end;        // cost before the item; where this CTA's share ends
+    int head, part, block;  // KV head
+    int t0, tiles;          // first tile, and how many
+    bool wide;              // a chain each for the two halves of the columns
+
+    __device__ __forceinline__ bool place(const KvSharedArgs &a) {
+        if (at >= end) return false;
+        const int per = g.parts * g.blocks;
+        head = i / per;
+        const int rest = i - head * per;
+        block = rest / g.parts;
+        part = rest - block * g.parts;
+        t0 = static_cast<int>(static_cast<int64_t>(part) * g.tiles / g.parts);
+        tiles = static_cast<int>(static_cast<int64_t>(part + 1) * g.tiles / g.parts) - t0;
+        wide = g.rows * a.a.hpg - block * 2 * kTile > kTile;
+        return true;
+    }
+    __device__ __forceinline__ void load(const KvSharedArgs &a) {
+        g = a.seg[s];
+        items = a.a.kv_heads * g.blocks * g.parts;
+    }
+    __device__ __forceinline__ bool first(const KvSharedArgs &a, int lane) {
+        const int64_t total = a.seg[a.num_segments].cost0;
+        const int64_t from = total * blockIdx.x / gridDim.x;
+        end = total * (blockIdx.x + 1) / gridDim.x;
+        if (from >= end) return false;
+        s = 0;  // the segment that `from` lies in
+        for (int s0 = 0; s0 < a.num_segments; s0 += 32) {
+            const bool before = s0 + lane < a.num_segments && a.seg[s0 + lane + 1].cost0 <= from;
+            const int n = __popc(__ballot_sync(0xffffffffu, before));
+            s += n;
+            if (n < 32) break;
+        }
+        load(a);
+        i = static_cast<int>((from - g.cost0 + g.cost - 1) / g.cost);
+        at = g.cost0 + static_cast<int64_t>(i) * g.cost;
+        if (i >= items) return skip(a);
+        return place(a);
+    }
+    __device__ __forceinline__ bool skip(const KvSharedArgs &a) {  // to the next segment's first item
+        i = 0;
+        do {
+            if (++s >= a.num_segments) return false;
+            load(a);
+        } while (items == 0);
+        at = g.cost0;
+        return place(a);
+    }
+    __device__ __forceinline__ bool next(const KvSharedArgs &a) {
+        at += g.cost;
+        if (++i >= items) return at < end && skip(a);
+        return place(a);
+    }
+    // steps of a chain: every tile, or every other one
+    __device__ __forceinline__ int steps(int chain) const { return wide ? tiles : (tiles + 1 - chain) / 2; }
+};
+
+template <bool kFp8, int D>
+struct SharedCfg {
+    static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
+    static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;
+    static constexpr int kBoxes = kRowBytes / kBoxBytes;
+    static constexpr int kPlane = kTile * kBoxBytes;                  // one box column of a tile
+    static constexpr int kSlotBytes = kTile * kRowBytes;              // K or V of a tile as stored
+    static constexpr int kQBytes = kTile * D * 2;                     // a chain's columns, in bf16 or as two e4m3 terms
+    static constexpr int kVBytes = kFp8 ? kTile * D * 2 : 0;          // V of a tile in fp16
+    static constexpr int kVBufs = kFp8 ? 2 : 0;
+    // K and V alternate in one ring.  (FP8: an even number, so that a slot is K's or V's for good)
+    static constexpr int kSlots = (229376 - 2 * kQBytes - kVBufs * kVBytes) / kSlotBytes > 12
+                                      ? 12
+                                      : (229376 - 2 * kQBytes - kVBufs * kVBytes) / kSlotBytes;
+    static_assert(kSlots >= 4 && (!kFp8 || kSlots % 2 == 0), "ring");
+    static constexpr int kWarpgroups = kFp8 ? 4 : 3;  // two of softmax, (one that converts V,) the producer and the issuer
+    static constexpr int kThreads = 128 * kWarpgroups;
+    // Registers a thread: at launch, then the softmax warpgroups take some of the others'.
+    static constexpr int kLaunchRegs = kFp8 ? 128 : 168;
+    static constexpr int kSoftmaxRegs = kFp8 ? 184 : 208, kOtherRegs = kFp8 ? 72 : 88;
+    static_assert(2 * kSoftmaxRegs + (kWarpgroups - 2) * kOtherRegs == kWarpgroups * kLaunchRegs, "register split");
+    static constexpr uint32_t kTmemO = 2 * kTile;  // the chains' scores, then their outputs
+    static constexpr int OFF_V = 2 * kQBytes;
+    static constexpr int OFF_RING = OFF_V + kVBufs * kVBytes;
+    static constexpr int OFF_BARS = OFF_RING + kSlots * kSlotBytes;
+    static constexpr int kNumBars = 2 * kSlots + 2 + 1 + 2 + 2 + 2 + 2 * 2 + 1;
+    static constexpr int OFF_MISC = OFF_BARS + kNumBars * 8;
+    static constexpr int kSmemBytes = OFF_MISC + 16 + 1024;
+    static_assert(kSmemBytes <= 232448, "shared memory");
+    // FP16 weights reach 2^15 and a moved base leaves the largest at 2^7; bf16's range does not ask for a move
+    static constexpr float kHeadroom = kFp8 ? 15.0f : 40.0f, kBias = kFp8 ? 7.0f : 0.0f;
+};
+
+// A thread's column of queries into a chain's image: bf16 as it is, 64 dims to a 128-byte row.
+template <int D>
+__device__ __forceinline__ void put_query_bf16(uint8_t *img, const uint16_t *src, int n) {
+#pragma unroll
+    for (int u = 0; u < D / 8; ++u) {
+        const uint4 v = src == nullptr ? make_uint4(0u, 0u, 0u, 0u) : reinterpret_cast<const uint4 *>(src)[u];
+        *reinterpret_cast<uint4 *>(img + (u >> 3) * (kTile * 128) + fp8mla::sw128(n, u & 7)) = v;
+    }
+}
+
+// The exponent of 2 that brings a column's largest |q| to (224, 448]; finite: there is nothing but numbers in it.
+template <int D>
+__device__ __forceinline__ int query_exponent(const uint16_t *src, bool &finite) {
+    uint32_t top = 0;
+    if (src != nullptr) {
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u) {
+            const uint4 v = reinterpret_cast<const uint4 *>(src)[u];
+            const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) top = max(top, max(h[y] << 16 & 0x7fff0000u, h[y] & 0x7fff0000u));
+        }
+    }
+    finite = top < 0x7f800000u;
+    if (top == 0 || !finite) return 0;
+    const int e = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return max(-120, min(120, e));
+}
+
+// The column's values times 2^e as e4m3 hi and lo terms.
+template <int D>
+__device__ __forceinline__ void put_query_fp8(uint8_t *img, const uint16_t *src, int n, int e) {
+    const uint4 *q = reinterpret_cast<const uint4 *>(src);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll 2
+    for (int u = 0; u < D / 16; ++u) {
+        uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+        if (src != nullptr) {
+            const uint4 v0 = q[2 * u], v1 = q[2 * u + 1];
+            const uint32_t h[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const uint2 p0 = split_pair(bf16_lo(h[2 * y]) * up, bf16_hi(h[2 * y]) * up);
+                const uint2 p1 = split_pair(bf16_lo(h[2 * y + 1]) * up, bf16_hi(h[2 * y + 1]) * up);
+                hi[y] = p0.x | (p1.x << 16);
+                lo[y] = p0.y | (p1.y << 16);
+            }
+        }
+        const uint32_t at = D == 128 ? fp8mla::sw128(n, u) : static_cast<uint32_t>(n * 64 + ((u ^ (n >> 1 & 3)) << 4));
+        *reinterpret_cast<uint4 *>(img + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(img + kTile * D + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+}
+
+// Four e4m3 codes as two fp16 pairs (exact).
+__device__ __forceinline__ void codes_to_f16(uint32_t v, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
+}
+
+template <bool kFp8, int D>
+__global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
+    kv_shared_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ KvSharedArgs s) {
+    using C = SharedCfg<kFp8, D>;
+    constexpr int NS = C::kSlots;
+    const KvAttnArgs &a = s.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BARS);  // [NS] K or V landed
+    uint64_t *empty = full + NS;                                        // [NS] it has been used
+    uint64_t *q_full = empty + NS;                                      // [2] a chain's queries are in place
+    uint64_t *q_empty = q_full + 2;                                     // the item's scores are done
+    uint64_t *s_full = q_empty + 1;                                     // [2] a chain's scores in TMEM
+    uint64_t *p_full = s_full + 2;                                      // [2] its weights in their place
+    uint64_t *o_full = p_full + 2;                                      // [2] its item's output is done
+    uint64_t *v_full = o_full + 2;                                      // [2] V in fp16
+    uint64_t *v_empty = v_full + 2;                                     // [2] and its product done
+    uint64_t *drained = v_empty + 2;                                    // after a wait gave up: no MMA is left
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
+    constexpr int kProducer = 4 * (C::kWarpgroups - 1), kIssuer = kProducer + 1;
+    if (threadIdx.x == 0) {
+        *abort = 0;
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kFp8 && (i & 1) ? 4 : 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 4);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_full[i], 1);
+            mbar_init(&v_full[i], 4);
+            mbar_init(&v_empty[i], 1);
+        }
+        mbar_init(q_empty, 1);
+        mbar_init(drained, 1);
+        fence_mbar_init();
+        prefetch_tensormap(&kv_map);
+    }
+    if (warp == kIssuer) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    SharedCursor w;
+    bool more = w.first(s, lane);
+
+    if (wg >= 2) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+        if (kFp8 && wg == 2) {
+            // ---- V's codes as fp16: thread = token
+            const int t = threadIdx.x & 127;
+            uint32_t n = 0;  // tiles
+            bool ok = true;
+            for (; more && ok; more = w.next(s)) {
+                for (int i = 0; i < w.tiles && ok; ++i, ++n) {
+                    const uint32_t turn = 2 * n + 1, slot = turn % NS, buf = n & 1;
+                    ok = wait_mbar_warp(&full[slot], turn / NS & 1, abort) &&
+                         wait_mbar_warp(&v_empty[buf], (n >> 1 & 1) ^ 1, abort);
+                    if (!ok) break;
+                    const uint8_t *from = smem + C::OFF_RING + slot * C::kSlotBytes;
+                    uint8_t *to = smem + C::OFF_V + buf * C::kVBytes;
+#pragma unroll
+                    for (int u = 0; u < D / 16; ++u) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(
+                            from + (D == 128 ? fp8mla::sw128(t, u) : static_cast<uint32_t>(t * 64 + ((u ^ (t >> 1 & 3)) << 4))));
+                        uint4 x, y;
+                        codes_to_f16(v.x, x.x, x.y);
+                        codes_to_f16(v.y, x.z, x.w);
+                        codes_to_f16(v.z, y.x, y.y);
+                        codes_to_f16(v.w, y.z, y.w);
+                        uint8_t *plane = to + (u >> 2) * (kTile * 128);
+                        *reinterpret_cast<uint4 *>(plane + fp8mla::sw128(t, 2 * u & 7)) = x;
+                        *reinterpret_cast<uint4 *>(plane + fp8mla::sw128(t, (2 * u & 7) + 1)) = y;
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&v_full[buf]);
+                        mbar_arrive(&empty[slot]);
+                    }
+                }
+            }
+            if (!ok) gave_up(abort, a.status);
+        } else if (warp == kProducer) {
+            // ---- K and V: a tile is `boxes` runs of tokens by kBoxes columns, one a lane
+            const int box_rows = a.page_size, boxes = kTile >> a.page_shift;
+            const int b = lane / C::kBoxes, x = lane % C::kBoxes;
+            uint32_t turn = 0;  // slots filled
+            bool go = true;
+            for (; more && go; more = w.next(s)) {
+                const int32_t *table = a.block_table + static_cast<int64_t>(w.g.req) * a.bt_stride;
+                const int page0 = w.t0 << 7 >> a.page_shift, pages = w.tiles << 7 >> a.page_shift;
+                auto load_ids = [&](int p) { return p + lane < pages ? table[page0 + p + lane] : 0; };
+                int batch = 0;  // page ids batch .. batch + 31 of the item are in `ids`, one per lane
+                int32_t ids = load_ids(0), ids_next = load_ids(32);
+                for (int i = 0; i < w.tiles && go; ++i) {
+                    const int p = i << 7 >> a.page_shift;
+                    if (p >= batch + 32) {
+                        batch += 32;
+                        ids = ids_next;
+                        ids_next = load_ids(batch + 32);
+                    }
+                    int32_t id = __shfl_sync(0xffffffffu, ids, (p + min(b, boxes - 1) - batch) & 31);
+                    if (b < boxes && (id < 0 || id >= a.num_pages)) {
+                        report(a.status, DSA_ERR_BOUNDS);
+                        id = 0;
+                    }
+                    const int y = (id * a.kv_heads + w.head) * 2 * a.page_size;
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v, ++turn) {  // K, then V
+                        const uint32_t slot = turn % NS;
+                        if (!wait_mbar_warp(&empty[slot], (turn / NS & 1) ^ 1, abort)) {
+                            gave_up(abort, a.status);
+                            go = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&full[slot], C::kSlotBytes);
+                        __syncwarp();
+                        if (b < boxes)
+                            tma_load_2d(smem + C::OFF_RING + slot * C::kSlotBytes + x * C::kPlane + b * box_rows * C::kBoxBytes,
+                                        &kv_map, &full[slot], x * C::kBoxBytes, y + v * a.page_size);
+                    }
+                }
+            }
+            if (*abort && lane == 0) {  // leave no copy in flight behind
+                for (uint32_t i = turn > NS ? turn - NS : 0; i < turn; ++i) {
+                    const long long t0 = clock64();
+                    while (!mbar_try_wait(&full[i % NS], i / NS & 1) && clock64() - t0 < kWaitTimeoutCycles) {
+                    }
+                }
+            }
+        } else if (warp == kIssuer && lane == 0) {
+            // ---- the products of both chains.  MMAs run in the order of their issue: a chain's next scores, which take
+            // the place of its weights, are right behind the product that reads those
+            constexpr uint32_t kIdescS = make_idesc(kTile, kTile, kFp8 ? 0 : 1, kFp8 ? 0 : 1, false, false);
+            constexpr uint32_t kIdescO = make_idesc(kTile, D, kFp8 ? 0 : 1, kFp8 ? 0 : 1, false, true);
+            const uint32_t base = smem_u32(smem), ring = base + C::OFF_RING;
+            uint32_t n = 0, items = 0;             // tiles before the item, items
+            uint32_t s_count[2] = {0, 0}, p_count[2] = {0, 0};
+            bool ok = true;
+            for (; more && ok; more = w.next(s), ++items) {
+                const int most = w.steps(0);
+                auto tile_of = [&](int chain, int j) { return n + static_cast<uint32_t>(w.wide ? j : 2 * j + chain); };
+                auto scores = [&](int c, int j) {
+                    const uint32_t turn = 2 * tile_of(c, j), slot = turn % NS;
+                    ok = ok && wait_mbar(&full[slot], turn / NS & 1, abort);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t q = base + (w.wide ? c : 0) * C::kQBytes, k = ring + slot * C::kSlotBytes;
+                    const uint32_t d = tmem + c * kTile;
+                    if constexpr (kFp8) {
+#pragma unroll
+                        for (int term = 0; term < 2; ++term)
+#pragma unroll
+                            for (int i = 0; i < D / 32; ++i) {
+                                const uint32_t qa = q + term * (kTile * D) + i * 32, ka = k + i * 32;
+                                mma_f8(d, D == 128 ? sdesc_sw128(qa, 16, 1024) : sdesc_sw64(qa),
+                                       D == 128 ? sdesc_sw128(ka, 16, 1024) : sdesc_sw64(ka), kIdescS, term + i > 0);
+                            }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            const uint32_t off = (i >> 2) * (kTile * 128) + (i & 3) * 32;
+                            mma_f16(d, sdesc_sw128(q + off, 16, 1024), sdesc_sw128(k + off, 16, 1024), kIdescS, i > 0);
+                        }
+                    }
+                    mma_commit(&s_full[c]);
+                    if (!w.wide || c == 1) mma_commit(&empty[slot]);
+                    ++s_count[c];
+                };
+                ok = wait_mbar(&q_full[0], items & 1, abort) && wait_mbar(&q_full[1], items & 1, abort);
+                if (!ok) break;
+                scores(0, 0);
+                if (w.steps(1) > 0) scores(1, 0);
+                for (int j = 0; j < most && ok; ++j) {
+#pragma unroll 1
+                    for (int c = 0; c < 2 && ok; ++c) {
+                        const int steps = w.steps(c);
+                        if (j >= steps) break;
+                        const uint32_t tile = tile_of(c, j), turn = 2 * tile + 1, slot = turn % NS, buf = tile & 1;
+                        ok = wait_mbar(&p_full[c], p_count[c] & 1, abort) &&
+                             (kFp8 ? wait_mbar(&v_full[buf], tile >> 1 & 1, abort)
+                                   : wait_mbar(&full[slot], turn / NS & 1, abort));
+                        if (!ok) break;
+                        ++p_count[c];
+                        tc_fence_after();
+                        const uint32_t v = kFp8 ? base + C::OFF_V + buf * C::kVBytes : ring + slot * C::kSlotBytes;
+                        const uint32_t d = tmem + C::kTmemO + c * D, p = tmem + c * kTile;
+#pragma unroll
+                        for (int i = 0; i < kTile / 16; ++i)
+                            mma_f16_ts(d, p + i * 8, sdesc_sw128(v + i * 2048, kTile * 128, 1024), kIdescO, j + i > 0);
+                        if (!w.wide || c == 1) mma_commit(kFp8 ? &v_empty[buf] : &empty[slot]);
+                        if (j == steps - 1) mma_commit(&o_full[c]);
+                        else scores(c, j + 1);
+                    }
+                }
+                mma_commit(q_empty);
+                n += static_cast<uint32_t>(w.tiles);
+            }
+            if (!ok) gave_up(abort, a.status);
+            if (*abort) {  // leave no MMA in flight behind
+                mma_commit(drained);
+                const long long t0 = clock64();
+                while (!mbar_try_wait(drained, 0) && clock64() - t0 < kWaitTimeoutCycles) {
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+        // ---- softmax of chain wg: thread = column
+        const int self = threadIdx.x & 127, c = wg;
+        const uint32_t quad = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t st = quad + c * kTile, ot = quad + C::kTmemO + c * D;
+        uint32_t s_count = 0, items = 0, outs = 0;
+        bool ok = true;
+        for (; more && ok; more = w.next(s), ++items) {
+            const int hpg = a.hpg, col = w.block * 2 * kTile + (w.wide ? c * kTile : 0) + self;
+            const bool real = col < w.g.rows * hpg;
+            const int row = col / hpg, head = w.head * hpg + col - row * hpg;
+            ok = wait_mbar_warp(q_empty, (items & 1) ^ 1, abort);
+            if (!ok) break;
+            const uint16_t *src = real ? a.q + (w.g.row0 + row) * a.q_stride + static_cast<int64_t>(head) * D : nullptr;
+            const bool puts = w.wide || c == 0;  // (one image serves two chains of the same columns)
+            uint8_t *img = smem + c * C::kQBytes;
+            float scale = a.s_scale;
+            bool finite = true;
+            if constexpr (kFp8) {
+                const int e = query_exponent<D>(src, finite);
+                if (puts) put_query_fp8<D>(img, src, self, e);
+                scale *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            } else if (puts) {
+                put_query_bf16<D>(img, src, self);
+            }
+            // a score of -inf times the scale: neither zero nor infinity.  Over codes no number in q makes no score
+            scale = finite ? fminf(fmaxf(scale, 1.17549435e-38f), 3.40282347e38f) : __uint_as_float(0x7fc00000u);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[c]);
+            const int steps = w.steps(c);
+            float base = -INFINITY;
+            float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+            for (int j = 0; j < steps; ++j, ++s_count) {
+                ok = wait_mbar_warp(&s_full[c], s_count & 1, abort);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t h[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld32(st + 32 * i, h[i]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) reg_fence(h[i]);
+                float top[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    top[i] = __uint_as_float(h[i][0]);
+#pragma unroll
+                    for (int k = 1; k < 32; ++k) top[i] = fmaxf(top[i], __uint_as_float(h[i][k]));
+                }
+                const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;  // (a positive factor)
+                const bool moves = most > base + C::kHeadroom;
+                if (__any_sync(0xffffffffu, moves)) {
+                    // (this tile's scores are done, so the products before them are: O is at rest)
+                    const float f = moves ? ex2(base - (most - C::kBias)) : 1.f;
+                    if (moves) base = most - C::kBias;
+                    sum0.x *= f;
+                    sum0.y *= f;
+                    sum1.x *= f;
+                    sum1.y *= f;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int i = 0; i < D; i += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(ot + i, o);
+                            tmem_ld_wait();
+                            reg_fence(o);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st16(ot + i, o);
+                        }
+                    }
+                }
+                const float nb = base == -INFINITY ? 0.f : -base;
+                const float2 sc2 = make_float2(scale, scale), nb2 = make_float2(nb, nb);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        float2 x = __ffma2_rn(make_float2(__uint_as_float(h[i][k]), __uint_as_float(h[i][k + 1])), sc2, nb2);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        if (k & 2) sum1 = __fadd2_rn(sum1, x);
+                        else sum0 = __fadd2_rn(sum0, x);
+                        p[k / 2] = kFp8 ? pack_f16(x.x, x.y) : pack_bf16(x.x, x.y);
+                    }
+                    tmem_st16(st + 16 * i, p);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[c]);
+            }
+            if (!ok) break;
+            // ---- the item's output: a column's D numbers in a row
+            const float total = (sum0.x + sum1.x) + (sum0.y + sum1.y);
+            const int64_t entry = w.g.entry0 + static_cast<int64_t>(row) * w.g.entries + (w.wide ? w.part : 2 * w.part + c);
+            const int64_t at = entry * a.num_heads + head;
+            if (real) s.sml[at] = make_float2(part_base(base, total), total);
+            if (steps > 0) {
+                ok = wait_mbar_warp(&o_full[c], outs & 1, abort);
+                if (!ok) break;
+                ++outs;
+                tc_fence_after();
+                float4 *dst = reinterpret_cast<float4 *>(s.so + at * D);
+#pragma unroll 1
+                for (int i = 0; i < D; i += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(ot + i, o);
+                    tmem_ld_wait();
+                    reg_fence(o);
+                    if (real) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            dst[(i + k) / 4] = make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
+                                                           __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3]));
+                    }
+                }
+                tc_fence_before();
+            } else if (real) {  // (no tile for the second chain)
+                float4 *dst = reinterpret_cast<float4 *>(s.so + at * D);
+                for (int i = 0; i < D / 4; ++i) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+        if (!ok) gave_up(abort, a.status);
+    }
+    __syncthreads();
+    if (warp == kIssuer) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ the parts of a (row, head)
+
+// As kv_combine_kernel, over a row's own parts and then the shared ones.
+constexpr int kJoinThreads = 128, kJoinParts = 128 + 2 * kSharedCtas;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ KvSharedArgs s) {
+    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+    __shared__ float2 ml_s[kJoinParts];
+    __shared__ float4 x_s[kGroups][kLanes];
+    __shared__ float t_s[kGroups];
+    const KvAttnArgs &a = s.a;
+    // The kernel before lets this one start after its own wait, so what ran before it is complete: what is not of its
+    // making can be read before the wait
+    const int64_t at = blockIdx.x;
+    const int row = static_cast<int>(at / a.num_heads), head = static_cast<int>(at - static_cast<int64_t>(row) * a.num_heads);
+    int req;
+    bool bad;
+    const int my_ctx = kv_load_group(a, row / a.group * a.group, threadIdx.x & 31, req, bad);
+    const int ctx = __reduce_max_sync(0xffffffffu, my_ctx);
+    const int own = ctx > 0 ? kv_parts(ctx, kv_part_shift(ctx, a.parts_shift)) : 0;
+    int parts = own;
+    int64_t entry = 0;  // the first shared part
+    const int32_t seg = s.row_seg[row];
+    if (seg >= 0) {
+        const KvSharedSeg g = s.seg[seg];
+        const int r = row - g.row0, block = (r * a.hpg + head % a.hpg) / (2 * kTile);
+        const bool wide = g.rows * a.hpg - block * 2 * kTile > kTile;
+        parts += wide ? g.parts : 2 * g.parts;
+        entry = g.entry0 + static_cast<int64_t>(r) * g.entries;
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes;
+    const float4 *po = reinterpret_cast<const float4 *>(a.part_o + at * a.parts_bound * D) + d;
+    const float4 *so = reinterpret_cast<const float4 *>(s.so + (entry * a.num_heads + head) * D) + d;
+    const int64_t so_step = static_cast<int64_t>(a.num_heads) * kLanes;
+    auto part_at = [&](int p) { return p < own ? po[static_cast<int64_t>(p) * kLanes] : so[(p - own) * so_step]; };
+    // the first parts' outputs are on their way while the bases are compared
+    constexpr int kAhead = 8;
+    float4 y[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int p = grp + i * kGroups;
+        if (p < parts) y[i] = part_at(p);
+    }
+    for (int p = threadIdx.x; p < parts; p += kJoinThreads)
+        ml_s[p] = p < own ? a.part_ml[at * a.parts_bound + p] : s.sml[(entry + p - own) * a.num_heads + head];
+    __syncthreads();
+    float b = -INFINITY;
+    for (int p = threadIdx.x & 31; p < parts; p += 32) b = fmaxf(b, ml_s[p].x);
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, i));
+    const float b0 = b == -INFINITY ? 0.f : b;
+    float total = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](int p, const float4 &v) {
+        const float2 l = ml_s[p];
+        const float f = ex2(l.x - b0);
+        total += l.y * f;
+        x.x += v.x * f;
+        x.y += v.y * f;
+        x.z += v.z * f;
+        x.w += v.w * f;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (grp + i * kGroups < parts) add(grp + i * kGroups, y[i]);
+#pragma unroll 4
+    for (int p = grp + kAhead * kGroups; p < parts; p += kGroups) add(p, part_at(p));
+    x_s[grp][d] = x;
+    if (d == 0) t_s[grp] = total;
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
+        const float4 v = x_s[i][d];
+        x.x += v.x;
+        x.y += v.y;
+        x.z += v.z;
+        x.w += v.w;
+        total += t_s[i];
+    }
+    const bool none = total == 0.f;
+    const float inv = none ? 0.f : a.v_scale / total;
+    *reinterpret_cast<uint2 *>(a.out + at * D + 4 * d) =
+        none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+    if (d == 0 && a.lse != nullptr) a.lse[at] = none ? -INFINITY : (b0 + log2f(total)) * 0.6931471805599453f;
+}
+
+// ------------------------------------------------------------------ launches
+
+template <bool kFp8, int D>
+cudaError_t launch_shared(const KvSharedArgs &s, cudaStream_t stream) {
+    using C = SharedCfg<kFp8, D>;
+    auto kern = kv_shared_kernel<kFp8, D>;
+    static std::atomic<uint64_t> configured{0};
+    cudaError_t e = raise_smem_limit(kern, C::kSmemBytes, configured);
+    if (e != cudaSuccess) return e;
+    // the register split waits forever in a CTA launched with fewer
+    static std::atomic<int> regs{0};
+    if (regs.load() == 0) {
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, kern);
+        if (e != cudaSuccess) return e;
+        regs.store(fa.numRegs);
+    }
+    if (regs.load() < C::kLaunchRegs) return cudaErrorInvalidConfiguration;
+    CUtensorMap map;
+    if (!encode_kv_rows_map(&map, s.a.pool, s.a.pool_rows, C::kRowBytes, s.a.page_size)) return cudaErrorInvalidValue;
+    return launch_pdl(kern, dim3(kSharedCtas), dim3(C::kThreads), C::kSmemBytes, stream, map, s);
+}
+
+// Shared parts of all (row, head) at most, divided by the heads.  With at least rows x heads / 256 items a part,
+// shared_parts_cap leaves a segment 4 parts a row or 2 x 152 x 256 / heads in all.
+size_t shared_entries(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t max_ctx, int32_t num_segments) {
+    const int64_t tiles = max_ctx / kTile, most = tiles / kMinTiles > 1 ? tiles / kMinTiles : 1;
+    const int64_t cap = shared_parts_cap(kv_heads) < most ? shared_parts_cap(kv_heads) : most;
+    const int64_t by_row = num_rows * 2 * cap;
+    const int64_t by_segment = 4 * num_rows + num_segments * (2ll * kSharedCtas * 2 * kTile / num_heads + 1);
+    return static_cast<size_t>(by_row < by_segment ? by_row : by_segment);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, void *workspace, cudaStream_t s) {
+size_t kv_attention_shared_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
+                                           int32_t max_ctx, int32_t num_segments) {
+    const size_t entries = shared_entries(num_rows, num_heads, kv_heads, max_ctx, num_segments) * static_cast<size_t>(num_heads);
+    return kv_attention_workspace_bytes(num_rows, num_heads, kv_heads, head_dim, max_ctx, true) +
+           3 * align256(static_cast<size_t>(num_rows) * 4) +
+           align256((static_cast<size_t>(num_segments) + 1) * sizeof(KvSharedSeg)) +
+           align256(entries * static_cast<size_t>(head_dim) * 4) + align256(entries * 8);
+}
+
+cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, void *workspace, cudaStream_t stream) {
     if (a.num_rows == 0) return cudaSuccess;
-    const cudaError_t e = launch_pdl(kv_segments_kernel, dim3(1), dim3(kThreads), 0, s, seg);
-    return e != cudaSuccess ? e : launch_kv_attention(a, workspace, s);
+    KvSharedArgs s = {};
+    s.first_row = seg.first_row;
+    s.shared_ctx = seg.shared_ctx;
+    s.num_segments = seg.num_segments;
+    s.row_ctx = a.row_ctx;
+    const size_t rows = align256(static_cast<size_t>(a.num_rows) * 4);
+    uint8_t *at = static_cast<uint8_t *>(workspace) +
+                  kv_attention_workspace_bytes(a.num_rows, a.num_heads, a.kv_heads, a.head_dim, a.max_ctx, true);
+    const auto take = [&](size_t bytes) {
+        uint8_t *p = at;
+        at += bytes;
+        return p;
+    };
+    s.own_ctx = reinterpret_cast<int32_t *>(take(rows));
+    s.row_begin = reinterpret_cast<int32_t *>(take(rows));
+    s.row_seg = reinterpret_cast<int32_t *>(take(rows));
+    s.seg = reinterpret_cast<KvSharedSeg *>(take(align256((static_cast<size_t>(seg.num_segments) + 1) * sizeof(KvSharedSeg))));
+    const size_t entries = shared_entries(a.num_rows, a.num_heads, a.kv_heads, a.max_ctx, seg.num_segments) *
+                           static_cast<size_t>(a.num_heads);
+    s.so = reinterpret_cast<float *>(take(align256(entries * static_cast<size_t>(a.head_dim) * 4)));
+    s.sml = reinterpret_cast<float2 *>(take(align256(entries * 8)));
+    s.a = a;
+    cudaError_t e = launch_pdl(kv_segments_kernel, dim3(1), dim3(kSegThreads), 0, stream, s);
+    if (e != cudaSuccess) return e;
+    a.row_ctx = s.own_ctx;
+    a.row_begin = s.row_begin;
+    a.keep_parts = true;
+    e = launch_kv_attention_parts(a, workspace, stream);
+    if (e != cudaSuccess) return e;
+    s.a = a;
+    if (a.fp8) e = a.head_dim == 64 ? launch_shared<true, 64>(s, stream) : launch_shared<true, 128>(s, stream);
+    else e = a.head_dim == 64 ? launch_shared<false, 64>(s, stream) : launch_shared<false, 128>(s, stream);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = static_cast<int64_t>(a.num_rows) * a.num_heads;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const dim3 gr(static_cast<unsigned>(grid)), b(kJoinThreads);
+    return a.head_dim == 64 ? launch_pdl(kv_join_kernel<64>, gr, b, 0, stream, s)
+                            : launch_pdl(kv_join_kernel<128>, gr, b, 0, stream, s);
 }
 
 }  // namespace dsa
