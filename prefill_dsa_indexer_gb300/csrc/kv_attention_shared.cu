@@ -50,13 +50,20 @@ struct KvSharedSeg {
 };
 static_assert(sizeof(KvSharedSeg) == 48, "segment layout");
 
+// Where a CTA begins, and the cost at which its share of all ends.
+struct KvSharedCta {
+    int32_t seg, item;  // seg -1: nothing to do
+    int64_t end;
+};
+
 struct KvSharedArgs {
     KvAttnArgs a;                 // row_ctx: what a row reads itself
     const int32_t *row_ctx;       // the call's
     const int32_t *first_row, *shared_ctx;
     int32_t num_segments;
     int32_t *own_ctx, *row_begin, *row_seg;  // [R]; row_seg: -1 where nothing is shared
-    KvSharedSeg *seg;             // [num_segments + 1]
+    KvSharedSeg *seg;             // [num_segments]
+    KvSharedCta *cta;             // [kSharedCtas]
     float *so;                    // [entry][H][D]
     float2 *sml;                  // [entry][H]
 };
@@ -64,8 +71,10 @@ struct KvSharedArgs {
 constexpr int32_t kItemTiles = 6;  // what an item costs beside its tiles
 constexpr int32_t kMinTiles = 4;   // of a part
 
+// Parts of a segment with so many items a part: an item a CTA where that is possible, else few enough that their
+// outputs stay small beside the products, and enough to fill the last round of CTAs.
 __host__ __device__ __forceinline__ int32_t shared_parts_cap(int32_t units) {
-    return units >= kSharedCtas / 2 ? 2 : kSharedCtas / units;
+    return units <= kSharedCtas / 8 ? kSharedCtas / units : units <= kSharedCtas ? 8 : units <= 4 * kSharedCtas ? 4 : 2;
 }
 
 // ------------------------------------------------------------------ who reads what
@@ -142,7 +151,8 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
             uint64_t best = ~0ull;
             for (int p = 1 + lane; p <= most; p += 32) {
                 const uint32_t waves = (static_cast<uint32_t>(units) * p + kSharedCtas - 1) / kSharedCtas;
-                const uint64_t t = static_cast<uint64_t>(waves) * ((g.tiles + p - 1) / p * each + kItemTiles);
+                const uint64_t t = static_cast<uint64_t>(waves) * ((g.tiles + p - 1) / p * each + kItemTiles) +
+                                   (static_cast<uint64_t>(g.rows) * a.num_heads * a.head_dim * p >> 18);  // and the join
                 best = min(best, t << 16 | static_cast<uint32_t>(p));
             }
             for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
@@ -161,36 +171,64 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
         if (lane == 0) s.seg[i] = g;
     }
     __syncthreads();
-    if (warp != 0) return;
-    int64_t entry0 = 0, cost0 = 0;
-    for (int i0 = 0; i0 <= s.num_segments; i0 += 32) {
-        const int i = i0 + lane;
-        int64_t entries = 0, cost = 0;
-        if (i < s.num_segments) {
-            const KvSharedSeg &g = s.seg[i];
-            entries = static_cast<int64_t>(g.rows) * g.entries;
-            cost = static_cast<int64_t>(a.kv_heads) * g.blocks * g.parts * g.cost;
-        }
-        int64_t e = entries, c = cost;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, e, o), v = __shfl_up_sync(0xffffffffu, c, o);
-            if (lane >= o) {
-                e += u;
-                c += v;
+    __shared__ int64_t total_s;
+    if (warp == 0) {
+        int64_t entry0 = 0, cost0 = 0;
+        for (int i0 = 0; i0 < s.num_segments; i0 += 32) {
+            const int i = i0 + lane;
+            int64_t entries = 0, cost = 0;
+            if (i < s.num_segments) {
+                const KvSharedSeg &g = s.seg[i];
+                entries = static_cast<int64_t>(g.rows) * g.entries;
+                cost = static_cast<int64_t>(a.kv_heads) * g.blocks * g.parts * g.cost;
             }
+            int64_t e = entries, c = cost;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, e, o), v = __shfl_up_sync(0xffffffffu, c, o);
+                if (lane >= o) {
+                    e += u;
+                    c += v;
+                }
+            }
+            if (i < s.num_segments) {
+                s.seg[i].entry0 = entry0 + e - entries;
+                s.seg[i].cost0 = cost0 + c - cost;
+            }
+            entry0 += __shfl_sync(0xffffffffu, e, 31);
+            cost0 += __shfl_sync(0xffffffffu, c, 31);
         }
-        if (i <= s.num_segments) {
-            s.seg[i].entry0 = entry0 + e - entries;
-            s.seg[i].cost0 = cost0 + c - cost;
+        if (lane == 0) total_s = cost0;
+    }
+    __syncthreads();
+    // a CTA takes the items that start within its share of the cost
+    if (threadIdx.x < kSharedCtas) {
+        const int64_t from = total_s * threadIdx.x / kSharedCtas;
+        KvSharedCta w = {-1, 0, total_s * (threadIdx.x + 1) / kSharedCtas};
+        int lo = 0, hi = s.num_segments;  // the last segment that begins at or before `from`
+        while (hi - lo > 1) {
+            const int m = (lo + hi) >> 1;
+            if (s.seg[m].cost0 <= from) lo = m;
+            else hi = m;
         }
-        entry0 += __shfl_sync(0xffffffffu, e, 31);
-        cost0 += __shfl_sync(0xffffffffu, c, 31);
+        int64_t at = w.end;
+        for (int i = lo; i < s.num_segments; ++i) {
+            const KvSharedSeg &g = s.seg[i];
+            const int items = a.kv_heads * g.blocks * g.parts;
+            if (items == 0) continue;
+            w.item = from > g.cost0 ? static_cast<int>((from - g.cost0 + g.cost - 1) / g.cost) : 0;
+            if (w.item >= items) continue;
+            w.seg = i;
+            at = g.cost0 + static_cast<int64_t>(w.item) * g.cost;
+            break;
+        }
+        if (at >= w.end) w.seg = -1;
+        s.cta[threadIdx.x] = w;
     }
 }
 
 // ------------------------------------------------------------------ the shared tokens
 
-// A CTA's items: those that start within its share of the cost of all.  Warp-collective.
+// A CTA's items: those that start within its share of the cost of all.
 struct SharedCursor {
     KvSharedSeg g;
     int s, i, items;        // segment, item of it
@@ -206,8 +244,9 @@ struct SharedCursor {
         const int rest = i - head * per;
         block = rest / g.parts;
         part = rest - block * g.parts;
-        t0 = static_cast<int>(static_cast<int64_t>(part) * g.tiles / g.parts);
-        tiles = static_cast<int>(static_cast<int64_t>(part + 1) * g.tiles / g.parts) - t0;
+        // (at most 152 parts of at most 2^23 tiles)
+        t0 = static_cast<int>(static_cast<uint32_t>(part * g.tiles) / g.parts);
+        tiles = static_cast<int>(static_cast<uint32_t>((part + 1) * g.tiles) / g.parts) - t0;
         wide = g.rows * a.a.hpg - block * 2 * kTile > kTile;
         return true;
     }
@@ -215,22 +254,14 @@ struct SharedCursor {
         g = a.seg[s];
         items = a.a.kv_heads * g.blocks * g.parts;
     }
-    __device__ __forceinline__ bool first(const KvSharedArgs &a, int lane) {
-        const int64_t total = a.seg[a.num_segments].cost0;
-        const int64_t from = total * blockIdx.x / gridDim.x;
-        end = total * (blockIdx.x + 1) / gridDim.x;
-        if (from >= end) return false;
-        s = 0;  // the segment that `from` lies in
-        for (int s0 = 0; s0 < a.num_segments; s0 += 32) {
-            const bool before = s0 + lane < a.num_segments && a.seg[s0 + lane + 1].cost0 <= from;
-            const int n = __popc(__ballot_sync(0xffffffffu, before));
-            s += n;
-            if (n < 32) break;
-        }
+    __device__ __forceinline__ bool first(const KvSharedArgs &a) {
+        const KvSharedCta w = a.cta[blockIdx.x];
+        if (w.seg < 0) return false;
+        s = w.seg;
+        i = w.item;
+        end = w.end;
         load(a);
-        i = static_cast<int>((from - g.cost0 + g.cost - 1) / g.cost);
         at = g.cost0 + static_cast<int64_t>(i) * g.cost;
-        if (i >= items) return skip(a);
         return place(a);
     }
     __device__ __forceinline__ bool skip(const KvSharedArgs &a) {  // to the next segment's first item
@@ -265,65 +296,81 @@ struct SharedCfg {
     static constexpr int kSlots = (229376 - 2 * kQBytes - kVBufs * kVBytes) / kSlotBytes > 12
                                       ? 12
                                       : (229376 - 2 * kQBytes - kVBufs * kVBytes) / kSlotBytes;
-    static_assert(kSlots >= 4 && (!kFp8 || kSlots % 2 == 0), "ring");
+    static_assert(kSlots >= 5 && (!kFp8 || kSlots % 2 == 0), "ring");
     static constexpr int kWarpgroups = kFp8 ? 4 : 3;  // two of softmax, (one that converts V,) the producer and the issuer
     static constexpr int kThreads = 128 * kWarpgroups;
-    // Registers a thread: at launch, then the softmax warpgroups take some of the others'.
-    static constexpr int kLaunchRegs = kFp8 ? 128 : 168;
-    static constexpr int kSoftmaxRegs = kFp8 ? 184 : 208, kOtherRegs = kFp8 ? 72 : 88;
-    static_assert(2 * kSoftmaxRegs + (kWarpgroups - 2) * kOtherRegs == kWarpgroups * kLaunchRegs, "register split");
+    static constexpr int kRun = kFp8 ? 16 : 32;    // scores in registers at a time: a fourth warpgroup leaves 128 a thread
     static constexpr uint32_t kTmemO = 2 * kTile;  // the chains' scores, then their outputs
     static constexpr int OFF_V = 2 * kQBytes;
     static constexpr int OFF_RING = OFF_V + kVBufs * kVBytes;
     static constexpr int OFF_BARS = OFF_RING + kSlots * kSlotBytes;
-    static constexpr int kNumBars = 2 * kSlots + 2 + 1 + 2 + 2 + 2 + 2 * 2 + 1;
+    static constexpr int kNumBars = 2 * kSlots + 1 + 2 * 8;
     static constexpr int OFF_MISC = OFF_BARS + kNumBars * 8;
-    static constexpr int kSmemBytes = OFF_MISC + 16 + 1024;
+    static constexpr int OFF_FACTORS = OFF_MISC + 16;
+    static constexpr int kSmemBytes = OFF_FACTORS + (kFp8 ? 2 * kTile * 4 : 0) + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory");
-    // FP16 weights reach 2^15 and a moved base leaves the largest at 2^7; bf16's range does not ask for a move
-    static constexpr float kHeadroom = kFp8 ? 15.0f : 40.0f, kBias = kFp8 ? 7.0f : 0.0f;
+    // A base leaves the largest weight that it was made for at 2^kBias, so that fp16's steps are 2^-31 of it, and moves
+    // when a tile's weights make up more than kMost (fp16 holds 65504; 128 of 2^7 are 2^14).
+    static constexpr float kBias = kFp8 ? 7.0f : 0.0f, kMost = kFp8 ? 32768.0f : 1048576.0f;
 };
 
-// A thread's column of queries into a chain's image: bf16 as it is, 64 dims to a 128-byte row.
-template <int D>
-__device__ __forceinline__ void put_query_bf16(uint8_t *img, const uint16_t *src, int n) {
-#pragma unroll
-    for (int u = 0; u < D / 8; ++u) {
-        const uint4 v = src == nullptr ? make_uint4(0u, 0u, 0u, 0u) : reinterpret_cast<const uint4 *>(src)[u];
-        *reinterpret_cast<uint4 *>(img + (u >> 3) * (kTile * 128) + fp8mla::sw128(n, u & 7)) = v;
-    }
+// 16 bytes to shared memory while the thread goes on; zeros unless `there`.
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
-// The exponent of 2 that brings a column's largest |q| to (224, 448]; finite: there is nothing but numbers in it.
-template <int D>
-__device__ __forceinline__ int query_exponent(const uint16_t *src, bool &finite) {
-    uint32_t top = 0;
-    if (src != nullptr) {
-#pragma unroll
-        for (int u = 0; u < D / 8; ++u) {
-            const uint4 v = reinterpret_cast<const uint4 *>(src)[u];
-            const uint32_t h[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) top = max(top, max(h[y] << 16 & 0x7fff0000u, h[y] & 0x7fff0000u));
+// A warp's 32 columns (lane l: column l's elements at `src`, NULL behind the last) into the chain's image, from row
+// `n0` on.  kLanes lanes take a column, so that the warp reads whole runs of memory (a thread a column: 11,000
+// cycles); in rolled loops, for code that runs once waits for its way in.  bf16 as it is, 64 dims to a 128-byte row; or
+// e4m3 hi and lo terms of the column's values times 2^e, which brings the largest to (224, 448].  Returns column
+// `lane`'s factor 2^-e (NaN: not only numbers in it).
+template <bool kFp8, int D>
+__device__ __forceinline__ float put_queries(uint8_t *img, const uint16_t *src, int n0, int lane) {
+    constexpr int kElems = kFp8 ? 16 : 8, kLanes = D / kElems, kCols = 32 / kLanes;  // of a lane; of a turn
+    const int unit = lane % kLanes, sub = lane / kLanes;
+    float factor = 1.f;
+    const auto of = [&](int n) {
+        return reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), n));
+    };
+    if constexpr (!kFp8) {
+#pragma unroll 1
+        for (int n = sub; n < 32; n += kCols) {
+            const uint16_t *q = of(n);
+            copy16(img + (unit >> 3) * (kTile * 128) + fp8mla::sw128(n0 + n, unit & 7),
+                   q != nullptr ? q + unit * 8 : reinterpret_cast<const uint16_t *>(img), q != nullptr);
         }
-    }
-    finite = top < 0x7f800000u;
-    if (top == 0 || !finite) return 0;
-    const int e = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return max(-120, min(120, e));
-}
-
-// The column's values times 2^e as e4m3 hi and lo terms.
-template <int D>
-__device__ __forceinline__ void put_query_fp8(uint8_t *img, const uint16_t *src, int n, int e) {
-    const uint4 *q = reinterpret_cast<const uint4 *>(src);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll 2
-    for (int u = 0; u < D / 16; ++u) {
-        uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-        if (src != nullptr) {
-            const uint4 v0 = q[2 * u], v1 = q[2 * u + 1];
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        uint4 v0, v1, w0, w1;  // this turn's and the next one's
+        const auto load = [&](int n, uint4 &x, uint4 &y) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(of(n & 31));
+            x = y = make_uint4(0u, 0u, 0u, 0u);
+            if (q != nullptr) {
+                x = q[2 * unit];
+                y = q[2 * unit + 1];
+            }
+        };
+        load(sub, v0, v1);
+        load(sub + kCols, w0, w1);
+#pragma unroll 1
+        for (int n = sub; n < 32; n += kCols) {
             const uint32_t h[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            v0 = w0;
+            v1 = w1;
+            load(n + 2 * kCols, w0, w1);
+            uint32_t top = 0;  // by the bits: an infinity or a NaN is above every number
+#pragma unroll
+            for (int y = 0; y < 8; ++y) top = max(top, max(h[y] << 16 & 0x7fff0000u, h[y] & 0x7fff0000u));
+#pragma unroll
+            for (int y = 1; y < kLanes; y <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
+            const bool finite = top < 0x7f800000u;
+            int e = 0;
+            if (top > 0 && finite) {
+                e = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+                e = max(-120, min(120, e));
+            }
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 const uint2 p0 = split_pair(bf16_lo(h[2 * y]) * up, bf16_hi(h[2 * y]) * up);
@@ -331,11 +378,18 @@ __device__ __forceinline__ void put_query_fp8(uint8_t *img, const uint16_t *src,
                 hi[y] = p0.x | (p1.x << 16);
                 lo[y] = p0.y | (p1.y << 16);
             }
+            const int r = n0 + n;
+            const uint32_t at = D == 128 ? fp8mla::sw128(r, unit) : static_cast<uint32_t>(r * 64 + ((unit ^ (r >> 1 & 3)) << 4));
+            *reinterpret_cast<uint4 *>(img + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(img + kTile * D + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            // the lane of each of the turn's columns takes its factor from the column's first lane
+            const float f = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : __uint_as_float(0x7fc00000u);
+            const int c = lane - (n - sub);
+            const float mine = __shfl_sync(0xffffffffu, f, (c & (kCols - 1)) * kLanes);
+            if (c >= 0 && c < kCols) factor = mine;
         }
-        const uint32_t at = D == 128 ? fp8mla::sw128(n, u) : static_cast<uint32_t>(n * 64 + ((u ^ (n >> 1 & 3)) << 4));
-        *reinterpret_cast<uint4 *>(img + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(img + kTile * D + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
+    return factor;
 }
 
 // Four e4m3 codes as two fp16 pairs (exact).
@@ -363,9 +417,11 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
     uint64_t *o_full = p_full + 2;                                      // [2] its item's output is done
     uint64_t *v_full = o_full + 2;                                      // [2] V in fp16
     uint64_t *v_empty = v_full + 2;                                     // [2] and its product done
-    uint64_t *drained = v_empty + 2;                                    // after a wait gave up: no MMA is left
+    uint64_t *my_turn = v_empty + 2;                                    // [2] the other chain's warp has issued
+    uint64_t *drained = my_turn + 2;                                    // [2] after a wait gave up: no MMA is left
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+    float *factors_s = reinterpret_cast<float *>(smem + C::OFF_FACTORS);  // [2][kTile] (FP8)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
     constexpr int kProducer = 4 * (C::kWarpgroups - 1), kIssuer = kProducer + 1;
@@ -373,7 +429,7 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
         *abort = 0;
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], kFp8 && (i & 1) ? 4 : 1);
+            mbar_init(&empty[i], kFp8 && (i & 1) ? 4 : 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 4);
@@ -381,10 +437,11 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
             mbar_init(&v_full[i], 4);
-            mbar_init(&v_empty[i], 1);
+            mbar_init(&v_empty[i], 2);
+            mbar_init(&my_turn[i], 1);
+            mbar_init(&drained[i], 1);
         }
-        mbar_init(q_empty, 1);
-        mbar_init(drained, 1);
+        mbar_init(q_empty, 2);
         fence_mbar_init();
         prefetch_tensormap(&kv_map);
     }
@@ -396,14 +453,15 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_wait();
+    // What this kernel reads was complete when the one before it (kv_attention*.cu), which writes nothing that this one
+    // reads or writes, passed its own wait and let this one start.  So it begins while that one ends, and waits for it at
+    // the end, for the join's sake.
     pdl_launch_dependents();
 
     SharedCursor w;
-    bool more = w.first(s, lane);
+    bool more = w.first(s);
 
     if (wg >= 2) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         if (kFp8 && wg == 2) {
             // ---- V's codes as fp16: thread = token
             const int t = threadIdx.x & 127;
@@ -487,85 +545,112 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                     }
                 }
             }
-        } else if (warp == kIssuer && lane == 0) {
-            // ---- the products of both chains.  MMAs run in the order of their issue: a chain's next scores, which take
-            // the place of its weights, are right behind the product that reads those
+        } else if (warp == kIssuer || warp == kIssuer + 1) {
+            // ---- the products.  An MMA's issue lasts as long as its passage, and what lies between two runs of MMAs
+            // (some 300 cycles of waits and commits) is another warp's time: chains that take the same tiles have a warp
+            // each, and the warps take turns, so that one chain's products stay beside the other's softmax (left to
+            // themselves the chains fall into step: 3,690 cycles for a tile of both, in turns 2,400; one warp for both
+            // 3,150).  Of chains that share tiles out one warp issues for both, since a barrier's parity tells a slot's
+            // phases apart for a warp alone that waits for every one of them.  (All of an item's tiles have landed and all
+            // its weights have been seen when the next begins.)  MMAs of a thread run in the order of their issue, so a
+            // chain's next scores, which take the place of its weights, are right behind the product that reads those.
+            // A warp goes through all of this together, so that descriptors stay in uniform registers, and one lane
+            // issues
             constexpr uint32_t kIdescS = make_idesc(kTile, kTile, kFp8 ? 0 : 1, kFp8 ? 0 : 1, false, false);
             constexpr uint32_t kIdescO = make_idesc(kTile, D, kFp8 ? 0 : 1, kFp8 ? 0 : 1, false, true);
-            const uint32_t base = smem_u32(smem), ring = base + C::OFF_RING;
-            uint32_t n = 0, items = 0;             // tiles before the item, items
-            uint32_t s_count[2] = {0, 0}, p_count[2] = {0, 0};
+            const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), ring = base + C::OFF_RING;
+            const uint32_t t_mem = __shfl_sync(0xffffffffu, tmem, 0);
+            const int me = __shfl_sync(0xffffffffu, warp - kIssuer, 0);
+            uint32_t n = 0, items = 0, p_phases = 0, turns = 0;  // tiles before the item, items, a bit a chain, turns taken
             bool ok = true;
             for (; more && ok; more = w.next(s), ++items) {
-                const int most = w.steps(0);
-                auto tile_of = [&](int chain, int j) { return n + static_cast<uint32_t>(w.wide ? j : 2 * j + chain); };
-                auto scores = [&](int c, int j) {
-                    const uint32_t turn = 2 * tile_of(c, j), slot = turn % NS;
-                    ok = ok && wait_mbar(&full[slot], turn / NS & 1, abort);
+                const bool wide = __shfl_sync(0xffffffffu, w.wide, 0);
+                const int tiles = __shfl_sync(0xffffffffu, w.tiles, 0);
+                const int c0 = me, c1 = wide ? me : 1 - me;  // its chains (none: c1 < c0)
+                auto steps_of = [&](int c) { return wide ? tiles : (tiles + 1 - c) / 2; };
+                auto tile_of = [&](int c, int j) { return n + static_cast<uint32_t>(wide ? j : 2 * j + c); };
+                auto used = [&](uint64_t *bar) {  // two arrivals: one of each chain, or both of the only one
+                    mma_commit(bar);
+                    if (!wide) mma_commit(bar);
+                };
+                // the product of chain c's step j (from 0 on) and the scores of step j + 1 (where there is one)
+                auto step = [&](int c, int j) {
+                    const uint32_t tile = tile_of(c, j), v_turn = 2 * tile + 1, v_slot = v_turn % NS, buf = tile & 1;
+                    const uint32_t k_turn = 2 * tile_of(c, j + 1), k_slot = k_turn % NS;
+                    const bool product = j >= 0, next = j + 1 < steps_of(c);
+                    if (next) ok = ok && wait_mbar_warp(&full[k_slot], k_turn / NS & 1, abort);
+                    if (product)
+                        ok = ok && (kFp8 ? wait_mbar_warp(&v_full[buf], tile >> 1 & 1, abort)
+                                         : wait_mbar_warp(&full[v_slot], v_turn / NS & 1, abort));
+                    if (wide) ok = ok && wait_mbar_warp(&my_turn[c], (turns++ & 1) ^ (c == 0 ? 1 : 0), abort);
+                    if (product) {
+                        ok = ok && wait_mbar_warp(&p_full[c], p_phases >> c & 1, abort);
+                        p_phases ^= 1u << c;
+                    }
                     if (!ok) return;
                     tc_fence_after();
-                    const uint32_t q = base + (w.wide ? c : 0) * C::kQBytes, k = ring + slot * C::kSlotBytes;
-                    const uint32_t d = tmem + c * kTile;
-                    if constexpr (kFp8) {
+                    const uint32_t st = t_mem + c * kTile, ot = t_mem + C::kTmemO + c * D;
+                    const uint32_t v = kFp8 ? base + C::OFF_V + buf * C::kVBytes : ring + v_slot * C::kSlotBytes;
+                    const uint32_t q = base + (wide ? c : 0) * C::kQBytes, k = ring + k_slot * C::kSlotBytes;
+                    if (elect_one()) {
+                        if (product) {
+                            const uint64_t vd = sdesc_sw128(v, kTile * 128, 1024);
+                            const uint32_t add = j > 0;
 #pragma unroll
-                        for (int term = 0; term < 2; ++term)
-#pragma unroll
-                            for (int i = 0; i < D / 32; ++i) {
-                                const uint32_t qa = q + term * (kTile * D) + i * 32, ka = k + i * 32;
-                                mma_f8(d, D == 128 ? sdesc_sw128(qa, 16, 1024) : sdesc_sw64(qa),
-                                       D == 128 ? sdesc_sw128(ka, 16, 1024) : sdesc_sw64(ka), kIdescS, term + i > 0);
-                            }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            const uint32_t off = (i >> 2) * (kTile * 128) + (i & 3) * 32;
-                            mma_f16(d, sdesc_sw128(q + off, 16, 1024), sdesc_sw128(k + off, 16, 1024), kIdescS, i > 0);
+                            for (int i = 0; i < kTile / 16; ++i)
+                                mma_f16_ts(ot, st + i * 8, vd + i * 128, kIdescO, i > 0 ? 1u : add);
                         }
-                    }
-                    mma_commit(&s_full[c]);
-                    if (!w.wide || c == 1) mma_commit(&empty[slot]);
-                    ++s_count[c];
-                };
-                ok = wait_mbar(&q_full[0], items & 1, abort) && wait_mbar(&q_full[1], items & 1, abort);
-                if (!ok) break;
-                scores(0, 0);
-                if (w.steps(1) > 0) scores(1, 0);
-                for (int j = 0; j < most && ok; ++j) {
-#pragma unroll 1
-                    for (int c = 0; c < 2 && ok; ++c) {
-                        const int steps = w.steps(c);
-                        if (j >= steps) break;
-                        const uint32_t tile = tile_of(c, j), turn = 2 * tile + 1, slot = turn % NS, buf = tile & 1;
-                        ok = wait_mbar(&p_full[c], p_count[c] & 1, abort) &&
-                             (kFp8 ? wait_mbar(&v_full[buf], tile >> 1 & 1, abort)
-                                   : wait_mbar(&full[slot], turn / NS & 1, abort));
-                        if (!ok) break;
-                        ++p_count[c];
-                        tc_fence_after();
-                        const uint32_t v = kFp8 ? base + C::OFF_V + buf * C::kVBytes : ring + slot * C::kSlotBytes;
-                        const uint32_t d = tmem + C::kTmemO + c * D, p = tmem + c * kTile;
+                        if (next) {
+                            if constexpr (kFp8) {
+                                const uint64_t qd = D == 128 ? sdesc_sw128(q, 16, 1024) : sdesc_sw64(q);
+                                const uint64_t kd = D == 128 ? sdesc_sw128(k, 16, 1024) : sdesc_sw64(k);
 #pragma unroll
-                        for (int i = 0; i < kTile / 16; ++i)
-                            mma_f16_ts(d, p + i * 8, sdesc_sw128(v + i * 2048, kTile * 128, 1024), kIdescO, j + i > 0);
-                        if (!w.wide || c == 1) mma_commit(kFp8 ? &v_empty[buf] : &empty[slot]);
-                        if (j == steps - 1) mma_commit(&o_full[c]);
-                        else scores(c, j + 1);
+                                for (int term = 0; term < 2; ++term)
+#pragma unroll
+                                    for (int i = 0; i < D / 32; ++i)
+                                        mma_f8(st, qd + term * (kTile * D / 16) + i * 2, kd + i * 2, kIdescS, term + i > 0);
+                            } else {
+                                const uint64_t qd = sdesc_sw128(q, 16, 1024), kd = sdesc_sw128(k, 16, 1024);
+#pragma unroll
+                                for (int i = 0; i < D / 16; ++i) {
+                                    const uint32_t off = (i >> 2) * (kTile * 128 / 16) + (i & 3) * 2;
+                                    mma_f16(st, qd + off, kd + off, kIdescS, i > 0);
+                                }
+                            }
+                        }
+                        if (wide) mbar_arrive(&my_turn[1 - c]);
+                        if (next) {
+                            mma_commit(&s_full[c]);
+                            used(&empty[k_slot]);
+                        } else {
+                            mma_commit(&o_full[c]);
+                        }
+                        if (product) used(kFp8 ? &v_empty[buf] : &empty[v_slot]);
                     }
-                }
-                mma_commit(q_empty);
-                n += static_cast<uint32_t>(w.tiles);
+                    __syncwarp();
+                };
+                ok = wait_mbar_warp(&q_full[0], items & 1, abort) && wait_mbar_warp(&q_full[1], items & 1, abort);
+                for (int j = -1; c0 <= c1 && j < steps_of(c0) && ok; ++j)
+#pragma unroll 1
+                    for (int c = c0; c <= c1 && j < steps_of(c) && steps_of(c) > 0 && ok; ++c) step(c, j);
+                if (!ok) break;
+                if (elect_one()) mma_commit(q_empty);
+                __syncwarp();
+                for (int c = 0; c < 2; ++c)
+                    if (c < c0 || c > c1) p_phases ^= (steps_of(c) & 1u) << c;
+                n += static_cast<uint32_t>(tiles);
             }
             if (!ok) gave_up(abort, a.status);
             if (*abort) {  // leave no MMA in flight behind
-                mma_commit(drained);
+                if (elect_one()) mma_commit(&drained[me]);
+                __syncwarp();
                 const long long t0 = clock64();
-                while (!mbar_try_wait(drained, 0) && clock64() - t0 < kWaitTimeoutCycles) {
+                while (!mbar_try_wait(&drained[me], 0) && clock64() - t0 < kWaitTimeoutCycles) {
                 }
             }
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         // ---- softmax of chain wg: thread = column
         const int self = threadIdx.x & 127, c = wg;
         const uint32_t quad = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -575,120 +660,163 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
         for (; more && ok; more = w.next(s), ++items) {
             const int hpg = a.hpg, col = w.block * 2 * kTile + (w.wide ? c * kTile : 0) + self;
             const bool real = col < w.g.rows * hpg;
-            const int row = col / hpg, head = w.head * hpg + col - row * hpg;
             ok = wait_mbar_warp(q_empty, (items & 1) ^ 1, abort);
             if (!ok) break;
-            const uint16_t *src = real ? a.q + (w.g.row0 + row) * a.q_stride + static_cast<int64_t>(head) * D : nullptr;
-            const bool puts = w.wide || c == 0;  // (one image serves two chains of the same columns)
-            uint8_t *img = smem + c * C::kQBytes;
-            float scale = a.s_scale;
-            bool finite = true;
-            if constexpr (kFp8) {
-                const int e = query_exponent<D>(src, finite);
-                if (puts) put_query_fp8<D>(img, src, self, e);
-                scale *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            } else if (puts) {
-                put_query_bf16<D>(img, src, self);
+            const int of = w.wide ? c : 0;  // (one image serves two chains of the same columns)
+            // this column's row of the segment and head; where its output goes, in outputs of D
+            const int row = static_cast<int>(static_cast<uint32_t>(col) / static_cast<uint32_t>(hpg));
+            const int head = w.head * hpg + col - row * hpg;
+            const int64_t place = (w.g.entry0 + static_cast<int64_t>(row) * w.g.entries + (w.wide ? w.part : 2 * w.part + c)) *
+                                      a.num_heads + head;
+            if (of == c) {
+                const uint16_t *src = real ? a.q + (w.g.row0 + row) * a.q_stride + static_cast<int64_t>(head) * D : nullptr;
+                const float f = put_queries<kFp8, D>(smem + c * C::kQBytes, src, (warp & 3) * 32, lane);
+                if constexpr (kFp8) factors_s[c * kTile + self] = f;
+                fence_async_smem();
             }
-            // a score of -inf times the scale: neither zero nor infinity.  Over codes no number in q makes no score
-            scale = finite ? fminf(fmaxf(scale, 1.17549435e-38f), 3.40282347e38f) : __uint_as_float(0x7fc00000u);
-            fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[c]);
             const int steps = w.steps(c);
+            float scale = a.s_scale;
+            if constexpr (kFp8) {
+                if (steps > 0) ok = wait_mbar_warp(&q_full[of], items & 1, abort);
+                if (!ok) break;
+                scale *= factors_s[of * kTile + self];
+            }
+            // a score of -inf times the scale: neither zero nor infinity.  Over codes no number in q makes no score
+            if (scale == scale) scale = fminf(fmaxf(scale, 1.17549435e-38f), 3.40282347e38f);
             float base = -INFINITY;
-            float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+            float2 sum = make_float2(0.f, 0.f);
             for (int j = 0; j < steps; ++j, ++s_count) {
                 ok = wait_mbar_warp(&s_full[c], s_count & 1, abort);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t h[4][32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld32(st + 32 * i, h[i]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) reg_fence(h[i]);
-                float top[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    top[i] = __uint_as_float(h[i][0]);
-#pragma unroll
-                    for (int k = 1; k < 32; ++k) top[i] = fmaxf(top[i], __uint_as_float(h[i][k]));
-                }
-                const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;  // (a positive factor)
-                const bool moves = most > base + C::kHeadroom;
-                if (__any_sync(0xffffffffu, moves)) {
-                    // (this tile's scores are done, so the products before them are: O is at rest)
-                    const float f = moves ? ex2(base - (most - C::kBias)) : 1.f;
-                    if (moves) base = most - C::kBias;
-                    sum0.x *= f;
-                    sum0.y *= f;
-                    sum1.x *= f;
-                    sum1.y *= f;
-                    if (j > 0) {
+                // P = 2^(scale S - b), kRun tokens at a time with the next ones on their way, into registers: S is
+                // overwritten when no weight is too large for b.  A tile's sum tells that as well as its largest would,
+                // without one more pass; the largest is looked for where it is, and where there is no base yet.  (Half a
+                // tile at a time, with the first half's product beside the second's exponentials: 2,900 cycles for a
+                // tile of both chains against 2,820, since the chains' exponentials then meet.)
+                uint32_t p[kTile / 2];
+                bool moves = base == -INFINITY, moved = false;
 #pragma unroll 1
-                        for (int i = 0; i < D; i += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(ot + i, o);
+                while (true) {  // (three times at most: a column's base moves once a tile)
+                    if (__any_sync(0xffffffffu, moves)) {
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int i = 0; i < kTile; i += 32) {
+                            uint32_t h[32];
+                            tmem_ld32(st + i, h);
                             tmem_ld_wait();
-                            reg_fence(o);
+                            reg_fence(h);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st16(ot + i, o);
+                            for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(h[k]));
+                        }
+                        top = top * scale - C::kBias;  // (a positive factor)
+                        moved |= moves;
+                        moves = moves && top > base;
+                        const float f = moves ? ex2(base - top) : 1.f;
+                        if (moves) base = top;
+                        sum.x *= f;
+                        sum.y *= f;
+                        // (this tile's scores are done, so the products before them are: O is at rest)
+                        if (j > 0 && __any_sync(0xffffffffu, moves)) {
+#pragma unroll 1
+                            for (int i = 0; i < D; i += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(ot + i, o);
+                                tmem_ld_wait();
+                                reg_fence(o);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                tmem_st16(ot + i, o);
+                            }
                         }
                     }
-                }
-                const float nb = base == -INFINITY ? 0.f : -base;
-                const float2 sc2 = make_float2(scale, scale), nb2 = make_float2(nb, nb);
+                    const float nb = base == -INFINITY ? 0.f : -base;
+                    const float2 sc2 = make_float2(scale, scale), nb2 = make_float2(nb, nb);
+                    float2 t0 = make_float2(0.f, 0.f), t1 = make_float2(0.f, 0.f);
+                    constexpr int kRun = C::kRun;
+                    uint32_t h[2][kRun];
+                    auto load = [&](int i) {
+                        if constexpr (kRun == 32) tmem_ld32(st + 32 * i, h[i & 1]);
+                        else tmem_ld16(st + 16 * i, h[i & 1]);
+                    };
+                    load(0);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t p[16];
+                    for (int i = 0; i < kTile / kRun; ++i) {
+                        tmem_ld_wait();
+                        reg_fence(h[i & 1]);
+                        if (i + 1 < kTile / kRun) load(i + 1);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        float2 x = __ffma2_rn(make_float2(__uint_as_float(h[i][k]), __uint_as_float(h[i][k + 1])), sc2, nb2);
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
-                        if (k & 2) sum1 = __fadd2_rn(sum1, x);
-                        else sum0 = __fadd2_rn(sum0, x);
-                        p[k / 2] = kFp8 ? pack_f16(x.x, x.y) : pack_bf16(x.x, x.y);
+                        for (int k = 0; k < kRun; k += 2) {
+                            float2 x = __ffma2_rn(
+                                make_float2(__uint_as_float(h[i & 1][k]), __uint_as_float(h[i & 1][k + 1])), sc2, nb2);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            if (k & 2) t1 = __fadd2_rn(t1, x);
+                            else t0 = __fadd2_rn(t0, x);
+                            p[(kRun * i + k) / 2] = kFp8 ? pack_f16(x.x, x.y) : pack_bf16(x.x, x.y);
+                        }
                     }
-                    tmem_st16(st + 16 * i, p);
+                    t0 = __fadd2_rn(t0, t1);
+                    moves = !moved && t0.x + t0.y > C::kMost;
+                    if (!__any_sync(0xffffffffu, moves)) {
+                        sum = __fadd2_rn(sum, t0);
+                        break;
+                    }
                 }
+                tmem_st32(st, *reinterpret_cast<uint32_t(*)[32]>(p));
+                tmem_st32(st + 32, *reinterpret_cast<uint32_t(*)[32]>(p + 32));
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[c]);
             }
             if (!ok) break;
-            // ---- the item's output: a column's D numbers in a row
-            const float total = (sum0.x + sum1.x) + (sum0.y + sum1.y);
-            const int64_t entry = w.g.entry0 + static_cast<int64_t>(row) * w.g.entries + (w.wide ? w.part : 2 * w.part + c);
-            const int64_t at = entry * a.num_heads + head;
-            if (real) s.sml[at] = make_float2(part_base(base, total), total);
+            // ---- the item's output, by way of the chain's queries' place: a warp writes whole runs of memory (a thread a
+            // column: 5,400 cycles)
+            const float total = sum.x + sum.y;
+            if (real) s.sml[place] = make_float2(part_base(base, total), total);
             if (steps > 0) {
                 ok = wait_mbar_warp(&o_full[c], outs & 1, abort);
-                if (!ok) break;
                 ++outs;
-                tc_fence_after();
-                float4 *dst = reinterpret_cast<float4 *>(s.so + at * D);
-#pragma unroll 1
-                for (int i = 0; i < D; i += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(ot + i, o);
-                    tmem_ld_wait();
-                    reg_fence(o);
-                    if (real) {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            dst[(i + k) / 4] = make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]),
-                                                           __uint_as_float(o[k + 2]), __uint_as_float(o[k + 3]));
-                    }
-                }
-                tc_fence_before();
-            } else if (real) {  // (no tile for the second chain)
-                float4 *dst = reinterpret_cast<float4 *>(s.so + at * D);
-                for (int i = 0; i < D / 4; ++i) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
+            if (of == c && !w.wide) ok = ok && wait_mbar_warp(q_empty, items & 1, abort);  // (the other chain's scores read it too)
+            if (!ok) break;
+            tc_fence_after();
+            uint8_t *stage = smem + c * C::kQBytes + (warp & 3) * (C::kQBytes / 4);  // the warp's 32 columns by kDims dims
+            constexpr int kDims = D / 2, kUnits = kDims / 4, kCols = 32 / kUnits;  // 16-byte units of a column, columns a turn
+#pragma unroll 1
+            for (int d0 = 0; d0 < D; d0 += kDims) {
+                __syncwarp();
+#pragma unroll 1
+                for (int i = 0; i < kDims; i += 16) {
+                    uint32_t o[16];
+                    if (steps > 0) {
+                        tmem_ld16(ot + d0 + i, o);
+                        tmem_ld_wait();
+                        reg_fence(o);
+                    } else {  // (no tile for the second chain)
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = 0u;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4)
+                        *reinterpret_cast<uint4 *>(stage + lane * (kDims * 4) + (((i + k) / 4 ^ (lane & 7)) << 4)) =
+                            make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                }
+                __syncwarp();
+                const int u = lane % kUnits;
+#pragma unroll 4
+                for (int n0 = 0; n0 < 32; n0 += kCols) {
+                    const int n = n0 + lane / kUnits;
+                    const int64_t at = __shfl_sync(0xffffffffu, real ? place : -1, n);
+                    if (at >= 0)
+                        *reinterpret_cast<uint4 *>(s.so + at * D + d0 + 4 * u) =
+                            *reinterpret_cast<const uint4 *>(stage + n * (kDims * 4) + ((u ^ (n & 7)) << 4));
+                }
+            }
+            tc_fence_before();
         }
         if (!ok) gave_up(abort, a.status);
     }
@@ -697,6 +825,7 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    pdl_wait();
 }
 
 // ------------------------------------------------------------------ the parts of a (row, head)
@@ -711,8 +840,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_cons
     __shared__ float4 x_s[kGroups][kLanes];
     __shared__ float t_s[kGroups];
     const KvAttnArgs &a = s.a;
-    // The kernel before lets this one start after its own wait, so what ran before it is complete: what is not of its
-    // making can be read before the wait
+    // The kernel before this one starts when kv_segments_kernel is complete, so what that wrote can be read before the
+    // wait
     const int64_t at = blockIdx.x;
     const int row = static_cast<int>(at / a.num_heads), head = static_cast<int>(at - static_cast<int64_t>(row) * a.num_heads);
     int req;
@@ -798,27 +927,18 @@ cudaError_t launch_shared(const KvSharedArgs &s, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
     cudaError_t e = raise_smem_limit(kern, C::kSmemBytes, configured);
     if (e != cudaSuccess) return e;
-    // the register split waits forever in a CTA launched with fewer
-    static std::atomic<int> regs{0};
-    if (regs.load() == 0) {
-        cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, kern);
-        if (e != cudaSuccess) return e;
-        regs.store(fa.numRegs);
-    }
-    if (regs.load() < C::kLaunchRegs) return cudaErrorInvalidConfiguration;
     CUtensorMap map;
     if (!encode_kv_rows_map(&map, s.a.pool, s.a.pool_rows, C::kRowBytes, s.a.page_size)) return cudaErrorInvalidValue;
     return launch_pdl(kern, dim3(kSharedCtas), dim3(C::kThreads), C::kSmemBytes, stream, map, s);
 }
 
-// Shared parts of all (row, head) at most, divided by the heads.  With at least rows x heads / 256 items a part,
-// shared_parts_cap leaves a segment 4 parts a row or 2 x 152 x 256 / heads in all.
+// Shared parts of all (row, head) at most, divided by the heads.  A part has at least rows x heads / 256 items, so
+// shared_parts_cap leaves a segment 2 x 4 outputs a row, or 2 x 8 x 152 x 256 / heads in all.
 size_t shared_entries(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t max_ctx, int32_t num_segments) {
     const int64_t tiles = max_ctx / kTile, most = tiles / kMinTiles > 1 ? tiles / kMinTiles : 1;
     const int64_t cap = shared_parts_cap(kv_heads) < most ? shared_parts_cap(kv_heads) : most;
     const int64_t by_row = num_rows * 2 * cap;
-    const int64_t by_segment = 4 * num_rows + num_segments * (2ll * kSharedCtas * 2 * kTile / num_heads + 1);
+    const int64_t by_segment = 8 * num_rows + num_segments * (16ll * kSharedCtas * 2 * kTile / num_heads + 1);
     return static_cast<size_t>(by_row < by_segment ? by_row : by_segment);
 }
 
@@ -829,7 +949,7 @@ size_t kv_attention_shared_workspace_bytes(int64_t num_rows, int32_t num_heads, 
     const size_t entries = shared_entries(num_rows, num_heads, kv_heads, max_ctx, num_segments) * static_cast<size_t>(num_heads);
     return kv_attention_workspace_bytes(num_rows, num_heads, kv_heads, head_dim, max_ctx, true) +
            3 * align256(static_cast<size_t>(num_rows) * 4) +
-           align256((static_cast<size_t>(num_segments) + 1) * sizeof(KvSharedSeg)) +
+           align256(static_cast<size_t>(num_segments) * sizeof(KvSharedSeg)) + align256(kSharedCtas * sizeof(KvSharedCta)) +
            align256(entries * static_cast<size_t>(head_dim) * 4) + align256(entries * 8);
 }
 
@@ -851,7 +971,8 @@ cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, 
     s.own_ctx = reinterpret_cast<int32_t *>(take(rows));
     s.row_begin = reinterpret_cast<int32_t *>(take(rows));
     s.row_seg = reinterpret_cast<int32_t *>(take(rows));
-    s.seg = reinterpret_cast<KvSharedSeg *>(take(align256((static_cast<size_t>(seg.num_segments) + 1) * sizeof(KvSharedSeg))));
+    s.seg = reinterpret_cast<KvSharedSeg *>(take(align256(static_cast<size_t>(seg.num_segments) * sizeof(KvSharedSeg))));
+    s.cta = reinterpret_cast<KvSharedCta *>(take(align256(kSharedCtas * sizeof(KvSharedCta))));
     const size_t entries = shared_entries(a.num_rows, a.num_heads, a.kv_heads, a.max_ctx, seg.num_segments) *
                            static_cast<size_t>(a.num_heads);
     s.so = reinterpret_cast<float *>(take(align256(entries * static_cast<size_t>(a.head_dim) * 4)));
