@@ -79,55 +79,79 @@ __host__ __device__ __forceinline__ int32_t shared_parts_cap(int32_t units) {
 
 // ------------------------------------------------------------------ who reads what
 
-constexpr int kSegThreads = 1024;
+// One CTA.  Its time is that of a chain of dependent reads, so what it goes through again stays in shared memory while it
+// fits.
+constexpr int kSegThreads = 512, kSegRows = 8192, kSegSegs = 64;
 
 __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __grid_constant__ KvSharedArgs s) {
     const KvAttnArgs &a = s.a;
-    __shared__ int32_t tops[kSegThreads];
+    __shared__ int32_t tops[kSegThreads / 32];
+    __shared__ int32_t ctx_s[kSegRows];
+    __shared__ KvSharedSeg seg_s[kSegSegs];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hpg = a.num_heads / a.kv_heads;
+    int32_t *ctx = a.num_rows <= kSegRows ? ctx_s : s.own_ctx;  // what each row reads itself (-1: its group is refused)
+    KvSharedSeg *seg = s.num_segments <= kSegSegs ? seg_s : s.seg;
     pdl_wait();
     pdl_launch_dependents();
-    // every row by itself at first; -1: its group is refused
+    // every row by itself at first
     for (int g = threadIdx.x; g < a.num_rows / a.group; g += kSegThreads) {
         const int row0 = g * a.group;
-        bool bad = false;
-        for (int r = row0; r < row0 + a.group; ++r) bad |= kv_refused(a, s.row_ctx[r], a.row_req[r], a.row_req[row0]);
-        for (int r = row0; r < row0 + a.group; ++r) {
-            s.own_ctx[r] = bad ? -1 : s.row_ctx[r];
-            s.row_begin[r] = 0;
-            s.row_seg[r] = -1;
+        int32_t n[kMaxGroup], req[kMaxGroup];
+#pragma unroll
+        for (int r = 0; r < kMaxGroup; ++r) {
+            const int row = row0 + (r < a.group ? r : 0);
+            n[r] = s.row_ctx[row];
+            req[r] = a.row_req[row];
         }
+        bool bad = false;
+#pragma unroll
+        for (int r = 0; r < kMaxGroup; ++r) bad |= kv_refused(a, n[r], req[r], req[0]);
+#pragma unroll
+        for (int r = 0; r < kMaxGroup; ++r)
+            if (r < a.group) {
+                ctx[row0 + r] = bad ? -1 : n[r];
+                s.row_begin[row0 + r] = 0;
+                s.row_seg[row0 + r] = -1;
+            }
     }
     // a segment begins at or behind every bound before it
     const int per = (s.num_segments + kSegThreads) / kSegThreads, lo = min(s.num_segments + 1, static_cast<int>(threadIdx.x) * per);
     const int hi = min(s.num_segments + 1, lo + per);
     int32_t top = INT32_MIN;
     for (int i = lo; i < hi; ++i) top = max(top, s.first_row[i]);
-    tops[threadIdx.x] = top;
+    int32_t upto = top;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto = max(upto, u);
+    }
+    if (lane == 31) tops[warp] = upto;
+    top = __shfl_up_sync(0xffffffffu, upto, 1);
+    if (lane == 0) top = INT32_MIN;
     __syncthreads();
-    top = INT32_MIN;
-    for (int t = 0; t < static_cast<int>(threadIdx.x) && lo < hi; ++t) top = max(top, tops[t]);
+    for (int t = 0; t < warp; ++t) top = max(top, tops[t]);
     for (int i = lo; i < min(hi, s.num_segments); ++i) {
-        const int32_t first = s.first_row[i], end = s.first_row[i + 1];
+        const int32_t first = s.first_row[i], end = s.first_row[i + 1], shared = s.shared_ctx[i];
         const bool bad = first < 0 || first < top || end < first || end > a.num_rows || first % a.group != 0 ||
-                         end % a.group != 0 || s.shared_ctx[i] < 0;
+                         end % a.group != 0 || shared < 0;
         if (bad) report(a.status, DSA_ERR_BOUNDS);
         KvSharedSeg g = {};
         g.row0 = bad ? 0 : first;
         g.rows = bad ? 0 : end - first;
-        s.seg[i] = g;
+        g.tiles = bad ? 0 : shared / kTile;
+        seg[i] = g;
         top = max(top, first);
     }
     __syncthreads();
     // a warp a segment: what all its rows see, and how that is cut
     for (int i = warp; i < s.num_segments; i += kSegThreads / 32) {
-        KvSharedSeg g = s.seg[i];
+        KvSharedSeg g = seg[i];
         const int groups = g.rows / a.group;
         int32_t least = INT32_MAX, lead = INT32_MAX, live = 0;
         for (int j = lane; j < groups; j += 32) {
             bool sees = false;
             for (int r = g.row0 + j * a.group; r < g.row0 + (j + 1) * a.group; ++r) {
-                const int32_t n = s.own_ctx[r];
+                const int32_t n = ctx[r];
                 if (n > 0) {
                     least = min(least, n);
                     sees = true;
@@ -139,7 +163,7 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
         least = __reduce_min_sync(0xffffffffu, least);
         lead = __reduce_min_sync(0xffffffffu, lead);
         live = __reduce_add_sync(0xffffffffu, live);
-        if (live >= 2) g.tiles = min(least, s.shared_ctx[i]) / kTile;
+        g.tiles = live >= 2 ? min(least / kTile, g.tiles) : 0;
         if (g.tiles > 0) {
             const int cols = g.rows * hpg;
             g.blocks = (cols + 2 * kTile - 1) / (2 * kTile);
@@ -160,15 +184,15 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
             g.entries = narrow ? 2 * g.parts : g.parts;
             g.cost = (g.tiles + g.parts - 1) / g.parts * each + kItemTiles;
             for (int r = g.row0 + lane; r < g.row0 + g.rows; r += 32) {
-                const int32_t n = s.own_ctx[r];
+                const int32_t n = ctx[r];
                 s.row_begin[r] = g.tiles * kTile;
                 if (n > 0) {
-                    s.own_ctx[r] = n - g.tiles * kTile;
+                    ctx[r] = n - g.tiles * kTile;
                     s.row_seg[r] = i;
                 }
             }
         }
-        if (lane == 0) s.seg[i] = g;
+        if (lane == 0) seg[i] = g;
     }
     __syncthreads();
     __shared__ int64_t total_s;
@@ -178,7 +202,7 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
             const int i = i0 + lane;
             int64_t entries = 0, cost = 0;
             if (i < s.num_segments) {
-                const KvSharedSeg &g = s.seg[i];
+                const KvSharedSeg &g = seg[i];
                 entries = static_cast<int64_t>(g.rows) * g.entries;
                 cost = static_cast<int64_t>(a.kv_heads) * g.blocks * g.parts * g.cost;
             }
@@ -191,15 +215,19 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
                 }
             }
             if (i < s.num_segments) {
-                s.seg[i].entry0 = entry0 + e - entries;
-                s.seg[i].cost0 = cost0 + c - cost;
+                seg[i].entry0 = entry0 + e - entries;
+                seg[i].cost0 = cost0 + c - cost;
             }
             entry0 += __shfl_sync(0xffffffffu, e, 31);
             cost0 += __shfl_sync(0xffffffffu, c, 31);
         }
         if (lane == 0) total_s = cost0;
+    } else if (ctx == ctx_s) {
+        for (int r = threadIdx.x - 32; r < a.num_rows; r += kSegThreads - 32) s.own_ctx[r] = ctx_s[r];
     }
     __syncthreads();
+    if (seg == seg_s)
+        for (int i = threadIdx.x; i < s.num_segments; i += kSegThreads) s.seg[i] = seg_s[i];
     // a CTA takes the items that start within its share of the cost
     if (threadIdx.x < kSharedCtas) {
         const int64_t from = total_s * threadIdx.x / kSharedCtas;
@@ -207,12 +235,12 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
         int lo = 0, hi = s.num_segments;  // the last segment that begins at or before `from`
         while (hi - lo > 1) {
             const int m = (lo + hi) >> 1;
-            if (s.seg[m].cost0 <= from) lo = m;
+            if (seg[m].cost0 <= from) lo = m;
             else hi = m;
         }
         int64_t at = w.end;
         for (int i = lo; i < s.num_segments; ++i) {
-            const KvSharedSeg &g = s.seg[i];
+            const KvSharedSeg &g = seg[i];
             const int items = a.kv_heads * g.blocks * g.parts;
             if (items == 0) continue;
             w.item = from > g.cost0 ? static_cast<int>((from - g.cost0 + g.cost - 1) / g.cost) : 0;
@@ -830,23 +858,28 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
 
 // ------------------------------------------------------------------ the parts of a (row, head)
 
-// As kv_combine_kernel, over a row's own parts and then the shared ones.
-constexpr int kJoinThreads = 128, kJoinParts = 128 + 2 * kSharedCtas;
+// A row's own parts, then the shared ones.  kWarps warps take a (row, head): one, where there are enough of those, else
+// four, which share out the parts.  D / 4 lanes take a part, four dims each.
+//   us                                    one warp   four
+constexpr int kJoinThreads = 128;
+constexpr int64_t kJoinPairs = 1024;
 
-template <int D>
+template <int D, int kWarps>
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ KvSharedArgs s) {
-    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
-    __shared__ float2 ml_s[kJoinParts];
-    __shared__ float4 x_s[kGroups][kLanes];
-    __shared__ float t_s[kGroups];
+    constexpr int kLanes = D / 4, kAt = 32 / kLanes;  // lanes of a part, parts a turn of a warp
+    constexpr int kPairs = kJoinThreads / 32 / kWarps;
+    __shared__ float4 x_s[kWarps > 1 ? kJoinThreads : 1];
+    __shared__ float2 t_s[kWarps > 1 ? kWarps : 1];
     const KvAttnArgs &a = s.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp % kWarps;
     // The kernel before this one starts when kv_segments_kernel is complete, so what that wrote can be read before the
     // wait
-    const int64_t at = blockIdx.x;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * kPairs + warp / kWarps;
+    if (kWarps == 1 && at >= static_cast<int64_t>(a.num_rows) * a.num_heads) return;
     const int row = static_cast<int>(at / a.num_heads), head = static_cast<int>(at - static_cast<int64_t>(row) * a.num_heads);
     int req;
     bool bad;
-    const int my_ctx = kv_load_group(a, row / a.group * a.group, threadIdx.x & 31, req, bad);
+    const int my_ctx = kv_load_group(a, row / a.group * a.group, lane, req, bad);
     const int ctx = __reduce_max_sync(0xffffffffu, my_ctx);
     const int own = ctx > 0 ? kv_parts(ctx, kv_part_shift(ctx, a.parts_shift)) : 0;
     int parts = own;
@@ -861,61 +894,101 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_cons
     }
     pdl_wait();
     pdl_launch_dependents();
-    const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes;
+    const int d = lane % kLanes, sub = lane / kLanes;
     const float4 *po = reinterpret_cast<const float4 *>(a.part_o + at * a.parts_bound * D) + d;
     const float4 *so = reinterpret_cast<const float4 *>(s.so + (entry * a.num_heads + head) * D) + d;
     const int64_t so_step = static_cast<int64_t>(a.num_heads) * kLanes;
-    auto part_at = [&](int p) { return p < own ? po[static_cast<int64_t>(p) * kLanes] : so[(p - own) * so_step]; };
-    // the first parts' outputs are on their way while the bases are compared
-    constexpr int kAhead = 8;
-    float4 y[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-        const int p = grp + i * kGroups;
-        if (p < parts) y[i] = part_at(p);
-    }
-    for (int p = threadIdx.x; p < parts; p += kJoinThreads)
-        ml_s[p] = p < own ? a.part_ml[at * a.parts_bound + p] : s.sml[(entry + p - own) * a.num_heads + head];
-    __syncthreads();
-    float b = -INFINITY;
-    for (int p = threadIdx.x & 31; p < parts; p += 32) b = fmaxf(b, ml_s[p].x);
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, i));
-    const float b0 = b == -INFINITY ? 0.f : b;
-    float total = 0.f;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](int p, const float4 &v) {
-        const float2 l = ml_s[p];
-        const float f = ex2(l.x - b0);
-        total += l.y * f;
-        x.x += v.x * f;
-        x.y += v.y * f;
-        x.z += v.z * f;
-        x.w += v.w * f;
+    const auto ml_at = [&](int p) {
+        return p >= parts ? make_float2(-INFINITY, 0.f)
+                          : p < own ? a.part_ml[at * a.parts_bound + p] : s.sml[(entry + p - own) * a.num_heads + head];
     };
+    // 32 parts at a time, this warp's first: lane l holds the base and sum of part p0 + l
+    float b = -INFINITY, total = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 32 * mine; p0 < parts; p0 += 32 * kWarps) {
+        const float2 ml = ml_at(p0 + lane);
+        float top = ml.x;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-        if (grp + i * kGroups < parts) add(grp + i * kGroups, y[i]);
-#pragma unroll 4
-    for (int p = grp + kAhead * kGroups; p < parts; p += kGroups) add(p, part_at(p));
-    x_s[grp][d] = x;
-    if (d == 0) t_s[grp] = total;
-    __syncthreads();
-    if (grp > 0) return;
+        for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+        top = fmaxf(top, b);
+        const float b0 = top == -INFINITY ? 0.f : top, back = ex2(b - b0);
+        b = top;
+        const float f = ex2(ml.x - b0);
+        total = total * back + ml.y * f;  // (of this lane's parts; added up below)
+        x.x *= back;
+        x.y *= back;
+        x.z *= back;
+        x.w *= back;
+        const int n = min(32, parts - p0);
+#pragma unroll 1
+        for (int i = 0; i < n; i += 8 * kAt) {
+            float4 y[8];
 #pragma unroll
-    for (int i = 1; i < kGroups; ++i) {
-        const float4 v = x_s[i][d];
-        x.x += v.x;
-        x.y += v.y;
-        x.z += v.z;
-        x.w += v.w;
-        total += t_s[i];
+            for (int k = 0; k < 8; ++k) {
+                const int p = p0 + i + k * kAt + sub;
+                y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (p < p0 + n) y[k] = p < own ? po[static_cast<int64_t>(p) * kLanes] : so[(p - own) * so_step];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float w = __shfl_sync(0xffffffffu, f, (i + k * kAt + sub) & 31);
+                if (i + k * kAt + sub >= n) continue;
+                x.x = fmaf(y[k].x, w, x.x);
+                x.y = fmaf(y[k].y, w, x.y);
+                x.z = fmaf(y[k].z, w, x.z);
+                x.w = fmaf(y[k].w, w, x.w);
+            }
+        }
     }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) total += __shfl_xor_sync(0xffffffffu, total, i);
+#pragma unroll
+    for (int i = kLanes; i < 32; i <<= 1) {
+        x.x += __shfl_xor_sync(0xffffffffu, x.x, i);
+        x.y += __shfl_xor_sync(0xffffffffu, x.y, i);
+        x.z += __shfl_xor_sync(0xffffffffu, x.z, i);
+        x.w += __shfl_xor_sync(0xffffffffu, x.w, i);
+    }
+    if constexpr (kWarps > 1) {
+        x_s[threadIdx.x] = x;
+        if (lane == 0) t_s[warp] = make_float2(b, total);
+        __syncthreads();
+        if (warp > 0) return;
+        float top = b;
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) top = fmaxf(top, t_s[i].x);
+        const float b0 = top == -INFINITY ? 0.f : top;
+        total = 0.f;
+        x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            const float f = ex2(t_s[i].x - b0);
+            const float4 v = x_s[32 * i + lane];
+            total += t_s[i].y * f;
+            x.x += v.x * f;
+            x.y += v.y * f;
+            x.z += v.z * f;
+            x.w += v.w * f;
+        }
+        b = top;
+    }
+    const float b0 = b == -INFINITY ? 0.f : b;
     const bool none = total == 0.f;
     const float inv = none ? 0.f : a.v_scale / total;
-    *reinterpret_cast<uint2 *>(a.out + at * D + 4 * d) =
-        none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
-    if (d == 0 && a.lse != nullptr) a.lse[at] = none ? -INFINITY : (b0 + log2f(total)) * 0.6931471805599453f;
+    if (sub == 0)
+        *reinterpret_cast<uint2 *>(a.out + at * D + 4 * d) =
+            none ? make_uint2(0u, 0u) : make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+    if (lane == 0 && a.lse != nullptr) a.lse[at] = none ? -INFINITY : (b0 + log2f(total)) * 0.6931471805599453f;
+}
+
+template <int D>
+cudaError_t launch_join(const KvSharedArgs &s, cudaStream_t stream) {
+    const int64_t pairs = static_cast<int64_t>(s.a.num_rows) * s.a.num_heads;
+    if (pairs > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    constexpr int kPairs = kJoinThreads / 32;
+    if (pairs < kJoinPairs) return launch_pdl(kv_join_kernel<D, 4>, dim3(static_cast<unsigned>(pairs)), dim3(kJoinThreads), 0, stream, s);
+    return launch_pdl(kv_join_kernel<D, 1>, dim3(static_cast<unsigned>((pairs + kPairs - 1) / kPairs)), dim3(kJoinThreads), 0,
+                      stream, s);
 }
 
 // ------------------------------------------------------------------ launches
@@ -989,11 +1062,7 @@ cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, 
     if (a.fp8) e = a.head_dim == 64 ? launch_shared<true, 64>(s, stream) : launch_shared<true, 128>(s, stream);
     else e = a.head_dim == 64 ? launch_shared<false, 64>(s, stream) : launch_shared<false, 128>(s, stream);
     if (e != cudaSuccess) return e;
-    const int64_t grid = static_cast<int64_t>(a.num_rows) * a.num_heads;
-    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const dim3 gr(static_cast<unsigned>(grid)), b(kJoinThreads);
-    return a.head_dim == 64 ? launch_pdl(kv_join_kernel<64>, gr, b, 0, stream, s)
-                            : launch_pdl(kv_join_kernel<128>, gr, b, 0, stream, s);
+    return a.head_dim == 64 ? launch_join<64>(s, stream) : launch_join<128>(s, stream);
 }
 
 }  // namespace dsa
