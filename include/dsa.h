@@ -648,10 +648,13 @@ typedef struct dsa_kv_segments {
     const int32_t *first_row;  /* device [num_segments + 1] (dsa_kv_step.segment_rows) */
     const int32_t *shared_ctx; /* device [num_segments] */
     int32_t num_segments;      /* 0: plain dsa_kv_attention */
+    int64_t least_saved;       /* bytes of the pool that sharing has to save in a segment, or its rows read by
+                                  themselves; 0: the library's choice, 1: any */
 } dsa_kv_segments;
 
 /*
- * Everything not said above is as in dsa_kv_attention.  A row's bits depend on its segment and nothing else.
+ * Everything not said above is as in dsa_kv_attention.  A row's bits depend on its segment and the call's shapes (and
+ * on least_saved: a segment in which too little would be saved is read row by row).
  * workspace: dsa_kv_attention_shared_workspace_size bytes, otherwise as there.  Over the shared tokens of a
  * bf16 pool the softmax weights are rounded to bf16, of an FP8 pool to fp16 (in steps of 2^-31 of their
  * part's largest).

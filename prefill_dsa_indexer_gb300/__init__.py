@@ -72,7 +72,8 @@ class _RopeTensor(ctypes.Structure):
 
 
 class _KvSegments(ctypes.Structure):
-    _fields_ = [("first_row", ctypes.c_void_p), ("shared_ctx", ctypes.c_void_p), ("num_segments", ctypes.c_int32)]
+    _fields_ = [("first_row", ctypes.c_void_p), ("shared_ctx", ctypes.c_void_p), ("num_segments", ctypes.c_int32),
+                ("least_saved", ctypes.c_int64)]
 
 
 class _KvStep(ctypes.Structure):
@@ -568,7 +569,7 @@ _PACK_ROPE_SPEC = struct.Struct("PPif").pack
 _PACK_ROPE_AXES = struct.Struct("PPqPiif").pack
 _PACK_ROPE_TENSORS = [None] + [struct.Struct("PPiiqqqq" * n).pack for n in range(1, 5)]
 _PACK_KV_ROWS = struct.Struct("PPqqii").pack
-_PACK_SEGMENTS = struct.Struct("PPi").pack
+_PACK_SEGMENTS = struct.Struct("PPiq").pack
 _PACK_STEP = struct.Struct("iiqPPPPqPPiiPiiPPPPPPPPP").pack
 _PACK_ROWS = struct.Struct("PqiPPiii0q").pack
 _packed = {}
@@ -926,12 +927,14 @@ def kv_attention(kv, block_table, row_req, row_ctx, max_ctx, q, sm_scale=None, r
 
 
 def kv_attention_shared(kv, block_table, row_req, row_ctx, max_ctx, q, segment_rows, segment_ctx, sm_scale=None,
-                        rows_per_group=1, out=None, lse=None, workspace=None, status=None, stream=None):
+                        rows_per_group=1, out=None, lse=None, workspace=None, status=None, stream=None, least_saved=0):
     """dsa_kv_attention_shared: kv_attention of rows of which segment_rows[s] .. segment_rows[s + 1] - 1 (int32
-    [segments + 1]) have their first segment_ctx[s] tokens (int32 [segments]) in common, read once for all of them."""
+    [segments + 1]) have their first segment_ctx[s] tokens (int32 [segments]) in common, read once for all of them
+    where that saves `least_saved` bytes (0: the library's choice, 1: always)."""
     device, segments = kv.device, segment_ctx.shape[0]
     packed = _PACK_SEGMENTS(_flat(segment_rows, "segment_rows", device, _I32, (segments + 1,)),
-                            _flat(segment_ctx, "segment_ctx", device, _I32, (segments,)), segments)
+                            _flat(segment_ctx, "segment_ctx", device, _I32, (segments,)), segments,
+                            int(least_saved))
     return _attention("dsa_kv_attention_shared", segments, (packed,), kv, block_table, row_req, row_ctx, max_ctx, q,
                       sm_scale, rows_per_group, out, lse, workspace, status, stream)
 

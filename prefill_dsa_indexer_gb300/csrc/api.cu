@@ -971,7 +971,7 @@ static int attention_call(const dsa_kv_cache *cache, const dsa_rows *rows, const
     a.lse = lse;
     a.status = dev_status;
     if (segments == nullptr) return launch_status(launch_kv_attention(a, workspace, static_cast<cudaStream_t>(stream)));
-    const KvSegmentArgs seg = {segments->first_row, segments->shared_ctx, segments->num_segments};
+    const KvSegmentArgs seg = {segments->first_row, segments->shared_ctx, segments->num_segments, segments->least_saved};
     return launch_status(launch_kv_attention_shared(seg, a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
@@ -995,7 +995,7 @@ size_t dsa_kv_attention_shared_workspace_size(const dsa_kv_cache *cache, int32_t
 int dsa_kv_attention_shared(const dsa_kv_cache *cache, const dsa_rows *rows, const dsa_kv_segments *segments,
                             const uint16_t *q, int64_t q_stride, int32_t num_heads, float sm_scale, uint16_t *out,
                             float *lse, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream) {
-    if (segments == nullptr || segments->num_segments < 0) return DSA_ERR_INVALID_ARG;
+    if (segments == nullptr || segments->num_segments < 0 || segments->least_saved < 0) return DSA_ERR_INVALID_ARG;
     const bool some = segments->num_segments > 0 && rows != nullptr && rows->max_ctx > 0;
     return attention_call(cache, rows, some ? segments : nullptr, q, q_stride, num_heads, sm_scale, out, lse, workspace,
                           workspace_bytes, dev_status, stream);

@@ -385,6 +385,7 @@ cudaError_t launch_kv_attention_parts(KvAttnArgs &a, void *workspace, cudaStream
 struct KvSegmentArgs {
     const int32_t *first_row, *shared_ctx;
     int32_t num_segments;
+    int64_t least_saved;
 };
 
 cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, void *workspace, cudaStream_t s);

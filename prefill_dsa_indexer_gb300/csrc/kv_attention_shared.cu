@@ -61,6 +61,7 @@ struct KvSharedArgs {
     const int32_t *row_ctx;       // the call's
     const int32_t *first_row, *shared_ctx;
     int32_t num_segments;
+    int64_t least_saved;          // bytes, in a segment
     int32_t *own_ctx, *row_begin, *row_seg;  // [R]; row_seg: -1 where nothing is shared
     KvSharedSeg *seg;             // [num_segments]
     KvSharedCta *cta;             // [kSharedCtas]
@@ -73,6 +74,19 @@ constexpr int32_t kMinTiles = 4;   // of a part
 
 // Parts of a segment with so many items a part: an item a CTA where that is possible, else few enough that their
 // outputs stay small beside the products, and enough to fill the last round of CTAs.
+// Bytes that sharing has to save: those that the other rows of a segment would read.  One launch more, and another chain
+// of latencies, cost as much as 64 MB of an FP8 pool and 96 MB of a bf16 one; of several segments each bears its share.
+// us, in a graph, each row by itself / shared (4 KV heads of 128, one segment):
+//   FP8, 16 rows of 4K    63 MB  27.7 / 30.4     bf16, 16 rows of 4K   126 MB  25.7 / 25.7
+//   FP8, 64 rows of 1K    66 MB  35.7 / 31.5     bf16, 64 rows of 1K   132 MB  30.2 / 26.3
+//   FP8, 64 rows of 512   33 MB  29.3 / 31.2     bf16, 64 rows of 512   66 MB  23.9 / 26.1
+//   FP8, 16 rows of 8K   126 MB  35.7 / 32.6     bf16, 8 rows of 8K    117 MB  25.5 / 27.0
+int64_t shared_least_bytes(bool fp8, int32_t num_segments) { return (fp8 ? 64ll << 20 : 96ll << 20) / num_segments; }
+
+__host__ __device__ __forceinline__ int64_t token_bytes(const KvAttnArgs &a) {
+    return 2ll * a.kv_heads * a.head_dim * (a.fp8 ? 1 : 2);
+}
+
 __host__ __device__ __forceinline__ int32_t shared_parts_cap(int32_t units) {
     return units <= kSharedCtas / 8 ? kSharedCtas / units : units <= kSharedCtas ? 8 : units <= 4 * kSharedCtas ? 4 : 2;
 }
@@ -82,6 +96,38 @@ __host__ __device__ __forceinline__ int32_t shared_parts_cap(int32_t units) {
 // One CTA.  Its time is that of a chain of dependent reads, so what it goes through again stays in shared memory while it
 // fits.
 constexpr int kSegThreads = 512, kSegRows = 8192, kSegSegs = 64;
+
+// put(segment, first row, rows, shared tokens) of every segment, of no rows where it cannot be, which is reported.  All
+// threads of the CTA.
+template <typename Put>
+__device__ __forceinline__ void check_segments(const KvSharedArgs &s, int32_t *tops, const Put &put) {
+    const KvAttnArgs &a = s.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // a segment begins at or behind every bound before it
+    const int per = (s.num_segments + kSegThreads) / kSegThreads, lo = min(s.num_segments + 1, static_cast<int>(threadIdx.x) * per);
+    const int hi = min(s.num_segments + 1, lo + per);
+    int32_t top = INT32_MIN;
+    for (int i = lo; i < hi; ++i) top = max(top, s.first_row[i]);
+    int32_t upto = top;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto = max(upto, u);
+    }
+    if (lane == 31) tops[warp] = upto;
+    top = __shfl_up_sync(0xffffffffu, upto, 1);
+    if (lane == 0) top = INT32_MIN;
+    __syncthreads();
+    for (int t = 0; t < warp; ++t) top = max(top, tops[t]);
+    for (int i = lo; i < min(hi, s.num_segments); ++i) {
+        const int32_t first = s.first_row[i], end = s.first_row[i + 1], shared = s.shared_ctx[i];
+        const bool bad = first < 0 || first < top || end < first || end > a.num_rows || first % a.group != 0 ||
+                         end % a.group != 0 || shared < 0;
+        if (bad) report(a.status, DSA_ERR_BOUNDS);
+        put(i, bad ? 0 : first, bad ? 0 : end - first, bad ? 0 : shared);
+        top = max(top, first);
+    }
+}
 
 __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __grid_constant__ KvSharedArgs s) {
     const KvAttnArgs &a = s.a;
@@ -114,34 +160,13 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
                 s.row_seg[row0 + r] = -1;
             }
     }
-    // a segment begins at or behind every bound before it
-    const int per = (s.num_segments + kSegThreads) / kSegThreads, lo = min(s.num_segments + 1, static_cast<int>(threadIdx.x) * per);
-    const int hi = min(s.num_segments + 1, lo + per);
-    int32_t top = INT32_MIN;
-    for (int i = lo; i < hi; ++i) top = max(top, s.first_row[i]);
-    int32_t upto = top;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int32_t u = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto = max(upto, u);
-    }
-    if (lane == 31) tops[warp] = upto;
-    top = __shfl_up_sync(0xffffffffu, upto, 1);
-    if (lane == 0) top = INT32_MIN;
-    __syncthreads();
-    for (int t = 0; t < warp; ++t) top = max(top, tops[t]);
-    for (int i = lo; i < min(hi, s.num_segments); ++i) {
-        const int32_t first = s.first_row[i], end = s.first_row[i + 1], shared = s.shared_ctx[i];
-        const bool bad = first < 0 || first < top || end < first || end > a.num_rows || first % a.group != 0 ||
-                         end % a.group != 0 || shared < 0;
-        if (bad) report(a.status, DSA_ERR_BOUNDS);
+    check_segments(s, tops, [&](int i, int32_t row0, int32_t rows, int32_t shared) {
         KvSharedSeg g = {};
-        g.row0 = bad ? 0 : first;
-        g.rows = bad ? 0 : end - first;
-        g.tiles = bad ? 0 : shared / kTile;
+        g.row0 = row0;
+        g.rows = rows;
+        g.tiles = shared / kTile;
         seg[i] = g;
-        top = max(top, first);
-    }
+    });
     __syncthreads();
     // a warp a segment: what all its rows see, and how that is cut
     for (int i = warp; i < s.num_segments; i += kSegThreads / 32) {
@@ -164,6 +189,7 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
         lead = __reduce_min_sync(0xffffffffu, lead);
         live = __reduce_add_sync(0xffffffffu, live);
         g.tiles = live >= 2 ? min(least / kTile, g.tiles) : 0;
+        if ((live - 1ll) * g.tiles * kTile * token_bytes(a) < s.least_saved) g.tiles = 0;
         if (g.tiles > 0) {
             const int cols = g.rows * hpg;
             g.blocks = (cols + 2 * kTile - 1) / (2 * kTile);
@@ -981,6 +1007,14 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_cons
     if (lane == 0 && a.lse != nullptr) a.lse[at] = none ? -INFINITY : (b0 + log2f(total)) * 0.6931471805599453f;
 }
 
+// Checks of kv_segments_kernel alone.
+__global__ void __launch_bounds__(kSegThreads, 1) kv_segments_check_kernel(const __grid_constant__ KvSharedArgs s) {
+    pdl_wait();
+    pdl_launch_dependents();
+    __shared__ int32_t tops[kSegThreads / 32];
+    check_segments(s, tops, [](int, int32_t, int32_t, int32_t) {});
+}
+
 template <int D>
 cudaError_t launch_join(const KvSharedArgs &s, cudaStream_t stream) {
     const int64_t pairs = static_cast<int64_t>(s.a.num_rows) * s.a.num_heads;
@@ -1032,6 +1066,7 @@ cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, 
     s.first_row = seg.first_row;
     s.shared_ctx = seg.shared_ctx;
     s.num_segments = seg.num_segments;
+    s.least_saved = seg.least_saved > 0 ? seg.least_saved : shared_least_bytes(a.fp8, seg.num_segments);
     s.row_ctx = a.row_ctx;
     const size_t rows = align256(static_cast<size_t>(a.num_rows) * 4);
     uint8_t *at = static_cast<uint8_t *>(workspace) +
@@ -1051,7 +1086,15 @@ cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, 
     s.so = reinterpret_cast<float *>(take(align256(entries * static_cast<size_t>(a.head_dim) * 4)));
     s.sml = reinterpret_cast<float2 *>(take(align256(entries * 8)));
     s.a = a;
-    cudaError_t e = launch_pdl(kv_segments_kernel, dim3(1), dim3(kSegThreads), 0, stream, s);
+    cudaError_t e;
+    // nothing to gain in any segment of such a call
+    const int64_t most = (a.num_rows / a.group - 1ll) * a.max_ctx * token_bytes(a);
+    if (most < s.least_saved) {
+        e = launch_kv_attention(a, workspace, stream);
+        if (e != cudaSuccess || a.status == nullptr) return e;
+        return launch_pdl(kv_segments_check_kernel, dim3(1), dim3(kSegThreads), 0, stream, s);
+    }
+    e = launch_pdl(kv_segments_kernel, dim3(1), dim3(kSegThreads), 0, stream, s);
     if (e != cudaSuccess) return e;
     a.row_ctx = s.own_ctx;
     a.row_begin = s.row_begin;

@@ -98,8 +98,8 @@ def test_rope_with_axes_refusals(lib):  # noqa: F811
         assert lib.dsa_rope_with_axes(spec, one, n, dt, tok, None) == want
 
 
-def segments(first=FAKE, ctx=FAKE, n=2):
-    return P._KvSegments(first, ctx, n)
+def segments(first=FAKE, ctx=FAKE, n=2, least=0):
+    return P._KvSegments(first, ctx, n, least)
 
 
 def test_shared_attention_refusals(lib):  # noqa: F811
@@ -114,7 +114,8 @@ def test_shared_attention_refusals(lib):  # noqa: F811
     for bad in (dict(heads=0), dict(heads=62), dict(sm=0.0), dict(sm=float("nan")), dict(q=None), dict(out=None),
                 dict(q=ODD), dict(out=ODD), dict(stride=8191), dict(stride=8196), dict(rw=rows(n=-1)),
                 dict(rw=rows(n=3, g=2)), dict(rw=rows(table=None)), dict(c=kv(base=ODD)), dict(seg=segments(first=None)),
-                dict(seg=segments(ctx=None)), dict(seg=segments(n=-1)), dict(out=FAKE)):
+                dict(seg=segments(ctx=None)), dict(seg=segments(n=-1)), dict(seg=segments(least=-1)),
+                dict(out=FAKE)):
         assert call(**bad) == P.ERR_INVALID_ARG, bad
     assert call(heads=4 * 129, stride=1 << 20) == P.ERR_UNSUPPORTED
     size = lib.dsa_kv_attention_shared_workspace_size

@@ -70,7 +70,9 @@ class Shared:
         self.sm = dim ** -0.5
 
     def run(self, **kw):
+        """Shared wherever there is anything to share, unless `least_saved` says otherwise."""
         status = P.new_status()
+        kw.setdefault("least_saved", 1)
         a = dict(starts=self.starts, shared=self.shared, q=self.q)
         a.update({k: kw.pop(k) for k in tuple(kw) if k in a})
         got = P.kv_attention_shared(self.kv, self.table, self.row_req, self.row_ctx, self.max_ctx, a["q"], a["starts"],
@@ -177,12 +179,13 @@ def test_shared_without_a_segment_is_the_plain_call(fmt):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("starts, shared", [([0, 3, 2, 4], [300, 300, 300]), ([-1, 2], [300]), ([0, 5], [300]),
                                             ([0, 2, 4], [300, -5]), ([4, 0], [300])])
-def test_shared_segments_that_cannot_be_are_reported(fmt, starts, shared):
+@pytest.mark.parametrize("least", [0, 1])
+def test_shared_segments_that_cannot_be_are_reported(fmt, starts, shared, least):
     """And their rows are answered as if in none."""
     c = Shared(17, fmt, [(300, [301, 500, 302, 900])], 2, 4, 128, 64)
     status = P.new_status()
     out, lse = P.kv_attention_shared(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q, ints(starts), ints(shared),
-                                     status=status)
+                                     status=status, least_saved=least)
     torch.cuda.synchronize()
     assert status.item() == P.ERR_BOUNDS
     c.check(out, lse)
@@ -192,7 +195,7 @@ def test_shared_segments_that_cut_a_group_are_reported():
     c = Shared(18, "bf16", [(300, [301, 500])], 2, 4, 128, 64, group=2)
     status = P.new_status()
     out, lse = P.kv_attention_shared(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q, ints([0, 3]), ints([300]),
-                                     rows_per_group=2, status=status)
+                                     rows_per_group=2, status=status, least_saved=1)
     torch.cuda.synchronize()
     assert status.item() == P.ERR_BOUNDS
     c.check(out, lse)
@@ -216,7 +219,7 @@ def test_shared_device_errors_are_reported(fmt):
         if what == "own page":
             c.table[1, 11] = -1
         out, lse = P.kv_attention_shared(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q, c.starts, c.shared,
-                                         status=status)
+                                         status=status, least_saved=1)
         torch.cuda.synchronize()
         assert status.item() == P.ERR_BOUNDS, what
         if what in ("ctx", "negative", "request"):
@@ -364,7 +367,7 @@ def test_shared_calls_in_graphs_on_streams_and_at_once():
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             P.kv_attention_shared(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q, c.starts, c.shared,
-                                  rows_per_group=c.group, out=o, lse=l, workspace=ws)
+                                  rows_per_group=c.group, out=o, lse=l, workspace=ws, least_saved=1)
         graphs.append((graph, o, l, ws, torch.cuda.Stream()))
     for _ in range(4):
         for _, o, l, ws, _ in graphs:
@@ -381,6 +384,23 @@ def test_shared_calls_in_graphs_on_streams_and_at_once():
         for (_, o, l, _, _), w in zip(graphs, want):
             assert torch.equal(o, w[0]) and torch.equal(l, w[1])
         assert torch.equal(eager[0], want[1][0]) and torch.equal(eager[1], want[1][1])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_shared_where_it_pays(fmt):
+    """The library's choice: a call too small by its shapes is the plain one, bit for bit, and so is a segment that saves
+    too little beside one that saves enough."""
+    c = Shared(33, fmt, [(700, [701, 900, 1000])], 2, 4, 128, 64)
+    got, want = c.run(least_saved=0), P.kv_attention(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    tokens, most = 2 * 128 * (1 if fmt == "fp8" else 2) * 2, (64 if fmt == "fp8" else 96) << 20
+    n = -(-most // (2 * 15 * tokens * 128)) * 128  # the least that pays for 16 rows, of two segments
+    c = Shared(34, fmt, [(n, [n + i for i in range(16)]), (n - 128, [n] * 16)], 2, 2, 128, 128)
+    out, lse = c.run(least_saved=0)
+    both, plain = c.run(), P.kv_attention(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q)
+    assert torch.equal(out[:16], both[0][:16]) and torch.equal(out[16:], plain[0][16:])
+    assert not torch.equal(lse[:16], plain[1][:16])
+    c.check(out, lse, rows=[0, 7, 15, 16, 31])
 
 
 def test_shared_calls_without_a_row():
