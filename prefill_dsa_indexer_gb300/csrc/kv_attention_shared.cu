@@ -345,20 +345,18 @@ struct SharedCfg {
     static constexpr int kSlotBytes = kTile * kRowBytes;              // K or V of a tile as stored
     static constexpr int kQBytes = kTile * D * 2;                     // a chain's columns, in bf16 or as two e4m3 terms
     static constexpr int kVBytes = kFp8 ? kTile * D * 2 : 0;          // V of a tile in fp16
-    static constexpr int kVBufs = kFp8 ? 2 : 0;
-    // K and V alternate in one ring.  (FP8: an even number, so that a slot is K's or V's for good)
-    static constexpr int kSlots = (229376 - 2 * kQBytes - kVBufs * kVBytes) / kSlotBytes > 12
-                                      ? 12
-                                      : (229376 - 2 * kQBytes - kVBufs * kVBytes) / kSlotBytes;
-    static_assert(kSlots >= 5 && (!kFp8 || kSlots % 2 == 0), "ring");
+    static constexpr int kVBufs = kFp8 ? 3 : 0;
+    // A ring for K and one for V, each of an even number of slots: a tile's are those of every other tile.
+    static constexpr int kRoom = (229376 - 2 * kQBytes - kVBufs * kVBytes) / (2 * kSlotBytes) / 2 * 2, kSlots = kRoom > 6 ? 6 : kRoom;
+    static_assert(kSlots >= 2, "rings");
     static constexpr int kWarpgroups = kFp8 ? 4 : 3;  // two of softmax, (one that converts V,) the producer and the issuer
     static constexpr int kThreads = 128 * kWarpgroups;
     static constexpr int kRun = kFp8 ? 16 : 32;    // scores in registers at a time: a fourth warpgroup leaves 128 a thread
     static constexpr uint32_t kTmemO = 2 * kTile;  // the chains' scores, then their outputs
     static constexpr int OFF_V = 2 * kQBytes;
     static constexpr int OFF_RING = OFF_V + kVBufs * kVBytes;
-    static constexpr int OFF_BARS = OFF_RING + kSlots * kSlotBytes;
-    static constexpr int kNumBars = 2 * kSlots + 1 + 2 * 8;
+    static constexpr int OFF_BARS = OFF_RING + 2 * kSlots * kSlotBytes;
+    static constexpr int kNumBars = 4 * kSlots + 1 + 2 * 6 + 2 * 3;
     static constexpr int OFF_MISC = OFF_BARS + kNumBars * 8;
     static constexpr int OFF_FACTORS = OFF_MISC + 16;
     static constexpr int kSmemBytes = OFF_FACTORS + (kFp8 ? 2 * kTile * 4 : 0) + 1024;
@@ -462,38 +460,40 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
     const KvAttnArgs &a = s.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BARS);  // [NS] K or V landed
-    uint64_t *empty = full + NS;                                        // [NS] it has been used
-    uint64_t *q_full = empty + NS;                                      // [2] a chain's queries are in place
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BARS);  // [2 NS] K, then V landed
+    uint64_t *empty = full + 2 * NS;                                    // [2 NS] it has been used
+    uint64_t *q_full = empty + 2 * NS;                                      // [2] a chain's queries are in place
     uint64_t *q_empty = q_full + 2;                                     // the item's scores are done
     uint64_t *s_full = q_empty + 1;                                     // [2] a chain's scores in TMEM
     uint64_t *p_full = s_full + 2;                                      // [2] its weights in their place
     uint64_t *o_full = p_full + 2;                                      // [2] its item's output is done
-    uint64_t *v_full = o_full + 2;                                      // [2] V in fp16
-    uint64_t *v_empty = v_full + 2;                                     // [2] and its product done
-    uint64_t *my_turn = v_empty + 2;                                    // [2] the other chain's warp has issued
+    uint64_t *v_full = o_full + 2;                                      // [3] V in fp16
+    uint64_t *v_empty = v_full + 3;                                     // [3] and its product done
+    uint64_t *my_turn = v_empty + 3;                                    // [2] the other chain's warp has issued
     uint64_t *drained = my_turn + 2;                                    // [2] after a wait gave up: no MMA is left
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     float *factors_s = reinterpret_cast<float *>(smem + C::OFF_FACTORS);  // [2][kTile] (FP8)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
-    constexpr int kProducer = 4 * (C::kWarpgroups - 1), kIssuer = kProducer + 1;
+    constexpr int kProducer = 4 * (C::kWarpgroups - 1), kIssuer = kProducer + 2;  // two warps each
     if (threadIdx.x == 0) {
         *abort = 0;
-        for (int i = 0; i < NS; ++i) {
+        for (int i = 0; i < 2 * NS; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], kFp8 && (i & 1) ? 4 : 2);
+            mbar_init(&empty[i], kFp8 && i >= NS ? 4 : 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 4);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
-            mbar_init(&v_full[i], 4);
-            mbar_init(&v_empty[i], 2);
             mbar_init(&my_turn[i], 1);
             mbar_init(&drained[i], 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&v_full[i], 4);
+            mbar_init(&v_empty[i], 2);
         }
         mbar_init(q_empty, 2);
         fence_mbar_init();
@@ -523,9 +523,9 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
             bool ok = true;
             for (; more && ok; more = w.next(s)) {
                 for (int i = 0; i < w.tiles && ok; ++i, ++n) {
-                    const uint32_t turn = 2 * n + 1, slot = turn % NS, buf = n & 1;
-                    ok = wait_mbar_warp(&full[slot], turn / NS & 1, abort) &&
-                         wait_mbar_warp(&v_empty[buf], (n >> 1 & 1) ^ 1, abort);
+                    const uint32_t slot = NS + n % NS, buf = n % 3;
+                    ok = wait_mbar_warp(&full[slot], n / NS & 1, abort) &&
+                         wait_mbar_warp(&v_empty[buf], (n / 3 & 1) ^ 1, abort);
                     if (!ok) break;
                     const uint8_t *from = smem + C::OFF_RING + slot * C::kSlotBytes;
                     uint8_t *to = smem + C::OFF_V + buf * C::kVBytes;
@@ -551,11 +551,13 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                 }
             }
             if (!ok) gave_up(abort, a.status);
-        } else if (warp == kProducer) {
-            // ---- K and V: a tile is `boxes` runs of tokens by kBoxes columns, one a lane
+        } else if (warp < kIssuer) {
+            // ---- K, and V by another warp (in one order V, whose place is taken until its weights are done, would hold up
+            // the next K): a tile is `boxes` runs of tokens by kBoxes columns, one a lane
+            const int v = __shfl_sync(0xffffffffu, warp - kProducer, 0);
             const int box_rows = a.page_size, boxes = kTile >> a.page_shift;
             const int b = lane / C::kBoxes, x = lane % C::kBoxes;
-            uint32_t turn = 0;  // slots filled
+            uint32_t turn = 0;  // tiles
             bool go = true;
             for (; more && go; more = w.next(s)) {
                 const int32_t *table = a.block_table + static_cast<int64_t>(w.g.req) * a.bt_stride;
@@ -563,7 +565,7 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                 auto load_ids = [&](int p) { return p + lane < pages ? table[page0 + p + lane] : 0; };
                 int batch = 0;  // page ids batch .. batch + 31 of the item are in `ids`, one per lane
                 int32_t ids = load_ids(0), ids_next = load_ids(32);
-                for (int i = 0; i < w.tiles && go; ++i) {
+                for (int i = 0; i < w.tiles; ++i, ++turn) {
                     const int p = i << 7 >> a.page_shift;
                     if (p >= batch + 32) {
                         batch += 32;
@@ -575,73 +577,67 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                         report(a.status, DSA_ERR_BOUNDS);
                         id = 0;
                     }
-                    const int y = (id * a.kv_heads + w.head) * 2 * a.page_size;
-#pragma unroll 1
-                    for (int v = 0; v < 2; ++v, ++turn) {  // K, then V
-                        const uint32_t slot = turn % NS;
-                        if (!wait_mbar_warp(&empty[slot], (turn / NS & 1) ^ 1, abort)) {
-                            gave_up(abort, a.status);
-                            go = false;
-                            break;
-                        }
-                        if (lane == 0) mbar_arrive_expect_tx(&full[slot], C::kSlotBytes);
-                        __syncwarp();
-                        if (b < boxes)
-                            tma_load_2d(smem + C::OFF_RING + slot * C::kSlotBytes + x * C::kPlane + b * box_rows * C::kBoxBytes,
-                                        &kv_map, &full[slot], x * C::kBoxBytes, y + v * a.page_size);
+                    const int y = ((id * a.kv_heads + w.head) * 2 + v) * a.page_size;
+                    const uint32_t slot = v * NS + turn % NS;
+                    if (!wait_mbar_warp(&empty[slot], (turn / NS & 1) ^ 1, abort)) {
+                        gave_up(abort, a.status);
+                        go = false;
+                        break;
                     }
+                    if (lane == 0) mbar_arrive_expect_tx(&full[slot], C::kSlotBytes);
+                    __syncwarp();
+                    if (b < boxes)
+                        tma_load_2d(smem + C::OFF_RING + slot * C::kSlotBytes + x * C::kPlane + b * box_rows * C::kBoxBytes,
+                                    &kv_map, &full[slot], x * C::kBoxBytes, y);
                 }
             }
             if (*abort && lane == 0) {  // leave no copy in flight behind
                 for (uint32_t i = turn > NS ? turn - NS : 0; i < turn; ++i) {
                     const long long t0 = clock64();
-                    while (!mbar_try_wait(&full[i % NS], i / NS & 1) && clock64() - t0 < kWaitTimeoutCycles) {
+                    while (!mbar_try_wait(&full[v * NS + i % NS], i / NS & 1) && clock64() - t0 < kWaitTimeoutCycles) {
                     }
                 }
             }
-        } else if (warp == kIssuer || warp == kIssuer + 1) {
-            // ---- the products.  An MMA's issue lasts as long as its passage, and what lies between two runs of MMAs
-            // (some 300 cycles of waits and commits) is another warp's time: chains that take the same tiles have a warp
-            // each, and the warps take turns, so that one chain's products stay beside the other's softmax (left to
-            // themselves the chains fall into step: 3,690 cycles for a tile of both, in turns 2,400; one warp for both
-            // 3,150).  Of chains that share tiles out one warp issues for both, since a barrier's parity tells a slot's
-            // phases apart for a warp alone that waits for every one of them.  (All of an item's tiles have landed and all
-            // its weights have been seen when the next begins.)  MMAs of a thread run in the order of their issue, so a
-            // chain's next scores, which take the place of its weights, are right behind the product that reads those.
-            // A warp goes through all of this together, so that descriptors stay in uniform registers, and one lane
-            // issues
+        } else {
+            // ---- the products, a warp a chain: an MMA's issue lasts as long as its passage, and what lies between two runs
+            // of MMAs (1,000 cycles of commits and waits) is the other warp's time.  The warps take turns, so that one
+            // chain's products stay beside the other's softmax: left to themselves the chains fall into step (3,690
+            // cycles for a tile of both, in turns 2,450; one warp for both 3,150).  MMAs of a thread run in the order of
+            // their issue, so a chain's next scores, which take the place of its weights, are right behind the product that
+            // reads those.  A warp goes through all of this together, so that descriptors stay in uniform registers, and
+            // one lane issues.
+            // (Of tiles that the chains share out a warp waits for its own alone.  The slots of every other tile are the
+            // same ones, V's conversions come in order, and all of an item's tiles have landed when the next begins: so the
+            // phase before an awaited one is over, and a barrier's parity tells.)
             constexpr uint32_t kIdescS = make_idesc(kTile, kTile, kFp8 ? 0 : 1, kFp8 ? 0 : 1, false, false);
             constexpr uint32_t kIdescO = make_idesc(kTile, D, kFp8 ? 0 : 1, kFp8 ? 0 : 1, false, true);
             const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), ring = base + C::OFF_RING;
             const uint32_t t_mem = __shfl_sync(0xffffffffu, tmem, 0);
-            const int me = __shfl_sync(0xffffffffu, warp - kIssuer, 0);
-            uint32_t n = 0, items = 0, p_phases = 0, turns = 0;  // tiles before the item, items, a bit a chain, turns taken
+            const int c = __shfl_sync(0xffffffffu, warp - kIssuer, 0);
+            uint32_t n = 0, items = 0, p_count = 0, turns = 0;  // tiles before the item, items, products, turns taken
             bool ok = true;
             for (; more && ok; more = w.next(s), ++items) {
                 const bool wide = __shfl_sync(0xffffffffu, w.wide, 0);
                 const int tiles = __shfl_sync(0xffffffffu, w.tiles, 0);
-                const int c0 = me, c1 = wide ? me : 1 - me;  // its chains (none: c1 < c0)
-                auto steps_of = [&](int c) { return wide ? tiles : (tiles + 1 - c) / 2; };
-                auto tile_of = [&](int c, int j) { return n + static_cast<uint32_t>(wide ? j : 2 * j + c); };
+                const int most = wide ? tiles : (tiles + 1) / 2, steps = wide ? tiles : (tiles + 1 - c) / 2;
+                auto tile_of = [&](int j) { return n + static_cast<uint32_t>(wide ? j : 2 * j + c); };
                 auto used = [&](uint64_t *bar) {  // two arrivals: one of each chain, or both of the only one
+                    if (!wide) mbar_arrive(bar);
                     mma_commit(bar);
-                    if (!wide) mma_commit(bar);
                 };
-                // the product of chain c's step j (from 0 on) and the scores of step j + 1 (where there is one)
-                auto step = [&](int c, int j) {
-                    const uint32_t tile = tile_of(c, j), v_turn = 2 * tile + 1, v_slot = v_turn % NS, buf = tile & 1;
-                    const uint32_t k_turn = 2 * tile_of(c, j + 1), k_slot = k_turn % NS;
-                    const bool product = j >= 0, next = j + 1 < steps_of(c);
-                    if (next) ok = ok && wait_mbar_warp(&full[k_slot], k_turn / NS & 1, abort);
+                ok = wait_mbar_warp(&q_full[0], items & 1, abort) && wait_mbar_warp(&q_full[1], items & 1, abort);
+                // the product of step j (from 0 on) and the scores of step j + 1 (where there is one)
+                for (int j = -1; j < most && ok; ++j) {
+                    const uint32_t tile = tile_of(j), v_slot = NS + tile % NS, buf = tile % 3;
+                    const uint32_t k_tile = tile_of(j + 1), k_slot = k_tile % NS;
+                    const bool product = j >= 0 && j < steps, next = j + 1 < steps;
+                    if (next) ok = ok && wait_mbar_warp(&full[k_slot], k_tile / NS & 1, abort);
                     if (product)
-                        ok = ok && (kFp8 ? wait_mbar_warp(&v_full[buf], tile >> 1 & 1, abort)
-                                         : wait_mbar_warp(&full[v_slot], v_turn / NS & 1, abort));
-                    if (wide) ok = ok && wait_mbar_warp(&my_turn[c], (turns++ & 1) ^ (c == 0 ? 1 : 0), abort);
-                    if (product) {
-                        ok = ok && wait_mbar_warp(&p_full[c], p_phases >> c & 1, abort);
-                        p_phases ^= 1u << c;
-                    }
-                    if (!ok) return;
+                        ok = ok && (kFp8 ? wait_mbar_warp(&v_full[buf], tile / 3 & 1, abort)
+                                         : wait_mbar_warp(&full[v_slot], tile / NS & 1, abort));
+                    ok = ok && wait_mbar_warp(&my_turn[c], (turns++ & 1) ^ (c == 0 ? 1 : 0), abort);
+                    if (product) ok = ok && wait_mbar_warp(&p_full[c], p_count++ & 1, abort);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t st = t_mem + c * kTile, ot = t_mem + C::kTmemO + c * D;
                     const uint32_t v = kFp8 ? base + C::OFF_V + buf * C::kVBytes : ring + v_slot * C::kSlotBytes;
@@ -672,34 +668,28 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                                 }
                             }
                         }
-                        if (wide) mbar_arrive(&my_turn[1 - c]);
+                        mbar_arrive(&my_turn[1 - c]);
                         if (next) {
                             mma_commit(&s_full[c]);
                             used(&empty[k_slot]);
-                        } else {
+                        } else if (product) {
                             mma_commit(&o_full[c]);
                         }
                         if (product) used(kFp8 ? &v_empty[buf] : &empty[v_slot]);
                     }
                     __syncwarp();
-                };
-                ok = wait_mbar_warp(&q_full[0], items & 1, abort) && wait_mbar_warp(&q_full[1], items & 1, abort);
-                for (int j = -1; c0 <= c1 && j < steps_of(c0) && ok; ++j)
-#pragma unroll 1
-                    for (int c = c0; c <= c1 && j < steps_of(c) && steps_of(c) > 0 && ok; ++c) step(c, j);
+                }
                 if (!ok) break;
                 if (elect_one()) mma_commit(q_empty);
                 __syncwarp();
-                for (int c = 0; c < 2; ++c)
-                    if (c < c0 || c > c1) p_phases ^= (steps_of(c) & 1u) << c;
                 n += static_cast<uint32_t>(tiles);
             }
             if (!ok) gave_up(abort, a.status);
             if (*abort) {  // leave no MMA in flight behind
-                if (elect_one()) mma_commit(&drained[me]);
+                if (elect_one()) mma_commit(&drained[c]);
                 __syncwarp();
                 const long long t0 = clock64();
-                while (!mbar_try_wait(&drained[me], 0) && clock64() - t0 < kWaitTimeoutCycles) {
+                while (!mbar_try_wait(&drained[c], 0) && clock64() - t0 < kWaitTimeoutCycles) {
                 }
             }
         }
