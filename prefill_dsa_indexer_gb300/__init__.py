@@ -840,28 +840,43 @@ class KvPlan:
     allocate nothing: row_req, row_ctx, positions, slots [max_rows], row_start [num_requests + 1], granted and context
     [num_requests], free_count [1] and segment_rows [num_segments + 1] hold what the last `run` made."""
 
-    def __init__(self, num_requests, max_rows, page_size, num_pages, rows_per_group=1, num_segments=0, device="cuda"):
-        n, rows, self.num_segments = int(num_requests), int(max_rows), int(num_segments)
-        self.page_size, self.num_pages, self.rows_per_group = int(page_size), int(num_pages), int(rows_per_group)
+    _NAMES = ("row_req", "row_ctx", "positions", "slots", "row_start", "granted", "context", "free_count",
+              "segment_rows")
 
-        def new(size, value):
-            return torch.full((size,), value, dtype=torch.int32, device=device)
-        self.row_req, self.row_ctx = new(rows, 0), new(rows, 0)
-        self.positions, self.slots = new(rows, -1), new(rows, -1)
-        self.row_start, self.granted, self.context, self.free_count = new(n + 1, 0), new(n, 0), new(n, 0), new(1, 0)
-        self.segment_rows = new(self.num_segments + 1 if self.num_segments else 0, 0)
-        self.status = new_status(device)
+    def __init__(self, num_requests, max_rows, page_size, num_pages, rows_per_group=1, num_segments=0, device="cuda"):
+        n, rows, segments = int(num_requests), int(max_rows), int(num_segments)
+        self._sizes = n, rows, segments, int(rows_per_group), int(page_size), int(num_pages)
+        sizes = (rows, rows, rows, rows, n + 1, n, n, 1, segments + 1 if segments else 0)
+        self._buffers = {name: torch.full((size,), -1 if name in ("positions", "slots") else 0, dtype=torch.int32,
+                                          device=device) for name, size in zip(self._NAMES, sizes)}
+        self._addresses = [t.data_ptr() for t in self._buffers.values()]
+        self._device = self.row_req.get_device()
+        self._status = new_status(device)
+        if self._device < 0:
+            raise DsaError("libdsa takes device tensors only")
 
     def run(self, context, new_tokens, block_table, free_pages, free_count, first_own=None, segment_requests=None,
             stream=None):
         """context and free_count may be the plan's own of the step before.  Returns self."""
-        if (segment_requests is None) != (self.num_segments == 0):
-            raise DsaError(f"the plan is of {self.num_segments} segments")
-        kv_plan(context, new_tokens, block_table, free_pages, free_count, self.page_size, self.num_pages, self.row_req,
-                self.row_ctx, self.positions, self.slots, first_own, segment_requests,
-                None if segment_requests is None else self.segment_rows, self.row_start, self.granted, self.context,
-                self.free_count, self.rows_per_group, self.status, stream)
+        n, rows, segments, group, page_size, num_pages = self._sizes
+        if (segment_requests is None) != (segments == 0):
+            raise DsaError(f"the plan is of {segments} segments")
+        d, of, table = self._device, (n,), block_table.shape
+        if len(table) != 2 or table[0] != n:
+            raise DsaError(f"the block table is [{n}, pages]: got {tuple(table)}")
+        _launch("dsa_kv_plan", d, stream, _PACK_STEP(
+            n, page_size, num_pages, _flat(context, "context", d, _I32, of), _flat(new_tokens, "new_tokens", d, _I32, of),
+            0 if first_own is None else _flat(first_own, "first_own", d, _I32, of),
+            _flat(block_table, "block_table", d, _I32), table[1], _flat(free_pages, "free_pages", d, _I32),
+            _flat(free_count, "free_count", d, _I32, (1,)), free_pages.numel(), segments,
+            0 if segments == 0 else _flat(segment_requests, "segment_requests", d, _I32, (segments + 1,)), rows, group,
+            *self._addresses), self._status.data_ptr())
         return self
+
+
+for _name in KvPlan._NAMES:  # (read only: a step is written at the addresses of these tensors)
+    setattr(KvPlan, _name, property(lambda self, _name=_name: self._buffers[_name]))
+KvPlan.status = property(lambda self: self._status)
 
 
 def kv_attention_workspace_size(kv, num_rows, num_heads, max_ctx) -> int:

@@ -312,8 +312,7 @@ cudaError_t launch_rope(const RopeArgs &a, int32_t dtype, cudaStream_t s);
 cudaError_t launch_kv_insert(const KvInsertArgs &a, cudaStream_t s);
 
 // ---- a step's rows, slots and pages (plan.cu)
-constexpr int kPlanMaxRequests = DSA_KV_PLAN_MAX_REQUESTS;  // (their sums are in shared memory: 128 KB)
-constexpr int kPlanOneCtaRows = 1024;
+constexpr int kPlanMaxRequests = DSA_KV_PLAN_MAX_REQUESTS;  // (their sums are in shared memory: 192 KB)
 
 struct KvPlanArgs {
     int32_t num_requests, page_size, page_shift;

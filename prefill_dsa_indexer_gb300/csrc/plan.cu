@@ -8,9 +8,12 @@
 //
 // Sums over the requests and then four numbers a row: a few hundred KB for the largest steps, so nothing but latency
 // counts, and it is one launch.  Every CTA of one cluster makes the same sums over all requests (lengths are few) and
-// keeps them in shared memory; a row finds its request there by bisection.  What one CTA writes and another reads (pages
-// that ended requests give back) or what a call may update in place (contexts, the stack's count, which all CTAs read
-// first) is set apart by cluster barriers.
+// keeps them in shared memory; rows, pages begun and pages given back are shared out one by one, and each finds its
+// request there by bisection.  (A warp a request for the pages: 27 us where 28 of 257 requests gave back 500 pages each.)
+// What one CTA writes and another reads (pages given back) or what a call may update in place (contexts, the stack's
+// count, which all CTAs read first) is set apart by cluster barriers.
+#include <atomic>
+
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -18,7 +21,9 @@ namespace dsa {
 
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
+// A cluster of the largest portable size: one CTA takes as long for 8 rows (4.7 us in a graph), and 32 us in the place of
+// 12 for 2,048 requests of 16,384 rows.
+constexpr int kThreads = 1024, kWarps = kThreads / 32, kCtas = 8;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -74,37 +79,50 @@ __device__ __forceinline__ Sums shifted(const Sums &s, int by) {
             __shfl_up_sync(0xffffffffu, s.back, by)};
 }
 
-__device__ __forceinline__ int32_t capped(int64_t x, int32_t most) {
-    return static_cast<int32_t>(x < most ? x : most);
+__device__ __forceinline__ int32_t capped(int64_t x) { return static_cast<int32_t>(x < INT32_MAX ? x : INT32_MAX); }
+
+// The last of `sums` (ascending, n + 1 of them, the first 0) at or before x < sums[n].
+__device__ __forceinline__ int32_t owner(const int32_t *sums, int32_t n, int32_t x) {
+    int32_t b = 0, e = n;
+    while (e - b > 1) {
+        const int32_t m = (b + e) >> 1;
+        if (sums[m] <= x) b = m;
+        else e = m;
+    }
+    return b;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) kv_plan_kernel(const __grid_constant__ KvPlanArgs a) {
-    // [requests + 1] first row of each; [requests] place among the pages begun (or -1: no tokens for it this time), or
-    // among those given back
+    // [requests + 1] each: rows, pages begun and pages given back before a request's
     extern __shared__ int32_t sums_s[];
     __shared__ Sums warp_s[kWarps];
+    __shared__ int32_t taken_s[kWarps];
     const int n = a.num_requests;
-    int32_t *start = sums_s, *place = sums_s + n + 1;
+    int32_t *start = sums_s, *begun = start + n + 1, *back = begun + n + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(cluster_rank()), ctas = static_cast<int>(gridDim.x);
+    const int rank = static_cast<int>(cluster_rank()), threads = static_cast<int>(gridDim.x) * kThreads;
+    const int tid = rank * kThreads + static_cast<int>(threadIdx.x);
     const bool first = rank == 0;
     pdl_wait();
     pdl_launch_dependents();
-    int32_t count = *a.free_count;
-    if (count < 0 || count > a.free_capacity) {
-        if (first && threadIdx.x == 0) report(a.status, DSA_ERR_BOUNDS);
-        count = count < 0 ? 0 : a.free_capacity;
-    }
-    // ---- sums: a thread takes neighbouring requests
-    const int per = (n + kThreads - 1) / kThreads, lo = min(n, static_cast<int>(threadIdx.x) * per), hi = min(n, lo + per);
-    Sums mine = {0, 0, 0};
-    for (int i = lo; i < hi; ++i) {
+    const int32_t given = *a.free_count;
+    const int32_t old = min(max(given, 0), a.free_capacity);
+    if (old != given && tid == 0) report(a.status, DSA_ERR_BOUNDS);
+    // ---- sums: every length is read once, side by side, then a thread takes neighbouring requests
+    for (int i = threadIdx.x; i < n; i += kThreads) {
         const Request r = read_request(a, i);
         if (r.bad && first) report(a.status, DSA_ERR_BOUNDS);
-        mine.add({r.need, r.wide, r.back});
+        start[i] = static_cast<int32_t>(r.wide);
+        begun[i] = r.need;
+        back[i] = r.back;
     }
+    __syncthreads();
+    const int per = (n + kThreads - 1) / kThreads | 1;  // (odd: without bank conflicts)
+    const int lo = min(n, static_cast<int>(threadIdx.x) * per), hi = min(n, lo + per);
+    Sums mine = {0, 0, 0};
+    for (int i = lo; i < hi; ++i) mine.add({begun[i], static_cast<uint32_t>(start[i]), back[i]});
     Sums upto = mine;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const Sums s = shifted(upto, o);
         if (lane >= o) upto.add(s);
@@ -113,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_plan_kernel(const __grid_const
     __syncthreads();
     if (warp == 0) {
         Sums s = warp_s[lane];
-#pragma unroll
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
             const Sums u = shifted(s, o);
             if (lane >= o) s.add(u);
@@ -125,60 +143,57 @@ __global__ void __launch_bounds__(kThreads, 1) kv_plan_kernel(const __grid_const
     Sums at = {upto.need - mine.need, upto.wide - mine.wide, upto.back - mine.back};
     if (warp > 0) at.add(warp_s[warp - 1]);
     // what ended requests give back goes onto the stack first
-    if (count + total.back > a.free_capacity && first && threadIdx.x == 0) report(a.status, DSA_ERR_BOUNDS);
-    const int32_t old = count;
-    count = capped(count + total.back, a.free_capacity);
+    const int32_t count = static_cast<int32_t>(min(old + total.back, static_cast<int64_t>(a.free_capacity)));
+    if (old + total.back > a.free_capacity && tid == 0) report(a.status, DSA_ERR_BOUNDS);
+    const auto fits = [&](int32_t need, uint32_t wide, int64_t pages, int64_t rows) {  // with the sums behind the request
+        return (need == 0 || pages <= count) && (wide == 0 || rows <= a.max_rows);
+    };
+    const auto granted = [&](const Request &r, int i) {
+        return fits(r.need, r.wide, begun[i] + static_cast<int64_t>(r.need), start[i] + static_cast<int64_t>(r.wide));
+    };
     bool denied = false;
+    int32_t taken = 0;  // pages of those that get them: of all up to the first that does not
     for (int i = lo; i < hi; ++i) {
-        const Request r = read_request(a, i);
-        start[i] = capped(at.wide, a.max_rows);
-        const bool fits = (r.need == 0 || at.need + r.need <= count) && (r.wide == 0 || at.wide + r.wide <= a.max_rows);
-        denied |= !fits;
-        place[i] = r.ended ? capped(at.back, INT32_MAX) : fits ? capped(at.need, INT32_MAX) : -1;
-        at.add({r.need, r.wide, r.back});
+        const Sums r = {begun[i], static_cast<uint32_t>(start[i]), back[i]};
+        start[i] = capped(at.wide);
+        begun[i] = capped(at.need);
+        back[i] = capped(at.back);
+        at.add(r);
+        const bool ok = fits(static_cast<int32_t>(r.need), static_cast<uint32_t>(r.wide), at.need, at.wide);
+        denied |= !ok;
+        if (ok && r.need > 0) taken = static_cast<int32_t>(at.need);
     }
-    if (threadIdx.x == 0) start[n] = capped(total.wide, a.max_rows);
+    if (threadIdx.x == 0) {
+        start[n] = capped(total.wide);
+        begun[n] = capped(total.need);
+        back[n] = capped(total.back);
+    }
     if (denied && first && a.granted == nullptr) report(a.status, DSA_ERR_BOUNDS);
+    taken = __reduce_max_sync(0xffffffffu, taken);
+    if (lane == 0) taken_s[warp] = taken;
     __syncthreads();
-    // ---- pages given back: a warp a request
-    const int warps = ctas * kWarps, my_warp = rank * kWarps + warp;
+    taken = __reduce_max_sync(0xffffffffu, taken_s[lane]);
+    // ---- pages given back
     if (total.back > 0) {
-        for (int i0 = my_warp * 32; i0 < n; i0 += warps * 32) {
-            const int i = i0 + lane;
-            Request r = {};
-            if (i < n) r = read_request(a, i);
-            for (uint32_t some = __ballot_sync(0xffffffffu, r.back > 0); some != 0; some &= some - 1) {
-                const int l = __ffs(some) - 1, j = i0 + l;
-                const int32_t back = __shfl_sync(0xffffffffu, r.back, l), had = __shfl_sync(0xffffffffu, r.had, l);
-                const int32_t *from = a.block_table + j * a.bt_stride + (had - back);
-                for (int k = lane; k < back; k += 32) {
-                    const int64_t to = static_cast<int64_t>(old) + place[j] + k;
-                    if (to < a.free_capacity) a.free_pages[to] = from[k];
-                }
-            }
+        for (int t = tid; t < count - old; t += threads) {
+            const int32_t i = owner(back, n, t);
+            const Request r = read_request(a, i);
+            a.free_pages[old + t] = a.block_table[i * a.bt_stride + (r.had - r.back) + (t - back[i])];
         }
         cluster_meet();
     }
     // ---- rows
-    const auto page_of = [&](int i, const Request &r, int p) {
-        return p < r.had ? a.block_table[i * a.bt_stride + p] : a.free_pages[count - 1 - (place[i] + p - r.had)];
-    };
-    const int threads = ctas * kThreads, tid = rank * kThreads + static_cast<int>(threadIdx.x);
     for (int row = tid; row < a.max_rows; row += threads) {
         int32_t req = 0, pos = -1, slot = -1;
         if (row < start[n]) {
-            int b = 0, e = n;  // the last request that starts at or before the row
-            while (e - b > 1) {
-                const int m = (b + e) >> 1;
-                if (start[m] <= row) b = m;
-                else e = m;
-            }
-            req = b;
+            req = owner(start, n, row);
             const Request r = read_request(a, req);
             const int32_t j = row - start[req];
-            if (j < r.fresh && place[req] >= 0) {
+            if (j < r.fresh && granted(r, req)) {
                 pos = r.ctx + j;
-                const int32_t id = page_of(req, r, pos >> a.page_shift);
+                const int32_t p = pos >> a.page_shift;
+                const int32_t id = p < r.had ? a.block_table[req * a.bt_stride + p]
+                                             : a.free_pages[count - 1 - (begun[req] + p - r.had)];
                 if (id >= 0 && id < a.num_pages) slot = id * a.page_size + (pos & (a.page_size - 1));
                 else report(a.status, DSA_ERR_BOUNDS);
             }
@@ -188,34 +203,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_plan_kernel(const __grid_const
         if (a.positions != nullptr) a.positions[row] = pos;
         if (a.slots != nullptr) a.slots[row] = slot;
     }
-    // ---- table entries of the pages begun: the first of each request by its lane, longer runs by the warp
-    for (int i0 = my_warp * 32; i0 < n; i0 += warps * 32) {
-        const int i = i0 + lane;
-        Request r = {};
-        if (i < n) r = read_request(a, i);
-        const int32_t need = i < n && place[i] >= 0 ? r.need : 0;
-        if (need > 0) a.block_table[i * a.bt_stride + r.had] = page_of(i, r, r.had);
-        for (uint32_t some = __ballot_sync(0xffffffffu, need > 1); some != 0; some &= some - 1) {
-            const int l = __ffs(some) - 1, j = i0 + l;
-            const int32_t pages = __shfl_sync(0xffffffffu, need, l), had = __shfl_sync(0xffffffffu, r.had, l);
-            for (int k = 1 + lane; k < pages; k += 32)
-                a.block_table[j * a.bt_stride + had + k] = a.free_pages[count - 1 - (place[j] + k)];
-        }
-    }
-    // ---- what may stand where it was read from
-    int64_t taken = 0;  // the requests that get pages are those up to the first that does not
-    for (int i = lo; i < hi; ++i) {
+    // ---- table entries of the pages begun
+    for (int t = tid; t < taken; t += threads) {
+        const int32_t i = owner(begun, n, t);
         const Request r = read_request(a, i);
-        if (r.need > 0 && place[i] >= 0) taken = static_cast<int64_t>(place[i]) + r.need;
+        a.block_table[i * a.bt_stride + r.had + (t - begun[i])] = a.free_pages[count - 1 - t];
     }
     cluster_meet();
+    // ---- what may stand where it was read from (a thread reads the lengths that it alone replaces)
     for (int i = tid; i < n; i += threads) {
-        // (a thread reads the lengths that it alone replaces)
         const Request r = read_request(a, i);
-        const int32_t granted = place[i] >= 0 ? r.fresh : 0;
-        if (a.granted != nullptr) a.granted[i] = granted;
-        if (a.context_out != nullptr) a.context_out[i] = r.ended ? 0 : r.ctx + granted;
-        if (a.row_start != nullptr) a.row_start[i] = start[i];
+        const int32_t fresh = granted(r, i) ? r.fresh : 0;
+        if (a.granted != nullptr) a.granted[i] = fresh;
+        if (a.context_out != nullptr) a.context_out[i] = r.ended ? 0 : r.ctx + fresh;
+        if (a.row_start != nullptr) a.row_start[i] = min(start[i], a.max_rows);
     }
     for (int i = tid; i <= a.num_segments && a.num_segments > 0; i += threads) {
         int32_t req = a.segment_requests[i];
@@ -223,34 +224,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_plan_kernel(const __grid_const
             report(a.status, DSA_ERR_BOUNDS);
             req = req < 0 ? 0 : n;
         }
-        a.segment_rows[i] = start[req];
+        a.segment_rows[i] = min(start[req], a.max_rows);
     }
-    if (!first) return;
-    if (threadIdx.x == 0 && a.row_start != nullptr) a.row_start[n] = start[n];
-    // the largest `taken` of the threads
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, o));
-    if (lane == 0) warp_s[warp].need = taken;
-    __syncthreads();
-    if (warp == 0) {
-        taken = warp_s[lane].need;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, o));
-        if (lane == 0 && a.free_count_out != nullptr) *a.free_count_out = count - static_cast<int32_t>(taken);
+    if (tid == 0) {
+        if (a.row_start != nullptr) a.row_start[n] = min(start[n], a.max_rows);
+        if (a.free_count_out != nullptr) *a.free_count_out = count - taken;
     }
 }
 
 }  // namespace
 
 cudaError_t launch_kv_plan(const KvPlanArgs &a, cudaStream_t s) {
-    const size_t smem = (2 * static_cast<size_t>(a.num_requests) + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>((2 * kPlanMaxRequests + 1) * 4));
-    if (e != cudaSuccess) return e;
-    // one CTA writes the few rows of a decode step sooner than eight that have to meet
-    const unsigned ctas = a.max_rows > kPlanOneCtaRows || a.num_requests > kPlanOneCtaRows ? 8 : 1;
+    const size_t smem = 3 * (static_cast<size_t>(a.num_requests) + 1) * 4;
+    if (smem > 49152) {
+        static std::atomic<uint64_t> configured{0};  // a bit a device
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = 1ull << (dev & 63);
+        if (dev >= 64 || !(configured.load() & bit)) {
+            e = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     3 * (kPlanMaxRequests + 1) * 4);
+            if (e != cudaSuccess) return e;
+            if (dev < 64) configured.fetch_or(bit);
+        }
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
+    cfg.gridDim = dim3(kCtas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -258,7 +258,7 @@ cudaError_t launch_kv_plan(const KvPlanArgs &a, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.x = kCtas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
