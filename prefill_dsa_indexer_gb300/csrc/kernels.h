@@ -349,8 +349,8 @@ struct KvAttnArgs {
     int32_t num_rows;
     int32_t max_ctx;
     int32_t group;     // rows per group
-    const int32_t *row_begin;  // or NULL: each row's tokens before this one (a multiple of 128) are read elsewhere, and
-                               // row_ctx counts from it; of rows that share a group, one
+    const int32_t *row_begin;  // or NULL: each row's tokens before this one (a multiple of 128; below that, how its parts
+                               // are cut) are read elsewhere, and row_ctx counts from it; of a row group, one
     bool keep_parts;   // a row's only part goes to the workspace too
     const uint16_t *q;
     int64_t q_stride;

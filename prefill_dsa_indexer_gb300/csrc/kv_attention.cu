@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     pdl_wait();
     const bool direct = kv_direct(a);
-    if (direct) pdl_launch_dependents();
+    if (direct || a.keep_parts) pdl_launch_dependents();
     KvSchedule *sched = reinterpret_cast<KvSchedule *>(smem + C::OFF_SCHED);
     kv_fill_schedule(a, sched);
     __syncthreads();
@@ -333,10 +333,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
         }
+        // (Where the parts are kept, what comes next takes an SM as a whole, and is let start at once.)
         // With many items only now: the merge's CTAs beside this one's start took it 2,000 cycles and more (23 ragged
         // rows of head_dim 64: 20.8 us against 19.8).  With few it is better early (four rows of 256 tokens: 7.3 us
         // against 8.4).
-        if (!direct) pdl_launch_dependents();
+        if (!direct && !a.keep_parts) pdl_launch_dependents();
         if (*abort && lane == 0) {  // leave no copy in flight behind
             for (int i = max(0, issued - C::kStages); i < issued; ++i) {
                 const long long t0 = clock64();
@@ -764,7 +765,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const __gri
     bool bad;
     const int my_ctx = kv_load_group(a, static_cast<int>(at / a.num_heads) / a.group * a.group, threadIdx.x & 31, req, bad);
     const int ctx = __reduce_max_sync(0xffffffffu, my_ctx);
-    const int parts = kv_parts(ctx, kv_part_shift(ctx, a.parts_shift));
+    const int parts = kv_parts(ctx, kv_part_shift(ctx, a.parts_shift, kPartMin));
     pdl_wait();
     pdl_launch_dependents();
     if (parts == 1) return;  // written by the attention kernel

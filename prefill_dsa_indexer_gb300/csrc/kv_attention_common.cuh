@@ -37,10 +37,19 @@ __host__ __device__ __forceinline__ int32_t kv_parts_shift(int32_t kv_heads) {
     return kv_heads >= 8 ? 4 : kv_heads >= 4 ? 5 : kv_heads >= 2 ? 6 : 7;
 }
 
-// log2 of a part's tokens: the smallest k >= kPartMin with 2^(k + parts_shift) >= ctx.
-__device__ __forceinline__ int32_t kv_part_shift(int32_t ctx, int32_t parts_shift) {
-    return kPartMin + (32 - __clz(max(ctx - 1, 0) >> (kPartMin + parts_shift)));
+// log2 of a part's tokens: the smallest k >= part_min with 2^(k + parts_shift) >= ctx.
+__device__ __forceinline__ int32_t kv_part_shift(int32_t ctx, int32_t parts_shift, int32_t part_min) {
+    return part_min + (32 - __clz(max(ctx - 1, 0) >> (part_min + parts_shift)));
 }
+
+// What KvAttnArgs.row_begin says of a row: the first of its tokens that are read here, and log2 of its parts' least
+// tokens below that (kPartMin or more).
+constexpr int32_t kBeginUnit = 128;
+
+__device__ __forceinline__ int32_t kv_begin(const KvAttnArgs &a, int row) {
+    return a.row_begin == nullptr ? kPartMin : a.row_begin[row];
+}
+__device__ __forceinline__ int32_t kv_part_min(int32_t begin) { return begin & (kBeginUnit - 1); }
 
 __device__ __forceinline__ int32_t kv_parts(int32_t ctx, int32_t part_shift) {
     return max(1, (ctx + (1 << part_shift) - 1) >> part_shift);
@@ -71,8 +80,8 @@ struct KvSchedule {
 };
 
 // Cost of a group with this longest context, for one KV head and column block.
-__device__ __forceinline__ uint32_t kv_cost(int32_t ctx, int32_t parts_shift) {
-    return kv_parts(ctx, kv_part_shift(ctx, parts_shift)) * kItemCost + ((ctx + 127) >> 7);
+__device__ __forceinline__ uint32_t kv_cost(int32_t ctx, int32_t part_shift) {
+    return kv_parts(ctx, part_shift) * kItemCost + ((ctx + 127) >> 7);
 }
 
 __device__ __forceinline__ bool kv_direct(const KvAttnArgs &a) { return a.items <= gridDim.x; }  // an item a CTA
@@ -95,8 +104,7 @@ __device__ __forceinline__ int kv_load_group(const KvAttnArgs &a, int row0, int 
 
 // A row group's entries of the block table, from the first token that its rows read here.
 __device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req, int row0) {
-    const int32_t *table = a.block_table + static_cast<int64_t>(req) * a.bt_stride;
-    return a.row_begin == nullptr ? table : table + (a.row_begin[row0] >> a.page_shift);
+    return a.block_table + static_cast<int64_t>(req) * a.bt_stride + ((kv_begin(a, row0) & -kBeginUnit) >> a.page_shift);
 }
 
 // Fills `sched`; every thread of the CTA calls it, then __syncthreads.
@@ -123,7 +131,8 @@ __device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule
                 bad |= kv_refused(a, n[r], req[r], req[0]);
                 ctx = max(ctx, n[r]);
             }
-            sum += kv_cost(bad ? 0 : ctx, a.parts_shift);
+            if (bad) ctx = 0;
+            sum += kv_cost(ctx, kv_part_shift(ctx, a.parts_shift, kv_part_min(kv_begin(a, row0))));
         }
         sched->before[e + 1] = sum * (static_cast<uint64_t>(a.kv_heads) * a.col_blocks);
     }
@@ -160,7 +169,7 @@ struct KvCursor {
         my_ctx = kv_load_group(a, row0, lane, req, bad);
         ctx = __reduce_max_sync(0xffffffffu, my_ctx);
         ctx_min = __reduce_min_sync(0xffffffffu, my_ctx);
-        shift = kv_part_shift(ctx, a.parts_shift);
+        shift = kv_part_shift(ctx, a.parts_shift, kv_part_min(kv_begin(a, row0)));
         parts = kv_parts(ctx, shift);
     }
 
@@ -209,7 +218,7 @@ struct KvCursor {
 #pragma unroll 1
         for (;; ++group) {
             load_group(a, lane);
-            unit = kv_cost(ctx, a.parts_shift);
+            unit = kv_cost(ctx, shift);
             const uint64_t all = static_cast<uint64_t>(unit) * heads;
             if (start + all > from) break;
             start += all;

@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
     const bool direct = kv_direct(a);
-    if (direct) pdl_launch_dependents();
+    if (direct || a.keep_parts) pdl_launch_dependents();
     KvSchedule *sched = reinterpret_cast<KvSchedule *>(smem + C::OFF_SCHED);
     kv_fill_schedule(a, sched);
     __syncthreads();
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                 }
             }
             // (with many items only now, as in kv_attention_kernel; 4 x 8K: 14.6 us early, 12.9 so)
-            if (!direct) pdl_launch_dependents();
+            if (!direct && !a.keep_parts) pdl_launch_dependents();
             if (*abort && lane == 0) {  // leave no copy in flight behind: the last tiles issued in either ring
                 for (int v = 0; v < 2; ++v) {
                     const uint32_t ring = v ? C::kV : C::kK;
