@@ -39,7 +39,7 @@ constexpr int kTile = 128;       // tokens of a tile, and columns of a chain
 constexpr int kSharedCtas = 152;  // an SM each; a constant, so that the split does not go by the device
 
 // A segment's work.
-struct KvSharedSeg {
+struct alignas(16) KvSharedSeg {
     int32_t row0, rows;
     int32_t tiles;          // of its shared tokens
     int32_t req;            // whose block table lists them
@@ -51,7 +51,7 @@ struct KvSharedSeg {
 static_assert(sizeof(KvSharedSeg) == 48, "segment layout");
 
 // Where a CTA begins, and the cost at which its share of all ends.
-struct KvSharedCta {
+struct alignas(16) KvSharedCta {
     int32_t seg, item;  // seg -1: nothing to do
     int64_t end;
 };
@@ -68,6 +68,17 @@ struct KvSharedArgs {
     float *so;                    // [entry][H][D]
     float2 *sml;                  // [entry][H]
 };
+
+// As it is in L2: read before the kernel's wait, past what an earlier kernel may have left in L1.
+__device__ __forceinline__ KvSharedSeg read_segment(const KvSharedSeg *p) {
+    union {
+        int4 words[3];
+        KvSharedSeg seg;
+    } u;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) u.words[i] = __ldcg(reinterpret_cast<const int4 *>(p) + i);
+    return u.seg;
+}
 
 constexpr int32_t kItemTiles = 6;  // what an item costs beside its tiles
 constexpr int32_t kMinTiles = 4;   // of a part
@@ -308,15 +319,15 @@ struct SharedCursor {
         return true;
     }
     __device__ __forceinline__ void load(const KvSharedArgs &a) {
-        g = a.seg[s];
+        g = read_segment(a.seg + s);
         items = a.a.kv_heads * g.blocks * g.parts;
     }
     __device__ __forceinline__ bool first(const KvSharedArgs &a) {
-        const KvSharedCta w = a.cta[blockIdx.x];
-        if (w.seg < 0) return false;
-        s = w.seg;
-        i = w.item;
-        end = w.end;
+        const int4 w = __ldcg(reinterpret_cast<const int4 *>(a.cta + blockIdx.x));  // (a KvSharedCta)
+        if (w.x < 0) return false;
+        s = w.x;
+        i = w.y;
+        end = static_cast<int64_t>(static_cast<uint32_t>(w.w)) << 32 | static_cast<uint32_t>(w.z);
         load(a);
         at = g.cost0 + static_cast<int64_t>(i) * g.cost;
         return place(a);
@@ -903,9 +914,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_cons
     const int own = ctx > 0 ? kv_parts(ctx, kv_part_shift(ctx, a.parts_shift, kv_part_min(kv_begin(a, row)))) : 0;
     int parts = own;
     int64_t entry = 0;  // the first shared part
-    const int32_t seg = s.row_seg[row];
+    const int32_t seg = __ldcg(s.row_seg + row);
     if (seg >= 0) {
-        const KvSharedSeg g = s.seg[seg];
+        const KvSharedSeg g = read_segment(s.seg + seg);
         const int r = row - g.row0, block = (r * a.hpg + head % a.hpg) / (2 * kTile);
         const bool wide = g.rows * a.hpg - block * 2 * kTile > kTile;
         parts += wide ? g.parts : 2 * g.parts;

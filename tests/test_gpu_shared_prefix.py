@@ -403,6 +403,45 @@ def test_shared_where_it_pays(fmt):
     c.check(out, lse, rows=[0, 7, 15, 16, 31])
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("kv_heads, hpg, rows", [(40, 1, 130), (33, 3, 100), (5, 16, 600), (160, 1, 5)])
+def test_shared_of_many_heads(fmt, kv_heads, hpg, rows):
+    """More items than CTAs in every part, or nearly."""
+    c = Shared(35, fmt, [(700, [701 + i % 50 for i in range(rows)]), (400, [401, 500])], kv_heads, hpg, 64, 64)
+    out, lse = c.run()
+    c.check(out, lse, rows=[0, 1, rows // 2, rows - 1, rows, rows + 1])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_shared_of_very_many_rows(fmt):
+    """More rows than the segments' kernel keeps in shared memory."""
+    c = Shared(36, fmt, [(520, [528 + i % 9 for i in range(1040)]), (130, [140] * 2)], 1, 2, 64, 16, group=8, pad=2)
+    out, lse = c.run()
+    c.check(out, lse, rows=[0, 1, 4099, 8191, 8192, 8319, 8320, 8335, 8336, 8351])
+    again = c.run()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_shared_calls_that_follow_one_another_in_one_workspace():
+    """Of different segments, pools and shapes, without a wait between them: nothing of one call is taken for another's."""
+    cases = [Shared(37, "fp8", [(1500, [1501 + i for i in range(9)]), (400, [500, 600])], 2, 8, 128, 64),
+             Shared(38, "fp8", [(300, [301] * 3), (2000, [2001 + i for i in range(30)])], 2, 8, 128, 64),
+             Shared(39, "bf16", [(900, [901, 1000]), (500, [501, 700]), (2500, [2600] * 20)], 2, 8, 128, 64)]
+    want = [c.run() for c in cases]
+    need = max(P.kv_attention_shared_workspace_size(c.kv, c.q.shape[0], c.q.shape[1], c.max_ctx, c.shared.numel())
+               for c in cases)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = []
+    for i in range(60):
+        c = cases[(i * 7 + i // 5) % 3]
+        got.append(((i * 7 + i // 5) % 3, P.kv_attention_shared(
+            c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q, c.starts, c.shared, rows_per_group=c.group, workspace=ws,
+            least_saved=1)))
+    torch.cuda.synchronize()
+    for i, (o, l) in got:
+        assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
+
+
 def test_shared_calls_without_a_row():
     c = Shared(32, "bf16", [(300, [301, 302])], 2, 4, 128, 64)
     none = ints([], (0,))
