@@ -365,7 +365,7 @@ struct SharedCfg {
     static_assert(kSlots >= 2, "rings");
     static constexpr int kWarpgroups = kFp8 ? 4 : 3;  // two of softmax, (one that converts V,) the producer and the issuer
     static constexpr int kThreads = 128 * kWarpgroups;
-    static constexpr int kRun = kFp8 ? 16 : 32;    // scores in registers at a time: a fourth warpgroup leaves 128 a thread
+    static constexpr int kRun = 16;                // scores in registers at a time (32: bf16 67.0 us in the place of 65.0)
     static constexpr uint32_t kTmemO = 2 * kTile;  // the chains' scores, then their outputs
     static constexpr int OFF_V = 2 * kQBytes;
     static constexpr int OFF_RING = OFF_V + kVBufs * kVBytes;
@@ -628,6 +628,8 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
             const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), ring = base + C::OFF_RING;
             const uint32_t t_mem = __shfl_sync(0xffffffffu, tmem, 0);
             const int c = __shfl_sync(0xffffffffu, warp - kIssuer, 0);
+            const uint32_t st = t_mem + c * kTile, ot = t_mem + C::kTmemO + c * D;
+            const bool lead = elect_one();
             uint32_t n = 0, items = 0, p_count = 0, turns = 0;  // tiles before the item, items, products, turns taken
             bool ok = true;
             for (; more && ok; more = w.next(s), ++items) {
@@ -635,6 +637,8 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                 const int tiles = __shfl_sync(0xffffffffu, w.tiles, 0);
                 const int most = wide ? tiles : (tiles + 1) / 2, steps = wide ? tiles : (tiles + 1 - c) / 2;
                 auto tile_of = [&](int j) { return n + static_cast<uint32_t>(wide ? j : 2 * j + c); };
+                const uint32_t q = base + (wide ? c : 0) * C::kQBytes;
+                const uint64_t qd = !kFp8 || D == 128 ? sdesc_sw128(q, 16, 1024) : sdesc_sw64(q);
                 auto used = [&](uint64_t *bar) {  // two arrivals: one of each chain, or both of the only one
                     if (!wide) mbar_arrive(bar);
                     mma_commit(bar);
@@ -645,6 +649,10 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                     const uint32_t tile = tile_of(j), v_slot = NS + tile % NS, buf = tile % 3;
                     const uint32_t k_tile = tile_of(j + 1), k_slot = k_tile % NS;
                     const bool product = j >= 0 && j < steps, next = j + 1 < steps;
+                    const uint32_t k = ring + k_slot * C::kSlotBytes;
+                    const uint32_t v = kFp8 ? base + C::OFF_V + buf * C::kVBytes : ring + v_slot * C::kSlotBytes;
+                    const uint64_t vd = sdesc_sw128(v, kTile * 128, 1024);
+                    const uint64_t kd = !kFp8 || D == 128 ? sdesc_sw128(k, 16, 1024) : sdesc_sw64(k);
                     if (next) ok = ok && wait_mbar_warp(&full[k_slot], k_tile / NS & 1, abort);
                     if (product)
                         ok = ok && (kFp8 ? wait_mbar_warp(&v_full[buf], tile / 3 & 1, abort)
@@ -653,12 +661,8 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                     if (product) ok = ok && wait_mbar_warp(&p_full[c], p_count++ & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t st = t_mem + c * kTile, ot = t_mem + C::kTmemO + c * D;
-                    const uint32_t v = kFp8 ? base + C::OFF_V + buf * C::kVBytes : ring + v_slot * C::kSlotBytes;
-                    const uint32_t q = base + (wide ? c : 0) * C::kQBytes, k = ring + k_slot * C::kSlotBytes;
-                    if (elect_one()) {
+                    if (lead) {
                         if (product) {
-                            const uint64_t vd = sdesc_sw128(v, kTile * 128, 1024);
                             const uint32_t add = j > 0;
 #pragma unroll
                             for (int i = 0; i < kTile / 16; ++i)
@@ -666,15 +670,12 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                         }
                         if (next) {
                             if constexpr (kFp8) {
-                                const uint64_t qd = D == 128 ? sdesc_sw128(q, 16, 1024) : sdesc_sw64(q);
-                                const uint64_t kd = D == 128 ? sdesc_sw128(k, 16, 1024) : sdesc_sw64(k);
 #pragma unroll
                                 for (int term = 0; term < 2; ++term)
 #pragma unroll
                                     for (int i = 0; i < D / 32; ++i)
                                         mma_f8(st, qd + term * (kTile * D / 16) + i * 2, kd + i * 2, kIdescS, term + i > 0);
                             } else {
-                                const uint64_t qd = sdesc_sw128(q, 16, 1024), kd = sdesc_sw128(k, 16, 1024);
 #pragma unroll
                                 for (int i = 0; i < D / 16; ++i) {
                                     const uint32_t off = (i >> 2) * (kTile * 128 / 16) + (i & 3) * 2;
@@ -694,13 +695,13 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (elect_one()) mma_commit(q_empty);
+                if (lead) mma_commit(q_empty);
                 __syncwarp();
                 n += static_cast<uint32_t>(tiles);
             }
             if (!ok) gave_up(abort, a.status);
             if (*abort) {  // leave no MMA in flight behind
-                if (elect_one()) mma_commit(&drained[c]);
+                if (lead) mma_commit(&drained[c]);
                 __syncwarp();
                 const long long t0 = clock64();
                 while (!mbar_try_wait(&drained[c], 0) && clock64() - t0 < kWaitTimeoutCycles) {
@@ -794,11 +795,9 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                     const float2 sc2 = make_float2(scale, scale), nb2 = make_float2(nb, nb);
                     float2 t0 = make_float2(0.f, 0.f), t1 = make_float2(0.f, 0.f);
                     constexpr int kRun = C::kRun;
+                    static_assert(kRun == 16, "load");
                     uint32_t h[2][kRun];
-                    auto load = [&](int i) {
-                        if constexpr (kRun == 32) tmem_ld32(st + 32 * i, h[i & 1]);
-                        else tmem_ld16(st + 16 * i, h[i & 1]);
-                    };
+                    auto load = [&](int i) { tmem_ld16(st + kRun * i, h[i & 1]); };
                     load(0);
 #pragma unroll
                     for (int i = 0; i < kTile / kRun; ++i) {
