@@ -85,14 +85,20 @@ constexpr int32_t kMinTiles = 4;   // of a part
 
 // Parts of a segment with so many items a part: an item a CTA where that is possible, else few enough that their
 // outputs stay small beside the products, and enough to fill the last round of CTAs.
-// Bytes that sharing has to save: those that the other rows of a segment would read.  One launch more, and another chain
-// of latencies, cost as much as 64 MB of an FP8 pool and 96 MB of a bf16 one; of several segments each bears its share.
-// us, in a graph, each row by itself / shared (4 KV heads of 128, one segment):
-//   FP8, 16 rows of 4K    63 MB  27.7 / 30.4     bf16, 16 rows of 4K   126 MB  25.7 / 25.7
-//   FP8, 64 rows of 1K    66 MB  35.7 / 31.5     bf16, 64 rows of 1K   132 MB  30.2 / 26.3
-//   FP8, 64 rows of 512   33 MB  29.3 / 31.2     bf16, 64 rows of 512   66 MB  23.9 / 26.1
-//   FP8, 16 rows of 8K   126 MB  35.7 / 32.6     bf16, 8 rows of 8K    117 MB  25.5 / 27.0
-int64_t shared_least_bytes(bool fp8, int32_t num_segments) { return (fp8 ? 64ll << 20 : 96ll << 20) / num_segments; }
+// Bytes that sharing has to save (those that the other rows of a segment would read) to make up for two launches more and
+// another chain of latencies.  A call whose shapes leave less is dsa_kv_attention's; in one that is not, where half of
+// that is spent already, a segment has to save half, and of several each its share.
+// us in a graph, 1 to 200 tokens of their own, each row by itself / in a call that shares nothing / shared:
+//                       FP8, 4 heads of 128      bf16, 4 heads of 128     bf16, 3 heads of 64
+//   8 rows of 8K         56 MB  21 / 28 / 30     112 MB  20 / 27 / 25      42 MB  12 / 19 / 20
+//   16 rows of 8K       120 MB  30 / 36 / 32     240 MB  28 / 35 / 26      90 MB  18 / 25 / 20
+//   64 rows of 1K        63 MB  30 / 33 / 33     126 MB  25 / 29 / 26      47 MB  14 / 20 / 22
+//   64 rows of 2K       126 MB  42 / 45 / 33     252 MB  35 / 40 / 26      95 MB  19 / 24 / 22
+//   4 rows of 32K        96 MB  26 / 34 / 34     192 MB  27 / 33 / 30      72 MB  16 / 23 / 21
+int64_t shared_least_bytes(const KvAttnArgs &a) {
+    const int64_t mb = a.fp8 ? 120 : 200;
+    return (a.head_dim == 64 ? mb * 2 / 3 : mb) << 20;
+}
 
 __host__ __device__ __forceinline__ int64_t token_bytes(const KvAttnArgs &a) {
     return 2ll * a.kv_heads * a.head_dim * (a.fp8 ? 1 : 2);
@@ -489,6 +495,16 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     float *factors_s = reinterpret_cast<float *>(smem + C::OFF_FACTORS);  // [2][kTile] (FP8)
 
+    // What this kernel reads was complete when the one before it (kv_attention*.cu), which writes nothing that this one
+    // reads or writes, passed its own wait and let this one start.  So it begins while that one ends, and waits for it at
+    // the end, for the join's sake.
+    pdl_launch_dependents();
+    SharedCursor w;
+    bool more = w.first(s);
+    if (!more) {
+        pdl_wait();
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
     constexpr int kProducer = 4 * (C::kWarpgroups - 1), kIssuer = kProducer + 2;  // two warps each
     if (threadIdx.x == 0) {
@@ -521,14 +537,6 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // What this kernel reads was complete when the one before it (kv_attention*.cu), which writes nothing that this one
-    // reads or writes, passed its own wait and let this one start.  So it begins while that one ends, and waits for it at
-    // the end, for the join's sake.
-    pdl_launch_dependents();
-
-    SharedCursor w;
-    bool more = w.first(s);
-
     if (wg >= 2) {
         if (kFp8 && wg == 2) {
             // ---- V's codes as fp16: thread = token
@@ -1069,7 +1077,8 @@ cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, 
     s.first_row = seg.first_row;
     s.shared_ctx = seg.shared_ctx;
     s.num_segments = seg.num_segments;
-    s.least_saved = seg.least_saved > 0 ? seg.least_saved : shared_least_bytes(a.fp8, seg.num_segments);
+    const int64_t least = seg.least_saved > 0 ? seg.least_saved : shared_least_bytes(a);
+    s.least_saved = seg.least_saved > 0 ? seg.least_saved : least / 2 / seg.num_segments;
     s.row_ctx = a.row_ctx;
     const size_t rows = align256(static_cast<size_t>(a.num_rows) * 4);
     uint8_t *at = static_cast<uint8_t *>(workspace) +
@@ -1092,7 +1101,7 @@ cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, 
     cudaError_t e;
     // nothing to gain in any segment of such a call
     const int64_t most = (a.num_rows / a.group - 1ll) * a.max_ctx * token_bytes(a);
-    if (most < s.least_saved) {
+    if (most < least) {
         e = launch_kv_attention(a, workspace, stream);
         if (e != cudaSuccess || a.status == nullptr) return e;
         return launch_pdl(kv_segments_check_kernel, dim3(1), dim3(kSegThreads), 0, stream, s);

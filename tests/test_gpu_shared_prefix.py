@@ -388,19 +388,21 @@ def test_shared_calls_in_graphs_on_streams_and_at_once():
 
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_shared_where_it_pays(fmt):
-    """The library's choice: a call too small by its shapes is the plain one, bit for bit, and so is a segment that saves
-    too little beside one that saves enough."""
+    """The library's choice: a call too small by its shapes is the plain one, bit for bit, and a segment that saves too
+    little beside one that saves enough is as if it shared nothing."""
     c = Shared(33, fmt, [(700, [701, 900, 1000])], 2, 4, 128, 64)
     got, want = c.run(least_saved=0), P.kv_attention(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
-    tokens, most = 2 * 128 * (1 if fmt == "fp8" else 2) * 2, (64 if fmt == "fp8" else 96) << 20
-    n = -(-most // (2 * 15 * tokens * 128)) * 128  # the least that pays for 16 rows, of two segments
+    token, least = 2 * 2 * 128 * (1 if fmt == "fp8" else 2), (120 if fmt == "fp8" else 200) << 20
+    n = -(-least // (4 * 15 * token * 128)) * 128  # the least that pays for 16 rows, of two segments
     c = Shared(34, fmt, [(n, [n + i for i in range(16)]), (n - 128, [n] * 16)], 2, 2, 128, 128)
-    out, lse = c.run(least_saved=0)
-    both, plain = c.run(), P.kv_attention(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q)
-    assert torch.equal(out[:16], both[0][:16]) and torch.equal(out[16:], plain[0][16:])
-    assert not torch.equal(lse[:16], plain[1][:16])
-    c.check(out, lse, rows=[0, 7, 15, 16, 31])
+    assert 31 * c.max_ctx * token < least  # too little by its shapes
+    got, plain = c.run(least_saved=0), P.kv_attention(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q)
+    assert torch.equal(got[0], plain[0]) and torch.equal(got[1], plain[1])
+    c = Shared(34, fmt, [(n, [n + i for i in range(16)]), (n - 128, [n] * 16)], 2, 2, 128, 128, after=[64, 4 * n])
+    (out, lse), first, both = c.run(least_saved=0), c.run(shared=ints([n, 0])), c.run()
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1]) and not torch.equal(lse[16:32], both[1][16:32])
+    c.check(out, lse, rows=[0, 7, 15, 16, 31, 32, 33])
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
