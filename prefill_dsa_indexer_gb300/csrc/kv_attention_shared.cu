@@ -495,16 +495,6 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
     float *factors_s = reinterpret_cast<float *>(smem + C::OFF_FACTORS);  // [2][kTile] (FP8)
 
-    // What this kernel reads was complete when the one before it (kv_attention*.cu), which writes nothing that this one
-    // reads or writes, passed its own wait and let this one start.  So it begins while that one ends, and waits for it at
-    // the end, for the join's sake.
-    pdl_launch_dependents();
-    SharedCursor w;
-    bool more = w.first(s);
-    if (!more) {
-        pdl_wait();
-        return;
-    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
     constexpr int kProducer = 4 * (C::kWarpgroups - 1), kIssuer = kProducer + 2;  // two warps each
     if (threadIdx.x == 0) {
@@ -537,6 +527,12 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // What this kernel reads was complete when the one before it (kv_attention*.cu), which writes nothing that this one
+    // reads or writes, passed its own wait and let this one start.  So it begins while that one ends, and waits for it at
+    // the end, for the join's sake.
+    pdl_launch_dependents();
+    SharedCursor w;
+    bool more = w.first(s);
     if (wg >= 2) {
         if (kFp8 && wg == 2) {
             // ---- V's codes as fp16: thread = token
