@@ -80,7 +80,7 @@ __device__ __forceinline__ KvSharedSeg read_segment(const KvSharedSeg *p) {
     return u.seg;
 }
 
-constexpr int32_t kItemTiles = 6;  // what an item costs beside its tiles
+constexpr int32_t kItemTiles = 12;  // what an item costs beside its tiles
 constexpr int32_t kMinTiles = 4;   // of a part
 
 // Parts of a segment with so many items a part: an item a CTA where that is possible, else few enough that their
@@ -112,7 +112,7 @@ __host__ __device__ __forceinline__ int32_t shared_parts_cap(int32_t units) {
 
 // One CTA.  Its time is that of a chain of dependent reads, so what it goes through again stays in shared memory while it
 // fits.
-constexpr int kSegThreads = 512, kSegRows = 8192, kSegSegs = 64;
+constexpr int kSegThreads = 256, kSegRows = 8192, kSegSegs = 64;
 
 // put(segment, first row, rows, shared tokens) of every segment, of no rows where it cannot be, which is reported.  All
 // threads of the CTA.
@@ -213,17 +213,26 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
             g.req = a.row_req[lead];
             const bool narrow = cols - (g.blocks - 1) * 2 * kTile <= kTile;  // the last block is of one chain's columns
             const int each = g.blocks == 1 && narrow ? 1 : 2;                // tiles of one chain that a tile makes
-            // the parts that end first, if an item a CTA runs at a time; of those that are as good the fewest
+            // The parts that end first, if all segments are as this one and a CTA runs an item at a time; the fewest of
+            // those that are as good.  Beside others, which may be small, the most of those within a quarter.  us, so and
+            // as if each segment were alone: eight of 8 rows of 8K 45 and 68, sixteen of 16 rows of 4K 82 and 115, one of
+            // 32 rows of 64K beside seven small ones 74 and 74
             const int units = a.kv_heads * g.blocks, most = min(shared_parts_cap(units), max(1, g.tiles / kMinTiles));
+            const auto time_of = [&](int p) {
+                const uint64_t items = static_cast<uint64_t>(units) * p * s.num_segments;
+                return (items + kSharedCtas - 1) / kSharedCtas * ((g.tiles + p - 1) / p * each + kItemTiles) +
+                       (static_cast<uint64_t>(g.rows) * a.num_heads * a.head_dim * p >> 18);  // and the join
+            };
             uint64_t best = ~0ull;
-            for (int p = 1 + lane; p <= most; p += 32) {
-                const uint32_t waves = (static_cast<uint32_t>(units) * p + kSharedCtas - 1) / kSharedCtas;
-                const uint64_t t = static_cast<uint64_t>(waves) * ((g.tiles + p - 1) / p * each + kItemTiles) +
-                                   (static_cast<uint64_t>(g.rows) * a.num_heads * a.head_dim * p >> 18);  // and the join
-                best = min(best, t << 16 | static_cast<uint32_t>(p));
-            }
+            for (int p = 1 + lane; p <= most; p += 32) best = min(best, time_of(p) << 8 | static_cast<uint32_t>(p));
             for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
-            g.parts = static_cast<int32_t>(best & 0xffff);
+            g.parts = static_cast<int32_t>(best & 0xff);
+            if (s.num_segments > 1) {
+                int last = 0;
+                for (int p = 1 + lane; p <= most; p += 32)
+                    if (4 * time_of(p) <= 5 * (best >> 8)) last = p;
+                g.parts = __reduce_max_sync(0xffffffffu, last);
+            }
             g.entries = narrow ? 2 * g.parts : g.parts;
             g.cost = (g.tiles + g.parts - 1) / g.parts * each + kItemTiles;
             // Of many rows fewer parts each: 2^10 tokens at least.  32 rows of 4 KV heads and 32K tokens, with 100 to 4,096
