@@ -17,9 +17,18 @@
 //                                           and puts P over S in TMEM, in 16 bits
 //   O[128 columns x D] += P V               P from TMEM, V from shared memory, O in TMEM for the whole item
 //
-// A CTA has two such chains, each with a warpgroup for its softmax, so that one's products run beside the other's
-// exponentials.  An item of more than 128 columns has 128 for each chain, and every tile of K and V serves both; one of
-// fewer has the same columns in both, which then take every other tile.
+// A CTA (one an SM: 512 TMEM columns, 198 to 227 KB) has two such chains, each with a warpgroup for its softmax and a warp
+// that issues its products, so that one's products run beside the other's exponentials.  An item of more than 128 columns
+// has 128 for each chain, and every tile of K and V serves both; one of fewer has the same columns in both, which then
+// take every other tile.  K and V come by TMA, a warp and a ring each.
+//
+// What bounds it (4 KV heads of 128, in a graph): many rows, the chain of a tile: 1,024 cycles of MMA, 830 of
+// exponentials, 500 to 600 of waits between them, so that two chains take 2,350 (bf16) to 2,550 (FP8) cycles a tile where
+// the tensor core needs 2,048.  256 rows of 64K, 16 query heads each: 550 GFLOP in 320 us (1.7 PFLOP/s, 0.89 of cuBLAS's
+// burst) of a call of 375; 64 rows of 64K and 8, bf16: 47 us of 71, tensor pipe 62% busy.  Few rows, bytes: 4 rows of
+// 128K, bf16 65 us, 268 MB.  Below that the latencies of four kernels: checks 4, own tokens 8, a shared item's start
+// (10,000 cycles to its first weights) and output (6,000: 128 KB at what an SM writes) 8, join 5 us.  Head_dim 64 has
+// half the products and as many exponentials: 256 rows of 32K 167 us against 71 of products.
 //
 // Precision.  bf16 pool: products are exact, P is rounded to bf16 (2^-8 of itself; kv_attention.cu's second term would
 // make the second product, half of all, twice as long).  FP8 pool: q as two e4m3 terms against K's codes as they
