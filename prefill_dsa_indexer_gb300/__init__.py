@@ -845,15 +845,17 @@ class KvPlan:
 
     def __init__(self, num_requests, max_rows, page_size, num_pages, rows_per_group=1, num_segments=0, device="cuda"):
         n, rows, segments = int(num_requests), int(max_rows), int(num_segments)
-        self._sizes = n, rows, segments, int(rows_per_group), int(page_size), int(num_pages)
         sizes = (rows, rows, rows, rows, n + 1, n, n, 1, segments + 1 if segments else 0)
-        self._buffers = {name: torch.full((size,), -1 if name in ("positions", "slots") else 0, dtype=torch.int32,
-                                          device=device) for name, size in zip(self._NAMES, sizes)}
-        self._addresses = [t.data_ptr() for t in self._buffers.values()]
-        self._device = self.row_req.get_device()
-        self._status = new_status(device)
+        buffers = {name: torch.full((size,), -1 if name in ("positions", "slots") else 0, dtype=torch.int32,
+                                    device=device) for name, size in zip(self._NAMES, sizes)}
+        self.__dict__.update(buffers, status=new_status(device), _addresses=[t.data_ptr() for t in buffers.values()],
+                             _sizes=(n, rows, segments, int(rows_per_group), int(page_size), int(num_pages)),
+                             _device=buffers["row_req"].get_device())
         if self._device < 0:
             raise DsaError("libdsa takes device tensors only")
+
+    def __setattr__(self, name, value):
+        raise DsaError(f"a plan writes into its own buffers: {name} cannot be another")
 
     def run(self, context, new_tokens, block_table, free_pages, free_count, first_own=None, segment_requests=None,
             stream=None):
@@ -870,13 +872,8 @@ class KvPlan:
             _flat(block_table, "block_table", d, _I32), table[1], _flat(free_pages, "free_pages", d, _I32),
             _flat(free_count, "free_count", d, _I32, (1,)), free_pages.numel(), segments,
             0 if segments == 0 else _flat(segment_requests, "segment_requests", d, _I32, (segments + 1,)), rows, group,
-            *self._addresses), self._status.data_ptr())
+            *self._addresses), self.status.data_ptr())
         return self
-
-
-for _name in KvPlan._NAMES:  # (read only: a step is written at the addresses of these tensors)
-    setattr(KvPlan, _name, property(lambda self, _name=_name: self._buffers[_name]))
-KvPlan.status = property(lambda self: self._status)
 
 
 def kv_attention_workspace_size(kv, num_rows, num_heads, max_ctx) -> int:

@@ -227,6 +227,24 @@ def test_plans_that_follow_one_another_in_place(n, most, graph):
         first.context = plan.context.tolist()
 
 
+def test_plan_refusals_of_the_binding():
+    step = Step([4, 5], [1, 2], 16, 4, segments=[0, 2])
+    plan, (context, new, table, free, count) = step.plan(), step.tensors()
+    seg = ints(step.segments)
+    call = lambda **k: plan.run(**{**dict(context=context, new_tokens=new, block_table=table, free_pages=free,  # noqa: E731
+                                          free_count=count, segment_requests=seg), **k})
+    for bad in (dict(context=context.long()), dict(new_tokens=new[:1]), dict(block_table=table[0]), dict(block_table=table[:1]),
+                dict(block_table=table.t()), dict(free_pages=free.cpu()), dict(free_count=count[:0]), dict(first_own=new[:1]),
+                dict(segment_requests=None), dict(segment_requests=seg[:1]), dict(context=plan.granted),
+                dict(free_pages=plan.row_req), dict(new_tokens=plan.context)):
+        with pytest.raises(P.DsaError):
+            call(**bad)
+    with pytest.raises(P.DsaError):
+        plan.slots = plan.row_req
+    call()
+    step.check(plan, table, free)
+
+
 def test_plans_on_two_streams_at_once():
     steps = [Step([7 * i % 90 for i in range(n)], [i % 5 for i in range(n)], 16, 4 * n) for n in (70, 1300)]
     runs = [(s, s.plan(), s.tensors(), torch.cuda.Stream()) for s in steps]
