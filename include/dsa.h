@@ -636,9 +636,9 @@ size_t dsa_kv_attention_workspace_size(const dsa_kv_cache *cache, int32_t num_ro
  * dsa_kv_attention of a batch whose rows share a prefix: rows first_row[s] .. first_row[s + 1] - 1 make
  * segment s, and the first shared_ctx[s] tokens of their requests are the same (their block tables list
  * the same pages there, or pages that hold the same).  Outputs are those of dsa_kv_attention, but the
- * shared tokens are read once for all rows of a segment, by its first row's block table: as many of
- * them as every row of the segment that sees any token sees, in whole tiles of 128 (and none for a segment
- * of one row group, which shares its reads already); each row reads the rest by its own table.
+ * shared tokens are read once for all rows of a segment, by the block table of the first of them that sees
+ * any token: as many of them as every such row sees, in whole tiles of 128 (and none for a segment of one
+ * row group, which shares its reads already); each row reads the rest by its own table.
  *
  * Rows before first_row[0] and from first_row[num_segments] on are in no segment.  first_row ascends (an
  * empty segment is allowed), from 0 at least to num_rows at most, at whole row groups; a segment that does not,

@@ -642,6 +642,8 @@ class RopeTable:
             self.axis = axis.clone()
             self.axis_address = self.axis.data_ptr()
             self.num_axes = int(axis.max()) + 1 if num_axes is None else int(num_axes)
+            if self.num_axes < 1:
+                raise DsaError(f"positions of {self.num_axes} axes: 1 at least")
 
 
 def rope_table(rot_dim, theta=10000.0, scaling="none", factor=1.0, trained_ctx=0, device="cuda", sections=None,
@@ -974,13 +976,15 @@ class KvLayer:
     def run(self, row_req, row_ctx, slots, positions, q, k, v, stream=None, segment_rows=None, segment_ctx=None):
         """q [R, H, head_dim] is rotated in place; returns (out, lse).  With segment_rows and segment_ctx (of at most
         num_segments segments) the rows' common prefixes are read once (kv_attention_shared)."""
+        if (segment_rows is None) != (segment_ctx is None):
+            raise DsaError("segment_rows and segment_ctx come together")
         if self.rope is None:
             kv_insert(self.kv, slots, k, v, status=self.status, stream=stream)
         else:
             part = q[..., self.rot_offset:self.rot_offset + self.rope.rot_dim]
             kv_insert(self.kv, slots, k, v, rope=self.rope, positions=positions, layout=self.layout,
                       rot_offset=self.rot_offset, q=part, status=self.status, stream=stream)
-        if segment_ctx is not None:
+        if segment_rows is not None:
             return kv_attention_shared(self.kv, self.block_table, row_req, row_ctx, self.max_ctx, q, segment_rows,
                                        segment_ctx, self.sm_scale, self.rows_per_group, out=self.out, lse=self.lse,
                                        workspace=self.workspace, status=self.status, stream=stream)

@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         bool go = true;
         for (; more && go; more = w.next<kCols>(a, lane)) {
             const int num_pages = (w.t_end + a.page_size - 1) >> a.page_shift;
-            const int32_t *table = kv_table(a, w.req, w.row0);
+            const int32_t *table = kv_table(a, w.req, w.begin);
             auto load_ids = [&](int p) { return p + lane < num_pages ? table[p + lane] : 0; };
             int batch = w.t_begin >> a.page_shift;  // page ids batch .. batch + 31 are in `ids`, one per lane
             int32_t ids = load_ids(batch), ids_next = load_ids(batch + 32);

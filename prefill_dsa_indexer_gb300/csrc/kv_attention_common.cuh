@@ -103,8 +103,8 @@ __device__ __forceinline__ int kv_load_group(const KvAttnArgs &a, int row0, int 
 }
 
 // A row group's entries of the block table, from the first token that its rows read here.
-__device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req, int row0) {
-    return a.block_table + static_cast<int64_t>(req) * a.bt_stride + ((kv_begin(a, row0) & -kBeginUnit) >> a.page_shift);
+__device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req, int32_t begin) {
+    return a.block_table + static_cast<int64_t>(req) * a.bt_stride + ((begin & -kBeginUnit) >> a.page_shift);
 }
 
 // Fills `sched`; every thread of the CTA calls it, then __syncthreads.
@@ -118,6 +118,7 @@ __device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule
             // (all loads first: one latency)
             const int row0 = gi * a.group;
             int n[kMaxGroup], req[kMaxGroup];
+            const int32_t begin = kv_begin(a, row0);
 #pragma unroll
             for (int r = 0; r < kMaxGroup; ++r) {
                 const int row = row0 + (r < a.group ? r : 0);
@@ -132,7 +133,7 @@ __device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule
                 ctx = max(ctx, n[r]);
             }
             if (bad) ctx = 0;
-            sum += kv_cost(ctx, kv_part_shift(ctx, a.parts_shift, kv_part_min(kv_begin(a, row0))));
+            sum += kv_cost(ctx, kv_part_shift(ctx, a.parts_shift, kv_part_min(begin)));
         }
         sched->before[e + 1] = sum * (static_cast<uint64_t>(a.kv_heads) * a.col_blocks);
     }
@@ -162,14 +163,16 @@ struct KvCursor {
     int my_ctx;  // of row `lane` of the group
     bool bad;
     int group, head, shift;  // head: KV head and column block
+    int32_t begin;           // kv_begin
     uint64_t start, end;     // cost before the item, and where this CTA's share ends
 
     __device__ __forceinline__ void load_group(const KvAttnArgs &a, int lane) {
         row0 = group * a.group;
+        begin = kv_begin(a, row0);
         my_ctx = kv_load_group(a, row0, lane, req, bad);
         ctx = __reduce_max_sync(0xffffffffu, my_ctx);
         ctx_min = __reduce_min_sync(0xffffffffu, my_ctx);
-        shift = kv_part_shift(ctx, a.parts_shift, kv_part_min(kv_begin(a, row0)));
+        shift = kv_part_shift(ctx, a.parts_shift, kv_part_min(begin));
         parts = kv_parts(ctx, shift);
     }
 

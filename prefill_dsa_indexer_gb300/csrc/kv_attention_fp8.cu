@@ -65,7 +65,7 @@ struct Item {
     int32_t t_begin, t_end;
     int32_t ctx_min, ctx_max;  // over the rows of the group
     int32_t cols;              // real columns
-    int32_t part, parts;
+    int32_t part, to_parts;    // (whether its output goes to the workspace)
     int32_t ctx[8];            // the group's contexts
     int32_t image_last;        // the next item has another query image
     int32_t pad[15];
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
             bool go = true;
             for (; more && go; more = w.next<NC>(a, lane)) {
                 const int num_pages = (w.t_end + a.page_size - 1) >> a.page_shift;
-                const int32_t *table = kv_table(a, w.req, w.row0);
+                const int32_t *table = kv_table(a, w.req, w.begin);
                 auto load_ids = [&](int p) { return p + lane < num_pages ? table[p + lane] : 0; };
                 int batch = w.t_begin >> a.page_shift;  // page ids batch .. batch + 31 are in `ids`, one per lane
                 int32_t ids = load_ids(batch), ids_next = load_ids(batch + 32);
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
                     item->cols = min(NC, cols - w.col0);
                     item->image_last = fresh;
                     item->part = w.part;
-                    item->parts = w.parts;
+                    item->to_parts = w.parts > 1 || a.keep_parts;
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -610,8 +610,7 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
             const Columns<NC> *cs = cols_s + (image & 1);
             image += item->image_last != 0;
             const int t_begin = item->t_begin, t_end = item->t_end, ctx_min = item->ctx_min, ctx_max = item->ctx_max;
-            const int ncols = item->cols, part = item->part;
-            const bool to_parts = item->parts > 1 || a.keep_parts;  // the output goes to the workspace
+            const int ncols = item->cols, part = item->part, to_parts = item->to_parts;
             const int tiles = (t_end - t_begin + kTile - 1) / kTile;
 
             float l[kMine];  // a thread's sums of weights, unless they are in TMEM

@@ -90,10 +90,8 @@ __device__ __forceinline__ KvSharedSeg read_segment(const KvSharedSeg *p) {
 }
 
 constexpr int32_t kItemTiles = 12;  // what an item costs beside its tiles
-constexpr int32_t kMinTiles = 4;   // of a part
+constexpr int32_t kMinTiles = 4;    // of a part
 
-// Parts of a segment with so many items a part: an item a CTA where that is possible, else few enough that their
-// outputs stay small beside the products, and enough to fill the last round of CTAs.
 // Bytes that sharing has to save (those that the other rows of a segment would read) to make up for two launches more and
 // another chain of latencies.  A call whose shapes leave less is dsa_kv_attention's; in one that is not, where half of
 // that is spent already, a segment has to save half, and of several each its share.
@@ -113,6 +111,8 @@ __host__ __device__ __forceinline__ int64_t token_bytes(const KvAttnArgs &a) {
     return 2ll * a.kv_heads * a.head_dim * (a.fp8 ? 1 : 2);
 }
 
+// The most parts of a segment with so many items a part: an item a CTA where that is possible, else few enough that their
+// outputs stay small beside the products, and enough to fill the last round of CTAs.
 __host__ __device__ __forceinline__ int32_t shared_parts_cap(int32_t units) {
     return units <= kSharedCtas / 8 ? kSharedCtas / units : units <= kSharedCtas ? 8 : units <= 4 * kSharedCtas ? 4 : 2;
 }
@@ -911,7 +911,14 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
 
 // A row's own parts, then the shared ones.  kWarps warps take a (row, head): one, where there are enough of those, else
 // four, which share out the parts.  D / 4 lanes take a part, four dims each.
-//   us                                    one warp   four
+//   us of a call over 32K tokens, 32 heads of 128    one warp, four
+//     bf16   4 rows   128 (row, head)                37.0  28.3
+//           16        512                            34.1  31.8
+//           31        992                            37.0  34.5
+//           40      1,280                            45.7  45.7
+//           64      2,048                            45.2  50.3
+//     FP8   31        992                            41.8  38.8
+//           64      2,048                            47.3  52.3
 constexpr int kJoinThreads = 128;
 constexpr int64_t kJoinPairs = 1024;
 

@@ -95,13 +95,6 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
-// Bring box (x, y) of a 2D tiled tensor into L2.
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int32_t x, int32_t y) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y)
-                 : "memory");
-}
-
 // L2 policy for data read once (streamed keys): evict these lines first.
 __device__ __forceinline__ uint64_t l2_evict_first_policy() {
     uint64_t p;

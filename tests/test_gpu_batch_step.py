@@ -373,6 +373,22 @@ def test_insert_with_axes_is_rope_with_axes_and_insert(fmt, tokens, kv_heads, hp
         assert torch.equal(q_out, ref)
 
 
+def test_tables_without_an_axis_are_refused():
+    freq, _ = P.rope_frequencies(64, 10000.0)
+    turns, axis = P.rope_turns(freq).cuda(), P.rope_sections((12, 10, 10))
+    for bad in (dict(axis=axis, num_axes=0), dict(axis=axis, num_axes=-1), dict(axis=axis[:16]), dict(axis=axis.int()),
+                dict(axis=axis.cuda())):
+        with pytest.raises(P.DsaError):
+            P.RopeTable(turns, **bad)
+    x, at = torch.zeros(3, 1, 64, device="cuda"), ints([0, 1, 2]).expand(3, 3)
+    for axes in (2, 5):  # fewer than the pairs name; more than there may be
+        with pytest.raises(P.DsaError):
+            P.rope(x, P.RopeTable(turns, axis=axis, num_axes=axes), ints([0, 1, 2]).expand(axes, 3))
+    with pytest.raises(P.DsaError):
+        P.rope(x, P.RopeTable(turns, axis=axis), at[:2])
+    P.rope(x, P.RopeTable(turns, axis=axis), at)
+
+
 def test_insert_reports_a_slot_of_a_token_without_a_place():
     g = gen(9)
     pool = new_pool(g, "bf16", 2, 1, 16, 64)

@@ -444,6 +444,40 @@ def test_shared_calls_that_follow_one_another_in_one_workspace():
         assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_shared_rows_of_one_request(fmt):
+    """A chunk of a prompt, row by row over what its request has in the cache: one request in all rows of a segment."""
+    c = Shared(41, fmt, [(2000, [2300])], 4, 8, 128, 64)
+    c.rows = list(range(2001, 2301))
+    c.row_ctx, c.row_req, c.starts = ints(c.rows), ints([0] * 300), ints([0, 300])
+    c.q = randn(gen(42), 300, 32, 128).to(torch.bfloat16)
+    c.check(*c.run(), rows=[0, 1, 46, 47, 48, 175, 299])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_shared_pages_of_a_large_pool(fmt):
+    """Pages whose elements lie beyond 2^31, and their bytes beyond 2^32."""
+    c = Shared(43, fmt, [(700, [701, 900, 1500]), (300, [301, 400])], 4, 8, 128, 128)
+    (out, lse), far = c.run(), (1 << 32) // (2 * 4 * 128 * 128 * c.pool.element_size())
+    big = torch.empty(far + c.pool.shape[0], *c.pool.shape[1:], dtype=c.pool.dtype, device="cuda")
+    bits(big)[far:] = bits(c.pool)
+    c.table = torch.where(c.table < c.pool.shape[0], c.table + far, c.table)
+    c.pool, c.kv = big, P.KvCache(big, c.ks, c.vs)
+    got = c.run()
+    assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+
+
+def test_layer_takes_both_of_its_segments_tensors():
+    c = Shared(44, "bf16", [(300, [301, 302])], 2, 4, 128, 64)
+    layer = P.KvLayer(c.kv, c.table, c.max_ctx, 2, 8, num_segments=1)
+    slots, k = ints([-1, -1]), torch.zeros(2, 2, 128, dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(segment_rows=c.starts), dict(segment_ctx=c.shared)):
+        with pytest.raises(P.DsaError):
+            layer.run(c.row_req, c.row_ctx, slots, None, c.q, k, k, **bad)
+    want, got = c.run(), layer.run(c.row_req, c.row_ctx, slots, None, c.q, k, k, segment_rows=c.starts, segment_ctx=c.shared)
+    torch.testing.assert_close(got[0], want[0], atol=2e-2, rtol=2e-2)
+
+
 def test_shared_calls_without_a_row():
     c = Shared(32, "bf16", [(300, [301, 302])], 2, 4, 128, 64)
     none = ints([], (0,))
