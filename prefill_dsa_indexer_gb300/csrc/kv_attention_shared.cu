@@ -863,8 +863,15 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
             if (of == c && !w.wide) ok = ok && wait_mbar_warp(q_empty, items & 1, abort);  // (the other chain's scores read it too)
             if (!ok) break;
             tc_fence_after();
-            uint8_t *stage = smem + c * C::kQBytes + (warp & 3) * (C::kQBytes / 4);  // the warp's 32 columns by kDims dims
+            // kDims dims of the warp's 32 columns at a time, where its own part of the image is: another warp of the chain
+            // may be at the next item's queries already (a barrier between them would wait for a warp that gave up)
             constexpr int kDims = D / 2, kUnits = kDims / 4, kCols = 32 / kUnits;  // 16-byte units of a column, columns a turn
+            constexpr int kPlanes = kFp8 || D == 128 ? 2 : 1, kRows = 32 / kPlanes;  // of the image
+            uint8_t *stage = smem + c * C::kQBytes + (warp & 3) * (C::kQBytes / 4 / kPlanes);
+            const auto stage_at = [&](int n, int unit) {
+                return reinterpret_cast<uint4 *>(stage + n / kRows * (C::kQBytes / kPlanes) + n % kRows * (kDims * 4) +
+                                                 ((unit ^ (n & 7)) << 4));
+            };
 #pragma unroll 1
             for (int d0 = 0; d0 < D; d0 += kDims) {
                 __syncwarp();
@@ -881,8 +888,7 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                     }
 #pragma unroll
                     for (int k = 0; k < 16; k += 4)
-                        *reinterpret_cast<uint4 *>(stage + lane * (kDims * 4) + (((i + k) / 4 ^ (lane & 7)) << 4)) =
-                            make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        *stage_at(lane, (i + k) / 4) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                 }
                 __syncwarp();
                 const int u = lane % kUnits;
@@ -890,11 +896,10 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                 for (int n0 = 0; n0 < 32; n0 += kCols) {
                     const int n = n0 + lane / kUnits;
                     const int64_t at = __shfl_sync(0xffffffffu, real ? place : -1, n);
-                    if (at >= 0)
-                        *reinterpret_cast<uint4 *>(s.so + at * D + d0 + 4 * u) =
-                            *reinterpret_cast<const uint4 *>(stage + n * (kDims * 4) + ((u ^ (n & 7)) << 4));
+                    if (at >= 0) *reinterpret_cast<uint4 *>(s.so + at * D + d0 + 4 * u) = *stage_at(n, u);
                 }
             }
+            __syncwarp();
             tc_fence_before();
         }
         if (!ok) gave_up(abort, a.status);

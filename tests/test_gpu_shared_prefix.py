@@ -415,6 +415,21 @@ def test_shared_of_many_heads(fmt, kv_heads, hpg, rows):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hpg, rows", [(8, 4), (8, 5), (1, 40), (5, 20), (16, 9)])
+def test_shared_items_that_follow_one_another(fmt, dim, hpg, rows):
+    """Several items a CTA, of columns that leave some of its warps with little or nothing to write, which are at the next
+    item's queries while the others write."""
+    segments = [(300 + 150 * s, [310 + 160 * s + i for i in range(rows)]) for s in range(12)]
+    c = Shared(45, fmt, segments, 40, hpg, dim, 64)
+    out, lse = c.run()
+    c.check(out, lse, rows=range(0, len(c.rows), 11))
+    for _ in range(10):
+        again = c.run()
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_shared_of_very_many_rows(fmt):
     """More rows than the segments' kernel keeps in shared memory."""
     c = Shared(36, fmt, [(520, [528 + i % 9 for i in range(1040)]), (130, [140] * 2)], 1, 2, 64, 16, group=8, pad=2)
