@@ -934,7 +934,8 @@ static int attention_call(const dsa_kv_cache *cache, const dsa_rows *rows, const
                             ? kv_attention_workspace_bytes(rows->num_rows, num_heads, cache->kv_heads, cache->head_dim,
                                                            rows->max_ctx)
                             : kv_attention_shared_workspace_bytes(rows->num_rows, num_heads, cache->kv_heads,
-                                                                  cache->head_dim, rows->max_ctx, segments->num_segments);
+                                                                  cache->head_dim, rows->max_ctx, segments->num_segments,
+                                                                  cache->format == DSA_KV_FP8);
     if (need > 0) {
         if (workspace == nullptr || workspace_bytes < need) return DSA_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return DSA_ERR_INVALID_ARG;
@@ -989,7 +990,7 @@ size_t dsa_kv_attention_shared_workspace_size(const dsa_kv_cache *cache, int32_t
     if (check_kv_cache(cache) != DSA_OK || num_rows <= 0 || num_heads <= 0 || max_ctx <= 0) return 0;
     if (max_ctx > DSA_KV_MAX_CTX) return 0;
     return kv_attention_shared_workspace_bytes(num_rows, num_heads, cache->kv_heads, cache->head_dim, max_ctx,
-                                               num_segments);
+                                               num_segments, cache->format == DSA_KV_FP8);
 }
 
 int dsa_kv_attention_shared(const dsa_kv_cache *cache, const dsa_rows *rows, const dsa_kv_segments *segments,

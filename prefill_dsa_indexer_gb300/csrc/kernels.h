@@ -389,7 +389,7 @@ struct KvSegmentArgs {
 
 cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, void *workspace, cudaStream_t s);
 size_t kv_attention_shared_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
-                                           int32_t max_ctx, int32_t num_segments);
+                                           int32_t max_ctx, int32_t num_segments, bool fp8);
 
 // The parts of an FP8 pool of head_dim 128 (kv_attention_fp8.cu; called by launch_kv_attention).
 cudaError_t launch_kv_attention_fp8(KvAttnArgs &a, cudaStream_t s);

@@ -76,6 +76,8 @@ struct KvSharedArgs {
     KvSharedCta *cta;             // [kSharedCtas]
     float *so;                    // [entry][H][D]
     float2 *sml;                  // [entry][H]
+    uint8_t *q_terms;             // FP8: [R][H][2][D] e4m3, hi and lo terms of the queries times 2^e
+    float *q_factor;              // [R][H] 2^-e (NaN: not only numbers in the query)
 };
 
 // As it is in L2: read before the kernel's wait, past what an earlier kernel may have left in L1.
@@ -155,6 +157,55 @@ __device__ __forceinline__ void check_segments(const KvSharedArgs &s, int32_t *t
     }
 }
 
+// The queries over an FP8 pool as two e4m3 terms, times 2^e which brings a query's largest value to (224, 448], for all
+// parts of its columns at once: by CTAs beside the one that works out the segments, in the time that it takes (each part
+// for itself took 6,600 cycles before its first scores, a copy of the terms takes 2,300).  D / 16 lanes take a query.
+template <int D>
+__device__ __forceinline__ void split_queries(const KvSharedArgs &s, int cta, int ctas) {
+    constexpr int kLanes = D / 16, kAt = 32 / kLanes;
+    const KvAttnArgs &a = s.a;
+    const int lane = threadIdx.x & 31, unit = lane % kLanes;
+    const int64_t pairs = static_cast<int64_t>(a.num_rows) * a.num_heads, warps = static_cast<int64_t>(ctas) * (kSegThreads / 32);
+    for (int64_t p0 = (cta * (kSegThreads / 32) + (threadIdx.x >> 5)) * kAt; p0 < pairs; p0 += warps * kAt) {
+        const int64_t p = p0 + lane / kLanes;
+        uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
+        if (p < pairs) {
+            const int64_t row = p / a.num_heads;
+            const uint4 *q = reinterpret_cast<const uint4 *>(a.q + row * a.q_stride + (p - row * a.num_heads) * D) + 2 * unit;
+            v0 = q[0];
+            v1 = q[1];
+        }
+        const uint32_t h[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        uint32_t top = 0;  // by the bits: an infinity or a NaN is above every number
+#pragma unroll
+        for (int y = 0; y < 8; ++y) top = max(top, max(h[y] << 16 & 0x7fff0000u, h[y] & 0x7fff0000u));
+#pragma unroll
+        for (int y = 1; y < kLanes; y <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
+        const bool finite = top < 0x7f800000u;
+        int e = 0;
+        if (top > 0 && finite) {
+            e = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+            e = max(-120, min(120, e));
+        }
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const uint2 x = split_pair(bf16_lo(h[2 * y]) * up, bf16_hi(h[2 * y]) * up);
+            const uint2 z = split_pair(bf16_lo(h[2 * y + 1]) * up, bf16_hi(h[2 * y + 1]) * up);
+            hi[y] = x.x | (z.x << 16);
+            lo[y] = x.y | (z.y << 16);
+        }
+        if (p >= pairs) continue;
+        uint4 *to = reinterpret_cast<uint4 *>(s.q_terms + p * (2 * D)) + unit;
+        to[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        to[D / 16] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (unit == 0)
+            s.q_factor[p] = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : __uint_as_float(0x7fc00000u);
+    }
+}
+
+// CTA 0: the segments; the others, over an FP8 pool: the queries' terms.
 __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __grid_constant__ KvSharedArgs s) {
     const KvAttnArgs &a = s.a;
     __shared__ int32_t tops[kSegThreads / 32];
@@ -165,6 +216,11 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
     KvSharedSeg *seg = s.num_segments <= kSegSegs ? seg_s : s.seg;
     pdl_wait();
     pdl_launch_dependents();
+    if (blockIdx.x > 0) {
+        if (a.head_dim == 64) split_queries<64>(s, blockIdx.x - 1, gridDim.x - 1);
+        else split_queries<128>(s, blockIdx.x - 1, gridDim.x - 1);
+        return;
+    }
     // every row by itself at first
     for (int g = threadIdx.x; g < a.num_rows / a.group; g += kSegThreads) {
         const int row0 = g * a.group;
@@ -402,8 +458,7 @@ struct SharedCfg {
     static constexpr int OFF_BARS = OFF_RING + 2 * kSlots * kSlotBytes;
     static constexpr int kNumBars = 4 * kSlots + 1 + 2 * 6 + 2 * 3;
     static constexpr int OFF_MISC = OFF_BARS + kNumBars * 8;
-    static constexpr int OFF_FACTORS = OFF_MISC + 16;
-    static constexpr int kSmemBytes = OFF_FACTORS + (kFp8 ? 2 * kTile * 4 : 0) + 1024;
+    static constexpr int kSmemBytes = OFF_MISC + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory");
     // A base leaves the largest weight that it was made for at 2^kBias, so that fp16's steps are 2^-31 of it, and moves
     // when a tile's weights make up more than kMost (fp16 holds 65504; 128 of 2^7 are 2^14).
@@ -415,77 +470,23 @@ __device__ __forceinline__ void copy16(void *dst, const void *src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
-// A warp's 32 columns (lane l: column l's elements at `src`, NULL behind the last) into the chain's image, from row
-// `n0` on.  kLanes lanes take a column, so that the warp reads whole runs of memory (a thread a column: 11,000
-// cycles); in rolled loops, for code that runs once waits for its way in.  bf16 as it is, 64 dims to a 128-byte row; or
-// e4m3 hi and lo terms of the column's values times 2^e, which brings the largest to (224, 448].  Returns column
-// `lane`'s factor 2^-e (NaN: not only numbers in it).
+// A warp's 32 columns (lane l: column l's 2 D bytes at `src`, NULL behind the last) into the chain's image, from row
+// `n0` on: bf16, 64 dims to a 128-byte row, or e4m3 terms, hi and then lo.  D / 8 lanes take a column, so that the warp
+// reads whole runs of memory (a thread a column: 11,000 cycles), all of it on its way at once; in a rolled loop, for code
+// that runs once waits for its way in.
 template <bool kFp8, int D>
-__device__ __forceinline__ float put_queries(uint8_t *img, const uint16_t *src, int n0, int lane) {
-    constexpr int kElems = kFp8 ? 16 : 8, kLanes = D / kElems, kCols = 32 / kLanes;  // of a lane; of a turn
+__device__ __forceinline__ void put_queries(uint8_t *img, const uint8_t *src, int n0, int lane) {
+    constexpr int kLanes = D / 8, kCols = 32 / kLanes;  // of a column; of a turn
     const int unit = lane % kLanes, sub = lane / kLanes;
-    float factor = 1.f;
-    const auto of = [&](int n) {
-        return reinterpret_cast<const uint16_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), n));
-    };
-    if constexpr (!kFp8) {
 #pragma unroll 1
-        for (int n = sub; n < 32; n += kCols) {
-            const uint16_t *q = of(n);
-            copy16(img + (unit >> 3) * (kTile * 128) + fp8mla::sw128(n0 + n, unit & 7),
-                   q != nullptr ? q + unit * 8 : reinterpret_cast<const uint16_t *>(img), q != nullptr);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-    } else {
-        uint4 v0, v1, w0, w1;  // this turn's and the next one's
-        const auto load = [&](int n, uint4 &x, uint4 &y) {
-            const uint4 *q = reinterpret_cast<const uint4 *>(of(n & 31));
-            x = y = make_uint4(0u, 0u, 0u, 0u);
-            if (q != nullptr) {
-                x = q[2 * unit];
-                y = q[2 * unit + 1];
-            }
-        };
-        load(sub, v0, v1);
-        load(sub + kCols, w0, w1);
-#pragma unroll 1
-        for (int n = sub; n < 32; n += kCols) {
-            const uint32_t h[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-            v0 = w0;
-            v1 = w1;
-            load(n + 2 * kCols, w0, w1);
-            uint32_t top = 0;  // by the bits: an infinity or a NaN is above every number
-#pragma unroll
-            for (int y = 0; y < 8; ++y) top = max(top, max(h[y] << 16 & 0x7fff0000u, h[y] & 0x7fff0000u));
-#pragma unroll
-            for (int y = 1; y < kLanes; y <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
-            const bool finite = top < 0x7f800000u;
-            int e = 0;
-            if (top > 0 && finite) {
-                e = 135 - static_cast<int>(top >> 23) - ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-                e = max(-120, min(120, e));
-            }
-            const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const uint2 p0 = split_pair(bf16_lo(h[2 * y]) * up, bf16_hi(h[2 * y]) * up);
-                const uint2 p1 = split_pair(bf16_lo(h[2 * y + 1]) * up, bf16_hi(h[2 * y + 1]) * up);
-                hi[y] = p0.x | (p1.x << 16);
-                lo[y] = p0.y | (p1.y << 16);
-            }
-            const int r = n0 + n;
-            const uint32_t at = D == 128 ? fp8mla::sw128(r, unit) : static_cast<uint32_t>(r * 64 + ((unit ^ (r >> 1 & 3)) << 4));
-            *reinterpret_cast<uint4 *>(img + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(img + kTile * D + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            // the lane of each of the turn's columns takes its factor from the column's first lane
-            const float f = finite ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : __uint_as_float(0x7fc00000u);
-            const int c = lane - (n - sub);
-            const float mine = __shfl_sync(0xffffffffu, f, (c & (kCols - 1)) * kLanes);
-            if (c >= 0 && c < kCols) factor = mine;
-        }
+    for (int n = sub; n < 32; n += kCols) {
+        const uint8_t *q = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), n));
+        const int r = n0 + n;
+        const uint32_t at = kFp8 && D == 64 ? (unit >> 2) * (kTile * 64) + r * 64 + (((unit & 3) ^ (r >> 1 & 3)) << 4)
+                                            : (unit >> 3) * (kTile * 128) + fp8mla::sw128(r, unit & 7);
+        copy16(img + at, q != nullptr ? q + unit * 16 : img, q != nullptr);
     }
-    return factor;
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Four e4m3 codes as two fp16 pairs (exact).
@@ -517,7 +518,6 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
     uint64_t *drained = my_turn + 2;                                    // [2] after a wait gave up: no MMA is left
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
-    float *factors_s = reinterpret_cast<float *>(smem + C::OFF_FACTORS);  // [2][kTile] (FP8)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2;
     constexpr int kProducer = 4 * (C::kWarpgroups - 1), kIssuer = kProducer + 2;  // two warps each
@@ -755,21 +755,19 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
             const int head = w.head * hpg + col - row * hpg;
             const int64_t place = (w.g.entry0 + static_cast<int64_t>(row) * w.g.entries + (w.wide ? w.part : 2 * w.part + c)) *
                                       a.num_heads + head;
+            const int64_t at = (w.g.row0 + row) * static_cast<int64_t>(a.num_heads) + head;
+            const int steps = w.steps(c);
+            float scale = a.s_scale;
+            if (kFp8 && real) scale *= __ldcg(s.q_factor + at);
             if (of == c) {
-                const uint16_t *src = real ? a.q + (w.g.row0 + row) * a.q_stride + static_cast<int64_t>(head) * D : nullptr;
-                const float f = put_queries<kFp8, D>(smem + c * C::kQBytes, src, (warp & 3) * 32, lane);
-                if constexpr (kFp8) factors_s[c * kTile + self] = f;
+                const uint8_t *src = kFp8 ? s.q_terms + at * (2 * D)
+                                          : reinterpret_cast<const uint8_t *>(a.q + (w.g.row0 + row) * a.q_stride +
+                                                                              static_cast<int64_t>(head) * D);
+                put_queries<kFp8, D>(smem + c * C::kQBytes, real ? src : nullptr, (warp & 3) * 32, lane);
                 fence_async_smem();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[c]);
-            const int steps = w.steps(c);
-            float scale = a.s_scale;
-            if constexpr (kFp8) {
-                if (steps > 0) ok = wait_mbar_warp(&q_full[of], items & 1, abort);
-                if (!ok) break;
-                scale *= factors_s[of * kTile + self];
-            }
             // a score of -inf times the scale: neither zero nor infinity.  Over codes no number in q makes no score
             if (scale == scale) scale = fminf(fmaxf(scale, 1.17549435e-38f), 3.40282347e38f);
             float base = -INFINITY;
@@ -1095,12 +1093,14 @@ size_t shared_entries(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int
 }  // namespace
 
 size_t kv_attention_shared_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
-                                           int32_t max_ctx, int32_t num_segments) {
+                                           int32_t max_ctx, int32_t num_segments, bool fp8) {
+    const size_t pairs = fp8 ? static_cast<size_t>(num_rows) * static_cast<size_t>(num_heads) : 0;
     const size_t entries = shared_entries(num_rows, num_heads, kv_heads, max_ctx, num_segments) * static_cast<size_t>(num_heads);
     return kv_attention_workspace_bytes(num_rows, num_heads, kv_heads, head_dim, max_ctx, true) +
            3 * align256(static_cast<size_t>(num_rows) * 4) +
            align256(static_cast<size_t>(num_segments) * sizeof(KvSharedSeg)) + align256(kSharedCtas * sizeof(KvSharedCta)) +
-           align256(entries * static_cast<size_t>(head_dim) * 4) + align256(entries * 8);
+           align256(entries * static_cast<size_t>(head_dim) * 4) + align256(entries * 8) +
+           align256(pairs * 2 * static_cast<size_t>(head_dim)) + align256(pairs * 4);
 }
 
 cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, void *workspace, cudaStream_t stream) {
@@ -1129,6 +1129,11 @@ cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, 
                            static_cast<size_t>(a.num_heads);
     s.so = reinterpret_cast<float *>(take(align256(entries * static_cast<size_t>(a.head_dim) * 4)));
     s.sml = reinterpret_cast<float2 *>(take(align256(entries * 8)));
+    const int64_t pairs = static_cast<int64_t>(a.num_rows) * a.num_heads;
+    if (a.fp8) {
+        s.q_terms = take(align256(static_cast<size_t>(pairs) * 2 * static_cast<size_t>(a.head_dim)));
+        s.q_factor = reinterpret_cast<float *>(take(align256(static_cast<size_t>(pairs) * 4)));
+    }
     s.a = a;
     cudaError_t e;
     // nothing to gain in any segment of such a call
@@ -1138,7 +1143,10 @@ cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, 
         if (e != cudaSuccess || a.status == nullptr) return e;
         return launch_pdl(kv_segments_check_kernel, dim3(1), dim3(kSegThreads), 0, stream, s);
     }
-    e = launch_pdl(kv_segments_kernel, dim3(1), dim3(kSegThreads), 0, stream, s);
+    const int64_t at_once = kSegThreads * 16 / a.head_dim;  // queries of a CTA
+    const int64_t ctas = a.fp8 ? (pairs + at_once - 1) / at_once : 0;
+    e = launch_pdl(kv_segments_kernel, dim3(static_cast<unsigned>(1 + (ctas < kSharedCtas - 1 ? ctas : kSharedCtas - 1))),
+                   dim3(kSegThreads), 0, stream, s);
     if (e != cudaSuccess) return e;
     a.row_ctx = s.own_ctx;
     a.row_begin = s.row_begin;
