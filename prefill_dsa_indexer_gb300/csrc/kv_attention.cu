@@ -52,12 +52,6 @@ constexpr int kThreads = 32 * (kConsumers + 2);
 constexpr float kHeadroom = 15.0f;                // weights reach 2^15 (fp16 holds 65504) ...
 constexpr float kBias = 7.0f;                     // ... and a moved base leaves the largest at 2^7
 
-// Bound of kv_parts over every context up to max_ctx.
-uint32_t kv_parts_bound(int32_t max_ctx, int32_t parts_shift) {
-    const int64_t n = (static_cast<int64_t>(max_ctx) + (1 << kPartMin) - 1) >> kPartMin, most = 1ll << parts_shift;
-    return static_cast<uint32_t>(n < 1 ? 1 : (n < most ? n : most));
-}
-
 // kColWarps consumer warps side by side over the columns (16 each), kTokWarps over a tile's tokens.
 template <bool kFp8, int D, int kColWarps>
 struct KvCfg {

@@ -37,6 +37,12 @@ __host__ __device__ __forceinline__ int32_t kv_parts_shift(int32_t kv_heads) {
     return kv_heads >= 8 ? 4 : kv_heads >= 4 ? 5 : kv_heads >= 2 ? 6 : 7;
 }
 
+// Bound of kv_parts over every context up to max_ctx.
+inline uint32_t kv_parts_bound(int32_t max_ctx, int32_t parts_shift) {
+    const int64_t n = (static_cast<int64_t>(max_ctx) + (1 << kPartMin) - 1) >> kPartMin, most = 1ll << parts_shift;
+    return static_cast<uint32_t>(n < 1 ? 1 : (n < most ? n : most));
+}
+
 // log2 of a part's tokens: the smallest k >= part_min with 2^(k + parts_shift) >= ctx.
 __device__ __forceinline__ int32_t kv_part_shift(int32_t ctx, int32_t parts_shift, int32_t part_min) {
     return part_min + (32 - __clz(max(ctx - 1, 0) >> (part_min + parts_shift)));
@@ -76,6 +82,7 @@ constexpr int kMaxGroup = 8;        // rows of a group
 constexpr int kSchedEntries = 512;  // running costs kept in shared memory, one for every so many groups
 
 struct KvSchedule {
+    int32_t mine, upto, of;  // with own_sms: this CTA's shares, and how many there are
     uint64_t before[kSchedEntries + 1];  // cost of all groups before the entry's
 };
 
@@ -107,9 +114,58 @@ __device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req,
     return a.block_table + static_cast<int64_t>(req) * a.bt_stride + ((begin & -kBeginUnit) >> a.page_shift);
 }
 
+// The share of a CTA where only own_sms[0] SMs are to work: the CTAs that are there take two shares each SM, and the last
+// one of all to look takes what is left (nothing, unless an SM got fewer than two CTAs: then its run of shares may have
+// others' among them, which are made twice, alike).  Warp-collective; out of line, for the callers' registers.
+[[maybe_unused]] static __device__ __noinline__ void kv_share(int32_t *own_sms, KvSchedule *sched, int lane) {
+    const int sms = __ldcg(own_sms);
+    int mine = static_cast<int>(blockIdx.x), upto = mine + 1, of = static_cast<int>(gridDim.x);
+    if (2 * sms < of) {
+        int *arrived = own_sms + 1, *taken = own_sms + 2;
+        uint32_t sm;
+        asm volatile("mov.u32 %0, %%smid;" : "=r"(sm));
+        of = 2 * sms;
+        mine = of;
+        upto = 0;
+        int last = 0;
+        if (lane == 0) {
+            if (sm < static_cast<uint32_t>(sms)) {
+                const int n = atomicAdd(taken + sm, 1);
+                if (n < 2) {
+                    mine = 2 * static_cast<int>(sm) + n;
+                    upto = mine + 1;
+                }
+                __threadfence();
+            }
+            last = atomicAdd(arrived, 1) + 1 == static_cast<int>(gridDim.x);
+        }
+        if (__shfl_sync(0xffffffffu, last, 0)) {
+            __threadfence();
+            for (int i = lane; i < sms; i += 32) {
+                const int n = __ldcg(taken + i);
+                if (n >= 2) continue;
+                mine = min(mine, 2 * i + n);
+                upto = max(upto, 2 * i + 2);
+            }
+            mine = __reduce_min_sync(0xffffffffu, mine);
+            upto = __reduce_max_sync(0xffffffffu, upto);
+        }
+    }
+    if (lane == 0) {
+        sched->mine = mine;
+        sched->upto = upto;
+        sched->of = of;
+    }
+}
+
 // Fills `sched`; every thread of the CTA calls it, then __syncthreads.
 __device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule *sched) {
     if (kv_direct(a)) return;
+    if (a.own_sms != nullptr) {
+        if (threadIdx.x < 32) kv_share(a.own_sms, sched, threadIdx.x);
+        __syncthreads();
+        if (sched->mine >= sched->upto) return;
+    }
     const int per = a.sched_per, entries = a.sched_entries;
     for (int e = threadIdx.x; e < entries; e += blockDim.x) {
         uint64_t sum = 0;
@@ -207,8 +263,15 @@ struct KvCursor {
         const int per = a.sched_per, entries = a.sched_entries;
         // total * b / n: exact for products below 2^64 / n, and no total is near (a token costs 2^-6 or less)
         const uint64_t total = sched->before[entries];
-        const uint64_t from = __umul64hi(total * blockIdx.x, a.ctas_inv);
-        end = __umul64hi(total * (blockIdx.x + 1), a.ctas_inv);
+        uint64_t from;
+        if (a.own_sms == nullptr) {
+            from = __umul64hi(total * blockIdx.x, a.ctas_inv);
+            end = __umul64hi(total * (blockIdx.x + 1), a.ctas_inv);
+        } else {
+            if (sched->mine >= sched->upto) return false;
+            from = total * sched->mine / sched->of;
+            end = total * sched->upto / sched->of;
+        }
         if (from >= end) return false;
         int lo = 0;  // the last entry with nothing of the share before it
 #pragma unroll 1

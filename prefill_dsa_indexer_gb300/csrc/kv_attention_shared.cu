@@ -4,7 +4,7 @@
 //
 // where the tokens before a segment's S are the same for all of its rows.  The sum is split at S: the shared tokens are
 // read once for all rows of the segment (kv_shared_kernel), each row reads the others by itself (kv_attention.cu, from
-// an offset into its table), and kv_join_kernel adds the parts up by log-sum-exp.  kv_segments_kernel works out S, a
+// an offset into its table, on SMs of its own), and kv_join_kernel adds the parts up by log-sum-exp.  kv_segments_kernel works out S, a
 // multiple of 128, and who does what.  S is at most what every row of the segment that sees any token sees, so no
 // score of a shared token is ever masked, whatever its V holds.
 //
@@ -23,11 +23,11 @@
 // take every other tile.  K and V come by TMA, a warp and a ring each.
 //
 // What bounds it (4 KV heads of 128, in a graph): many rows, the chain of a tile: 1,024 cycles of MMA, 830 of
-// exponentials, 500 to 600 of waits between them, so that two chains take 2,350 (bf16) to 2,550 (FP8) cycles a tile where
-// the tensor core needs 2,048.  256 rows of 64K, 16 query heads each: 550 GFLOP in 320 us (1.7 PFLOP/s, 0.89 of cuBLAS's
-// burst) of a call of 375; 64 rows of 64K and 8, bf16: 47 us of 71, tensor pipe 62% busy.  Few rows, bytes: 4 rows of
-// 128K, bf16 65 us, 268 MB.  Below that the latencies of four kernels: checks 4, own tokens 8, a shared item's start
-// (10,000 cycles to its first weights) and output (6,000: 128 KB at what an SM writes) 8, join 5 us.  Head_dim 64 has
+// exponentials, 500 to 600 of waits between them, so that two chains take 2,350 (bf16) to 2,450 (FP8) cycles a tile where
+// the tensor core needs 2,048.  256 rows of 64K, 16 query heads each: 550 GFLOP in 352 us (1.56 PFLOP/s, 0.82 of cuBLAS's
+// burst), 128 SMs at the shared tokens for 325 of them.  64 rows of 64K and 8, bf16: 70 us for 36 of products.  Few rows,
+// bytes: 4 rows of 128K, bf16 65 us, 268 MB.  Below that the latencies of four kernels: checks 6, a shared item's start
+// (7,000 cycles to its first weights) and output (6,300: 128 KB at what an SM writes) 7, join 5 us.  Head_dim 64 has
 // half the products and as many exponentials: 256 rows of 32K 167 us against 71 of products.
 //
 // Precision.  bf16 pool: products are exact, P is rounded to bf16 (2^-8 of itself; kv_attention.cu's second term would
@@ -76,6 +76,9 @@ struct KvSharedArgs {
     KvSharedCta *cta;             // [kSharedCtas]
     float *so;                    // [entry][H][D]
     float2 *sml;                  // [entry][H]
+    int32_t *own_sms;             // SMs that the rows' own tokens take while the others read shared ones
+    bool beside;                  // whether they do
+    float own_tile, own_item;     // what a tile of them and an item cost an SM, in tiles of a chain
     uint8_t *q_terms;             // FP8: [R][H][2][D] e4m3, hi and lo terms of the queries times 2^e
     float *q_factor;              // [R][H] 2^-e (NaN: not only numbers in the query)
 };
@@ -91,6 +94,10 @@ __device__ __forceinline__ KvSharedSeg read_segment(const KvSharedSeg *p) {
     return u.seg;
 }
 
+// Rows' own tokens in parts of 2^10 at least where a segment has so many (row group, KV head): 32 rows of 4 KV heads and 32K
+// tokens, with 100 to 4,096 of their own: 61 us, with 2^8 66; 256 rows of 64K 390 and 394; but four segments of 4 row
+// groups 76 and 72
+constexpr int32_t kManyGroups = 128, kManyPartMin = 10;
 constexpr int32_t kItemTiles = 12;  // what an item costs beside its tiles
 constexpr int32_t kMinTiles = 4;    // of a part
 
@@ -205,23 +212,54 @@ __device__ __forceinline__ void split_queries(const KvSharedArgs &s, int cta, in
     }
 }
 
+// What a row group's own tokens cost, for one KV head and block of columns.
+__device__ __forceinline__ float own_cost(const KvSharedArgs &s, int32_t ctx, int32_t part_min) {
+    if (ctx <= 0) return 0.f;
+    const int32_t parts = kv_parts(ctx, kv_part_shift(ctx, kv_parts_shift(s.a.kv_heads), part_min));
+    return static_cast<float>((ctx + kTile - 1) / kTile) * s.own_tile + static_cast<float>(parts) * s.own_item;
+}
+
+template <typename T>
+__device__ __forceinline__ T warp_sum(T x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// The rows' own tokens wait for memory most of the time and the shared ones for the tensor core, and an SM has room for
+// one of the two kernels.  So the own ones get some SMs (KvAttnArgs.own_sms) and the shared ones the others, so many that
+// both end together, or all SMs one after the other where that is as good.  us, one after the other / beside: 32 rows of
+// 32K and 100 to 4,096 59.6 / 50.0, verify rows of 16 requests 60.4 / 53.6, 256 rows of 64K 367 / 352, 64 rows of 64K
+// bf16 71 / 70, 45 ragged rows of head_dim 64 24.9 / 23.1.
+constexpr int kFewestSms = 8, kMostSms = kSharedCtas - 4;
+
+__device__ __forceinline__ float rounds_of(float items, float sms) { return ceilf(__fdiv_rn(items, sms)); }
+
 // CTA 0: the segments; the others, over an FP8 pool: the queries' terms.
 __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __grid_constant__ KvSharedArgs s) {
     const KvAttnArgs &a = s.a;
     __shared__ int32_t tops[kSegThreads / 32];
+    __shared__ unsigned long long own_s;  // what the rows' own tokens cost
+    __shared__ int sms_s;                 // for the shared ones
     __shared__ int32_t ctx_s[kSegRows];
     __shared__ KvSharedSeg seg_s[kSegSegs];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hpg = a.num_heads / a.kv_heads;
     int32_t *ctx = a.num_rows <= kSegRows ? ctx_s : s.own_ctx;  // what each row reads itself (-1: its group is refused)
     KvSharedSeg *seg = s.num_segments <= kSegSegs ? seg_s : s.seg;
+    // what the rows' own tokens cost is right to within the length of the parts, which is as in a segment of all rows
+    const int32_t any_part_min = a.num_rows / a.group * a.kv_heads >= kManyGroups ? kManyPartMin : kPartMin;
+    const float own_heads = static_cast<float>(a.kv_heads * ((a.group * hpg + 63) / 64));
+    if (threadIdx.x == 0) own_s = 0;
+    __syncthreads();
     pdl_wait();
-    pdl_launch_dependents();
     if (blockIdx.x > 0) {
         if (a.head_dim == 64) split_queries<64>(s, blockIdx.x - 1, gridDim.x - 1);
         else split_queries<128>(s, blockIdx.x - 1, gridDim.x - 1);
         return;
     }
+    for (int i = threadIdx.x; i < 1 + kOwnSms; i += kSegThreads) s.own_sms[1 + i] = 0;
     // every row by itself at first
+    float mine = 0.f;
     for (int g = threadIdx.x; g < a.num_rows / a.group; g += kSegThreads) {
         const int row0 = g * a.group;
         int32_t n[kMaxGroup], req[kMaxGroup];
@@ -241,7 +279,13 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
                 s.row_begin[row0 + r] = kPartMin;
                 s.row_seg[row0 + r] = -1;
             }
+        int32_t most = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxGroup; ++r) most = max(most, n[r]);
+        if (!bad) mine += own_cost(s, most, any_part_min);
     }
+    mine = warp_sum(mine);
+    if (lane == 0) atomicAdd(&own_s, static_cast<unsigned long long>(static_cast<long long>(mine)));
     check_segments(s, tops, [&](int i, int32_t row0, int32_t rows, int32_t shared) {
         KvSharedSeg g = {};
         g.row0 = row0;
@@ -278,57 +322,107 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
             g.req = a.row_req[lead];
             const bool narrow = cols - (g.blocks - 1) * 2 * kTile <= kTile;  // the last block is of one chain's columns
             const int each = g.blocks == 1 && narrow ? 1 : 2;                // tiles of one chain that a tile makes
-            // The parts that end first, if all segments are as this one and a CTA runs an item at a time; the fewest of
-            // those that are as good.  Beside others, which may be small, the most of those within a quarter.  us, so and
-            // as if each segment were alone: eight of 8 rows of 8K 45 and 68, sixteen of 16 rows of 4K 82 and 115, one of
-            // 32 rows of 64K beside seven small ones 74 and 74
-            const int units = a.kv_heads * g.blocks, most = min(shared_parts_cap(units), max(1, g.tiles / kMinTiles));
-            const auto time_of = [&](int p) {
-                const uint64_t items = static_cast<uint64_t>(units) * p * s.num_segments;
-                return (items + kSharedCtas - 1) / kSharedCtas * ((g.tiles + p - 1) / p * each + kItemTiles) +
-                       (static_cast<uint64_t>(g.rows) * a.num_heads * a.head_dim * p >> 18);  // and the join
-            };
-            uint64_t best = ~0ull;
-            for (int p = 1 + lane; p <= most; p += 32) best = min(best, time_of(p) << 8 | static_cast<uint32_t>(p));
-            for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
-            g.parts = static_cast<int32_t>(best & 0xff);
-            if (s.num_segments > 1) {
-                int last = 0;
-                for (int p = 1 + lane; p <= most; p += 32)
-                    if (4 * time_of(p) <= 5 * (best >> 8)) last = p;
-                g.parts = __reduce_max_sync(0xffffffffu, last);
+            const int32_t part_min = live * a.kv_heads >= kManyGroups ? kManyPartMin : kPartMin;
+            float own = 0.f, before = 0.f;
+            for (int j = lane; j < groups; j += 32) {
+                int32_t most = 0;
+                for (int r = g.row0 + j * a.group; r < g.row0 + (j + 1) * a.group; ++r) {
+                    const int32_t n = ctx[r];
+                    s.row_begin[r] = g.tiles * kTile + part_min;
+                    if (n > 0) {
+                        ctx[r] = n - g.tiles * kTile;
+                        s.row_seg[r] = i;
+                    }
+                    most = max(most, n);
+                }
+                before += own_cost(s, most, any_part_min);
+                own += own_cost(s, most - g.tiles * kTile, part_min);
             }
+            own = warp_sum(own);
+            before = warp_sum(before);
+            if (lane == 0) atomicAdd(&own_s, static_cast<unsigned long long>(static_cast<long long>(own - before)));
+            // The parts that end first, if the call's other rows are as these and a CTA runs an item at a time (so a row's
+            // bits depend on its segment and the call's shapes); the fewest of those that are as good, or, beside other
+            // segments, the most of those within an eighth
+            const int units = a.kv_heads * g.blocks, most = min(shared_parts_cap(units), max(1, g.tiles / kMinTiles));
+            const float alike = __fdiv_rn(static_cast<float>(a.num_rows), static_cast<float>(g.rows));
+            const float all = static_cast<float>(units) * alike;
+            float sms = kSharedCtas;
+            if (s.beside) {
+                const float work = all * static_cast<float>(g.tiles * each) + kSharedCtas * kItemTiles;
+                sms = rintf(kSharedCtas * __fdiv_rn(work, work + own * own_heads * alike));
+                sms = fminf(fmaxf(sms, kFewestSms), kMostSms);
+            }
+            const float join = static_cast<float>(g.rows) * static_cast<float>(a.num_heads * a.head_dim) * 0x1p-18f;
+            const auto time_of = [&](int p) {
+                return rounds_of(all * static_cast<float>(p), sms) * static_cast<float>((g.tiles + p - 1) / p * each + kItemTiles) +
+                       join * static_cast<float>(p);
+            };
+            float best = INFINITY;
+            for (int p = 1 + lane; p <= most; p += 32) best = fminf(best, time_of(p));
+            best = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(best)));
+            int first = INT32_MAX, last = 0;
+            for (int p = 1 + lane; p <= most; p += 32) {
+                const float time = time_of(p);
+                if (time == best) first = min(first, p);
+                if (time <= 1.125f * best) last = p;
+            }
+            first = __reduce_min_sync(0xffffffffu, first);
+            last = __reduce_max_sync(0xffffffffu, last);
+            g.parts = s.num_segments > 1 ? last : first;
             g.entries = narrow ? 2 * g.parts : g.parts;
             g.cost = (g.tiles + g.parts - 1) / g.parts * each + kItemTiles;
-            // Of many rows fewer parts each: 2^10 tokens at least.  32 rows of 4 KV heads and 32K tokens, with 100 to 4,096
-            // of their own: 61 us, with 2^8 66; 256 rows of 64K 390 and 394; but four segments of 4 row groups 76 and 72
-            const int32_t part_min = live * a.kv_heads >= 128 ? 10 : kPartMin;
-            for (int r = g.row0 + lane; r < g.row0 + g.rows; r += 32) {
-                const int32_t n = ctx[r];
-                s.row_begin[r] = g.tiles * kTile + part_min;
-                if (n > 0) {
-                    ctx[r] = n - g.tiles * kTile;
-                    s.row_seg[r] = i;
-                }
-            }
         }
         if (lane == 0) seg[i] = g;
     }
     __syncthreads();
+    // (not before: kv_attention*'s CTAs are to find every SM free, for two of them on each)
+    pdl_launch_dependents();
     __shared__ int64_t total_s;
     if (warp == 0) {
         // Where there is a CTA for each item, one each, whatever they cost (by cost a CTA may have two that are short, and
         // take longer than for the longest: verify rows of 16 requests over prompts of 8K to 16K 64 us, 62.9)
-        int64_t items = 0;
-        for (int i = lane; i < s.num_segments; i += 32) items += static_cast<int64_t>(a.kv_heads) * seg[i].blocks * seg[i].parts;
-        for (int o = 16; o > 0; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
+        int64_t items = 0, work = 0;
+        int32_t longest = 0;
+        for (int i = lane; i < s.num_segments; i += 32) {
+            const int64_t n = static_cast<int64_t>(a.kv_heads) * seg[i].blocks * seg[i].parts;
+            items += n;
+            work += n * seg[i].cost;
+            if (n > 0) longest = max(longest, seg[i].cost);
+        }
+        items = warp_sum(items);
+        work = warp_sum(work);
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        int sms = kSharedCtas;
+        if (s.beside && work > 0) {
+            const float own = static_cast<float>(static_cast<long long>(own_s)) * own_heads;
+            const float count = static_cast<float>(items), top = static_cast<float>(longest), sum = static_cast<float>(work);
+            const bool alike = work == items * longest;
+            const auto shared_time = [&](float n) {
+                return alike ? rounds_of(count, n) * top : count <= n ? top : __fdividef(sum, n) + top;
+            };
+            float best = shared_time(kSharedCtas) + own * (1.f / kSharedCtas) + 14.f;  // one after the other
+            for (int n = kFewestSms + lane; n <= kMostSms; n += 32) {
+                const float time = fmaxf(shared_time(n), __fdividef(own, static_cast<float>(kSharedCtas - n)) + 5.f);
+                if (time < best) {
+                    best = time;
+                    sms = n;
+                }
+            }
+            const float least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(best)));
+            sms = __reduce_min_sync(0xffffffffu, best == least ? sms : kSharedCtas);
+        }
+        if (lane == 0) {
+            sms_s = sms;
+            s.own_sms[0] = sms < kSharedCtas ? kSharedCtas - sms : kSharedCtas;
+        }
         int64_t entry0 = 0, cost0 = 0;
         for (int i0 = 0; i0 < s.num_segments; i0 += 32) {
             const int i = i0 + lane;
             int64_t entries = 0, cost = 0;
             if (i < s.num_segments) {
                 KvSharedSeg &g = seg[i];
-                if (items <= kSharedCtas) g.cost = 1;
+                if (items <= sms) g.cost = 1;
                 entries = static_cast<int64_t>(g.rows) * g.entries;
                 cost = static_cast<int64_t>(a.kv_heads) * g.blocks * g.parts * g.cost;
             }
@@ -356,8 +450,9 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
         for (int i = threadIdx.x; i < s.num_segments; i += kSegThreads) s.seg[i] = seg_s[i];
     // a CTA takes the items that start within its share of the cost
     if (threadIdx.x < kSharedCtas) {
-        const int64_t from = total_s * threadIdx.x / kSharedCtas;
-        KvSharedCta w = {-1, 0, total_s * (threadIdx.x + 1) / kSharedCtas};
+        const int sms = sms_s;
+        const int64_t from = total_s * threadIdx.x / sms;
+        KvSharedCta w = {-1, 0, total_s * (threadIdx.x + 1) / sms};
         int lo = 0, hi = s.num_segments;  // the last segment that begins at or before `from`
         while (hi - lo > 1) {
             const int m = (lo + hi) >> 1;
@@ -375,7 +470,7 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
             at = g.cost0 + static_cast<int64_t>(w.item) * g.cost;
             break;
         }
-        if (at >= w.end) w.seg = -1;
+        if (at >= w.end || static_cast<int>(threadIdx.x) >= sms) w.seg = -1;
         s.cta[threadIdx.x] = w;
     }
 }
@@ -1068,6 +1163,16 @@ cudaError_t launch_join(const KvSharedArgs &s, cudaStream_t stream) {
 
 // ------------------------------------------------------------------ launches
 
+// What a tile of rows' own tokens costs an SM, in tiles of a chain (0.63 us), for one KV head and so many columns.  Measured
+// over 16 x 32K tokens, us an SM and tile for 4 / 8 / 16 / 32 / 64 columns: bf16 0.68 / 0.70 / 0.89 / 1.54 / 2.69, of
+// head_dim 64 0.41 / 0.41 / 0.50 / 0.84 / 1.51; FP8 0.63 / 0.64 / 0.66 / 0.99 / 1.68, 0.38 / 0.39 / 0.44 / 0.74 / 1.30.
+float own_tile(bool fp8, int32_t head_dim, float cols) {
+    const float least = head_dim == 128 ? (fp8 ? 1.02f : 1.1f) : fp8 ? 0.62f : 0.66f;
+    const float some = head_dim == 128 ? (fp8 ? 0.47f + cols * 0.034f : 0.56f + cols * 0.058f)
+                                       : fp8 ? 0.23f + cols * 0.029f : 0.28f + cols * 0.033f;
+    return some > least ? some : least;
+}
+
 template <bool kFp8, int D>
 cudaError_t launch_shared(const KvSharedArgs &s, cudaStream_t stream) {
     using C = SharedCfg<kFp8, D>;
@@ -1098,7 +1203,7 @@ size_t kv_attention_shared_workspace_bytes(int64_t num_rows, int32_t num_heads, 
     const size_t entries = shared_entries(num_rows, num_heads, kv_heads, max_ctx, num_segments) * static_cast<size_t>(num_heads);
     return kv_attention_workspace_bytes(num_rows, num_heads, kv_heads, head_dim, max_ctx, true) +
            3 * align256(static_cast<size_t>(num_rows) * 4) +
-           align256(static_cast<size_t>(num_segments) * sizeof(KvSharedSeg)) + align256(kSharedCtas * sizeof(KvSharedCta)) +
+           align256((2 + kOwnSms) * 4) + align256(static_cast<size_t>(num_segments) * sizeof(KvSharedSeg)) + align256(kSharedCtas * sizeof(KvSharedCta)) +
            align256(entries * static_cast<size_t>(head_dim) * 4) + align256(entries * 8) +
            align256(pairs * 2 * static_cast<size_t>(head_dim)) + align256(pairs * 4);
 }
@@ -1125,6 +1230,13 @@ cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, 
     s.row_seg = reinterpret_cast<int32_t *>(take(rows));
     s.seg = reinterpret_cast<KvSharedSeg *>(take(align256(static_cast<size_t>(seg.num_segments) * sizeof(KvSharedSeg))));
     s.cta = reinterpret_cast<KvSharedCta *>(take(align256(kSharedCtas * sizeof(KvSharedCta))));
+    s.own_sms = reinterpret_cast<int32_t *>(take(align256((2 + kOwnSms) * 4)));
+    const int64_t cols = static_cast<int64_t>(a.group) * (a.num_heads / a.kv_heads);
+    s.beside = static_cast<int64_t>(a.num_rows / a.group) * a.kv_heads * ((cols + 63) / 64) *
+                   kv_parts_bound(a.max_ctx, kv_parts_shift(a.kv_heads)) >
+               2 * kSharedCtas;
+    s.own_tile = own_tile(a.fp8, a.head_dim, static_cast<float>(cols < 64 ? cols : 64));
+    s.own_item = 3.1f;
     const size_t entries = shared_entries(a.num_rows, a.num_heads, a.kv_heads, a.max_ctx, seg.num_segments) *
                            static_cast<size_t>(a.num_heads);
     s.so = reinterpret_cast<float *>(take(align256(entries * static_cast<size_t>(a.head_dim) * 4)));
@@ -1151,6 +1263,7 @@ cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, 
     a.row_ctx = s.own_ctx;
     a.row_begin = s.row_begin;
     a.keep_parts = true;
+    a.own_sms = s.own_sms;
     e = launch_kv_attention_parts(a, workspace, stream);
     if (e != cudaSuccess) return e;
     s.a = a;

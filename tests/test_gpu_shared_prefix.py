@@ -387,6 +387,24 @@ def test_shared_calls_in_graphs_on_streams_and_at_once():
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_shared_calls_beside_other_work(fmt, dim):
+    """SMs that other kernels hold: whichever are left to the rows' own tokens, all of those are read."""
+    c = Shared(46, fmt, [(4000, [4001 + 97 * i for i in range(40)])], 4, 8, dim, 64)
+    want, stream = c.run(), torch.cuda.Stream()
+    c.check(*want, rows=[0, 17, 39])
+    a = torch.randn(2048, 2048, device="cuda", dtype=torch.bfloat16)
+    for i in range(20):
+        with torch.cuda.stream(stream):
+            for _ in range(1 + i % 4):
+                a @ a
+                a.sum()
+        got = c.run()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_shared_where_it_pays(fmt):
     """The library's choice: a call too small by its shapes is the plain one, bit for bit, and a segment that saves too
     little beside one that saves enough is as if it shared nothing."""
