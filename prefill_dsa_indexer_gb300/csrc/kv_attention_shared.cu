@@ -95,8 +95,8 @@ __device__ __forceinline__ KvSharedSeg read_segment(const KvSharedSeg *p) {
 }
 
 // Rows' own tokens in parts of 2^10 at least where a segment has so many (row group, KV head): 32 rows of 4 KV heads and 32K
-// tokens, with 100 to 4,096 of their own: 61 us, with 2^8 66; 256 rows of 64K 390 and 394; but four segments of 4 row
-// groups 76 and 72
+// tokens, with 100 to 4,096 of their own: 50.7 us, with 2^9 53.6, with 2^8 57.7; 256 rows of 64K 354 and with 2^8 436; but
+// four segments of 4 row groups 60.5 and 54.8
 constexpr int32_t kManyGroups = 128, kManyPartMin = 10;
 constexpr int32_t kItemTiles = 12;  // what an item costs beside its tiles
 constexpr int32_t kMinTiles = 4;    // of a part
@@ -106,13 +106,13 @@ constexpr int32_t kMinTiles = 4;    // of a part
 // that is spent already, a segment has to save half, and of several each its share.
 // us in a graph, 1 to 200 tokens of their own, each row by itself / in a call that shares nothing / shared:
 //                       FP8, 4 heads of 128      bf16, 4 heads of 128     bf16, 3 heads of 64
-//   8 rows of 8K         56 MB  21 / 28 / 30     112 MB  20 / 27 / 25      42 MB  12 / 19 / 20
-//   16 rows of 8K       120 MB  30 / 36 / 32     240 MB  28 / 35 / 26      90 MB  18 / 25 / 20
-//   64 rows of 1K        63 MB  30 / 33 / 33     126 MB  25 / 29 / 26      47 MB  14 / 20 / 22
-//   64 rows of 2K       126 MB  42 / 45 / 33     252 MB  35 / 40 / 26      95 MB  19 / 24 / 22
-//   4 rows of 32K        96 MB  26 / 34 / 34     192 MB  27 / 33 / 30      72 MB  16 / 23 / 21
+//   8 rows of 8K         56 MB  21 / 29 / 26     112 MB  20 / 28 / 24      42 MB  12 / 19 / 19
+//   16 rows of 8K       120 MB  30 / 38 / 27     240 MB  28 / 36 / 24      90 MB  18 / 25 / 20
+//   64 rows of 1K        63 MB  30 / 34 / 28     126 MB  25 / 30 / 24      47 MB  14 / 21 / 21
+//   64 rows of 2K       126 MB  42 / 47 / 30     252 MB  35 / 42 / 24      95 MB  19 / 25 / 22
+//   4 rows of 32K        96 MB  26 / 34 / 32     192 MB  27 / 35 / 29      72 MB  16 / 24 / 21
 int64_t shared_least_bytes(const KvAttnArgs &a) {
-    const int64_t mb = a.fp8 ? 120 : 200;
+    const int64_t mb = a.fp8 ? 100 : 160;
     return (a.head_dim == 64 ? mb * 2 / 3 : mb) << 20;
 }
 

@@ -411,7 +411,7 @@ def test_shared_where_it_pays(fmt):
     c = Shared(33, fmt, [(700, [701, 900, 1000])], 2, 4, 128, 64)
     got, want = c.run(least_saved=0), P.kv_attention(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
-    token, least = 2 * 2 * 128 * (1 if fmt == "fp8" else 2), (120 if fmt == "fp8" else 200) << 20
+    token, least = 2 * 2 * 128 * (1 if fmt == "fp8" else 2), (100 if fmt == "fp8" else 160) << 20
     n = -(-least // (4 * 15 * token * 128)) * 128  # the least that pays for 16 rows, of two segments
     c = Shared(34, fmt, [(n, [n + i for i in range(16)]), (n - 128, [n] * 16)], 2, 2, 128, 128)
     assert 31 * c.max_ctx * token < least  # too little by its shapes
