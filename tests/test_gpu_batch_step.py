@@ -168,6 +168,16 @@ def test_plan_gives_pages_on_that_ended_requests_gave_back():
     assert step.bad
 
 
+@pytest.mark.parametrize("free", [None, 30000])
+def test_plan_takes_back_the_pages_of_long_requests(free):
+    """Runs of them much longer than what a warp goes through at once, beside short and empty ones; or more than the stack
+    has room for."""
+    rng = random.Random(9)
+    context = [rng.choice((0, 1, 500, 40000 + 17 * i, 16 * 257)) for i in range(60)]
+    new = [-1 if i % 3 else rng.randint(0, 200) for i in range(60)]
+    Step(context, new, 16, 4000, first_own=[rng.choice((0, 5, 300)) for _ in range(60)], free=free, count=free and 29000).run()
+
+
 def test_plan_refuses_lengths_that_cannot_be():
     for context, new, extra in (([-1, 20], [3, 4], {}), ([5, 20], [-2, 4], {}), ([40, 20], [9, 13], dict(width=2)),
                                 ([33, 20], [-1, 4], dict(width=2)), ([5, 20], [2147483647, 4], dict(width=4)),
