@@ -118,33 +118,31 @@ __device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req,
 // one of all to look takes what is left (nothing, unless an SM got fewer than two CTAs: then its run of shares may have
 // others' among them, which are made twice, alike).  Warp-collective; out of line, for the callers' registers.
 [[maybe_unused]] static __device__ __noinline__ void kv_share(int32_t *own_sms, KvSchedule *sched, int lane) {
-    const int sms = __ldcg(own_sms);
+    int32_t *arrived = own_sms + 1, *taken = own_sms + 2;
+    uint32_t sm;
+    asm volatile("mov.u32 %0, %%smid;" : "=r"(sm));
+    // (one latency for the three; one CTA may be seen to have come and not yet to have taken, so a share be made twice)
+    int32_t v = 2;
+    if (lane == 0 && sm < kOwnSms) v = atomicAdd(taken + sm, 1);
+    if (lane == 1) v = atomicAdd(arrived, 1);
+    if (lane == 2) v = __ldcg(own_sms);
+    const int n = __shfl_sync(0xffffffffu, v, 0), before = __shfl_sync(0xffffffffu, v, 1), sms = __shfl_sync(0xffffffffu, v, 2);
     int mine = static_cast<int>(blockIdx.x), upto = mine + 1, of = static_cast<int>(gridDim.x);
     if (2 * sms < of) {
-        int *arrived = own_sms + 1, *taken = own_sms + 2;
-        uint32_t sm;
-        asm volatile("mov.u32 %0, %%smid;" : "=r"(sm));
+        const bool last = before + 1 == of;
         of = 2 * sms;
         mine = of;
         upto = 0;
-        int last = 0;
-        if (lane == 0) {
-            if (sm < static_cast<uint32_t>(sms)) {
-                const int n = atomicAdd(taken + sm, 1);
-                if (n < 2) {
-                    mine = 2 * static_cast<int>(sm) + n;
-                    upto = mine + 1;
-                }
-                __threadfence();
-            }
-            last = atomicAdd(arrived, 1) + 1 == static_cast<int>(gridDim.x);
+        if (sm < static_cast<uint32_t>(sms) && n < 2) {
+            mine = 2 * static_cast<int>(sm) + n;
+            upto = mine + 1;
         }
-        if (__shfl_sync(0xffffffffu, last, 0)) {
+        if (last) {
             __threadfence();
             for (int i = lane; i < sms; i += 32) {
-                const int n = __ldcg(taken + i);
-                if (n >= 2) continue;
-                mine = min(mine, 2 * i + n);
+                const int there = __ldcg(taken + i);
+                if (there >= 2) continue;
+                mine = min(mine, 2 * i + there);
                 upto = max(upto, 2 * i + 2);
             }
             mine = __reduce_min_sync(0xffffffffu, mine);
