@@ -53,7 +53,7 @@ __device__ __forceinline__ int32_t kv_part_shift(int32_t ctx, int32_t parts_shif
 constexpr int32_t kBeginUnit = 128;
 
 __device__ __forceinline__ int32_t kv_begin(const KvAttnArgs &a, int row) {
-    return a.row_begin == nullptr ? kPartMin : a.row_begin[row];
+    return __builtin_expect(a.row_begin == nullptr, 1) ? kPartMin : a.row_begin[row];
 }
 __device__ __forceinline__ int32_t kv_part_min(int32_t begin) { return begin & (kBeginUnit - 1); }
 
@@ -159,7 +159,7 @@ __device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req,
 // Fills `sched`; every thread of the CTA calls it, then __syncthreads.
 __device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule *sched) {
     if (kv_direct(a)) return;
-    if (a.own_sms != nullptr) {
+    if (__builtin_expect(a.own_sms != nullptr, 0)) {
         if (threadIdx.x < 32) kv_share(a.own_sms, sched, threadIdx.x);
         __syncthreads();
         if (sched->mine >= sched->upto) return;
@@ -262,7 +262,7 @@ struct KvCursor {
         // total * b / n: exact for products below 2^64 / n, and no total is near (a token costs 2^-6 or less)
         const uint64_t total = sched->before[entries];
         uint64_t from;
-        if (a.own_sms == nullptr) {
+        if (__builtin_expect(a.own_sms == nullptr, 1)) {
             from = __umul64hi(total * blockIdx.x, a.ctas_inv);
             end = __umul64hi(total * (blockIdx.x + 1), a.ctas_inv);
         } else {

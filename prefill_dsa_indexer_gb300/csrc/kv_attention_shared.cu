@@ -4,9 +4,9 @@
 //
 // where the tokens before a segment's S are the same for all of its rows.  The sum is split at S: the shared tokens are
 // read once for all rows of the segment (kv_shared_kernel), each row reads the others by itself (kv_attention.cu, from
-// an offset into its table, on SMs of its own), and kv_join_kernel adds the parts up by log-sum-exp.  kv_segments_kernel works out S, a
-// multiple of 128, and who does what.  S is at most what every row of the segment that sees any token sees, so no
-// score of a shared token is ever masked, whatever its V holds.
+// an offset into its table, on SMs of its own), and kv_join_kernel adds the parts up by log-sum-exp.  kv_segments_kernel
+// works out S, a multiple of 128, and who does what.  S is at most what every row of the segment that sees any token
+// sees, so no score of a shared token is ever masked, whatever its V holds.
 //
 // A token of a KV head is 4 D bytes in bf16 (2 D in e4m3) and serves N = rows x query heads per KV head columns at
 // 4 D FLOP each: from N = 300 in bf16 (150 in e4m3) on the products take longer than the bytes.  So the columns go on
@@ -139,7 +139,8 @@ __device__ __forceinline__ void check_segments(const KvSharedArgs &s, int32_t *t
     const KvAttnArgs &a = s.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // a segment begins at or behind every bound before it
-    const int per = (s.num_segments + kSegThreads) / kSegThreads, lo = min(s.num_segments + 1, static_cast<int>(threadIdx.x) * per);
+    const int per = (s.num_segments + kSegThreads) / kSegThreads;
+    const int lo = min(s.num_segments + 1, static_cast<int>(threadIdx.x) * per);
     const int hi = min(s.num_segments + 1, lo + per);
     int32_t top = INT32_MIN;
     for (int i = lo; i < hi; ++i) top = max(top, s.first_row[i]);
@@ -172,7 +173,8 @@ __device__ __forceinline__ void split_queries(const KvSharedArgs &s, int cta, in
     constexpr int kLanes = D / 16, kAt = 32 / kLanes;
     const KvAttnArgs &a = s.a;
     const int lane = threadIdx.x & 31, unit = lane % kLanes;
-    const int64_t pairs = static_cast<int64_t>(a.num_rows) * a.num_heads, warps = static_cast<int64_t>(ctas) * (kSegThreads / 32);
+    const int64_t pairs = static_cast<int64_t>(a.num_rows) * a.num_heads;
+    const int64_t warps = static_cast<int64_t>(ctas) * (kSegThreads / 32);
     for (int64_t p0 = (cta * (kSegThreads / 32) + (threadIdx.x >> 5)) * kAt; p0 < pairs; p0 += warps * kAt) {
         const int64_t p = p0 + lane / kLanes;
         uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hpg = a.num_heads / a.kv_heads;
     int32_t *ctx = a.num_rows <= kSegRows ? ctx_s : s.own_ctx;  // what each row reads itself (-1: its group is refused)
     KvSharedSeg *seg = s.num_segments <= kSegSegs ? seg_s : s.seg;
-    // what the rows' own tokens cost is right to within the length of the parts, which is as in a segment of all rows
+    // (parts as in a segment of all rows: near enough for what all own tokens cost)
     const int32_t any_part_min = a.num_rows / a.group * a.kv_heads >= kManyGroups ? kManyPartMin : kPartMin;
     const float own_heads = static_cast<float>(a.kv_heads * ((a.group * hpg + 63) / 64));
     if (threadIdx.x == 0) own_s = 0;
@@ -355,8 +357,8 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
             }
             const float join = static_cast<float>(g.rows) * static_cast<float>(a.num_heads * a.head_dim) * 0x1p-18f;
             const auto time_of = [&](int p) {
-                return rounds_of(all * static_cast<float>(p), sms) * static_cast<float>((g.tiles + p - 1) / p * each + kItemTiles) +
-                       join * static_cast<float>(p);
+                const float item = static_cast<float>((g.tiles + p - 1) / p * each + kItemTiles);
+                return rounds_of(all * static_cast<float>(p), sms) * item + join * static_cast<float>(p);
             };
             float best = INFINITY;
             for (int p = 1 + lane; p <= most; p += 32) best = fminf(best, time_of(p));
@@ -364,12 +366,12 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
             int first = INT32_MAX, last = 0;
             for (int p = 1 + lane; p <= most; p += 32) {
                 const float time = time_of(p);
-                if (time == best) first = min(first, p);
+                if (time <= 1.0001f * best) first = min(first, p);
                 if (time <= 1.125f * best) last = p;
             }
             first = __reduce_min_sync(0xffffffffu, first);
             last = __reduce_max_sync(0xffffffffu, last);
-            g.parts = s.num_segments > 1 ? last : first;
+            g.parts = max(1, min(s.num_segments > 1 ? last : first, most));
             g.entries = narrow ? 2 * g.parts : g.parts;
             g.cost = (g.tiles + g.parts - 1) / g.parts * each + kItemTiles;
         }
@@ -542,7 +544,8 @@ struct SharedCfg {
     static constexpr int kVBytes = kFp8 ? kTile * D * 2 : 0;          // V of a tile in fp16
     static constexpr int kVBufs = kFp8 ? 3 : 0;
     // A ring for K and one for V, each of an even number of slots: a tile's are those of every other tile.
-    static constexpr int kRoom = (229376 - 2 * kQBytes - kVBufs * kVBytes) / (2 * kSlotBytes) / 2 * 2, kSlots = kRoom > 6 ? 6 : kRoom;
+    static constexpr int kRoom = (229376 - 2 * kQBytes - kVBufs * kVBytes) / (2 * kSlotBytes) / 2 * 2;
+    static constexpr int kSlots = kRoom > 6 ? 6 : kRoom;
     static_assert(kSlots >= 2, "rings");
     static constexpr int kWarpgroups = kFp8 ? 4 : 3;  // two of softmax, (one that converts V,) the producer and the issuer
     static constexpr int kThreads = 128 * kWarpgroups;
@@ -562,7 +565,8 @@ struct SharedCfg {
 
 // 16 bytes to shared memory while the thread goes on; zeros unless `there`.
 __device__ __forceinline__ void copy16(void *dst, const void *src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
 }
 
 // A warp's 32 columns (lane l: column l's 2 D bytes at `src`, NULL behind the last) into the chain's image, from row
@@ -575,7 +579,8 @@ __device__ __forceinline__ void put_queries(uint8_t *img, const uint8_t *src, in
     const int unit = lane % kLanes, sub = lane / kLanes;
 #pragma unroll 1
     for (int n = sub; n < 32; n += kCols) {
-        const uint8_t *q = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), n));
+        const auto *q = reinterpret_cast<const uint8_t *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), n));
         const int r = n0 + n;
         const uint32_t at = kFp8 && D == 64 ? (unit >> 2) * (kTile * 64) + r * 64 + (((unit & 3) ^ (r >> 1 & 3)) << 4)
                                             : (unit >> 3) * (kTile * 128) + fp8mla::sw128(r, unit & 7);
@@ -959,7 +964,8 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
                 ok = wait_mbar_warp(&o_full[c], outs & 1, abort);
                 ++outs;
             }
-            if (of == c && !w.wide) ok = ok && wait_mbar_warp(q_empty, items & 1, abort);  // (the other chain's scores read it too)
+            // (the other chain's scores read the image too)
+            if (of == c && !w.wide) ok = ok && wait_mbar_warp(q_empty, items & 1, abort);
             if (!ok) break;
             tc_fence_after();
             // kDims dims of the warp's 32 columns at a time, where its own part of the image is: another warp of the chain
@@ -1156,7 +1162,8 @@ cudaError_t launch_join(const KvSharedArgs &s, cudaStream_t stream) {
     const int64_t pairs = static_cast<int64_t>(s.a.num_rows) * s.a.num_heads;
     if (pairs > 0x7fffffff) return cudaErrorInvalidConfiguration;
     constexpr int kPairs = kJoinThreads / 32;
-    if (pairs < kJoinPairs) return launch_pdl(kv_join_kernel<D, 4>, dim3(static_cast<unsigned>(pairs)), dim3(kJoinThreads), 0, stream, s);
+    if (pairs < kJoinPairs)
+        return launch_pdl(kv_join_kernel<D, 4>, dim3(static_cast<unsigned>(pairs)), dim3(kJoinThreads), 0, stream, s);
     return launch_pdl(kv_join_kernel<D, 1>, dim3(static_cast<unsigned>((pairs + kPairs - 1) / kPairs)), dim3(kJoinThreads), 0,
                       stream, s);
 }
@@ -1200,10 +1207,12 @@ size_t shared_entries(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int
 size_t kv_attention_shared_workspace_bytes(int64_t num_rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
                                            int32_t max_ctx, int32_t num_segments, bool fp8) {
     const size_t pairs = fp8 ? static_cast<size_t>(num_rows) * static_cast<size_t>(num_heads) : 0;
-    const size_t entries = shared_entries(num_rows, num_heads, kv_heads, max_ctx, num_segments) * static_cast<size_t>(num_heads);
+    const size_t entries =
+        shared_entries(num_rows, num_heads, kv_heads, max_ctx, num_segments) * static_cast<size_t>(num_heads);
     return kv_attention_workspace_bytes(num_rows, num_heads, kv_heads, head_dim, max_ctx, true) +
            3 * align256(static_cast<size_t>(num_rows) * 4) +
-           align256((2 + kOwnSms) * 4) + align256(static_cast<size_t>(num_segments) * sizeof(KvSharedSeg)) + align256(kSharedCtas * sizeof(KvSharedCta)) +
+           align256(static_cast<size_t>(num_segments) * sizeof(KvSharedSeg)) +
+           align256(kSharedCtas * sizeof(KvSharedCta)) + align256((2 + kOwnSms) * 4) +
            align256(entries * static_cast<size_t>(head_dim) * 4) + align256(entries * 8) +
            align256(pairs * 2 * static_cast<size_t>(head_dim)) + align256(pairs * 4);
 }
