@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool direct = kv_direct(a);
     if (direct || a.keep_parts) pdl_launch_dependents();
     KvSchedule *sched = reinterpret_cast<KvSchedule *>(smem + C::OFF_SCHED);
-    kv_fill_schedule(a, sched);
+    if (!kv_fill_schedule(a, sched)) return;
     __syncthreads();
 
     const int hpg = a.hpg, cols = a.group * hpg;

@@ -156,13 +156,14 @@ __device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req,
     }
 }
 
-// Fills `sched`; every thread of the CTA calls it, then __syncthreads.
-__device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule *sched) {
-    if (kv_direct(a)) return;
+// Fills `sched`; every thread of the CTA calls it, then __syncthreads.  False: the CTA is to leave its SM to another kernel,
+// at once, since that one waits for its place.
+__device__ __forceinline__ bool kv_fill_schedule(const KvAttnArgs &a, KvSchedule *sched) {
+    if (kv_direct(a)) return true;
     if (__builtin_expect(a.own_sms != nullptr, 0)) {
         if (threadIdx.x < 32) kv_share(a.own_sms, sched, threadIdx.x);
         __syncthreads();
-        if (sched->mine >= sched->upto) return;
+        if (sched->mine >= sched->upto) return false;
     }
     const int per = a.sched_per, entries = a.sched_entries;
     for (int e = threadIdx.x; e < entries; e += blockDim.x) {
@@ -209,6 +210,7 @@ __device__ __forceinline__ void kv_fill_schedule(const KvAttnArgs &a, KvSchedule
             carry = __shfl_sync(0xffffffffu, v, 31);
         }
     }
+    return true;
 }
 
 // An item, and the way to the next one of this CTA.  Warp-collective.
@@ -266,7 +268,6 @@ struct KvCursor {
             from = __umul64hi(total * blockIdx.x, a.ctas_inv);
             end = __umul64hi(total * (blockIdx.x + 1), a.ctas_inv);
         } else {
-            if (sched->mine >= sched->upto) return false;
             from = total * sched->mine / sched->of;
             end = total * sched->upto / sched->of;
         }

@@ -352,7 +352,10 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
     const bool direct = kv_direct(a);
     if (direct || a.keep_parts) pdl_launch_dependents();
     KvSchedule *sched = reinterpret_cast<KvSchedule *>(smem + C::OFF_SCHED);
-    kv_fill_schedule(a, sched);
+    if (!kv_fill_schedule(a, sched)) {
+        if (warp == kScores) tmem_dealloc(tmem, C::kTmemCols);
+        return;
+    }
     __syncthreads();
 
     const int hpg = a.hpg, cols = a.group * hpg;
