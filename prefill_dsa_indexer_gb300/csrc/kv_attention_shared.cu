@@ -24,8 +24,8 @@
 //
 // What bounds it (4 KV heads of 128, in a graph): many rows, the chain of a tile: 1,024 cycles of MMA, 830 of
 // exponentials, 500 to 600 of waits between them, so that two chains take 2,350 (bf16) to 2,450 (FP8) cycles a tile where
-// the tensor core needs 2,048.  256 rows of 64K, 16 query heads each: 550 GFLOP in 352 us (1.56 PFLOP/s, 0.82 of cuBLAS's
-// burst), 128 SMs at the shared tokens for 325 of them.  64 rows of 64K and 8, bf16: 70 us for 36 of products.  Few rows,
+// the tensor core needs 2,048.  256 rows of 64K, 16 query heads each: 550 GFLOP in 351 us (1.57 PFLOP/s, 0.82 of cuBLAS's
+// burst), 128 SMs at the shared tokens for 325 of them.  64 rows of 64K and 8, bf16: 69 us for 36 of products.  Few rows,
 // bytes: 4 rows of 128K, bf16 65 us, 268 MB.  Below that the latencies of four kernels: checks 6, a shared item's start
 // (7,000 cycles to its first weights) and output (6,300: 128 KB at what an SM writes) 7, join 5 us.  Head_dim 64 has
 // half the products and as many exponentials: 256 rows of 32K 167 us against 71 of products.
@@ -231,8 +231,8 @@ __device__ __forceinline__ T warp_sum(T x) {
 // The rows' own tokens wait for memory most of the time and the shared ones for the tensor core, and an SM has room for
 // one of the two kernels.  So the own ones get some SMs (KvAttnArgs.own_sms) and the shared ones the others, so many that
 // both end together, or all SMs one after the other where that is as good.  us, one after the other / beside: 32 rows of
-// 32K and 100 to 4,096 59.6 / 50.0, verify rows of 16 requests 60.4 / 53.6, 256 rows of 64K 367 / 352, 64 rows of 64K
-// bf16 71 / 70, 45 ragged rows of head_dim 64 24.9 / 23.1.
+// 32K and 100 to 4,096 59.6 / 49.3, verify rows of 16 requests 60.4 / 52.4, 256 rows of 64K 367 / 351, 64 rows of 64K
+// bf16 71 / 69, 45 ragged rows of head_dim 64 24.9 / 23.0.
 constexpr int kFewestSms = 8, kMostSms = kSharedCtas - 4;
 
 __device__ __forceinline__ float rounds_of(float items, float sms) { return ceilf(__fdiv_rn(items, sms)); }
