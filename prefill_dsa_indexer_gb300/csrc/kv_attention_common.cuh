@@ -114,19 +114,22 @@ __device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req,
     return a.block_table + static_cast<int64_t>(req) * a.bt_stride + ((begin & -kBeginUnit) >> a.page_shift);
 }
 
-// The share of a CTA where only own_sms[0] SMs are to work: the CTAs that are there take two shares each SM, and the last
-// one of all to look takes what is left (nothing, unless an SM got fewer than two CTAs: then its run of shares may have
-// others' among them, which are made twice, alike).  Warp-collective; out of line, for the callers' registers.
+// The share of a CTA where only own_sms[0] SMs are to work: the CTAs that are there take two shares each SM.  One that comes
+// when others have left already (for want of room: an SM may be another kernel's) takes one that nobody took, and what is
+// left after that the last one of all to come (its run of shares may then have others' among them, made twice and alike).
+// Warp-collective; out of line, for the callers' registers.
 [[maybe_unused]] static __device__ __noinline__ void kv_share(int32_t *own_sms, KvSchedule *sched, int lane) {
-    int32_t *arrived = own_sms + 1, *taken = own_sms + 2;
+    int32_t *arrived = own_sms + 1, *left = own_sms + 2, *taken = own_sms + kOwnCounters;
     uint32_t sm;
     asm volatile("mov.u32 %0, %%smid;" : "=r"(sm));
-    // (one latency for the three; one CTA may be seen to have come and not yet to have taken, so a share be made twice)
+    // (one latency for all)
     int32_t v = 2;
     if (lane == 0 && sm < kOwnSms) v = atomicAdd(taken + sm, 1);
     if (lane == 1) v = atomicAdd(arrived, 1);
     if (lane == 2) v = __ldcg(own_sms);
-    const int n = __shfl_sync(0xffffffffu, v, 0), before = __shfl_sync(0xffffffffu, v, 1), sms = __shfl_sync(0xffffffffu, v, 2);
+    if (lane == 3) v = __ldcg(left);
+    const int n = __shfl_sync(0xffffffffu, v, 0), before = __shfl_sync(0xffffffffu, v, 1);
+    const int sms = __shfl_sync(0xffffffffu, v, 2), gone = __shfl_sync(0xffffffffu, v, 3);
     int mine = static_cast<int>(blockIdx.x), upto = mine + 1, of = static_cast<int>(gridDim.x);
     if (2 * sms < of) {
         const bool last = before + 1 == of;
@@ -137,16 +140,38 @@ __device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req,
             mine = 2 * static_cast<int>(sm) + n;
             upto = mine + 1;
         }
-        if (last) {
-            __threadfence();
-            for (int i = lane; i < sms; i += 32) {
-                const int there = __ldcg(taken + i);
-                if (there >= 2) continue;
-                mine = min(mine, 2 * i + there);
-                upto = max(upto, 2 * i + 2);
+        for (int tries = gone > 0 ? 16 : 0; tries > 0 && mine >= upto; --tries) {
+            int at = sms;  // of the SMs from one on that differs from CTA to CTA, the first with a share left
+            for (int i = lane; i < sms && at == sms; i += 32)
+                if (__ldcg(taken + (before + i) % sms) < 2) at = i;
+            at = __reduce_min_sync(0xffffffffu, at);
+            if (at == sms) break;
+            const int from = (before + at) % sms;
+            const int m = __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(taken + from, 1) : 0, 0);
+            if (m < 2) {
+                mine = 2 * from + m;
+                upto = mine + 1;
             }
-            mine = __reduce_min_sync(0xffffffffu, mine);
-            upto = __reduce_max_sync(0xffffffffu, upto);
+        }
+        if (mine >= upto && lane == 0) atomicAdd(left, 1);
+        if (last) {  // (the others have come, and take theirs within a few us)
+            int lo = of, hi = 0;
+            for (int tries = 0; tries < 32; ++tries) {
+                lo = of;
+                hi = 0;
+                for (int i = lane; i < sms; i += 32) {
+                    const int there = __ldcg(taken + i);
+                    if (there >= 2) continue;
+                    lo = min(lo, 2 * i + there);
+                    hi = max(hi, 2 * i + 2);
+                }
+                lo = __reduce_min_sync(0xffffffffu, lo);
+                hi = __reduce_max_sync(0xffffffffu, hi);
+                if (lo >= hi) break;
+                __nanosleep(500);
+            }
+            mine = min(mine, lo);
+            upto = max(upto, hi);
         }
     }
     if (lane == 0) {
