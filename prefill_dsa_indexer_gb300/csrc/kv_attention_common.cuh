@@ -140,8 +140,10 @@ __device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req,
             mine = 2 * static_cast<int>(sm) + n;
             upto = mine + 1;
         }
+#pragma unroll 1
         for (int tries = gone > 0 ? 16 : 0; tries > 0 && mine >= upto; --tries) {
             int at = sms;  // of the SMs from one on that differs from CTA to CTA, the first with a share left
+#pragma unroll 1
             for (int i = lane; i < sms && at == sms; i += 32)
                 if (__ldcg(taken + (before + i) % sms) < 2) at = i;
             at = __reduce_min_sync(0xffffffffu, at);
@@ -156,9 +158,11 @@ __device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req,
         if (mine >= upto && lane == 0) atomicAdd(left, 1);
         if (last) {  // (the others have come, and take theirs within a few us)
             int lo = of, hi = 0;
+#pragma unroll 1
             for (int tries = 0; tries < 32; ++tries) {
                 lo = of;
                 hi = 0;
+#pragma unroll 1
                 for (int i = lane; i < sms; i += 32) {
                     const int there = __ldcg(taken + i);
                     if (there >= 2) continue;
