@@ -48,12 +48,25 @@ __device__ __forceinline__ int32_t kv_part_shift(int32_t ctx, int32_t parts_shif
     return part_min + (32 - __clz(max(ctx - 1, 0) >> (part_min + parts_shift)));
 }
 
+// A read, before the kernel's own griddepcontrol.wait, of what an earlier kernel wrote: the rows' lengths in the merges
+// (kv_combine_kernel, kv_join_kernel); the split, the block table and the queries in kv_shared_kernel.  The writer was
+// complete when the attention kernel in between passed its wait, and only then did that one let the next start, so the
+// values are in L2.  But L1 may hold what a call before this one read at the same address (the same workspace in every
+// layer, a block table that each step extends), and only the wait promises otherwise: so whatever is read before it is read
+// past L1, by this, by cp.async.cg or by TMA.
+template <typename T>
+__device__ __forceinline__ T early_read(const T *p) {
+    return __ldcg(p);
+}
+
 // What KvAttnArgs.row_begin says of a row: the first of its tokens that are read here, and log2 of its parts' least
 // tokens below that (kPartMin or more).
 constexpr int32_t kBeginUnit = 128;
 
+template <bool kEarly = false>
 __device__ __forceinline__ int32_t kv_begin(const KvAttnArgs &a, int row) {
-    return __builtin_expect(a.row_begin == nullptr, 1) ? kPartMin : a.row_begin[row];
+    if (__builtin_expect(a.row_begin == nullptr, 1)) return kPartMin;
+    return kEarly ? early_read(a.row_begin + row) : a.row_begin[row];
 }
 __device__ __forceinline__ int32_t kv_part_min(int32_t begin) { return begin & (kBeginUnit - 1); }
 
@@ -100,10 +113,12 @@ __device__ __forceinline__ bool kv_refused(const KvAttnArgs &a, int n, int req, 
 }
 
 // A lane's context of the group (of row `lane`, or of the first), its rows' request, and whether it is refused: then
-// all contexts are 0.  Warp-collective.
+// all contexts are 0.  Warp-collective.  kEarly: before the kernel's wait.
+template <bool kEarly = false>
 __device__ __forceinline__ int kv_load_group(const KvAttnArgs &a, int row0, int lane, int &req, bool &bad) {
     const int row = row0 + (lane < a.group ? lane : 0);
-    const int n = a.row_ctx[row], r = a.row_req[row];
+    const int n = kEarly ? early_read(a.row_ctx + row) : a.row_ctx[row];
+    const int r = kEarly ? early_read(a.row_req + row) : a.row_req[row];
     req = __shfl_sync(0xffffffffu, r, 0);
     bad = __any_sync(0xffffffffu, kv_refused(a, n, r, req));
     return bad ? 0 : n;

@@ -83,14 +83,14 @@ struct KvSharedArgs {
     float *q_factor;              // [R][H] 2^-e (NaN: not only numbers in the query)
 };
 
-// As it is in L2: read before the kernel's wait, past what an earlier kernel may have left in L1.
+// (an early_read)
 __device__ __forceinline__ KvSharedSeg read_segment(const KvSharedSeg *p) {
     union {
         int4 words[3];
         KvSharedSeg seg;
     } u;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) u.words[i] = __ldcg(reinterpret_cast<const int4 *>(p) + i);
+    for (int i = 0; i < 3; ++i) u.words[i] = early_read(reinterpret_cast<const int4 *>(p) + i);
     return u.seg;
 }
 
@@ -506,7 +506,7 @@ struct SharedCursor {
         items = a.a.kv_heads * g.blocks * g.parts;
     }
     __device__ __forceinline__ bool first(const KvSharedArgs &a) {
-        const int4 w = __ldcg(reinterpret_cast<const int4 *>(a.cta + blockIdx.x));  // (a KvSharedCta)
+        const int4 w = early_read(reinterpret_cast<const int4 *>(a.cta + blockIdx.x));  // (a KvSharedCta)
         if (w.x < 0) return false;
         s = w.x;
         i = w.y;
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
             for (; more && go; more = w.next(s)) {
                 const int32_t *table = a.block_table + static_cast<int64_t>(w.g.req) * a.bt_stride;
                 const int page0 = w.t0 << 7 >> a.page_shift, pages = w.tiles << 7 >> a.page_shift;
-                auto load_ids = [&](int p) { return p + lane < pages ? table[page0 + p + lane] : 0; };
+                auto load_ids = [&](int p) { return p + lane < pages ? early_read(table + page0 + p + lane) : 0; };
                 int batch = 0;  // page ids batch .. batch + 31 of the item are in `ids`, one per lane
                 int32_t ids = load_ids(0), ids_next = load_ids(32);
                 for (int i = 0; i < w.tiles; ++i, ++turn) {
@@ -858,7 +858,7 @@ __global__ void __launch_bounds__(SharedCfg<kFp8, D>::kThreads, 1)
             const int64_t at = (w.g.row0 + row) * static_cast<int64_t>(a.num_heads) + head;
             const int steps = w.steps(c);
             float scale = a.s_scale;
-            if (kFp8 && real) scale *= __ldcg(s.q_factor + at);
+            if (kFp8 && real) scale *= early_read(s.q_factor + at);
             if (of == c) {
                 const uint8_t *src = kFp8 ? s.q_terms + at * (2 * D)
                                           : reinterpret_cast<const uint8_t *>(a.q + (w.g.row0 + row) * a.q_stride +
@@ -1040,19 +1040,18 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_cons
     __shared__ float2 t_s[kWarps > 1 ? kWarps : 1];
     const KvAttnArgs &a = s.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp % kWarps;
-    // The kernel before this one starts when kv_segments_kernel is complete, so what that wrote can be read before the
-    // wait
+    // (early_reads of what kv_segments_kernel wrote, and of the call's rows)
     const int64_t at = static_cast<int64_t>(blockIdx.x) * kPairs + warp / kWarps;
     if (kWarps == 1 && at >= static_cast<int64_t>(a.num_rows) * a.num_heads) return;
     const int row = static_cast<int>(at / a.num_heads), head = static_cast<int>(at - static_cast<int64_t>(row) * a.num_heads);
     int req;
     bool bad;
-    const int my_ctx = kv_load_group(a, row / a.group * a.group, lane, req, bad);
+    const int my_ctx = kv_load_group<true>(a, row / a.group * a.group, lane, req, bad);
     const int ctx = __reduce_max_sync(0xffffffffu, my_ctx);
-    const int own = ctx > 0 ? kv_parts(ctx, kv_part_shift(ctx, a.parts_shift, kv_part_min(kv_begin(a, row)))) : 0;
+    const int own = ctx > 0 ? kv_parts(ctx, kv_part_shift(ctx, a.parts_shift, kv_part_min(kv_begin<true>(a, row)))) : 0;
     int parts = own;
     int64_t entry = 0;  // the first shared part
-    const int32_t seg = __ldcg(s.row_seg + row);
+    const int32_t seg = early_read(s.row_seg + row);
     if (seg >= 0) {
         const KvSharedSeg g = read_segment(s.seg + seg);
         const int r = row - g.row0, block = (r * a.hpg + head % a.hpg) / (2 * kTile);

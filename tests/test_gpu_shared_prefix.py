@@ -500,6 +500,51 @@ def test_shared_pages_of_a_large_pool(fmt):
     assert torch.equal(got[0], out) and torch.equal(got[1], lse)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("graph", [False, True])
+def test_shared_calls_whose_inputs_change_in_place(fmt, graph):
+    """Lengths, segments and block table stand at the same addresses in every call of one workspace, and each call finds
+    other ones there: nothing that an earlier call read is taken for this one's (merges and the shared tokens' kernel read
+    before they wait).  Few rows, so that many SMs run none of the kernels that wait first."""
+    cases = [Shared(47, fmt, [(1500, [1501 + 9 * i for i in range(6)]), (400, [500, 600])], 2, 4, 128, 64),
+             Shared(48, fmt, [(300, [310, 460, 610]), (2000, [2100 + 90 * i for i in range(5)])], 2, 4, 128, 64),
+             Shared(49, fmt, [(0, [1, 9, 5, 700]), (0, [4000, 3, 2500, 128])], 2, 4, 128, 64)]
+    most, width = max(c.max_ctx for c in cases), max(c.table.shape[1] for c in cases)
+    H, names = cases[0].q.shape[1], ("table", "row_req", "row_ctx", "starts", "shared")
+    for c in cases:
+        c.table = torch.nn.functional.pad(c.table, (0, width - c.table.shape[1]))
+    ours = {n: torch.empty_like(getattr(cases[0], n)) for n in names}
+    need = P.kv_attention_shared_workspace_size(cases[0].kv, 8, H, most, 2)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+
+    def both(c, a, ws):
+        shared = P.kv_attention_shared(c.kv, a["table"], a["row_req"], a["row_ctx"], most, c.q, a["starts"], a["shared"],
+                                       workspace=ws, least_saved=1)
+        return shared + P.kv_attention(c.kv, a["table"], a["row_req"], a["row_ctx"], most, c.q, workspace=ws)
+    want = []
+    for c in cases:
+        want.append(both(c, {n: getattr(c, n) for n in names}, None))
+        torch.cuda.synchronize()
+
+    def calls():
+        got = []
+        for i in (0, 1, 2, 1, 0, 2, 0, 1):
+            for n in names:
+                ours[n].copy_(getattr(cases[i], n))
+            got.append((i, both(cases[i], ours, ws)))
+        return got
+    if graph:
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            got = calls()
+    for _ in range(5):
+        captured.replay() if graph else None
+        got = got if graph else calls()
+        torch.cuda.synchronize()
+        for i, tensors in got:
+            assert all(torch.equal(x, y) for x, y in zip(tensors, want[i])), i
+
+
 def test_layer_takes_both_of_its_segments_tensors():
     c = Shared(44, "bf16", [(300, [301, 302])], 2, 4, 128, 64)
     layer = P.KvLayer(c.kv, c.table, c.max_ctx, 2, 8, num_segments=1)
