@@ -334,8 +334,7 @@ struct KvPlanArgs {
 
 cudaError_t launch_kv_plan(const KvPlanArgs &a, cudaStream_t s);
 
-constexpr int kOwnSms = 256;  // (SMs from there on do not)
-constexpr int kOwnCounters = 3;
+constexpr int kOwnSms = 256;  // SMs with a counter in own_sms
 
 struct KvAttnArgs {
     const void *pool;
@@ -355,8 +354,8 @@ struct KvAttnArgs {
     const int32_t *row_begin;  // or NULL: each row's tokens before this one (a multiple of 128; below that, how its parts
                                // are cut) are read elsewhere, and row_ctx counts from it; of a row group, one
     bool keep_parts;   // a row's only part goes to the workspace too
-    int32_t *own_sms;  // or NULL; device [kOwnCounters + kOwnSms]: how many SMs are to work, the others being another
-                       // kernel's, and zeros
+    int32_t *own_sms;  // or NULL; device [1 + kOwnSms]: how many SMs are to work, the others being another kernel's, and
+                       // zeros
     const uint16_t *q;
     int64_t q_stride;
     int32_t num_heads;

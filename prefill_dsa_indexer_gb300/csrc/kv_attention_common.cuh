@@ -95,7 +95,7 @@ constexpr int kMaxGroup = 8;        // rows of a group
 constexpr int kSchedEntries = 512;  // running costs kept in shared memory, one for every so many groups
 
 struct KvSchedule {
-    int32_t mine, upto, of;  // with own_sms: this CTA's shares, and how many there are
+    int32_t mine, of;  // with own_sms: this CTA's share (-1: none), and how many there are
     uint64_t before[kSchedEntries + 1];  // cost of all groups before the entry's
 };
 
@@ -129,73 +129,43 @@ __device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req,
     return a.block_table + static_cast<int64_t>(req) * a.bt_stride + ((begin & -kBeginUnit) >> a.page_shift);
 }
 
-// The share of a CTA where only own_sms[0] SMs are to work: the CTAs that are there take two shares each SM.  One that comes
-// when others have left already (for want of room: an SM may be another kernel's) takes one that nobody took, and what is
-// left after that the last one of all to come (its run of shares may then have others' among them, made twice and alike).
-// Warp-collective; out of line, for the callers' registers.
+// The share of a CTA where only own_sms[0] SMs are to work, two shares each: its SM's next one, if it has one left.  Where
+// the SM has none (it is another kernel's, or CTAs of other SMs were quicker), the CTA takes a share of another SM while any
+// is left; but the first two on an SM that is to have none leave at once.
+// Those are at most 2 (gridDim / 2 - own_sms[0]) CTAs, however the CTAs are put and in whatever order they come.  All others,
+// 2 own_sms[0] or more, end with a share or have seen that none is left: so none is left, and an atomic add gives each
+// to one CTA.  Warp-collective; out of line, for the callers' registers.
 [[maybe_unused]] static __device__ __noinline__ void kv_share(int32_t *own_sms, KvSchedule *sched, int lane) {
-    int32_t *arrived = own_sms + 1, *left = own_sms + 2, *taken = own_sms + kOwnCounters;
+    int32_t *taken = own_sms + 1;  // by SM: its shares that are taken (more: nothing was left)
     uint32_t sm;
     asm volatile("mov.u32 %0, %%smid;" : "=r"(sm));
-    // (one latency for all)
-    int32_t v = 2;
+    int32_t v = 2;  // (both in one latency)
     if (lane == 0 && sm < kOwnSms) v = atomicAdd(taken + sm, 1);
-    if (lane == 1) v = atomicAdd(arrived, 1);
-    if (lane == 2) v = __ldcg(own_sms);
-    if (lane == 3) v = __ldcg(left);
-    const int n = __shfl_sync(0xffffffffu, v, 0), before = __shfl_sync(0xffffffffu, v, 1);
-    const int sms = __shfl_sync(0xffffffffu, v, 2), gone = __shfl_sync(0xffffffffu, v, 3);
-    int mine = static_cast<int>(blockIdx.x), upto = mine + 1, of = static_cast<int>(gridDim.x);
+    if (lane == 1) v = __ldcg(own_sms);
+    const int n = __shfl_sync(0xffffffffu, v, 0), sms = __shfl_sync(0xffffffffu, v, 1);
+    const uint32_t ctas = gridDim.x;
+    int mine = static_cast<int>(blockIdx.x), of = static_cast<int>(ctas);
     if (2 * sms < of) {
-        const bool last = before + 1 == of;
+        const bool one_of = sm < static_cast<uint32_t>(sms);
         of = 2 * sms;
-        mine = of;
-        upto = 0;
-        if (sm < static_cast<uint32_t>(sms) && n < 2) {
-            mine = 2 * static_cast<int>(sm) + n;
-            upto = mine + 1;
-        }
+        mine = one_of && n < 2 ? 2 * static_cast<int>(sm) + n : -1;
+        // (an SM is found full once at most, so the bound never ends the search)
+        const int most = mine >= 0 || (!one_of && n < 2 && sm < ctas / 2) ? 0 : sms + 1;
 #pragma unroll 1
-        for (int tries = gone > 0 ? 16 : 0; tries > 0 && mine >= upto; --tries) {
+        for (int tries = 0; tries < most && mine < 0; ++tries) {
             int at = sms;  // of the SMs from one on that differs from CTA to CTA, the first with a share left
 #pragma unroll 1
             for (int i = lane; i < sms && at == sms; i += 32)
-                if (__ldcg(taken + (before + i) % sms) < 2) at = i;
+                if (__ldcg(taken + (blockIdx.x + i) % sms) < 2) at = i;
             at = __reduce_min_sync(0xffffffffu, at);
             if (at == sms) break;
-            const int from = (before + at) % sms;
+            const int from = static_cast<int>((blockIdx.x + at) % sms);
             const int m = __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(taken + from, 1) : 0, 0);
-            if (m < 2) {
-                mine = 2 * from + m;
-                upto = mine + 1;
-            }
-        }
-        if (mine >= upto && lane == 0) atomicAdd(left, 1);
-        if (last) {  // (the others have come, and take theirs within a few us)
-            int lo = of, hi = 0;
-#pragma unroll 1
-            for (int tries = 0; tries < 32; ++tries) {
-                lo = of;
-                hi = 0;
-#pragma unroll 1
-                for (int i = lane; i < sms; i += 32) {
-                    const int there = __ldcg(taken + i);
-                    if (there >= 2) continue;
-                    lo = min(lo, 2 * i + there);
-                    hi = max(hi, 2 * i + 2);
-                }
-                lo = __reduce_min_sync(0xffffffffu, lo);
-                hi = __reduce_max_sync(0xffffffffu, hi);
-                if (lo >= hi) break;
-                __nanosleep(500);
-            }
-            mine = min(mine, lo);
-            upto = max(upto, hi);
+            if (m < 2) mine = 2 * from + m;
         }
     }
     if (lane == 0) {
         sched->mine = mine;
-        sched->upto = upto;
         sched->of = of;
     }
 }
@@ -207,7 +177,7 @@ __device__ __forceinline__ bool kv_fill_schedule(const KvAttnArgs &a, KvSchedule
     if (__builtin_expect(a.own_sms != nullptr, 0)) {
         if (threadIdx.x < 32) kv_share(a.own_sms, sched, threadIdx.x);
         __syncthreads();
-        if (sched->mine >= sched->upto) return false;
+        if (sched->mine < 0) return false;
     }
     const int per = a.sched_per, entries = a.sched_entries;
     for (int e = threadIdx.x; e < entries; e += blockDim.x) {
@@ -313,7 +283,7 @@ struct KvCursor {
             end = __umul64hi(total * (blockIdx.x + 1), a.ctas_inv);
         } else {
             from = total * sched->mine / sched->of;
-            end = total * sched->upto / sched->of;
+            end = total * (sched->mine + 1) / sched->of;
         }
         if (from >= end) return false;
         int lo = 0;  // the last entry with nothing of the share before it

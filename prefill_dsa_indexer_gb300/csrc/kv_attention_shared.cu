@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kSegThreads, 1) kv_segments_kernel(const __gri
         else split_queries<128>(s, blockIdx.x - 1, gridDim.x - 1);
         return;
     }
-    for (int i = 1 + threadIdx.x; i < kOwnCounters + kOwnSms; i += kSegThreads) s.own_sms[i] = 0;
+    for (int i = 1 + threadIdx.x; i < 1 + kOwnSms; i += kSegThreads) s.own_sms[i] = 0;
     // every row by itself at first
     float mine = 0.f;
     for (int g = threadIdx.x; g < a.num_rows / a.group; g += kSegThreads) {
@@ -1211,7 +1211,7 @@ size_t kv_attention_shared_workspace_bytes(int64_t num_rows, int32_t num_heads, 
     return kv_attention_workspace_bytes(num_rows, num_heads, kv_heads, head_dim, max_ctx, true) +
            3 * align256(static_cast<size_t>(num_rows) * 4) +
            align256(static_cast<size_t>(num_segments) * sizeof(KvSharedSeg)) +
-           align256(kSharedCtas * sizeof(KvSharedCta)) + align256((kOwnCounters + kOwnSms) * 4) +
+           align256(kSharedCtas * sizeof(KvSharedCta)) + align256((1 + kOwnSms) * 4) +
            align256(entries * static_cast<size_t>(head_dim) * 4) + align256(entries * 8) +
            align256(pairs * 2 * static_cast<size_t>(head_dim)) + align256(pairs * 4);
 }
@@ -1238,7 +1238,7 @@ cudaError_t launch_kv_attention_shared(const KvSegmentArgs &seg, KvAttnArgs &a, 
     s.row_seg = reinterpret_cast<int32_t *>(take(rows));
     s.seg = reinterpret_cast<KvSharedSeg *>(take(align256(static_cast<size_t>(seg.num_segments) * sizeof(KvSharedSeg))));
     s.cta = reinterpret_cast<KvSharedCta *>(take(align256(kSharedCtas * sizeof(KvSharedCta))));
-    s.own_sms = reinterpret_cast<int32_t *>(take(align256((kOwnCounters + kOwnSms) * 4)));
+    s.own_sms = reinterpret_cast<int32_t *>(take(align256((1 + kOwnSms) * 4)));
     const int64_t cols = static_cast<int64_t>(a.group) * (a.num_heads / a.kv_heads);
     s.beside = static_cast<int64_t>(a.num_rows / a.group) * a.kv_heads * ((cols + 63) / 64) *
                    kv_parts_bound(a.max_ctx, kv_parts_shift(a.kv_heads)) >
