@@ -961,10 +961,10 @@ class KvLayer:
     """
 
     def __init__(self, kv, block_table, max_ctx, num_rows, num_heads, rope=None, layout=ROPE_HALF, rot_offset=0,
-                 rows_per_group=1, sm_scale=None, num_segments=0):
+                 rows_per_group=1, sm_scale=None, num_segments=0, least_saved=0):
         self.kv, self.block_table, self.max_ctx = kv, block_table, int(max_ctx)
         self.rope, self.layout, self.rot_offset = rope, layout, int(rot_offset)
-        self.rows_per_group, self.sm_scale = rows_per_group, sm_scale
+        self.rows_per_group, self.sm_scale, self.least_saved = rows_per_group, sm_scale, int(least_saved)
         R, H, device = int(num_rows), int(num_heads), kv.pool.device
         self.out = torch.empty((R, H, kv.head_dim), dtype=torch.bfloat16, device=device)
         self.lse = torch.empty((R, H), dtype=torch.float32, device=device)
@@ -975,7 +975,8 @@ class KvLayer:
 
     def run(self, row_req, row_ctx, slots, positions, q, k, v, stream=None, segment_rows=None, segment_ctx=None):
         """q [R, H, head_dim] is rotated in place; returns (out, lse).  With segment_rows and segment_ctx (of at most
-        num_segments segments) the rows' common prefixes are read once (kv_attention_shared)."""
+        num_segments segments) the rows' common prefixes are read once (kv_attention_shared), where that saves the layer's
+        least_saved bytes."""
         if (segment_rows is None) != (segment_ctx is None):
             raise DsaError("segment_rows and segment_ctx come together")
         if self.rope is None:
@@ -987,7 +988,8 @@ class KvLayer:
         if segment_rows is not None:
             return kv_attention_shared(self.kv, self.block_table, row_req, row_ctx, self.max_ctx, q, segment_rows,
                                        segment_ctx, self.sm_scale, self.rows_per_group, out=self.out, lse=self.lse,
-                                       workspace=self.workspace, status=self.status, stream=stream)
+                                       workspace=self.workspace, status=self.status, stream=stream,
+                                       least_saved=self.least_saved)
         return kv_attention(self.kv, self.block_table, row_req, row_ctx, self.max_ctx, q, self.sm_scale,
                             self.rows_per_group, out=self.out, lse=self.lse, workspace=self.workspace,
                             status=self.status, stream=stream)

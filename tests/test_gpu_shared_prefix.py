@@ -639,3 +639,86 @@ def test_steps_of_a_batch_over_a_shared_prefix(fmt, graph):
         c.check(layer.out, layer.lse)
         own = (table[2, whole[0]:-(-ctx[2] // page)].tolist(), table[0, whole[0]:-(-ctx[0] // page)].tolist())
         assert not set(own[0]) & set(own[1])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_layer_shares_what_it_is_told_to(fmt, dim):
+    """A layer's call is kv_attention_shared's, bit for bit, by the layer's least_saved; by the library's choice these few
+    rows are read one by one."""
+    c = Shared(50, fmt, [(1500, [1501, 1700, 2000]), (640, [650 + i for i in range(4)])], 2, 4, dim, 64, after=[30])
+    slots, k = ints([-1] * 8), torch.zeros(8, 2, dim, dtype=torch.bfloat16, device="cuda")
+    plain = P.kv_attention(c.kv, c.table, c.row_req, c.row_ctx, c.max_ctx, c.q)
+    for least, want in ((1, c.run()), (0, plain)):
+        layer = P.KvLayer(c.kv, c.table, c.max_ctx, 8, 8, num_segments=2, least_saved=least)
+        got = layer.run(c.row_req, c.row_ctx, slots, None, c.q, k, k, segment_rows=c.starts, segment_ctx=c.shared)
+        checked(layer.status)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        c.check(*got)
+    assert not torch.equal(c.run()[0], plain[0])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("group", [1, 2])
+def test_steps_of_a_batch_that_reads_its_prefixes_once(fmt, graph, group):
+    """Steps of five requests over two prefixes of several tiles, by the kernels of shared tokens: plan, rotate, insert
+    and attend, captured once and replayed, or eagerly.  The plan's segments are those of its requests, the layer's outputs
+    the formula's and, bit for bit, those of the attention call on what the plan made."""
+    g = gen(51)
+    page, dim, kv_heads, hpg, n, rows = 16, 128, 2, 4, 5, 16
+    H, width, prefix = kv_heads * hpg, 110, [1500, 700]  # tokens of requests 0 - 2 and 3 - 4
+    whole = [p // page for p in prefix]
+    pages = sum(whole) + 60
+    pool = new_pool(g, fmt, pages, kv_heads, page, dim)
+    kv = P.KvCache(pool, *((1 / 72, 1 / 90) if fmt == "fp8" else (1.0, 1.0)))
+    ids = torch.randperm(pages, generator=g, device="cuda").int()
+    table = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+    table[:3, :whole[0]] = ids[:whole[0]]
+    table[3:, :whole[1]] = ids[whole[0]:sum(whole)]
+    free = torch.full((pages,), -1, dtype=torch.int32, device="cuda")
+    free[:60] = ids[sum(whole):]
+    plan = P.KvPlan(n, rows, page, pages, group, num_segments=2)
+    kept = [w * page for w in whole]
+    ctx = [kept[0]] * 3 + [kept[1]] * 2
+    plan.context.copy_(ints(ctx))
+    plan.free_count.fill_(60)
+    first_own, seg_req, seg_ctx = ints([whole[0]] * 3 + [whole[1]] * 2), ints([0, 3, 5]), ints(kept)
+    rope = P.rope_table(64, sections=(12, 10, 10), order="cycle")
+    layer = P.KvLayer(kv, table, width * page, rows, H, rope=rope, rot_offset=32, rows_per_group=group, num_segments=2,
+                      least_saved=1)
+    new, qkv = ints([0] * n), torch.zeros(rows, H + 2 * kv_heads, dim, dtype=torch.bfloat16, device="cuda")
+    parts = qkv[:, :H], qkv[:, H:H + kv_heads], qkv[:, H + kv_heads:]
+
+    def step():
+        plan.run(plan.context, new, table, free, plan.free_count, first_own, seg_req)
+        layer.run(plan.row_req, plan.row_ctx, plan.slots, plan.positions.expand(3, rows), *parts,
+                  segment_rows=plan.segment_rows, segment_ctx=seg_ctx)
+    if graph:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            step()  # (of no tokens)
+        torch.cuda.synchronize()
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            step()
+    wide = lambda t: -(-t // group) * group  # noqa: E731
+    for fresh in ([1, 1, 2, 1, 3], [1, -1, 2, 2, 1], [4, 0, 1, 1, 1], [2, 0, 3, 1, 0], [1, 0, 1, 1, 4]):
+        new.copy_(ints(fresh))
+        qkv.copy_(randn(g, rows, H + 2 * kv_heads, dim))
+        captured.replay() if graph else step()
+        torch.cuda.synchronize()
+        checked(plan.status)
+        checked(layer.status)
+        ctx = [0 if t == -1 else x + t for x, t in zip(ctx, fresh)]
+        starts = [sum(wide(max(t, 0)) for t in fresh[:i]) for i in (0, 3, 5)]
+        assert plan.context.tolist() == ctx and plan.segment_rows.tolist() == starts
+        q = parts[0].contiguous()
+        call = lambda f, *a, **k: f(kv, table, plan.row_req, plan.row_ctx, width * page, q, *a,  # noqa: E731
+                                    rows_per_group=group, **k)
+        want = call(P.kv_attention_shared, plan.segment_rows, seg_ctx, least_saved=1)
+        assert torch.equal(layer.out, want[0]) and torch.equal(layer.lse, want[1])
+        assert not torch.equal(layer.out, call(P.kv_attention)[0])
+        c = object.__new__(Shared)
+        c.fmt, c.dim, c.page, c.hpg, c.pool, c.table, c.sm = fmt, dim, page, hpg, pool, table, dim ** -0.5
+        c.ks, c.vs, c.rows, c.row_req, c.q = kv.k_scale, kv.v_scale, plan.row_ctx.tolist(), plan.row_req, q
+        c.check(layer.out, layer.lse)
