@@ -722,3 +722,31 @@ def test_steps_of_a_batch_that_reads_its_prefixes_once(fmt, graph, group):
         c.fmt, c.dim, c.page, c.hpg, c.pool, c.table, c.sm = fmt, dim, page, hpg, pool, table, dim ** -0.5
         c.ks, c.vs, c.rows, c.row_req, c.q = kv.k_scale, kv.v_scale, plan.row_ctx.tolist(), plan.row_req, q
         c.check(layer.out, layer.lse)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("segments", [1, 3])
+def test_a_rows_bits_depend_on_its_segment_and_the_shapes_alone(fmt, dim, segments):
+    """Two calls of the same shapes, with one segment of 24 rows over many parts the same and everything else of other
+    lengths, prefixes, values and places, so that SMs and items are shared out otherwise."""
+    one = (9000, [9001 + 41 * i for i in range(24)])
+    others = [([(300, [301 + i for i in range(8)]), one, (128, [200] * 8)], [5000 + 700 * i for i in range(6)]),
+              ([(6000, [6001 + 300 * i for i in range(8)]), one, (700, [5, 3000] + [701] * 6)], [1 + i for i in range(6)])]
+    cases = [Shared(52 + i, fmt, s if segments == 3 else [one], 4, 8, dim, 64, after=after if segments == 3 else
+                    after + [n for _, own in (s[0], s[2]) for n in own]) for i, (s, after) in enumerate(others)]
+    a, b = cases
+    at = 8 if segments == 3 else 0
+    most = max(c.max_ctx for c in cases)
+    for c in cases:
+        c.table = torch.nn.functional.pad(c.table, (0, -(-most // 64) - c.table.shape[1]))
+        c.max_ctx = most
+    assert len(a.rows) == len(b.rows) == 46 and a.rows != b.rows
+    for r in range(at, at + 24):  # the same tokens and queries in the other batch's pages
+        for p in range(-(-a.rows[r] // 64)):
+            bits(b.pool)[b.table[r, p].item()] = bits(a.pool)[a.table[r, p].item()]
+    b.q[at:at + 24] = a.q[at:at + 24]
+    want, got = a.run(), b.run()
+    assert torch.equal(got[0][at:at + 24], want[0][at:at + 24]) and torch.equal(got[1][at:at + 24], want[1][at:at + 24])
+    a.check(*want, rows=[0, at, at + 11, at + 23, 45])
+    b.check(*got, rows=[0, at, at + 11, at + 23, 45])
