@@ -670,11 +670,14 @@ size_t dsa_kv_attention_shared_workspace_size(const dsa_kv_cache *cache, int32_t
 /*
  * ---- A step's rows, slots and pages from the lengths of its requests (dsa_kv_plan): the row_req,
  * row_ctx, positions, slots and block table that the calls above take, made on the device, so that
- * a serving loop (or a captured graph of one) needs no host between its steps.
+ * a serving loop (or a captured graph of one) needs no host between its steps, as long as it does not
+ * give up a prefix.
  *
  * Request i has context[i] tokens in the cache, listed by its row of the block table, and gets
  * new_tokens[i] >= 0 more; -1: it has ended, and its pages from first_own[i] on (those before belong
- * to a prefix that others use too) go back to the free ones.  Free pages are a stack, free_count[0]
+ * to a prefix that others use too) go back to the free ones.  Nobody counts a prefix's users here: its
+ * pages stay taken when the last one ends, until whoever keeps that count puts them on the stack
+ * between two steps.  Free pages are a stack, free_count[0]
  * entries of free_pages, the last one taken first: what ended requests give back is put on it, in
  * the order of requests and pages, then the others' new pages are taken, in that order too.  With
  *   need_i = ceil((context_i + new_i) / page_size) - ceil(context_i / page_size)
@@ -687,7 +690,10 @@ size_t dsa_kv_attention_shared_workspace_size(const dsa_kv_cache *cache, int32_t
  * max_rows, is padding: positions and slots -1, row_ctx 0, row_req i (behind the last request's: 0).
  * Bit for bit reproducible.  Lengths that cannot be (context < 0 or longer than a row of the table lists,
  * together with the new tokens too, new_tokens < -1, first_own < 0) are DSA_ERR_BOUNDS, and their
- * request is as one without new tokens; a page id outside the pool in a row's place is, with slot -1;
+ * request is as one without new tokens, which gives no page back either; its context_out is its context
+ * or, with new_tokens -1, 0.  So the pages of an ended request with such lengths stay taken, and its row of the
+ * table, left as it was, lists them: a call in which its context and first_own are put right, and new_tokens is
+ * -1 again, gives them back.  A page id outside the pool in a row's place is DSA_ERR_BOUNDS too, with slot -1;
  * so are a free_count outside [0, free_capacity] (taken as the nearer one), pages given back beyond
  * free_capacity (which are lost), and, unless `granted` is there to tell, a request that gets nothing.
  */

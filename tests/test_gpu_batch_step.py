@@ -198,6 +198,36 @@ def test_plan_refuses_lengths_that_cannot_be():
     assert status.item() == P.ERR_BOUNDS and rows.tolist() == [[0, 1, 0, 0], [17, 0, 0, 0]]
 
 
+@pytest.mark.parametrize("wrong", ["first_own", "context"])
+def test_pages_of_an_ended_request_with_lengths_that_cannot_be_can_be_given_back(wrong):
+    """Contexts in place: the request ends without giving a page back, its row of the table still lists them, and a call
+    with its lengths put right gives them back, to the next request that needs some."""
+    first = Step([70, 20, 5], [-1, 40, 1], 16, 64, first_own=[1, 0, 0], width=5, count=3)
+    context, new, table, free, count = first.tensors()
+    plan, own = first.plan(), ints([1, 0, 0])
+    plan.context.copy_(context)
+    plan.free_count.copy_(count)
+    if wrong == "first_own":
+        first.first_own[0] = own[0] = -1
+    else:
+        first.context[0] = plan.context[0] = 81  # the table lists 80
+    plan.run(plan.context, new, table, free, plan.free_count, own)
+    first.check(plan, table, free)
+    assert first.bad and plan.context.tolist() == [0, 60, 6] and table[0].tolist() == first.table[0]
+    assert plan.free_count.item() == 1
+    plan.context[0], own[0] = 70, 1
+    plan.status.zero_()
+    again = Step([70, 60, 6], [-1, 5, 60], 16, 96, first_own=[1, 0, 0], width=5, pages=first.pages)
+    again.table, again.free, again.count = table.tolist(), free.tolist(), 1
+    new.copy_(ints(again.new))
+    plan = again.plan()
+    plan.context.copy_(ints(again.context))
+    plan.free_count.fill_(1)
+    plan.run(plan.context, new, table, free, plan.free_count, own)
+    again.check(plan, table, free)
+    assert not again.bad and plan.granted.tolist() == [0, 5, 60] and plan.free_count.item() == 0
+
+
 def test_plan_without_requests_or_rows():
     Step([], [], 16, 5, free=3, count=2).run()
     Step([], [], 16, 0, free=0, count=0).run()
