@@ -649,7 +649,9 @@ typedef struct dsa_kv_segments {
     const int32_t *shared_ctx; /* device [num_segments] */
     int32_t num_segments;      /* 0: plain dsa_kv_attention */
     int64_t least_saved;       /* bytes of the pool that sharing has to save in a segment, or its rows read by
-                                  themselves; 0: the library's choice, 1: any */
+                                  themselves; 0: the library's choice, by the call's shapes (num_rows and max_ctx
+                                  among them: a max_ctx near the longest context leaves a call that is too small
+                                  to dsa_kv_attention) and then by segment; 1: any */
 } dsa_kv_segments;
 
 /*

@@ -17,7 +17,7 @@
 //                                           and puts P over S in TMEM, in 16 bits
 //   O[128 columns x D] += P V               P from TMEM, V from shared memory, O in TMEM for the whole item
 //
-// A CTA (one an SM: 512 TMEM columns, 198 to 227 KB) has two such chains, each with a warpgroup for its softmax and a warp
+// A CTA (one an SM: 512 TMEM columns, 182 to 231 KB) has two such chains, each with a warpgroup for its softmax and a warp
 // that issues its products, so that one's products run beside the other's exponentials.  An item of more than 128 columns
 // has 128 for each chain, and every tile of K and V serves both; one of fewer has the same columns in both, which then
 // take every other tile.  K and V come by TMA, a warp and a ring each.
@@ -28,7 +28,8 @@
 // burst), 128 SMs at the shared tokens for 325 of them.  64 rows of 64K and 8, bf16: 69 us for 36 of products.  Few rows,
 // bytes: 4 rows of 128K, bf16 65 us, 268 MB.  Below that the latencies of four kernels: checks 6, a shared item's start
 // (7,000 cycles to its first weights) and output (6,300: 128 KB at what an SM writes) 7, join 5 us.  Head_dim 64 has
-// half the products and as many exponentials: 256 rows of 32K 167 us against 71 of products.
+// half the products and as many exponentials: 256 rows of 32K, 16 query heads each, FP8 168 us and bf16 199 against 72 of
+// products.
 //
 // Precision.  bf16 pool: products are exact, P is rounded to bf16 (2^-8 of itself; kv_attention.cu's second term would
 // make the second product, half of all, twice as long).  FP8 pool: q as two e4m3 terms against K's codes as they
@@ -96,14 +97,24 @@ __device__ __forceinline__ KvSharedSeg read_segment(const KvSharedSeg *p) {
 
 // Rows' own tokens in parts of 2^10 at least where a segment has so many (row group, KV head): 32 rows of 4 KV heads and 32K
 // tokens, with 100 to 4,096 of their own: 50.7 us, with 2^9 53.6, with 2^8 57.7; 256 rows of 64K 354 and with 2^8 436; but
-// four segments of 4 row groups 60.5 and 54.8
+// four segments of 4 groups of 4 rows 60.5 and 54.8.  us with 2^10 / 2^8 everywhere, 16 query heads a KV head:
+//   (row group, KV head) of a segment     16         32         48         64         80         96         128        256
+//   one segment of 32K, FP8             31.4/29.7  36.3/31.7  40.7/36.6  38.1/38.3  47.3/50.0  47.2/52.6  49.3/55.8  86/103
+//                       bf16            31.4/28.8  36.6/34.4  39.0/40.3  42.7/40.0  49.5/50.8  52.0/54.4  56.1/59.9  89/105
+//   four segments of 16K, FP8           38.2/41.7  50.6/59.1             63.5/78.8             109/141    114/145
+//                       bf16            51.8/57.2  64.7/73.3             95/110                125/144    171/205
+// So for rows one by one the rule turns late (the parts pay from 80, beside other segments from 16); for rows in groups, 16
+// to a segment, they cost.
 constexpr int32_t kManyGroups = 128, kManyPartMin = 10;
 constexpr int32_t kItemTiles = 12;  // what an item costs beside its tiles
 constexpr int32_t kMinTiles = 4;    // of a part
 
 // Bytes that sharing has to save (those that the other rows of a segment would read) to make up for two launches more and
-// another chain of latencies.  A call whose shapes leave less is dsa_kv_attention's; in one that is not, where half of
-// that is spent already, a segment has to save half, and of several each its share.
+// another chain of latencies.  A call whose shapes leave less is dsa_kv_attention's (with dev_status, one launch more for the
+// segments' checks: 10.3 us for 8.8); in one that is not, where half of that is spent already, a segment has to save half,
+// and of several each its share.  The shapes are the rows and max_ctx, all that the host knows: with a bound far above the
+// contexts a small batch goes through all four kernels with little or nothing shared (4 rows of 2K, bf16, max_ctx 131,072:
+// 18.0 us, by dsa_kv_attention 10.6; 8 rows of 8K, FP8 24.5 and 20.6, bf16 22.8 and 24.1).
 // us in a graph, 1 to 200 tokens of their own, each row by itself / in a call that shares nothing / shared:
 //                       FP8, 4 heads of 128      bf16, 4 heads of 128     bf16, 3 heads of 64
 //   8 rows of 8K         56 MB  21 / 29 / 26     112 MB  20 / 28 / 24      42 MB  12 / 19 / 19
@@ -129,7 +140,9 @@ __host__ __device__ __forceinline__ int32_t shared_parts_cap(int32_t units) {
 // ------------------------------------------------------------------ who reads what
 
 // One CTA.  Its time is that of a chain of dependent reads, so what it goes through again stays in shared memory while it
-// fits.
+// fits.  A warp takes a segment, so from 8 on they follow one another: us by itself, cold, for 1 / 16 / 64 / 128 segments
+// 8 / 10 / 20 / 33.  Of 128 pairs of rows (FP8, 4 heads of 128, 8 query heads each) sharing 2,048 tokens takes 144 us and
+// each by itself 139, of 4,096 tokens 184 and 234.
 constexpr int kSegThreads = 256, kSegRows = 8192, kSegSegs = 64;
 
 // put(segment, first row, rows, shared tokens) of every segment, of no rows where it cannot be, which is reported.  All
