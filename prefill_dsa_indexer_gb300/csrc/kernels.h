@@ -353,9 +353,9 @@ struct KvAttnArgs {
     int32_t group;     // rows per group
     const int32_t *row_begin;  // or NULL: each row's tokens before this one (a multiple of 128; below that, how its parts
                                // are cut) are read elsewhere, and row_ctx counts from it; of a row group, one
-    bool keep_parts;   // a row's only part goes to the workspace too
-    int32_t *own_sms;  // or NULL; device [1 + kOwnSms]: how many SMs are to work, the others being another kernel's, and
-                       // zeros
+    bool keep_parts;           // with row_begin: a row's only part goes to the workspace too
+    int32_t *own_sms;  // with row_begin; device [1 + kOwnSms]: how many SMs are to work, the others being another
+                       // kernel's, and zeros
     const uint16_t *q;
     int64_t q_stride;
     int32_t num_heads;

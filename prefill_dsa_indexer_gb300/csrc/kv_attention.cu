@@ -165,7 +165,8 @@ struct QueryTurn {
     static constexpr int kUnits = D / 16, kTurnCols = 32 / kUnits;
     uint4 v0, v1;
 
-    __device__ __forceinline__ void load(const KvAttnArgs &a, const KvCursor &w, int n, int cols, int hpg, int lane) {
+    template <int kForm>
+    __device__ __forceinline__ void load(const KvAttnArgs &a, const KvCursor<kForm> &w, int n, int cols, int hpg, int lane) {
         const int col = w.col0 + n + lane / kUnits;
         v0 = v1 = make_uint4(0u, 0u, 0u, 0u);
         if (col < cols) {
@@ -179,9 +180,9 @@ struct QueryTurn {
     }
 
     // Into a column warp's place in 16 bits, columns as rows, with each column's scale and context.
-    template <bool kFp8>
-    __device__ __forceinline__ void put(uint8_t *queries, float2 *cols_s, const KvAttnArgs &a, const KvCursor &w, int n,
-                                        int cols, int hpg, int lane) {
+    template <bool kFp8, int kForm>
+    __device__ __forceinline__ void put(uint8_t *queries, float2 *cols_s, const KvAttnArgs &a, const KvCursor<kForm> &w,
+                                        int n, int cols, int hpg, int lane) {
         const int unit = lane % kUnits;
         n += lane / kUnits;
         const int col = w.col0 + n;
@@ -221,7 +222,7 @@ struct QueryTurn {
 };
 
 // kWide: more than 8 columns per warp (two n-tiles of the second product).
-template <bool kFp8, int D, bool kWide, int kColWarps>
+template <bool kFp8, int D, bool kWide, int kColWarps, KvForm kForm>
 __global__ void __launch_bounds__(kThreads, 2)
     kv_attention_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ KvAttnArgs a) {
     using C = KvCfg<kFp8, D, kColWarps>;
@@ -255,15 +256,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     pdl_wait();
     const bool direct = kv_direct(a);
-    if (direct || a.keep_parts) pdl_launch_dependents();
+    if (direct || kForm == kBeside) pdl_launch_dependents();
     KvSchedule *sched = reinterpret_cast<KvSchedule *>(smem + C::OFF_SCHED);
-    if (!kv_fill_schedule(a, sched)) return;
+    if (!kv_fill_schedule<kForm>(a, sched)) return;
     __syncthreads();
 
     const int hpg = a.hpg, cols = a.group * hpg;
     const int gi = lane >> 2, ji = lane & 3;
-    KvCursor w;
-    bool more = w.first<kCols>(a, sched, lane);
+    KvCursor<kForm> w;
+    bool more = w.template first<kCols>(a, sched, lane);
     using Turn = QueryTurn<D>;
 
     if (warp == kProducer) {
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         int s = 0, issued = 0;
         uint32_t phase = 1;
         bool go = true;
-        for (; more && go; more = w.next<kCols>(a, lane)) {
+        for (; more && go; more = w.template next<kCols>(a, lane)) {
             const int num_pages = (w.t_end + a.page_size - 1) >> a.page_shift;
             const int32_t *table = kv_table(a, w.req, w.begin);
             auto load_ids = [&](int p) { return p + lane < num_pages ? table[p + lane] : 0; };
@@ -327,11 +328,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
         }
-        // (Where the parts are kept, what comes next takes an SM as a whole, and is let start at once.)
+        // (Beside: what comes next takes an SM as a whole, and is let start at once.)
         // With many items only now: the merge's CTAs beside this one's start took it 2,000 cycles and more (23 ragged
         // rows of head_dim 64: 20.8 us against 19.8).  With few it is better early (four rows of 256 tokens: 7.3 us
         // against 8.4).
-        if (!direct && !a.keep_parts) pdl_launch_dependents();
+        if (!direct && kForm == kAlone) pdl_launch_dependents();
         if (*abort && lane == 0) {  // leave no copy in flight behind
             for (int i = max(0, issued - C::kStages); i < issued; ++i) {
                 const long long t0 = clock64();
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint32_t phase = 1;
         bool fresh = false;
         if (more) named_bar_sync(2, 32 * (kConsumers + 1));
-        for (; more; more = w.next<kCols>(a, lane)) {
+        for (; more; more = w.template next<kCols>(a, lane)) {
             if (w.bad && w.part == 0 && lane == 0) report(a.status, DSA_ERR_BOUNDS);
             // the first 16 columns are loaded while the consumers still have the item before
             constexpr int kTurns = 16 / Turn::kTurnCols;
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             return static_cast<int64_t>(row0 + row) * a.num_heads + g * hpg + col - row * hpg;
         };
         auto finish = [&](int64_t at, int d, const float4 &x, float b, float total) {  // dims d .. d + 3 of head `at`
-            if (parts > 1 || a.keep_parts) {
+            if (kForm == kBeside || parts > 1) {
                 *reinterpret_cast<float4 *>(a.part_o + (at * a.parts_bound + part) * D + d) = x;
                 if (d == 0) a.part_ml[at * a.parts_bound + part] = make_float2(part_base(b, total), total);
             } else {
@@ -817,10 +818,10 @@ __global__ void __launch_bounds__(kCombineThreads) kv_combine_kernel(const __gri
     if (d == 0 && a.lse != nullptr) a.lse[at] = none ? -INFINITY : (b0 + log2f(total)) * 0.6931471805599453f;
 }
 
-template <bool kFp8, int D, bool kWide, int kColWarps>
-cudaError_t launch_variant(KvAttnArgs &a, cudaStream_t s) {
+template <bool kFp8, int D, bool kWide, int kColWarps, KvForm kForm>
+cudaError_t launch_form(KvAttnArgs &a, cudaStream_t s) {
     using C = KvCfg<kFp8, D, kColWarps>;
-    auto kern = kv_attention_kernel<kFp8, D, kWide, kColWarps>;
+    auto kern = kv_attention_kernel<kFp8, D, kWide, kColWarps, kForm>;
     static std::atomic<uint64_t> configured{0};
     cudaError_t e = raise_smem_limit(kern, C::kSmemBytes, configured);
     if (e != cudaSuccess) return e;
@@ -830,6 +831,12 @@ cudaError_t launch_variant(KvAttnArgs &a, cudaStream_t s) {
     const uint32_t ctas = persistent_ctas(a);
     if (ctas == 0) return cudaErrorInvalidDevice;
     return launch_pdl(kern, dim3(ctas), dim3(kThreads), C::kSmemBytes, s, map, a);
+}
+
+template <bool kFp8, int D, bool kWide, int kColWarps>
+cudaError_t launch_variant(KvAttnArgs &a, cudaStream_t s) {
+    return a.row_begin != nullptr ? launch_form<kFp8, D, kWide, kColWarps, kBeside>(a, s)
+                                  : launch_form<kFp8, D, kWide, kColWarps, kAlone>(a, s);
 }
 
 template <bool kFp8, int D>

@@ -59,14 +59,21 @@ __device__ __forceinline__ T early_read(const T *p) {
     return __ldcg(p);
 }
 
+// An attention kernel works by itself, or beside kv_shared_kernel (where a.row_begin is there), with each row's first
+// tokens left to that one.  kv_attention_kernel has a form for each: in one for both, 23 ragged rows of head_dim 64 take
+// 16.7 us by themselves in the place of 16.4, four rows of 2K 8.8 and 8.5.  kv_attention_fp8_kernel has one for both: in
+// forms of their own, 32 rows of 32K by themselves took 135.3 us in the place of 134.5, and what it tests stands at each
+// branch, expected there (by way of a function, four groups of four rows of 64K took 97.5 us in the place of 91.3).
+enum KvForm { kAlone, kBeside, kEither };
+
 // What KvAttnArgs.row_begin says of a row: the first of its tokens that are read here, and log2 of its parts' least
 // tokens below that (kPartMin or more).
 constexpr int32_t kBeginUnit = 128;
 
-template <bool kEarly = false>
+template <int kForm>
 __device__ __forceinline__ int32_t kv_begin(const KvAttnArgs &a, int row) {
-    if (__builtin_expect(a.row_begin == nullptr, 1)) return kPartMin;
-    return kEarly ? early_read(a.row_begin + row) : a.row_begin[row];
+    if (kForm == kEither ? __builtin_expect(a.row_begin == nullptr, 1) : kForm == kAlone) return kPartMin;
+    return a.row_begin[row];
 }
 __device__ __forceinline__ int32_t kv_part_min(int32_t begin) { return begin & (kBeginUnit - 1); }
 
@@ -95,7 +102,7 @@ constexpr int kMaxGroup = 8;        // rows of a group
 constexpr int kSchedEntries = 512;  // running costs kept in shared memory, one for every so many groups
 
 struct KvSchedule {
-    int32_t mine, of;  // with own_sms: this CTA's share (-1: none), and how many there are
+    int32_t mine, of;  // beside: this CTA's share (-1: none), and how many there are
     uint64_t before[kSchedEntries + 1];  // cost of all groups before the entry's
 };
 
@@ -172,9 +179,10 @@ __device__ __forceinline__ const int32_t *kv_table(const KvAttnArgs &a, int req,
 
 // Fills `sched`; every thread of the CTA calls it, then __syncthreads.  False: the CTA is to leave its SM to another kernel,
 // at once, since that one waits for its place.
+template <int kForm>
 __device__ __forceinline__ bool kv_fill_schedule(const KvAttnArgs &a, KvSchedule *sched) {
     if (kv_direct(a)) return true;
-    if (__builtin_expect(a.own_sms != nullptr, 0)) {
+    if (kForm == kEither ? __builtin_expect(a.own_sms != nullptr, 0) : kForm == kBeside) {
         if (threadIdx.x < 32) kv_share(a.own_sms, sched, threadIdx.x);
         __syncthreads();
         if (sched->mine < 0) return false;
@@ -187,7 +195,7 @@ __device__ __forceinline__ bool kv_fill_schedule(const KvAttnArgs &a, KvSchedule
             // (all loads first: one latency)
             const int row0 = gi * a.group;
             int n[kMaxGroup], req[kMaxGroup];
-            const int32_t begin = kv_begin(a, row0);
+            const int32_t begin = kv_begin<kForm>(a, row0);
 #pragma unroll
             for (int r = 0; r < kMaxGroup; ++r) {
                 const int row = row0 + (r < a.group ? r : 0);
@@ -228,6 +236,7 @@ __device__ __forceinline__ bool kv_fill_schedule(const KvAttnArgs &a, KvSchedule
 }
 
 // An item, and the way to the next one of this CTA.  Warp-collective.
+template <int kForm>
 struct KvCursor {
     int part, parts, col0, g, row0, req, t_begin, t_end, ctx, ctx_min;
     int my_ctx;  // of row `lane` of the group
@@ -238,7 +247,7 @@ struct KvCursor {
 
     __device__ __forceinline__ void load_group(const KvAttnArgs &a, int lane) {
         row0 = group * a.group;
-        begin = kv_begin(a, row0);
+        begin = kv_begin<kForm>(a, row0);
         my_ctx = kv_load_group(a, row0, lane, req, bad);
         ctx = __reduce_max_sync(0xffffffffu, my_ctx);
         ctx_min = __reduce_min_sync(0xffffffffu, my_ctx);
@@ -278,7 +287,7 @@ struct KvCursor {
         // total * b / n: exact for products below 2^64 / n, and no total is near (a token costs 2^-6 or less)
         const uint64_t total = sched->before[entries];
         uint64_t from;
-        if (__builtin_expect(a.own_sms == nullptr, 1)) {
+        if (kForm == kEither ? __builtin_expect(a.own_sms == nullptr, 1) : kForm == kAlone) {
             from = __umul64hi(total * blockIdx.x, a.ctas_inv);
             end = __umul64hi(total * (blockIdx.x + 1), a.ctas_inv);
         } else {

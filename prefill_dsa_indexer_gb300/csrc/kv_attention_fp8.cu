@@ -234,7 +234,7 @@ __device__ __forceinline__ bool any_nan4(uint32_t v) { return __vcmpeq4(v & 0x7f
 // A column's query as hi and lo terms, and its scale.  The 16 bf16 elements of lane's unit (lane & 7) of column n
 // are in v0, v1; the eight lanes of a column work together, so a warp takes four.
 template <int NC>
-__device__ __forceinline__ void convert_query(uint8_t *img, Columns<NC> *cs, const KvAttnArgs &a, const KvCursor &w,
+__device__ __forceinline__ void convert_query(uint8_t *img, Columns<NC> *cs, const KvAttnArgs &a, const KvCursor<kEither> &w,
                                               int n, int cols, int hpg, uint4 v0, uint4 v1, int lane) {
     const int unit = lane & 7;
     const uint32_t h[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
@@ -275,7 +275,7 @@ __device__ __forceinline__ void convert_query(uint8_t *img, Columns<NC> *cs, con
 }
 
 // The 16 elements that convert_query wants of column n; zeros behind the last column.
-__device__ __forceinline__ void load_query(const KvAttnArgs &a, const KvCursor &w, int n, int cols, int hpg, int lane,
+__device__ __forceinline__ void load_query(const KvAttnArgs &a, const KvCursor<kEither> &w, int n, int cols, int hpg, int lane,
                                            uint4 &v0, uint4 &v1) {
     v0 = v1 = make_uint4(0u, 0u, 0u, 0u);
     const int col = w.col0 + n;
@@ -352,14 +352,14 @@ __global__ void __launch_bounds__(Cfg<NC>::kThreads, 2)
     const bool direct = kv_direct(a);
     if (direct || a.keep_parts) pdl_launch_dependents();
     KvSchedule *sched = reinterpret_cast<KvSchedule *>(smem + C::OFF_SCHED);
-    if (!kv_fill_schedule(a, sched)) {
+    if (!kv_fill_schedule<kEither>(a, sched)) {
         if (warp == kScores) tmem_dealloc(tmem, C::kTmemCols);
         return;
     }
     __syncthreads();
 
     const int hpg = a.hpg, cols = a.group * hpg;
-    KvCursor w;
+    KvCursor<kEither> w;
     bool more = w.first<NC>(a, sched, lane);
     if (!direct) __syncthreads();  // the schedule's place is P's
 

@@ -1061,7 +1061,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_cons
     bool bad;
     const int my_ctx = kv_load_group<true>(a, row / a.group * a.group, lane, req, bad);
     const int ctx = __reduce_max_sync(0xffffffffu, my_ctx);
-    const int own = ctx > 0 ? kv_parts(ctx, kv_part_shift(ctx, a.parts_shift, kv_part_min(kv_begin<true>(a, row)))) : 0;
+    const int own = ctx > 0 ? kv_parts(ctx, kv_part_shift(ctx, a.parts_shift, kv_part_min(early_read(a.row_begin + row)))) : 0;
     int parts = own;
     int64_t entry = 0;  // the first shared part
     const int32_t seg = early_read(s.row_seg + row);
