@@ -659,6 +659,27 @@ def test_layer_shares_what_it_is_told_to(fmt, dim):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+def test_a_layer_with_a_long_bound_can_keep_to_the_plain_call(fmt):
+    """By its bound the library shares (as far as there is anything to share), with more to save than its shapes leave it is
+    dsa_kv_attention with that bound, bit for bit, and still reports segments that cannot be."""
+    c = Shared(54, fmt, [(700, [701, 900, 1000, 2000])], 4, 8, 128, 64)
+    most, slots = 131072, ints([-1] * 4)
+    c.table = torch.nn.functional.pad(c.table, (0, most // 64 - c.table.shape[1]))
+    k = torch.zeros(4, 4, 128, dtype=torch.bfloat16, device="cuda")
+    want = P.kv_attention(c.kv, c.table, c.row_req, c.row_ctx, most, c.q)
+    for least in (0, 1 << 40):
+        layer = P.KvLayer(c.kv, c.table, most, 4, 32, num_segments=1, least_saved=least)
+        got = layer.run(c.row_req, c.row_ctx, slots, None, c.q, k, k, segment_rows=c.starts, segment_ctx=c.shared)
+        checked(layer.status)
+        c.check(*got)
+        if least:
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        layer.run(c.row_req, c.row_ctx, slots, None, c.q, k, k, segment_rows=ints([3, 2]), segment_ctx=c.shared)
+        torch.cuda.synchronize()
+        assert layer.status.item() == P.ERR_BOUNDS
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("graph", [False, True])
 @pytest.mark.parametrize("group", [1, 2])
 def test_steps_of_a_batch_that_reads_its_prefixes_once(fmt, graph, group):
